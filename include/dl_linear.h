@@ -61,7 +61,7 @@
 extern "C" {
 #endif
 
-#define DL_VERSION 3
+#define DL_VERSION 4
 
 /* Leading workspace bytes that must be zero before a call (see conventions). */
 #define DL_WORKSPACE_ZERO_BYTES (256u + 16384u * 4u)
@@ -294,6 +294,138 @@ void dl_graph_cache_clear(void);
 
 /* Number of graphs currently cached by dl_decode_stream (host call). */
 int dl_graph_cache_size(void);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Cached attention: what a decode or verify step does between its linears.
+ *
+ * The cache keeps keys and values in 8 bits: e4m3 codes with one fp32 scale
+ * for each block of `block` consecutive tokens of a page and each head,
+ *     K[token][d] = e4m3(code) * scale[block of token].
+ * Tokens lie in pages of `page_size`; a sequence's block table names, for each
+ * run of page_size tokens, the page that holds them.
+ *
+ * Sequences of a call: sequence b has seq_lens[b] tokens in the cache INCLUDING
+ * this call's new ones, which are the rows q_start[b] .. q_start[b+1]-1 of q, k
+ * and v.  With n = q_start[b+1] - q_start[b], its new token i has cache index
+ * seq_lens[b] - n + i (negative: it has no place in the cache).
+ *
+ * All three arrays are read on the device, so a call needs no host copy of
+ * them; max_q is the host's bound on n and sizes the launch.  Values out of
+ * range are contained, not reported: q_start is taken inside [0, tokens],
+ * seq_lens inside [0, table_cols * page_size], tokens of a page outside
+ * [0, num_pages) count as absent, and of a sequence with more than max_q new
+ * tokens only the first max_q are worked on.
+ *
+ * Unlike the linear layers, q, k and v may be views of a wider row (the fused
+ * QKV projection's output): q_stride, k_stride, v_stride are elements from one
+ * token to the next, multiples of 8; a token's heads are dense.
+ * ---------------------------------------------------------------------------
+ */
+typedef struct dl_kv_cache {
+    void* k;                     /* e4m3 codes, 16-byte aligned: (page p, head h, token t,  */
+    void* v;                     /*   dim d) at p*page_stride + h*head_stride + t*head_dim + d */
+    float* k_scale;              /* (p, h, block c) at p*scale_page_stride                 */
+    float* v_scale;              /*   + h*scale_head_stride + c; finite, >= 0; 4-byte aligned */
+    long long page_stride;       /* bytes, multiples of 16                                 */
+    long long head_stride;
+    long long scale_page_stride; /* elements                                               */
+    long long scale_head_stride;
+    int num_pages;               /* >= 1                                                   */
+    int num_heads;               /* key/value heads                                        */
+    int page_size;               /* tokens of a page: a power of two, 8 .. 1024            */
+    int head_dim;                /* 64 or 128                                              */
+    int block;                   /* tokens of a scale: a power of two, 1 .. page_size      */
+} dl_kv_cache;
+
+/*
+ * Rotate the new tokens' queries and keys by their positions and append keys
+ * and values to the cache.
+ *   q      bf16 [tokens][q_heads][D] or NULL; q_out bf16 [tokens][q_heads][D]
+ *          dense (required with q): the rotated queries, rounded once.  q_out
+ *          may be q itself (q_stride == q_heads * D), not another overlap.
+ *   k, v   bf16 [tokens][num_heads][D]
+ *   cos, sin  fp32 [max_pos][rotary_dim / 2], 16-byte aligned, or both NULL (no
+ *          rotation).  With h = rotary_dim / 2 and d < h:
+ *              x'[d]     = x[d] cos[pos][d] - x[d + h] sin[pos][d]
+ *              x'[d + h] = x[d + h] cos[pos][d] + x[d] sin[pos][d]
+ *          each product and each sum rounded to fp32 (no fused
+ *          multiply-add), so that the codes below are reproducible; dims from
+ *          rotary_dim on pass through.  rotary_dim % 16 == 0, <= D.
+ *   positions  int32 [tokens] or NULL (a token's cache index); taken inside
+ *          [0, max_pos).
+ *   block_table int32 [batch][table_cols], seq_lens int32 [batch],
+ *   q_start int32 [batch + 1]: see above.
+ * The scale of a block is a power of two, the smallest 2^e >= 2^-40 with
+ * 2^e * 448 >= the largest finite |value| in it, and only grows while the
+ * block fills: a block that already holds tokens keeps the larger of its old
+ * scale and the new tokens' one, and where that grew its old codes are
+ * rescaled (rounded to nearest even; exact unless they become subnormal).
+ * Codes are e4m3(value / scale), to nearest even; infinities become +-448
+ * codes, NaN the NaN code.  Slots past a sequence's end are not written.
+ * Two sequences of a call must not share a page that either appends to.
+ */
+dl_status dl_kv_append(const dl_kv_cache* cache, const void* q, const void* k, const void* v,
+                       long long q_stride, long long k_stride, long long v_stride, void* q_out,
+                       const float* cos, const float* sin, int rotary_dim, int max_pos,
+                       const int* positions, const int* block_table, int table_cols,
+                       const int* seq_lens, const int* q_start, int batch, int tokens, int q_heads,
+                       int max_q, void* stream);
+
+/*
+ * Attention from the new tokens to the cache (which already holds them):
+ *     out[t][h] = sum_j p_j V[j][h'] ,  p = softmax_j(scale * q[t][h] . K[j][h'])
+ * over the cached tokens j <= the cache index of t, h' = h / (q_heads / num_heads).
+ * A token that sees nothing (cache index < 0, or only absent pages) gets zeros.
+ * Sums, maxima and exponentials are fp32; what is stored in the cache past a
+ * token's index, NaN included, does not reach its output.
+ *   q      bf16 [tokens][q_heads][D], 16-byte aligned
+ *   out    bf16 [tokens][q_heads][D] dense, 16-byte aligned, rounded once
+ *   lse    fp32 [tokens][q_heads] or NULL: log sum_j exp(scale * q . K_j)
+ *          (-inf where nothing is seen)
+ *   scale  usually D^-1/2
+ *   q_heads a multiple of num_heads, q_heads / num_heads <= 128
+ *   workspace, ws_bytes: at least dl_attention_workspace_bytes(...), zero
+ *          prefix as for the linear layers; one workspace serves both.
+ */
+dl_status dl_attention_paged(const dl_kv_cache* cache, const void* q, long long q_stride, void* out,
+                             float* lse, const int* block_table, int table_cols,
+                             const int* seq_lens, const int* q_start, int batch, int tokens,
+                             int q_heads, int max_q, float scale, void* workspace, size_t ws_bytes,
+                             void* stream);
+
+/* Workspace bytes of dl_attention_paged on the current device (0: invalid sizes). */
+size_t dl_attention_workspace_bytes(int batch, int tokens, int q_heads, int kv_heads, int head_dim,
+                                    int max_q);
+
+/*
+ * Verify drafted tokens against the target model's probabilities, with given
+ * random numbers (speculative sampling).  Sequence b has n = draft_lens[b]
+ * (NULL: `drafts`) drafted tokens x_i; p_i = target_probs[b][i] are the
+ * target's probabilities at draft position i (p_n: after all of them) and
+ * g_i = draft_probs[b][i] the draft's (NULL: 1 at x_i, 0 elsewhere).
+ *   - x_i is accepted while u_accept[b][i] * g_i(x_i) < p_i(x_i), compared exactly;
+ *     an x_i outside [0, vocab) and a NaN are not accepted.
+ *   - the next token is drawn from max(p_c - g_c, 0), c the number accepted, or
+ *     from p_n if all n were (and from p_c where the difference is zero
+ *     everywhere): the first token whose running sum exceeds
+ *     floor(total * r / 2^24), r = floor(u_next[b] * 2^24).  Probabilities count as whole
+ *     multiples of 2^-44 (rounded to nearest even, taken inside [0, 1], NaN as
+ *     0), so the sums are integers: exact, and the same in any order.
+ *   tokens int32 [batch][drafts + 1]: the accepted tokens, then the next one,
+ *          then -1; the next token is -1 if p_c is zero everywhere
+ *   count  int32 [batch]: the number accepted
+ *   probs_dtype DL_PROBS_F32 or DL_PROBS_BF16, of both probability arrays,
+ *          dense [batch][drafts + 1][vocab] and [batch][drafts][vocab]
+ *   u_accept fp32 [batch][drafts], u_next fp32 [batch], in [0, 1)
+ *   0 <= drafts <= 63; 1 <= vocab <= 262144 (so that a sum fits 64 bits)
+ */
+#define DL_PROBS_F32 0
+#define DL_PROBS_BF16 1
+dl_status dl_verify_draft(const int* draft_tokens, const void* draft_probs,
+                          const void* target_probs, int probs_dtype, const float* u_accept,
+                          const float* u_next, const int* draft_lens, int* tokens, int* count,
+                          int batch, int drafts, int vocab, void* stream);
 
 /*
  * Process-wide tuning overrides, for tests and tuning; 0 = automatic.

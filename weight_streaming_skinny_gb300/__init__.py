@@ -24,7 +24,8 @@ __all__ = [
     "linear_bf16_static_scratch", "STATIC_SCRATCH_BYTES", "WORKSPACE_ZERO_BYTES",
     "linear_fp8_block128", "decode_stream", "decode_stream_workspace_bytes",
     "decode_stream_launches", "graph_cache_clear", "graph_cache_size", "set_wait_test",
-    "set_override",
+    "set_override", "PagedKVCache", "kv_append", "attention_paged", "attention_workspace_bytes",
+    "verify_draft",
     "device_status", "exported_symbols", "header_symbols",
 ]
 
@@ -56,7 +57,16 @@ class _Layer(ctypes.Structure):
                 ("scales", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("y", ctypes.c_void_p),
                 ("act", ctypes.c_int)]
 
-ABI_VERSION = 3   # DL_VERSION this binding marshals for
+class _KVCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_stride", ctypes.c_longlong),
+                ("head_stride", ctypes.c_longlong), ("scale_page_stride", ctypes.c_longlong),
+                ("scale_head_stride", ctypes.c_longlong), ("num_pages", ctypes.c_int),
+                ("num_heads", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("block", ctypes.c_int)]
+
+
+ABI_VERSION = 4   # DL_VERSION this binding marshals for
 
 
 def library_path() -> str:
@@ -96,6 +106,17 @@ def load():
         lib.dl_linear_argmax.argtypes = [i, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, vp, sz, vp]
         lib.dl_linear_argmax.restype = i
         lib.dl_linear_swiglu.restype = i
+        ll, f = ctypes.c_longlong, ctypes.c_float
+        lib.dl_kv_append.argtypes = [ctypes.POINTER(_KVCache), vp, vp, vp, ll, ll, ll, vp, vp, vp, i, i,
+                                     vp, vp, i, vp, vp, i, i, i, i, vp]
+        lib.dl_kv_append.restype = i
+        lib.dl_attention_paged.argtypes = [ctypes.POINTER(_KVCache), vp, ll, vp, vp, vp, i, vp, vp,
+                                           i, i, i, i, f, vp, sz, vp]
+        lib.dl_attention_paged.restype = i
+        lib.dl_attention_workspace_bytes.argtypes = [i, i, i, i, i, i]
+        lib.dl_attention_workspace_bytes.restype = sz
+        lib.dl_verify_draft.argtypes = [vp, vp, vp, i, vp, vp, vp, vp, vp, i, i, i, vp]
+        lib.dl_verify_draft.restype = i
         lib.dl_set_override.argtypes = [i, i, i]
         lib.dl_set_override.restype = i
         lib.dl_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint)]
@@ -453,6 +474,226 @@ def decode_stream_launches(layers, workspace: Workspace) -> int:
     if n < 0:
         raise ValueError("invalid layer list: " + load().dl_last_error().decode())
     return n
+
+
+class PagedKVCache:
+    """A paged cache of keys and values in 8 bits (see dl_kv_cache in dl_linear.h).
+
+    k, v              e4m3 codes (uint8 or float8_e4m3fn) [num_pages, kv_heads, page_size, head_dim];
+                      a page's tokens and dims are dense, its page and head strides are free
+                      (multiples of 16, the same for both), so k and v may be views of one buffer
+    k_scale, v_scale  fp32 [num_pages, kv_heads, page_size // block], dense in the last dim: one
+                      scale for each block of tokens and head
+
+    The object holds the tensors and is made once; the calls below read and
+    write them in place.  ``PagedKVCache.empty`` makes them.
+    """
+
+    def __init__(self, k, v, k_scale, v_scale):
+        for t, n in ((k, "k"), (v, "v"), (k_scale, "k_scale"), (v_scale, "v_scale")):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{n} must be a torch.Tensor")
+            if not t.is_cuda or t.device != k.device:
+                raise ValueError("the cache must be CUDA tensors of one device (there is no CPU path)")
+        for t, n in ((k, "k"), (v, "v")):
+            if t.dtype not in (torch.uint8, torch.float8_e4m3fn):
+                raise ValueError(f"{n} must be e4m3 codes (uint8 or float8_e4m3fn), got {t.dtype}")
+            if t.dim() != 4 or t.shape != k.shape or t.stride() != k.stride():
+                raise ValueError("k and v must be [num_pages, kv_heads, page_size, head_dim] with equal strides")
+            if t.numel() and (t.stride(3) != 1 or t.stride(2) != t.shape[3]):
+                raise ValueError(f"a page of {n} must be dense in its tokens and dims")
+        pages, heads, page, dim = k.shape
+        for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t.dtype != torch.float32:
+                raise ValueError(f"{n} must be torch.float32, got {t.dtype}")
+            if t.dim() != 3 or t.shape != k_scale.shape or t.stride() != k_scale.stride() or \
+                    t.shape[:2] != (pages, heads) or t.shape[2] < 1 or page % t.shape[2]:
+                raise ValueError("k_scale and v_scale must be [num_pages, kv_heads, page_size // block] "
+                                 "with equal strides")
+            if t.shape[2] > 1 and t.stride(2) != 1:
+                raise ValueError(f"{n} must be dense in its last dim")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, page, dim
+        self.block = page // k_scale.shape[2]
+        self.device = k.device
+        self._struct = _KVCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                k.stride(0), k.stride(1), k_scale.stride(0), k_scale.stride(1),
+                                pages, heads, page, dim, self.block)
+        self._ref = ctypes.byref(self._struct)
+
+    @classmethod
+    def empty(cls, num_pages, kv_heads, head_dim, *, page_size=64, block=16, device="cuda"):
+        """A cache with nothing in it (codes and scales zero)."""
+        shape = (num_pages, kv_heads, page_size, head_dim)
+        k, v = (torch.zeros(shape, dtype=torch.uint8, device=device) for _ in range(2))
+        ks, vs = (torch.zeros((num_pages, kv_heads, page_size // block), dtype=torch.float32,
+                              device=device) for _ in range(2))
+        return cls(k, v, ks, vs)
+
+
+def _need_sequences(cache, block_table, seq_lens, q_start):
+    dev = cache.device
+    _need(block_table, "block_table", torch.int32, dev)
+    _need(seq_lens, "seq_lens", torch.int32, dev)
+    _need(q_start, "q_start", torch.int32, dev)
+    B = seq_lens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != B or q_start.numel() != B + 1:
+        raise ValueError("block_table must be [batch, pages], seq_lens [batch], q_start [batch + 1]")
+    return B
+
+
+def _need_rows(t, name, heads, dim, device):
+    """bf16 [tokens, heads, dim], a token's heads dense, any stride between tokens."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device} (there is no CPU path)")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [tokens, {'heads' if heads is None else heads}, {dim}]")
+    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != dim)):
+        raise ValueError(f"{name} must be dense in a token's heads and dims")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * dim) // 8 * 8
+
+
+def kv_append(q, k, v, cache: PagedKVCache, block_table, seq_lens, q_start, *, max_q: int, cos=None,
+              sin=None, positions=None, out_q=None, stream=None):
+    """Rotate the new tokens' queries and keys and append keys and values to `cache`.
+
+    q [tokens, q_heads, head_dim] (or None), k, v [tokens, kv_heads, head_dim]: bf16, possibly
+    views of the fused QKV output.  seq_lens [batch] counts the cached tokens including the
+    new ones, which are rows q_start[b] .. q_start[b + 1] - 1; max_q bounds a sequence's new
+    tokens.  cos, sin: fp32 [positions, rotary_dim / 2] (None: no rotation); positions: int32
+    [tokens] (None: the place in the cache).  Returns the rotated queries (`out_q`, which may
+    be q; None without q).  See dl_kv_append for the scales and the rounding.
+    """
+    dev, D = cache.device, cache.head_dim
+    ks = _need_rows(k, "k", cache.kv_heads, D, dev)
+    vs = _need_rows(v, "v", cache.kv_heads, D, dev)
+    T = k.shape[0]
+    B = _need_sequences(cache, block_table, seq_lens, q_start)
+    qs = Hq = 0
+    if q is not None:
+        qs = _need_rows(q, "q", None, D, dev)
+        Hq = q.shape[1]
+        if out_q is None:
+            out_q = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+        _need(out_q, "out_q", torch.bfloat16, dev)
+    elif out_q is not None:
+        raise ValueError("out_q needs q")
+    if v.shape[0] != T or (q is not None and (q.shape[0] != T or out_q.shape != q.shape)):
+        raise ValueError("q, k, v and out_q must have the same tokens")
+    rd = P = 0
+    if cos is not None or sin is not None:
+        _need(cos, "cos", torch.float32, dev)
+        _need(sin, "sin", torch.float32, dev)
+        if cos.dim() != 2 or cos.shape != sin.shape:
+            raise ValueError("cos and sin must be [positions, rotary_dim / 2]")
+        P, rd = cos.shape[0], 2 * cos.shape[1]
+    if positions is not None:
+        _need(positions, "positions", torch.int32, dev)
+        if positions.numel() != T:
+            raise ValueError("positions must be [tokens]")
+    with torch.cuda.device(dev):
+        _check(load().dl_kv_append(cache._ref, _ptr(q), _ptr(k), _ptr(v), qs, ks, vs, _ptr(out_q),
+                                   _ptr(cos), _ptr(sin), rd, P, _ptr(positions), _ptr(block_table),
+                                   block_table.shape[1], _ptr(seq_lens), _ptr(q_start), B, T, Hq,
+                                   max_q, _stream(stream, dev)))
+    return out_q
+
+
+def attention_workspace_bytes(batch: int, tokens: int, q_heads: int, kv_heads: int, head_dim: int,
+                              *, max_q: int) -> int:
+    """Workspace attention_paged needs on the current device (0 = invalid sizes)."""
+    return int(load().dl_attention_workspace_bytes(batch, tokens, q_heads, kv_heads, head_dim, max_q))
+
+
+def attention_paged(q, cache: PagedKVCache, block_table, seq_lens, q_start, *, max_q: int, scale=None,
+                    out=None, out_lse=None, workspace: Workspace | None = None, stream=None):
+    """Attention of the new tokens (q, bf16 [tokens, q_heads, head_dim]) over `cache`, which
+    already holds them; causal among them.  Returns out, bf16 like q but dense; out_lse (fp32
+    [tokens, q_heads]) gets the log-sum-exp of the scaled scores.  scale: head_dim ** -0.5 if
+    None.  The sequences are described as for kv_append; see dl_attention_paged.
+    """
+    dev, D = cache.device, cache.head_dim
+    qs = _need_rows(q, "q", None, D, dev)
+    T, Hq = q.shape[0], q.shape[1]
+    B = _need_sequences(cache, block_table, seq_lens, q_start)
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(out, "out", torch.bfloat16, dev)
+        if out.numel() != T * Hq * D:
+            raise ValueError("out must hold tokens * q_heads * head_dim elements")
+    if out_lse is not None:
+        _need(out_lse, "out_lse", torch.float32, dev)
+        if out_lse.numel() != T * Hq:
+            raise ValueError("out_lse must hold tokens * q_heads elements")
+    with torch.cuda.device(dev):
+        lib = load()
+        ws = workspace
+        if ws is None:
+            ws = _workspace(None, attention_workspace_bytes(B, T, Hq, cache.kv_heads, D, max_q=max_q), dev)
+        _check(lib.dl_attention_paged(cache._ref, _ptr(q), qs, _ptr(out), _ptr(out_lse),
+                                      _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
+                                      _ptr(q_start), B, T, Hq, max_q,
+                                      D ** -0.5 if scale is None else scale, ws.ptr, ws.nbytes,
+                                      _stream(stream, dev)))
+    return out
+
+
+def verify_draft(draft_tokens, target_probs, u_accept, u_next, *, draft_probs=None, draft_lens=None,
+                 out_tokens=None, out_count=None, stream=None):
+    """Accept a prefix of the drafted tokens and draw the next one (see dl_verify_draft).
+
+    draft_tokens int32 [batch, drafts]; target_probs [batch, drafts + 1, vocab] and draft_probs
+    [batch, drafts, vocab] (None: the draft was deterministic), both fp32 or both bf16;
+    u_accept fp32 [batch, drafts] and u_next fp32 [batch], random numbers in [0, 1);
+    draft_lens int32 [batch] or None.  Returns (tokens int32 [batch, drafts + 1]: accepted
+    tokens, the next one, then -1; count int32 [batch]: how many were accepted).
+    """
+    if not isinstance(target_probs, torch.Tensor):
+        raise TypeError("target_probs must be a torch.Tensor")
+    kind, dev = target_probs.dtype, target_probs.device
+    if kind not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"target_probs must be torch.float32 or torch.bfloat16, got {kind}")
+    _need(target_probs, "target_probs", kind)
+    _need(draft_tokens, "draft_tokens", torch.int32, dev)
+    _need(u_accept, "u_accept", torch.float32, dev)
+    _need(u_next, "u_next", torch.float32, dev)
+    if draft_tokens.dim() != 2:
+        raise ValueError("draft_tokens must be [batch, drafts]")
+    B, S = draft_tokens.shape
+    if target_probs.dim() != 3 or target_probs.shape[:2] != (B, S + 1):
+        raise ValueError("target_probs must be [batch, drafts + 1, vocab]")
+    V = target_probs.shape[2]
+    if u_accept.numel() != B * S or u_next.numel() != B:
+        raise ValueError("u_accept must be [batch, drafts] and u_next [batch]")
+    if draft_probs is not None:
+        _need(draft_probs, "draft_probs", kind, dev)
+        if draft_probs.shape != (B, S, V):
+            raise ValueError("draft_probs must be [batch, drafts, vocab]")
+    if draft_lens is not None:
+        _need(draft_lens, "draft_lens", torch.int32, dev)
+        if draft_lens.numel() != B:
+            raise ValueError("draft_lens must be [batch]")
+    if out_tokens is None:
+        out_tokens = torch.empty((B, S + 1), dtype=torch.int32, device=dev)
+    else:
+        _need(out_tokens, "out_tokens", torch.int32, dev)
+    if out_count is None:
+        out_count = torch.empty((B,), dtype=torch.int32, device=dev)
+    else:
+        _need(out_count, "out_count", torch.int32, dev)
+    if out_tokens.numel() != B * (S + 1) or out_count.numel() != B:
+        raise ValueError("out_tokens must be [batch, drafts + 1] and out_count [batch]")
+    with torch.cuda.device(dev):
+        _check(load().dl_verify_draft(_ptr(draft_tokens), _ptr(draft_probs), _ptr(target_probs),
+                                      0 if kind == torch.float32 else 1, _ptr(u_accept),
+                                      _ptr(u_next), _ptr(draft_lens), _ptr(out_tokens),
+                                      _ptr(out_count), B, S, V, _stream(stream, dev)))
+    return out_tokens, out_count
 
 
 def graph_cache_clear():

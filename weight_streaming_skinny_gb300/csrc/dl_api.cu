@@ -17,6 +17,7 @@
 #include <vector>
 
 #include "dl_linear.h"
+#include "dl_host.h"
 #include "dl_kernel.cuh"
 #include "dl_launch.h"
 
@@ -1103,3 +1104,32 @@ dl_status dl_device_status(unsigned int* flags) {
 }
 
 }  // extern "C"
+
+// ----------------------------------------------------------------- shared with the other entry points
+
+namespace dl {
+
+dl_status host_fail(dl_status s, const char* fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_err, sizeof g_err, fmt, ap);
+    va_end(ap);
+    return s;
+}
+
+dl_status host_ok() { return ok(); }
+
+dl_status host_device(HostDevice& out) {
+    DeviceInfo di;
+    const dl_status s = device_info(di);
+    if (s != DL_OK) return s;
+    out.sm_count = di.sm_count;
+    out.err_word = di.err_word;
+    const long long wait_o = g_wait_ns_override.load();
+    out.wait_limit_ns = wait_o > 0 ? (unsigned long long)wait_o : kWaitLimitNs;
+    return DL_OK;
+}
+
+dl_status host_encode(EncodeTiled& fn) { return get_encode(fn); }
+
+}  // namespace dl
