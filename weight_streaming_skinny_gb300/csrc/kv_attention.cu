@@ -1,83 +1,51 @@
-// Attention over the paged 8-bit cache (dl_attention_paged).
+// Attention over the paged 8-bit cache (dl_attention_paged): arguments, the
+// shape of a row tile, the workspace and the launch.
 #include "dl_host.h"
-#include "kv_cache.cuh"
+#include "kv_attention.cuh"
 
-namespace dl {
+namespace {
 
-struct AttnParams {
-    dl_kv_cache c;
-    const uint16_t* q;
-    uint16_t* out;
-    float* lse;
-    long long q_stride;
-    int q_heads, group;
-    int page_shift, block_shift;
-    float scale_log2;            // scale * log2(e)
-    Sequences s;
+// Row tiles of at most 128 rows, as even as the new tokens allow.
+struct RowTiles {
+    int tokens, count, padded;
 };
 
-// One warp for each (token, query head): lanes take tokens for the scores and
-// dims for the sum.
-__global__ void __launch_bounds__(128) attention_simple_kernel(const __grid_constant__ AttnParams p) {
-    const int D = p.c.head_dim, lane = threadIdx.x & 31;
-    const long long unit = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (unit >= (long long)p.s.tokens * p.q_heads) return;
-    const int t = (int)(unit / p.q_heads), h = (int)(unit % p.q_heads), hk = h / p.group;
-    int b = 0;
-    while (b < p.s.batch && p.s.q_start[b + 1] <= t) ++b;
-    if (b >= p.s.batch) return;
-    const SequenceView sv = sequence_view(p.s, b, p.c.page_size);
-    const int i = t - sv.row0;
-    if (i < 0 || i >= sv.n_work) return;
-    const int seen = max(sv.len - sv.n + i + 1, 0);
-    const uint16_t* q = p.q + (size_t)t * p.q_stride + (size_t)h * D;
-    float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int j0 = 0; j0 < seen; j0 += 32) {
-        const int j = j0 + lane;
-        int page = -1;
-        if (j < seen) page = p.s.block_table[(size_t)b * p.s.table_cols + (j >> p.page_shift)];
-        const bool in = page >= 0 && page < p.c.num_pages;
-        const int in_page = j & (p.c.page_size - 1);
-        const long long at = page * p.c.page_stride + hk * p.c.head_stride + (long long)in_page * D;
-        const long long sc = page * p.c.scale_page_stride + hk * p.c.scale_head_stride + (in_page >> p.block_shift);
-        float s = -INFINITY;
-        if (in) {
-            s = 0.f;
-            const uint8_t* k = static_cast<const uint8_t*>(p.c.k) + at;
-            for (int d = 0; d < D; d += 2) {
-                const uint32_t kk = e4m3x2_to_bf16x2(k[d] | (uint32_t)k[d + 1] << 8);
-                s = fma2_bf16(kk, q[d] | (uint32_t)q[d + 1] << 16, s);
-            }
-            s *= p.c.k_scale[sc] * p.scale_log2;
-        }
-        float top = s;
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-        const float m1 = fmaxf(m, top);
-        const float base = m1 == -INFINITY ? 0.f : m1;
-        const float fix = exp2f(m - base);
-        const float w = in ? exp2f(s - base) : 0.f;
-        l = l * fix + w;
-        for (float& a : acc) a *= fix;
-        m = m1;
-        for (int r = 0; r < 32 && j0 + r < seen; ++r) {
-            const float wr = __shfl_sync(~0u, w, r);
-            const long long ar = __shfl_sync(~0u, at, r), sr = __shfl_sync(~0u, sc, r);
-            if (!__shfl_sync(~0u, (int)in, r)) continue;
-            const uint8_t* v = static_cast<const uint8_t*>(p.c.v) + ar;
-            const float ws = wr * p.c.v_scale[sr];
-            for (int c = 0; c < D / 32; ++c)
-                acc[c] = fmaf(ws, __uint_as_float(e4m3x2_to_bf16x2(v[32 * c + lane]) << 16), acc[c]);
-        }
-    }
-    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
-    for (int c = 0; c < D / 32; ++c)
-        p.out[((size_t)t * p.q_heads + h) * D + 32 * c + lane] =
-            f32_to_bf16_rne(l == 0.f ? 0.f : acc[c] / l);
-    if (p.lse && lane == 0)
-        p.lse[(size_t)t * p.q_heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718056f;
+RowTiles row_tiles(int tokens, int max_q, int group) {
+    const int most = 128 / group, n = max_q < tokens ? max_q : tokens;
+    RowTiles r;
+    r.count = (n + most - 1) / most;
+    r.tokens = (n + r.count - 1) / r.count;
+    r.padded = dl::attn_rows_padded(r.tokens * group);
+    return r;
 }
 
-}  // namespace dl
+size_t split_bytes(int grid) { return ((size_t)grid * sizeof(dl::AttnSplit) + 255) / 256 * 256; }
+
+size_t workspace_bytes(int grid, int rp, int dim) {
+    return DL_WORKSPACE_ZERO_BYTES + split_bytes(grid) + (size_t)grid * 2 * rp * (dim + 2) * sizeof(float);
+}
+
+// The codes as a tensor (dim, token, head, page); a box is a page's tokens, at
+// most a tile's.
+dl_status encode_codes(const dl_kv_cache& c, void* codes, CUtensorMap& map) {
+    dl::EncodeTiled enc;
+    const dl_status s = dl::host_encode(enc);
+    if (s != DL_OK) return s;
+    const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size, (cuuint64_t)c.num_heads,
+                                (cuuint64_t)c.num_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.head_stride, (cuuint64_t)c.page_stride};
+    const cuuint32_t box[4] = {(cuuint32_t)c.head_dim,
+                               (cuuint32_t)(c.page_size < dl::kTile ? c.page_size : dl::kTile), 1, 1};
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    const CUresult r = enc(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, codes, dims, strides, box, ones,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           c.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return dl::host_fail(DL_ERR_CUDA, "cuTensorMapEncodeTiled(cache): %d", (int)r);
+    return DL_OK;
+}
+
+}  // namespace
 
 extern "C" size_t dl_attention_workspace_bytes(int batch, int tokens, int q_heads, int kv_heads,
                                                int head_dim, int max_q) {
@@ -86,7 +54,11 @@ extern "C" size_t dl_attention_workspace_bytes(int batch, int tokens, int q_head
         dl::host_fail(DL_ERR_UNSUPPORTED_SHAPE, "attention sizes are out of range");
         return 0;
     }
-    return DL_WORKSPACE_ZERO_BYTES;
+    if (batch == 0 || tokens == 0 || max_q == 0) return DL_WORKSPACE_ZERO_BYTES;
+    dl::HostDevice dev;
+    if (dl::host_device(dev) != DL_OK) return 0;
+    const int rp = row_tiles(tokens, max_q, q_heads / kv_heads).padded;
+    return workspace_bytes(dev.sm_count * dl::attn_ctas_per_sm(rp), rp, head_dim);
 }
 
 extern "C" dl_status dl_attention_paged(const dl_kv_cache* cache, const void* q, long long q_stride,
@@ -110,27 +82,49 @@ extern "C" dl_status dl_attention_paged(const dl_kv_cache* cache, const void* q,
     if (((uintptr_t)q | (uintptr_t)out) & 15)
         return host_fail(DL_ERR_MISALIGNED, "q and out must be 16-byte aligned");
     if ((uintptr_t)lse & 3) return host_fail(DL_ERR_MISALIGNED, "lse must be 4-byte aligned");
-    const size_t need = dl_attention_workspace_bytes(batch, tokens, q_heads, cache->num_heads,
-                                                     cache->head_dim, max_q);
     if (!workspace) return host_fail(DL_ERR_WORKSPACE, "workspace is NULL");
+    if ((uintptr_t)workspace & 255) return host_fail(DL_ERR_MISALIGNED, "workspace must be 256-byte aligned");
+    HostDevice dev;
+    if ((s = host_device(dev)) != DL_OK) return s;
+    const int group = q_heads / cache->num_heads;
+    const RowTiles rt = row_tiles(tokens, max_q, group);
+    if ((long long)batch * rt.count > 0x7fffffffLL)
+        return host_fail(DL_ERR_UNSUPPORTED_SHAPE, "batch=%d times %d row tiles exceed one launch", batch, rt.count);
+    AttnLaunch a = {};
+    a.grid = dev.sm_count * attn_ctas_per_sm(rt.padded);
+    a.stream = static_cast<cudaStream_t>(stream);
+    const size_t need = workspace_bytes(a.grid, rt.padded, cache->head_dim);
     if (ws_bytes < need)
         return host_fail(DL_ERR_WORKSPACE, "workspace holds %zu bytes, %zu are needed", ws_bytes, need);
-    AttnParams p = {};
-    p.c = *cache;
+    if ((s = encode_codes(*cache, cache->k, a.tk)) != DL_OK) return s;
+    if ((s = encode_codes(*cache, cache->v, a.tv)) != DL_OK) return s;
+    AttnParams& p = a.p;
     p.q = static_cast<const uint16_t*>(q);
     p.out = static_cast<uint16_t*>(out);
     p.lse = lse;
+    p.k_scale = cache->k_scale;
+    p.v_scale = cache->v_scale;
     p.q_stride = q_stride;
+    p.scale_page_stride = cache->scale_page_stride;
+    p.scale_head_stride = cache->scale_head_stride;
+    p.num_pages = cache->num_pages;
+    p.kv_heads = cache->num_heads;
     p.q_heads = q_heads;
-    p.group = q_heads / cache->num_heads;
+    p.group = group;
+    p.page_size = cache->page_size;
     while ((1 << p.page_shift) < cache->page_size) ++p.page_shift;
     while ((1 << p.block_shift) < cache->block) ++p.block_shift;
-    p.scale_log2 = scale * 1.44269504089f;
+    p.tile_tokens = rt.tokens;
+    p.row_tiles = rt.count;
+    p.scale_log2 = scale * 1.44269504088896341f;
     p.s = Sequences{block_table, seq_lens, q_start, table_cols, batch, tokens, max_q};
-    const long long units = ((long long)tokens * q_heads + 3) / 4;
-    if (units > 0x7fffffffLL) return host_fail(DL_ERR_UNSUPPORTED_SHAPE, "too many tokens for one launch");
-    attention_simple_kernel<<<(unsigned)units, 128, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    unsigned char* ws = static_cast<unsigned char*>(workspace) + DL_WORKSPACE_ZERO_BYTES;
+    p.split = reinterpret_cast<AttnSplit*>(ws);
+    p.partial = reinterpret_cast<float*>(ws + split_bytes(a.grid));
+    p.err_word = dev.err_word;
+    p.wait_limit_ns = dev.wait_limit_ns;
+    const cudaError_t e = cache->head_dim == 128 ? launch_attention_d128(rt.padded, a)
+                                                 : launch_attention_d64(rt.padded, a);
     if (e != cudaSuccess) return host_fail(DL_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
     return host_ok();
 }

@@ -1,0 +1,55 @@
+// Instantiation of the attention kernels for one head dimension.
+#pragma once
+
+#include <atomic>
+
+#include "kv_attention.cuh"
+
+namespace dl {
+
+template <class C>
+cudaError_t launch_attention_instance(const AttnLaunch& a) {
+    static std::atomic<bool> ready[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!ready[dev].load()) {
+        e = cudaFuncSetAttribute(attention_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+        if (e != cudaSuccess) return e;
+        ready[dev].store(true);
+    }
+    // Both kernels may start while the one before drains; they wait for it
+    // before they touch memory.
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.grid);
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = a.stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, attention_kernel<C>, a.tk, a.tv, a.p)) != cudaSuccess) return e;
+    cfg.gridDim = dim3(a.grid, (a.p.tile_tokens * a.p.group + 3) / 4);
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, attention_combine_kernel<C::D>, a.p, C::RP, a.grid);
+}
+
+template <int D>
+cudaError_t launch_attention_dim(int rp, const AttnLaunch& a) {
+    switch (rp) {
+        case 8: return launch_attention_instance<AttnShape<D, 8>>(a);
+        case 16: return launch_attention_instance<AttnShape<D, 16>>(a);
+        case 32: return launch_attention_instance<AttnShape<D, 32>>(a);
+        case 48: return launch_attention_instance<AttnShape<D, 48>>(a);
+        case 64: return launch_attention_instance<AttnShape<D, 64>>(a);
+        case 96: return launch_attention_instance<AttnShape<D, 96>>(a);
+        case 128: return launch_attention_instance<AttnShape<D, 128>>(a);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace dl

@@ -24,11 +24,11 @@ struct SequenceView {
 
 __device__ __forceinline__ SequenceView sequence_view(const Sequences& s, int b, int page_size) {
     SequenceView r;
-    r.row0 = min(max(__ldg(s.q_start + b), 0), s.tokens);
-    r.n = min(max(__ldg(s.q_start + b + 1), r.row0), s.tokens) - r.row0;
+    r.row0 = min(max(s.q_start[b], 0), s.tokens);
+    r.n = min(max(s.q_start[b + 1], r.row0), s.tokens) - r.row0;
     r.n_work = min(r.n, s.max_q);
     const long long room = (long long)s.table_cols * page_size;
-    const int len = max(__ldg(s.seq_lens + b), 0);
+    const int len = max(s.seq_lens[b], 0);
     r.len = (long long)len > room ? (int)room : len;
     return r;
 }
