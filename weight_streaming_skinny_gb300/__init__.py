@@ -76,6 +76,8 @@ def library_path() -> str:
 def load():
     """Load the shared library (raises if it is missing: there is no fallback)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -162,6 +164,9 @@ def _stream(stream, device):
 
 
 def _need(t, name, dtype, device=None):
+    if type(t) is torch.Tensor and t.dtype is dtype and t.is_contiguous() and \
+            (t.is_cuda if device is None else t.device == device):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -531,30 +536,60 @@ class PagedKVCache:
         return cls(k, v, ks, vs)
 
 
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _enqueue(fn, device, stream, *args):
+    """fn(*args, stream) with `device` current (entered only where it is not)."""
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(device.index)
+    elif isinstance(stream, torch.cuda.Stream):
+        stream = stream.cuda_stream
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, stream)
+    if status:
+        _check(status)
+
+
 def _need_sequences(cache, block_table, seq_lens, q_start):
-    dev = cache.device
-    _need(block_table, "block_table", torch.int32, dev)
-    _need(seq_lens, "seq_lens", torch.int32, dev)
-    _need(q_start, "q_start", torch.int32, dev)
-    B = seq_lens.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != B or q_start.numel() != B + 1:
+    """(batch, columns of the table)."""
+    dev, i32 = cache.device, torch.int32
+    if not (type(block_table) is type(seq_lens) is type(q_start) is torch.Tensor and
+            block_table.dtype is seq_lens.dtype is q_start.dtype is i32 and
+            block_table.device == seq_lens.device == q_start.device == dev and
+            block_table.is_contiguous() and seq_lens.is_contiguous() and q_start.is_contiguous()):
+        _need(block_table, "block_table", i32, dev)
+        _need(seq_lens, "seq_lens", i32, dev)
+        _need(q_start, "q_start", i32, dev)
+    B, shape = seq_lens.numel(), block_table.shape
+    if len(shape) != 2 or shape[0] != B or q_start.numel() != B + 1:
         raise ValueError("block_table must be [batch, pages], seq_lens [batch], q_start [batch + 1]")
-    return B
+    return B, shape[1]
 
 
 def _need_rows(t, name, heads, dim, device):
-    """bf16 [tokens, heads, dim], a token's heads dense, any stride between tokens."""
+    """bf16 [tokens, heads, dim], a token's heads dense, any stride between tokens: (tokens, heads,
+    elements from one token to the next)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be a CUDA tensor on {device} (there is no CPU path)")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
+    if t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device} (there is no CPU path)")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, {dim}]")
+    T, H, d = t.shape
+    st, sh, sd = t.stride()
+    if d != dim or (heads is not None and H != heads):
         raise ValueError(f"{name} must be [tokens, {'heads' if heads is None else heads}, {dim}]")
-    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != dim)):
+    if (sd != 1 or (sh != dim and H > 1)) and T and H:
         raise ValueError(f"{name} must be dense in a token's heads and dims")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * dim) // 8 * 8
+    # one token has no next one: any stride will do
+    return T, H, st if T > 1 else H * dim
 
 
 def kv_append(q, k, v, cache: PagedKVCache, block_table, seq_lens, q_start, *, max_q: int, cos=None,
@@ -569,37 +604,37 @@ def kv_append(q, k, v, cache: PagedKVCache, block_table, seq_lens, q_start, *, m
     be q; None without q).  See dl_kv_append for the scales and the rounding.
     """
     dev, D = cache.device, cache.head_dim
-    ks = _need_rows(k, "k", cache.kv_heads, D, dev)
-    vs = _need_rows(v, "v", cache.kv_heads, D, dev)
-    T = k.shape[0]
-    B = _need_sequences(cache, block_table, seq_lens, q_start)
-    qs = Hq = 0
+    T, _, ks = _need_rows(k, "k", cache.kv_heads, D, dev)
+    Tv, _, vs = _need_rows(v, "v", cache.kv_heads, D, dev)
+    B, cols = _need_sequences(cache, block_table, seq_lens, q_start)
+    Tq, Hq, qs = T, 0, 0
     if q is not None:
-        qs = _need_rows(q, "q", None, D, dev)
-        Hq = q.shape[1]
+        Tq, Hq, qs = _need_rows(q, "q", None, D, dev)
         if out_q is None:
-            out_q = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
-        _need(out_q, "out_q", torch.bfloat16, dev)
+            out_q = q.new_empty((Tq, Hq, D))
+        else:
+            _need(out_q, "out_q", torch.bfloat16, dev)
+            if out_q.shape != q.shape:
+                raise ValueError("q, k, v and out_q must have the same tokens")
     elif out_q is not None:
         raise ValueError("out_q needs q")
-    if v.shape[0] != T or (q is not None and (q.shape[0] != T or out_q.shape != q.shape)):
+    if Tv != T or Tq != T:
         raise ValueError("q, k, v and out_q must have the same tokens")
     rd = P = 0
     if cos is not None or sin is not None:
         _need(cos, "cos", torch.float32, dev)
         _need(sin, "sin", torch.float32, dev)
-        if cos.dim() != 2 or cos.shape != sin.shape:
+        shape = cos.shape
+        if len(shape) != 2 or shape != sin.shape:
             raise ValueError("cos and sin must be [positions, rotary_dim / 2]")
-        P, rd = cos.shape[0], 2 * cos.shape[1]
+        P, rd = shape[0], 2 * shape[1]
     if positions is not None:
         _need(positions, "positions", torch.int32, dev)
         if positions.numel() != T:
             raise ValueError("positions must be [tokens]")
-    with torch.cuda.device(dev):
-        _check(load().dl_kv_append(cache._ref, _ptr(q), _ptr(k), _ptr(v), qs, ks, vs, _ptr(out_q),
-                                   _ptr(cos), _ptr(sin), rd, P, _ptr(positions), _ptr(block_table),
-                                   block_table.shape[1], _ptr(seq_lens), _ptr(q_start), B, T, Hq,
-                                   max_q, _stream(stream, dev)))
+    _enqueue(load().dl_kv_append, dev, stream, cache._ref, _addr(q), k.data_ptr(), v.data_ptr(), qs, ks,
+             vs, _addr(out_q), _addr(cos), _addr(sin), rd, P, _addr(positions), block_table.data_ptr(),
+             cols, seq_lens.data_ptr(), q_start.data_ptr(), B, T, Hq, max_q)
     return out_q
 
 
@@ -617,11 +652,10 @@ def attention_paged(q, cache: PagedKVCache, block_table, seq_lens, q_start, *, m
     None.  The sequences are described as for kv_append; see dl_attention_paged.
     """
     dev, D = cache.device, cache.head_dim
-    qs = _need_rows(q, "q", None, D, dev)
-    T, Hq = q.shape[0], q.shape[1]
-    B = _need_sequences(cache, block_table, seq_lens, q_start)
+    T, Hq, qs = _need_rows(q, "q", None, D, dev)
+    B, cols = _need_sequences(cache, block_table, seq_lens, q_start)
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+        out = q.new_empty((T, Hq, D))
     else:
         _need(out, "out", torch.bfloat16, dev)
         if out.numel() != T * Hq * D:
@@ -630,16 +664,12 @@ def attention_paged(q, cache: PagedKVCache, block_table, seq_lens, q_start, *, m
         _need(out_lse, "out_lse", torch.float32, dev)
         if out_lse.numel() != T * Hq:
             raise ValueError("out_lse must hold tokens * q_heads elements")
-    with torch.cuda.device(dev):
-        lib = load()
-        ws = workspace
-        if ws is None:
-            ws = _workspace(None, attention_workspace_bytes(B, T, Hq, cache.kv_heads, D, max_q=max_q), dev)
-        _check(lib.dl_attention_paged(cache._ref, _ptr(q), qs, _ptr(out), _ptr(out_lse),
-                                      _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
-                                      _ptr(q_start), B, T, Hq, max_q,
-                                      D ** -0.5 if scale is None else scale, ws.ptr, ws.nbytes,
-                                      _stream(stream, dev)))
+    if workspace is None:
+        with torch.cuda.device(dev):
+            workspace = _workspace(None, attention_workspace_bytes(B, T, Hq, cache.kv_heads, D, max_q=max_q), dev)
+    _enqueue(load().dl_attention_paged, dev, stream, cache._ref, q.data_ptr(), qs, out.data_ptr(),
+             _addr(out_lse), block_table.data_ptr(), cols, seq_lens.data_ptr(), q_start.data_ptr(), B, T,
+             Hq, max_q, D ** -0.5 if scale is None else scale, workspace.tensor.data_ptr(), workspace.nbytes)
     return out
 
 
@@ -679,20 +709,18 @@ def verify_draft(draft_tokens, target_probs, u_accept, u_next, *, draft_probs=No
         if draft_lens.numel() != B:
             raise ValueError("draft_lens must be [batch]")
     if out_tokens is None:
-        out_tokens = torch.empty((B, S + 1), dtype=torch.int32, device=dev)
+        out_tokens = draft_tokens.new_empty((B, S + 1))
     else:
         _need(out_tokens, "out_tokens", torch.int32, dev)
     if out_count is None:
-        out_count = torch.empty((B,), dtype=torch.int32, device=dev)
+        out_count = draft_tokens.new_empty((B,))
     else:
         _need(out_count, "out_count", torch.int32, dev)
     if out_tokens.numel() != B * (S + 1) or out_count.numel() != B:
         raise ValueError("out_tokens must be [batch, drafts + 1] and out_count [batch]")
-    with torch.cuda.device(dev):
-        _check(load().dl_verify_draft(_ptr(draft_tokens), _ptr(draft_probs), _ptr(target_probs),
-                                      0 if kind == torch.float32 else 1, _ptr(u_accept),
-                                      _ptr(u_next), _ptr(draft_lens), _ptr(out_tokens),
-                                      _ptr(out_count), B, S, V, _stream(stream, dev)))
+    _enqueue(load().dl_verify_draft, dev, stream, draft_tokens.data_ptr(), _addr(draft_probs),
+             target_probs.data_ptr(), 0 if kind is torch.float32 else 1, u_accept.data_ptr(),
+             u_next.data_ptr(), _addr(draft_lens), out_tokens.data_ptr(), out_count.data_ptr(), B, S, V)
     return out_tokens, out_count
 
 

@@ -15,26 +15,69 @@ struct AppendParams {
     int rotary_dim, max_pos, q_heads;
     int page_shift, block_shift;
     int blocks_per_seq;          // most blocks a sequence's new tokens touch
+    int team, kv_ctas;           // threads of a block, CTAs that take blocks
+    long long kv_units;          // blocks of keys (as many of values follow)
     Sequences s;
 };
 
-constexpr int kAppendThreads = 128;
-
-// The new value of dim d of one row (a token's head), rotated at `pos`.
-__device__ __forceinline__ float rotated(const AppendParams& p, const uint16_t* row, int d, int pos) {
-    const float x = bf16_bits_to_f32(row[d]);
-    if (!p.cos || d >= p.rotary_dim) return x;
-    const int h = p.rotary_dim / 2;
-    const int i = d < h ? d : d - h;
-    const float c = p.cos[(size_t)pos * h + i], s = p.sin[(size_t)pos * h + i];
-    const float y = bf16_bits_to_f32(row[d < h ? d + h : d - h]);
-    return d < h ? __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s))
-                 : __fadd_rn(__fmul_rn(x, c), __fmul_rn(y, s));
-}
+// What bounds it: memory.  A token's queries are read and written once, keys and
+// values read once and written as codes.  A thread takes 16 dims at a time, the
+// two groups of 8 that rotate into one another (or 16 dims that pass through):
+// 16-byte loads and stores, and cos and sin stay in its registers while it goes
+// through a token's heads.
+constexpr int kAppendThreads = 256;
 
 __device__ __forceinline__ int position_of(const AppendParams& p, int t, int index) {
     const int at = p.positions ? p.positions[t] : index;
     return min(max(at, 0), p.max_pos - 1);
+}
+
+// Unit u of a row's D / 16: its two groups of 8 dims start at `a` and `b`.
+struct RowUnit {
+    int a, b, angle;            // angle: index of the first cos / sin, or -1
+};
+__device__ __forceinline__ RowUnit row_unit(int u, int rotary_dim) {
+    const int pairs = rotary_dim / 16;
+    if (u < pairs) return {8 * u, 8 * u + rotary_dim / 2, 8 * u};
+    return {16 * u, 16 * u + 8, -1};
+}
+
+__device__ __forceinline__ void load_angles(const AppendParams& p, int pos, int angle, float (&c)[8], float (&s)[8]) {
+    const size_t at = (size_t)pos * (p.rotary_dim / 2) + angle;
+#pragma unroll
+    for (int k = 0; k < 8; k += 4) {
+        const uint4 x = ldg128(p.cos + at + k), y = ldg128(p.sin + at + k);
+        c[k] = __uint_as_float(x.x); c[k + 1] = __uint_as_float(x.y);
+        c[k + 2] = __uint_as_float(x.z); c[k + 3] = __uint_as_float(x.w);
+        s[k] = __uint_as_float(y.x); s[k + 1] = __uint_as_float(y.y);
+        s[k + 2] = __uint_as_float(y.z); s[k + 3] = __uint_as_float(y.w);
+    }
+}
+
+__device__ __forceinline__ void unpack8(const uint4& v, float* f) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        f[2 * k] = __uint_as_float(w[k] << 16);
+        f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    }
+}
+
+// f[0..8) and f[8..16) rotated into one another; each product and sum rounded
+// on its own, so that the codes do not depend on how it is compiled.
+__device__ __forceinline__ void rotate(float (&f)[16], const float (&c)[8], const float (&s)[8]) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float x = f[k], y = f[k + 8];
+        f[k] = __fsub_rn(__fmul_rn(x, c[k]), __fmul_rn(y, s[k]));
+        f[k + 8] = __fadd_rn(__fmul_rn(y, c[k]), __fmul_rn(x, s[k]));
+    }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
 }
 
 __device__ __forceinline__ float e4m3_value(uint8_t code) {
@@ -53,87 +96,163 @@ __device__ __forceinline__ float block_scale(float amax) {
     return __uint_as_float((unsigned)(e + 127) << 23);
 }
 
-// grid.x: first one CTA for each token's queries, then one for each (sequence,
-// touched block, head, key or value).
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_constant__ AppendParams p) {
-    const int D = p.c.head_dim;
+// One CTA: a token's queries, every head.
+template <int D>
+__device__ __forceinline__ void append_queries(const AppendParams& p, int t) {
+    constexpr int kUnits = D / 16;
     const int tid = threadIdx.x;
-    int unit = blockIdx.x;
-    if (p.q) {
-        if (unit < p.s.tokens) {
-            const int t = unit;
-            int before = 0;
-            for (int b = 0; b < p.s.batch; ++b) before += p.s.q_start[b + 1] <= t;
-            if (before >= p.s.batch) return;
-            const SequenceView sv = sequence_view(p.s, before, p.c.page_size);
-            const int i = t - sv.row0;
-            if (i < 0 || i >= sv.n_work) return;
-            const int pos = position_of(p, t, sv.len - sv.n + i);
-            // both dims of a rotation by one thread, so that q_out may be q
-            const int half = D / 2, hr = p.cos ? p.rotary_dim / 2 : 0;
-            for (int e = tid; e < p.q_heads * half; e += kAppendThreads) {
-                const int h = e / half, i2 = e % half;
-                const int d0 = i2 < hr ? i2 : 2 * i2, d1 = i2 < hr ? i2 + hr : 2 * i2 + 1;
-                const uint16_t* row = p.q + (size_t)t * p.q_stride + (size_t)h * D;
-                const float a = rotated(p, row, d0, pos), c = rotated(p, row, d1, pos);
-                uint16_t* to = p.q_out + ((size_t)t * p.q_heads + h) * D;
-                to[d0] = f32_to_bf16_rne(a);
-                to[d1] = f32_to_bf16_rne(c);
-            }
-            return;
-        }
-        unit -= p.s.tokens;
+    int before = 0;                     // sequences that end at or before t
+    for (int b0 = 0; b0 < p.s.batch; b0 += kAppendThreads) {
+        const int b = b0 + tid;
+        before += __syncthreads_count(b < p.s.batch && p.s.q_start[b + 1] <= t);
     }
-    const bool is_v = unit & 1;
-    unit >>= 1;
-    const int h = unit % p.c.num_heads;
-    unit /= p.c.num_heads;
-    const int j = unit % p.blocks_per_seq, b = unit / p.blocks_per_seq;
-    const SequenceView sv = sequence_view(p.s, b, p.c.page_size);
-    const int first = sv.len - sv.n;                        // cache index of the first new token
-    const int last = first + sv.n_work;                     // past the last one worked on
-    const int begin = max(first, 0);
-    const int blk = ((begin >> p.block_shift) + j) << p.block_shift;
-    if (blk >= last) return;
-    const int page = p.s.block_table[(size_t)b * p.s.table_cols + (blk >> p.page_shift)];
-    if (page < 0 || page >= p.c.num_pages) return;
-    const int t0 = blk & (p.c.page_size - 1);
-    uint8_t* codes = static_cast<uint8_t*>(is_v ? p.c.v : p.c.k) + page * p.c.page_stride +
-                     h * p.c.head_stride + (size_t)t0 * D;
-    float* scale = (is_v ? p.c.v_scale : p.c.k_scale) + page * p.c.scale_page_stride +
-                   h * p.c.scale_head_stride + (t0 >> p.block_shift);
-    const uint16_t* src = is_v ? p.v : p.k;
-    const long long stride = is_v ? p.v_stride : p.k_stride;
-    const int lo = max(blk, begin), hi = min(blk + p.c.block, last);
+    if (before >= p.s.batch) return;
+    const SequenceView sv = sequence_view(p.s, before, p.c.page_size);
+    const int i = t - sv.row0;
+    if (i < 0 || i >= sv.n_work) return;
+    const RowUnit u = row_unit(tid % kUnits, p.rotary_dim);
+    float c[8], s[8];
+    if (u.angle >= 0) load_angles(p, position_of(p, t, sv.len - sv.n + i), u.angle, c, s);
+    const uint16_t* src = p.q + (size_t)t * p.q_stride;
+    uint16_t* dst = p.q_out + (size_t)t * p.q_heads * D;
+#pragma unroll 2
+    for (int h = tid / kUnits; h < p.q_heads; h += kAppendThreads / kUnits) {
+        float f[16];
+        unpack8(ldg128(src + (size_t)h * D + u.a), f);
+        unpack8(ldg128(src + (size_t)h * D + u.b), f + 8);
+        if (u.angle >= 0) rotate(f, c, s);
+        uint4 x, y;
+        x.x = pack_bf16(f[0], f[1]); x.y = pack_bf16(f[2], f[3]);
+        x.z = pack_bf16(f[4], f[5]); x.w = pack_bf16(f[6], f[7]);
+        y.x = pack_bf16(f[8], f[9]); y.y = pack_bf16(f[10], f[11]);
+        y.z = pack_bf16(f[12], f[13]); y.w = pack_bf16(f[14], f[15]);
+        *reinterpret_cast<uint4*>(dst + (size_t)h * D + u.a) = x;
+        *reinterpret_cast<uint4*>(dst + (size_t)h * D + u.b) = y;
+    }
+}
 
-    auto value = [&](int index, int d) {
-        const int t = sv.row0 + index - first;
-        const uint16_t* row = src + (size_t)t * stride + (size_t)h * D;
-        return is_v ? bf16_bits_to_f32(row[d]) : rotated(p, row, d, position_of(p, t, index));
+// `team` threads (a power of two, a multiple of D / 16) take one block of one
+// head's keys or values.  The block's largest value comes first, then its
+// codes; where the block is more than one pass long its rows are read again
+// (from L1 or L2) rather than held.
+template <int D>
+__device__ __forceinline__ void append_block(const AppendParams& p, long long unit, int at, int team) {
+    constexpr int kUnits = D / 16;
+    const bool is_v = unit >= p.kv_units;
+    if (is_v) unit -= p.kv_units;
+    const bool live = unit < p.kv_units;
+    const int h = live ? (int)(unit % p.c.num_heads) : 0;
+    const long long rest = live ? unit / p.c.num_heads : 0;
+    const int j = (int)(rest % p.blocks_per_seq), b = (int)(rest / p.blocks_per_seq);
+    int lo = 0, hi = 0, blk = 0, first = 0, row0 = 0;
+    uint8_t* codes = nullptr;
+    float* scale = nullptr;
+    if (live) {
+        const SequenceView sv = sequence_view(p.s, b, p.c.page_size);
+        first = sv.len - sv.n;                              // cache index of the first new token
+        const int last = first + sv.n_work;                 // past the last one worked on
+        const int begin = max(first, 0);
+        row0 = sv.row0;
+        blk = ((begin >> p.block_shift) + j) << p.block_shift;
+        if (blk < last) {
+            const int page = p.s.block_table[(size_t)b * p.s.table_cols + (blk >> p.page_shift)];
+            if ((unsigned)page < (unsigned)p.c.num_pages) {
+                const int t0 = blk & (p.c.page_size - 1);
+                codes = static_cast<uint8_t*>(is_v ? p.c.v : p.c.k) + page * p.c.page_stride +
+                        h * p.c.head_stride + (size_t)t0 * D;
+                scale = (is_v ? p.c.v_scale : p.c.k_scale) + page * p.c.scale_page_stride +
+                        h * p.c.scale_head_stride + (t0 >> p.block_shift);
+                lo = max(blk, begin);
+                hi = min(blk + p.c.block, last);
+            }
+        }
+    }
+    const uint16_t* src = (is_v ? p.v : p.k) + (size_t)h * D;
+    const long long stride = is_v ? p.v_stride : p.k_stride;
+    const RowUnit u = row_unit(at % kUnits, is_v ? 0 : p.rotary_dim);
+    auto values = [&](int index, float (&f)[16]) {
+        const int t = row0 + index - first;
+        const uint16_t* row = src + (size_t)t * stride;
+        unpack8(ldg128(row + u.a), f);
+        unpack8(ldg128(row + u.b), f + 8);
+        if (u.angle >= 0) {
+            float c[8], s[8];
+            load_angles(p, position_of(p, t, index), u.angle, c, s);
+            rotate(f, c, s);
+        }
     };
+    const float s0 = scale ? *scale : 1.f;
+    const int step = team / kUnits;
+    float f[16];
     float amax = 0.f;
-    for (int e = tid; e < (hi - lo) * D; e += kAppendThreads) {
-        const float a = fabsf(value(lo + e / D, e % D));
-        if (a <= 3.402823466e38f) amax = fmaxf(amax, a);
+    for (int index = lo + at / kUnits; index < hi; index += step) {
+        values(index, f);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const float a = fabsf(f[k]);
+            if (a <= 3.402823466e38f) amax = fmaxf(amax, a);
+        }
     }
     __shared__ float part[kAppendThreads / 32];
-    amax = __uint_as_float(warp_max_u32(__float_as_uint(amax)));
-    if ((tid & 31) == 0) part[tid >> 5] = amax;
-    __syncthreads();
-    for (int w = 0; w < kAppendThreads / 32; ++w) amax = fmaxf(amax, part[w]);
+    for (int o = min(team, 32) / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+    if (team > 32) {
+        const int warp = threadIdx.x >> 5, w0 = warp & ~(team / 32 - 1);
+        if ((threadIdx.x & 31) == 0) part[warp] = amax;
+        __syncthreads();
+        for (int w = 0; w < team / 32; ++w) amax = fmaxf(amax, part[w0 + w]);
+    }
+    if (hi <= lo) return;
     float s1 = block_scale(amax);
-    const float s0 = *scale;
     const bool had = lo > blk;
     if (had && !(s0 < s1)) s1 = s0;
     const float inv = __frcp_rn(s1);
-    __syncthreads();
     if (had && s1 != s0)
-        for (int e = tid; e < (lo - blk) * D; e += kAppendThreads)
+        for (int e = at; e < (lo - blk) * D; e += team)
             codes[e] = (uint8_t)f32x2_to_e4m3x2(__fmul_rn(__fmul_rn(e4m3_value(codes[e]), s0), inv), 0.f);
-    for (int e = tid; e < (hi - lo) * D; e += kAppendThreads)
-        codes[(lo - blk) * D + e] =
-            (uint8_t)f32x2_to_e4m3x2(__fmul_rn(value(lo + e / D, e % D), inv), 0.f);
-    if (tid == 0) *scale = s1;
+    const bool once = hi - lo <= step;          // the values of the first pass are still held
+    for (int index = lo + at / kUnits; index < hi; index += step) {
+        if (!once) values(index, f);
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            w[k] = f32x2_to_e4m3x2(__fmul_rn(f[4 * k], inv), __fmul_rn(f[4 * k + 1], inv)) |
+                   f32x2_to_e4m3x2(__fmul_rn(f[4 * k + 2], inv), __fmul_rn(f[4 * k + 3], inv)) << 16;
+        uint8_t* row = codes + (size_t)(index - blk) * D;
+        if (u.angle >= 0) {
+            *reinterpret_cast<uint2*>(row + u.a) = make_uint2(w[0], w[1]);
+            *reinterpret_cast<uint2*>(row + u.b) = make_uint2(w[2], w[3]);
+        } else {
+            *reinterpret_cast<uint4*>(row + u.a) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+    if (at == 0) *scale = s1;
+}
+
+// grid.x: the CTAs of the blocks, then one for each token's queries.
+template <int D>
+__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_constant__ AppendParams p) {
+    griddep_wait();
+    griddep_launch_dependents();
+    if ((int)blockIdx.x >= p.kv_ctas) {
+        append_queries<D>(p, blockIdx.x - p.kv_ctas);
+    } else {
+        const int team = p.team, per = kAppendThreads / team;
+        append_block<D>(p, (long long)blockIdx.x * per + threadIdx.x / team, threadIdx.x % team, team);
+    }
+}
+
+template <int D>
+cudaError_t launch_append(const AppendParams& p, unsigned grid, cudaStream_t stream) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kAppendThreads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv_append_kernel<D>, p);
 }
 
 namespace {
@@ -230,7 +349,7 @@ extern "C" dl_status dl_kv_append(const dl_kv_cache* cache, const void* q, const
     p.cos = cos;
     p.sin = sin;
     p.positions = positions;
-    p.rotary_dim = rotary_dim;
+    p.rotary_dim = cos ? rotary_dim : 0;
     p.max_pos = cos ? max_pos : 1;
     p.q_heads = q_heads;
     p.page_shift = log2i(cache->page_size);
@@ -238,11 +357,16 @@ extern "C" dl_status dl_kv_append(const dl_kv_cache* cache, const void* q, const
     p.s = Sequences{block_table, seq_lens, q_start, table_cols, batch, tokens, max_q};
     const long long most = max_q < tokens ? max_q : tokens;
     p.blocks_per_seq = (int)((most + cache->block - 2) / cache->block + 1);
-    const long long units = (q ? tokens : 0) + 2LL * batch * p.blocks_per_seq * cache->num_heads;
-    if (units > 0x7fffffffLL)
-        return host_fail(DL_ERR_UNSUPPORTED_SHAPE, "%lld blocks to write exceed one launch", units);
-    kv_append_kernel<<<(unsigned)units, kAppendThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    // threads of a block: one for each 16 of its values, as far as a CTA goes
+    p.team = cache->block * D / 16 < kAppendThreads ? cache->block * D / 16 : kAppendThreads;
+    p.kv_units = (long long)batch * p.blocks_per_seq * cache->num_heads;
+    const int per = kAppendThreads / p.team;
+    const long long kv_ctas = (2 * p.kv_units + per - 1) / per, grid = kv_ctas + (q ? tokens : 0);
+    if (grid > 0x7fffffffLL)
+        return host_fail(DL_ERR_UNSUPPORTED_SHAPE, "%lld blocks to write exceed one launch", 2 * p.kv_units);
+    p.kv_ctas = (int)kv_ctas;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = D == 128 ? launch_append<128>(p, (unsigned)grid, st) : launch_append<64>(p, (unsigned)grid, st);
     if (e != cudaSuccess) return host_fail(DL_ERR_CUDA, "kv_append launch: %s", cudaGetErrorString(e));
     return host_ok();
 }
