@@ -5,17 +5,20 @@
 
 namespace {
 
-// Row tiles of at most 128 rows, as even as the new tokens allow.
+// Row tiles of at most kMaxRows rows, as even as the new tokens allow.  A group
+// of more heads is cut into equal parts that each read the cache.
 struct RowTiles {
-    int tokens, count, padded;
+    int parts, tokens, count, padded;
 };
 
 RowTiles row_tiles(int tokens, int max_q, int group) {
-    const int most = 128 / group, n = max_q < tokens ? max_q : tokens;
     RowTiles r;
+    r.parts = 1;
+    while (group / r.parts > dl::kMaxRows || group % r.parts) ++r.parts;
+    const int heads = group / r.parts, most = dl::kMaxRows / heads, n = max_q < tokens ? max_q : tokens;
     r.count = (n + most - 1) / most;
     r.tokens = (n + r.count - 1) / r.count;
-    r.padded = dl::attn_rows_padded(r.tokens * group);
+    r.padded = dl::attn_rows_padded(r.tokens * heads);
     return r;
 }
 
@@ -108,9 +111,10 @@ extern "C" dl_status dl_attention_paged(const dl_kv_cache* cache, const void* q,
     p.scale_page_stride = cache->scale_page_stride;
     p.scale_head_stride = cache->scale_head_stride;
     p.num_pages = cache->num_pages;
-    p.kv_heads = cache->num_heads;
+    p.head_parts = rt.parts;
+    p.kv_heads = cache->num_heads * rt.parts;
     p.q_heads = q_heads;
-    p.group = group;
+    p.group = group / rt.parts;
     p.page_size = cache->page_size;
     while ((1 << p.page_shift) < cache->page_size) ++p.page_shift;
     while ((1 << p.block_shift) < cache->block) ++p.block_shift;

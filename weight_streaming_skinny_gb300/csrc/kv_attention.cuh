@@ -9,25 +9,21 @@
 // bounds what is multiplied, and costs nothing per element.  n_r places the
 // first tile's largest P (kTarget) and moves only when one passes the top (kTop).
 //
-// Both products run on the tensor cores with tokens on the TMEM lanes:
+// Both products run as tcgen05.mma kind::f8f6f4 on the codes exactly as they
+// lie in the cache, tokens on the TMEM lanes; nothing converts keys or values:
 //     S^T [128 tokens x rows] = K [128 x D] . Q^T
 //     O^T [D x rows]         += V^T [D x 128] . P^T
-// S is kind::f8f6f4 on the codes as they lie in the cache.  A bf16 query has 8
-// significant bits and an e4m3 number 4, so a query is the sum of two e4m3 parts,
-// exact down to 2^-17 of the row's largest element (each row is scaled to the top of
-// the range).  O has two forms:
-//   up to 16 rows  kind::f8f6f4 on the codes too, P as four e4m3 parts of 16 times
-//                  each other's scale, in columns of their own: 11 bits (an fp16
-//                  step comes first) down to 2^-13 of the row's largest, 2^-21 of
-//                  it absolute below.  Nothing touches a value but the MMA: shared
-//                  memory moves 64 KB a tile, half of what the other form moves.
-//   more rows      kind::f16: values widened to fp16 (exact), P rounded to fp16:
-//                  relative 2^-12, absolute 2^-28 of the row's largest.  The
-//                  widening costs the same for any rows, the parts 7
-//                  instructions for each probability.
-// (Two parts of P would do for even weights, but leave 18 bits of range for both the
-// tokens that weigh little and a maximum that grows: moving n_r took most of the time
-// at 128 rows.)  Scores, maxima, exponentials, sums and accumulators are fp32.
+// The 16-bit side goes in as sums of e4m3 numbers of 4 significant bits.  A bf16
+// query has 8 and is the sum of two parts, exact down to 2^-17 of the row's
+// largest element (each row is scaled to the top of the range).  P is rounded to
+// fp16 and cut into parts of 16 times each other's scale, each in accumulator columns
+// of its own: four up to 16 rows, three beyond.  That is exact to fp16's 11 bits
+// near the top, to 2^-8 down to 2^-13 of the row's largest, 2^-21 of it absolute
+// below, and leaves room for the maximum to grow (by 2^9 or 2^5) before n_r has
+// to move.  (Measured against it: two parts have 18 bits of range for both, and moving
+// n_r took most of the time at 128 rows; fp16 products need the values widened in
+// shared memory, which then moves twice the bytes and bounds the kernel at 48 rows.)
+// Scores, maxima, exponentials, sums and accumulators are fp32.
 //
 // A CTA runs a contiguous range of 128-token tiles of the whole call (sequence,
 // row tile, head, tile), the same number for every CTA to within one: the work
@@ -50,7 +46,8 @@ struct AttnParams {
     float* lse;
     const float *k_scale, *v_scale;
     long long q_stride, scale_page_stride, scale_head_stride;
-    int num_pages, kv_heads, q_heads, group;
+    int num_pages, q_heads;
+    int kv_heads, head_parts, group;    // key/value heads times parts of their query heads; heads of a part
     int page_size, page_shift, block_shift;
     int tile_tokens, row_tiles;         // new tokens of a row tile, row tiles of max_q
     float scale_log2;                   // scale * log2(e)
@@ -65,7 +62,7 @@ struct AttnParams {
 struct AttnSplit {
     int n;                              // CTAs that share it, consecutive
     int slot0;                          // which of the first CTA's two slots it uses
-    int row0, rows, head;               // first token row, rows, key/value head
+    int row0, rows, head;               // first token row, rows, head (part)
 };
 
 // One row tile of a sequence.
@@ -98,43 +95,37 @@ __device__ __forceinline__ int attn_cta_of(long long total, int grid, long long 
     return (int)(((tile + 1) * grid - 1) / total);
 }
 
-// RP rows.  The softmax warpgroups are TG tile groups, which take tiles in turn
-// and have accumulators of their own, of CG column groups of RW rows each.  A
-// tile's chain of waits and dependent instructions is about as long as its share of
-// the memory's time, so two tiles are in work on an SM: two CTAs up to 16 rows, two
-// tile groups to 64; beyond, registers leave room for one tile.
+// RP rows.  A tile's chain of waits and dependent instructions is longer than its
+// share of the memory's time, so two tiles are in work on an SM: two CTAs up to 16
+// rows, beyond that one CTA whose two softmax warpgroups (TG tile groups) take
+// tiles in turn, with accumulators of their own, and share the pipeline's slots.
 template <int D_, int RP_>
 struct AttnShape {
     static constexpr int D = D_, RP = RP_;
-    static constexpr bool kParts = RP <= 16;            // P as e4m3 parts (else fp16)
-    static constexpr int TG = RP > 16 && RP <= 64 ? 2 : 1;
-    static constexpr int CG = RP > 64 ? 4 : RP > 48 ? 2 : 1;
-    static constexpr int NWG = TG * CG;
-    static constexpr int RW = RP / CG;
-    static constexpr bool kConcat = kParts;             // S columns: hi parts, then lo parts
+    static constexpr int kParts = RP <= 16 ? 4 : 3;
+    static constexpr int TG = RP > 16 ? 2 : 1;
+    static constexpr bool kConcat = RP <= 48;           // S columns: hi parts, then lo parts (else summed by the MMA)
     static constexpr int kScoreCols = kConcat ? 2 * RP : RP;
     static constexpr int kOutCol = 2 * kScoreCols;
-    static constexpr int kOutCols = kParts ? 4 * RP : RP;
+    static constexpr int kOutCols = kParts * RP;
     static constexpr int kCols = kOutCol + TG * kOutCols;
     static constexpr int kTmem = kCols <= 32 ? 32 : kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
-    static constexpr int kCtas = kParts ? 2 : 1;        // resident CTAs per SM
-    static constexpr int kThreads = NWG * 128 + 96;
+    static constexpr int kCtas = 3 - TG;                // resident CTAs per SM
+    static constexpr int kThreads = TG * 128 + 96;
     static constexpr int kTileBytes = kTile * D;        // codes of K, and of V
     static constexpr int kQBytes = 2 * RP * D;
-    static constexpr int kPBytes = kOutCols * kTile * (kParts ? 1 : 2);
-    static constexpr int kVBytes = kParts ? 0 : kTile * D * 2;      // widened values
-    static constexpr int kPBufs = RP < 96 ? 2 : 1, kVBufs = 2;
-    static constexpr int kMisc = 1024 + RP * (8 + 8 * TG) + NWG * 4 * RW * 4 + D * 4 + 256;
+    static constexpr int kPBytes = kOutCols * kTile;    // one of two buffers
+    static constexpr int kMisc = 1024 + RP * (16 + 16 * TG) + TG * 4 * RP * 4 + D * 4 + 256;
     static constexpr int kBudget = (kCtas == 1 ? 227 : 113) * 1024;
-    // a tile's slot: its codes, and 16 bytes a token of values made from the scales
-    static constexpr int kPairBytes = 2 * kTileBytes + kTile * 16;
-    static constexpr int kRoom = kBudget - 1024 - kQBytes - kPBufs * kPBytes - kVBufs * kVBytes - kMisc;
-    static constexpr int kKeySlots = kRoom / kPairBytes > 6 ? 6 : kRoom / kPairBytes;
-    static constexpr int kMore = kRoom - kKeySlots * kPairBytes >= kTileBytes + kTile * 16 ? 1 : 0;
-    static constexpr int kValueSlots = kKeySlots + kMore;
-    static constexpr size_t kSmem = 1024 + (size_t)kKeySlots * kTileBytes + (size_t)kValueSlots * (kTileBytes + kTile * 16) +
-                                    kQBytes + kPBufs * kPBytes + kVBufs * kVBytes + kMisc;
-    static_assert(kKeySlots >= 2, "two tiles in flight");
+    // a tile's slots: its codes, and 8 bytes of scales for each token
+    static constexpr int kScaleBytes = kTile * 8;
+    static constexpr int kRoom = kBudget - 1024 - kQBytes - 2 * kPBytes - kMisc;
+    static constexpr int kFit = kRoom / (2 * kTileBytes + kScaleBytes);
+    static constexpr int kKeySlots = kFit > 6 ? 6 : kFit;
+    static constexpr int kValueSlots = kKeySlots + (kRoom - kKeySlots * (2 * kTileBytes + kScaleBytes) >= kTileBytes + kScaleBytes);
+    static constexpr size_t kSmem = 1024 + (size_t)kKeySlots * kTileBytes + (size_t)kValueSlots * (kTileBytes + kScaleBytes) +
+                                    kQBytes + 2 * kPBytes + kMisc;
+    static_assert(kKeySlots >= 2 && kCols <= 512 && kCols * kCtas <= 512 && kOutCols <= 256, "fits an SM");
 };
 
 // ---------------------------------------------------------------- device helpers
@@ -155,19 +146,17 @@ __device__ __forceinline__ uint64_t umma_desc(uint32_t saddr, uint32_t lead, uin
            (uint64_t)1 << 46 | (uint64_t)layout << 61;
 }
 
-// Instruction descriptor, M x N with an fp32 accumulator: e4m3 x e4m3 for
-// kind::f8f6f4, fp16 x fp16 for kind::f16; mn = 1: both operands have their M / N
-// dimension contiguous in memory.
+// Instruction descriptor of kind::f8f6f4, e4m3 x e4m3 -> fp32, M x N; mn = 1:
+// both operands have their M / N dimension contiguous in memory.
 __host__ __device__ constexpr uint32_t umma_idesc(int m, int n, int mn) {
     return (1u << 4) | (mn ? 3u << 15 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-// D[taddr] (+)= A . B^T for one K step of 16, fp16 operands.
-__device__ __forceinline__ void umma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                         uint32_t accumulate) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                 ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
 }
 
 template <int N>
@@ -276,27 +265,32 @@ __device__ __forceinline__ void lds_f2x2(const float* p, F2& a, F2& b) {
     b = v.y;
 }
 
-// Four probabilities -> their four e4m3 parts, each the rest of the one before
-// times 16.  The fp16 step in between rounds to 2^-11.
-__device__ __forceinline__ void split_e4m3(const float (&e)[4], uint32_t (&part)[4]) {
+// Four probabilities -> their e4m3 parts, each the rest of the one before times 16.
+// The fp16 step in between rounds to 2^-11.
+template <int N>
+__device__ __forceinline__ void split_e4m3(float e0, float e1, float e2, float e3, uint32_t (&part)[N]) {
     constexpr uint32_t kSixteen = 0x4C004C00u;          // f16x2
-    uint32_t x = f32x2_to_f16x2(e[0], e[1]), y = f32x2_to_f16x2(e[2], e[3]);
+    uint32_t x = f32x2_to_f16x2(e0, e1), y = f32x2_to_f16x2(e2, e3);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N; ++i) {
+        uint32_t u, v;
         asm("{\n\t"
             ".reg .b16 a, b;\n\t"
-            ".reg .b32 u, v;\n\t"
-            "cvt.rn.satfinite.e4m3x2.f16x2 a, %1;\n\t"
-            "cvt.rn.satfinite.e4m3x2.f16x2 b, %2;\n\t"
-            "cvt.rn.f16x2.e4m3x2 u, a;\n\t"
-            "cvt.rn.f16x2.e4m3x2 v, b;\n\t"
-            "sub.rn.f16x2 u, %1, u;\n\t"
-            "sub.rn.f16x2 v, %2, v;\n\t"
-            "mul.rn.f16x2 %1, u, %3;\n\t"
-            "mul.rn.f16x2 %2, v, %3;\n\t"
+            "cvt.rn.satfinite.e4m3x2.f16x2 a, %3;\n\t"
+            "cvt.rn.satfinite.e4m3x2.f16x2 b, %4;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %1, a;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %2, b;\n\t"
             "mov.b32 %0, {a, b};\n\t"
             "}"
-            : "=r"(part[i]), "+r"(x), "+r"(y) : "r"(kSixteen));
+            : "=r"(part[i]), "=r"(u), "=r"(v) : "r"(x), "r"(y));
+        if (i + 1 < N)
+            asm("{\n\t"
+                "sub.rn.f16x2 %0, %0, %2;\n\t"
+                "sub.rn.f16x2 %1, %1, %3;\n\t"
+                "mul.rn.f16x2 %0, %0, %4;\n\t"
+                "mul.rn.f16x2 %1, %1, %4;\n\t"
+                "}"
+                : "+r"(x), "+r"(y) : "r"(u), "r"(v), "r"(kSixteen));
     }
 }
 
@@ -391,33 +385,31 @@ struct AttnWalk {
 
 // ---------------------------------------------------------------- the kernel
 
-// What the softmax needs of a token, from its scales: c * ks, log2 vs, 1 / vs
-// (< 0: the token is absent) and a factor of P, 1 but for scales below 2^-60.
-struct __align__(16) TokenScales {
-    float key, log_value, inv_value, fix;
+// The scales of a token's blocks; value < 0: the token is absent.
+struct __align__(8) TokenScales {
+    float key, value;
 };
 
 template <class C>
 __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                  const __grid_constant__ AttnParams p) {
-    constexpr int D = C::D, RP = C::RP, RW = C::RW, TG = C::TG, CG = C::CG, NWG = C::NWG;
+    constexpr int D = C::D, RP = C::RP, TG = C::TG;
     constexpr int NK = C::kKeySlots, NV = C::kValueSlots;
-    constexpr int kProducer = NWG * 4, kMma = NWG * 4 + 1, kScaler = NWG * 4 + 2;
-    constexpr int kAllBar = NWG + 1, kSoftmax = NWG * 128;
+    constexpr int kProducer = TG * 4, kMma = TG * 4 + 1, kScaler = TG * 4 + 2;
+    constexpr int kAllBar = TG + 1, kSoftmax = TG * 128;
     // one accumulator lane per dim: M = 64 leaves 16 rows in each warp's lanes
     constexpr int kDimLanes = D / 4;
     constexpr uint32_t kSwizzle = D == 128 ? 2 : 4;
-    // largest exponent of a probability (log2 448 = 8.807; fp16 ends at 2^16), and the one a maximum gets
-    constexpr float kTop = C::kParts ? 8.8f : 15.9f, kTarget = C::kParts ? -1.f : 3.f;
+    // largest exponent of a probability (log2 448 = 8.807), and the one a maximum gets
+    constexpr float kTop = 8.8f, kTarget = C::kParts == 4 ? -1.f : 3.f;
     constexpr float kTinyScale = 8.67361737988403547e-19f;       // 2^-60
 
     extern __shared__ unsigned char smem_raw[];
     unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    unsigned char* sp = base;                                     // P [rows / 16 bytes][128 tokens][16 bytes]
-    unsigned char* sq = sp + C::kPBufs * C::kPBytes;              // query parts [2][RP][D]
-    unsigned char* sv = sq + C::kQBytes;                          // widened values [dims / 64][128 tokens][64]
-    unsigned char* keys = sv + C::kVBufs * C::kVBytes;            // codes, [128 tokens][D] each
+    unsigned char* sp = base;                                     // [2] P [columns / 16][128 tokens][16]
+    unsigned char* sq = sp + 2 * C::kPBytes;                      // query parts [2][RP][D]
+    unsigned char* keys = sq + C::kQBytes;                        // codes, [128 tokens][D] each
     unsigned char* values = keys + NK * C::kTileBytes;
     TokenScales* scales = reinterpret_cast<TokenScales*>(values + NV * C::kTileBytes);   // [NV][128]
     unsigned char* misc = reinterpret_cast<unsigned char*>(scales + NV * kTile);
@@ -427,14 +419,16 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 1);
     int* s_stop = reinterpret_cast<int*>(tmem_slot + 1);
     long long* s_walk = reinterpret_cast<long long*>(misc + 512);     // total, begin, end, entry, within
-    int* s_force = reinterpret_cast<int*>(misc + 576);                // [NWG] a row has no n_r yet
+    int* s_force = reinterpret_cast<int*>(misc + 576);                // [TG] a row has no n_r yet
     int* s_flags = reinterpret_cast<int*>(misc + 640);                // [NV] kAbsent: some token is, kTiny: some scale is
     float* s_qs = reinterpret_cast<float*>(misc + 1024);              // [RP] a row's query scale
     int* s_lim = reinterpret_cast<int*>(s_qs + RP);                   // [RP] cached tokens a row sees
-    float* s_n = reinterpret_cast<float*>(s_lim + RP);                // [TG][RP] n_r
+    long long* s_out = reinterpret_cast<long long*>(s_lim + RP);      // [RP] a row's place among tokens x heads
+    float* s_n = reinterpret_cast<float*>(s_out + RP);                // [TG][RP] n_r
     float* s_l = s_n + TG * RP;                                       // [TG][RP] sums of P / vs
-    float* s_red = s_l + TG * RP;                                     // [NWG][4][RW]
-    int* s_nan = reinterpret_cast<int*>(s_red + NWG * 4 * RW);        // [D] first NaN among the new tokens' values
+    float* s_f = s_l + TG * RP;                                       // [TG][RP] factors of the accumulators
+    float* s_red = s_f + TG * RP;                                     // [TG][4][RP]
+    int* s_nan = reinterpret_cast<int*>(s_red + TG * 4 * RP);         // [D] first NaN among the new tokens' values
     constexpr int kAbsent = 1, kTiny = 2;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -448,14 +442,14 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
             }
             for (int i = 0; i < NV; ++i) {
                 mbar_init(smem_u32(v_full + i), 2);                    // the codes, the scales
-                mbar_init(smem_u32(v_empty + i), C::kParts ? 1 : CG * 4);
+                mbar_init(smem_u32(v_empty + i), 1);
             }
             for (int i = 0; i < 2; ++i) {
                 mbar_init(smem_u32(s_full + i), 1);
-                mbar_init(smem_u32(p_full + i), CG * 4);
+                mbar_init(smem_u32(p_full + i), 4);
                 mbar_init(smem_u32(pv_done + i), 1);
             }
-            mbar_init(smem_u32(q_full), NWG * 4);
+            mbar_init(smem_u32(q_full), TG * 4);
             *s_stop = 0;
             fence_mbarrier_init();
         }
@@ -544,7 +538,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                 __syncwarp();
                 if (page >= 0 && !is_v)
                     tma_load_4d(smem_u32(keys + ks * C::kTileBytes + sub * box * D), &tk, smem_u32(k_full + ks), 0, at,
-                                w.head, page);
+                                w.head / p.head_parts, page);
                 if (it >= NV) ok = __all_sync(~0u, wait(smem_u32(v_empty + vs), (it / NV - 1) & 1, kErrProducerWait));
                 if (!ok) {
                     mbar_wait_bounded(smem_u32(k_full + ks), (it / NK) & 1, wait.ctl, kErrDrainWait);
@@ -554,7 +548,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                 __syncwarp();
                 if (page >= 0 && is_v)
                     tma_load_4d(smem_u32(values + vs * C::kTileBytes + sub * box * D), &tv, smem_u32(v_full + vs), 0, at,
-                                w.head, page);
+                                w.head / p.head_parts, page);
                 page = next;
             }
         } while (ok && w.next(p));
@@ -572,6 +566,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
         bool ok = true;
         do {
             const int* table = p.s.block_table + (size_t)w.entry.b * p.s.table_cols;
+            const int head = w.head / p.head_parts;
             auto pages_of = [&](int tile, int (&pg)[4]) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -587,7 +582,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                     b[k] = -1.f;
                     if ((unsigned)pg[k] < (unsigned)p.num_pages) {
                         const int t = (tile * kTile + 32 * k + lane) & (p.page_size - 1);
-                        const long long o = pg[k] * p.scale_page_stride + w.head * p.scale_head_stride + (t >> p.block_shift);
+                        const long long o = pg[k] * p.scale_page_stride + head * p.scale_head_stride + (t >> p.block_shift);
                         a[k] = p.k_scale[o];
                         b[k] = p.v_scale[o];
                     }
@@ -610,11 +605,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const bool absent = (unsigned)pg[k] >= (unsigned)p.num_pages;
-                    const bool tiny = !absent && b[k] < kTinyScale;
-                    const float used = absent ? 1.f : tiny ? kTinyScale : b[k];
-                    flags |= (absent ? kAbsent : 0) | (tiny ? kTiny : 0);
-                    scales[s * kTile + 32 * k + lane] =
-                        TokenScales{a[k], log2_fast(used), absent ? -1.f : __frcp_rn(used), tiny ? b[k] * (1.f / kTinyScale) : 1.f};
+                    flags |= absent ? kAbsent : b[k] < kTinyScale ? kTiny : 0;
+                    scales[s * kTile + 32 * k + lane] = TokenScales{a[k], b[k]};
                 }
                 flags = __reduce_or_sync(~0u, flags);
                 if (lane == 0) s_flags[s] = flags;
@@ -630,66 +622,64 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
             }
         } while (ok && w.next(p));
     } else if (work && warp == kMma) {
-        // ------------------------------------------------ products, issued by one lane
-        if (lane == 0) {
-            constexpr uint32_t kScoreIdesc = umma_idesc(128, C::kScoreCols, 0);
-            constexpr uint32_t kOutIdesc = umma_idesc(D, C::kOutCols, 1);
-            const uint32_t q0 = smem_u32(sq);
-            int it = 0, seg = 0;
-            bool ok = true;
-            auto scores = [&](int i) {
-                if (!wait(smem_u32(k_full + i % NK), (i / NK) & 1, kErrConsumerWait)) return false;
-                tc_fence_after_sync();
-                const uint32_t k0 = smem_u32(keys + i % NK * C::kTileBytes);
-                const uint32_t d = tmem + (i & 1) * C::kScoreCols;
+        // ------------------------------------------------ products: the warp waits, one lane issues
+        constexpr uint32_t kScoreIdesc = umma_idesc(128, C::kScoreCols, 0);
+        constexpr uint32_t kOutIdesc = umma_idesc(D, C::kOutCols, 1);
+        const bool leader = elect_one();
+        const uint64_t q_desc = umma_desc(smem_u32(sq), 16, 8 * D, kSwizzle);
+        const uint64_t k_desc = umma_desc(smem_u32(keys), 16, 8 * D, kSwizzle);
+        const uint64_t v_desc = umma_desc(smem_u32(values), 16, 8 * D, kSwizzle);
+        const uint64_t p_desc = umma_desc(smem_u32(sp), 128, kTile * 16, 0);
+        int it = 0, seg = 0;
+        bool ok = true;
+        auto scores = [&](int i) {
+            const int s = i % NK;
+            if (!__all_sync(~0u, wait(smem_u32(k_full + s), (i / NK) & 1, kErrConsumerWait))) return false;
+            tc_fence_after_sync();
+            const uint64_t a = k_desc + (uint32_t)(s * C::kTileBytes >> 4);
+            const uint32_t d = tmem + (i & 1) * C::kScoreCols;
+            if (leader) {
 #pragma unroll
                 for (int part = 0; part < (C::kConcat ? 1 : 2); ++part)
 #pragma unroll
                     for (int k = 0; k < D / 32; ++k)
-                        umma_e4m3(d, umma_desc(k0 + 32 * k, 16, 8 * D, kSwizzle),
-                                  umma_desc(q0 + part * RP * D + 32 * k, 16, 8 * D, kSwizzle), kScoreIdesc,
-                                  part > 0 || k > 0);
+                        umma_e4m3(d, a + 2 * k, q_desc + (part * RP * D >> 4) + 2 * k, kScoreIdesc, part > 0 || k > 0);
                 umma_commit(smem_u32(s_full + (i & 1)));
-                umma_commit(smem_u32(k_empty + i % NK));
-                return true;
-            };
-            do {
-                ok = wait(smem_u32(q_full), seg & 1, kErrConsumerWait) && scores(it);
-                for (int tile = w.tile0; tile < w.tile1 && ok; ++tile, ++it) {
-                    if (tile + 1 < w.tile1 && !(ok = scores(it + 1))) break;
-                    if (!(ok = wait(smem_u32(p_full + (it & 1)), (it >> 1) & 1, kErrConsumerWait))) break;
-                    tc_fence_after_sync();
-                    const uint32_t p0 = smem_u32(sp + it % C::kPBufs * C::kPBytes);
-                    const uint32_t o = tmem + C::kOutCol + (TG == 2 ? (it & 1) * C::kOutCols : 0);
-                    const bool more = tile - w.tile0 >= TG;          // this accumulator holds something
-                    if constexpr (C::kParts) {
-                        const uint32_t v0 = smem_u32(values + it % NV * C::kTileBytes);
+                umma_commit(smem_u32(k_empty + s));
+            }
+            __syncwarp();
+            return true;
+        };
+        do {
+            ok = __all_sync(~0u, wait(smem_u32(q_full), seg & 1, kErrConsumerWait)) && scores(it);
+            for (int tile = w.tile0; tile < w.tile1 && ok; ++tile, ++it) {
+                if (tile + 1 < w.tile1 && !(ok = scores(it + 1))) break;
+                if (!(ok = __all_sync(~0u, wait(smem_u32(p_full + (it & 1)), (it >> 1) & 1, kErrConsumerWait)))) break;
+                tc_fence_after_sync();
+                const int s = it % NV;
+                const uint64_t a = v_desc + (uint32_t)(s * C::kTileBytes >> 4);
+                const uint64_t b = p_desc + (uint32_t)((it & 1) * C::kPBytes >> 4);
+                const uint32_t o = tmem + C::kOutCol + (TG == 2 ? (it & 1) * C::kOutCols : 0);
+                const uint32_t more = tile - w.tile0 >= TG;      // this accumulator holds something
+                if (leader) {
 #pragma unroll
-                        for (int k = 0; k < kTile / 32; ++k)
-                            umma_e4m3(o, umma_desc(v0 + k * 32 * D, 16, 8 * D, kSwizzle),
-                                      umma_desc(p0 + k * 32 * 16, 128, kTile * 16, 0), kOutIdesc, more || k > 0);
-                        umma_commit(smem_u32(v_empty + it % NV));
-                    } else {
-                        const uint32_t v0 = smem_u32(sv + it % C::kVBufs * C::kVBytes);
-#pragma unroll
-                        for (int k = 0; k < kTile / 16; ++k)
-                            umma_f16(o, umma_desc(v0 + k * 16 * 128, kTile * 128, 1024, 2),
-                                     umma_desc(p0 + k * 16 * 16, 128, kTile * 16, 0), kOutIdesc, more || k > 0);
-                    }
+                    for (int k = 0; k < kTile / 32; ++k)
+                        umma_e4m3(o, a + k * (32 * D >> 4), b + k * 32, kOutIdesc, k > 0 ? 1u : more);
                     umma_commit(smem_u32(pv_done + (it & 1)));
+                    umma_commit(smem_u32(v_empty + s));
                 }
-                ++seg;
-            } while (ok && w.next(p));
-        }
-        __syncwarp();
+                __syncwarp();
+            }
+            ++seg;
+        } while (ok && w.next(p));
     } else if (work && warp < kProducer) {
         // ------------------------------------------------ softmax: a token each thread
         // (a wait that gives up is not left by: the others of the group are at its barriers)
-        const int wg = warp >> 2, wq = warp & 3, tl = tid & 127, bar_id = 1 + wg;
-        const int tg = wg / CG, r0 = wg % CG * RW;          // tile group, first row
+        const int tg = warp >> 2, wq = warp & 3, tl = tid & 127, bar_id = 1 + tg;
         const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
-        float* red = s_red + wg * 4 * RW;
-        float* my_n = s_n + tg * RP + r0;
+        const uint32_t out_at = lanes + C::kOutCol + tg * C::kOutCols;
+        float* red = s_red + tg * 4 * RP;
+        float* my_n = s_n + tg * RP;
         int it0 = 0;                                        // the segment's first tile, counted by the CTA
         int slot = 0;
         auto pv_wait = [&](int i) {         // the product of tile i has been made
@@ -752,89 +742,95 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                                        __uint_as_float((uint32_t)(127 + (e - 7) - (e - 7) / 2) << 23);
                     s_qs[row] = row < rows ? (odd ? __uint_as_float(0x7fffffffu) : down * p.scale_log2) : 0.f;
                     s_lim[row] = row < rows ? max(en.seen0 + i, 0) : 0;
+                    s_out[row] = (long long)(en.row0 + i) * p.q_heads + w.head * p.group + g;
                 }
             }
             if (tid < D) s_nan[tid] = 0x7fffffff;
-            if (tl < RW) my_n[tl] = 0.f;
-            if (tl == 0) s_force[wg] = 1;
+            if (tl < RP) my_n[tl] = 0.f;
+            if (tl == 0) s_force[tg] = 1;
             fence_proxy_async_smem();
             group_sync(kAllBar, kSoftmax);
             if (lane == 0) mbar_arrive(smem_u32(q_full));
 
-            F2 l[RW / 2];
+            F2 l[RP / 2];
 #pragma unroll
-            for (int r = 0; r < RW / 2; ++r) l[r] = 0;
-            uint32_t unset = ~0u;            // threads below RW: this row has no n_r yet
+            for (int r = 0; r < RP / 2; ++r) l[r] = 0;
+            uint32_t unset = ~0u;            // threads below RP: this row has no n_r yet
             const int t_first = TG == 2 ? (it0 + tg) & 1 : 0;       // the group's tiles have its parity
             for (int t = t_first; t < tiles; t += TG) {
                 const int it = it0 + t, tile = w.tile0 + t, j = tile * kTile + tl;
                 wait(smem_u32(v_full + it % NV), (it / NV) & 1, kErrConsumerWait);
                 const TokenScales ts = scales[it % NV * kTile + tl];
                 const int flags = s_flags[it % NV];
-                const bool absent = ts.inv_value < 0.f;
+                const bool absent = ts.value < 0.f;
+                const float value = absent ? 1.f : ts.value < kTinyScale ? kTinyScale : ts.value;
+                const float lv = log2_fast(value), inv = __fdividef(1.f, value);
                 const bool masked = (tile + 1) * kTile > en.seen_first || (flags & kAbsent);
 
                 // exponents t + n
                 wait(smem_u32(s_full + (it & 1)), (it >> 1) & 1, kErrConsumerWait);
                 tc_fence_after_sync();
-                float d[RW];
-                const uint32_t sc = lanes + (it & 1) * C::kScoreCols + r0;
-                if constexpr (C::kConcat) {
-                    float both[2 * RP];
+                float d[RP];
+                const uint32_t sc = lanes + (it & 1) * C::kScoreCols;
+                const F2 ks2 = f2(ts.key, ts.key), lv2 = f2(lv, lv);
+                constexpr int kStep = RP < 16 ? 8 : 16;
+                {
+                    float lo[RP];
 #pragma unroll
-                    for (int r = 0; r < 2 * RP; r += 16) tmem_ld<16>(sc + r, both + r);
+                    for (int r = 0; r < RP; r += kStep) {
+                        tmem_ld<kStep>(sc + r, d + r);
+                        if (C::kConcat) tmem_ld<kStep>(sc + RP + r, lo + r);
+                    }
                     tmem_wait_ld();
 #pragma unroll
-                    for (int r = 0; r < RW; ++r) d[r] = both[r] + both[RP + r];
-                } else {
-#pragma unroll
-                    for (int r = 0; r + 16 <= RW; r += 16) tmem_ld<16>(sc + r, d + r);
-                    if constexpr (RW % 16) tmem_ld<8>(sc + RW - 8, d + RW - 8);
-                    tmem_wait_ld();
-                }
-                const F2 ks2 = f2(ts.key, ts.key), lv2 = f2(ts.log_value, ts.log_value);
-#pragma unroll
-                for (int r = 0; r < RW; r += 4) {
-                    F2 q0, q1, n0, n1;
-                    lds_f2x2(s_qs + r0 + r, q0, q1);
-                    lds_f2x2(my_n + r, n0, n1);
-                    unpack(add2(fma2(mul2(f2(d[r], d[r + 1]), q0), ks2, lv2), n0), d[r], d[r + 1]);
-                    unpack(add2(fma2(mul2(f2(d[r + 2], d[r + 3]), q1), ks2, lv2), n1), d[r + 2], d[r + 3]);
+                    for (int r = 0; r < RP; r += 4) {
+                        F2 q0, q1, n0, n1, x0 = f2(d[r], d[r + 1]), x1 = f2(d[r + 2], d[r + 3]);
+                        lds_f2x2(s_qs + r, q0, q1);
+                        lds_f2x2(my_n + r, n0, n1);
+                        if (C::kConcat) {
+                            x0 = add2(x0, f2(lo[r], lo[r + 1]));
+                            x1 = add2(x1, f2(lo[r + 2], lo[r + 3]));
+                        }
+                        unpack(add2(fma2(mul2(x0, q0), ks2, lv2), n0), d[r], d[r + 1]);
+                        unpack(add2(fma2(mul2(x1, q1), ks2, lv2), n1), d[r + 2], d[r + 3]);
+                    }
                 }
                 if (masked) {
+                    // new token i, rows i * group on, sees cache indexes below seen0 + i
+                    const int from = absent ? RP : max(min(j - en.seen0 + 1, RP), 0) * p.group;
 #pragma unroll
-                    for (int r = 0; r < RW; ++r)
-                        if (absent || j >= s_lim[r0 + r]) d[r] = -INFINITY;
+                    for (int r = 0; r < RP; ++r)
+                        if (r < from) d[r] = -INFINITY;
                 }
                 float top = -INFINITY;
 #pragma unroll
-                for (int r = 0; r < RW; r += 2) top = max3(top, d[r], d[r + 1]);
+                for (int r = 0; r < RP; r += 2) top = max3(top, d[r], d[r + 1]);
                 // a row passes the top, or has no n_r yet: its n_r moves, and its sums follow
-                if (group_any(bar_id, 128, top > kTop || (tl == 0 && s_force[wg]))) {
+                if (group_any(bar_id, 128, top > kTop || (tl == 0 && s_force[tg]))) {
                     float m0 = 0.f;
 #pragma unroll
-                    for (int r = 0; r < RW; ++r) {
+                    for (int r = 0; r < RP; ++r) {
                         const float m = warp_max_f32(d[r]);
                         if (lane == (r & 31)) m0 = m;
-                        if ((r & 31) == 31 || r == RW - 1)
-                            if (lane <= (r & 31)) red[wq * RW + (r & ~31) + lane] = m0;
+                        if ((r & 31) == 31 || r == RP - 1)
+                            if (lane <= (r & 31)) red[wq * RP + (r & ~31) + lane] = m0;
                     }
                     group_sync(bar_id, 128);
                     float move = 0.f;
-                    if (tl < RW) {
-                        const float m = fmaxf(fmaxf(red[tl], red[RW + tl]), fmaxf(red[2 * RW + tl], red[3 * RW + tl]));
+                    if (tl < RP) {
+                        const float m = fmaxf(fmaxf(red[tl], red[RP + tl]), fmaxf(red[2 * RP + tl], red[3 * RP + tl]));
                         if (m > -INFINITY && (m > kTop || unset)) {
                             move = kTarget - m;
                             my_n[tl] += move;
                             unset = 0;
                         }
                     }
-                    const bool more = group_any(bar_id, 128, tl < RW && unset && r0 + tl < rows);
-                    if (tl < RW) red[tl] = move;
-                    if (tl == 0) s_force[wg] = more;
+                    const bool more = group_any(bar_id, 128, tl < RP && unset && tl < rows);
+                    if (tl < RP) red[tl] = move;
+                    if (tl == 0) s_force[tg] = more;
                     group_sync(bar_id, 128);
 #pragma unroll
-                    for (int r = 0; r < RW; r += 4) {
+                    for (int r = 0; r < RP; r += 4) {
                         const float4 x = *reinterpret_cast<const float4*>(red + r);
                         d[r] = min_nan(d[r] + x.x, kTop);
                         d[r + 1] = min_nan(d[r + 1] + x.y, kTop);
@@ -847,7 +843,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                         pv_wait(it - TG);
                         tc_fence_after_sync();
 #pragma unroll 1
-                        for (int r = 0; r < RW; r += 8) {
+                        for (int r = 0; r < RP; r += 8) {
                             float f[8], o[8];
                             bool same = true;
 #pragma unroll
@@ -857,107 +853,74 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                             }
                             if (same) continue;
 #pragma unroll 1
-                            for (int part = 0; part < (C::kParts ? 4 : 1); ++part) {
-                                const uint32_t at = lanes + C::kOutCol + tg * C::kOutCols + part * RP + r0 + r;
-                                tmem_ld<8>(at, o);
+                            for (int part = 0; part < C::kParts; ++part) {
+                                tmem_ld<8>(out_at + part * RP + r, o);
                                 tmem_wait_ld();
 #pragma unroll
                                 for (int k = 0; k < 8; ++k) o[k] *= shrink(f[k]);
-                                tmem_st8(at, o);
+                                tmem_st8(out_at + part * RP + r, o);
                             }
                         }
                         tmem_wait_st();
                     }
                 }
 
-                // this token's values: what some row must not see is taken out -- all of an absent
-                // token, and NaN codes of the new tokens (0 x NaN would reach every row), which
-                // are noted by dim -- and, for fp16 products, they are widened
-                unsigned char* codes = values + it % NV * C::kTileBytes + tl * D;
-                constexpr int kChunks = D / 16 / CG;
-                const int c0 = wg % CG * kChunks;
-                auto at_chunk = [&](int c) {
-                    return reinterpret_cast<uint4*>(codes + (D == 128 ? (c ^ (tl & 7)) : (c ^ ((tl >> 1) & 3))) * 16);
-                };
-                if (!C::kParts || masked) {
-                    if (!C::kParts) pv_wait(it - C::kVBufs);
-                    constexpr int kBatch = kChunks < 4 ? kChunks : 4;   // loads before the first store
-                    unsigned char* wide = C::kParts ? nullptr : sv + it % C::kVBufs * C::kVBytes + tl * 128;
-#pragma unroll
-                    for (int i0 = 0; i0 < kChunks; i0 += kBatch) {
-                        uint4 x[kBatch];
-#pragma unroll
-                        for (int i = 0; i < kBatch; ++i) x[i] = *at_chunk(c0 + i0 + i);
-                        if (masked) {
-#pragma unroll
-                            for (int i = 0; i < kBatch; ++i) {
-                                const int c = c0 + i0 + i;
-                                if (absent) {
-                                    x[i] = make_uint4(0, 0, 0, 0);
-                                } else if (j >= en.seen_first) {
-                                    uint32_t* word = &x[i].x;
-#pragma unroll
-                                    for (int k = 0; k < 4; ++k) {
-                                        const uint32_t bad = __vcmpeq4(word[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                                        word[k] &= ~bad;
-                                        for (int m = 0; bad && m < 4; ++m)
-                                            if (bad >> (8 * m) & 1) atomicMin(s_nan + 16 * c + 4 * k + m, j);
-                                    }
-                                }
-                                if (C::kParts) *at_chunk(c) = x[i];
-                            }
+                // values that some row must not see are taken out: all of an absent token, and NaN codes
+                // of the new tokens (0 x NaN would reach every row), which are noted by dim
+                if (masked && (absent || j >= en.seen_first)) {
+                    unsigned char* codes = values + it % NV * C::kTileBytes + tl * D;
+#pragma unroll 1
+                    for (int c = 0; c < D / 16; ++c) {
+                        uint4* at = reinterpret_cast<uint4*>(codes + c * 16);
+                        if (absent) {
+                            *at = make_uint4(0, 0, 0, 0);
+                            continue;
                         }
-                        if constexpr (!C::kParts) {
+                        uint4 x = *at;
+                        uint32_t* word = &x.x;
+                        uint32_t any = 0;
 #pragma unroll
-                            for (int i = 0; i < kBatch; ++i) {
-                                const int c = c0 + i0 + i, q = c % 4 * 2;
-                                uint32_t h[8];
-                                e4m3x4_to_f16x2x2(x[i].x, h[0], h[1]);
-                                e4m3x4_to_f16x2x2(x[i].y, h[2], h[3]);
-                                e4m3x4_to_f16x2x2(x[i].z, h[4], h[5]);
-                                e4m3x4_to_f16x2x2(x[i].w, h[6], h[7]);
-                                unsigned char* to = wide + c / 4 * (kTile * 128);
-                                sts128(smem_u32(to + ((q ^ (tl & 7)) * 16)), h[0], h[1], h[2], h[3]);
-                                sts128(smem_u32(to + (((q + 1) ^ (tl & 7)) * 16)), h[4], h[5], h[6], h[7]);
-                            }
+                        for (int k = 0; k < 4; ++k) any |= (word[k] & 0x7f7f7f7fu) + 0x01010101u;
+                        if (!(any & 0x80808080u)) continue;
+                        const int dims = (D == 128 ? (c ^ (tl & 7)) : (c ^ ((tl >> 1) & 3))) * 16;
+#pragma unroll 1
+                        for (int k = 0; k < 16; ++k) {
+                            unsigned char* byte = codes + c * 16 + k;
+                            if ((*byte & 0x7f) != 0x7f) continue;
+                            *byte = 0;
+                            atomicMin(s_nan + dims + k, j);
                         }
-                    }
-                    if constexpr (!C::kParts) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(v_empty + it % NV));
                     }
                 }
 
-                // probabilities
-                if (C::kParts || C::kPBufs < C::kVBufs) pv_wait(it - C::kPBufs);
-                unsigned char* dst = sp + it % C::kPBufs * C::kPBytes + tl * 16;
-                const F2 inv2 = f2(ts.inv_value, ts.inv_value);
+                // probabilities, cut into parts: columns of part i, then row, 16 to a chunk of 2 KB
+                pv_wait(it - 2);
+                unsigned char* dst = sp + (it & 1) * C::kPBytes + tl * 16;
+                const F2 inv2 = f2(inv, inv);
+                const float fix = ts.value < kTinyScale ? ts.value * (1.f / kTinyScale) : 1.f;
 #pragma unroll
-                for (int r = 0; r < RW; r += 8) {
-                    float e[8];
+                for (int r = 0; r < RP; r += kStep) {
+                    uint32_t part[kStep / 4][C::kParts];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) e[k] = exp2_fast(d[r + k]);
+                    for (int k = 0; k < kStep; k += 4) {
+                        float e[4];
 #pragma unroll
-                    for (int k = 0; k < 8; k += 2) l[(r + k) / 2] = fma2(f2(e[k], e[k + 1]), inv2, l[(r + k) / 2]);
-                    if (flags & kTiny)
+                        for (int m = 0; m < 4; ++m) e[m] = exp2_fast(d[r + k + m]);
+                        l[(r + k) / 2] = fma2(f2(e[0], e[1]), inv2, l[(r + k) / 2]);
+                        l[(r + k) / 2 + 1] = fma2(f2(e[2], e[3]), inv2, l[(r + k) / 2 + 1]);
+                        if (flags & kTiny) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) e[k] *= ts.fix;
-                    if constexpr (C::kParts) {
-                        // columns: RP of each part, 16 to a chunk of 2 KB
-                        uint32_t a[4], b[4];
-                        split_e4m3({e[0], e[1], e[2], e[3]}, a);
-                        split_e4m3({e[4], e[5], e[6], e[7]}, b);
-                        if constexpr (RP == 8) {
-                            sts128(smem_u32(dst), a[0], b[0], a[1], b[1]);
-                            sts128(smem_u32(dst + kTile * 16), a[2], b[2], a[3], b[3]);
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                *reinterpret_cast<uint2*>(dst + k * (kTile * 16) + r) = make_uint2(a[k], b[k]);
+                            for (int m = 0; m < 4; ++m) e[m] *= fix;
                         }
+                        split_e4m3<C::kParts>(e[0], e[1], e[2], e[3], part[k / 4]);
+                    }
+                    if constexpr (RP == 8) {
+                        sts128(smem_u32(dst), part[0][0], part[1][0], part[0][1], part[1][1]);
+                        sts128(smem_u32(dst + kTile * 16), part[0][2], part[1][2], part[0][3], part[1][3]);
                     } else {
-                        sts128(smem_u32(dst + (r0 + r) / 8 * (kTile * 16)), f32x2_to_f16x2(e[0], e[1]), f32x2_to_f16x2(e[2], e[3]),
-                               f32x2_to_f16x2(e[4], e[5]), f32x2_to_f16x2(e[6], e[7]));
+#pragma unroll
+                        for (int i = 0; i < C::kParts; ++i)
+                            sts128(smem_u32(dst + (i * RP + r) / 16 * (kTile * 16)), part[0][i], part[1][i], part[2][i], part[3][i]);
                     }
                 }
                 fence_proxy_async_smem();
@@ -968,72 +931,79 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
 
             // ---------------------------------------- the segment's sums
 #pragma unroll
-            for (int r = 0; r < RW; r += 8) {
+            for (int r = 0; r < RP; r += 8) {
                 float v[8];
 #pragma unroll
                 for (int k = 0; k < 8; k += 2) unpack(l[(r + k) / 2], v[k], v[k + 1]);
                 warp_sums<8>(v, lane);
                 if (r == 0) group_sync(bar_id, 128);         // red: the last moves have been read
-                if (lane % 4 == 0) red[wq * RW + r + lane_value<8>(lane)] = v[0];
+                if (lane % 4 == 0) red[wq * RP + r + lane_value<8>(lane)] = v[0];
             }
             group_sync(bar_id, 128);
-            if (tl < RW)
-                s_l[tg * RP + r0 + tl] = (red[tl] + red[RW + tl]) + (red[2 * RW + tl] + red[3 * RW + tl]);
+            if (tl < RP) s_l[tg * RP + tl] = (red[tl] + red[RP + tl]) + (red[2 * RP + tl] + red[3 * RP + tl]);
             it0 += tiles;
+            if (TG == 2) group_sync(kAllBar, kSoftmax);
+            const bool whole = w.whole();
+            const int cta_slot = blockIdx.x * 2 + slot;
+            if (tid < RP) {
+                // a row's sum over the tile groups, and what its accumulators count for; a group whose
+                // sum is 0 saw nothing (or had no tile: its accumulator is stale)
+                float sum = s_l[tid], n = s_n[tid], f0 = sum == 0.f ? 0.f : 1.f, f1 = 0.f;
+                if (TG == 2) {
+                    const float l0 = sum, l1 = s_l[RP + tid], n1 = s_n[RP + tid];
+                    const float least = l0 == 0.f ? n1 : l1 == 0.f ? n : fminf(n, n1);
+                    f0 = l0 == 0.f ? 0.f : exp2_fast(least - n);
+                    f1 = l1 == 0.f ? 0.f : exp2_fast(least - n1);
+                    sum = l0 * f0 + l1 * f1;
+                    n = least;
+                }
+                if (whole) {
+                    const float scale = sum == 0.f ? 0.f : 1.f / sum;
+                    f0 *= scale;
+                    f1 *= scale;
+                    if (p.lse && tid < rows) p.lse[s_out[tid]] = sum == 0.f ? -INFINITY : (log2f(sum) - n) * 0.693147180559945f;
+                } else {
+                    float* ps = p.partial + (size_t)gridDim.x * 2 * RP * D + ((size_t)cta_slot * RP + tid) * 2;
+                    ps[0] = sum == 0.f ? INFINITY : n;           // nothing seen here
+                    ps[1] = sum;
+                }
+                s_f[tid] = f0;
+                if (TG == 2) s_f[RP + tid] = f1;
+            }
             pv_wait(it0 - 1);
             if (TG == 2) pv_wait(it0 - 2);
             tc_fence_after_sync();
             group_sync(kAllBar, kSoftmax);
-            const bool whole = w.whole();
-            const int cta_slot = blockIdx.x * 2 + slot;
             const int dim = wq * kDimLanes + lane;
             const int nan_from = lane < kDimLanes ? s_nan[dim] : 0x7fffffff;
-            float* po = p.partial + (size_t)cta_slot * RP * D;
-            float* ps = p.partial + (size_t)gridDim.x * 2 * RP * D + (size_t)cta_slot * RP * 2;
+            float* po = p.partial + (size_t)cta_slot * RP * D + dim;
 #pragma unroll 1
-            for (int r = wg * 8; r < rows; r += NWG * 8) {
-                float a[8], b[8] = {};
-                tmem_ld<8>(lanes + C::kOutCol + r, a);
-                if constexpr (C::kParts) {
-                    float c[8], e[8];
-                    tmem_ld<8>(lanes + C::kOutCol + RP + r, b);
-                    tmem_ld<8>(lanes + C::kOutCol + 2 * RP + r, c);
-                    tmem_ld<8>(lanes + C::kOutCol + 3 * RP + r, e);
+            for (int r = tg * 8; r < rows; r += TG * 8) {
+                float o[8] = {};
+#pragma unroll
+                for (int g = 0; g < TG; ++g) {
+                    float x[C::kParts][8];
+#pragma unroll
+                    for (int i = 0; i < C::kParts; ++i) tmem_ld<8>(lanes + C::kOutCol + g * C::kOutCols + i * RP + r, x[i]);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        a[k] = fmaf(fmaf(fmaf(e[k], 1.f / 16, c[k]), 1.f / 16, b[k]), 1.f / 16, a[k]);
-                } else {
-                    if (TG == 2) tmem_ld<8>(lanes + C::kOutCol + C::kOutCols + r, b);
-                    tmem_wait_ld();
+                    for (int k = 0; k < 8; ++k) {
+                        float y = x[C::kParts - 1][k];
+#pragma unroll
+                        for (int i = C::kParts - 2; i >= 0; --i) y = fmaf(y, 1.f / 16, x[i][k]);
+                        const float f = s_f[g * RP + r + k];
+                        if (f != 0.f) o[k] = fmaf(y, f, o[k]);
+                    }
                 }
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     const int row = r + k;
-                    if (row >= rows) break;
-                    float sum = s_l[row], n = s_n[row], o = a[k];
-                    if (TG == 2) {
-                        // a group whose sum is 0 saw nothing (or had no tile: its accumulator is stale)
-                        const float l0 = sum, l1 = s_l[RP + row], n1 = s_n[RP + row];
-                        const float least = fminf(l0 == 0.f ? n1 : n, l1 == 0.f ? n : n1);
-                        const float f0 = l0 == 0.f ? 0.f : exp2_fast(least - n), f1 = l1 == 0.f ? 0.f : exp2_fast(least - n1);
-                        o = (l0 == 0.f ? 0.f : a[k] * f0) + (l1 == 0.f ? 0.f : b[k] * f1);
-                        sum = l0 * f0 + l1 * f1;
-                        n = least;
-                    }
-                    if (nan_from < s_lim[row]) o = __uint_as_float(0x7fffffffu);
-                    const int i = row / p.group, g = row - i * p.group;
-                    const size_t at = (size_t)(en.row0 + i) * p.q_heads + w.head * p.group + g;
-                    if (whole) {
-                        if (lane < kDimLanes) p.out[at * D + dim] = f32_to_bf16_rne(sum == 0.f ? 0.f : o / sum);
-                        if (p.lse && wq == 0 && lane == 0)
-                            p.lse[at] = sum == 0.f ? -INFINITY : (log2f(sum) - n) * 0.693147180559945f;
-                    } else {
-                        if (lane < kDimLanes) po[(size_t)row * D + dim] = o;
-                        if (wq == 0 && lane == 0) {
-                            ps[2 * row] = sum == 0.f ? INFINITY : n;           // nothing seen here
-                            ps[2 * row + 1] = sum;
-                        }
+                    if (nan_from < s_lim[row]) o[k] = __uint_as_float(0x7fffffffu);
+                    if (row < rows && lane < kDimLanes) {
+                        if (whole)
+                            p.out[s_out[row] * D + dim] = f32_to_bf16_rne(o[k]);
+                        else
+                            po[row * D] = o[k];
                     }
                 }
             }
@@ -1128,12 +1098,9 @@ struct AttnLaunch {
     cudaStream_t stream;
 };
 
-// RP, resident CTAs per SM of the instance for `rows` rows.
-inline int attn_rows_padded(int rows) {
-    for (int rp : {8, 16, 32, 48, 64, 96, 128})
-        if (rows <= rp) return rp;
-    return 0;
-}
+// RP and resident CTAs per SM of the instance for `rows` rows (at most kMaxRows).
+constexpr int kMaxRows = 64;
+inline int attn_rows_padded(int rows) { return rows <= 8 ? 8 : rows <= 48 ? (rows + 15) / 16 * 16 : 64; }
 inline int attn_ctas_per_sm(int rp) { return rp > 16 ? 1 : 2; }
 
 cudaError_t launch_attention_d64(int rp, const AttnLaunch& a);

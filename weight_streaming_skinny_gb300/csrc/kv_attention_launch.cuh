@@ -49,8 +49,6 @@ cudaError_t launch_attention_dim(int rp, const AttnLaunch& a) {
         case 32: return launch_attention_instance<AttnShape<D, 32>>(a);
         case 48: return launch_attention_instance<AttnShape<D, 48>>(a);
         case 64: return launch_attention_instance<AttnShape<D, 64>>(a);
-        case 96: return launch_attention_instance<AttnShape<D, 96>>(a);
-        case 128: return launch_attention_instance<AttnShape<D, 128>>(a);
         default: return cudaErrorInvalidValue;
     }
 }
