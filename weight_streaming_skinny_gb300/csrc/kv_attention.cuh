@@ -273,17 +273,16 @@ __device__ __forceinline__ void split_e4m3(float e0, float e1, float e2, float e
     uint32_t x = f32x2_to_f16x2(e0, e1), y = f32x2_to_f16x2(e2, e3);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        uint32_t u, v;
         asm("{\n\t"
             ".reg .b16 a, b;\n\t"
-            "cvt.rn.satfinite.e4m3x2.f16x2 a, %3;\n\t"
-            "cvt.rn.satfinite.e4m3x2.f16x2 b, %4;\n\t"
-            "cvt.rn.f16x2.e4m3x2 %1, a;\n\t"
-            "cvt.rn.f16x2.e4m3x2 %2, b;\n\t"
+            "cvt.rn.satfinite.e4m3x2.f16x2 a, %1;\n\t"
+            "cvt.rn.satfinite.e4m3x2.f16x2 b, %2;\n\t"
             "mov.b32 %0, {a, b};\n\t"
             "}"
-            : "=r"(part[i]), "=r"(u), "=r"(v) : "r"(x), "r"(y));
-        if (i + 1 < N)
+            : "=r"(part[i]) : "r"(x), "r"(y));
+        if (i + 1 < N) {
+            uint32_t u, v;
+            e4m3x4_to_f16x2x2(part[i], u, v);
             asm("{\n\t"
                 "sub.rn.f16x2 %0, %0, %2;\n\t"
                 "sub.rn.f16x2 %1, %1, %3;\n\t"
@@ -291,6 +290,7 @@ __device__ __forceinline__ void split_e4m3(float e0, float e1, float e2, float e
                 "mul.rn.f16x2 %1, %1, %4;\n\t"
                 "}"
                 : "+r"(x), "+r"(y) : "r"(u), "r"(v), "r"(kSixteen));
+        }
     }
 }
 
@@ -415,7 +415,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     unsigned char* misc = reinterpret_cast<unsigned char*>(scales + NV * kTile);
     uint64_t* bars = reinterpret_cast<uint64_t*>(misc);
     uint64_t *k_full = bars, *k_empty = k_full + NK, *v_full = k_empty + NK, *v_empty = v_full + NV,
-             *s_full = v_empty + NV, *p_full = s_full + 2, *pv_done = p_full + 2, *q_full = pv_done + 2;
+             *s_full = v_empty + NV, *s_read = s_full + 2, *p_full = s_read + 2, *pv_done = p_full + 2, *q_full = pv_done + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 1);
     int* s_stop = reinterpret_cast<int*>(tmem_slot + 1);
     long long* s_walk = reinterpret_cast<long long*>(misc + 512);     // total, begin, end, entry, within
@@ -446,6 +446,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
             }
             for (int i = 0; i < 2; ++i) {
                 mbar_init(smem_u32(s_full + i), 1);
+                mbar_init(smem_u32(s_read + i), 4);
                 mbar_init(smem_u32(p_full + i), 4);
                 mbar_init(smem_u32(pv_done + i), 1);
             }
@@ -651,9 +652,13 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
             return true;
         };
         do {
-            ok = __all_sync(~0u, wait(smem_u32(q_full), seg & 1, kErrConsumerWait)) && scores(it);
+            // scores run two tiles ahead: as soon as those of the tile before in their buffer are read
+            ok = __all_sync(~0u, wait(smem_u32(q_full), seg & 1, kErrConsumerWait)) && scores(it) &&
+                 (w.tile0 + 1 >= w.tile1 || scores(it + 1));
             for (int tile = w.tile0; tile < w.tile1 && ok; ++tile, ++it) {
-                if (tile + 1 < w.tile1 && !(ok = scores(it + 1))) break;
+                if (tile + 2 < w.tile1 &&
+                    !(ok = __all_sync(~0u, wait(smem_u32(s_read + (it & 1)), (it >> 1) & 1, kErrConsumerWait)) && scores(it + 2)))
+                    break;
                 if (!(ok = __all_sync(~0u, wait(smem_u32(p_full + (it & 1)), (it >> 1) & 1, kErrConsumerWait)))) break;
                 tc_fence_after_sync();
                 const int s = it % NV;
@@ -782,6 +787,9 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                         if (C::kConcat) tmem_ld<kStep>(sc + RP + r, lo + r);
                     }
                     tmem_wait_ld();
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(s_read + (it & 1)));
 #pragma unroll
                     for (int r = 0; r < RP; r += 4) {
                         F2 q0, q1, n0, n1, x0 = f2(d[r], d[r + 1]), x1 = f2(d[r + 2], d[r + 3]);
