@@ -97,13 +97,16 @@ __device__ __forceinline__ int attn_cta_of(long long total, int grid, long long 
 
 // RP rows.  A tile's chain of waits and dependent instructions is longer than its
 // share of the memory's time, so two tiles are in work on an SM: two CTAs up to 16
-// rows, beyond that one CTA whose two softmax warpgroups (TG tile groups) take
-// tiles in turn, with accumulators of their own, and share the pipeline's slots.
+// rows, beyond that one CTA whose two tile groups (TG) take tiles in turn, with
+// accumulators of their own, and share the pipeline's slots.  A tile group is CG
+// warpgroups of RW rows each: more warps to hide one another's latencies.
 template <int D_, int RP_>
 struct AttnShape {
     static constexpr int D = D_, RP = RP_;
     static constexpr int kParts = RP <= 16 ? 4 : 3;
     static constexpr int TG = RP > 16 ? 2 : 1;
+    static constexpr int CG = RP > 32 ? 2 : 1;
+    static constexpr int RW = RP / CG;
     static constexpr bool kConcat = RP <= 48;           // S columns: hi parts, then lo parts (else summed by the MMA)
     static constexpr int kScoreCols = kConcat ? 2 * RP : RP;
     static constexpr int kOutCol = 2 * kScoreCols;
@@ -111,7 +114,7 @@ struct AttnShape {
     static constexpr int kCols = kOutCol + TG * kOutCols;
     static constexpr int kTmem = kCols <= 32 ? 32 : kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
     static constexpr int kCtas = 3 - TG;                // resident CTAs per SM
-    static constexpr int kThreads = TG * 128 + 96;
+    static constexpr int kThreads = TG * CG * 128 + 96;
     static constexpr int kTileBytes = kTile * D;        // codes of K, and of V
     static constexpr int kQBytes = 2 * RP * D;
     static constexpr int kPBytes = kOutCols * kTile;    // one of two buffers
@@ -394,10 +397,10 @@ template <class C>
 __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                  const __grid_constant__ AttnParams p) {
-    constexpr int D = C::D, RP = C::RP, TG = C::TG;
+    constexpr int D = C::D, RP = C::RP, RW = C::RW, TG = C::TG, CG = C::CG, NWG = TG * CG;
     constexpr int NK = C::kKeySlots, NV = C::kValueSlots;
-    constexpr int kProducer = TG * 4, kMma = TG * 4 + 1, kScaler = TG * 4 + 2;
-    constexpr int kAllBar = TG + 1, kSoftmax = TG * 128;
+    constexpr int kProducer = NWG * 4, kMma = NWG * 4 + 1, kScaler = NWG * 4 + 2;
+    constexpr int kAllBar = NWG + 1, kSoftmax = NWG * 128;
     // one accumulator lane per dim: M = 64 leaves 16 rows in each warp's lanes
     constexpr int kDimLanes = D / 4;
     constexpr uint32_t kSwizzle = D == 128 ? 2 : 4;
@@ -419,7 +422,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 1);
     int* s_stop = reinterpret_cast<int*>(tmem_slot + 1);
     long long* s_walk = reinterpret_cast<long long*>(misc + 512);     // total, begin, end, entry, within
-    int* s_force = reinterpret_cast<int*>(misc + 576);                // [TG] a row has no n_r yet
+    int* s_force = reinterpret_cast<int*>(misc + 576);                // [NWG] a row has no n_r yet
     int* s_flags = reinterpret_cast<int*>(misc + 640);                // [NV] kAbsent: some token is, kTiny: some scale is
     float* s_qs = reinterpret_cast<float*>(misc + 1024);              // [RP] a row's query scale
     int* s_lim = reinterpret_cast<int*>(s_qs + RP);                   // [RP] cached tokens a row sees
@@ -427,7 +430,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     float* s_n = reinterpret_cast<float*>(s_out + RP);                // [TG][RP] n_r
     float* s_l = s_n + TG * RP;                                       // [TG][RP] sums of P / vs
     float* s_f = s_l + TG * RP;                                       // [TG][RP] factors of the accumulators
-    float* s_red = s_f + TG * RP;                                     // [TG][4][RP]
+    float* s_red = s_f + TG * RP;                                     // [NWG][4][RW]
     int* s_nan = reinterpret_cast<int*>(s_red + TG * 4 * RP);         // [D] first NaN among the new tokens' values
     constexpr int kAbsent = 1, kTiny = 2;
 
@@ -446,11 +449,11 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
             }
             for (int i = 0; i < 2; ++i) {
                 mbar_init(smem_u32(s_full + i), 1);
-                mbar_init(smem_u32(s_read + i), 4);
-                mbar_init(smem_u32(p_full + i), 4);
+                mbar_init(smem_u32(s_read + i), CG * 4);
+                mbar_init(smem_u32(p_full + i), CG * 4);
                 mbar_init(smem_u32(pv_done + i), 1);
             }
-            mbar_init(smem_u32(q_full), TG * 4);
+            mbar_init(smem_u32(q_full), NWG * 4);
             *s_stop = 0;
             fence_mbarrier_init();
         }
@@ -680,11 +683,12 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     } else if (work && warp < kProducer) {
         // ------------------------------------------------ softmax: a token each thread
         // (a wait that gives up is not left by: the others of the group are at its barriers)
-        const int tg = warp >> 2, wq = warp & 3, tl = tid & 127, bar_id = 1 + tg;
+        const int wg = warp >> 2, wq = warp & 3, tl = tid & 127, bar_id = 1 + wg;
+        const int tg = wg / CG, r0 = wg % CG * RW;          // tile group, first row
         const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
-        const uint32_t out_at = lanes + C::kOutCol + tg * C::kOutCols;
-        float* red = s_red + tg * 4 * RP;
-        float* my_n = s_n + tg * RP;
+        const uint32_t out_at = lanes + C::kOutCol + tg * C::kOutCols + r0;
+        float* red = s_red + wg * 4 * RW;
+        float* my_n = s_n + tg * RP + r0;
         int it0 = 0;                                        // the segment's first tile, counted by the CTA
         int slot = 0;
         auto pv_wait = [&](int i) {         // the product of tile i has been made
@@ -751,16 +755,16 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                 }
             }
             if (tid < D) s_nan[tid] = 0x7fffffff;
-            if (tl < RP) my_n[tl] = 0.f;
-            if (tl == 0) s_force[tg] = 1;
+            if (tl < RW) my_n[tl] = 0.f;
+            if (tl == 0) s_force[wg] = 1;
             fence_proxy_async_smem();
             group_sync(kAllBar, kSoftmax);
             if (lane == 0) mbar_arrive(smem_u32(q_full));
 
-            F2 l[RP / 2];
+            F2 l[RW / 2];
 #pragma unroll
-            for (int r = 0; r < RP / 2; ++r) l[r] = 0;
-            uint32_t unset = ~0u;            // threads below RP: this row has no n_r yet
+            for (int r = 0; r < RW / 2; ++r) l[r] = 0;
+            uint32_t unset = ~0u;            // threads below RW: this row has no n_r yet
             const int t_first = TG == 2 ? (it0 + tg) & 1 : 0;       // the group's tiles have its parity
             for (int t = t_first; t < tiles; t += TG) {
                 const int it = it0 + t, tile = w.tile0 + t, j = tile * kTile + tl;
@@ -775,14 +779,14 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                 // exponents t + n
                 wait(smem_u32(s_full + (it & 1)), (it >> 1) & 1, kErrConsumerWait);
                 tc_fence_after_sync();
-                float d[RP];
-                const uint32_t sc = lanes + (it & 1) * C::kScoreCols;
+                float d[RW];
+                const uint32_t sc = lanes + (it & 1) * C::kScoreCols + r0;
                 const F2 ks2 = f2(ts.key, ts.key), lv2 = f2(lv, lv);
-                constexpr int kStep = RP < 16 ? 8 : 16;
+                constexpr int kStep = RW % 16 ? 8 : 16;
                 {
-                    float lo[RP];
+                    float lo[RW];
 #pragma unroll
-                    for (int r = 0; r < RP; r += kStep) {
+                    for (int r = 0; r < RW; r += kStep) {
                         tmem_ld<kStep>(sc + r, d + r);
                         if (C::kConcat) tmem_ld<kStep>(sc + RP + r, lo + r);
                     }
@@ -791,9 +795,9 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(s_read + (it & 1)));
 #pragma unroll
-                    for (int r = 0; r < RP; r += 4) {
+                    for (int r = 0; r < RW; r += 4) {
                         F2 q0, q1, n0, n1, x0 = f2(d[r], d[r + 1]), x1 = f2(d[r + 2], d[r + 3]);
-                        lds_f2x2(s_qs + r, q0, q1);
+                        lds_f2x2(s_qs + r0 + r, q0, q1);
                         lds_f2x2(my_n + r, n0, n1);
                         if (C::kConcat) {
                             x0 = add2(x0, f2(lo[r], lo[r + 1]));
@@ -805,40 +809,40 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                 }
                 if (masked) {
                     // new token i, rows i * group on, sees cache indexes below seen0 + i
-                    const int from = absent ? RP : max(min(j - en.seen0 + 1, RP), 0) * p.group;
+                    const int from = absent ? RP : max(min(j - en.seen0 + 1, RP), 0) * p.group - r0;
 #pragma unroll
-                    for (int r = 0; r < RP; ++r)
+                    for (int r = 0; r < RW; ++r)
                         if (r < from) d[r] = -INFINITY;
                 }
                 float top = -INFINITY;
 #pragma unroll
-                for (int r = 0; r < RP; r += 2) top = max3(top, d[r], d[r + 1]);
+                for (int r = 0; r < RW; r += 2) top = max3(top, d[r], d[r + 1]);
                 // a row passes the top, or has no n_r yet: its n_r moves, and its sums follow
-                if (group_any(bar_id, 128, top > kTop || (tl == 0 && s_force[tg]))) {
+                if (group_any(bar_id, 128, top > kTop || (tl == 0 && s_force[wg]))) {
                     float m0 = 0.f;
 #pragma unroll
-                    for (int r = 0; r < RP; ++r) {
+                    for (int r = 0; r < RW; ++r) {
                         const float m = warp_max_f32(d[r]);
                         if (lane == (r & 31)) m0 = m;
-                        if ((r & 31) == 31 || r == RP - 1)
-                            if (lane <= (r & 31)) red[wq * RP + (r & ~31) + lane] = m0;
+                        if ((r & 31) == 31 || r == RW - 1)
+                            if (lane <= (r & 31)) red[wq * RW + (r & ~31) + lane] = m0;
                     }
                     group_sync(bar_id, 128);
                     float move = 0.f;
-                    if (tl < RP) {
-                        const float m = fmaxf(fmaxf(red[tl], red[RP + tl]), fmaxf(red[2 * RP + tl], red[3 * RP + tl]));
+                    if (tl < RW) {
+                        const float m = fmaxf(fmaxf(red[tl], red[RW + tl]), fmaxf(red[2 * RW + tl], red[3 * RW + tl]));
                         if (m > -INFINITY && (m > kTop || unset)) {
                             move = kTarget - m;
                             my_n[tl] += move;
                             unset = 0;
                         }
                     }
-                    const bool more = group_any(bar_id, 128, tl < RP && unset && tl < rows);
-                    if (tl < RP) red[tl] = move;
-                    if (tl == 0) s_force[tg] = more;
+                    const bool more = group_any(bar_id, 128, tl < RW && unset && r0 + tl < rows);
+                    if (tl < RW) red[tl] = move;
+                    if (tl == 0) s_force[wg] = more;
                     group_sync(bar_id, 128);
 #pragma unroll
-                    for (int r = 0; r < RP; r += 4) {
+                    for (int r = 0; r < RW; r += 4) {
                         const float4 x = *reinterpret_cast<const float4*>(red + r);
                         d[r] = min_nan(d[r] + x.x, kTop);
                         d[r + 1] = min_nan(d[r + 1] + x.y, kTop);
@@ -851,7 +855,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                         pv_wait(it - TG);
                         tc_fence_after_sync();
 #pragma unroll 1
-                        for (int r = 0; r < RP; r += 8) {
+                        for (int r = 0; r < RW; r += 8) {
                             float f[8], o[8];
                             bool same = true;
 #pragma unroll
@@ -878,7 +882,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                 if (masked && (absent || j >= en.seen_first)) {
                     unsigned char* codes = values + it % NV * C::kTileBytes + tl * D;
 #pragma unroll 1
-                    for (int c = 0; c < D / 16; ++c) {
+                    for (int c = wg % CG; c < D / 16; c += CG) {
                         uint4* at = reinterpret_cast<uint4*>(codes + c * 16);
                         if (absent) {
                             *at = make_uint4(0, 0, 0, 0);
@@ -907,7 +911,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                 const F2 inv2 = f2(inv, inv);
                 const float fix = ts.value < kTinyScale ? ts.value * (1.f / kTinyScale) : 1.f;
 #pragma unroll
-                for (int r = 0; r < RP; r += kStep) {
+                for (int r = 0; r < RW; r += kStep) {
                     uint32_t part[kStep / 4][C::kParts];
 #pragma unroll
                     for (int k = 0; k < kStep; k += 4) {
@@ -927,8 +931,14 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                         sts128(smem_u32(dst + kTile * 16), part[0][2], part[1][2], part[0][3], part[1][3]);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < C::kParts; ++i)
-                            sts128(smem_u32(dst + (i * RP + r) / 16 * (kTile * 16)), part[0][i], part[1][i], part[2][i], part[3][i]);
+                        for (int i = 0; i < C::kParts; ++i) {
+                            const int col = i * RP + r0 + r;
+                            unsigned char* to = dst + col / 16 * (kTile * 16);
+                            if constexpr (kStep == 16)
+                                sts128(smem_u32(to), part[0][i], part[1][i], part[2][i], part[3][i]);
+                            else
+                                *reinterpret_cast<uint2*>(to + col % 16) = make_uint2(part[0][i], part[1][i]);
+                        }
                     }
                 }
                 fence_proxy_async_smem();
@@ -939,18 +949,18 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
 
             // ---------------------------------------- the segment's sums
 #pragma unroll
-            for (int r = 0; r < RP; r += 8) {
+            for (int r = 0; r < RW; r += 8) {
                 float v[8];
 #pragma unroll
                 for (int k = 0; k < 8; k += 2) unpack(l[(r + k) / 2], v[k], v[k + 1]);
                 warp_sums<8>(v, lane);
                 if (r == 0) group_sync(bar_id, 128);         // red: the last moves have been read
-                if (lane % 4 == 0) red[wq * RP + r + lane_value<8>(lane)] = v[0];
+                if (lane % 4 == 0) red[wq * RW + r + lane_value<8>(lane)] = v[0];
             }
             group_sync(bar_id, 128);
-            if (tl < RP) s_l[tg * RP + tl] = (red[tl] + red[RP + tl]) + (red[2 * RP + tl] + red[3 * RP + tl]);
+            if (tl < RW) s_l[tg * RP + r0 + tl] = (red[tl] + red[RW + tl]) + (red[2 * RW + tl] + red[3 * RW + tl]);
             it0 += tiles;
-            if (TG == 2) group_sync(kAllBar, kSoftmax);
+            if (NWG > 1) group_sync(kAllBar, kSoftmax);
             const bool whole = w.whole();
             const int cta_slot = blockIdx.x * 2 + slot;
             if (tid < RP) {
@@ -986,7 +996,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
             const int nan_from = lane < kDimLanes ? s_nan[dim] : 0x7fffffff;
             float* po = p.partial + (size_t)cta_slot * RP * D + dim;
 #pragma unroll 1
-            for (int r = tg * 8; r < rows; r += TG * 8) {
+            for (int r = wg * 8; r < rows; r += NWG * 8) {
                 float o[8] = {};
 #pragma unroll
                 for (int g = 0; g < TG; ++g) {
