@@ -87,13 +87,27 @@ __device__ __forceinline__ AttnEntry attn_entry(const AttnParams& p, int e) {
     return r;
 }
 
-// The tiles [begin(c), begin(c + 1)) of CTA c, and the CTA of a tile.
-__device__ __forceinline__ long long attn_begin(long long total, int grid, int c) {
-    return total * c / grid;
-}
-__device__ __forceinline__ int attn_cta_of(long long total, int grid, long long tile) {
-    return (int)(((tile + 1) * grid - 1) / total);
-}
+// The tiles of the call dealt to `grid` CTAs in runs of equal length, the first
+// `more` of them one longer.
+struct AttnShare {
+    long long each;
+    int more;
+    __device__ __forceinline__ AttnShare(long long total, int grid) {
+        if (total >> 31) {
+            each = total / grid;
+            more = (int)(total % grid);
+        } else {                        // 32-bit division is several times faster
+            const unsigned q = (unsigned)total / (unsigned)grid;
+            each = q;
+            more = (int)((unsigned)total - q * (unsigned)grid);
+        }
+    }
+    __device__ __forceinline__ long long begin(int c) const { return c * each + min(c, more); }
+    __device__ __forceinline__ int cta_of(long long tile) const {
+        const long long head = more * (each + 1);
+        return tile < head ? (int)(tile / (each + 1)) : more + (int)((tile - head) / each);
+    }
+};
 
 // RP rows.  A tile's chain of waits and dependent instructions is longer than its
 // share of the memory's time, so two tiles are in work on an SM: two CTAs up to 16
@@ -107,7 +121,7 @@ struct AttnShape {
     static constexpr int TG = RP > 16 ? 2 : 1;
     static constexpr int CG = RP > 32 ? 2 : 1;
     static constexpr int RW = RP / CG;
-    static constexpr bool kConcat = RP <= 48;           // S columns: hi parts, then lo parts (else summed by the MMA)
+    static constexpr bool kConcat = RP <= 32;           // S columns: hi parts, then lo parts (else summed by the MMA)
     static constexpr int kScoreCols = kConcat ? 2 * RP : RP;
     static constexpr int kOutCol = 2 * kScoreCols;
     static constexpr int kOutCols = kParts * RP;
@@ -362,13 +376,13 @@ struct AttnWalk {
         item_begin = at - tile0;
     }
     // `within`: tiles of entry e before `at`
-    __device__ __forceinline__ void start(const AttnParams& p, long long at_, long long end_, int e_, long long within) {
+    __device__ __forceinline__ void start(const AttnEntry& entry_, long long at_, long long end_, int e_, int within) {
         at = at_;
         end = end_;
         e = e_;
-        entry = attn_entry(p, e);
-        head = (int)(within / entry.tiles);
-        tile0 = (int)(within - (long long)head * entry.tiles);
+        entry = entry_;
+        head = (int)((unsigned)within / (unsigned)entry.tiles);
+        tile0 = (int)within - head * entry.tiles;
         item();
     }
     __device__ __forceinline__ bool next(const AttnParams& p) {
@@ -409,7 +423,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     constexpr float kTinyScale = 8.67361737988403547e-19f;       // 2^-60
 
     extern __shared__ unsigned char smem_raw[];
-    unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    // (an offset, not a rounded pointer: the compiler keeps seeing shared memory)
+    unsigned char* base = smem_raw + (-smem_u32(smem_raw) & 1023);
     unsigned char* sp = base;                                     // [2] P [columns / 16][128 tokens][16]
     unsigned char* sq = sp + 2 * C::kPBytes;                      // query parts [2][RP][D]
     unsigned char* keys = sq + C::kQBytes;                        // codes, [128 tokens][D] each
@@ -421,8 +436,10 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
              *s_full = v_empty + NV, *s_read = s_full + 2, *p_full = s_read + 2, *pv_done = p_full + 2, *q_full = pv_done + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 1);
     int* s_stop = reinterpret_cast<int*>(tmem_slot + 1);
-    long long* s_walk = reinterpret_cast<long long*>(misc + 512);     // total, begin, end, entry, within
-    int* s_force = reinterpret_cast<int*>(misc + 576);                // [NWG] a row has no n_r yet
+    long long* s_walk = reinterpret_cast<long long*>(misc + 512);     // total, begin, end
+    int* s_start = reinterpret_cast<int*>(misc + 536);                // first entry, tiles of it before `begin`
+    AttnEntry* s_entry = reinterpret_cast<AttnEntry*>(misc + 544);
+    int* s_force = reinterpret_cast<int*>(misc + 608);                // [NWG] a row has no n_r yet
     int* s_flags = reinterpret_cast<int*>(misc + 640);                // [NV] kAbsent: some token is, kTiny: some scale is
     float* s_qs = reinterpret_cast<float*>(misc + 1024);              // [RP] a row's query scale
     int* s_lim = reinterpret_cast<int*>(s_qs + RP);                   // [RP] cached tokens a row sees
@@ -467,31 +484,55 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     griddep_wait();
     griddep_launch_dependents();
     if (warp == 0) {
-        // the CTA's tiles, and the entry in which they begin
+        // the CTA's tiles, and the entry in which they begin: entries 32 at a time, the first
+        // kHeld of them read once
+        constexpr int kHeld = 4;
         const int entries = p.s.batch * p.row_tiles;
+        AttnEntry held[kHeld];
         long long total = 0;
-        for (int e = lane; e < entries; e += 32) total += attn_entry(p, e).tiles;
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            held[i].tiles = 0;
+            if (32 * i + lane < entries) held[i] = attn_entry(p, 32 * i + lane);
+            total += held[i].tiles;
+        }
+        for (int e = 32 * kHeld + lane; e < entries; e += 32) total += attn_entry(p, e).tiles;
         for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
         total *= p.kv_heads;
         const int grid = total < gridDim.x ? (int)total : (int)gridDim.x;
-        long long begin = 0, end = 0, within = 0;
-        int found = -1;
+        long long begin = 0, end = 0;
+        bool found = false;
         if ((int)blockIdx.x < grid) {
-            begin = attn_begin(total, grid, blockIdx.x);
-            end = attn_begin(total, grid, blockIdx.x + 1);
+            const AttnShare share(total, grid);
+            begin = share.begin(blockIdx.x);
+            end = share.begin(blockIdx.x + 1);
             long long run = 0;
-            for (int e0 = 0; e0 < entries && found < 0; e0 += 32) {
-                const long long mine = e0 + lane < entries ? (long long)attn_entry(p, e0 + lane).tiles * p.kv_heads : 0;
+#pragma unroll 1
+            for (int e0 = 0; e0 < entries && !found; e0 += 32) {
+                AttnEntry en;
+                en.tiles = 0;
+                if (e0 < 32 * kHeld) {
+#pragma unroll
+                    for (int i = 0; i < kHeld; ++i)
+                        if (e0 == 32 * i) en = held[i];
+                } else if (e0 + lane < entries) {
+                    en = attn_entry(p, e0 + lane);
+                }
+                const long long mine = (long long)en.tiles * p.kv_heads;
                 long long inc = mine;
+#pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const long long y = __shfl_up_sync(~0u, inc, o);
                     if (lane >= o) inc += y;
                 }
                 const unsigned hit = __ballot_sync(~0u, run + inc > begin);
                 if (hit) {
-                    const int src = __ffs(hit) - 1;
-                    found = e0 + src;
-                    within = begin - run - __shfl_sync(~0u, inc - mine, src);
+                    found = true;
+                    if (lane == __ffs(hit) - 1) {
+                        s_start[0] = e0 + lane;
+                        s_start[1] = (int)(begin - run - (inc - mine));
+                        *s_entry = en;
+                    }
                 }
                 run += __shfl_sync(~0u, inc, 31);
             }
@@ -499,9 +540,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
         if (lane == 0) {
             s_walk[0] = total;
             s_walk[1] = begin;
-            s_walk[2] = found < 0 ? begin : end;
-            s_walk[3] = found;
-            s_walk[4] = within;
+            s_walk[2] = found ? end : begin;
             p.split[blockIdx.x].n = 0;
         }
     }
@@ -512,7 +551,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     const long long total = s_walk[0];
     const bool work = s_walk[2] > s_walk[1];
     AttnWalk w;
-    if (work) w.start(p, s_walk[1], s_walk[2], (int)s_walk[3], s_walk[4]);
+    if (work) w.start(*s_entry, s_walk[1], s_walk[2], s_start[0], s_start[1]);
 
     if (work && warp == kProducer) {
         // ------------------------------------------------ loads: a page's rows each lane, keys by
@@ -694,23 +733,37 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
         auto pv_wait = [&](int i) {         // the product of tile i has been made
             if (i >= 0) wait(smem_u32(pv_done + (i & 1)), (i >> 1) & 1, kErrConsumerWait);
         };
+        // a segment's queries: 16 elements each thread (and pass), read before the segment before it is finished
+        constexpr int TPR = D / 16;                         // threads of a row
+        constexpr int kPasses = (RP * TPR + kSoftmax - 1) / kSoftmax;
+        uint4 queries[kPasses][2];
+        auto load_queries = [&](const AttnWalk& v) {
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i) {
+                const int row = tid / TPR + i * (kSoftmax / TPR), token = row / p.group;
+                queries[i][0] = queries[i][1] = make_uint4(0, 0, 0, 0);
+                if (row < v.entry.tokens * p.group) {
+                    const uint16_t* src = p.q + (size_t)(v.entry.row0 + token) * p.q_stride +
+                                          (size_t)(v.head * p.group + row - token * p.group) * D + tid % TPR * 16;
+                    queries[i][0] = ldg128(src);
+                    queries[i][1] = ldg128(src + 8);
+                }
+            }
+        };
+        load_queries(w);
+        bool more_segments = true;
         do {
-            const AttnEntry& en = w.entry;
-            const int rows = en.tokens * p.group, tiles = w.tile1 - w.tile0;
+            const AttnEntry en = w.entry;
+            const int rows = en.tokens * p.group, tiles = w.tile1 - w.tile0, tile_first = w.tile0;
 
             // the row tile's queries as two e4m3 parts, each row scaled to the top of the range
             group_sync(kAllBar, kSoftmax);
-            constexpr int TPR = D / 16;             // threads of a row, 16 elements each
-            for (int row = tid / TPR; row < RP; row += kSoftmax / TPR) {
-                const int c = tid % TPR;
-                const int i = row / p.group, g = row - i * p.group;
-                uint32_t x[8] = {};
-                if (row < rows) {
-                    const uint16_t* src = p.q + (size_t)(en.row0 + i) * p.q_stride + (size_t)(w.head * p.group + g) * D + 16 * c;
-                    const uint4 a = ldg128(src), b = ldg128(src + 8);
-                    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-                    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-                }
+#pragma unroll
+            for (int pass = 0; pass < kPasses; ++pass) {
+                const int c = tid % TPR, row = tid / TPR + pass * (kSoftmax / TPR);
+                if (row >= RP) break;
+                const uint4 qa = queries[pass][0], qb = queries[pass][1];
+                const uint32_t x[8] = {qa.x, qa.y, qa.z, qa.w, qb.x, qb.y, qb.z, qb.w};
                 uint32_t top = 0;                   // largest magnitude: bf16 bits order as integers
 #pragma unroll
                 for (int k = 0; k < 8; ++k) top = max(top, max(x[k] & 0x7fffu, (x[k] >> 16) & 0x7fffu));
@@ -750,8 +803,9 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                     const float down = __uint_as_float((uint32_t)(127 + (e - 7) / 2) << 23) *
                                        __uint_as_float((uint32_t)(127 + (e - 7) - (e - 7) / 2) << 23);
                     s_qs[row] = row < rows ? (odd ? __uint_as_float(0x7fffffffu) : down * p.scale_log2) : 0.f;
-                    s_lim[row] = row < rows ? max(en.seen0 + i, 0) : 0;
-                    s_out[row] = (long long)(en.row0 + i) * p.q_heads + w.head * p.group + g;
+                    const int token = row / p.group;
+                    s_lim[row] = row < rows ? max(en.seen0 + token, 0) : 0;
+                    s_out[row] = (long long)(en.row0 + token) * p.q_heads + w.head * p.group + row - token * p.group;
                 }
             }
             if (tid < D) s_nan[tid] = 0x7fffffff;
@@ -767,7 +821,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
             uint32_t unset = ~0u;            // threads below RW: this row has no n_r yet
             const int t_first = TG == 2 ? (it0 + tg) & 1 : 0;       // the group's tiles have its parity
             for (int t = t_first; t < tiles; t += TG) {
-                const int it = it0 + t, tile = w.tile0 + t, j = tile * kTile + tl;
+                const int it = it0 + t, tile = tile_first + t, j = tile * kTile + tl;
                 wait(smem_u32(v_full + it % NV), (it / NV) & 1, kErrConsumerWait);
                 const TokenScales ts = scales[it % NV * kTile + tl];
                 const int flags = s_flags[it % NV];
@@ -947,6 +1001,13 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                 if (lane == 0) mbar_arrive(smem_u32(p_full + (it & 1)));
             }
 
+            // the next segment's queries are on their way while this one's sums are made
+            const bool whole = w.whole();
+            const int head = w.head;
+            const long long item_begin = w.item_begin;
+            more_segments = w.next(p);
+            if (more_segments) load_queries(w);
+
             // ---------------------------------------- the segment's sums
 #pragma unroll
             for (int r = 0; r < RW; r += 8) {
@@ -961,7 +1022,6 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
             if (tl < RW) s_l[tg * RP + r0 + tl] = (red[tl] + red[RW + tl]) + (red[2 * RW + tl] + red[3 * RW + tl]);
             it0 += tiles;
             if (NWG > 1) group_sync(kAllBar, kSoftmax);
-            const bool whole = w.whole();
             const int cta_slot = blockIdx.x * 2 + slot;
             if (tid < RP) {
                 // a row's sum over the tile groups, and what its accumulators count for; a group whose
@@ -1025,14 +1085,14 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                     }
                 }
             }
-            if (!whole && w.tile0 == 0 && tid == 0) {
+            if (!whole && tile_first == 0 && tid == 0) {
                 // this CTA begins a split item
-                const int last = attn_cta_of(total, total < gridDim.x ? (int)total : (int)gridDim.x,
-                                             w.item_begin + en.tiles - 1);
-                p.split[blockIdx.x] = AttnSplit{last - (int)blockIdx.x + 1, slot, en.row0, rows, w.head};
+                const AttnShare share(total, total < gridDim.x ? (int)total : (int)gridDim.x);
+                p.split[blockIdx.x] =
+                    AttnSplit{share.cta_of(item_begin + en.tiles - 1) - (int)blockIdx.x + 1, slot, en.row0, rows, head};
             }
             slot = 1;
-        } while (w.next(p));
+        } while (more_segments);
         tc_fence_before_sync();
     }
     __syncthreads();
