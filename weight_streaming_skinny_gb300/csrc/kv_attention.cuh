@@ -132,7 +132,9 @@ struct AttnShape {
     static constexpr int kTileBytes = kTile * D;        // codes of K, and of V
     static constexpr int kQBytes = 2 * RP * D;
     static constexpr int kPBytes = kOutCols * kTile;    // one of two buffers
-    static constexpr int kMisc = 1024 + RP * (16 + 16 * TG) + TG * 4 * RP * 4 + D * 4 + 256;
+    // segment descriptors: one more than tiles can be in flight, and the one in work
+    static constexpr int kSegments = 10;
+    static constexpr int kMisc = 1024 + kSegments * 32 + RP * (16 + 16 * TG) + TG * 4 * RP * 4 + D * 4 + 256;
     static constexpr int kBudget = (kCtas == 1 ? 227 : 113) * 1024;
     // a tile's slots: its codes, and 8 bytes of scales for each token
     static constexpr int kScaleBytes = kTile * 8;
@@ -142,7 +144,7 @@ struct AttnShape {
     static constexpr int kValueSlots = kKeySlots + (kRoom - kKeySlots * (2 * kTileBytes + kScaleBytes) >= kTileBytes + kScaleBytes);
     static constexpr size_t kSmem = 1024 + (size_t)kKeySlots * kTileBytes + (size_t)kValueSlots * (kTileBytes + kScaleBytes) +
                                     kQBytes + 2 * kPBytes + kMisc;
-    static_assert(kKeySlots >= 2 && kCols <= 512 && kCols * kCtas <= 512 && kOutCols <= 256, "fits an SM");
+    static_assert(kValueSlots + 2 <= kSegments && kKeySlots >= 2 && kCols <= 512 && kCols * kCtas <= 512 && kOutCols <= 256, "fits an SM");
 };
 
 // ---------------------------------------------------------------- device helpers
@@ -402,6 +404,14 @@ struct AttnWalk {
 
 // ---------------------------------------------------------------- the kernel
 
+// What the softmax needs of a segment, made by the warp that walks ahead.
+struct __align__(16) AttnSegment {
+    int row0, rows, seen0, head;        // first token row, rows, cached tokens the first sees, head (part)
+    int tile0, tiles;
+    int share;                          // 0: a whole item; n: begins one that n CTAs share; -1: a later piece
+    int last;                           // the CTA's last segment
+};
+
 // The scales of a token's blocks; value < 0: the token is absent.
 struct __align__(8) TokenScales {
     float key, value;
@@ -412,7 +422,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                  const __grid_constant__ AttnParams p) {
     constexpr int D = C::D, RP = C::RP, RW = C::RW, TG = C::TG, CG = C::CG, NWG = TG * CG;
-    constexpr int NK = C::kKeySlots, NV = C::kValueSlots;
+    constexpr int NK = C::kKeySlots, NV = C::kValueSlots, NS = C::kSegments;
     constexpr int kProducer = NWG * 4, kMma = NWG * 4 + 1, kScaler = NWG * 4 + 2;
     constexpr int kAllBar = NWG + 1, kSoftmax = NWG * 128;
     // one accumulator lane per dim: M = 64 leaves 16 rows in each warp's lanes
@@ -433,15 +443,17 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     unsigned char* misc = reinterpret_cast<unsigned char*>(scales + NV * kTile);
     uint64_t* bars = reinterpret_cast<uint64_t*>(misc);
     uint64_t *k_full = bars, *k_empty = k_full + NK, *v_full = k_empty + NK, *v_empty = v_full + NV,
-             *s_full = v_empty + NV, *s_read = s_full + 2, *p_full = s_read + 2, *pv_done = p_full + 2, *q_full = pv_done + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 1);
+             *s_full = v_empty + NV, *s_read = s_full + 2, *p_full = s_read + 2, *pv_done = p_full + 2, *q_full = pv_done + 2,
+             *seg_full = q_full + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(seg_full + NS);
     int* s_stop = reinterpret_cast<int*>(tmem_slot + 1);
     long long* s_walk = reinterpret_cast<long long*>(misc + 512);     // total, begin, end
     int* s_start = reinterpret_cast<int*>(misc + 536);                // first entry, tiles of it before `begin`
     AttnEntry* s_entry = reinterpret_cast<AttnEntry*>(misc + 544);
     int* s_force = reinterpret_cast<int*>(misc + 608);                // [NWG] a row has no n_r yet
     int* s_flags = reinterpret_cast<int*>(misc + 640);                // [NV] kAbsent: some token is, kTiny: some scale is
-    float* s_qs = reinterpret_cast<float*>(misc + 1024);              // [RP] a row's query scale
+    AttnSegment* s_seg = reinterpret_cast<AttnSegment*>(misc + 1024); // [NS]
+    float* s_qs = reinterpret_cast<float*>(s_seg + NS);               // [RP] a row's query scale
     int* s_lim = reinterpret_cast<int*>(s_qs + RP);                   // [RP] cached tokens a row sees
     long long* s_out = reinterpret_cast<long long*>(s_lim + RP);      // [RP] a row's place among tokens x heads
     float* s_n = reinterpret_cast<float*>(s_out + RP);                // [TG][RP] n_r
@@ -471,7 +483,10 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                 mbar_init(smem_u32(pv_done + i), 1);
             }
             mbar_init(smem_u32(q_full), NWG * 4);
+            for (int i = 0; i < NS; ++i) mbar_init(smem_u32(seg_full + i), 1);
             *s_stop = 0;
+            // read only after a wait that gave up: nothing to do, and nothing after it
+            for (int i = 0; i < NS; ++i) s_seg[i] = AttnSegment{0, 0, 0, 0, 0, 0, -1, 1};
             fence_mbarrier_init();
         }
         __syncwarp();
@@ -604,10 +619,23 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
         }
     } else if (work && warp == kScaler) {
         // ------------------------------------------------ scales: four tokens each lane; a tile's
-        // pages are read two tiles ahead, its scales one
-        int it = 0;
+        // pages are read two tiles ahead, its scales one.  And what the softmax needs of a segment: a
+        // descriptor's slot comes round again after more segments than tiles can be in flight.
+        int it = 0, seg = 0;
         bool ok = true;
         do {
+            if (lane == 0) {
+                int share = w.whole() ? 0 : -1;
+                if (share < 0 && w.tile0 == 0) {
+                    const AttnShare dealt(total, total < gridDim.x ? (int)total : (int)gridDim.x);
+                    share = dealt.cta_of(w.item_begin + w.entry.tiles - 1) - (int)blockIdx.x + 1;
+                }
+                s_seg[seg % NS] = AttnSegment{w.entry.row0, w.entry.tokens * p.group, w.entry.seen0, w.head, w.tile0,
+                                              w.tile1 - w.tile0, share, w.at + (w.tile1 - w.tile0) >= w.end};
+                mbar_arrive(smem_u32(seg_full + seg % NS));
+            }
+            __syncwarp();
+            ++seg;
             const int* table = p.s.block_table + (size_t)w.entry.b * p.s.table_cols;
             const int head = w.head / p.head_parts;
             auto pages_of = [&](int tile, int (&pg)[4]) {
@@ -737,24 +765,26 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
         constexpr int TPR = D / 16;                         // threads of a row
         constexpr int kPasses = (RP * TPR + kSoftmax - 1) / kSoftmax;
         uint4 queries[kPasses][2];
-        auto load_queries = [&](const AttnWalk& v) {
+        auto load_queries = [&](const AttnSegment& v) {
 #pragma unroll
             for (int i = 0; i < kPasses; ++i) {
                 const int row = tid / TPR + i * (kSoftmax / TPR), token = row / p.group;
                 queries[i][0] = queries[i][1] = make_uint4(0, 0, 0, 0);
-                if (row < v.entry.tokens * p.group) {
-                    const uint16_t* src = p.q + (size_t)(v.entry.row0 + token) * p.q_stride +
+                if (row < v.rows) {
+                    const uint16_t* src = p.q + (size_t)(v.row0 + token) * p.q_stride +
                                           (size_t)(v.head * p.group + row - token * p.group) * D + tid % TPR * 16;
                     queries[i][0] = ldg128(src);
                     queries[i][1] = ldg128(src + 8);
                 }
             }
         };
-        load_queries(w);
-        bool more_segments = true;
+        wait(smem_u32(seg_full), 0, kErrConsumerWait);
+        load_queries(s_seg[0]);
+        int seg = 0;
+        bool last = false;
         do {
-            const AttnEntry en = w.entry;
-            const int rows = en.tokens * p.group, tiles = w.tile1 - w.tile0, tile_first = w.tile0;
+            const AttnSegment* sg = s_seg + seg % NS;
+            const int tile_first = sg->tile0, tiles = sg->tiles, seen0 = sg->seen0, seen_first = max(seen0, 0);
 
             // the row tile's queries as two e4m3 parts, each row scaled to the top of the range
             group_sync(kAllBar, kSoftmax);
@@ -802,10 +832,10 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                 if (c == 0) {
                     const float down = __uint_as_float((uint32_t)(127 + (e - 7) / 2) << 23) *
                                        __uint_as_float((uint32_t)(127 + (e - 7) - (e - 7) / 2) << 23);
-                    s_qs[row] = row < rows ? (odd ? __uint_as_float(0x7fffffffu) : down * p.scale_log2) : 0.f;
+                    s_qs[row] = row < sg->rows ? (odd ? __uint_as_float(0x7fffffffu) : down * p.scale_log2) : 0.f;
                     const int token = row / p.group;
-                    s_lim[row] = row < rows ? max(en.seen0 + token, 0) : 0;
-                    s_out[row] = (long long)(en.row0 + token) * p.q_heads + w.head * p.group + row - token * p.group;
+                    s_lim[row] = row < sg->rows ? max(seen0 + token, 0) : 0;
+                    s_out[row] = (long long)(sg->row0 + token) * p.q_heads + sg->head * p.group + row - token * p.group;
                 }
             }
             if (tid < D) s_nan[tid] = 0x7fffffff;
@@ -828,7 +858,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                 const bool absent = ts.value < 0.f;
                 const float value = absent ? 1.f : ts.value < kTinyScale ? kTinyScale : ts.value;
                 const float lv = log2_fast(value), inv = __fdividef(1.f, value);
-                const bool masked = (tile + 1) * kTile > en.seen_first || (flags & kAbsent);
+                const bool masked = (tile + 1) * kTile > seen_first || (flags & kAbsent);
 
                 // exponents t + n
                 wait(smem_u32(s_full + (it & 1)), (it >> 1) & 1, kErrConsumerWait);
@@ -863,7 +893,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                 }
                 if (masked) {
                     // new token i, rows i * group on, sees cache indexes below seen0 + i
-                    const int from = absent ? RP : max(min(j - en.seen0 + 1, RP), 0) * p.group - r0;
+                    const int from = absent ? RP : max(min(j - seen0 + 1, RP), 0) * p.group - r0;
 #pragma unroll
                     for (int r = 0; r < RW; ++r)
                         if (r < from) d[r] = -INFINITY;
@@ -891,7 +921,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                             unset = 0;
                         }
                     }
-                    const bool more = group_any(bar_id, 128, tl < RW && unset && r0 + tl < rows);
+                    const bool more = group_any(bar_id, 128, tl < RW && unset && r0 + tl < sg->rows);
                     if (tl < RW) red[tl] = move;
                     if (tl == 0) s_force[wg] = more;
                     group_sync(bar_id, 128);
@@ -933,7 +963,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
 
                 // values that some row must not see are taken out: all of an absent token, and NaN codes
                 // of the new tokens (0 x NaN would reach every row), which are noted by dim
-                if (masked && (absent || j >= en.seen_first)) {
+                if (masked && (absent || j >= seen_first)) {
                     unsigned char* codes = values + it % NV * C::kTileBytes + tl * D;
 #pragma unroll 1
                     for (int c = wg % CG; c < D / 16; c += CG) {
@@ -1002,11 +1032,13 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
             }
 
             // the next segment's queries are on their way while this one's sums are made
-            const bool whole = w.whole();
-            const int head = w.head;
-            const long long item_begin = w.item_begin;
-            more_segments = w.next(p);
-            if (more_segments) load_queries(w);
+            const int rows = sg->rows;
+            const bool whole = sg->share == 0;
+            last = sg->last;
+            if (!last) {
+                wait(smem_u32(seg_full + (seg + 1) % NS), ((seg + 1) / NS) & 1, kErrConsumerWait);
+                load_queries(s_seg[(seg + 1) % NS]);
+            }
 
             // ---------------------------------------- the segment's sums
 #pragma unroll
@@ -1085,14 +1117,11 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                     }
                 }
             }
-            if (!whole && tile_first == 0 && tid == 0) {
-                // this CTA begins a split item
-                const AttnShare share(total, total < gridDim.x ? (int)total : (int)gridDim.x);
-                p.split[blockIdx.x] =
-                    AttnSplit{share.cta_of(item_begin + en.tiles - 1) - (int)blockIdx.x + 1, slot, en.row0, rows, head};
-            }
+            if (sg->share > 0 && tid == 0)
+                p.split[blockIdx.x] = AttnSplit{sg->share, slot, sg->row0, rows, sg->head};
             slot = 1;
-        } while (more_segments);
+            ++seg;
+        } while (!last);
         tc_fence_before_sync();
     }
     __syncthreads();
