@@ -611,7 +611,7 @@ def kv_append(q, k, v, cache: PagedKVCache, block_table, seq_lens, q_start, *, m
     if q is not None:
         Tq, Hq, qs = _need_rows(q, "q", None, D, dev)
         if out_q is None:
-            out_q = q.new_empty((Tq, Hq, D))
+            out_q = torch.empty_like(q, memory_format=torch.contiguous_format)
         else:
             _need(out_q, "out_q", torch.bfloat16, dev)
             if out_q.shape != q.shape:
@@ -655,7 +655,7 @@ def attention_paged(q, cache: PagedKVCache, block_table, seq_lens, q_start, *, m
     T, Hq, qs = _need_rows(q, "q", None, D, dev)
     B, cols = _need_sequences(cache, block_table, seq_lens, q_start)
     if out is None:
-        out = q.new_empty((T, Hq, D))
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _need(out, "out", torch.bfloat16, dev)
         if out.numel() != T * Hq * D:
@@ -709,11 +709,11 @@ def verify_draft(draft_tokens, target_probs, u_accept, u_next, *, draft_probs=No
         if draft_lens.numel() != B:
             raise ValueError("draft_lens must be [batch]")
     if out_tokens is None:
-        out_tokens = draft_tokens.new_empty((B, S + 1))
+        out_tokens = torch.empty((B, S + 1), dtype=torch.int32, device=dev)
     else:
         _need(out_tokens, "out_tokens", torch.int32, dev)
     if out_count is None:
-        out_count = draft_tokens.new_empty((B,))
+        out_count = torch.empty((B,), dtype=torch.int32, device=dev)
     else:
         _need(out_count, "out_count", torch.int32, dev)
     if out_tokens.numel() != B * (S + 1) or out_count.numel() != B:
