@@ -16,6 +16,7 @@ struct AppendParams {
     int page_shift, block_shift;
     int blocks_per_seq;          // most blocks a sequence's new tokens touch
     int team, kv_ctas;           // threads of a block, CTAs that take blocks
+    int per;                     // tokens whose queries a CTA takes
     long long kv_units;          // blocks of keys (as many of values follow)
     Sequences s;
 };
@@ -96,38 +97,55 @@ __device__ __forceinline__ float block_scale(float amax) {
     return __uint_as_float((unsigned)(e + 127) << 23);
 }
 
-// One CTA: a token's queries, every head.
+// One CTA: the queries of `per` (1 or 4) tokens, every head, a share of the threads for each
+// token.  The first heads are read before the token's sequence and position are
+// known, so that the latencies of the two overlap.
 template <int D>
-__device__ __forceinline__ void append_queries(const AppendParams& p, int t) {
-    constexpr int kUnits = D / 16;
-    const int tid = threadIdx.x;
-    int before = 0;                     // sequences that end at or before t
-    for (int b0 = 0; b0 < p.s.batch; b0 += kAppendThreads) {
-        const int b = b0 + tid;
-        before += __syncthreads_count(b < p.s.batch && p.s.q_start[b + 1] <= t);
-    }
-    if (before >= p.s.batch) return;
-    const SequenceView sv = sequence_view(p.s, before, p.c.page_size);
+__device__ __forceinline__ void append_queries(const AppendParams& p, int t0) {
+    constexpr int kUnits = D / 16, kAhead = 2;
+    const int threads = kAppendThreads / p.per, step = threads / kUnits;
+    const int tid = threadIdx.x % threads, h0 = tid / kUnits, t = t0 + threadIdx.x / threads;
+    const RowUnit u = row_unit(tid % kUnits, p.rotary_dim);
+    const uint16_t* src = p.q + (size_t)min(t, p.s.tokens - 1) * p.q_stride;
+    uint4 x[kAhead], y[kAhead];
+    auto read = [&](int h) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (h + i * step < p.q_heads) {
+                x[i] = ldg128(src + (size_t)(h + i * step) * D + u.a);
+                y[i] = ldg128(src + (size_t)(h + i * step) * D + u.b);
+            }
+    };
+    read(h0);
+    int b = 0;                          // sequences that end at or before t
+    for (int i = 0; i < p.s.batch; i += kAppendThreads)
+        b += __syncthreads_count(i + (int)threadIdx.x < p.s.batch && p.s.q_start[i + threadIdx.x + 1] <= t0);
+    if (t >= p.s.tokens) return;
+    while (b < p.s.batch && p.s.q_start[b + 1] <= t) ++b;
+    if (b >= p.s.batch) return;
+    const SequenceView sv = sequence_view(p.s, b, p.c.page_size);
     const int i = t - sv.row0;
     if (i < 0 || i >= sv.n_work) return;
-    const RowUnit u = row_unit(tid % kUnits, p.rotary_dim);
     float c[8], s[8];
     if (u.angle >= 0) load_angles(p, position_of(p, t, sv.len - sv.n + i), u.angle, c, s);
-    const uint16_t* src = p.q + (size_t)t * p.q_stride;
     uint16_t* dst = p.q_out + (size_t)t * p.q_heads * D;
-#pragma unroll 2
-    for (int h = tid / kUnits; h < p.q_heads; h += kAppendThreads / kUnits) {
-        float f[16];
-        unpack8(ldg128(src + (size_t)h * D + u.a), f);
-        unpack8(ldg128(src + (size_t)h * D + u.b), f + 8);
-        if (u.angle >= 0) rotate(f, c, s);
-        uint4 x, y;
-        x.x = pack_bf16(f[0], f[1]); x.y = pack_bf16(f[2], f[3]);
-        x.z = pack_bf16(f[4], f[5]); x.w = pack_bf16(f[6], f[7]);
-        y.x = pack_bf16(f[8], f[9]); y.y = pack_bf16(f[10], f[11]);
-        y.z = pack_bf16(f[12], f[13]); y.w = pack_bf16(f[14], f[15]);
-        *reinterpret_cast<uint4*>(dst + (size_t)h * D + u.a) = x;
-        *reinterpret_cast<uint4*>(dst + (size_t)h * D + u.b) = y;
+    for (int h = h0;;) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (h + k * step >= p.q_heads) continue;
+            float f[16];
+            unpack8(x[k], f);
+            unpack8(y[k], f + 8);
+            if (u.angle >= 0) rotate(f, c, s);
+            uint16_t* to = dst + (size_t)(h + k * step) * D;
+            *reinterpret_cast<uint4*>(to + u.a) =
+                make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+            *reinterpret_cast<uint4*>(to + u.b) =
+                make_uint4(pack_bf16(f[8], f[9]), pack_bf16(f[10], f[11]), pack_bf16(f[12], f[13]), pack_bf16(f[14], f[15]));
+        }
+        h += kAhead * step;
+        if (h >= p.q_heads) break;
+        read(h);
     }
 }
 
@@ -228,13 +246,13 @@ __device__ __forceinline__ void append_block(const AppendParams& p, long long un
     if (at == 0) *scale = s1;
 }
 
-// grid.x: the CTAs of the blocks, then one for each token's queries.
+// grid.x: the CTAs of the blocks, then those of the queries.
 template <int D>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_constant__ AppendParams p) {
     griddep_wait();
     griddep_launch_dependents();
     if ((int)blockIdx.x >= p.kv_ctas) {
-        append_queries<D>(p, blockIdx.x - p.kv_ctas);
+        append_queries<D>(p, (blockIdx.x - p.kv_ctas) * p.per);
     } else {
         const int team = p.team, per = kAppendThreads / team;
         append_block<D>(p, (long long)blockIdx.x * per + threadIdx.x / team, threadIdx.x % team, team);
@@ -360,8 +378,12 @@ extern "C" dl_status dl_kv_append(const dl_kv_cache* cache, const void* q, const
     // threads of a block: one for each 16 of its values, as far as a CTA goes
     p.team = cache->block * D / 16 < kAppendThreads ? cache->block * D / 16 : kAppendThreads;
     p.kv_units = (long long)batch * p.blocks_per_seq * cache->num_heads;
-    const int per = kAppendThreads / p.team;
-    const long long kv_ctas = (2 * p.kv_units + per - 1) / per, grid = kv_ctas + (q ? tokens : 0);
+    const int blocks = kAppendThreads / p.team;
+    HostDevice dev;
+    if ((s = host_device(dev)) != DL_OK) return s;
+    // a CTA's search and position are shared by four tokens once that leaves several CTAs to each SM
+    p.per = tokens >= 16 * dev.sm_count ? 4 : 1;
+    const long long kv_ctas = (2 * p.kv_units + blocks - 1) / blocks, grid = kv_ctas + (q ? (tokens + p.per - 1) / p.per : 0);
     if (grid > 0x7fffffffLL)
         return host_fail(DL_ERR_UNSUPPORTED_SHAPE, "%lld blocks to write exceed one launch", 2 * p.kv_units);
     p.kv_ctas = (int)kv_ctas;

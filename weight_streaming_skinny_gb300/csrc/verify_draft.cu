@@ -1,6 +1,8 @@
 // Verification of drafted tokens and the draw of the next one (dl_verify_draft).
 #include <cooperative_groups.h>
 
+#include <atomic>
+
 #include "dl_host.h"
 #include "dl_device.cuh"
 
@@ -15,17 +17,14 @@ struct VerifyParams {
     int drafts, vocab;
 };
 
-// A cluster of CTAs takes one sequence, each a contiguous part of its vocabulary.
-// What bounds it: for many sequences the one read of p (and g), for few the
-// chain of dependent loads (draft token, its probabilities, the row).  The sums
-// of the first pass are kept by CTA, tile and warp, so that the drawn token is
-// found by reading 128 entries again, not the row.
+// A cluster of CTAs takes one sequence, each warp a contiguous run of its vocabulary.
+// What bounds it: for many sequences the one read of p (and g) and the arithmetic on
+// it, for few the chain of dependent loads (draft token, its probabilities, the
+// row).  The first pass keeps the sums by CTA and warp, so that the drawn token is
+// found by reading one warp's run again, not the row.
 constexpr int kVerifyThreads = 512;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
-constexpr int kVerifyTile = kVerifyThreads * 4;             // entries of a tile
-constexpr int kMaxCluster = 8;
-constexpr int kMaxTiles = (1 << 18) / kMaxCluster / kVerifyTile;
-constexpr int kWeightBits = 44;
+constexpr int kMaxCluster = 16;
 
 // Four consecutive probabilities from entry i on, entries at or past `end` as
 // zeros; `wide`: the row's groups of four are aligned to their size.
@@ -52,26 +51,56 @@ __device__ __forceinline__ void four(const uint16_t* row, int i, int end, bool w
 __device__ __forceinline__ float prob(const float* p, size_t i) { return p[i]; }
 __device__ __forceinline__ float prob(const uint16_t* p, size_t i) { return bf16_bits_to_f32(p[i]); }
 
-// A probability, taken inside [0, 1] (NaN: 0), as the whole number nearest to x 2^44: hi 2^22 + lo.
-// Adding 1.5 * 2^23 leaves a rounded integer in an fp32's low bits; hi's rounding error is
-// exact in fp32, so lo rounds the whole value once, to even at ties (hi 2^22 is even).
+// A probability, taken inside [0, 1] (NaN: 0), as the whole number nearest to x 2^44: hi 2^22 + lo,
+// both offset by kOffset.  Adding 1.5 * 2^23 leaves a rounded integer in an fp32's
+// low bits; hi's rounding error is exact in fp32, so lo rounds the whole value
+// once, to even at ties (hi 2^22 is even).
+constexpr float kMagic = 12582912.f, kStep = 4194304.f;       // 1.5 * 2^23, 2^22
+constexpr int kOffset = 0x4B400000;                           // the bits of kMagic
 __device__ __forceinline__ void whole(float x, int& hi, int& lo) {
-    constexpr float kMagic = 12582912.f, kStep = 4194304.f;   // 1.5 * 2^23, 2^22
-    x = fminf(fmaxf(x, 0.f), 1.f);
-    const float y = __fmul_rn(x, kStep);
-    const float a = __fadd_rn(y, kMagic);
-    hi = __float_as_int(a) - __float_as_int(kMagic);
+    const float y = __fmul_rn(x, kStep), a = __fadd_rn(y, kMagic);
     const float rest = __fsub_rn(y, __fsub_rn(a, kMagic));
-    lo = __float_as_int(__fadd_rn(__fmul_rn(rest, kStep), kMagic)) - __float_as_int(kMagic);
+    hi = __float_as_int(a);
+    lo = __float_as_int(__fmaf_rn(rest, kStep, kMagic));
 }
+
+// The weights max(P - G, 0) of four entries, as hi 2^22 + lo each (P >= G exactly where p >= g).
+template <bool G>
+__device__ __forceinline__ void weights(const float (&f)[4], const float (&g)[4], int (&hi)[4], int (&lo)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float x = __saturatef(f[k]);
+        int gh = kOffset, gl = kOffset, ph, pl;
+        whole(x, ph, pl);
+        bool more = true;
+        if (G) {
+            const float z = __saturatef(g[k]);
+            whole(z, gh, gl);
+            more = x > z;
+        }
+        hi[k] = more ? ph - gh : 0;
+        lo[k] = more ? pl - gl : 0;
+    }
+}
+__device__ __forceinline__ long long joined(int hi, int lo) { return (long long)hi * (1 << 22) + lo; }
 
 __device__ __forceinline__ long long warp_sum(long long w) {
     for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(~0u, w, o);
     return w;
 }
 
-template <class T>
-__global__ void __launch_bounds__(kVerifyThreads) verify_draft_kernel(const __grid_constant__ VerifyParams p) {
+__device__ __forceinline__ long long warp_scan(long long w, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(~0u, w, o);
+        if (lane >= o) w += y;
+    }
+    return w;
+}
+
+// BATCH: groups of 128 entries that a warp has in flight.
+template <class T, int BATCH>
+__global__ void __launch_bounds__(kVerifyThreads, BATCH > 2 ? 1 : 3) verify_draft_kernel(const __grid_constant__ VerifyParams p) {
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
     const int size = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -82,7 +111,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_draft_kernel(const __gr
     const T* guess = p.draft_probs ? static_cast<const T*>(p.draft_probs) + (size_t)b * p.drafts * V : nullptr;
     const int* drafts = p.draft_tokens + (size_t)b * p.drafts;
     const int n = p.draft_lens ? min(max(p.draft_lens[b], 0), p.drafts) : p.drafts;
-    __shared__ long long s_sum[kMaxTiles * kVerifyWarps], s_total;
+    __shared__ long long s_sum[kVerifyWarps], s_total;
     __shared__ int s_no[2];
 
     // every CTA accepts for itself: one draft position each thread of two warps
@@ -104,94 +133,109 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_draft_kernel(const __gr
     const int c = min(min(s_no[0], s_no[1]), n);
     const T* pr = target + (size_t)c * V;
     const T* gr = guess && c < n ? guess + (size_t)c * V : nullptr;
-    const int x = c < n && !guess ? drafts[c] : -1;
+    // without probabilities of its own the draft has all weight at its token: nothing is left there
+    const int skip = c < n && !guess ? drafts[c] : -1;
     const bool wide = !(((uintptr_t)pr | (uintptr_t)gr) & (4 * sizeof(T) - 1));
-    // this CTA's part, a whole number of tiles from its begin on
-    const int tiles = ((V + kVerifyTile - 1) / kVerifyTile + size - 1) / size;
-    const int begin = min(rank * tiles * kVerifyTile, V), end = min(begin + tiles * kVerifyTile, V);
-    auto weights = [&](int i, bool plain, long long (&w)[4]) {
-        float f[4], g[4] = {0.f, 0.f, 0.f, 0.f};
+    // this warp's run of entries, a multiple of 128, and the CTA's
+    const int run = ((V + size * kVerifyWarps - 1) / (size * kVerifyWarps) + 127) / 128 * 128;
+    const int cta_begin = min(rank * kVerifyWarps * run, V);
+    auto run_begin = [&](int w) { return min(cta_begin + w * run, V); };
+    auto load = [&](int i, int end, bool plain, float (&f)[4], float (&g)[4]) {
         four(pr, i, end, wide, f);
         if (gr && !plain) four(gr, i, end, wide, g);
+        if (!plain && (unsigned)(skip - i) < 4u) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            int ph, pl, gh, gl;
-            whole(f[k], ph, pl);
-            whole(g[k], gh, gl);
-            if (i + k == x && !plain) gh = 1 << (kWeightBits - 22);
-            const long long d = (long long)(ph - gh) * (1 << 22) + (pl - gl);
-            w[k] = d > 0 ? d : 0;
+            for (int k = 0; k < 4; ++k)
+                if (i + k == skip) f[k] = 0.f;
         }
+    };
+    auto weigh = [&](bool plain, const float (&f)[4], const float (&g)[4], int (&hi)[4], int (&lo)[4]) {
+        if (gr && !plain)
+            weights<true>(f, g, hi, lo);
+        else
+            weights<false>(f, g, hi, lo);
     };
     long long total = 0, before = 0;
     bool plain = false;
     for (int pass = 0; pass < 2; ++pass) {
         plain = pass == 1;              // nothing left of p - g: draw from p
-        long long mine = 0;
-#pragma unroll 2
-        for (int t = 0; t < tiles; ++t) {
-            const int i = begin + t * kVerifyTile + tid * 4;
-            long long w[4] = {0, 0, 0, 0};
-            if (i < end) weights(i, plain, w);
-            const long long s = warp_sum((w[0] + w[1]) + (w[2] + w[3]));
-            if (lane == 0) s_sum[t * kVerifyWarps + warp] = s;
+        long long sum = 0;
+        const int end = run_begin(warp + 1);
+        for (int i0 = run_begin(warp); i0 < end; i0 += 128 * BATCH) {
+            float f[BATCH][4] = {}, g[BATCH][4] = {};
+#pragma unroll
+            for (int t = 0; t < BATCH; ++t) {
+                const int i = i0 + 128 * t + lane * 4;
+                if (i < end) load(i, end, plain, f[t], g[t]);
+            }
+            int hi_sum = 0, lo_sum = 0;     // of at most 20 entries
+#pragma unroll
+            for (int t = 0; t < BATCH; ++t) {
+                int hi[4], lo[4];
+                weigh(plain, f[t], g[t], hi, lo);
+                hi_sum += (hi[0] + hi[1]) + (hi[2] + hi[3]);
+                lo_sum += (lo[0] + lo[1]) + (lo[2] + lo[3]);
+            }
+            sum += joined(hi_sum, lo_sum);
         }
+        sum = warp_sum(sum);
+        if (lane == 0) s_sum[warp] = sum;
         __syncthreads();
         if (warp == 0) {
-            for (int i = lane; i < tiles * kVerifyWarps; i += 32) mine += s_sum[i];
-            mine = warp_sum(mine);
-            if (lane == 0) s_total = mine;
+            const long long all = warp_sum(lane < kVerifyWarps ? s_sum[lane] : 0);
+            if (lane == 0) s_total = all;
         }
         cluster.sync();
-        total = before = 0;
-        for (int r = 0; r < size; ++r) {
-            const long long s = *cluster.map_shared_rank(&s_total, r);
-            if (r < rank) before += s;
-            total += s;
-        }
+        // every rank's total, a lane each
+        const long long theirs = lane < size ? *cluster.map_shared_rank(&s_total, lane) : 0;
+        total = warp_sum(theirs);
+        before = warp_sum(lane < rank ? theirs : 0);
         cluster.sync();
         if (total > 0) break;
     }
-    if (total > 0 && warp == 0) {
+    if (total > 0) {
         long long r = (long long)floorf(fminf(fmaxf(p.u_next[b], 0.f), 1.f) * 16777216.f);
         if (r > (1ll << 24) - 1) r = (1ll << 24) - 1;
         // floor(total r / 2^24)
         const long long mark = (total >> 24) * r + (((total & ((1ll << 24) - 1)) * r) >> 24);
-        // the warp's run of 128 entries whose sums pass the mark, then the entry
-        long long run = before;
+        // the warp whose run passes the mark, in the CTA whose part does
+        long long at = before;
         int found = -1;
-        for (int i0 = 0; i0 < tiles * kVerifyWarps && found < 0; i0 += 32) {
-            const long long s = i0 + lane < tiles * kVerifyWarps ? s_sum[i0 + lane] : 0;
-            long long inc = s;
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(~0u, inc, o);
-                if (lane >= o) inc += y;
-            }
-            const unsigned hit = __ballot_sync(~0u, run + inc > mark);
-            if (hit) {
-                const int src = __ffs(hit) - 1;
-                found = i0 + src;
-                run += __shfl_sync(~0u, inc - s, src);
-            } else {
-                run += __shfl_sync(~0u, inc, 31);
-            }
+#pragma unroll
+        for (int w = 0; w < kVerifyWarps; ++w) {
+            const long long s = s_sum[w];
+            if (found < 0 && at + s > mark) found = w;
+            if (found < 0) at += s;
         }
-        if (found >= 0 && before <= mark) {
-            const int i = begin + found / kVerifyWarps * kVerifyTile + found % kVerifyWarps * 128 + lane * 4;
-            long long w[4] = {0, 0, 0, 0};
-            if (i < end) weights(i, plain, w);
-            long long inc = (w[0] + w[1]) + (w[2] + w[3]);
-            const long long own = inc;
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(~0u, inc, o);
-                if (lane >= o) inc += y;
-            }
-            const unsigned hit = __ballot_sync(~0u, run + inc > mark);
-            if (lane == __ffs(hit) - 1) {
-                long long at = run + inc - own;
-                int k = 0;
-                while (k < 3 && at + w[k] <= mark) at += w[k++];
-                p.tokens[(size_t)b * (p.drafts + 1) + c] = i + k;
+        if (before <= mark && found >= 0) {
+            const int end = run_begin(found + 1);
+            for (int i0 = run_begin(found); i0 < end; i0 += kVerifyThreads * 4) {
+                const int i = i0 + tid * 4;
+                float f[4] = {}, g[4] = {};
+                int hi[4], lo[4];
+                if (i < end) load(i, end, plain, f, g);
+                weigh(plain, f, g, hi, lo);
+                const long long own = joined((hi[0] + hi[1]) + (hi[2] + hi[3]), (lo[0] + lo[1]) + (lo[2] + lo[3]));
+                const long long inc = warp_scan(own, lane);
+                __syncthreads();
+                if (lane == 31) s_sum[warp] = inc;
+                __syncthreads();
+                long long first = at + inc - own;
+#pragma unroll
+                for (int w = 0; w < kVerifyWarps; ++w) {
+                    const long long s = s_sum[w];
+                    if (w < warp) first += s;
+                    at += s;
+                }
+                if (first <= mark && first + own > mark) {
+                    int k = 0;
+                    while (k < 3 && first + joined(hi[k], lo[k]) <= mark) {
+                        first += joined(hi[k], lo[k]);
+                        ++k;
+                    }
+                    p.tokens[(size_t)b * (p.drafts + 1) + c] = i + k;
+                }
+                if (at > mark) break;
             }
         }
     }
@@ -202,11 +246,18 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_draft_kernel(const __gr
     }
 }
 
-template <class T>
-cudaError_t launch_verify(const VerifyParams& p, int batch, cudaStream_t stream) {
-    // CTAs of a sequence: one for each two tiles of its vocabulary, up to the portable 8
-    int size = 1;
-    while (size < kMaxCluster && size * 2 * kVerifyTile < p.vocab) size *= 2;
+template <class T, int BATCH>
+cudaError_t launch_verify_batch(const VerifyParams& p, int batch, int size, cudaStream_t stream) {
+    static std::atomic<bool> ready[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!ready[dev].load()) {
+        e = cudaFuncSetAttribute(verify_draft_kernel<T, BATCH>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        ready[dev].store(true);
+    }
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -220,7 +271,20 @@ cudaError_t launch_verify(const VerifyParams& p, int batch, cudaStream_t stream)
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, verify_draft_kernel<T>, p);
+    return cudaLaunchKernelEx(&cfg, verify_draft_kernel<T, BATCH>, p);
+}
+
+template <class T>
+cudaError_t launch_verify(const VerifyParams& p, int batch, int sm_count, cudaStream_t stream) {
+    // CTAs of a sequence: as many as leave three to each SM, at most 16 (a cluster), each warp
+    // with 128 entries at least.  Where an SM has one CTA, its warps have five groups of
+    // entries in flight, else two, and registers for three CTAs.
+    int size = 1;
+    while (size < kMaxCluster && (long long)batch * size * 2 <= 3LL * sm_count &&
+           size * kVerifyWarps * 128 < p.vocab)
+        size *= 2;
+    return (long long)batch * size <= sm_count ? launch_verify_batch<T, 5>(p, batch, size, stream)
+                                               : launch_verify_batch<T, 2>(p, batch, size, stream);
 }
 
 }  // namespace dl
@@ -250,8 +314,11 @@ extern "C" dl_status dl_verify_draft(const int* draft_tokens, const void* draft_
     const VerifyParams p = {draft_tokens, drafts ? draft_probs : nullptr, target_probs, u_accept, u_next,
                             draft_lens, tokens, count, drafts, vocab};
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = probs_dtype == DL_PROBS_F32 ? launch_verify<float>(p, batch, st)
-                                                      : launch_verify<uint16_t>(p, batch, st);
+    HostDevice device;
+    const dl_status s = host_device(device);
+    if (s != DL_OK) return s;
+    const cudaError_t e = probs_dtype == DL_PROBS_F32 ? launch_verify<float>(p, batch, device.sm_count, st)
+                                                      : launch_verify<uint16_t>(p, batch, device.sm_count, st);
     if (e != cudaSuccess) return host_fail(DL_ERR_CUDA, "verify_draft launch: %s", cudaGetErrorString(e));
     return host_ok();
 }
