@@ -105,7 +105,9 @@ struct AttnShare {
     __device__ __forceinline__ long long begin(int c) const { return c * each + min(c, more); }
     __device__ __forceinline__ int cta_of(long long tile) const {
         const long long head = more * (each + 1);
-        return tile < head ? (int)(tile / (each + 1)) : more + (int)((tile - head) / each);
+        const bool longer = tile < head;
+        const long long at = longer ? tile : tile - head, run = longer ? each + 1 : each;
+        return (longer ? 0 : more) + ((at | run) >> 31 ? (int)(at / run) : (int)((unsigned)at / (unsigned)run));
     }
 };
 
@@ -134,7 +136,7 @@ struct AttnShape {
     static constexpr int kPBytes = kOutCols * kTile;    // one of two buffers
     // segment descriptors: one more than tiles can be in flight, and the one in work
     static constexpr int kSegments = 10;
-    static constexpr int kMisc = 1024 + kSegments * 32 + RP * (16 + 16 * TG) + TG * 4 * RP * 4 + D * 4 + 256;
+    static constexpr int kMisc = 1024 + kSegments * 36 + 8 + RP * (16 + 16 * TG) + TG * 4 * RP * 4 + D * 4 + 256;
     static constexpr int kBudget = (kCtas == 1 ? 227 : 113) * 1024;
     // a tile's slots: its codes, and 8 bytes of scales for each token
     static constexpr int kScaleBytes = kTile * 8;
@@ -408,8 +410,7 @@ struct AttnWalk {
 struct __align__(16) AttnSegment {
     int row0, rows, seen0, head;        // first token row, rows, cached tokens the first sees, head (part)
     int tile0, tiles;
-    int share;                          // 0: a whole item; n: begins one that n CTAs share; -1: a later piece
-    int last;                           // the CTA's last segment
+    int whole, last;                    // a whole item; the CTA's last segment
 };
 
 // The scales of a token's blocks; value < 0: the token is absent.
@@ -453,7 +454,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     int* s_force = reinterpret_cast<int*>(misc + 608);                // [NWG] a row has no n_r yet
     int* s_flags = reinterpret_cast<int*>(misc + 640);                // [NV] kAbsent: some token is, kTiny: some scale is
     AttnSegment* s_seg = reinterpret_cast<AttnSegment*>(misc + 1024); // [NS]
-    float* s_qs = reinterpret_cast<float*>(s_seg + NS);               // [RP] a row's query scale
+    int* s_share = reinterpret_cast<int*>(s_seg + NS);                // [NS] CTAs that share an item begun here, or 0
+    float* s_qs = reinterpret_cast<float*>(s_share + (NS + 3) / 4 * 4);   // [RP] a row's query scale
     int* s_lim = reinterpret_cast<int*>(s_qs + RP);                   // [RP] cached tokens a row sees
     long long* s_out = reinterpret_cast<long long*>(s_lim + RP);      // [RP] a row's place among tokens x heads
     float* s_n = reinterpret_cast<float*>(s_out + RP);                // [TG][RP] n_r
@@ -486,7 +488,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
             for (int i = 0; i < NS; ++i) mbar_init(smem_u32(seg_full + i), 1);
             *s_stop = 0;
             // read only after a wait that gave up: nothing to do, and nothing after it
-            for (int i = 0; i < NS; ++i) s_seg[i] = AttnSegment{0, 0, 0, 0, 0, 0, -1, 1};
+            for (int i = 0; i < NS; ++i) s_seg[i] = AttnSegment{0, 0, 0, 0, 0, 0, 1, 1};
             fence_mbarrier_init();
         }
         __syncwarp();
@@ -499,57 +501,69 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     griddep_wait();
     griddep_launch_dependents();
     if (warp == 0) {
-        // the CTA's tiles, and the entry in which they begin: entries 32 at a time, the first
-        // kHeld of them read once
-        constexpr int kHeld = 4;
+        // the CTA's tiles, and the entry in which they begin: entries 32 at a time
         const int entries = p.s.batch * p.row_tiles;
-        AttnEntry held[kHeld];
-        long long total = 0;
-#pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-            held[i].tiles = 0;
-            if (32 * i + lane < entries) held[i] = attn_entry(p, 32 * i + lane);
-            total += held[i].tiles;
-        }
-        for (int e = 32 * kHeld + lane; e < entries; e += 32) total += attn_entry(p, e).tiles;
-        for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
-        total *= p.kv_heads;
-        const int grid = total < gridDim.x ? (int)total : (int)gridDim.x;
-        long long begin = 0, end = 0;
+        AttnEntry held;
+        held.tiles = 0;
+        if (lane < entries) held = attn_entry(p, lane);
+        long long total = 0, begin = 0, end = 0;
+        int grid = gridDim.x;
         bool found = false;
-        if ((int)blockIdx.x < grid) {
-            const AttnShare share(total, grid);
-            begin = share.begin(blockIdx.x);
-            end = share.begin(blockIdx.x + 1);
-            long long run = 0;
+        auto hit = [&](const AttnEntry& en, int e, long long before) {
+            s_start[0] = e;
+            s_start[1] = (int)(begin - before);
+            *s_entry = en;
+        };
+        if (entries <= 32 && __all_sync(~0u, held.tiles < (1 << 25) / p.kv_heads)) {
+            // one round, in 32 bits
+            const int mine = held.tiles * p.kv_heads;
+            int inc = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(~0u, inc, o);
+                if (lane >= o) inc += y;
+            }
+            total = __shfl_sync(~0u, inc, 31);
+            grid = min(grid, (int)total);
+            if ((int)blockIdx.x < grid) {
+                const AttnShare share(total, grid);
+                begin = share.begin(blockIdx.x);
+                end = share.begin(blockIdx.x + 1);
+                found = true;
+                if (inc > begin && inc - mine <= begin) hit(held, lane, inc - mine);
+            }
+        } else {
+            total = held.tiles;
+            for (int e = 32 + lane; e < entries; e += 32) total += attn_entry(p, e).tiles;
+            for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
+            total *= p.kv_heads;
+            if (total < grid) grid = (int)total;
+            if ((int)blockIdx.x < grid) {
+                const AttnShare share(total, grid);
+                begin = share.begin(blockIdx.x);
+                end = share.begin(blockIdx.x + 1);
+                long long run = 0;
 #pragma unroll 1
-            for (int e0 = 0; e0 < entries && !found; e0 += 32) {
-                AttnEntry en;
-                en.tiles = 0;
-                if (e0 < 32 * kHeld) {
-#pragma unroll
-                    for (int i = 0; i < kHeld; ++i)
-                        if (e0 == 32 * i) en = held[i];
-                } else if (e0 + lane < entries) {
-                    en = attn_entry(p, e0 + lane);
-                }
-                const long long mine = (long long)en.tiles * p.kv_heads;
-                long long inc = mine;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const long long y = __shfl_up_sync(~0u, inc, o);
-                    if (lane >= o) inc += y;
-                }
-                const unsigned hit = __ballot_sync(~0u, run + inc > begin);
-                if (hit) {
-                    found = true;
-                    if (lane == __ffs(hit) - 1) {
-                        s_start[0] = e0 + lane;
-                        s_start[1] = (int)(begin - run - (inc - mine));
-                        *s_entry = en;
+                for (int e0 = 0; e0 < entries && !found; e0 += 32) {
+                    AttnEntry en = held;
+                    if (e0 > 0) {
+                        en.tiles = 0;
+                        if (e0 + lane < entries) en = attn_entry(p, e0 + lane);
                     }
+                    const long long mine = (long long)en.tiles * p.kv_heads;
+                    long long inc = mine;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const long long y = __shfl_up_sync(~0u, inc, o);
+                        if (lane >= o) inc += y;
+                    }
+                    const unsigned which = __ballot_sync(~0u, run + inc > begin);
+                    if (which) {
+                        found = true;
+                        if (lane == __ffs(which) - 1) hit(en, e0 + lane, run + inc - mine);
+                    }
+                    run += __shfl_sync(~0u, inc, 31);
                 }
-                run += __shfl_sync(~0u, inc, 31);
             }
         }
         if (lane == 0) {
@@ -625,17 +639,11 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
         bool ok = true;
         do {
             if (lane == 0) {
-                int share = w.whole() ? 0 : -1;
-                if (share < 0 && w.tile0 == 0) {
-                    const AttnShare dealt(total, total < gridDim.x ? (int)total : (int)gridDim.x);
-                    share = dealt.cta_of(w.item_begin + w.entry.tiles - 1) - (int)blockIdx.x + 1;
-                }
                 s_seg[seg % NS] = AttnSegment{w.entry.row0, w.entry.tokens * p.group, w.entry.seen0, w.head, w.tile0,
-                                              w.tile1 - w.tile0, share, w.at + (w.tile1 - w.tile0) >= w.end};
+                                              w.tile1 - w.tile0, w.whole(), w.at + (w.tile1 - w.tile0) >= w.end};
                 mbar_arrive(smem_u32(seg_full + seg % NS));
             }
             __syncwarp();
-            ++seg;
             const int* table = p.s.block_table + (size_t)w.entry.b * p.s.table_cols;
             const int head = w.head / p.head_parts;
             auto pages_of = [&](int tile, int (&pg)[4]) {
@@ -664,6 +672,16 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
             pages_of(w.tile0, pg);
             pages_of(w.tile0 + 1, next);
             load(w.tile0, pg, a, b);
+            if (lane == 0) {
+                // read after the segment's last tile, so nobody waits for the divisions
+                int share = 0;
+                if (w.tile0 == 0 && !w.whole()) {
+                    const AttnShare dealt(total, total < gridDim.x ? (int)total : (int)gridDim.x);
+                    share = dealt.cta_of(w.item_begin + w.entry.tiles - 1) - (int)blockIdx.x + 1;
+                }
+                s_share[seg % NS] = share;
+            }
+            ++seg;
             for (int tile = w.tile0; tile < w.tile1; ++tile, ++it) {
                 float a1[4], b1[4];
                 int later[4];
@@ -1033,7 +1051,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
 
             // the next segment's queries are on their way while this one's sums are made
             const int rows = sg->rows;
-            const bool whole = sg->share == 0;
+            const bool whole = sg->whole;
             last = sg->last;
             if (!last) {
                 wait(smem_u32(seg_full + (seg + 1) % NS), ((seg + 1) / NS) & 1, kErrConsumerWait);
@@ -1117,8 +1135,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                     }
                 }
             }
-            if (sg->share > 0 && tid == 0)
-                p.split[blockIdx.x] = AttnSplit{sg->share, slot, sg->row0, rows, sg->head};
+            if (tid == 0 && s_share[seg % NS] > 0)
+                p.split[blockIdx.x] = AttnSplit{s_share[seg % NS], slot, sg->row0, rows, sg->head};
             slot = 1;
             ++seg;
         } while (!last);
