@@ -431,6 +431,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     constexpr uint32_t kSwizzle = D == 128 ? 2 : 4;
     // largest exponent of a probability (log2 448 = 8.807), and the one a maximum gets
     constexpr float kTop = 8.8f, kTarget = C::kParts == 4 ? -1.f : 3.f;
+    // rows that a softmax thread works on at a time, and columns of a load: as registers allow
+    constexpr int kHalf = RW > 24 && C::CG == 2 ? RW / 2 : RW, kStep = kHalf % 16 ? 8 : 16;
     constexpr float kTinyScale = 8.67361737988403547e-19f;       // 2^-60
 
     extern __shared__ unsigned char smem_raw[];
@@ -451,7 +453,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     long long* s_walk = reinterpret_cast<long long*>(misc + 512);     // total, begin, end
     int* s_start = reinterpret_cast<int*>(misc + 536);                // first entry, tiles of it before `begin`
     AttnEntry* s_entry = reinterpret_cast<AttnEntry*>(misc + 544);
-    int* s_force = reinterpret_cast<int*>(misc + 608);                // [NWG] a row has no n_r yet
+    int* s_force = reinterpret_cast<int*>(misc + 592);                // [NWG][2] a row has no n_r yet
     int* s_flags = reinterpret_cast<int*>(misc + 640);                // [NV] kAbsent: some token is, kTiny: some scale is
     AttnSegment* s_seg = reinterpret_cast<AttnSegment*>(misc + 1024); // [NS]
     int* s_share = reinterpret_cast<int*>(s_seg + NS);                // [NS] CTAs that share an item begun here, or 0
@@ -858,7 +860,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
             }
             if (tid < D) s_nan[tid] = 0x7fffffff;
             if (tl < RW) my_n[tl] = 0.f;
-            if (tl == 0) s_force[wg] = 1;
+            if (tl < 2) s_force[wg * 2 + tl] = 1;
             fence_proxy_async_smem();
             group_sync(kAllBar, kSoftmax);
             if (lane == 0) mbar_arrive(smem_u32(q_full));
@@ -878,107 +880,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                 const float lv = log2_fast(value), inv = __fdividef(1.f, value);
                 const bool masked = (tile + 1) * kTile > seen_first || (flags & kAbsent);
 
-                // exponents t + n
                 wait(smem_u32(s_full + (it & 1)), (it >> 1) & 1, kErrConsumerWait);
                 tc_fence_after_sync();
-                float d[RW];
-                const uint32_t sc = lanes + (it & 1) * C::kScoreCols + r0;
-                const F2 ks2 = f2(ts.key, ts.key), lv2 = f2(lv, lv);
-                constexpr int kStep = RW % 16 ? 8 : 16;
-                {
-                    float lo[RW];
-#pragma unroll
-                    for (int r = 0; r < RW; r += kStep) {
-                        tmem_ld<kStep>(sc + r, d + r);
-                        if (C::kConcat) tmem_ld<kStep>(sc + RP + r, lo + r);
-                    }
-                    tmem_wait_ld();
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(s_read + (it & 1)));
-#pragma unroll
-                    for (int r = 0; r < RW; r += 4) {
-                        F2 q0, q1, n0, n1, x0 = f2(d[r], d[r + 1]), x1 = f2(d[r + 2], d[r + 3]);
-                        lds_f2x2(s_qs + r0 + r, q0, q1);
-                        lds_f2x2(my_n + r, n0, n1);
-                        if (C::kConcat) {
-                            x0 = add2(x0, f2(lo[r], lo[r + 1]));
-                            x1 = add2(x1, f2(lo[r + 2], lo[r + 3]));
-                        }
-                        unpack(add2(fma2(mul2(x0, q0), ks2, lv2), n0), d[r], d[r + 1]);
-                        unpack(add2(fma2(mul2(x1, q1), ks2, lv2), n1), d[r + 2], d[r + 3]);
-                    }
-                }
-                if (masked) {
-                    // new token i, rows i * group on, sees cache indexes below seen0 + i
-                    const int from = absent ? RP : max(min(j - seen0 + 1, RP), 0) * p.group - r0;
-#pragma unroll
-                    for (int r = 0; r < RW; ++r)
-                        if (r < from) d[r] = -INFINITY;
-                }
-                float top = -INFINITY;
-#pragma unroll
-                for (int r = 0; r < RW; r += 2) top = max3(top, d[r], d[r + 1]);
-                // a row passes the top, or has no n_r yet: its n_r moves, and its sums follow
-                if (group_any(bar_id, 128, top > kTop || (tl == 0 && s_force[wg]))) {
-                    float m0 = 0.f;
-#pragma unroll
-                    for (int r = 0; r < RW; ++r) {
-                        const float m = warp_max_f32(d[r]);
-                        if (lane == (r & 31)) m0 = m;
-                        if ((r & 31) == 31 || r == RW - 1)
-                            if (lane <= (r & 31)) red[wq * RW + (r & ~31) + lane] = m0;
-                    }
-                    group_sync(bar_id, 128);
-                    float move = 0.f;
-                    if (tl < RW) {
-                        const float m = fmaxf(fmaxf(red[tl], red[RW + tl]), fmaxf(red[2 * RW + tl], red[3 * RW + tl]));
-                        if (m > -INFINITY && (m > kTop || unset)) {
-                            move = kTarget - m;
-                            my_n[tl] += move;
-                            unset = 0;
-                        }
-                    }
-                    const bool more = group_any(bar_id, 128, tl < RW && unset && r0 + tl < sg->rows);
-                    if (tl < RW) red[tl] = move;
-                    if (tl == 0) s_force[wg] = more;
-                    group_sync(bar_id, 128);
-#pragma unroll
-                    for (int r = 0; r < RW; r += 4) {
-                        const float4 x = *reinterpret_cast<const float4*>(red + r);
-                        d[r] = min_nan(d[r] + x.x, kTop);
-                        d[r + 1] = min_nan(d[r + 1] + x.y, kTop);
-                        d[r + 2] = min_nan(d[r + 2] + x.z, kTop);
-                        d[r + 3] = min_nan(d[r + 3] + x.w, kTop);
-                        l[r / 2] = mul2(l[r / 2], f2(shrink(x.x), shrink(x.y)));
-                        l[r / 2 + 1] = mul2(l[r / 2 + 1], f2(shrink(x.z), shrink(x.w)));
-                    }
-                    if (t >= TG) {
-                        pv_wait(it - TG);
-                        tc_fence_after_sync();
-#pragma unroll 1
-                        for (int r = 0; r < RW; r += 8) {
-                            float f[8], o[8];
-                            bool same = true;
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                f[k] = red[r + k];
-                                same &= f[k] == 0.f;
-                            }
-                            if (same) continue;
-#pragma unroll 1
-                            for (int part = 0; part < C::kParts; ++part) {
-                                tmem_ld<8>(out_at + part * RP + r, o);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) o[k] *= shrink(f[k]);
-                                tmem_st8(out_at + part * RP + r, o);
-                            }
-                        }
-                        tmem_wait_st();
-                    }
-                }
-
                 // values that some row must not see are taken out: all of an absent token, and NaN codes
                 // of the new tokens (0 x NaN would reach every row), which are noted by dim
                 if (masked && (absent || j >= seen_first)) {
@@ -1007,39 +910,142 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                     }
                 }
 
-                // probabilities, cut into parts: columns of part i, then row, 16 to a chunk of 2 KB
-                pv_wait(it - 2);
+                const uint32_t sc = lanes + (it & 1) * C::kScoreCols + r0;
+                const F2 ks2 = f2(ts.key, ts.key), lv2 = f2(lv, lv), inv2 = f2(inv, inv);
                 unsigned char* dst = sp + (it & 1) * C::kPBytes + tl * 16;
-                const F2 inv2 = f2(inv, inv);
-                const float fix = ts.value < kTinyScale ? ts.value * (1.f / kTinyScale) : 1.f;
+                // new token i, rows i * group on, sees cache indexes below seen0 + i: rows before `from` do not see this one
+                const int from = absent ? RP : max(min(j - seen0 + 1, RP), 0) * p.group - r0;
 #pragma unroll
-                for (int r = 0; r < RW; r += kStep) {
-                    uint32_t part[kStep / 4][C::kParts];
+                for (int h = 0; h < RW; h += kHalf) {
+                    // exponents t + n of kHalf rows
+                    float d[kHalf];
+                    {
+                        float lo[kHalf];
 #pragma unroll
-                    for (int k = 0; k < kStep; k += 4) {
-                        float e[4];
-#pragma unroll
-                        for (int m = 0; m < 4; ++m) e[m] = exp2_fast(d[r + k + m]);
-                        l[(r + k) / 2] = fma2(f2(e[0], e[1]), inv2, l[(r + k) / 2]);
-                        l[(r + k) / 2 + 1] = fma2(f2(e[2], e[3]), inv2, l[(r + k) / 2 + 1]);
-                        if (flags & kTiny) {
-#pragma unroll
-                            for (int m = 0; m < 4; ++m) e[m] *= fix;
+                        for (int r = 0; r < kHalf; r += kStep) {
+                            tmem_ld<kStep>(sc + h + r, d + r);
+                            if (C::kConcat) tmem_ld<kStep>(sc + RP + h + r, lo + r);
                         }
-                        split_e4m3<C::kParts>(e[0], e[1], e[2], e[3], part[k / 4]);
-                    }
-                    if constexpr (RP == 8) {
-                        sts128(smem_u32(dst), part[0][0], part[1][0], part[0][1], part[1][1]);
-                        sts128(smem_u32(dst + kTile * 16), part[0][2], part[1][2], part[0][3], part[1][3]);
-                    } else {
+                        tmem_wait_ld();
+                        if (h + kHalf == RW) {
+                            tc_fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(smem_u32(s_read + (it & 1)));
+                        }
 #pragma unroll
-                        for (int i = 0; i < C::kParts; ++i) {
-                            const int col = i * RP + r0 + r;
-                            unsigned char* to = dst + col / 16 * (kTile * 16);
-                            if constexpr (kStep == 16)
-                                sts128(smem_u32(to), part[0][i], part[1][i], part[2][i], part[3][i]);
-                            else
-                                *reinterpret_cast<uint2*>(to + col % 16) = make_uint2(part[0][i], part[1][i]);
+                        for (int r = 0; r < kHalf; r += 4) {
+                            F2 q0, q1, n0, n1, x0 = f2(d[r], d[r + 1]), x1 = f2(d[r + 2], d[r + 3]);
+                            lds_f2x2(s_qs + r0 + h + r, q0, q1);
+                            lds_f2x2(my_n + h + r, n0, n1);
+                            if (C::kConcat) {
+                                x0 = add2(x0, f2(lo[r], lo[r + 1]));
+                                x1 = add2(x1, f2(lo[r + 2], lo[r + 3]));
+                            }
+                            unpack(add2(fma2(mul2(x0, q0), ks2, lv2), n0), d[r], d[r + 1]);
+                            unpack(add2(fma2(mul2(x1, q1), ks2, lv2), n1), d[r + 2], d[r + 3]);
+                        }
+                    }
+                    if (masked) {
+#pragma unroll
+                        for (int r = 0; r < kHalf; ++r)
+                            if (h + r < from) d[r] = -INFINITY;
+                    }
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int r = 0; r < kHalf; r += 2) top = max3(top, d[r], d[r + 1]);
+                    // a row passes the top, or has no n_r yet: its n_r moves, and its sums follow
+                    if (group_any(bar_id, 128, top > kTop || (tl == 0 && s_force[wg * 2 + h / kHalf]))) {
+                        float m0 = 0.f;
+#pragma unroll
+                        for (int r = 0; r < kHalf; ++r) {
+                            const float m = warp_max_f32(d[r]);
+                            if (lane == r) m0 = m;
+                        }
+                        if (lane < kHalf) red[wq * kHalf + lane] = m0;
+                        group_sync(bar_id, 128);
+                        float move = 0.f;
+                        const uint32_t bit = 1u << (h / kHalf);
+                        if (tl < kHalf) {
+                            const float m = fmaxf(fmaxf(red[tl], red[kHalf + tl]), fmaxf(red[2 * kHalf + tl], red[3 * kHalf + tl]));
+                            if (m > -INFINITY && (m > kTop || (unset & bit))) {
+                                move = kTarget - m;
+                                my_n[h + tl] += move;
+                                unset &= ~bit;
+                            }
+                        }
+                        const bool more = group_any(bar_id, 128, tl < kHalf && (unset & bit) && r0 + h + tl < sg->rows);
+                        if (tl < kHalf) red[tl] = move;
+                        if (tl == 0) s_force[wg * 2 + h / kHalf] = more;
+                        group_sync(bar_id, 128);
+#pragma unroll
+                        for (int r = 0; r < kHalf; r += 4) {
+                            const float4 x = *reinterpret_cast<const float4*>(red + r);
+                            d[r] = min_nan(d[r] + x.x, kTop);
+                            d[r + 1] = min_nan(d[r + 1] + x.y, kTop);
+                            d[r + 2] = min_nan(d[r + 2] + x.z, kTop);
+                            d[r + 3] = min_nan(d[r + 3] + x.w, kTop);
+                            l[(h + r) / 2] = mul2(l[(h + r) / 2], f2(shrink(x.x), shrink(x.y)));
+                            l[(h + r) / 2 + 1] = mul2(l[(h + r) / 2 + 1], f2(shrink(x.z), shrink(x.w)));
+                        }
+                        if (t >= TG) {
+                            pv_wait(it - TG);
+                            tc_fence_after_sync();
+#pragma unroll 1
+                            for (int r = 0; r < kHalf; r += 8) {
+                                float f[8], o[8];
+                                bool same = true;
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) {
+                                    f[k] = red[r + k];
+                                    same &= f[k] == 0.f;
+                                }
+                                if (same) continue;
+#pragma unroll 1
+                                for (int part = 0; part < C::kParts; ++part) {
+                                    tmem_ld<8>(out_at + part * RP + h + r, o);
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int k = 0; k < 8; ++k) o[k] *= shrink(f[k]);
+                                    tmem_st8(out_at + part * RP + h + r, o);
+                                }
+                            }
+                            tmem_wait_st();
+                        }
+                        group_sync(bar_id, 128);         // red has been read
+                    }
+
+                    // probabilities, cut into parts: columns of part i, then row, 16 to a chunk of 2 KB
+                    if (h == 0) pv_wait(it - 2);
+#pragma unroll
+                    for (int r = 0; r < kHalf; r += kStep) {
+                        uint32_t part[kStep / 4][C::kParts];
+#pragma unroll
+                        for (int k = 0; k < kStep; k += 4) {
+                            float e[4];
+#pragma unroll
+                            for (int m = 0; m < 4; ++m) e[m] = exp2_fast(d[r + k + m]);
+                            const int at = (h + r + k) / 2;
+                            l[at] = fma2(f2(e[0], e[1]), inv2, l[at]);
+                            l[at + 1] = fma2(f2(e[2], e[3]), inv2, l[at + 1]);
+                            if (flags & kTiny) {
+#pragma unroll
+                                for (int m = 0; m < 4; ++m) e[m] *= ts.value < kTinyScale ? ts.value * (1.f / kTinyScale) : 1.f;
+                            }
+                            split_e4m3<C::kParts>(e[0], e[1], e[2], e[3], part[k / 4]);
+                        }
+                        if constexpr (RP == 8) {
+                            sts128(smem_u32(dst), part[0][0], part[1][0], part[0][1], part[1][1]);
+                            sts128(smem_u32(dst + kTile * 16), part[0][2], part[1][2], part[0][3], part[1][3]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < C::kParts; ++i) {
+                                const int col = i * RP + r0 + h + r;
+                                unsigned char* to = dst + col / 16 * (kTile * 16);
+                                if constexpr (kStep == 16)
+                                    sts128(smem_u32(to), part[0][i], part[1][i], part[2][i], part[3][i]);
+                                else
+                                    *reinterpret_cast<uint2*>(to + col % 16) = make_uint2(part[0][i], part[1][i]);
+                            }
                         }
                     }
                 }
