@@ -294,16 +294,17 @@ __device__ __forceinline__ void split_e4m3(float e0, float e1, float e2, float e
     uint32_t x = f32x2_to_f16x2(e0, e1), y = f32x2_to_f16x2(e2, e3);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        asm("{\n\t"
-            ".reg .b16 a, b;\n\t"
-            "cvt.rn.satfinite.e4m3x2.f16x2 a, %1;\n\t"
-            "cvt.rn.satfinite.e4m3x2.f16x2 b, %2;\n\t"
-            "mov.b32 %0, {a, b};\n\t"
-            "}"
-            : "=r"(part[i]) : "r"(x), "r"(y));
         if (i + 1 < N) {
             uint32_t u, v;
-            e4m3x4_to_f16x2x2(part[i], u, v);
+            asm("{\n\t"
+                ".reg .b16 a, b;\n\t"
+                "cvt.rn.satfinite.e4m3x2.f16x2 a, %3;\n\t"
+                "cvt.rn.satfinite.e4m3x2.f16x2 b, %4;\n\t"
+                "cvt.rn.f16x2.e4m3x2 %1, a;\n\t"
+                "cvt.rn.f16x2.e4m3x2 %2, b;\n\t"
+                "mov.b32 %0, {a, b};\n\t"
+                "}"
+                : "=r"(part[i]), "=r"(u), "=r"(v) : "r"(x), "r"(y));
             asm("{\n\t"
                 "sub.rn.f16x2 %0, %0, %2;\n\t"
                 "sub.rn.f16x2 %1, %1, %3;\n\t"
@@ -311,6 +312,14 @@ __device__ __forceinline__ void split_e4m3(float e0, float e1, float e2, float e
                 "mul.rn.f16x2 %1, %1, %4;\n\t"
                 "}"
                 : "+r"(x), "+r"(y) : "r"(u), "r"(v), "r"(kSixteen));
+        } else {
+            asm("{\n\t"
+                ".reg .b16 a, b;\n\t"
+                "cvt.rn.satfinite.e4m3x2.f16x2 a, %1;\n\t"
+                "cvt.rn.satfinite.e4m3x2.f16x2 b, %2;\n\t"
+                "mov.b32 %0, {a, b};\n\t"
+                "}"
+                : "=r"(part[i]) : "r"(x), "r"(y));
         }
     }
 }
@@ -454,7 +463,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     int* s_start = reinterpret_cast<int*>(misc + 536);                // first entry, tiles of it before `begin`
     AttnEntry* s_entry = reinterpret_cast<AttnEntry*>(misc + 544);
     int* s_force = reinterpret_cast<int*>(misc + 592);                // [NWG][2] a row has no n_r yet
-    int* s_flags = reinterpret_cast<int*>(misc + 640);                // [NV] kAbsent: some token is, kTiny: some scale is
+    int* s_flags = reinterpret_cast<int*>(misc + 640);                // [NV] some token is absent, or its scale tiny
     AttnSegment* s_seg = reinterpret_cast<AttnSegment*>(misc + 1024); // [NS]
     int* s_share = reinterpret_cast<int*>(s_seg + NS);                // [NS] CTAs that share an item begun here, or 0
     float* s_qs = reinterpret_cast<float*>(s_share + (NS + 3) / 4 * 4);   // [RP] a row's query scale
@@ -465,7 +474,6 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     float* s_f = s_l + TG * RP;                                       // [TG][RP] factors of the accumulators
     float* s_red = s_f + TG * RP;                                     // [NWG][4][RW]
     int* s_nan = reinterpret_cast<int*>(s_red + TG * 4 * RP);         // [D] first NaN among the new tokens' values
-    constexpr int kAbsent = 1, kTiny = 2;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const CtaWait wait{{p.err_word, p.wait_limit_ns}, s_stop};
@@ -695,8 +703,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                 int flags = 0;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const bool absent = (unsigned)pg[k] >= (unsigned)p.num_pages;
-                    flags |= absent ? kAbsent : b[k] < kTinyScale ? kTiny : 0;
+                    flags |= b[k] < kTinyScale;             // -1 where absent
                     scales[s * kTile + 32 * k + lane] = TokenScales{a[k], b[k]};
                 }
                 flags = __reduce_or_sync(~0u, flags);
@@ -876,20 +883,22 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                 const TokenScales ts = scales[it % NV * kTile + tl];
                 const int flags = s_flags[it % NV];
                 const bool absent = ts.value < 0.f;
-                const float value = absent ? 1.f : ts.value < kTinyScale ? kTinyScale : ts.value;
+                // a scale too small for its logarithm counts as zero: the token weighs, its values do not
+                const bool empty = absent || ts.value < kTinyScale;
+                const float value = empty ? 1.f : ts.value;
                 const float lv = log2_fast(value), inv = __fdividef(1.f, value);
-                const bool masked = (tile + 1) * kTile > seen_first || (flags & kAbsent);
+                const bool masked = (tile + 1) * kTile > seen_first || flags;
 
                 wait(smem_u32(s_full + (it & 1)), (it >> 1) & 1, kErrConsumerWait);
                 tc_fence_after_sync();
-                // values that some row must not see are taken out: all of an absent token, and NaN codes
-                // of the new tokens (0 x NaN would reach every row), which are noted by dim
-                if (masked && (absent || j >= seen_first)) {
+                // values that do not count are taken out: all of an absent token or of a zero scale, and NaN
+                // codes of the new tokens (0 x NaN would reach every row), which are noted by dim
+                if (masked && (empty || j >= seen_first)) {
                     unsigned char* codes = values + it % NV * C::kTileBytes + tl * D;
 #pragma unroll 1
                     for (int c = wg % CG; c < D / 16; c += CG) {
                         uint4* at = reinterpret_cast<uint4*>(codes + c * 16);
-                        if (absent) {
+                        if (empty) {
                             *at = make_uint4(0, 0, 0, 0);
                             continue;
                         }
@@ -1027,10 +1036,6 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                             const int at = (h + r + k) / 2;
                             l[at] = fma2(f2(e[0], e[1]), inv2, l[at]);
                             l[at + 1] = fma2(f2(e[2], e[3]), inv2, l[at + 1]);
-                            if (flags & kTiny) {
-#pragma unroll
-                                for (int m = 0; m < 4; ++m) e[m] *= ts.value < kTinyScale ? ts.value * (1.f / kTinyScale) : 1.f;
-                            }
                             split_e4m3<C::kParts>(e[0], e[1], e[2], e[3], part[k / 4]);
                         }
                         if constexpr (RP == 8) {
