@@ -244,7 +244,12 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 __device__ __forceinline__ float log2_fast(float x) {
     float r;
-    asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 
@@ -355,6 +360,20 @@ __device__ __forceinline__ int lane_value(int lane) {
     return lane / (32 / N);
 }
 
+// A ring's slot and the parity of its current round.
+template <int N>
+struct Ring {
+    int slot = 0;
+    uint32_t round = 0;
+    __device__ __forceinline__ void step(int n = 1) {
+        slot += n;
+        if (slot >= N) {
+            slot -= N;
+            round ^= 1;
+        }
+    }
+};
+
 // Waits of one CTA: bounded, and short once any of them has given up.
 struct CtaWait {
     WaitCtl ctl;
@@ -462,7 +481,6 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     long long* s_walk = reinterpret_cast<long long*>(misc + 512);     // total, begin, end
     int* s_start = reinterpret_cast<int*>(misc + 536);                // first entry, tiles of it before `begin`
     AttnEntry* s_entry = reinterpret_cast<AttnEntry*>(misc + 544);
-    int* s_force = reinterpret_cast<int*>(misc + 592);                // [NWG][2] a row has no n_r yet
     int* s_flags = reinterpret_cast<int*>(misc + 640);                // [NV] some token is absent, or its scale tiny
     AttnSegment* s_seg = reinterpret_cast<AttnSegment*>(misc + 1024); // [NS]
     int* s_share = reinterpret_cast<int*>(s_seg + NS);                // [NS] CTAs that share an item begun here, or 0
@@ -730,11 +748,12 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
         const uint64_t p_desc = umma_desc(smem_u32(sp), 128, kTile * 16, 0);
         int it = 0, seg = 0;
         bool ok = true;
+        Ring<NK> kr;
+        Ring<NV> vr;
         auto scores = [&](int i) {
-            const int s = i % NK;
-            if (!__all_sync(~0u, wait(smem_u32(k_full + s), (i / NK) & 1, kErrConsumerWait))) return false;
+            if (!__all_sync(~0u, wait(smem_u32(k_full + kr.slot), kr.round, kErrConsumerWait))) return false;
             tc_fence_after_sync();
-            const uint64_t a = k_desc + (uint32_t)(s * C::kTileBytes >> 4);
+            const uint64_t a = k_desc + (uint32_t)(kr.slot * C::kTileBytes >> 4);
             const uint32_t d = tmem + (i & 1) * C::kScoreCols;
             if (leader) {
 #pragma unroll
@@ -743,9 +762,10 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                     for (int k = 0; k < D / 32; ++k)
                         umma_e4m3(d, a + 2 * k, q_desc + (part * RP * D >> 4) + 2 * k, kScoreIdesc, part > 0 || k > 0);
                 umma_commit(smem_u32(s_full + (i & 1)));
-                umma_commit(smem_u32(k_empty + s));
+                umma_commit(smem_u32(k_empty + kr.slot));
             }
             __syncwarp();
+            kr.step();
             return true;
         };
         do {
@@ -758,8 +778,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                     break;
                 if (!(ok = __all_sync(~0u, wait(smem_u32(p_full + (it & 1)), (it >> 1) & 1, kErrConsumerWait)))) break;
                 tc_fence_after_sync();
-                const int s = it % NV;
-                const uint64_t a = v_desc + (uint32_t)(s * C::kTileBytes >> 4);
+                const uint64_t a = v_desc + (uint32_t)(vr.slot * C::kTileBytes >> 4);
                 const uint64_t b = p_desc + (uint32_t)((it & 1) * C::kPBytes >> 4);
                 const uint32_t o = tmem + C::kOutCol + (TG == 2 ? (it & 1) * C::kOutCols : 0);
                 const uint32_t more = tile - w.tile0 >= TG;      // this accumulator holds something
@@ -768,9 +787,10 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                     for (int k = 0; k < kTile / 32; ++k)
                         umma_e4m3(o, a + k * (32 * D >> 4), b + k * 32, kOutIdesc, k > 0 ? 1u : more);
                     umma_commit(smem_u32(pv_done + (it & 1)));
-                    umma_commit(smem_u32(v_empty + s));
+                    umma_commit(smem_u32(v_empty + vr.slot));
                 }
                 __syncwarp();
+                vr.step();
             }
             ++seg;
         } while (ok && w.next(p));
@@ -784,6 +804,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
         float* red = s_red + wg * 4 * RW;
         float* my_n = s_n + tg * RP + r0;
         int it0 = 0;                                        // the segment's first tile, counted by the CTA
+        Ring<NV> vr;                                        // its slot of values and scales
         int slot = 0;
         auto pv_wait = [&](int i) {         // the product of tile i has been made
             if (i >= 0) wait(smem_u32(pv_done + (i & 1)), (i >> 1) & 1, kErrConsumerWait);
@@ -867,7 +888,6 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
             }
             if (tid < D) s_nan[tid] = 0x7fffffff;
             if (tl < RW) my_n[tl] = 0.f;
-            if (tl < 2) s_force[wg * 2 + tl] = 1;
             fence_proxy_async_smem();
             group_sync(kAllBar, kSoftmax);
             if (lane == 0) mbar_arrive(smem_u32(q_full));
@@ -877,16 +897,19 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
             for (int r = 0; r < RW / 2; ++r) l[r] = 0;
             uint32_t unset = ~0u;            // threads below RW: this row has no n_r yet
             const int t_first = TG == 2 ? (it0 + tg) & 1 : 0;       // the group's tiles have its parity
+            Ring<NV> vt = vr;
+            if (t_first) vt.step();
+            bool force = true;               // some row has no n_r yet
             for (int t = t_first; t < tiles; t += TG) {
                 const int it = it0 + t, tile = tile_first + t, j = tile * kTile + tl;
-                wait(smem_u32(v_full + it % NV), (it / NV) & 1, kErrConsumerWait);
-                const TokenScales ts = scales[it % NV * kTile + tl];
-                const int flags = s_flags[it % NV];
+                wait(smem_u32(v_full + vt.slot), vt.round, kErrConsumerWait);
+                const TokenScales ts = scales[vt.slot * kTile + tl];
+                const int flags = s_flags[vt.slot];
                 const bool absent = ts.value < 0.f;
                 // a scale too small for its logarithm counts as zero: the token weighs, its values do not
                 const bool empty = absent || ts.value < kTinyScale;
                 const float value = empty ? 1.f : ts.value;
-                const float lv = log2_fast(value), inv = __fdividef(1.f, value);
+                const float lv = log2_fast(value), inv = rcp_fast(value);
                 const bool masked = (tile + 1) * kTile > seen_first || flags;
 
                 wait(smem_u32(s_full + (it & 1)), (it >> 1) & 1, kErrConsumerWait);
@@ -894,7 +917,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                 // values that do not count are taken out: all of an absent token or of a zero scale, and NaN
                 // codes of the new tokens (0 x NaN would reach every row), which are noted by dim
                 if (masked && (empty || j >= seen_first)) {
-                    unsigned char* codes = values + it % NV * C::kTileBytes + tl * D;
+                    unsigned char* codes = values + vt.slot * C::kTileBytes + tl * D;
 #pragma unroll 1
                     for (int c = wg % CG; c < D / 16; c += CG) {
                         uint4* at = reinterpret_cast<uint4*>(codes + c * 16);
@@ -924,6 +947,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                 unsigned char* dst = sp + (it & 1) * C::kPBytes + tl * 16;
                 // new token i, rows i * group on, sees cache indexes below seen0 + i: rows before `from` do not see this one
                 const int from = absent ? RP : max(min(j - seen0 + 1, RP), 0) * p.group - r0;
+                bool still = false;
 #pragma unroll
                 for (int h = 0; h < RW; h += kHalf) {
                     // exponents t + n of kHalf rows
@@ -963,7 +987,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
 #pragma unroll
                     for (int r = 0; r < kHalf; r += 2) top = max3(top, d[r], d[r + 1]);
                     // a row passes the top, or has no n_r yet: its n_r moves, and its sums follow
-                    if (group_any(bar_id, 128, top > kTop || (tl == 0 && s_force[wg * 2 + h / kHalf]))) {
+                    if (group_any(bar_id, 128, top > kTop || force)) {
                         float m0 = 0.f;
 #pragma unroll
                         for (int r = 0; r < kHalf; ++r) {
@@ -983,8 +1007,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                             }
                         }
                         const bool more = group_any(bar_id, 128, tl < kHalf && (unset & bit) && r0 + h + tl < sg->rows);
+                        still |= more;
                         if (tl < kHalf) red[tl] = move;
-                        if (tl == 0) s_force[wg * 2 + h / kHalf] = more;
                         group_sync(bar_id, 128);
 #pragma unroll
                         for (int r = 0; r < kHalf; r += 4) {
@@ -1058,6 +1082,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(p_full + (it & 1)));
+                if (force) force = still;
+                vt.step(TG);
             }
 
             // the next segment's queries are on their way while this one's sums are made
@@ -1082,6 +1108,11 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
             group_sync(bar_id, 128);
             if (tl < RW) s_l[tg * RP + r0 + tl] = (red[tl] + red[RW + tl]) + (red[2 * RW + tl] + red[3 * RW + tl]);
             it0 += tiles;
+            {
+                const int rounds = (vr.slot + tiles) / NV;
+                vr.slot += tiles - rounds * NV;
+                vr.round ^= rounds & 1;
+            }
             if (NWG > 1) group_sync(kAllBar, kSoftmax);
             const int cta_slot = blockIdx.x * 2 + slot;
             if (tid < RP) {
