@@ -1209,7 +1209,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
 template <int D, int W>
 __global__ void __launch_bounds__(128) attention_combine_kernel(const __grid_constant__ AttnParams p, int rp, int grid) {
     constexpr int V = D / 32;
-    __shared__ float s_acc[4][D], s_sum[4];
+    __shared__ float s_acc[4][D];
+    __shared__ float2 s_stat[4];
     griddep_wait();
     griddep_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1217,40 +1218,69 @@ __global__ void __launch_bounds__(128) attention_combine_kernel(const __grid_con
     const AttnSplit s = p.split[c];
     if (s.n == 0 || row >= s.rows) return;
     const float* stats = p.partial + (size_t)grid * 2 * rp * D;
-    auto slot = [&](int i) { return (size_t)(2 * (c + i) + (i == 0 ? s.slot0 : 0)); };
-    float least = INFINITY;
-    for (int i = lane; i < s.n; i += 32) least = fminf(least, stats[(slot(i) * rp + row) * 2]);
-    least = -warp_max_f32(-least);
-    float acc[V] = {}, sum = 0.f;
-#pragma unroll 5
-    for (int i = first; i < s.n; i += W) {
-        const size_t at = slot(i) * rp + row;
-        const float2 st = *reinterpret_cast<const float2*>(stats + at * 2);
-        const float f = st.x == INFINITY ? 0.f : exp2_fast(least - st.x);
-        sum = fmaf(f, st.y, sum);
-        const float* o = p.partial + at * D + lane * V;
-        if constexpr (V == 4) {
-            const float4 x = *reinterpret_cast<const float4*>(o);
-            acc[0] = fmaf(f, x.x, acc[0]);
-            acc[1] = fmaf(f, x.y, acc[1]);
-            acc[2] = fmaf(f, x.z, acc[2]);
-            acc[3] = fmaf(f, x.w, acc[3]);
-        } else {
-            const float2 x = *reinterpret_cast<const float2*>(o);
-            acc[0] = fmaf(f, x.x, acc[0]);
-            acc[1] = fmaf(f, x.y, acc[1]);
+    auto slot = [&](int i) { return (size_t)(2 * (c + i) + (i == 0 ? s.slot0 : 0)) * rp + row; };
+    float acc[V] = {}, sum = 0.f, least = INFINITY;
+    // this warp's pieces first + W k, kAhead of them at a time: all loads before their first use
+    constexpr int kAhead = 10;
+    for (int i0 = first; i0 < s.n; i0 += W * kAhead) {
+        float x[kAhead][V];
+        float2 st[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int i = i0 + W * k;
+            st[k] = make_float2(INFINITY, 0.f);
+            if (i < s.n) {
+                const float* at = p.partial + slot(i) * D + lane * V;
+                st[k] = *reinterpret_cast<const float2*>(stats + slot(i) * 2);
+                if constexpr (V == 4) {
+                    const float4 y = *reinterpret_cast<const float4*>(at);
+                    x[k][0] = y.x; x[k][1] = y.y; x[k][2] = y.z; x[k][3] = y.w;
+                } else {
+                    const float2 y = *reinterpret_cast<const float2*>(at);
+                    x[k][0] = y.x; x[k][1] = y.y;
+                }
+            }
+        }
+        float now = least;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) now = fminf(now, st[k].x);
+        const float fix = least == INFINITY ? 0.f : exp2_fast(now - least);
+        sum *= fix;
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] *= fix;
+        least = now;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (st[k].x == INFINITY) continue;              // nothing seen there, or no such piece
+            const float f = exp2_fast(least - st[k].x);
+            sum = fmaf(f, st[k].y, sum);
+#pragma unroll
+            for (int v = 0; v < V; ++v) acc[v] = fmaf(f, x[k][v], acc[v]);
         }
     }
     if constexpr (W == 4) {
 #pragma unroll
         for (int k = 0; k < V; ++k) s_acc[warp][lane * V + k] = acc[k];
-        if (lane == 0) s_sum[warp] = sum;
+        if (lane == 0) s_stat[warp] = make_float2(least, sum);
         __syncthreads();
         if (warp > 0) return;
+        float2 st[4];
 #pragma unroll
-        for (int k = 0; k < V; ++k)
-            acc[k] = (s_acc[0][lane * V + k] + s_acc[1][lane * V + k]) + (s_acc[2][lane * V + k] + s_acc[3][lane * V + k]);
-        sum = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
+        for (int w = 0; w < 4; ++w) {
+            st[w] = s_stat[w];
+            least = fminf(least, st[w].x);
+        }
+        sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            if (st[w].x == INFINITY) continue;
+            const float f = exp2_fast(least - st[w].x);
+            sum = fmaf(f, st[w].y, sum);
+#pragma unroll
+            for (int k = 0; k < V; ++k) acc[k] = fmaf(f, s_acc[w][lane * V + k], acc[k]);
+        }
     }
     const int i = row / p.group, g = row - i * p.group;
     const size_t at = (size_t)(s.row0 + i) * p.q_heads + s.head * p.group + g;
