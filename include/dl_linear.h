@@ -326,7 +326,8 @@ typedef struct dl_kv_cache {
     void* k;                     /* e4m3 codes, 16-byte aligned: (page p, head h, token t,  */
     void* v;                     /*   dim d) at p*page_stride + h*head_stride + t*head_dim + d */
     float* k_scale;              /* (p, h, block c) at p*scale_page_stride                 */
-    float* v_scale;              /*   + h*scale_head_stride + c; finite, >= 0; 4-byte aligned */
+    float* v_scale;              /*   + h*scale_head_stride + c; finite, >= 0 (v_scale below
+                                      2^-60 counts as 0); 4-byte aligned                   */
     long long page_stride;       /* bytes, multiples of 16                                 */
     long long head_stride;
     long long scale_page_stride; /* elements                                               */
@@ -452,7 +453,8 @@ dl_status dl_set_override(int kernel, int ctas_per_sm, int max_ctas);
  *                   k-th pipeline stage (the stage's barrier expects its
  *                   bytes) but never issues the copies that would fill it, so
  *                   every wait on that stage runs out; no copy is in flight
- *                   for it when the CTA leaves.  Needs 0 < wait_limit_ns <=
+ *                   for it when the CTA leaves.  In an attention launch CTA 0
+ *                   does the same with the keys of its k-th tile of 128 tokens.  Needs 0 < wait_limit_ns <=
  *                   100 ms (else DL_ERR_INVALID_ARG).
  * A launch that ran with a withheld stage leaves wrong outputs and may leave
  * arrival counters set in its workspace: zero the workspace's first

@@ -277,6 +277,28 @@ def test_workspace_serves_linears_too(cuda_device):
     assert not ws.tensor[:dl.WORKSPACE_ZERO_BYTES].any()
 
 
+@pytest.mark.parametrize("group,news,withhold", [(8, 1, 1), (8, 1, 2), (8, 6, 3), (8, 8, 2)])
+def test_a_withheld_tile_runs_out_and_reports(cuda_device, group, news, withhold):
+    """The keys of one tile never come: the waits on it run out, the call ends with an error status
+    and the context stays usable."""
+    # one head, 300 tiles and more: CTA 0 has several
+    step = Step([90000], [news], heads=group, kv_heads=1, page=64, block=16, seed=40)
+    q, c, seqs = step.q.to(cuda_device), step.cache(cuda_device), step.seqs(cuda_device)
+    first = dl.attention_paged(q, c, *seqs, max_q=news)
+    torch.cuda.synchronize(cuda_device)
+    assert dl.device_status() == 0
+    dl.set_wait_test(20_000_000, withhold)
+    try:
+        dl.attention_paged(q, c, *seqs, max_q=news)
+        torch.cuda.synchronize(cuda_device)
+        assert dl.device_status() & 1
+    finally:
+        dl.set_wait_test(0, 0)
+    again = dl.attention_paged(q, c, *seqs, max_q=news)
+    torch.cuda.synchronize(cuda_device)
+    assert dl.device_status() == 0 and torch.equal(first, again)
+
+
 def test_refusals(cuda_device):
     step = Step([9], [1], seed=39)
     c, seqs, q = step.cache(cuda_device), step.seqs(cuda_device), step.q.to(cuda_device)

@@ -1127,6 +1127,7 @@ dl_status host_device(HostDevice& out) {
     out.err_word = di.err_word;
     const long long wait_o = g_wait_ns_override.load();
     out.wait_limit_ns = wait_o > 0 ? (unsigned long long)wait_o : kWaitLimitNs;
+    out.withhold_stage = g_withhold_override.load();
     return DL_OK;
 }
 

@@ -18,6 +18,7 @@ struct HostDevice {
     int sm_count;
     unsigned* err_word;                   // the device error word
     unsigned long long wait_limit_ns;     // of every device-side wait
+    int withhold_stage;                   // dl_set_wait_test's (0: none)
 };
 // The current device's (cached) description.
 dl_status host_device(HostDevice& out);

@@ -127,6 +127,7 @@ extern "C" dl_status dl_attention_paged(const dl_kv_cache* cache, const void* q,
     p.partial = reinterpret_cast<float*>(ws + split_bytes(a.grid));
     p.err_word = dev.err_word;
     p.wait_limit_ns = dev.wait_limit_ns;
+    p.withhold = dev.withhold_stage;
     const cudaError_t e = cache->head_dim == 128 ? launch_attention_d128(rt.padded, a)
                                                  : launch_attention_d64(rt.padded, a);
     if (e != cudaSuccess) return host_fail(DL_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));

@@ -56,6 +56,7 @@ struct AttnParams {
     struct AttnSplit* split;            // [grid]
     unsigned* err_word;
     unsigned long long wait_limit_ns;
+    int withhold;                       // k: CTA 0 never copies its k-th tile's keys (0: none)
 };
 
 // A split item, at the index of the CTA that begins it (n = 0: none).
@@ -391,6 +392,7 @@ struct CtaWait {
     __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity, unsigned bit) const {
         // a test answers in a third of the time of a wait that may suspend
         if (__builtin_expect(mbar_test(bar, parity), 1)) return true;
+        if (*stop) return false;
 #pragma unroll 1
         for (int i = 0; i < 32; ++i)
             if (mbar_try_wait(bar, parity)) return true;
@@ -528,7 +530,10 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
             for (int i = 0; i < NS; ++i) mbar_init(smem_u32(seg_full + i), 1);
             *s_stop = 0;
             // read only after a wait that gave up: nothing to do, and nothing after it
-            for (int i = 0; i < NS; ++i) s_seg[i] = AttnSegment{0, 0, 0, 0, 0, 0, 1, 1};
+            for (int i = 0; i < NS; ++i) {
+                s_seg[i] = AttnSegment{0, 0, 0, 0, 0, 0, 1, 1};
+                s_share[i] = 0;
+            }
             fence_mbarrier_init();
         }
         __syncwarp();
@@ -648,7 +653,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                 if (!ok) break;
                 if (lane == 0) mbar_arrive_expect_tx(smem_u32(k_full + ks), bytes);
                 __syncwarp();
-                if (page >= 0 && !is_v)
+                if (page >= 0 && !is_v && !(it + 1 == p.withhold && blockIdx.x == 0))
                     tma_load_4d(smem_u32(keys + ks * C::kTileBytes + sub * box * D), &tk, smem_u32(k_full + ks), 0, at,
                                 w.head / p.head_parts, page);
                 if (it >= NV) ok = __all_sync(~0u, wait(smem_u32(v_empty + vs), (it / NV - 1) & 1, kErrProducerWait));
