@@ -190,8 +190,10 @@ __global__ void __launch_bounds__(kVerifyThreads, BATCH > 2 ? 1 : 3) verify_draf
         const long long theirs = lane < size ? *cluster.map_shared_rank(&s_total, lane) : 0;
         total = warp_sum(theirs);
         before = warp_sum(lane < rank ? theirs : 0);
-        cluster.sync();
-        if (total > 0) break;
+        // no CTA leaves, or writes its total again, before all have read it
+        cluster.barrier_arrive();
+        if (total > 0 || pass == 1) break;
+        cluster.barrier_wait();
     }
     if (total > 0) {
         long long r = (long long)floorf(fminf(fmaxf(p.u_next[b], 0.f), 1.f) * 16777216.f);
@@ -244,6 +246,7 @@ __global__ void __launch_bounds__(kVerifyThreads, BATCH > 2 ? 1 : 3) verify_draf
             p.tokens[(size_t)b * (p.drafts + 1) + tid] = tid < c ? drafts[tid] : -1;
         if (tid == 0) p.count[b] = c;
     }
+    cluster.barrier_wait();
 }
 
 template <class T, int BATCH>
@@ -276,9 +279,9 @@ cudaError_t launch_verify_batch(const VerifyParams& p, int batch, int size, cuda
 
 template <class T>
 cudaError_t launch_verify(const VerifyParams& p, int batch, int sm_count, cudaStream_t stream) {
-    // CTAs of a sequence: as many as leave three to each SM, at most 16 (a cluster), each warp
-    // with 128 entries at least.  Where an SM has one CTA, its warps have five groups of
-    // entries in flight, else two, and registers for three CTAs.
+    // CTAs of a sequence: a power of two, as many as leave three to each SM, at most 16 (a cluster), each warp with
+    // 128 entries at least.  Where an SM has one CTA, its warps have five groups of entries in
+    // flight, else two, and registers for three CTAs.
     int size = 1;
     while (size < kMaxCluster && (long long)batch * size * 2 <= 3LL * sm_count &&
            size * kVerifyWarps * 128 < p.vocab)
