@@ -17,7 +17,7 @@ struct AppendParams {
     int blocks_per_seq;          // most blocks a sequence's new tokens touch
     int team, kv_ctas;           // threads of a block, CTAs that take blocks
     int per;                     // tokens whose queries a CTA takes
-    long long kv_units;          // blocks of keys (as many of values follow)
+    long long kv_units;          // blocks that get new tokens, at most
     Sequences s;
 };
 
@@ -150,21 +150,18 @@ __device__ __forceinline__ void append_queries(const AppendParams& p, int t0) {
 }
 
 // `team` threads (a power of two, a multiple of D / 16) take one block of one
-// head's keys or values.  The block's largest value comes first, then its
-// codes; where the block is more than one pass long its rows are read again
-// (from L1 or L2) rather than held.
+// head, its keys and its values together: what leads to them (the sequence, then its
+// page) is a chain of loads that costs more than the block.  The block's largest
+// values come first, then its codes; where the block is more than one pass long its
+// rows are read again (from L1 or L2) rather than held.
 template <int D>
 __device__ __forceinline__ void append_block(const AppendParams& p, long long unit, int at, int team) {
     constexpr int kUnits = D / 16;
-    const bool is_v = unit >= p.kv_units;
-    if (is_v) unit -= p.kv_units;
     const bool live = unit < p.kv_units;
     const int h = live ? (int)(unit % p.c.num_heads) : 0;
     const long long rest = live ? unit / p.c.num_heads : 0;
     const int j = (int)(rest % p.blocks_per_seq), b = (int)(rest / p.blocks_per_seq);
     int lo = 0, hi = 0, blk = 0, first = 0, row0 = 0;
-    uint8_t* codes = nullptr;
-    float* scale = nullptr;
     if (live) {
         const SequenceView sv = sequence_view(p.s, b, p.c.page_size);
         first = sv.len - sv.n;                              // cache index of the first new token
@@ -173,82 +170,112 @@ __device__ __forceinline__ void append_block(const AppendParams& p, long long un
         row0 = sv.row0;
         blk = ((begin >> p.block_shift) + j) << p.block_shift;
         if (blk < last) {
-            const int page = p.s.block_table[(size_t)b * p.s.table_cols + (blk >> p.page_shift)];
-            if ((unsigned)page < (unsigned)p.c.num_pages) {
-                const int t0 = blk & (p.c.page_size - 1);
-                codes = static_cast<uint8_t*>(is_v ? p.c.v : p.c.k) + page * p.c.page_stride +
-                        h * p.c.head_stride + (size_t)t0 * D;
-                scale = (is_v ? p.c.v_scale : p.c.k_scale) + page * p.c.scale_page_stride +
-                        h * p.c.scale_head_stride + (t0 >> p.block_shift);
-                lo = max(blk, begin);
-                hi = min(blk + p.c.block, last);
-            }
+            lo = max(blk, begin);
+            hi = min(blk + p.c.block, last);
         }
     }
-    const uint16_t* src = (is_v ? p.v : p.k) + (size_t)h * D;
-    const long long stride = is_v ? p.v_stride : p.k_stride;
-    const RowUnit u = row_unit(at % kUnits, is_v ? 0 : p.rotary_dim);
-    auto values = [&](int index, float (&f)[16]) {
+    int page = -1;
+    if (hi > lo) page = p.s.block_table[(size_t)b * p.s.table_cols + (blk >> p.page_shift)];
+    const RowUnit uk = row_unit(at % kUnits, p.rotary_dim), uv = row_unit(at % kUnits, 0);
+    // a row's 16 keys of this thread, rotated, and its 16 values as they come (held in half the registers)
+    auto load = [&](int index, float (&f)[16], uint4 (&raw)[2]) {
         const int t = row0 + index - first;
-        const uint16_t* row = src + (size_t)t * stride;
-        unpack8(ldg128(row + u.a), f);
-        unpack8(ldg128(row + u.b), f + 8);
-        if (u.angle >= 0) {
-            float c[8], s[8];
-            load_angles(p, position_of(p, t, index), u.angle, c, s);
-            rotate(f, c, s);
-        }
+        const uint16_t* k = p.k + (size_t)t * p.k_stride + (size_t)h * D;
+        const uint16_t* v = p.v + (size_t)t * p.v_stride + (size_t)h * D;
+        const uint4 x0 = ldg128(k + uk.a), x1 = ldg128(k + uk.b);
+        raw[0] = ldg128(v + uv.a);
+        raw[1] = ldg128(v + uv.b);
+        float c[8], s[8];
+        if (uk.angle >= 0) load_angles(p, position_of(p, t, index), uk.angle, c, s);
+        unpack8(x0, f);
+        unpack8(x1, f + 8);
+        if (uk.angle >= 0) rotate(f, c, s);
     };
-    const float s0 = scale ? *scale : 1.f;
-    const int step = team / kUnits;
-    float f[16];
-    float amax = 0.f;
-    for (int index = lo + at / kUnits; index < hi; index += step) {
-        values(index, f);
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
+    auto largest = [](const float* f, int n, float m) {       // of the finite ones
+        for (int k = 0; k < n; ++k) {
             const float a = fabsf(f[k]);
-            if (a <= 3.402823466e38f) amax = fmaxf(amax, a);
+            if (a <= 3.402823466e38f) m = fmaxf(m, a);
+        }
+        return m;
+    };
+    const int step = team / kUnits;
+    float f[16], amax[2] = {0.f, 0.f};
+    uint4 raw[2];
+    for (int index = lo + at / kUnits; index < hi; index += step) {
+        load(index, f, raw);
+        amax[0] = largest(f, 16, amax[0]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float g[8];
+            unpack8(raw[i], g);
+            amax[1] = largest(g, 8, amax[1]);
         }
     }
-    __shared__ float part[kAppendThreads / 32];
-    for (int o = min(team, 32) / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+    __shared__ float part[2][kAppendThreads / 32];
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+        for (int o = min(team, 32) / 2; o; o >>= 1) amax[w] = fmaxf(amax[w], __shfl_xor_sync(~0u, amax[w], o));
+    const bool found = (unsigned)page < (unsigned)p.c.num_pages;
+    const int t0 = blk & (p.c.page_size - 1);
+    const long long scale_at = found ? page * p.c.scale_page_stride + h * p.c.scale_head_stride + (t0 >> p.block_shift) : 0;
+    const long long codes_at = found ? page * p.c.page_stride + h * p.c.head_stride + (long long)t0 * D : 0;
+    const bool had = lo > blk;
+    float s0[2] = {1.f, 1.f};
+    if (found && had) {
+        s0[0] = p.c.k_scale[scale_at];
+        s0[1] = p.c.v_scale[scale_at];
+    }
     if (team > 32) {
         const int warp = threadIdx.x >> 5, w0 = warp & ~(team / 32 - 1);
-        if ((threadIdx.x & 31) == 0) part[warp] = amax;
-        __syncthreads();
-        for (int w = 0; w < team / 32; ++w) amax = fmaxf(amax, part[w0 + w]);
-    }
-    if (hi <= lo) return;
-    float s1 = block_scale(amax);
-    const bool had = lo > blk;
-    if (had && !(s0 < s1)) s1 = s0;
-    const float inv = __frcp_rn(s1);
-    if (had && s1 != s0)
-        for (int e = at; e < (lo - blk) * D; e += team)
-            codes[e] = (uint8_t)f32x2_to_e4m3x2(__fmul_rn(__fmul_rn(e4m3_value(codes[e]), s0), inv), 0.f);
-    const bool once = hi - lo <= step;          // the values of the first pass are still held
-    for (int index = lo + at / kUnits; index < hi; index += step) {
-        if (!once) values(index, f);
-        uint32_t w[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            w[k] = f32x2_to_e4m3x2(__fmul_rn(f[4 * k], inv), __fmul_rn(f[4 * k + 1], inv)) |
-                   f32x2_to_e4m3x2(__fmul_rn(f[4 * k + 2], inv), __fmul_rn(f[4 * k + 3], inv)) << 16;
-        uint8_t* row = codes + (size_t)(index - blk) * D;
-        if (u.angle >= 0) {
-            *reinterpret_cast<uint2*>(row + u.a) = make_uint2(w[0], w[1]);
-            *reinterpret_cast<uint2*>(row + u.b) = make_uint2(w[2], w[3]);
-        } else {
-            *reinterpret_cast<uint4*>(row + u.a) = make_uint4(w[0], w[1], w[2], w[3]);
+        if ((threadIdx.x & 31) == 0) {
+            part[0][warp] = amax[0];
+            part[1][warp] = amax[1];
         }
+        __syncthreads();                    // and the old scales have been read by all
+        for (int i = 0; i < team / 32; ++i) {
+            amax[0] = fmaxf(amax[0], part[0][w0 + i]);
+            amax[1] = fmaxf(amax[1], part[1][w0 + i]);
+        }
+    } else {
+        __syncwarp();
     }
-    if (at == 0) *scale = s1;
+    if (hi <= lo || !found) return;
+    const bool once = hi - lo <= step;          // the values of the first pass are still held
+    float inv[2];
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        float s1 = block_scale(amax[w]);
+        if (had && !(s0[w] < s1)) s1 = s0[w];
+        inv[w] = __frcp_rn(s1);
+        if (had && s1 != s0[w]) {
+            uint8_t* codes = static_cast<uint8_t*>(w ? p.c.v : p.c.k) + codes_at;
+            for (int e = at; e < (lo - blk) * D; e += team)
+                codes[e] = (uint8_t)f32x2_to_e4m3x2(__fmul_rn(__fmul_rn(e4m3_value(codes[e]), s0[w]), inv[w]), 0.f);
+        }
+        if (at == 0) (w ? p.c.v_scale : p.c.k_scale)[scale_at] = s1;
+    }
+    for (int index = lo + at / kUnits; index < hi; index += step) {
+        if (!once) load(index, f, raw);
+        const size_t row = codes_at + (size_t)(index - blk) * D;
+        auto code = [](const float* x, float inv) {           // four values
+            return f32x2_to_e4m3x2(__fmul_rn(x[0], inv), __fmul_rn(x[1], inv)) |
+                   f32x2_to_e4m3x2(__fmul_rn(x[2], inv), __fmul_rn(x[3], inv)) << 16;
+        };
+        uint8_t* k = static_cast<uint8_t*>(p.c.k) + row;
+        *reinterpret_cast<uint2*>(k + uk.a) = make_uint2(code(f, inv[0]), code(f + 4, inv[0]));
+        *reinterpret_cast<uint2*>(k + uk.b) = make_uint2(code(f + 8, inv[0]), code(f + 12, inv[0]));
+        float g[8];
+        unpack8(raw[0], g);
+        const uint2 v0 = make_uint2(code(g, inv[1]), code(g + 4, inv[1]));
+        unpack8(raw[1], g);
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.c.v) + row + uv.a) =
+            make_uint4(v0.x, v0.y, code(g, inv[1]), code(g + 4, inv[1]));
+    }
 }
 
 // grid.x: the CTAs of the blocks, then those of the queries.
 template <int D>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const __grid_constant__ AppendParams p) {
     griddep_wait();
     griddep_launch_dependents();
     if ((int)blockIdx.x >= p.kv_ctas) {
@@ -383,9 +410,9 @@ extern "C" dl_status dl_kv_append(const dl_kv_cache* cache, const void* q, const
     if ((s = host_device(dev)) != DL_OK) return s;
     // a CTA's search and position are shared by four tokens once that leaves several CTAs to each SM
     p.per = tokens >= 16 * dev.sm_count ? 4 : 1;
-    const long long kv_ctas = (2 * p.kv_units + blocks - 1) / blocks, grid = kv_ctas + (q ? (tokens + p.per - 1) / p.per : 0);
+    const long long kv_ctas = (p.kv_units + blocks - 1) / blocks, grid = kv_ctas + (q ? (tokens + p.per - 1) / p.per : 0);
     if (grid > 0x7fffffffLL)
-        return host_fail(DL_ERR_UNSUPPORTED_SHAPE, "%lld blocks to write exceed one launch", 2 * p.kv_units);
+        return host_fail(DL_ERR_UNSUPPORTED_SHAPE, "%lld blocks to write exceed one launch", p.kv_units);
     p.kv_ctas = (int)kv_ctas;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = D == 128 ? launch_append<128>(p, (unsigned)grid, st) : launch_append<64>(p, (unsigned)grid, st);
