@@ -15,8 +15,8 @@ struct AppendParams {
     int rotary_dim, max_pos, q_heads;
     int page_shift, block_shift;
     int blocks_per_seq;          // most blocks a sequence's new tokens touch
-    int team, kv_ctas;           // threads of a block, CTAs that take blocks
-    int per;                     // tokens whose queries a CTA takes
+    int team, per;               // threads of a block; tokens whose queries a CTA takes
+    int kv_ctas, q_ctas, period; // CTAs that take blocks, and queries
     long long kv_units;          // blocks that get new tokens, at most
     Sequences s;
 };
@@ -273,16 +273,20 @@ __device__ __forceinline__ void append_block(const AppendParams& p, long long un
     }
 }
 
-// grid.x: the CTAs of the blocks, then those of the queries.
+// grid.x: the CTAs of the blocks and those of the queries in turn, `period` apart
+// the fewer ones: the blocks wait for their chains of loads while the queries stream.
 template <int D>
 __global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const __grid_constant__ AppendParams p) {
     griddep_wait();
     griddep_launch_dependents();
-    if ((int)blockIdx.x >= p.kv_ctas) {
-        append_queries<D>(p, (blockIdx.x - p.kv_ctas) * p.per);
+    const int i = blockIdx.x, turn = i / p.period, fewer = min(p.kv_ctas, p.q_ctas);
+    const bool of_fewer = i - turn * p.period == 0 && turn < fewer, kv_fewer = p.kv_ctas < p.q_ctas;
+    const int index = of_fewer ? turn : i - min(turn + 1, fewer);
+    if (of_fewer != kv_fewer) {
+        append_queries<D>(p, index * p.per);
     } else {
         const int team = p.team, per = kAppendThreads / team;
-        append_block<D>(p, (long long)blockIdx.x * per + threadIdx.x / team, threadIdx.x % team, team);
+        append_block<D>(p, (long long)index * per + threadIdx.x / team, threadIdx.x % team, team);
     }
 }
 
@@ -410,10 +414,13 @@ extern "C" dl_status dl_kv_append(const dl_kv_cache* cache, const void* q, const
     if ((s = host_device(dev)) != DL_OK) return s;
     // a CTA's search and position are shared by four tokens once that leaves several CTAs to each SM
     p.per = tokens >= 16 * dev.sm_count ? 4 : 1;
-    const long long kv_ctas = (p.kv_units + blocks - 1) / blocks, grid = kv_ctas + (q ? (tokens + p.per - 1) / p.per : 0);
+    const long long kv_ctas = (p.kv_units + blocks - 1) / blocks, q_ctas = q ? (tokens + p.per - 1) / p.per : 0;
+    const long long grid = kv_ctas + q_ctas, fewer = kv_ctas < q_ctas ? kv_ctas : q_ctas;
     if (grid > 0x7fffffffLL)
         return host_fail(DL_ERR_UNSUPPORTED_SHAPE, "%lld blocks to write exceed one launch", p.kv_units);
     p.kv_ctas = (int)kv_ctas;
+    p.q_ctas = (int)q_ctas;
+    p.period = fewer ? (int)(grid / fewer) : 1;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = D == 128 ? launch_append<128>(p, (unsigned)grid, st) : launch_append<64>(p, (unsigned)grid, st);
     if (e != cudaSuccess) return host_fail(DL_ERR_CUDA, "kv_append launch: %s", cudaGetErrorString(e));
