@@ -61,7 +61,7 @@ extern "C" size_t dl_attention_workspace_bytes(int batch, int tokens, int q_head
     dl::HostDevice dev;
     if (dl::host_device(dev) != DL_OK) return 0;
     const int rp = row_tiles(tokens, max_q, q_heads / kv_heads).padded;
-    return workspace_bytes(dev.sm_count * dl::attn_ctas_per_sm(rp), rp, head_dim);
+    return workspace_bytes(dev.sm_count * dl::attn_ctas_per_sm(rp, head_dim), rp, head_dim);
 }
 
 extern "C" dl_status dl_attention_paged(const dl_kv_cache* cache, const void* q, long long q_stride,
@@ -94,7 +94,7 @@ extern "C" dl_status dl_attention_paged(const dl_kv_cache* cache, const void* q,
     if ((long long)batch * rt.count > 0x7fffffffLL)
         return host_fail(DL_ERR_UNSUPPORTED_SHAPE, "batch=%d times %d row tiles exceed one launch", batch, rt.count);
     AttnLaunch a = {};
-    a.grid = dev.sm_count * attn_ctas_per_sm(rt.padded);
+    a.grid = dev.sm_count * attn_ctas_per_sm(rt.padded, cache->head_dim);
     a.stream = static_cast<cudaStream_t>(stream);
     const size_t need = workspace_bytes(a.grid, rt.padded, cache->head_dim);
     if (ws_bytes < need)

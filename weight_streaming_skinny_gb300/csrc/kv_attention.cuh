@@ -113,10 +113,12 @@ struct AttnShare {
 };
 
 // RP rows.  A tile's chain of waits and dependent instructions is longer than its
-// share of the memory's time, so two tiles are in work on an SM: two CTAs up to 16
-// rows, beyond that one CTA whose two tile groups (TG) take tiles in turn, with
-// accumulators of their own, and share the pipeline's slots.  A tile group is CG
-// warpgroups of RW rows each: more warps to hide one another's latencies.
+// share of the memory's time, so several tiles are in work on an SM: two CTAs up to
+// 16 rows (three with heads of 64, whose tiles are half as long: 32 sequences of
+// 4096 tokens, 8 rows, 28.1 -> 26.1 us), beyond that one CTA whose two tile groups
+// (TG) take tiles in turn, with accumulators of their own, and share the pipeline's
+// slots.  A tile group beyond 32 rows is two warpgroups (CG) of RW rows each: more
+// warps to hide one another's latencies (64 rows: 200 -> 159 us at 4 x 32768 tokens).
 template <int D_, int RP_>
 struct AttnShape {
     static constexpr int D = D_, RP = RP_;
@@ -130,7 +132,7 @@ struct AttnShape {
     static constexpr int kOutCols = kParts * RP;
     static constexpr int kCols = kOutCol + TG * kOutCols;
     static constexpr int kTmem = kCols <= 32 ? 32 : kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
-    static constexpr int kCtas = 3 - TG;                // resident CTAs per SM
+    static constexpr int kCtas = TG == 2 ? 1 : D == 64 ? 3 : 2;      // resident CTAs per SM
     static constexpr int kThreads = TG * CG * 128 + 96;
     static constexpr int kTileBytes = kTile * D;        // codes of K, and of V
     static constexpr int kQBytes = 2 * RP * D;
@@ -138,7 +140,7 @@ struct AttnShape {
     // segment descriptors: one more than tiles can be in flight, and the one in work
     static constexpr int kSegments = 10;
     static constexpr int kMisc = 1024 + kSegments * 36 + 8 + RP * (16 + 16 * TG) + TG * 4 * RP * 4 + D * 4 + 256;
-    static constexpr int kBudget = (kCtas == 1 ? 227 : 113) * 1024;
+    static constexpr int kBudget = (kCtas == 1 ? 227 : kCtas == 2 ? 113 : 75) * 1024;
     // a tile's slots: its codes, and 8 bytes of scales for each token
     static constexpr int kScaleBytes = kTile * 8;
     static constexpr int kRoom = kBudget - 1024 - kQBytes - 2 * kPBytes - kMisc;
@@ -1315,7 +1317,7 @@ struct AttnLaunch {
 // RP and resident CTAs per SM of the instance for `rows` rows (at most kMaxRows).
 constexpr int kMaxRows = 64;
 inline int attn_rows_padded(int rows) { return rows <= 8 ? 8 : rows <= 48 ? (rows + 15) / 16 * 16 : 64; }
-inline int attn_ctas_per_sm(int rp) { return rp > 16 ? 1 : 2; }
+inline int attn_ctas_per_sm(int rp, int dim) { return rp > 16 ? 1 : dim == 64 ? 3 : 2; }
 
 cudaError_t launch_attention_d64(int rp, const AttnLaunch& a);
 cudaError_t launch_attention_d128(int rp, const AttnLaunch& a);
