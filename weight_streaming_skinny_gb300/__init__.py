@@ -38,6 +38,7 @@ _LIB_PATH = os.path.join(_HERE, "libdecode_linear.so")
 _HEADER = os.path.join(os.path.dirname(_HERE), "include", "dl_linear.h")
 _lock = threading.Lock()
 _lib = None
+_native: dict = {}       # the calls of _binding, once the library is loaded
 
 _STATUS = {0: "DL_OK", 1: "DL_ERR_INVALID_ARG", 2: "DL_ERR_UNSUPPORTED_SHAPE",
            3: "DL_ERR_MISALIGNED", 4: "DL_ERR_WORKSPACE", 5: "DL_ERR_CUDA", 6: "DL_ERR_DEVICE"}
@@ -108,17 +109,8 @@ def load():
         lib.dl_linear_argmax.argtypes = [i, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, vp, sz, vp]
         lib.dl_linear_argmax.restype = i
         lib.dl_linear_swiglu.restype = i
-        ll, f = ctypes.c_longlong, ctypes.c_float
-        lib.dl_kv_append.argtypes = [ctypes.POINTER(_KVCache), vp, vp, vp, ll, ll, ll, vp, vp, vp, i, i,
-                                     vp, vp, i, vp, vp, i, i, i, i, vp]
-        lib.dl_kv_append.restype = i
-        lib.dl_attention_paged.argtypes = [ctypes.POINTER(_KVCache), vp, ll, vp, vp, vp, i, vp, vp,
-                                           i, i, i, i, f, vp, sz, vp]
-        lib.dl_attention_paged.restype = i
         lib.dl_attention_workspace_bytes.argtypes = [i, i, i, i, i, i]
         lib.dl_attention_workspace_bytes.restype = sz
-        lib.dl_verify_draft.argtypes = [vp, vp, vp, i, vp, vp, vp, vp, vp, i, i, i, vp]
-        lib.dl_verify_draft.restype = i
         lib.dl_set_override.argtypes = [i, i, i]
         lib.dl_set_override.restype = i
         lib.dl_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint)]
@@ -126,6 +118,12 @@ def load():
         if lib.dl_version() != ABI_VERSION:
             raise RuntimeError(f"{_LIB_PATH} is ABI version {lib.dl_version()}, this binding "
                                f"marshals version {ABI_VERSION}: rebuild the library")
+        from . import _binding
+        address = lambda f: ctypes.cast(f, vp).value   # noqa: E731
+        _binding.bind(torch.Tensor, torch.bfloat16, torch.int32, torch.float32,
+                      torch._C._cuda_getCurrentRawStream, address(lib.cudaGetDevice),
+                      address(lib.dl_kv_append), address(lib.dl_attention_paged), address(lib.dl_verify_draft))
+        _native.update(append=_binding.append, attention=_binding.attention, verify=_binding.verify)
         _lib = lib
         return lib
 
@@ -196,6 +194,7 @@ class Workspace:
         self.tensor = torch.zeros(self.nbytes, dtype=torch.uint8, device=device)
         # the zeros must be in place before a kernel on any stream reads them
         torch.cuda.synchronize(self.tensor.device)
+        self.addr = self.tensor.data_ptr()
 
     @classmethod
     def for_shapes(cls, shapes, device="cuda"):
@@ -524,7 +523,8 @@ class PagedKVCache:
         self._struct = _KVCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                 k.stride(0), k.stride(1), k_scale.stride(0), k_scale.stride(1),
                                 pages, heads, page, dim, self.block)
-        self._ref = ctypes.byref(self._struct)
+        # what a call passes of it: its description's address, its device, heads and dims
+        self._args = (ctypes.addressof(self._struct), self.device.index, heads, dim)
 
     @classmethod
     def empty(cls, num_pages, kv_heads, head_dim, *, page_size=64, block=16, device="cuda"):
@@ -536,60 +536,44 @@ class PagedKVCache:
         return cls(k, v, ks, vs)
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _enqueue(fn, device, stream, *args):
-    """fn(*args, stream) with `device` current (entered only where it is not)."""
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(device.index)
-    elif isinstance(stream, torch.cuda.Stream):
-        stream = stream.cuda_stream
-    if torch.cuda.current_device() == device.index:
-        status = fn(*args, stream)
-    else:
+def _call(name, device, *args):
+    """A call of _binding: True once it is enqueued, False if an argument is not in order (nothing was
+    called then); raises for a call that the library refuses."""
+    if not _native:
+        load()
+    fn = _native[name]
+    status = fn(*args)
+    if status == -2:                # another device is current
         with torch.cuda.device(device):
-            status = fn(*args, stream)
-    if status:
+            status = fn(*args)
+    if status > 0:
         _check(status)
+    return status == 0
 
 
 def _need_sequences(cache, block_table, seq_lens, q_start):
-    """(batch, columns of the table)."""
-    dev, i32 = cache.device, torch.int32
-    if not (type(block_table) is type(seq_lens) is type(q_start) is torch.Tensor and
-            block_table.dtype is seq_lens.dtype is q_start.dtype is i32 and
-            block_table.device == seq_lens.device == q_start.device == dev and
-            block_table.is_contiguous() and seq_lens.is_contiguous() and q_start.is_contiguous()):
-        _need(block_table, "block_table", i32, dev)
-        _need(seq_lens, "seq_lens", i32, dev)
-        _need(q_start, "q_start", i32, dev)
-    B, shape = seq_lens.numel(), block_table.shape
-    if len(shape) != 2 or shape[0] != B or q_start.numel() != B + 1:
+    dev = cache.device
+    _need(block_table, "block_table", torch.int32, dev)
+    _need(seq_lens, "seq_lens", torch.int32, dev)
+    _need(q_start, "q_start", torch.int32, dev)
+    B = seq_lens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != B or q_start.numel() != B + 1:
         raise ValueError("block_table must be [batch, pages], seq_lens [batch], q_start [batch + 1]")
-    return B, shape[1]
 
 
 def _need_rows(t, name, heads, dim, device):
-    """bf16 [tokens, heads, dim], a token's heads dense, any stride between tokens: (tokens, heads,
-    elements from one token to the next)."""
+    """bf16 [tokens, heads, dim], a token's heads dense, any stride between tokens; returns tokens."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not torch.bfloat16:
+    if t.dtype != torch.bfloat16:
         raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be a CUDA tensor on {device} (there is no CPU path)")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, {dim}]")
-    T, H, d = t.shape
-    st, sh, sd = t.stride()
-    if d != dim or (heads is not None and H != heads):
+    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
         raise ValueError(f"{name} must be [tokens, {'heads' if heads is None else heads}, {dim}]")
-    if (sd != 1 or (sh != dim and H > 1)) and T and H:
+    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != dim)):
         raise ValueError(f"{name} must be dense in a token's heads and dims")
-    # one token has no next one: any stride will do
-    return T, H, st if T > 1 else H * dim
+    return t.shape[0]
 
 
 def kv_append(q, k, v, cache: PagedKVCache, block_table, seq_lens, q_start, *, max_q: int, cos=None,
@@ -603,39 +587,37 @@ def kv_append(q, k, v, cache: PagedKVCache, block_table, seq_lens, q_start, *, m
     [tokens] (None: the place in the cache).  Returns the rotated queries (`out_q`, which may
     be q; None without q).  See dl_kv_append for the scales and the rounding.
     """
+    if q is not None and out_q is None and isinstance(q, torch.Tensor):
+        out_q = torch.empty_like(q, memory_format=torch.contiguous_format)
+    if not _call("append", cache.device, *cache._args, q, k, v, block_table, seq_lens, q_start, max_q, cos, sin,
+                 positions, out_q, stream):
+        _explain_append(q, k, v, cache, block_table, seq_lens, q_start, cos, sin, positions, out_q)
+    return out_q
+
+
+def _explain_append(q, k, v, cache, block_table, seq_lens, q_start, cos, sin, positions, out_q):
+    """Raise for the first argument of a kv_append call that is not in order."""
     dev, D = cache.device, cache.head_dim
-    T, _, ks = _need_rows(k, "k", cache.kv_heads, D, dev)
-    Tv, _, vs = _need_rows(v, "v", cache.kv_heads, D, dev)
-    B, cols = _need_sequences(cache, block_table, seq_lens, q_start)
-    Tq, Hq, qs = T, 0, 0
+    T = _need_rows(k, "k", cache.kv_heads, D, dev)
+    Tq = Tv = _need_rows(v, "v", cache.kv_heads, D, dev)
+    _need_sequences(cache, block_table, seq_lens, q_start)
     if q is not None:
-        Tq, Hq, qs = _need_rows(q, "q", None, D, dev)
-        if out_q is None:
-            out_q = torch.empty_like(q, memory_format=torch.contiguous_format)
-        else:
-            _need(out_q, "out_q", torch.bfloat16, dev)
-            if out_q.shape != q.shape:
-                raise ValueError("q, k, v and out_q must have the same tokens")
+        Tq = _need_rows(q, "q", None, D, dev)
+        _need(out_q, "out_q", torch.bfloat16, dev)
     elif out_q is not None:
         raise ValueError("out_q needs q")
-    if Tv != T or Tq != T:
+    if Tv != T or Tq != T or (q is not None and out_q.shape != q.shape):
         raise ValueError("q, k, v and out_q must have the same tokens")
-    rd = P = 0
     if cos is not None or sin is not None:
         _need(cos, "cos", torch.float32, dev)
         _need(sin, "sin", torch.float32, dev)
-        shape = cos.shape
-        if len(shape) != 2 or shape != sin.shape:
+        if cos.dim() != 2 or cos.shape != sin.shape:
             raise ValueError("cos and sin must be [positions, rotary_dim / 2]")
-        P, rd = shape[0], 2 * shape[1]
     if positions is not None:
         _need(positions, "positions", torch.int32, dev)
         if positions.numel() != T:
             raise ValueError("positions must be [tokens]")
-    _enqueue(load().dl_kv_append, dev, stream, cache._ref, _addr(q), k.data_ptr(), v.data_ptr(), qs, ks,
-             vs, _addr(out_q), _addr(cos), _addr(sin), rd, P, _addr(positions), block_table.data_ptr(),
-             cols, seq_lens.data_ptr(), q_start.data_ptr(), B, T, Hq, max_q)
-    return out_q
+    raise ValueError("max_q and stream must be integers, sizes below 2^31")
 
 
 def attention_workspace_bytes(batch: int, tokens: int, q_heads: int, kv_heads: int, head_dim: int,
@@ -651,26 +633,35 @@ def attention_paged(q, cache: PagedKVCache, block_table, seq_lens, q_start, *, m
     [tokens, q_heads]) gets the log-sum-exp of the scaled scores.  scale: head_dim ** -0.5 if
     None.  The sequences are described as for kv_append; see dl_attention_paged.
     """
-    dev, D = cache.device, cache.head_dim
-    T, Hq, qs = _need_rows(q, "q", None, D, dev)
-    B, cols = _need_sequences(cache, block_table, seq_lens, q_start)
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    else:
-        _need(out, "out", torch.bfloat16, dev)
-        if out.numel() != T * Hq * D:
-            raise ValueError("out must hold tokens * q_heads * head_dim elements")
+    if workspace is None:
+        _explain_attention(q, cache, block_table, seq_lens, q_start, out, out_lse)
+        with torch.cuda.device(cache.device):
+            workspace = _workspace(None, attention_workspace_bytes(
+                seq_lens.numel(), q.shape[0], q.shape[1], cache.kv_heads, cache.head_dim, max_q=max_q), cache.device)
+    if not _call("attention", cache.device, *cache._args, q, block_table, seq_lens, q_start, max_q,
+                 cache.head_dim ** -0.5 if scale is None else scale, out, out_lse, workspace.addr,
+                 workspace.nbytes, stream):
+        _explain_attention(q, cache, block_table, seq_lens, q_start, out, out_lse)
+        raise ValueError("max_q and stream must be integers, scale a number, sizes below 2^31")
+    return out
+
+
+def _explain_attention(q, cache, block_table, seq_lens, q_start, out, out_lse):
+    """Raise for the first argument of an attention_paged call that is not in order."""
+    dev, D = cache.device, cache.head_dim
+    T = _need_rows(q, "q", None, D, dev)
+    _need_sequences(cache, block_table, seq_lens, q_start)
+    _need(out, "out", torch.bfloat16, dev)
+    if out.numel() != q.numel():
+        raise ValueError("out must hold tokens * q_heads * head_dim elements")
     if out_lse is not None:
         _need(out_lse, "out_lse", torch.float32, dev)
-        if out_lse.numel() != T * Hq:
+        if out_lse.numel() != T * q.shape[1]:
             raise ValueError("out_lse must hold tokens * q_heads elements")
-    if workspace is None:
-        with torch.cuda.device(dev):
-            workspace = _workspace(None, attention_workspace_bytes(B, T, Hq, cache.kv_heads, D, max_q=max_q), dev)
-    _enqueue(load().dl_attention_paged, dev, stream, cache._ref, q.data_ptr(), qs, out.data_ptr(),
-             _addr(out_lse), block_table.data_ptr(), cols, seq_lens.data_ptr(), q_start.data_ptr(), B, T,
-             Hq, max_q, D ** -0.5 if scale is None else scale, workspace.tensor.data_ptr(), workspace.nbytes)
-    return out
 
 
 def verify_draft(draft_tokens, target_probs, u_accept, u_next, *, draft_probs=None, draft_lens=None,
@@ -683,45 +674,49 @@ def verify_draft(draft_tokens, target_probs, u_accept, u_next, *, draft_probs=No
     draft_lens int32 [batch] or None.  Returns (tokens int32 [batch, drafts + 1]: accepted
     tokens, the next one, then -1; count int32 [batch]: how many were accepted).
     """
-    if not isinstance(target_probs, torch.Tensor):
-        raise TypeError("target_probs must be a torch.Tensor")
-    kind, dev = target_probs.dtype, target_probs.device
+    if not isinstance(target_probs, torch.Tensor) or not isinstance(draft_tokens, torch.Tensor):
+        raise TypeError("target_probs and draft_tokens must be torch.Tensors")
+    if not target_probs.is_cuda:
+        raise ValueError("target_probs must be a CUDA tensor (there is no CPU path)")
+    if draft_tokens.dim() != 2:
+        raise ValueError("draft_tokens must be [batch, drafts]")
+    dev, (B, S) = target_probs.device, draft_tokens.shape
+    if out_tokens is None:
+        out_tokens = torch.empty((B, S + 1), dtype=torch.int32, device=dev)
+    if out_count is None:
+        out_count = torch.empty((B,), dtype=torch.int32, device=dev)
+    if not _call("verify", dev, dev.index, draft_tokens, target_probs, u_accept, u_next, draft_probs, draft_lens,
+                 out_tokens, out_count, stream):
+        _explain_verify(draft_tokens, target_probs, u_accept, u_next, draft_probs, draft_lens, out_tokens, out_count)
+    return out_tokens, out_count
+
+
+def _explain_verify(draft_tokens, target_probs, u_accept, u_next, draft_probs, draft_lens, out_tokens, out_count):
+    """Raise for the first argument of a verify_draft call that is not in order."""
+    kind, dev, (B, S) = target_probs.dtype, target_probs.device, draft_tokens.shape
     if kind not in (torch.float32, torch.bfloat16):
         raise ValueError(f"target_probs must be torch.float32 or torch.bfloat16, got {kind}")
     _need(target_probs, "target_probs", kind)
     _need(draft_tokens, "draft_tokens", torch.int32, dev)
     _need(u_accept, "u_accept", torch.float32, dev)
     _need(u_next, "u_next", torch.float32, dev)
-    if draft_tokens.dim() != 2:
-        raise ValueError("draft_tokens must be [batch, drafts]")
-    B, S = draft_tokens.shape
     if target_probs.dim() != 3 or target_probs.shape[:2] != (B, S + 1):
         raise ValueError("target_probs must be [batch, drafts + 1, vocab]")
-    V = target_probs.shape[2]
     if u_accept.numel() != B * S or u_next.numel() != B:
         raise ValueError("u_accept must be [batch, drafts] and u_next [batch]")
     if draft_probs is not None:
         _need(draft_probs, "draft_probs", kind, dev)
-        if draft_probs.shape != (B, S, V):
+        if draft_probs.shape != (B, S, target_probs.shape[2]):
             raise ValueError("draft_probs must be [batch, drafts, vocab]")
     if draft_lens is not None:
         _need(draft_lens, "draft_lens", torch.int32, dev)
         if draft_lens.numel() != B:
             raise ValueError("draft_lens must be [batch]")
-    if out_tokens is None:
-        out_tokens = torch.empty((B, S + 1), dtype=torch.int32, device=dev)
-    else:
-        _need(out_tokens, "out_tokens", torch.int32, dev)
-    if out_count is None:
-        out_count = torch.empty((B,), dtype=torch.int32, device=dev)
-    else:
-        _need(out_count, "out_count", torch.int32, dev)
+    _need(out_tokens, "out_tokens", torch.int32, dev)
+    _need(out_count, "out_count", torch.int32, dev)
     if out_tokens.numel() != B * (S + 1) or out_count.numel() != B:
         raise ValueError("out_tokens must be [batch, drafts + 1] and out_count [batch]")
-    _enqueue(load().dl_verify_draft, dev, stream, draft_tokens.data_ptr(), _addr(draft_probs),
-             target_probs.data_ptr(), 0 if kind is torch.float32 else 1, u_accept.data_ptr(),
-             u_next.data_ptr(), _addr(draft_lens), out_tokens.data_ptr(), out_count.data_ptr(), B, S, V)
-    return out_tokens, out_count
+    raise ValueError("stream must be an integer or a stream, sizes below 2^31")
 
 
 def graph_cache_clear():
