@@ -25,7 +25,9 @@ struct AppendParams {
 // values read once and written as codes.  A thread takes 16 dims at a time, the
 // two groups of 8 that rotate into one another (or 16 dims that pass through):
 // 16-byte loads and stores, and cos and sin stay in its registers while it goes
-// through a token's heads.
+// through a token's heads.  4 prompts of 4096 tokens (64 query and 8 key/value heads of
+// 128, 487 MB): 78 us, 6.2 TB/s; 48 x 6 tokens: 4.9 us, one token: 3.4 us, both the chain
+// launch, sequence, page, scale, codes.
 constexpr int kAppendThreads = 256;
 
 __device__ __forceinline__ int position_of(const AppendParams& p, int t, int index) {
@@ -412,7 +414,8 @@ extern "C" dl_status dl_kv_append(const dl_kv_cache* cache, const void* q, const
     const int blocks = kAppendThreads / p.team;
     HostDevice dev;
     if ((s = host_device(dev)) != DL_OK) return s;
-    // a CTA's search and position are shared by four tokens once that leaves several CTAs to each SM
+    // a CTA's search and position are shared by four tokens once that leaves several CTAs to each
+    // SM (4 x 4096 tokens: 85 -> 78 us; at 48 x 6 tokens one is better: 6.1 -> 4.9 us)
     p.per = tokens >= 16 * dev.sm_count ? 4 : 1;
     const long long kv_ctas = (p.kv_units + blocks - 1) / blocks, q_ctas = q ? (tokens + p.per - 1) / p.per : 0;
     const long long grid = kv_ctas + q_ctas, fewer = kv_ctas < q_ctas ? kv_ctas : q_ctas;

@@ -20,7 +20,8 @@ struct VerifyParams {
 // A cluster of CTAs takes one sequence, each warp a contiguous run of its vocabulary.
 // What bounds it: for many sequences the one read of p (and g) and the arithmetic on
 // it, for few the chain of dependent loads (draft token, its probabilities, the
-// row).  The first pass keeps the sums by CTA and warp, so that the drawn token is
+// row) and the cluster's two barriers: 7.1 us for one sequence of 152064 entries, 17 us
+// for 48 (45 MB: 2.6 TB/s).  The first pass keeps the sums by CTA and warp, so that the drawn token is
 // found by reading one warp's run again, not the row.
 constexpr int kVerifyThreads = 512;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
@@ -98,9 +99,13 @@ __device__ __forceinline__ long long warp_scan(long long w, int lane) {
     return w;
 }
 
-// BATCH: groups of 128 entries that a warp has in flight.
-template <class T, int BATCH>
-__global__ void __launch_bounds__(kVerifyThreads, BATCH > 2 ? 1 : 3) verify_draft_kernel(const __grid_constant__ VerifyParams p) {
+// Groups of 128 entries that a warp has in flight, with registers for three CTAs on an
+// SM: the other warps hide the rest (with five groups and one CTA, 48 sequences of 152064
+// entries take 44 us instead of 17, one sequence the same 7.1).
+constexpr int kGroups = 2;
+
+template <class T>
+__global__ void __launch_bounds__(kVerifyThreads, 3) verify_draft_kernel(const __grid_constant__ VerifyParams p) {
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
     const int size = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -161,16 +166,16 @@ __global__ void __launch_bounds__(kVerifyThreads, BATCH > 2 ? 1 : 3) verify_draf
         plain = pass == 1;              // nothing left of p - g: draw from p
         long long sum = 0;
         const int end = run_begin(warp + 1);
-        for (int i0 = run_begin(warp); i0 < end; i0 += 128 * BATCH) {
-            float f[BATCH][4] = {}, g[BATCH][4] = {};
+        for (int i0 = run_begin(warp); i0 < end; i0 += 128 * kGroups) {
+            float f[kGroups][4] = {}, g[kGroups][4] = {};
 #pragma unroll
-            for (int t = 0; t < BATCH; ++t) {
+            for (int t = 0; t < kGroups; ++t) {
                 const int i = i0 + 128 * t + lane * 4;
                 if (i < end) load(i, end, plain, f[t], g[t]);
             }
-            int hi_sum = 0, lo_sum = 0;     // of at most 20 entries
+            int hi_sum = 0, lo_sum = 0;     // of 4 kGroups entries
 #pragma unroll
-            for (int t = 0; t < BATCH; ++t) {
+            for (int t = 0; t < kGroups; ++t) {
                 int hi[4], lo[4];
                 weigh(plain, f[t], g[t], hi, lo);
                 hi_sum += (hi[0] + hi[1]) + (hi[2] + hi[3]);
@@ -249,15 +254,22 @@ __global__ void __launch_bounds__(kVerifyThreads, BATCH > 2 ? 1 : 3) verify_draf
     cluster.barrier_wait();
 }
 
-template <class T, int BATCH>
-cudaError_t launch_verify_batch(const VerifyParams& p, int batch, int size, cudaStream_t stream) {
+template <class T>
+cudaError_t launch_verify(const VerifyParams& p, int batch, int sm_count, cudaStream_t stream) {
+    // CTAs of a sequence: a power of two, as many as leave three to each SM (48 sequences of
+    // 152064 entries: 17 us; one to each SM 33 us), at most 16, a cluster (one sequence:
+    // 7.1 us; 8 take 8.4), each warp with 128 entries at least
+    int size = 1;
+    while (size < kMaxCluster && (long long)batch * size * 2 <= 3LL * sm_count &&
+           size * kVerifyWarps * 128 < p.vocab)
+        size *= 2;
     static std::atomic<bool> ready[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!ready[dev].load()) {
-        e = cudaFuncSetAttribute(verify_draft_kernel<T, BATCH>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        e = cudaFuncSetAttribute(verify_draft_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
         ready[dev].store(true);
     }
@@ -274,20 +286,7 @@ cudaError_t launch_verify_batch(const VerifyParams& p, int batch, int size, cuda
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, verify_draft_kernel<T, BATCH>, p);
-}
-
-template <class T>
-cudaError_t launch_verify(const VerifyParams& p, int batch, int sm_count, cudaStream_t stream) {
-    // CTAs of a sequence: a power of two, as many as leave three to each SM, at most 16 (a cluster), each warp with
-    // 128 entries at least.  Where an SM has one CTA, its warps have five groups of entries in
-    // flight, else two, and registers for three CTAs.
-    int size = 1;
-    while (size < kMaxCluster && (long long)batch * size * 2 <= 3LL * sm_count &&
-           size * kVerifyWarps * 128 < p.vocab)
-        size *= 2;
-    return (long long)batch * size <= sm_count ? launch_verify_batch<T, 5>(p, batch, size, stream)
-                                               : launch_verify_batch<T, 2>(p, batch, size, stream);
+    return cudaLaunchKernelEx(&cfg, verify_draft_kernel<T>, p);
 }
 
 }  // namespace dl
