@@ -34,11 +34,11 @@ cudaError_t launch_attention_instance(const AttnLaunch& a) {
     if ((e = cudaLaunchKernelEx(&cfg, attention_kernel<C>, a.tk, a.tv, a.p)) != cudaSuccess) return e;
     const int rows = a.p.tile_tokens * a.p.group;
     const bool wide = (long long)a.p.s.batch * a.p.row_tiles * a.p.kv_heads * 8 <= a.grid;
-    cfg.gridDim = dim3(a.grid, wide ? rows : (rows + 3) / 4);
+    cfg.gridDim = wide ? dim3((a.grid + 3) / 4, rows) : dim3(a.grid, (rows + 3) / 4);
     cfg.blockDim = dim3(128);
     cfg.dynamicSmemBytes = 0;
-    return wide ? cudaLaunchKernelEx(&cfg, attention_combine_kernel<C::D, 4>, a.p, C::RP, a.grid)
-                : cudaLaunchKernelEx(&cfg, attention_combine_kernel<C::D, 1>, a.p, C::RP, a.grid);
+    return wide ? cudaLaunchKernelEx(&cfg, attention_combine_kernel<C::D, 4, 4>, a.p, C::RP, a.grid)
+                : cudaLaunchKernelEx(&cfg, attention_combine_kernel<C::D, 1, 1>, a.p, C::RP, a.grid);
 }
 
 template <int D>
