@@ -52,35 +52,40 @@ __device__ __forceinline__ void four(const uint16_t* row, int i, int end, bool w
 __device__ __forceinline__ float prob(const float* p, size_t i) { return p[i]; }
 __device__ __forceinline__ float prob(const uint16_t* p, size_t i) { return bf16_bits_to_f32(p[i]); }
 
-// A probability, taken inside [0, 1] (NaN: 0), as the whole number nearest to x 2^44: hi 2^22 + lo,
-// both offset by kOffset.  Adding 1.5 * 2^23 leaves a rounded integer in an fp32's
-// low bits; hi's rounding error is exact in fp32, so lo rounds the whole value
-// once, to even at ties (hi 2^22 is even).
+// Two probabilities x of [0, 1], as the whole numbers nearest to x 2^44: hi 2^22 + lo each, both
+// offset by kOffset.  Adding 1.5 * 2^23 leaves a rounded integer in an fp32's low
+// bits; hi's rounding error is exact in fp32, so lo rounds the whole value once, to
+// even at ties (hi 2^22 is even).
 constexpr float kMagic = 12582912.f, kStep = 4194304.f;       // 1.5 * 2^23, 2^22
 constexpr int kOffset = 0x4B400000;                           // the bits of kMagic
-__device__ __forceinline__ void whole(float x, int& hi, int& lo) {
-    const float y = __fmul_rn(x, kStep), a = __fadd_rn(y, kMagic);
-    const float rest = __fsub_rn(y, __fsub_rn(a, kMagic));
-    hi = __float_as_int(a);
-    lo = __float_as_int(__fmaf_rn(rest, kStep, kMagic));
+__device__ __forceinline__ void whole2(float x0, float x1, int& hi0, int& hi1, int& lo0, int& lo1) {
+    const F2 x = f2(x0, x1), step = f2(kStep, kStep), magic = f2(kMagic, kMagic);
+    const F2 a = fma2(x, step, magic);
+    const F2 rest = fma2(x, step, fma2(a, f2(-1.f, -1.f), magic));
+    float h0, h1, l0, l1;
+    unpack(a, h0, h1);
+    unpack(fma2(rest, step, magic), l0, l1);
+    hi0 = __float_as_int(h0); hi1 = __float_as_int(h1);
+    lo0 = __float_as_int(l0); lo1 = __float_as_int(l1);
 }
 
-// The weights max(P - G, 0) of four entries, as hi 2^22 + lo each (P >= G exactly where p >= g).
+// The weights max(P - G, 0) of four entries, as hi 2^22 + lo each: P is never below G where
+// p is not, so max(p, g) in p's place leaves 0.  Probabilities are taken inside [0, 1] (NaN: 0).
 template <bool G>
 __device__ __forceinline__ void weights(const float (&f)[4], const float (&g)[4], int (&hi)[4], int (&lo)[4]) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float x = __saturatef(f[k]);
-        int gh = kOffset, gl = kOffset, ph, pl;
-        whole(x, ph, pl);
-        bool more = true;
+    for (int k = 0; k < 4; k += 2) {
+        float x[2] = {__saturatef(f[k]), __saturatef(f[k + 1])};
+        int gh[2] = {kOffset, kOffset}, gl[2] = {kOffset, kOffset};
         if (G) {
-            const float z = __saturatef(g[k]);
-            whole(z, gh, gl);
-            more = x > z;
+            const float z[2] = {__saturatef(g[k]), __saturatef(g[k + 1])};
+            whole2(z[0], z[1], gh[0], gh[1], gl[0], gl[1]);
+            x[0] = fmaxf(x[0], z[0]);
+            x[1] = fmaxf(x[1], z[1]);
         }
-        hi[k] = more ? ph - gh : 0;
-        lo[k] = more ? pl - gl : 0;
+        whole2(x[0], x[1], hi[k], hi[k + 1], lo[k], lo[k + 1]);
+        hi[k] -= gh[0]; hi[k + 1] -= gh[1];
+        lo[k] -= gl[0]; lo[k + 1] -= gl[1];
     }
 }
 __device__ __forceinline__ long long joined(int hi, int lo) { return (long long)hi * (1 << 22) + lo; }
