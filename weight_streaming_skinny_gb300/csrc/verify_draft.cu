@@ -2,6 +2,7 @@
 #include <cooperative_groups.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "dl_host.h"
 #include "dl_device.cuh"
@@ -28,9 +29,11 @@ constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kMaxCluster = 16;
 
 // Four consecutive probabilities from entry i on, entries at or past `end` as
-// zeros; `wide`: the row's groups of four are aligned to their size.
+// zeros; `wide`: the row's groups of four are aligned to their size; ALL: they are, and
+// end at or before `end`.
+template <bool ALL>
 __device__ __forceinline__ void four(const float* row, int i, int end, bool wide, float (&f)[4]) {
-    if (wide && i + 4 <= end) {
+    if (ALL || (wide && i + 4 <= end)) {
         const uint4 v = ldg128(row + i);
         f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y);
         f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
@@ -39,8 +42,9 @@ __device__ __forceinline__ void four(const float* row, int i, int end, bool wide
         for (int k = 0; k < 4; ++k) f[k] = i + k < end ? row[i + k] : 0.f;
     }
 }
+template <bool ALL>
 __device__ __forceinline__ void four(const uint16_t* row, int i, int end, bool wide, float (&f)[4]) {
-    if (wide && i + 4 <= end) {
+    if (ALL || (wide && i + 4 <= end)) {
         const uint2 v = ldg64(row + i);
         f[0] = __uint_as_float(v.x << 16); f[1] = __uint_as_float(v.x & 0xffff0000u);
         f[2] = __uint_as_float(v.y << 16); f[3] = __uint_as_float(v.y & 0xffff0000u);
@@ -150,9 +154,10 @@ __global__ void __launch_bounds__(kVerifyThreads, 3) verify_draft_kernel(const _
     const int run = ((V + size * kVerifyWarps - 1) / (size * kVerifyWarps) + 127) / 128 * 128;
     const int cta_begin = min(rank * kVerifyWarps * run, V);
     auto run_begin = [&](int w) { return min(cta_begin + w * run, V); };
-    auto load = [&](int i, int end, bool plain, float (&f)[4], float (&g)[4]) {
-        four(pr, i, end, wide, f);
-        if (gr && !plain) four(gr, i, end, wide, g);
+    auto load = [&](auto whole, int i, int end, bool plain, float (&f)[4], float (&g)[4]) {
+        constexpr bool all = decltype(whole)::value;
+        four<all>(pr, i, end, wide, f);
+        if (gr && !plain) four<all>(gr, i, end, wide, g);
         if (!plain && (unsigned)(skip - i) < 4u) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -173,10 +178,15 @@ __global__ void __launch_bounds__(kVerifyThreads, 3) verify_draft_kernel(const _
         const int end = run_begin(warp + 1);
         for (int i0 = run_begin(warp); i0 < end; i0 += 128 * kGroups) {
             float f[kGroups][4] = {}, g[kGroups][4] = {};
+            if (wide && i0 + 128 * kGroups <= end) {
 #pragma unroll
-            for (int t = 0; t < kGroups; ++t) {
-                const int i = i0 + 128 * t + lane * 4;
-                if (i < end) load(i, end, plain, f[t], g[t]);
+                for (int t = 0; t < kGroups; ++t) load(std::true_type(), i0 + 128 * t + lane * 4, end, plain, f[t], g[t]);
+            } else {
+#pragma unroll
+                for (int t = 0; t < kGroups; ++t) {
+                    const int i = i0 + 128 * t + lane * 4;
+                    if (i < end) load(std::false_type(), i, end, plain, f[t], g[t]);
+                }
             }
             int hi_sum = 0, lo_sum = 0;     // of 4 kGroups entries
 #pragma unroll
@@ -225,7 +235,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 3) verify_draft_kernel(const _
                 const int i = i0 + tid * 4;
                 float f[4] = {}, g[4] = {};
                 int hi[4], lo[4];
-                if (i < end) load(i, end, plain, f, g);
+                if (i < end) load(std::false_type(), i, end, plain, f, g);
                 weigh(plain, f, g, hi, lo);
                 const long long own = joined((hi[0] + hi[1]) + (hi[2] + hi[3]), (lo[0] + lo[1]) + (lo[2] + lo[3]));
                 const long long inc = warp_scan(own, lane);
