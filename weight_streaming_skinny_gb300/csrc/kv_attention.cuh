@@ -139,7 +139,7 @@ struct AttnShape {
     static constexpr int kPBytes = kOutCols * kTile;    // one of two buffers
     // segment descriptors: one more than tiles can be in flight, and the one in work
     static constexpr int kSegments = 10;
-    static constexpr int kMisc = 1024 + kSegments * 36 + 8 + RP * (16 + 16 * TG) + TG * 4 * RP * 4 + D * 4 + 256;
+    static constexpr int kMisc = 1024 + kSegments * 36 + 8 + RP * 32 * TG + TG * 4 * RP * 4 + TG * D * 4 + 256;
     static constexpr int kBudget = (kCtas == 1 ? 227 : kCtas == 2 ? 113 : 75) * 1024;
     // a tile's slots: its codes, and 8 bytes of scales for each token
     static constexpr int kScaleBytes = kTile * 8;
@@ -474,14 +474,15 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     int* s_flags = reinterpret_cast<int*>(misc + 640);                // [NV] some token is absent, or its scale tiny
     AttnSegment* s_seg = reinterpret_cast<AttnSegment*>(misc + 1024); // [NS]
     int* s_share = reinterpret_cast<int*>(s_seg + NS);                // [NS] CTAs that share an item begun here, or 0
-    float* s_qs = reinterpret_cast<float*>(s_share + (NS + 3) / 4 * 4);   // [RP] a row's query scale
-    int* s_lim = reinterpret_cast<int*>(s_qs + RP);                   // [RP] cached tokens a row sees
-    long long* s_out = reinterpret_cast<long long*>(s_lim + RP);      // [RP] a row's place among tokens x heads
-    float* s_n = reinterpret_cast<float*>(s_out + RP);                // [TG][RP] n_r
+    // [TG] of what belongs to a segment's rows: with two tile groups the next one's is made early
+    float* s_qs = reinterpret_cast<float*>(s_share + (NS + 3) / 4 * 4);   // [TG][RP] a row's query scale
+    int* s_lim = reinterpret_cast<int*>(s_qs + TG * RP);              // [TG][RP] cached tokens a row sees
+    long long* s_out = reinterpret_cast<long long*>(s_lim + TG * RP); // [TG][RP] where a row's output begins
+    float* s_n = reinterpret_cast<float*>(s_out + TG * RP);           // [TG][RP] n_r
     float* s_l = s_n + TG * RP;                                       // [TG][RP] sums of P / vs
     float* s_f = s_l + TG * RP;                                       // [TG][RP] factors of the accumulators
     float* s_red = s_f + TG * RP;                                     // [NWG][4][RW]
-    int* s_nan = reinterpret_cast<int*>(s_red + TG * 4 * RP);         // [D] first NaN among the new tokens' values
+    int* s_nan = reinterpret_cast<int*>(s_red + TG * 4 * RP);         // [TG][D] first NaN among the new tokens' values
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const CtaWait wait{{p.err_word, p.wait_limit_ns}, s_stop};
@@ -502,7 +503,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                 mbar_init(smem_u32(p_full + i), CG * 4);
                 mbar_init(smem_u32(pv_done + i), 1);
             }
-            mbar_init(smem_u32(q_full), NWG * 4);
+            mbar_init(smem_u32(q_full), CG * 4);
             for (int i = 0; i < NS; ++i) mbar_init(smem_u32(seg_full + i), 1);
             *s_stop = 0;
             // read only after a wait that gave up: nothing to do, and nothing after it
@@ -761,14 +762,16 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
             kr.step();
             return true;
         };
+        // the scores of tile i are read: their buffer is free
+        auto read = [&](int i) {
+            return i < 0 || __all_sync(~0u, wait(smem_u32(s_read + (i & 1)), (i >> 1) & 1, kErrConsumerWait));
+        };
         do {
             // scores run two tiles ahead: as soon as those of the tile before in their buffer are read
-            ok = __all_sync(~0u, wait(smem_u32(q_full), seg & 1, kErrConsumerWait)) && scores(it) &&
-                 (w.tile0 + 1 >= w.tile1 || scores(it + 1));
+            ok = __all_sync(~0u, wait(smem_u32(q_full), seg & 1, kErrConsumerWait)) && read(it - 2) && scores(it) &&
+                 (w.tile0 + 1 >= w.tile1 || (read(it - 1) && scores(it + 1)));
             for (int tile = w.tile0; tile < w.tile1 && ok; ++tile, ++it) {
-                if (tile + 2 < w.tile1 &&
-                    !(ok = __all_sync(~0u, wait(smem_u32(s_read + (it & 1)), (it >> 1) & 1, kErrConsumerWait)) && scores(it + 2)))
-                    break;
+                if (tile + 2 < w.tile1 && !(ok = read(it) && scores(it + 2))) break;
                 if (!(ok = __all_sync(~0u, wait(smem_u32(p_full + (it & 1)), (it >> 1) & 1, kErrConsumerWait)))) break;
                 tc_fence_after_sync();
                 const uint64_t a = v_desc + (uint32_t)(vr.slot * C::kTileBytes >> 4);
@@ -804,86 +807,89 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
         };
         // a segment's queries: 16 elements each thread (and pass), read before the segment before it is finished
         constexpr int TPR = D / 16;                         // threads of a row
-        constexpr int kPasses = (RP * TPR + kSoftmax - 1) / kSoftmax;
-        uint4 queries[kPasses][2];
-        auto load_queries = [&](const AttnSegment& v) {
-#pragma unroll
-            for (int i = 0; i < kPasses; ++i) {
-                const int row = tid / TPR + i * (kSoftmax / TPR), token = row / p.group;
-                queries[i][0] = queries[i][1] = make_uint4(0, 0, 0, 0);
-                if (row < v.rows) {
-                    const uint16_t* src = p.q + (size_t)(v.row0 + token) * p.q_stride +
-                                          (size_t)(v.head * p.group + row - token * p.group) * D + tid % TPR * 16;
-                    queries[i][0] = ldg128(src);
-                    queries[i][1] = ldg128(src + 8);
-                }
+        static_assert(RP * TPR <= kSoftmax, "16 dims each thread");
+        // a thread's 16 dims of a row of a segment's queries
+        auto load_query = [&](const AttnSegment& sg, int t, uint4 (&v)[2]) {
+            const int row = t / TPR, token = row / p.group;
+            v[0] = v[1] = make_uint4(0, 0, 0, 0);
+            if (row < sg.rows) {
+                const uint16_t* src = p.q + (size_t)(sg.row0 + token) * p.q_stride +
+                                      (size_t)(sg.head * p.group + row - token * p.group) * D + t % TPR * 16;
+                v[0] = ldg128(src);
+                v[1] = ldg128(src + 8);
             }
         };
+        // ... as two e4m3 parts, each row scaled to the top of the range; `buf`: where the segment's rows are noted
+        auto store_query = [&](const AttnSegment& sg, int buf, int t, const uint4 (&v)[2]) {
+            const int c = t % TPR, row = t / TPR;
+            const uint32_t x[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+            uint32_t top = 0;                   // largest magnitude: bf16 bits order as integers
+#pragma unroll
+            for (int k = 0; k < 8; ++k) top = max(top, max(x[k] & 0x7fffu, (x[k] >> 16) & 0x7fffu));
+            const unsigned mates = TPR == 8 ? 0xffu << (lane & 24) : 0xfu << (lane & 28);
+#pragma unroll
+            for (int o = TPR / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(mates, top, o));
+            // 2^e <= largest < 2^(e+1) becomes [128, 256); a row with an infinity or a NaN answers NaN
+            const int e = max((int)(top >> 7), 1) - 127;
+            const bool odd = (top >> 7) == 255;
+            // 2^(7-e) in two steps: each one fits fp32
+            const float up1 = __uint_as_float((uint32_t)(127 + (7 - e) / 2) << 23);
+            const float up2 = __uint_as_float((uint32_t)(127 + (7 - e) - (7 - e) / 2) << 23);
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float f[4], s[4];
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const uint32_t two = x[2 * k + m / 2];
+                    f[m] = __uint_as_float(m & 1 ? two & 0xffff0000u : two << 16) * up1 * up2;
+                }
+                hi[k] = f32x2_to_e4m3x2(f[0], f[1]) | f32x2_to_e4m3x2(f[2], f[3]) << 16;
+                uint32_t h01, h23;
+                e4m3x4_to_f16x2x2(hi[k], h01, h23);
+                asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+                    : "=f"(s[0]), "=f"(s[1]) : "r"(h01));
+                asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+                    : "=f"(s[2]), "=f"(s[3]) : "r"(h23));
+                lo[k] = f32x2_to_e4m3x2(f[0] - s[0], f[1] - s[1]) | f32x2_to_e4m3x2(f[2] - s[2], f[3] - s[3]) << 16;
+            }
+            const int sw = D == 128 ? (c ^ (row & 7)) : (c ^ ((row >> 1) & 3));
+            const int at = row * D + sw * 16;
+            // the parts' rows follow one another: RP is a multiple of 8, so both swizzle alike
+            sts128(smem_u32(sq + at), hi[0], hi[1], hi[2], hi[3]);
+            sts128(smem_u32(sq + RP * D + at), lo[0], lo[1], lo[2], lo[3]);
+            if (c == 0) {
+                const float down = __uint_as_float((uint32_t)(127 + (e - 7) / 2) << 23) *
+                                   __uint_as_float((uint32_t)(127 + (e - 7) - (e - 7) / 2) << 23);
+                s_qs[buf * RP + row] = row < sg.rows ? (odd ? __uint_as_float(0x7fffffffu) : down * p.scale_log2) : 0.f;
+                const int token = row / p.group;
+                s_lim[buf * RP + row] = row < sg.rows ? max(sg.seen0 + token, 0) : 0;
+                s_out[buf * RP + row] =
+                    ((long long)(sg.row0 + token) * p.q_heads + sg.head * p.group + row - token * p.group) * D;
+            }
+        };
+        uint4 query[2];
         wait(smem_u32(seg_full), 0, kErrConsumerWait);
-        load_queries(s_seg[0]);
+        if (tid < RP * TPR) load_query(s_seg[0], tid, query);
         int seg = 0;
         bool last = false;
         do {
             const AttnSegment* sg = s_seg + seg % NS;
             const int tile_first = sg->tile0, tiles = sg->tiles, seen0 = sg->seen0, seen_first = max(seen0, 0);
+            const int buf = TG == 2 ? seg & 1 : 0;
+            const float* my_qs = s_qs + buf * RP + r0;
 
-            // the row tile's queries as two e4m3 parts, each row scaled to the top of the range
-            group_sync(kAllBar, kSoftmax);
-#pragma unroll
-            for (int pass = 0; pass < kPasses; ++pass) {
-                const int c = tid % TPR, row = tid / TPR + pass * (kSoftmax / TPR);
-                if (row >= RP) break;
-                const uint4 qa = queries[pass][0], qb = queries[pass][1];
-                const uint32_t x[8] = {qa.x, qa.y, qa.z, qa.w, qb.x, qb.y, qb.z, qb.w};
-                uint32_t top = 0;                   // largest magnitude: bf16 bits order as integers
-#pragma unroll
-                for (int k = 0; k < 8; ++k) top = max(top, max(x[k] & 0x7fffu, (x[k] >> 16) & 0x7fffu));
-                const unsigned mates = TPR == 8 ? 0xffu << (lane & 24) : 0xfu << (lane & 28);
-#pragma unroll
-                for (int o = TPR / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(mates, top, o));
-                // 2^e <= largest < 2^(e+1) becomes [128, 256); a row with an infinity or a NaN answers NaN
-                const int e = max((int)(top >> 7), 1) - 127;
-                const bool odd = (top >> 7) == 255;
-                // 2^(7-e) in two steps: each one fits fp32
-                const float up1 = __uint_as_float((uint32_t)(127 + (7 - e) / 2) << 23);
-                const float up2 = __uint_as_float((uint32_t)(127 + (7 - e) - (7 - e) / 2) << 23);
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float f[4], s[4];
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        const uint32_t two = x[2 * k + m / 2];
-                        f[m] = __uint_as_float(m & 1 ? two & 0xffff0000u : two << 16) * up1 * up2;
-                    }
-                    hi[k] = f32x2_to_e4m3x2(f[0], f[1]) | f32x2_to_e4m3x2(f[2], f[3]) << 16;
-                    uint32_t h01, h23;
-                    e4m3x4_to_f16x2x2(hi[k], h01, h23);
-                    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-                        : "=f"(s[0]), "=f"(s[1]) : "r"(h01));
-                    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-                        : "=f"(s[2]), "=f"(s[3]) : "r"(h23));
-                    lo[k] = f32x2_to_e4m3x2(f[0] - s[0], f[1] - s[1]) | f32x2_to_e4m3x2(f[2] - s[2], f[3] - s[3]) << 16;
-                }
-                const int sw = D == 128 ? (c ^ (row & 7)) : (c ^ ((row >> 1) & 3));
-                const int at = row * D + sw * 16;
-                // the parts' rows follow one another: RP is a multiple of 8, so both swizzle alike
-                sts128(smem_u32(sq + at), hi[0], hi[1], hi[2], hi[3]);
-                sts128(smem_u32(sq + RP * D + at), lo[0], lo[1], lo[2], lo[3]);
-                if (c == 0) {
-                    const float down = __uint_as_float((uint32_t)(127 + (e - 7) / 2) << 23) *
-                                       __uint_as_float((uint32_t)(127 + (e - 7) - (e - 7) / 2) << 23);
-                    s_qs[row] = row < sg->rows ? (odd ? __uint_as_float(0x7fffffffu) : down * p.scale_log2) : 0.f;
-                    const int token = row / p.group;
-                    s_lim[row] = row < sg->rows ? max(seen0 + token, 0) : 0;
-                    s_out[row] = (long long)(sg->row0 + token) * p.q_heads + sg->head * p.group + row - token * p.group;
-                }
-            }
-            if (tid < D) s_nan[tid] = 0x7fffffff;
+            // the accumulators and the rows' notes of the segment before have been read
             if (tl < RW) my_n[tl] = 0.f;
-            fence_proxy_async_smem();
+            tc_fence_before_sync();
             group_sync(kAllBar, kSoftmax);
-            if (lane == 0) mbar_arrive(smem_u32(q_full));
+            if (TG == 1 || seg == 0) {
+                if (tid < RP * TPR) store_query(*sg, 0, tid, query);
+                if (tid < D) s_nan[tid] = 0x7fffffff;
+                fence_proxy_async_smem();
+                group_sync(kAllBar, kSoftmax);
+                if (tg == 0 && lane == 0) mbar_arrive(smem_u32(q_full));
+            }
 
             F2 l[RW / 2];
 #pragma unroll
@@ -930,7 +936,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                             unsigned char* byte = codes + c * 16 + k;
                             if ((*byte & 0x7f) != 0x7f) continue;
                             *byte = 0;
-                            atomicMin(s_nan + dims + k, j);
+                            atomicMin(s_nan + buf * D + dims + k, j);
                         }
                     }
                 }
@@ -961,7 +967,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
 #pragma unroll
                         for (int r = 0; r < kHalf; r += 4) {
                             F2 q0, q1, n0, n1, x0 = f2(d[r], d[r + 1]), x1 = f2(d[r + 2], d[r + 3]);
-                            lds_f2x2(s_qs + r0 + h + r, q0, q1);
+                            lds_f2x2(my_qs + h + r, q0, q1);
                             lds_f2x2(my_n + h + r, n0, n1);
                             if (C::kConcat) {
                                 x0 = add2(x0, f2(lo[r], lo[r + 1]));
@@ -1079,13 +1085,13 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                 vt.step(TG);
             }
 
-            // the next segment's queries are on their way while this one's sums are made
+            // with one tile group the next segment's queries are on their way while this one's sums are made
             const int rows = sg->rows;
             const bool whole = sg->whole;
             last = sg->last;
             if (!last) {
                 wait(smem_u32(seg_full + (seg + 1) % NS), ((seg + 1) / NS) & 1, kErrConsumerWait);
-                load_queries(s_seg[(seg + 1) % NS]);
+                if (TG == 1 && tid < RP * TPR) load_query(s_seg[(seg + 1) % NS], tid, query);
             }
 
             // ---------------------------------------- the segment's sums
@@ -1101,6 +1107,25 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
             group_sync(bar_id, 128);
             if (tl < RW) s_l[tg * RP + r0 + tl] = (red[tl] + red[RW + tl]) + (red[2 * RW + tl] + red[3 * RW + tl]);
             it0 += tiles;
+            // with two, the one that is ready first makes them while the other takes the last tile: the
+            // next scores are then there when that one is done (the last scores of this segment
+            // are what read these queries last)
+            if (TG == 2 && !last && tg != ((it0 - 1) & 1)) {
+                wait(smem_u32(s_full + ((it0 - 1) & 1)), ((it0 - 1) >> 1) & 1, kErrConsumerWait);
+                const AttnSegment& after = s_seg[(seg + 1) % NS];
+                const int t0 = (wg % CG) * 128 + tl;
+                constexpr int kGroupThreads = CG * 128;
+#pragma unroll 1
+                for (int t = t0; t < RP * TPR; t += kGroupThreads) {
+                    uint4 v[2];
+                    load_query(after, t, v);
+                    store_query(after, buf ^ 1, t, v);
+                }
+                for (int d = t0; d < D; d += kGroupThreads) s_nan[(buf ^ 1) * D + d] = 0x7fffffff;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(q_full));
+            }
             {
                 const int rounds = (vr.slot + tiles) / NV;
                 vr.slot += tiles - rounds * NV;
@@ -1124,7 +1149,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                     const float scale = sum == 0.f ? 0.f : 1.f / sum;
                     f0 *= scale;
                     f1 *= scale;
-                    if (p.lse && tid < rows) p.lse[s_out[tid]] = sum == 0.f ? -INFINITY : (log2f(sum) - n) * 0.693147180559945f;
+                    if (p.lse && tid < rows) p.lse[s_out[buf * RP + tid] / D] = sum == 0.f ? -INFINITY : (log2f(sum) - n) * 0.693147180559945f;
                 } else {
                     float* ps = p.partial + (size_t)gridDim.x * 2 * RP * D + ((size_t)cta_slot * RP + tid) * 2;
                     ps[0] = sum == 0.f ? INFINITY : n;           // nothing seen here
@@ -1138,35 +1163,48 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
             tc_fence_after_sync();
             group_sync(kAllBar, kSoftmax);
             const int dim = wq * kDimLanes + lane;
-            const int nan_from = lane < kDimLanes ? s_nan[dim] : 0x7fffffff;
-            float* po = p.partial + (size_t)cta_slot * RP * D + dim;
+            const int nan_from = lane < kDimLanes ? s_nan[buf * D + dim] : 0x7fffffff;
+            const bool nan_any = __any_sync(~0u, nan_from != 0x7fffffff);
 #pragma unroll 1
             for (int r = wg * 8; r < rows; r += NWG * 8) {
                 float o[8] = {};
 #pragma unroll
                 for (int g = 0; g < TG; ++g) {
-                    float x[C::kParts][8];
+                    float x[C::kParts][8], f[8];
 #pragma unroll
                     for (int i = 0; i < C::kParts; ++i) tmem_ld<8>(lanes + C::kOutCol + g * C::kOutCols + i * RP + r, x[i]);
+#pragma unroll
+                    for (int k = 0; k < 8; k += 4) {
+                        const float4 y = *reinterpret_cast<const float4*>(s_f + g * RP + r + k);
+                        f[k] = y.x; f[k + 1] = y.y; f[k + 2] = y.z; f[k + 3] = y.w;
+                    }
                     tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        float y = x[C::kParts - 1][k];
+                    for (int k = 0; k < 8; k += 2) {
+                        F2 y = f2(x[C::kParts - 1][k], x[C::kParts - 1][k + 1]);
 #pragma unroll
-                        for (int i = C::kParts - 2; i >= 0; --i) y = fmaf(y, 1.f / 16, x[i][k]);
-                        const float f = s_f[g * RP + r + k];
-                        if (f != 0.f) o[k] = fmaf(y, f, o[k]);
+                        for (int i = C::kParts - 2; i >= 0; --i) y = fma2(y, f2(1.f / 16, 1.f / 16), f2(x[i][k], x[i][k + 1]));
+                        float y0, y1;
+                        unpack(y, y0, y1);
+                        if (f[k] != 0.f) o[k] = fmaf(y0, f[k], o[k]);
+                        if (f[k + 1] != 0.f) o[k + 1] = fmaf(y1, f[k + 1], o[k + 1]);
                     }
                 }
+                if (nan_any) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int row = r + k;
-                    if (nan_from < s_lim[row]) o[k] = __uint_as_float(0x7fffffffu);
-                    if (row < rows && lane < kDimLanes) {
-                        if (whole)
-                            p.out[s_out[row] * D + dim] = f32_to_bf16_rne(o[k]);
-                        else
-                            po[row * D] = o[k];
+                    for (int k = 0; k < 8; ++k)
+                        if (nan_from < s_lim[buf * RP + r + k]) o[k] = __uint_as_float(0x7fffffffu);
+                }
+                if (lane < kDimLanes) {
+                    if (whole) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (r + k < rows) p.out[s_out[buf * RP + r + k] + dim] = f32_to_bf16_rne(o[k]);
+                    } else {
+                        float* to = p.partial + ((size_t)cta_slot * RP + r) * D + dim;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (r + k < rows) to[k * D] = o[k];
                     }
                 }
             }
