@@ -367,7 +367,11 @@ struct CtaWait {
     volatile int* stop;
     __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity, unsigned bit) const {
         // a test answers in a third of the time of a wait that may suspend
-        if (__builtin_expect(mbar_test(bar, parity), 1)) return true;
+        return after(mbar_test(bar, parity), bar, parity, bit);
+    }
+    // `done`: what a test made before has said
+    __device__ __forceinline__ bool after(bool done, uint32_t bar, uint32_t parity, unsigned bit) const {
+        if (__builtin_expect(done, 1)) return true;
         if (*stop) return false;
 #pragma unroll 1
         for (int i = 0; i < 32; ++i)
@@ -901,7 +905,10 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
             bool force = true;               // some row has no n_r yet
             for (int t = t_first; t < tiles; t += TG) {
                 const int it = it0 + t, tile = tile_first + t, j = tile * kTile + tl;
-                wait(smem_u32(v_full + vt.slot), vt.round, kErrConsumerWait);
+                // tests together, so that their answers' times overlap
+                const bool v_ok = mbar_test(smem_u32(v_full + vt.slot), vt.round);
+                const bool s_ok = mbar_test(smem_u32(s_full + (it & 1)), (it >> 1) & 1);
+                wait.after(v_ok, smem_u32(v_full + vt.slot), vt.round, kErrConsumerWait);
                 const TokenScales ts = scales[vt.slot * kTile + tl];
                 const int flags = s_flags[vt.slot];
                 const bool absent = ts.value < 0.f;
@@ -911,7 +918,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                 const float lv = log2_fast(value), inv = rcp_fast(value);
                 const bool masked = (tile + 1) * kTile > seen_first || flags;
 
-                wait(smem_u32(s_full + (it & 1)), (it >> 1) & 1, kErrConsumerWait);
+                wait.after(s_ok, smem_u32(s_full + (it & 1)), (it >> 1) & 1, kErrConsumerWait);
                 tc_fence_after_sync();
                 // values that do not count are taken out: all of an absent token or of a zero scale, and NaN
                 // codes of the new tokens (0 x NaN would reach every row), which are noted by dim
@@ -985,6 +992,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                     float top = -INFINITY;
 #pragma unroll
                     for (int r = 0; r < kHalf; r += 2) top = max3(top, d[r], d[r + 1]);
+                    const bool pv_ok = h > 0 || it < 2 || mbar_test(smem_u32(pv_done + (it & 1)), ((it >> 1) - 1) & 1);
                     // a row passes the top, or has no n_r yet: its n_r moves, and its sums follow
                     if (__builtin_expect(group_any(bar_id, 128, top > kTop || force), 0)) {
                         float m0 = 0.f;
@@ -1047,7 +1055,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                     }
 
                     // probabilities, cut into parts: columns of part i, then row, 16 to a chunk of 2 KB
-                    if (h == 0) pv_wait(it - 2);
+                    if (h == 0) wait.after(pv_ok, smem_u32(pv_done + (it & 1)), ((it >> 1) - 1) & 1, kErrConsumerWait);
 #pragma unroll
                     for (int r = 0; r < kHalf; r += kStep) {
                         uint32_t part[kStep / 4][C::kParts];
