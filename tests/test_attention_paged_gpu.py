@@ -85,6 +85,18 @@ def test_many_sequences(cuda_device):
     check(step, *run(step, cuda_device))
 
 
+@pytest.mark.parametrize("most,group", [(4, 8), (6, 8), (8, 8), (3, 3)])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_many_short_sequences_of_several_tokens(cuda_device, most, group, dim):
+    """One CTA goes through several sequences of one or two tiles each: the next one's queries
+    follow at once, and some sequences have no new token or see nothing."""
+    g = torch.Generator().manual_seed(most)
+    news = torch.randint(0, most + 1, (310,), generator=g).tolist()
+    lens = [max(n + int(e), 0) for n, e in zip(news, torch.randint(-2, 200, (310,), generator=g))]
+    step = Step(lens, news, heads=2 * group, kv_heads=2, dim=dim, page=32, block=8, seed=24)
+    check(step, *run(step, cuda_device))
+
+
 def test_rows_that_see_nothing(cuda_device):
     """No cached tokens, fewer cached than new ones, and only absent pages: zeros."""
     step = Step([0, 3, 40, 150], [2, 5, 1, 4], seed=23)
