@@ -680,32 +680,34 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
             __syncwarp();
             const int* table = p.s.block_table + (size_t)w.entry.b * p.s.table_cols;
             const int head = w.head / p.head_parts;
-            auto pages_of = [&](int tile, int (&pg)[4]) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int j = tile * kTile + 32 * k + lane;
-                    pg[k] = -1;
-                    if (tile < w.tile1 && j < w.entry.seen_last) pg[k] = table[j >> p.page_shift];
-                }
+            // four consecutive tokens are on one page, and share a block of four or more
+            auto page_of = [&](int tile) {
+                const int j = tile * kTile + 4 * lane;
+                return tile < w.tile1 && j < w.entry.seen_last ? table[j >> p.page_shift] : -1;
             };
-            auto load = [&](int tile, const int (&pg)[4], float (&a)[4], float (&b)[4]) {
+            auto load = [&](int tile, int pg, float (&a)[4], float (&b)[4]) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     a[k] = 0.f;
                     b[k] = -1.f;
-                    if ((unsigned)pg[k] < (unsigned)p.num_pages) {
-                        const int t = (tile * kTile + 32 * k + lane) & (p.page_size - 1);
-                        const long long o = pg[k] * p.scale_page_stride + head * p.scale_head_stride + (t >> p.block_shift);
-                        a[k] = p.k_scale[o];
-                        b[k] = p.v_scale[o];
-                    }
+                }
+                if ((unsigned)pg >= (unsigned)p.num_pages) return;
+                const int j = tile * kTile + 4 * lane, t = j & (p.page_size - 1);
+                const long long o = pg * p.scale_page_stride + head * p.scale_head_stride + (t >> p.block_shift);
+                a[0] = p.k_scale[o];
+                b[0] = p.v_scale[o];
+#pragma unroll
+                for (int k = 1; k < 4; ++k) {
+                    const int more = k >> p.block_shift;
+                    a[k] = more ? p.k_scale[o + more] : a[0];
+                    b[k] = more ? p.v_scale[o + more] : b[0];
+                    if (j + k >= w.entry.seen_last) b[k] = -1.f;
                 }
             };
-            int pg[4], next[4];
             float a[4], b[4];
-            pages_of(w.tile0, pg);
-            pages_of(w.tile0 + 1, next);
-            load(w.tile0, pg, a, b);
+            int next = page_of(w.tile0);
+            load(w.tile0, next, a, b);
+            next = page_of(w.tile0 + 1);
             if (lane == 0) {
                 // read after the segment's last tile, so nobody waits for the divisions
                 int share = 0;
@@ -718,26 +720,23 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
             ++seg;
             for (int tile = w.tile0; tile < w.tile1; ++tile, ++it) {
                 float a1[4], b1[4];
-                int later[4];
                 load(tile + 1, next, a1, b1);
-                pages_of(tile + 2, later);
+                next = page_of(tile + 2);
                 const int s = it % NV;
                 if (it >= NV) ok = __all_sync(~0u, wait(smem_u32(v_empty + s), (it / NV - 1) & 1, kErrProducerWait));
                 if (!ok) break;
                 int flags = 0;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    flags |= b[k] < kTinyScale;             // -1 where absent
-                    scales[s * kTile + 32 * k + lane] = TokenScales{a[k], b[k]};
-                }
+                for (int k = 0; k < 4; ++k) flags |= b[k] < kTinyScale;         // -1 where absent
+                float4* to = reinterpret_cast<float4*>(scales + s * kTile + 4 * lane);
+                to[0] = make_float4(a[0], b[0], a[1], b[1]);
+                to[1] = make_float4(a[2], b[2], a[3], b[3]);
                 flags = __reduce_or_sync(~0u, flags);
                 if (lane == 0) s_flags[s] = flags;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(v_full + s));
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    pg[k] = next[k];
-                    next[k] = later[k];
                     a[k] = a1[k];
                     b[k] = b1[k];
                 }
