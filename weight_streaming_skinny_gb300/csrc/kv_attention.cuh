@@ -126,13 +126,18 @@ struct AttnShare {
 // 4096 tokens, 8 rows, 28.1 -> 26.1 us), beyond that one CTA whose two tile groups
 // (TG) take tiles in turn, with accumulators of their own, and share the pipeline's
 // slots.  A tile group beyond 32 rows is two warpgroups (CG) of RW rows each: more
-// warps to hide one another's latencies (64 rows at 4 x 32768 tokens: 200 -> 159 us when it was built).
+// warps to hide one another's latencies (64 rows at 4 x 32768 tokens: 200 -> 159 us
+// when it was built).  With heads of 64, 17 to 32 rows are better off as two CTAs of one tile
+// group of two warpgroups (64 x 2048 tokens, 32 rows: 63.0 -> 49.6 us; 24 x 2049, 24
+// rows: 29.9 -> 24.2), with heads of 128 only where sequences are short (256 x 512: 128
+// -> 93 us, but 16 x 8192: 49 -> 58), which the host cannot know; 48 rows as two CTAs of heads
+// of 64 gain 2 % there and lose 10 % on one long sequence.
 template <int D_, int RP_>
 struct AttnShape {
     static constexpr int D = D_, RP = RP_;
     static constexpr int kParts = RP <= 16 ? 4 : 3;
-    static constexpr int TG = RP > 16 ? 2 : 1;
-    static constexpr int CG = RP > 32 ? 2 : 1;
+    static constexpr int TG = RP > 32 || (RP > 16 && D == 128) ? 2 : 1;
+    static constexpr int CG = RP > 32 || (RP > 16 && D == 64) ? 2 : 1;
     static constexpr int RW = RP / CG;
     static constexpr bool kConcat = RP <= 32;           // S columns: hi parts, then lo parts (else summed by the MMA)
     static constexpr int kScoreCols = kConcat ? 2 * RP : RP;
@@ -140,7 +145,7 @@ struct AttnShape {
     static constexpr int kOutCols = kParts * RP;
     static constexpr int kCols = kOutCol + TG * kOutCols;
     static constexpr int kTmem = kCols <= 32 ? 32 : kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
-    static constexpr int kCtas = TG == 2 ? 1 : D == 64 ? 3 : 2;      // resident CTAs per SM
+    static constexpr int kCtas = TG == 2 ? 1 : D == 64 && RP <= 16 ? 3 : 2;      // resident CTAs per SM
     static constexpr int kThreads = TG * CG * 128 + 96;
     static constexpr int kTileBytes = kTile * D;        // codes of K, and of V
     static constexpr int kQBytes = 2 * RP * D;
@@ -816,7 +821,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
         auto pv_wait = [&](int i) {         // the product of tile i has been made
             if (i >= 0) wait(smem_u32(pv_done + (i & 1)), (i >> 1) & 1, kErrConsumerWait);
         };
-        // a segment's queries: 16 elements each thread (and pass), read before the segment before it is finished
+        // a segment's queries: 16 elements each thread, read before the segment before it is finished
         constexpr int TPR = D / 16;                         // threads of a row
         static_assert(RP * TPR <= kSoftmax, "16 dims each thread");
         // a thread's 16 dims of a row of a segment's queries
@@ -1358,7 +1363,9 @@ struct AttnLaunch {
 // RP and resident CTAs per SM of the instance for `rows` rows (at most kMaxRows).
 constexpr int kMaxRows = 64;
 inline int attn_rows_padded(int rows) { return rows <= 8 ? 8 : rows <= 48 ? (rows + 15) / 16 * 16 : 64; }
-inline int attn_ctas_per_sm(int rp, int dim) { return rp > 16 ? 1 : dim == 64 ? 3 : 2; }
+inline int attn_ctas_per_sm(int rp, int dim) {
+    return dim == 128 ? (rp > 16 ? 1 : 2) : rp > 32 ? 1 : rp > 16 ? 2 : 3;
+}
 
 cudaError_t launch_attention_d64(int rp, const AttnLaunch& a);
 cudaError_t launch_attention_d128(int rp, const AttnLaunch& a);
