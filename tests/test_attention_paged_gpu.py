@@ -153,6 +153,30 @@ def test_nan_of_a_later_token_reaches_only_those_that_see_it(cuda_device):
     assert torch.isnan(out[4:]).all() and torch.isfinite(out[:4]).all()
 
 
+@pytest.mark.parametrize("news,group", [(1, 8), (2, 8), (3, 8), (6, 8), (8, 8)])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("low", [0, 1, 2])
+@pytest.mark.parametrize("sequences", [1, 500])
+def test_nan_of_a_token_without_weight(cuda_device, news, group, dim, low, sequences):
+    """A value that all rows see is NaN; its weight is too small for fp32, and 0 x NaN is NaN
+    still, whichever tile it lies in, on a CTA of its own or with the others."""
+    step = Step([384], [news], heads=group, kv_heads=1, dim=dim, page=128, block=128, seed=31)
+    step.B, step.T = sequences, sequences * news
+    step.lens, step.news = [384] * sequences, [news] * sequences
+    step.table = step.table.expand(sequences, -1).contiguous()
+    step.start = torch.arange(sequences + 1, dtype=torch.int32) * news
+    step.q = torch.ones(step.T, group, dim).bfloat16()
+    for t in range(3):
+        step.k[int(step.table[0, t])] = -16.0 if t == low else 16.0
+    step.k_scale.fill_(1)
+    step.v_scale.fill_(0.01)
+    step.v.view(torch.uint8)[int(step.table[0, low]), 0, 5, 7] = 0x7f
+    out, lse = run(step, cuda_device)
+    nan = torch.isnan(out.cpu())
+    assert nan[:, :, 7].all() and nan.sum() == step.T * group
+    assert torch.isfinite(lse).all()
+
+
 def test_nan_and_infinite_queries(cuda_device):
     step = Step([60, 60], [2, 2], seed=28)
     want = reference(step)[0]

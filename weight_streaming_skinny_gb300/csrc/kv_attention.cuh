@@ -1155,21 +1155,21 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
             if (NWG > 1) group_sync(kAllBar, kSoftmax);
             const int cta_slot = blockIdx.x * 2 + slot;
             if (tid < RP) {
-                // a row's sum over the tile groups, and what its accumulators count for; a group whose
-                // sum is 0 saw nothing (or had no tile: its accumulator is stale)
-                float sum = s_l[tid], n = s_n[tid], f0 = sum == 0.f ? 0.f : 1.f, f1 = 0.f;
+                // a row's sum over the tile groups, and what its accumulators count for: -1 for a group whose sum
+                // is 0, which saw nothing (or had no tile: its accumulator is stale); a factor of 0 counts (a NaN stays)
+                float sum = s_l[tid], n = s_n[tid], f0 = sum == 0.f ? -1.f : 1.f, f1 = -1.f;
                 if (TG == 2) {
                     const float l0 = sum, l1 = s_l[RP + tid], n1 = s_n[RP + tid];
                     const float least = l0 == 0.f ? n1 : l1 == 0.f ? n : fminf(n, n1);
-                    f0 = l0 == 0.f ? 0.f : exp2_fast(least - n);
-                    f1 = l1 == 0.f ? 0.f : exp2_fast(least - n1);
-                    sum = l0 * f0 + l1 * f1;
+                    f0 = l0 == 0.f ? -1.f : exp2_fast(least - n);
+                    f1 = l1 == 0.f ? -1.f : exp2_fast(least - n1);
+                    sum = (l0 == 0.f ? 0.f : l0 * f0) + (l1 == 0.f ? 0.f : l1 * f1);
                     n = least;
                 }
                 if (whole) {
-                    const float scale = sum == 0.f ? 0.f : 1.f / sum;
-                    f0 *= scale;
-                    f1 *= scale;
+                    const float scale = 1.f / sum;
+                    if (!(f0 < 0.f)) f0 *= scale;
+                    if (!(f1 < 0.f)) f1 *= scale;
                     if (p.lse && tid < rows) p.lse[s_out[buf * RP + tid] / D] = sum == 0.f ? -INFINITY : (log2f(sum) - n) * 0.693147180559945f;
                 } else {
                     float* ps = p.partial + (size_t)gridDim.x * 2 * RP * D + ((size_t)cta_slot * RP + tid) * 2;
@@ -1207,8 +1207,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                         for (int i = C::kParts - 2; i >= 0; --i) y = fma2(y, f2(1.f / 16, 1.f / 16), f2(x[i][k], x[i][k + 1]));
                         float y0, y1;
                         unpack(y, y0, y1);
-                        if (f[k] != 0.f) o[k] = fmaf(y0, f[k], o[k]);
-                        if (f[k + 1] != 0.f) o[k + 1] = fmaf(y1, f[k + 1], o[k + 1]);
+                        if (!(f[k] < 0.f)) o[k] = fmaf(y0, f[k], o[k]);
+                        if (!(f[k + 1] < 0.f)) o[k + 1] = fmaf(y1, f[k + 1], o[k + 1]);
                     }
                 }
                 if (nan_any) {
