@@ -924,9 +924,11 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                 const TokenScales ts = scales[vt.slot * kTile + tl];
                 const int flags = s_flags[vt.slot];
                 const bool absent = ts.value < 0.f;
-                // a scale too small for its logarithm counts as zero: the token weighs, its values do not
+                // a scale below the smallest that counts is a zero: the token weighs, its values do not.  Its P is
+                // that of the smallest scale, so that n_r is placed by tokens whose values count (were its
+                // scale taken as 1, scales of 2^-18 would be left with three bits beside it, of 2^-22 with none)
                 const bool empty = absent || ts.value < kTinyScale;
-                const float value = empty ? 1.f : ts.value;
+                const float value = absent ? 1.f : empty ? kTinyScale : ts.value;
                 const float lv = log2_fast(value), inv = rcp_fast(value);
                 const bool masked = (tile + 1) * kTile > seen_first || flags;
 
