@@ -378,8 +378,11 @@ dl_status dl_kv_append(const dl_kv_cache* cache, const void* q, const void* k, c
  *     out[t][h] = sum_j p_j V[j][h'] ,  p = softmax_j(scale * q[t][h] . K[j][h'])
  * over the cached tokens j <= the cache index of t, h' = h / (q_heads / num_heads).
  * A token that sees nothing (cache index < 0, or only absent pages) gets zeros.
- * Sums, maxima and exponentials are fp32; what is stored in the cache past a
- * token's index, NaN included, does not reach its output.
+ * Scores, maxima, exponentials, sums and the normaliser are fp32.  Two things have
+ * fewer bits: a weight goes into the product with V rounded to 11 significant
+ * bits (fp16), and to a multiple of 2^-33 of the row's largest p_j * v_scale; an element of
+ * q below 2^-9 of its row's largest magnitude counts to 2^-17 of that.  What is stored
+ * in the cache past a token's index, NaN included, does not reach its output.
  *   q      bf16 [tokens][q_heads][D], 16-byte aligned
  *   out    bf16 [tokens][q_heads][D] dense, 16-byte aligned, rounded once
  *   lse    fp32 [tokens][q_heads] or NULL: log sum_j exp(scale * q . K_j)

@@ -403,7 +403,8 @@ __device__ __forceinline__ void tc_fence_after_sync() {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
-// D[taddr] (+)= A . B^T for one K step, issued by a single thread.
+// D[taddr] (+)= A . B^T for one K step of A in e4m3 (B's type is in `idesc`), issued by a
+// single thread.
 __device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                           uint32_t idesc, uint32_t accumulate) {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"

@@ -13,14 +13,18 @@
 // lie in the cache, tokens on the TMEM lanes; nothing converts keys or values:
 //     S^T [128 tokens x rows] = K [128 x D] . Q^T
 //     O^T [D x rows]         += V^T [D x 128] . P^T
-// The 16-bit side goes in as sums of e4m3 numbers of 4 significant bits.  A bf16
-// query has 8 and is the sum of two parts, exact down to 2^-17 of the row's
-// largest element (each row is scaled to the top of the range).  P is rounded to
-// fp16 and cut into parts of 16 times each other's scale, each in accumulator columns
-// of its own: four up to 16 rows, three beyond.  That is exact to fp16's 11 bits
-// near the top, to 2^-8 down to 2^-13 of the row's largest, 2^-21 of it absolute
-// below, and leaves room for the maximum to grow (by 2^9 or 2^5) before n_r has
-// to move.  (Measured against it: two parts have 18 bits of range for both, and moving
+// The 16-bit side goes in as sums of 8-bit numbers.  A bf16 query has 8 significant
+// bits and is the sum of two e4m3 parts of 4: exact for elements from 2^-9 of the
+// row's largest on (each row is scaled to the top of the range), to 2^-17 of it absolute
+// below.  P is rounded to fp16 and cut into three e5m2 parts of 16 times each
+// other's scale, each in accumulator columns of its own.  A part has 3 significant bits
+// and a sign, so three hold fp16's 11 exactly, and with e5m2's range down to its
+// smallest number, 2^-24.  The row's largest P is at 2^9 at least: a weight loses no
+// more than 11 bits' rounding down to 2^-23 of the largest, 2^-34 of it absolute
+// below, so that a tail of many small ones counts beside a token that takes nearly all
+// weight.  The maximum may grow by 2^5.8 before n_r has to move.
+// (e4m3 parts end at 2^-21 of the largest, three or four of them: 32768 tokens of 2^-22
+// were lost, 0.8 % of the weight.  Two e4m3 parts have 18 bits of range for both, and moving
 // n_r took most of the time at 128 rows; fp16 products need the values widened in
 // shared memory, which then moves twice the bytes and bounds the kernel at 48 rows.)
 // Scores, maxima, exponentials, sums and accumulators are fp32.
@@ -135,14 +139,14 @@ struct AttnShare {
 template <int D_, int RP_>
 struct AttnShape {
     static constexpr int D = D_, RP = RP_;
-    static constexpr int kParts = RP <= 16 ? 4 : 3;
+    static constexpr int kParts = 3;
     static constexpr int TG = RP > 32 || (RP > 16 && D == 128) ? 2 : 1;
     static constexpr int CG = RP > 32 || (RP > 16 && D == 64) ? 2 : 1;
     static constexpr int RW = RP / CG;
     static constexpr bool kConcat = RP <= 32;           // S columns: hi parts, then lo parts (else summed by the MMA)
     static constexpr int kScoreCols = kConcat ? 2 * RP : RP;
     static constexpr int kOutCol = 2 * kScoreCols;
-    static constexpr int kOutCols = kParts * RP;
+    static constexpr int kOutCols = (kParts * RP + 15) / 16 * 16;    // P's columns come in chunks of 16
     static constexpr int kCols = kOutCol + TG * kOutCols;
     static constexpr int kTmem = kCols <= 32 ? 32 : kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
     static constexpr int kCtas = TG == 2 ? 1 : D == 64 && RP <= 16 ? 3 : 2;      // resident CTAs per SM
@@ -183,10 +187,13 @@ __device__ __forceinline__ uint64_t umma_desc(uint32_t saddr, uint32_t lead, uin
            (uint64_t)1 << 46 | (uint64_t)layout << 61;
 }
 
-// Instruction descriptor of kind::f8f6f4, e4m3 x e4m3 -> fp32, M x N; mn = 1:
-// both operands have their M / N dimension contiguous in memory.
-__host__ __device__ constexpr uint32_t umma_idesc(int m, int n, int mn) {
-    return (1u << 4) | (mn ? 3u << 15 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+// Instruction descriptors of kind::f8f6f4 -> fp32, M x N, A in e4m3: B in e4m3, both
+// operands with their K dimension contiguous in memory; and B in e5m2, M and N contiguous.
+__host__ __device__ constexpr uint32_t umma_idesc_k(int m, int n) {
+    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+__host__ __device__ constexpr uint32_t umma_idesc_mn_e5m2(int m, int n) {
+    return umma_idesc_k(m, n) | (1u << 10) | (3u << 15);
 }
 
 // One lane of a converged warp.
@@ -281,10 +288,10 @@ __device__ __forceinline__ void lds_f2x2(const float* p, F2& a, F2& b) {
     b = v.y;
 }
 
-// Four probabilities -> their e4m3 parts, each the rest of the one before times 16.
-// The fp16 step in between rounds to 2^-11.
+// Four probabilities -> their e5m2 parts, each the rest of the one before times 16.
+// The fp16 step in between rounds to 2^-11, and is all that is lost of numbers below 2^15.
 template <int N>
-__device__ __forceinline__ void split_e4m3(float e0, float e1, float e2, float e3, uint32_t (&part)[N]) {
+__device__ __forceinline__ void split_e5m2(float e0, float e1, float e2, float e3, uint32_t (&part)[N]) {
     constexpr uint32_t kSixteen = 0x4C004C00u;          // f16x2
     uint32_t x = f32x2_to_f16x2(e0, e1), y = f32x2_to_f16x2(e2, e3);
 #pragma unroll
@@ -293,10 +300,10 @@ __device__ __forceinline__ void split_e4m3(float e0, float e1, float e2, float e
             uint32_t u, v;
             asm("{\n\t"
                 ".reg .b16 a, b;\n\t"
-                "cvt.rn.satfinite.e4m3x2.f16x2 a, %3;\n\t"
-                "cvt.rn.satfinite.e4m3x2.f16x2 b, %4;\n\t"
-                "cvt.rn.f16x2.e4m3x2 %1, a;\n\t"
-                "cvt.rn.f16x2.e4m3x2 %2, b;\n\t"
+                "cvt.rn.satfinite.e5m2x2.f16x2 a, %3;\n\t"
+                "cvt.rn.satfinite.e5m2x2.f16x2 b, %4;\n\t"
+                "cvt.rn.f16x2.e5m2x2 %1, a;\n\t"
+                "cvt.rn.f16x2.e5m2x2 %2, b;\n\t"
                 "mov.b32 %0, {a, b};\n\t"
                 "}"
                 : "=r"(part[i]), "=r"(u), "=r"(v) : "r"(x), "r"(y));
@@ -310,8 +317,8 @@ __device__ __forceinline__ void split_e4m3(float e0, float e1, float e2, float e
         } else {
             asm("{\n\t"
                 ".reg .b16 a, b;\n\t"
-                "cvt.rn.satfinite.e4m3x2.f16x2 a, %1;\n\t"
-                "cvt.rn.satfinite.e4m3x2.f16x2 b, %2;\n\t"
+                "cvt.rn.satfinite.e5m2x2.f16x2 a, %1;\n\t"
+                "cvt.rn.satfinite.e5m2x2.f16x2 b, %2;\n\t"
                 "mov.b32 %0, {a, b};\n\t"
                 "}"
                 : "=r"(part[i]) : "r"(x), "r"(y));
@@ -464,8 +471,10 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     // one accumulator lane per dim: M = 64 leaves 16 rows in each warp's lanes
     constexpr int kDimLanes = D / 4;
     constexpr uint32_t kSwizzle = D == 128 ? 2 : 4;
-    // largest exponent of a probability (log2 448 = 8.807), and the one a maximum gets
-    constexpr float kTop = 8.8f, kTarget = C::kParts == 4 ? -1.f : 3.f;
+    // largest exponent of a probability (its parts hold numbers below 2^15), and the one a maximum
+    // gets: the rest is its room to grow.  (A maximum at 2^5, with 2^9.8 to grow: the same times up to
+    // 16 rows, 125.7 -> 124.8 us at 4 x 32768 tokens with 16 new ones; small weights would end at 2^-30.)
+    constexpr float kTop = 14.8f, kTarget = 9.f;
     // rows that a softmax thread works on at a time, and columns of a load: as registers allow
     constexpr int kHalf = RW > 24 && C::CG == 2 ? RW / 2 : RW, kStep = kHalf % 16 ? 8 : 16;
     constexpr float kTinyScale = 8.67361737988403547e-19f;       // 2^-60
@@ -749,8 +758,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
         } while (ok && w.next(p));
     } else if (work && warp == kMma) {
         // ------------------------------------------------ products: the warp waits, one lane issues
-        constexpr uint32_t kScoreIdesc = umma_idesc(128, C::kScoreCols, 0);
-        constexpr uint32_t kOutIdesc = umma_idesc(D, C::kOutCols, 1);
+        constexpr uint32_t kScoreIdesc = umma_idesc_k(128, C::kScoreCols);
+        constexpr uint32_t kOutIdesc = umma_idesc_mn_e5m2(D, C::kOutCols);
         const bool leader = elect_one();
         const uint64_t q_desc = umma_desc(smem_u32(sq), 16, 8 * D, kSwizzle);
         const uint64_t k_desc = umma_desc(smem_u32(keys), 16, 8 * D, kSwizzle);
@@ -1082,11 +1091,11 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                             const int at = (h + r + k) / 2;
                             l[at] = fma2(f2(e[0], e[1]), inv2, l[at]);
                             l[at + 1] = fma2(f2(e[2], e[3]), inv2, l[at + 1]);
-                            split_e4m3<C::kParts>(e[0], e[1], e[2], e[3], part[k / 4]);
+                            split_e5m2<C::kParts>(e[0], e[1], e[2], e[3], part[k / 4]);
                         }
                         if constexpr (RP == 8) {
                             sts128(smem_u32(dst), part[0][0], part[1][0], part[0][1], part[1][1]);
-                            sts128(smem_u32(dst + kTile * 16), part[0][2], part[1][2], part[0][3], part[1][3]);
+                            sts128(smem_u32(dst + kTile * 16), part[0][2], part[1][2], 0, 0);   // columns that fill the chunk
                         } else {
 #pragma unroll
                             for (int i = 0; i < C::kParts; ++i) {
