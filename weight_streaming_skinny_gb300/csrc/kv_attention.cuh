@@ -460,6 +460,24 @@ struct __align__(8) TokenScales {
     float key, value;
 };
 
+// After a wait that gave up: no copy and no product of the CTA may still be in flight when it
+// leaves.  Out of line: in line they cost a call without such a wait 0.2 us.
+// One limit for all copies, which have been under way together.
+template <int NK, int NV>
+__device__ __noinline__ void attn_drain_copies(uint32_t k_full, uint32_t v_full, int keys, int values, WaitCtl ctl) {
+    bool landed = true;
+    for (int i = max(keys - NK, 0); i < keys && landed; ++i)
+        landed = mbar_wait_bounded(k_full + 8 * (i % NK), (i / NK) & 1, ctl, kErrDrainWait);
+    for (int i = max(values - NV, 0); i < values && landed; ++i)
+        landed = mbar_wait_bounded(v_full + 8 * (i % NV), (i / NV) & 1, ctl, kErrDrainWait);
+}
+// By the warp that issued them.
+static __device__ __noinline__ void attn_drain_products(uint32_t all_done, WaitCtl ctl) {
+    if (elect_one()) umma_commit(all_done);
+    __syncwarp();
+    mbar_wait_bounded(all_done, 0, ctl, kErrDrainWait);
+}
+
 template <class C>
 __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
@@ -491,12 +509,14 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     uint64_t* bars = reinterpret_cast<uint64_t*>(misc);
     uint64_t *k_full = bars, *k_empty = k_full + NK, *v_full = k_empty + NK, *v_empty = v_full + NV,
              *s_full = v_empty + NV, *s_read = s_full + 2, *p_full = s_read + 2, *pv_done = p_full + 2, *q_full = pv_done + 2,
-             *seg_full = q_full + 1;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(seg_full + NS);
+             *seg_full = q_full + 1, *all_done = seg_full + NS;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(all_done + 1);
     int* s_stop = reinterpret_cast<int*>(tmem_slot + 1);
     long long* s_walk = reinterpret_cast<long long*>(misc + 512);     // total, begin, end
     int* s_start = reinterpret_cast<int*>(misc + 536);                // first entry, tiles of it before `begin`
     AttnEntry* s_entry = reinterpret_cast<AttnEntry*>(misc + 544);
+    int* s_copied = reinterpret_cast<int*>(misc + 592);               // tiles whose keys, and whose values, were copied
+    volatile int* s_quit = s_copied + 2;                              // a softmax thread has waited for a segment in vain
     int* s_flags = reinterpret_cast<int*>(misc + 640);                // [NV] some token is absent, or its scale tiny
     AttnSegment* s_seg = reinterpret_cast<AttnSegment*>(misc + 1024); // [NS]
     int* s_share = reinterpret_cast<int*>(s_seg + NS);                // [NS] CTAs that share an item begun here, or 0
@@ -531,12 +551,10 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
             }
             mbar_init(smem_u32(q_full), CG * 4);
             for (int i = 0; i < NS; ++i) mbar_init(smem_u32(seg_full + i), 1);
+            mbar_init(smem_u32(all_done), 1);
             *s_stop = 0;
-            // read only after a wait that gave up: nothing to do, and nothing after it
-            for (int i = 0; i < NS; ++i) {
-                s_seg[i] = AttnSegment{0, 0, 0, 0, 0, 0, 1, 1};
-                s_share[i] = 0;
-            }
+            s_copied[0] = s_copied[1] = *s_quit = 0;
+            for (int i = 0; i < NS; ++i) s_share[i] = 0;       // may be read before it is written, after a wait that gave up
             fence_mbarrier_init();
         }
         __syncwarp();
@@ -661,7 +679,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                                 w.head / p.head_parts, page);
                 if (it >= NV) ok = __all_sync(~0u, wait(smem_u32(v_empty + vs), (it / NV - 1) & 1, kErrProducerWait));
                 if (!ok) {
-                    mbar_wait_bounded(smem_u32(k_full + ks), (it / NK) & 1, wait.ctl, kErrDrainWait);
+                    if (lane == 0) s_copied[0] = 1;             // the keys of one tile more
                     break;
                 }
                 if (lane == 16) mbar_arrive_expect_tx(smem_u32(v_full + vs), bytes);
@@ -672,12 +690,9 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                 page = next;
             }
         } while (ok && w.next(p));
-        // after a wait that gave up: no copy of this CTA may still be in flight when it leaves
-        if (!ok) {
-            for (int i = max(it - NK, 0); i < it; ++i)
-                mbar_wait_bounded(smem_u32(k_full + i % NK), (i / NK) & 1, wait.ctl, kErrDrainWait);
-            for (int i = max(it - NV, 0); i < it; ++i)
-                mbar_wait_bounded(smem_u32(v_full + i % NV), (i / NV) & 1, wait.ctl, kErrDrainWait);
+        if (lane == 0) {
+            s_copied[0] += it;
+            s_copied[1] = it;
         }
     } else if (work && warp == kScaler) {
         // ------------------------------------------------ scales: four tokens each lane; a tile's
@@ -817,7 +832,9 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
         } while (ok && w.next(p));
     } else if (work && warp < kProducer) {
         // ------------------------------------------------ softmax: a token each thread
-        // (a wait that gives up is not left by: the others of the group are at its barriers)
+        // (a wait that gives up is not left by: the others of the group are at its barriers.  All leave together
+        // at a segment's end, once one of them has waited for the next one's descriptor in vain: s_quit is
+        // written before and read after a barrier of all)
         const int wg = warp >> 2, wq = warp & 3, tl = tid & 127, bar_id = 1 + wg;
         const int tg = wg / CG, r0 = wg % CG * RW;          // tile group, first row
         const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
@@ -894,8 +911,11 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
             }
         };
         uint4 query[2];
-        wait(smem_u32(seg_full), 0, kErrConsumerWait);
-        if (tid < RP * TPR) load_query(s_seg[0], tid, query);
+        // this segment's descriptor is there: the scales' warp writes no more once it has given up, and those
+        // in the ring are then old ones
+        bool ready = __all_sync(~0u, wait(smem_u32(seg_full), 0, kErrConsumerWait));
+        if (!ready) *s_quit = 1;
+        if (ready && tid < RP * TPR) load_query(s_seg[0], tid, query);
         int seg = 0;
         bool last = false;
         do {
@@ -914,6 +934,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                 fence_proxy_async_smem();
                 group_sync(kAllBar, kSoftmax);
                 if (tg == 0 && lane == 0) mbar_arrive(smem_u32(q_full));
+                if (seg == 0 && *s_quit) break;
             }
 
             F2 l[RW / 2];
@@ -1122,8 +1143,9 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
             const bool whole = sg->whole;
             last = sg->last;
             if (!last) {
-                wait(smem_u32(seg_full + (seg + 1) % NS), ((seg + 1) / NS) & 1, kErrConsumerWait);
-                if (TG == 1 && tid < RP * TPR) load_query(s_seg[(seg + 1) % NS], tid, query);
+                ready = __all_sync(~0u, wait(smem_u32(seg_full + (seg + 1) % NS), ((seg + 1) / NS) & 1, kErrConsumerWait));
+                if (!ready) *s_quit = 1;
+                if (TG == 1 && ready && tid < RP * TPR) load_query(s_seg[(seg + 1) % NS], tid, query);
             }
 
             // ---------------------------------------- the segment's sums
@@ -1142,7 +1164,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
             // with two, the one that is ready first makes them while the other takes the last tile: the
             // next scores are then there when that one is done (the last scores of this segment
             // are what read these queries last)
-            if (TG == 2 && !last && tg != ((it0 - 1) & 1)) {
+            if (TG == 2 && !last && ready && tg != ((it0 - 1) & 1)) {
                 wait(smem_u32(s_full + ((it0 - 1) & 1)), ((it0 - 1) >> 1) & 1, kErrConsumerWait);
                 const AttnSegment& after = s_seg[(seg + 1) % NS];
                 const int t0 = (wg % CG) * 128 + tl;
@@ -1194,6 +1216,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
             if (TG == 2) pv_wait(it0 - 2);
             tc_fence_after_sync();
             group_sync(kAllBar, kSoftmax);
+            last |= *s_quit;
             const int dim = wq * kDimLanes + lane;
             const int nan_from = lane < kDimLanes ? s_nan[buf * D + dim] : 0x7fffffff;
             const bool nan_any = __any_sync(~0u, nan_from != 0x7fffffff);
@@ -1248,6 +1271,10 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
         tc_fence_before_sync();
     }
     __syncthreads();
+    if (__builtin_expect(*s_stop, 0)) {
+        if (warp == kProducer) attn_drain_copies<NK, NV>(smem_u32(k_full), smem_u32(v_full), s_copied[0], s_copied[1], wait.ctl);
+        if (warp == kMma) attn_drain_products(smem_u32(all_done), wait.ctl);
+    }
     if (warp == kMma) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, C::kTmem);
