@@ -153,12 +153,35 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream, device):
+def _handle(stream, device) -> int:
+    """The address of the stream that a call runs on: a stream, an address, or None (the current one)."""
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-    if isinstance(stream, torch.cuda.Stream):
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(int(stream))
+        return torch.cuda.current_stream(device).cuda_stream
+    try:
+        return int(getattr(stream, "cuda_stream", stream))
+    except TypeError:
+        raise ValueError("stream must be a stream or its address") from None
+
+
+def _stream(stream, device):
+    return ctypes.c_void_p(_handle(stream, device))
+
+
+def _empty(shape, dtype, device, stream):
+    """An output of a call that runs on `stream`.  It is that stream's memory, so that what the
+    current stream has freed and may still use is not written, and it is held until the current
+    stream, on which the caller goes on, has done with it."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    handle, current = _handle(stream, device), torch.cuda.current_stream(device)
+    if handle == current.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)
+    return t
 
 
 def _need(t, name, dtype, device=None):
@@ -186,7 +209,8 @@ class Workspace:
     """A device buffer for the arrival counters (its first WORKSPACE_ZERO_BYTES,
     zero-filled here once; every call leaves them zero) and the calls' scratch
     (split-K partial sums, the FP8 activation copy).  Do not share one
-    Workspace between streams that may run at the same time.
+    Workspace between streams that may run at the same time; a call without
+    one takes the default of the stream that it runs on.
     """
 
     def __init__(self, nbytes: int, device="cuda"):
@@ -220,22 +244,26 @@ class Workspace:
 
 
 _default_ws: dict = {}
+_outgrown: list = []     # default workspaces that larger ones replaced: calls under way and graphs name them
 
 
-def _workspace(ws, need: int, device):
+def _workspace(ws, need: int, device, stream):
+    """`ws`, or the default one of the stream that the call runs on."""
     if ws is not None:
         return ws
-    key = (device.index, torch.cuda.current_stream(device).cuda_stream)
+    key = (device.index, _handle(stream, device))
     cur = _default_ws.get(key)
     if cur is None or cur.nbytes < need:
+        if cur is not None:
+            _outgrown.append(cur)
         cur = Workspace(need, device)
         _default_ws[key] = cur
     return cur
 
 
-def _out(out, out_f32, M, N, device):
+def _out(out, out_f32, M, N, device, stream):
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=device)
+        out = _empty((M, N), torch.bfloat16, device, stream)
     _need(out, "out", torch.bfloat16, device)
     if out.numel() != M * N:
         raise ValueError("out must hold M*N elements")
@@ -260,10 +288,10 @@ def linear_bf16(x, w, bias=None, *, out=None, out_f32=None, workspace: Workspace
     N = w.shape[0]
     if bias is not None and bias.numel() != N:
         raise ValueError("bias must be [N]")
-    out = _out(out, out_f32, M, N, dev)
+    out = _out(out, out_f32, M, N, dev, stream)
     with torch.cuda.device(dev):
         need = workspace_bytes(M, N, K, BF16)
-        ws = _workspace(workspace, need, dev)
+        ws = _workspace(workspace, need, dev, stream)
         _check(load().dl_linear_bf16(_ptr(x), _ptr(w), _ptr(bias), _ptr(out), _ptr(out_f32),
                                      M, N, K, ws.ptr, ws.nbytes, _stream(stream, dev)))
     return out
@@ -293,10 +321,10 @@ def linear_swiglu(x, w, scales=None, bias=None, *, out=None, out_f32=None,
     N = w.shape[0]
     if N % 16:
         raise ValueError("SwiGLU needs N % 16 == 0")
-    out = _out(out, out_f32, M, N // 2, dev)
+    out = _out(out, out_f32, M, N // 2, dev, stream)
     dt = FP8_B128 if fp8 else BF16
     with torch.cuda.device(dev):
-        ws = _workspace(workspace, workspace_bytes(M, N, K, dt), dev)
+        ws = _workspace(workspace, workspace_bytes(M, N, K, dt), dev, stream)
         _check(load().dl_linear_swiglu(dt, _ptr(x), _ptr(w), _ptr(scales), _ptr(bias), _ptr(out),
                                        _ptr(out_f32), M, N, K, ws.ptr, ws.nbytes, _stream(stream, dev)))
     return out
@@ -322,7 +350,7 @@ def linear_argmax(x, w, scales=None, bias=None, *, out_idx=None, out_max=None, o
     M, K = x.shape
     N = w.shape[0]
     if out_idx is None:
-        out_idx = torch.empty(M, dtype=torch.int32, device=dev)
+        out_idx = _empty((M,), torch.int32, dev, stream)
     _need(out_idx, "out_idx", torch.int32, dev)
     if out_max is not None:
         _need(out_max, "out_max", torch.float32, dev)
@@ -332,7 +360,7 @@ def linear_argmax(x, w, scales=None, bias=None, *, out_idx=None, out_max=None, o
         _need(out_f32, "out_f32", torch.float32, dev)
     dt = FP8_B128 if fp8 else BF16
     with torch.cuda.device(dev):
-        ws = _workspace(workspace, workspace_bytes(M, N, K, dt), dev)
+        ws = _workspace(workspace, workspace_bytes(M, N, K, dt), dev, stream)
         _check(load().dl_linear_argmax(dt, _ptr(x), _ptr(w), _ptr(scales), _ptr(bias), _ptr(out_idx),
                                        _ptr(out_max), _ptr(out), _ptr(out_f32), M, N, K, ws.ptr,
                                        ws.nbytes, _stream(stream, dev)))
@@ -373,7 +401,7 @@ def linear_bf16_static_scratch(x, w, bias=None, *, out, out_f32=None, stream=Non
     N = w.shape[0]
     if bias is not None and bias.numel() != N:
         raise ValueError("bias must be [N]")
-    out = _out(out, out_f32, M, N, dev)
+    out = _out(out, out_f32, M, N, dev, stream)
     lib = load()
     fn = lib.dl_linear_bf16_static_scratch
     vp, i = ctypes.c_void_p, ctypes.c_int
@@ -408,10 +436,10 @@ def linear_fp8_block128(x, wq, scales, bias=None, *, out=None, out_f32=None,
         raise ValueError("scales must be [ceil(N/128), ceil(K/128)]")
     if bias is not None and bias.numel() != N:
         raise ValueError("bias must be [N]")
-    out = _out(out, out_f32, M, N, dev)
+    out = _out(out, out_f32, M, N, dev, stream)
     with torch.cuda.device(dev):
         need = workspace_bytes(M, N, K, FP8_B128)
-        ws = _workspace(workspace, need, dev)
+        ws = _workspace(workspace, need, dev, stream)
         _check(load().dl_linear_fp8_block128(_ptr(x), _ptr(wq), _ptr(scales), _ptr(bias),
                                              _ptr(out), _ptr(out_f32), M, N, K, ws.ptr,
                                              ws.nbytes, _stream(stream, dev)))
@@ -588,7 +616,8 @@ def kv_append(q, k, v, cache: PagedKVCache, block_table, seq_lens, q_start, *, m
     be q; None without q).  See dl_kv_append for the scales and the rounding.
     """
     if q is not None and out_q is None and isinstance(q, torch.Tensor):
-        out_q = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out_q = torch.empty_like(q, memory_format=torch.contiguous_format) if stream is None else \
+            _empty(q.shape, q.dtype, q.device, stream)
     if not _call("append", cache.device, *cache._args, q, k, v, block_table, seq_lens, q_start, max_q, cos, sin,
                  positions, out_q, stream):
         _explain_append(q, k, v, cache, block_table, seq_lens, q_start, cos, sin, positions, out_q)
@@ -636,12 +665,14 @@ def attention_paged(q, cache: PagedKVCache, block_table, seq_lens, q_start, *, m
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format) if stream is None else \
+            _empty(q.shape, q.dtype, q.device, stream)
     if workspace is None:
         _explain_attention(q, cache, block_table, seq_lens, q_start, out, out_lse)
         with torch.cuda.device(cache.device):
             workspace = _workspace(None, attention_workspace_bytes(
-                seq_lens.numel(), q.shape[0], q.shape[1], cache.kv_heads, cache.head_dim, max_q=max_q), cache.device)
+                seq_lens.numel(), q.shape[0], q.shape[1], cache.kv_heads, cache.head_dim, max_q=max_q), cache.device,
+                stream)
     if not _call("attention", cache.device, *cache._args, q, block_table, seq_lens, q_start, max_q,
                  cache.head_dim ** -0.5 if scale is None else scale, out, out_lse, workspace.addr,
                  workspace.nbytes, stream):
@@ -682,9 +713,11 @@ def verify_draft(draft_tokens, target_probs, u_accept, u_next, *, draft_probs=No
         raise ValueError("draft_tokens must be [batch, drafts]")
     dev, (B, S) = target_probs.device, draft_tokens.shape
     if out_tokens is None:
-        out_tokens = torch.empty((B, S + 1), dtype=torch.int32, device=dev)
+        out_tokens = torch.empty((B, S + 1), dtype=torch.int32, device=dev) if stream is None else \
+            _empty((B, S + 1), torch.int32, dev, stream)
     if out_count is None:
-        out_count = torch.empty((B,), dtype=torch.int32, device=dev)
+        out_count = torch.empty((B,), dtype=torch.int32, device=dev) if stream is None else \
+            _empty((B,), torch.int32, dev, stream)
     if not _call("verify", dev, dev.index, draft_tokens, target_probs, u_accept, u_next, draft_probs, draft_lens,
                  out_tokens, out_count, stream):
         _explain_verify(draft_tokens, target_probs, u_accept, u_next, draft_probs, draft_lens, out_tokens, out_count)
