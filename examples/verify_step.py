@@ -55,7 +55,7 @@ class Decoder:
         cols = (hidden, heads * dim, hidden, intermediate)
         shapes = [(m, n, k, dl.BF16) for m in (1, 16) for n, k in zip(rows, cols)] + \
                  [(m, vocab, hidden, dl.BF16) for m in (1, 16)]
-        attention = max(dl.attention_workspace_bytes(batch, n, heads, kv_heads, dim, max_q=n) for n in range(1, 17))
+        attention = dl.attention_workspace_bytes(batch, 16, heads, kv_heads, dim, max_q=16)     # and of fewer tokens
         self.workspace = dl.Workspace(max(attention, *(dl.workspace_bytes(*s) for s in shapes)), device)
 
     @staticmethod

@@ -398,7 +398,8 @@ dl_status dl_attention_paged(const dl_kv_cache* cache, const void* q, long long 
                              int q_heads, int max_q, float scale, void* workspace, size_t ws_bytes,
                              void* stream);
 
-/* Workspace bytes of dl_attention_paged on the current device (0: invalid sizes). */
+/* Workspace bytes on the current device of every dl_attention_paged with these heads and
+ * head_dim, any batch, and at most these tokens and max_q (0: invalid sizes). */
 size_t dl_attention_workspace_bytes(int batch, int tokens, int q_heads, int kv_heads, int head_dim,
                                     int max_q);
 

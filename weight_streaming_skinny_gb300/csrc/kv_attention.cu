@@ -60,8 +60,15 @@ extern "C" size_t dl_attention_workspace_bytes(int batch, int tokens, int q_head
     if (batch == 0 || tokens == 0 || max_q == 0) return DL_WORKSPACE_ZERO_BYTES;
     dl::HostDevice dev;
     if (dl::host_device(dev) != DL_OK) return 0;
-    const int rp = row_tiles(tokens, max_q, q_heads / kv_heads).padded;
-    return workspace_bytes(dev.sm_count * dl::attn_ctas_per_sm(rp, head_dim), rp, head_dim);
+    // a step of fewer tokens may need more (its instance has more CTAs or rows): the largest need of
+    // all up to max_q.  Steps of more than one row tile have the tiles of some step of one.
+    size_t most = 0;
+    for (int n = 1; n <= dl::kMaxRows && n <= tokens && n <= max_q; ++n) {
+        const int rp = row_tiles(tokens, n, q_heads / kv_heads).padded;
+        const size_t need = workspace_bytes(dev.sm_count * dl::attn_ctas_per_sm(rp, head_dim), rp, head_dim);
+        most = need > most ? need : most;
+    }
+    return most;
 }
 
 extern "C" dl_status dl_attention_paged(const dl_kv_cache* cache, const void* q, long long q_stride,
