@@ -29,3 +29,13 @@ def test_one_workspace_serves_every_smaller_step(cuda_device, dim, most, news):
         args = (step.q.to(cuda_device), step.cache(cuda_device), *step.seqs(cuda_device))
         a = dl.attention_paged(*args, max_q=n, workspace=ws)
         assert torch.equal(a, dl.attention_paged(*args, max_q=n))
+
+
+def test_a_workspace_of_another_device_is_refused(cuda_device):
+    """Its address would mean nothing on the cache's device."""
+    step = Step([40], [1], seed=9)
+    ws = object.__new__(dl.Workspace)
+    ws.tensor = torch.zeros(1 << 24, dtype=torch.uint8)
+    ws.nbytes, ws.addr = ws.tensor.numel(), ws.tensor.data_ptr()
+    with pytest.raises(ValueError, match="workspace is on cpu"):
+        dl.attention_paged(step.q.to(cuda_device), step.cache(cuda_device), *step.seqs(cuda_device), max_q=1, workspace=ws)

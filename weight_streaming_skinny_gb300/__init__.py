@@ -673,6 +673,8 @@ def attention_paged(q, cache: PagedKVCache, block_table, seq_lens, q_start, *, m
             workspace = _workspace(None, attention_workspace_bytes(
                 seq_lens.numel(), q.shape[0], q.shape[1], cache.kv_heads, cache.head_dim, max_q=max_q), cache.device,
                 stream)
+    elif workspace.tensor.device != cache.device:
+        raise ValueError(f"workspace is on {workspace.tensor.device}, expected {cache.device}")
     if not _call("attention", cache.device, *cache._args, q, block_table, seq_lens, q_start, max_q,
                  cache.head_dim ** -0.5 if scale is None else scale, out, out_lse, workspace.addr,
                  workspace.nbytes, stream):
