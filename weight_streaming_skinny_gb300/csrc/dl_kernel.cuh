@@ -1224,8 +1224,10 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ 
     }
     if constexpr (FAM == kTC) {
         // The accumulators of two stages (two units each) in tensor memory.
-        // One CTA per SM, so the columns are free; this warp frees them
-        // before the CTA exits, on every path.
+        // One CTA of this kernel per SM, and what attention CTAs of the next
+        // launch may hold by now leaves enough columns (asserted where those
+        // are launched); this warp frees them before the CTA exits, on every
+        // path.
         if (warp == kMmaWarp) tmem_alloc(smem_u32(tmem_slot), TcShape<MTB>::cols);
         tc_fence_before_sync();
     }

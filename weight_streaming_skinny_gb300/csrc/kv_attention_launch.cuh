@@ -3,12 +3,26 @@
 
 #include <atomic>
 
+#include "dl_kernel.cuh"
 #include "kv_attention.cuh"
 
 namespace dl {
 
+// Tensor memory that a linear of the tensor-memory family finds taken.  It lets the next launch start
+// before it allocates, and an attention CTA allocates before it waits for the linear: were there
+// too few columns left, each would wait for the other.  As many CTAs of C as fit into an SM's
+// shared memory beside a linear's smallest CTA (two stages) leave the columns that it takes.
+template <class C, int MT>
+constexpr bool leaves_tmem_to_linear() {
+    constexpr int sm_bytes = 228 * 1024, reserved = 1024;           // of shared memory, per CTA
+    constexpr int linear = smem_layout(kFP8, kTC, MT, 2).total + 1024 + reserved;
+    constexpr int beside = (sm_bytes - linear) / ((int)C::kSmem + reserved);
+    return (beside < C::kCtas ? beside : C::kCtas) * C::kTmem + TcShape<MT>::cols <= 512;
+}
+
 template <class C>
 cudaError_t launch_attention_instance(const AttnLaunch& a) {
+    static_assert(leaves_tmem_to_linear<C, 8>() && leaves_tmem_to_linear<C, 16>(), "columns for a linear on the same SM");
     static std::atomic<bool> ready[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
