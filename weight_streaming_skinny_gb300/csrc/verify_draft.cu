@@ -21,7 +21,7 @@ struct VerifyParams {
 // A cluster of CTAs takes one sequence, each warp a contiguous run of its vocabulary.
 // What bounds it: for many sequences the one read of p (and g) and the arithmetic on
 // it, for few the chain of dependent loads (draft token, its probabilities, the
-// row) and the cluster's two barriers: 6.05 us for one sequence of 152064 entries, 15 us
+// row) and the cluster's two barriers: 6.6 us for one sequence of 152064 entries, 15 us
 // for 48 (45 MB: 3.0 TB/s).  The first pass keeps the sums by CTA and warp, so that the drawn token is
 // found by reading one warp's run again, not the row.
 constexpr int kVerifyThreads = 512;
@@ -108,11 +108,13 @@ __device__ __forceinline__ long long warp_scan(long long w, int lane) {
     return w;
 }
 
-// GROUPS: groups of 128 entries that a warp has in flight.  Two, with registers for three CTAs
-// on an SM, whose other warps hide the rest; five where an SM has one CTA at most (one sequence of 152064
-// entries: 6.5 -> 6.05 us; 48 would take 27.6 us instead of 15).
-template <class T, int GROUPS>
-__global__ void __launch_bounds__(kVerifyThreads, GROUPS > 2 ? 1 : 3) verify_draft_kernel(const __grid_constant__ VerifyParams p) {
+// Groups of 128 entries that a warp has in flight: two, with registers for three CTAs on an SM, whose
+// other warps hide the rest.  (Four with registers for one CTA gain 1 to 5 % up to 7 sequences
+// of 32768 to 262144 entries, and lose a third from 8 on, where not all clusters find SMs of their own.)
+constexpr int kGroups = 2;
+
+template <class T>
+__global__ void __launch_bounds__(kVerifyThreads, 3) verify_draft_kernel(const __grid_constant__ VerifyParams p) {
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
     const int size = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -174,21 +176,21 @@ __global__ void __launch_bounds__(kVerifyThreads, GROUPS > 2 ? 1 : 3) verify_dra
         plain = pass == 1;              // nothing left of p - g: draw from p
         long long sum = 0;
         const int end = run_begin(warp + 1);
-        for (int i0 = run_begin(warp); i0 < end; i0 += 128 * GROUPS) {
-            float f[GROUPS][4] = {}, g[GROUPS][4] = {};
-            if (wide && i0 + 128 * GROUPS <= end) {
+        for (int i0 = run_begin(warp); i0 < end; i0 += 128 * kGroups) {
+            float f[kGroups][4] = {}, g[kGroups][4] = {};
+            if (wide && i0 + 128 * kGroups <= end) {
 #pragma unroll
-                for (int t = 0; t < GROUPS; ++t) load(std::true_type(), i0 + 128 * t + lane * 4, end, plain, f[t], g[t]);
+                for (int t = 0; t < kGroups; ++t) load(std::true_type(), i0 + 128 * t + lane * 4, end, plain, f[t], g[t]);
             } else {
 #pragma unroll
-                for (int t = 0; t < GROUPS; ++t) {
+                for (int t = 0; t < kGroups; ++t) {
                     const int i = i0 + 128 * t + lane * 4;
                     if (i < end) load(std::false_type(), i, end, plain, f[t], g[t]);
                 }
             }
-            int hi_sum = 0, lo_sum = 0;     // of 4 GROUPS entries
+            int hi_sum = 0, lo_sum = 0;     // of 4 kGroups entries
 #pragma unroll
-            for (int t = 0; t < GROUPS; ++t) {
+            for (int t = 0; t < kGroups; ++t) {
                 int hi[4], lo[4];
                 weigh(plain, f[t], g[t], hi, lo);
                 hi_sum += (hi[0] + hi[1]) + (hi[2] + hi[3]);
@@ -267,15 +269,22 @@ __global__ void __launch_bounds__(kVerifyThreads, GROUPS > 2 ? 1 : 3) verify_dra
     cluster.barrier_wait();
 }
 
-template <class T, int GROUPS>
-cudaError_t launch_verify_groups(const VerifyParams& p, int batch, int size, cudaStream_t stream) {
+template <class T>
+cudaError_t launch_verify(const VerifyParams& p, int batch, int sm_count, cudaStream_t stream) {
+    // CTAs of a sequence: a power of two, as many as leave three to each SM (48 sequences of
+    // 152064 entries: 15 us; two to each SM 17 us, one 22 us), at most 16, a cluster (one sequence:
+    // 6.6 us; 8 take 7.1), each warp with 128 entries at least
+    int size = 1;
+    while (size < kMaxCluster && (long long)batch * size * 2 <= 3LL * sm_count &&
+           size * kVerifyWarps * 128 < p.vocab)
+        size *= 2;
     static std::atomic<bool> ready[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!ready[dev].load()) {
-        e = cudaFuncSetAttribute(verify_draft_kernel<T, GROUPS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        e = cudaFuncSetAttribute(verify_draft_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
         ready[dev].store(true);
     }
@@ -292,20 +301,7 @@ cudaError_t launch_verify_groups(const VerifyParams& p, int batch, int size, cud
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, verify_draft_kernel<T, GROUPS>, p);
-}
-
-template <class T>
-cudaError_t launch_verify(const VerifyParams& p, int batch, int sm_count, cudaStream_t stream) {
-    // CTAs of a sequence: a power of two, as many as leave three to each SM (48 sequences of
-    // 152064 entries: 15 us; two to each SM 17 us, one 22 us), at most 16, a cluster (one sequence:
-    // 6.5 us; 8 take 7.1), each warp with 128 entries at least
-    int size = 1;
-    while (size < kMaxCluster && (long long)batch * size * 2 <= 3LL * sm_count &&
-           size * kVerifyWarps * 128 < p.vocab)
-        size *= 2;
-    return (long long)batch * size <= sm_count ? launch_verify_groups<T, 5>(p, batch, size, stream)
-                                               : launch_verify_groups<T, 2>(p, batch, size, stream);
+    return cudaLaunchKernelEx(&cfg, verify_draft_kernel<T>, p);
 }
 
 }  // namespace dl
