@@ -142,6 +142,14 @@ static int current(long long dev) {
     return g_get_device(&now) == 0 && now == dev;
 }
 
+/* The library's calls: other Python threads run meanwhile (a launch waits where the driver's queue is full). */
+#define CALL(status, call)     \
+    do {                       \
+        Py_BEGIN_ALLOW_THREADS \
+        status = (call);       \
+        Py_END_ALLOW_THREADS \
+    } while (0)
+
 static PyObject* answer(long code) {
     if (code == LOOK) PyErr_Clear();
     return PyLong_FromLong(code);
@@ -167,9 +175,11 @@ static PyObject* attention(PyObject* self, PyObject* const* a, Py_ssize_t n) {
         return answer(LOOK);
     (void)heads;
     if (!current(dev)) return answer(OTHER_DEVICE);
-    return answer(g_attention((const dl_kv_cache*)cache, q.ptr, step, o.ptr, (float*)e.ptr, (const int*)t.ptr, (int)t.shape[1],
-                              (const int*)l.ptr, (const int*)s.ptr, (int)t.shape[0], (int)q.shape[0], (int)q.shape[1],
-                              (int)max_q, (float)scale, (void*)ws, (size_t)bytes, stream));
+    dl_status status;
+    CALL(status, g_attention((const dl_kv_cache*)cache, q.ptr, step, o.ptr, (float*)e.ptr, (const int*)t.ptr, (int)t.shape[1],
+                             (const int*)l.ptr, (const int*)s.ptr, (int)t.shape[0], (int)q.shape[0], (int)q.shape[1],
+                             (int)max_q, (float)scale, (void*)ws, (size_t)bytes, stream));
+    return answer(status);
 }
 
 /* append(cache, device, kv_heads, dim, q, k, v, table, lens, start, max_q, cos, sin, positions, out, stream) */
@@ -205,10 +215,12 @@ static PyObject* append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
         !stream_of(a[15], dev, &stream))
         return answer(LOOK);
     if (!current(dev)) return answer(OTHER_DEVICE);
-    return answer(g_append((const dl_kv_cache*)cache, q.ptr, k.ptr, v.ptr, qs, ks, vs, o.ptr, (const float*)c.ptr,
-                           (const float*)i.ptr, (int)rotary, (int)places, (const int*)p.ptr, (const int*)t.ptr,
-                           (int)t.shape[1], (const int*)l.ptr, (const int*)s.ptr, (int)t.shape[0], (int)k.shape[0],
-                           (int)q_heads, (int)max_q, stream));
+    dl_status status;
+    CALL(status, g_append((const dl_kv_cache*)cache, q.ptr, k.ptr, v.ptr, qs, ks, vs, o.ptr, (const float*)c.ptr,
+                          (const float*)i.ptr, (int)rotary, (int)places, (const int*)p.ptr, (const int*)t.ptr,
+                          (int)t.shape[1], (const int*)l.ptr, (const int*)s.ptr, (int)t.shape[0], (int)k.shape[0],
+                          (int)q_heads, (int)max_q, stream));
+    return answer(status);
 }
 
 /* verify(device, drafts, target, u, u_next, draft_probs, draft_lens, tokens, count, stream) */
@@ -235,9 +247,11 @@ static PyObject* verify(PyObject* self, PyObject* const* a, Py_ssize_t n) {
         numel(&c) != B || !fits(B) || !fits(S) || !fits(t.shape[2]) || !stream_of(a[9], dev, &stream))
         return answer(LOOK);
     if (!current(dev)) return answer(OTHER_DEVICE);
-    return answer(g_verify((const int*)d.ptr, g.ptr, t.ptr, kind == g_f32 ? DL_PROBS_F32 : DL_PROBS_BF16, (const float*)u.ptr,
-                           (const float*)x.ptr, (const int*)l.ptr, (int*)k.ptr, (int*)c.ptr, (int)B, (int)S,
-                           (int)t.shape[2], stream));
+    dl_status status;
+    CALL(status, g_verify((const int*)d.ptr, g.ptr, t.ptr, kind == g_f32 ? DL_PROBS_F32 : DL_PROBS_BF16, (const float*)u.ptr,
+                          (const float*)x.ptr, (const int*)l.ptr, (int*)k.ptr, (int*)c.ptr, (int)B, (int)S,
+                          (int)t.shape[2], stream));
+    return answer(status);
 }
 
 /* bind(Tensor, bfloat16, int32, float32, raw_stream, get_device, append, attention, verify): types, and addresses */
