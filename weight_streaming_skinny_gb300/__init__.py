@@ -527,10 +527,12 @@ class PagedKVCache:
                 raise TypeError(f"{n} must be a torch.Tensor")
             if not t.is_cuda or t.device != k.device:
                 raise ValueError("the cache must be CUDA tensors of one device (there is no CPU path)")
+        # one page, or one head, has no next one: its stride says nothing
+        steps = lambda t: [s for s, n in zip(t.stride(), t.shape) if n != 1]   # noqa: E731
         for t, n in ((k, "k"), (v, "v")):
             if t.dtype not in (torch.uint8, torch.float8_e4m3fn):
                 raise ValueError(f"{n} must be e4m3 codes (uint8 or float8_e4m3fn), got {t.dtype}")
-            if t.dim() != 4 or t.shape != k.shape or t.stride() != k.stride():
+            if t.dim() != 4 or t.shape != k.shape or steps(t) != steps(k):
                 raise ValueError("k and v must be [num_pages, kv_heads, page_size, head_dim] with equal strides")
             if t.numel() and (t.stride(3) != 1 or t.stride(2) != t.shape[3]):
                 raise ValueError(f"a page of {n} must be dense in its tokens and dims")
@@ -538,7 +540,7 @@ class PagedKVCache:
         for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
             if t.dtype != torch.float32:
                 raise ValueError(f"{n} must be torch.float32, got {t.dtype}")
-            if t.dim() != 3 or t.shape != k_scale.shape or t.stride() != k_scale.stride() or \
+            if t.dim() != 3 or t.shape != k_scale.shape or steps(t) != steps(k_scale) or \
                     t.shape[:2] != (pages, heads) or t.shape[2] < 1 or page % t.shape[2]:
                 raise ValueError("k_scale and v_scale must be [num_pages, kv_heads, page_size // block] "
                                  "with equal strides")
@@ -548,8 +550,12 @@ class PagedKVCache:
         self.num_pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, page, dim
         self.block = page // k_scale.shape[2]
         self.device = k.device
+        blocks = k_scale.shape[2]
         self._struct = _KVCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                                k.stride(0), k.stride(1), k_scale.stride(0), k_scale.stride(1),
+                                k.stride(0) if pages > 1 else heads * page * dim,
+                                k.stride(1) if heads > 1 else page * dim,
+                                k_scale.stride(0) if pages > 1 else heads * blocks,
+                                k_scale.stride(1) if heads > 1 else blocks,
                                 pages, heads, page, dim, self.block)
         # what a call passes of it: its description's address, its device, heads and dims
         self._args = (ctypes.addressof(self._struct), self.device.index, heads, dim)
