@@ -327,7 +327,7 @@ typedef struct dl_kv_cache {
     void* v;                     /*   dim d) at p*page_stride + h*head_stride + t*head_dim + d */
     float* k_scale;              /* (p, h, block c) at p*scale_page_stride                 */
     float* v_scale;              /*   + h*scale_head_stride + c; finite, >= 0 (v_scale below
-                                      2^-60 counts as 0); 4-byte aligned                   */
+                                      2^-60 counts as 0; a NaN code stays NaN); 4-byte aligned */
     long long page_stride;       /* bytes, multiples of 16                                 */
     long long head_stride;
     long long scale_page_stride; /* elements                                               */

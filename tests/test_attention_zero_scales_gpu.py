@@ -66,3 +66,24 @@ def test_nothing_but_zero_scales(cuda_device):
     got, lse = run(step, cuda_device)
     assert not got.any()
     assert ((lse - want_lse).abs() <= 1e-4 + 1e-5 * want_lse.abs()).all()
+
+
+@pytest.mark.parametrize("group,news", [(8, 1), (8, 2), (8, 4), (8, 6), (8, 8)])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("at", ["past", "new"])
+def test_a_nan_code_of_zero_scale_is_nan(cuda_device, group, news, dim, at):
+    """NaN times zero, as a quantiser leaves it that divides by the largest finite value of a block
+    without one: every row that sees the token has a NaN there, and no other."""
+    step = Step([140], [news], heads=group, kv_heads=1, dim=dim, page=16, block=1, seed=news)
+    j = 131 if at == "past" else 140 - (news + 1) // 2
+    p, o = step.slots(0, 140)[j]
+    step.v_scale[p, 0, o] = 0
+    step.v[p, 0, o] = torch.zeros(dim).to(step.v.dtype)
+    want = reference(step)[0]
+    step.v.view(torch.uint8)[p, 0, o, 37] = 0xff
+    got, _ = run(step, cuda_device)
+    first = max(j - (140 - news), 0)                        # the first new token that sees it
+    nan = torch.isnan(got)
+    assert nan[first:, :, 37].all() and nan.sum() == (news - first) * group
+    got[first:, :, 37] = want[first:, :, 37]
+    assert (got - want).norm() / want.norm() < RMS

@@ -963,14 +963,14 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
 
                 wait.after(s_ok, smem_u32(s_full + (it & 1)), (it >> 1) & 1, kErrConsumerWait);
                 tc_fence_after_sync();
-                // values that do not count are taken out: all of an absent token or of a zero scale, and NaN
-                // codes of the new tokens (0 x NaN would reach every row), which are noted by dim
+                // values that do not count are taken out: all of an absent token, those of a zero scale that
+                // are not NaN, and NaN codes of the new tokens (0 x NaN would reach every row), which are noted by dim
                 if (__builtin_expect(masked && (empty || j >= seen_first), 0)) {
                     unsigned char* codes = values + vt.slot * C::kTileBytes + tl * D;
 #pragma unroll 1
                     for (int c = wg % CG; c < D / 16; c += CG) {
                         uint4* at = reinterpret_cast<uint4*>(codes + c * 16);
-                        if (empty) {
+                        if (absent) {
                             *at = make_uint4(0, 0, 0, 0);
                             continue;
                         }
@@ -979,14 +979,17 @@ attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                         uint32_t any = 0;
 #pragma unroll
                         for (int k = 0; k < 4; ++k) any |= (word[k] & 0x7f7f7f7fu) + 0x01010101u;
-                        if (!(any & 0x80808080u)) continue;
+                        if (!(any & 0x80808080u)) {
+                            if (empty) *at = make_uint4(0, 0, 0, 0);
+                            continue;
+                        }
                         const int dims = (D == 128 ? (c ^ (tl & 7)) : (c ^ ((tl >> 1) & 3))) * 16;
 #pragma unroll 1
                         for (int k = 0; k < 16; ++k) {
                             unsigned char* byte = codes + c * 16 + k;
-                            if ((*byte & 0x7f) != 0x7f) continue;
-                            *byte = 0;
-                            atomicMin(s_nan + buf * D + dims + k, j);
+                            const bool nan = (*byte & 0x7f) == 0x7f;
+                            if (nan && j >= seen_first) atomicMin(s_nan + buf * D + dims + k, j);
+                            if (nan ? j >= seen_first : empty) *byte = 0;
                         }
                     }
                 }
