@@ -315,7 +315,9 @@ int dl_graph_cache_size(void);
  * range are contained, not reported: q_start is taken inside [0, tokens],
  * seq_lens inside [0, table_cols * page_size], tokens of a page outside
  * [0, num_pages) count as absent, and of a sequence with more than max_q new
- * tokens only the first max_q are worked on.
+ * tokens only the first max_q are worked on.  A call looks at batch * max_q places
+ * for new tokens: a prompt among many decoding sequences is better off in a call
+ * of its own.
  *
  * Unlike the linear layers, q, k and v may be views of a wider row (the fused
  * QKV projection's output): q_stride, k_stride, v_stride are elements from one
@@ -388,7 +390,8 @@ dl_status dl_kv_append(const dl_kv_cache* cache, const void* q, const void* k, c
  *   lse    fp32 [tokens][q_heads] or NULL: log sum_j exp(scale * q . K_j)
  *          (-inf where nothing is seen)
  *   scale  usually D^-1/2
- *   q_heads a multiple of num_heads, q_heads / num_heads <= 128
+ *   q_heads a multiple of num_heads, q_heads / num_heads <= 128 (beyond 64 the
+ *          fewest equal parts of at most 64, each of which reads the cache)
  *   workspace, ws_bytes: at least dl_attention_workspace_bytes(...), zero
  *          prefix as for the linear layers; one workspace serves both.
  */

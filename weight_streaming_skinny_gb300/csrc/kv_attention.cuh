@@ -39,9 +39,9 @@
 // with the join: up to 16 rows the read of the cache (64 sequences of up to 16384
 // tokens, 1.6 GB: 243 to 246 us, 6.6 TB/s, 0.97 of a copy's rate; 32 of up to 4096: 40 us, 5.1 TB/s),
 // or, where there is little of it, a chain of latencies (one sequence of 500 tokens
-// 7.4 us, of 30011 tokens 18 us).  Beyond, the softmax's instructions, about 620 a
-// warp and tile at 64 rows (4 x 32768 tokens, 16 new ones each: 126.5 us, 2.1 TB/s;
-// 16 x up to 8192 with 6: 58 us, 3.5 TB/s).
+// 7.5 us, of 30011 tokens 18 us).  Beyond, the softmax's instructions, about 610 a
+// warp and tile at 64 rows (4 x 32768 tokens, 16 new ones each: 126.7 us, 2.1 TB/s;
+// 16 x up to 8192 with 6: 59 us, 3.5 TB/s).
 #pragma once
 
 #include <type_traits>
