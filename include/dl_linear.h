@@ -61,7 +61,7 @@
 extern "C" {
 #endif
 
-#define DL_VERSION 4
+#define DL_VERSION 5
 
 /* Leading workspace bytes that must be zero before a call (see conventions). */
 #define DL_WORKSPACE_ZERO_BYTES (256u + 16384u * 4u)
@@ -434,6 +434,155 @@ dl_status dl_verify_draft(const int* draft_tokens, const void* draft_probs,
                           const void* target_probs, int probs_dtype, const float* u_accept,
                           const float* u_next, const int* draft_lens, int* tokens, int* count,
                           int batch, int drafts, int vocab, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Around the linears of a decode step of many requests: norms, adapters, and
+ * whose pages of the cache are.
+ *
+ * Rows of elements that these read and write; NULL, or data NULL: none.
+ * ---------------------------------------------------------------------------
+ */
+#define DL_ROWS_BF16 0
+#define DL_ROWS_F32 1
+typedef struct dl_rows {
+    void* data;          /* aligned to its type                                           */
+    long long stride;    /* elements from one row to the next, >= a row's; a row is dense */
+    int dtype;           /* DL_ROWS_BF16 or DL_ROWS_F32                                   */
+} dl_rows;
+
+/* N(v) = c / sqrt(mean(c^2) + eps) * (offset + weight) + bias over a row, with c = v
+ * (DL_NORM_RMS) or c = v - mean(v) (DL_NORM_LAYER). */
+#define DL_NORM_NONE 0
+#define DL_NORM_RMS 1
+#define DL_NORM_LAYER 2
+typedef struct dl_norm {
+    const void* weight;  /* [dim] or NULL: offset + weight counts as 1 */
+    const void* bias;    /* [dim] or NULL: 0                           */
+    float eps;           /* >= 0                                       */
+    float offset;        /* 1 where weights are stored as differences from 1 */
+    int kind;
+    int dtype;           /* of weight and bias: DL_ROWS_BF16 or DL_ROWS_F32 */
+} dl_norm;
+
+/*
+ * The end of one block and the start of the next:
+ *     u = post(y);  r = h_scale * h + scale * act(gate) * u;  x = pre(r)
+ * over rows [rows][dim], 1 <= dim <= 32768, all in fp32; h_out gets r and x_out gets
+ * x (or r, without pre), each rounded once: x is taken from r before that is rounded.
+ *   y, h   [rows][dim]; one of them may be missing (counts as zero)
+ *   post, pre  NULL or kind DL_NORM_NONE: the identity
+ *   gate   DL_GATE_ROW [rows][1], DL_GATE_CHANNEL [1][dim], DL_GATE_FULL [rows][dim];
+ *          gate_act DL_GATE_SIGMOID: 1 / (1 + exp(-gate))
+ *   h_out, x_out  [rows][dim]; one of them may be missing.  Each may be y or h
+ *          itself (the same rows, stride and type); they overlap nothing else.
+ * A square that leaves fp32's range does not: such rows are summed scaled.  NaN and
+ * infinities give what the formulas give, in their row only.
+ */
+#define DL_GATE_NONE 0
+#define DL_GATE_ROW 1
+#define DL_GATE_CHANNEL 2
+#define DL_GATE_FULL 3
+#define DL_GATE_PLAIN 0
+#define DL_GATE_SIGMOID 1
+dl_status dl_block_norm(const dl_rows* y, const dl_norm* post, const dl_rows* gate, int gate_kind,
+                        int gate_act, float scale, const dl_rows* h, float h_scale,
+                        const dl_norm* pre, const dl_rows* h_out, const dl_rows* x_out, int rows,
+                        int dim, void* stream);
+
+/*
+ * Low-rank adapters, all of one store and shape, for one projection K -> N (or
+ * for several that lie side by side in N, `parts` of them with first products of their
+ * own: queries, keys and values of a fused projection).
+ */
+typedef struct dl_adapters {
+    const void* a;       /* bf16 [num][parts * rank][K], 16-byte aligned                   */
+    const void* b;       /* bf16 [num][N][rank], 16-byte aligned                           */
+    const float* scale;  /* [num] or NULL: 1                                               */
+    const int* ranks;    /* [num] or NULL: rank.  Adapter i uses the first ranks[i] (taken
+                            inside [0, rank]) of each part's rows of a and of b's columns;
+                            what the others hold, NaN included, reaches nothing            */
+    int num;             /* 1 .. 16384                                                     */
+    int rank;            /* a multiple of 8, 8 .. 256                                      */
+    int K;               /* a multiple of 8                                                */
+    int N;
+    int parts;           /* 1 .. 8                                                         */
+    int part_end[8];     /* columns before part i's end: multiples of 16 but the last, N   */
+} dl_adapters;
+
+/*
+ * y[t][n] = base[t][n] + scale_a * sum_{r < ranks_a} b_a[n][r] * (a_a[p * rank + r] . x[t]),
+ * a = index[t], p the part that holds n.  A token whose index is outside [0, num) has no
+ * adapter: its row of y is base (left as it is where base is y).
+ *   x      bf16 [tokens][K], rows 16-byte aligned
+ *   index  int32 [tokens], in any order
+ *   base   [tokens][N], bf16 or fp32 (a linear's y or y_f32), or missing: 0
+ *   y      bf16 [tokens][N], rounded once; y_f32 fp32 [tokens][N] or missing: the value
+ *          before that.  Each may be base itself; they overlap nothing else.
+ * Sums are fp32, over tokens one by one: what a token gets does not depend on the
+ * others.  First products go into the second ones as fp32 rounded to 2^-18 of their value,
+ * whole where y_f32 is asked for.
+ *   tokens any number; workspace: dl_adapters_workspace_bytes(...), zero prefix as
+ *   for the linear layers (not used); one workspace serves all.
+ */
+dl_status dl_linear_adapters(const dl_adapters* adapters, const dl_rows* x, const int* index,
+                             const dl_rows* base, const dl_rows* y, const dl_rows* y_f32,
+                             int tokens, void* workspace, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of every dl_linear_adapters with these adapters and at most these
+ * tokens (0: invalid sizes). */
+size_t dl_adapters_workspace_bytes(int tokens, int num, int rank, int parts);
+
+/*
+ * Whose pages are: the state that goes with the paged caches of all layers.  It lies
+ * on the device and every call below changes it there, so a step needs no host copy of it.
+ *   refs[p]  how many rows' tables name page p; <= 0: the page is free
+ *   row b's first ceil(seq_lens[b] / page_size) table entries are its pages
+ * Row and page numbers out of range are contained: such an item is refused, such a page
+ * is absent and is neither counted nor copied.  Lengths are taken inside
+ * [0, table_cols * page_size].  Pages are taken from the lowest free number on, for the
+ * items of a list in their order: from the first that finds too few left on, those that
+ * need any are refused.  done[i] is 1 if item i was served, 0 if it was refused (its row
+ * is as it was).  A row that a list names twice is served at the first place, refused at
+ * the others.
+ */
+typedef struct dl_kv_pages {
+    const dl_kv_cache* caches;   /* HOST array, one of each layer: num_pages and page_size as
+                                    here, the other sizes alike; may be NULL (no caches) */
+    int* refs;                   /* [num_pages]         */
+    int* block_table;            /* [rows][table_cols]  */
+    int* seq_lens;               /* [rows]              */
+    int num_caches, num_pages, page_size;
+    int rows, table_cols;        /* rows <= 16384       */
+} dl_kv_pages;
+
+/* Give the pages of `n` <= rows listed rows back: their counts fall by one (not below
+ * 0) and the rows' lengths become 0; the tables stay.  rows is a device array, as all lists are. */
+dl_status dl_kv_free(const dl_kv_pages* pages, const int* rows, int n, void* stream);
+
+/*
+ * Row children[i] becomes a copy of row parents[i]: full pages are shared (their
+ * counts rise), a page that is begun is copied, in every cache, as far as it is filled, so
+ * that both may append.  children[i] must be empty (seq_lens <= 0) and another row, else
+ * the item is refused; parents[i] may be listed several times.
+ */
+dl_status dl_kv_fork(const dl_kv_pages* pages, const int* parents, const int* children, int* done,
+                     int n, void* workspace, size_t ws_bytes, void* stream);
+
+/* Room for tokens[i] >= 0 more tokens in row rows[i]: its length grows by that, and pages are
+ * taken for what does not fit its last one (before dl_kv_append, whose seq_lens count the new
+ * tokens). */
+dl_status dl_kv_reserve(const dl_kv_pages* pages, const int* rows, const int* tokens, int* done,
+                        int n, void* workspace, size_t ws_bytes, void* stream);
+
+/* Pages in use move to the front: with live[0] of them, those numbered live[0] and more go, in
+ * order, to the free pages before; contents in every cache, counts and tables follow. */
+dl_status dl_kv_compact(const dl_kv_pages* pages, int* live, void* workspace, size_t ws_bytes,
+                        void* stream);
+
+/* Workspace bytes of the three calls above for a pool (0: invalid sizes); zero prefix as for
+ * the linear layers (not used). */
+size_t dl_kv_pages_workspace_bytes(int num_pages, int rows);
 
 /*
  * Process-wide tuning overrides, for tests and tuning; 0 = automatic.

@@ -25,7 +25,8 @@ __all__ = [
     "linear_fp8_block128", "decode_stream", "decode_stream_workspace_bytes",
     "decode_stream_launches", "graph_cache_clear", "graph_cache_size", "set_wait_test",
     "set_override", "PagedKVCache", "kv_append", "attention_paged", "attention_workspace_bytes",
-    "verify_draft",
+    "verify_draft", "Norm", "block_norm", "Adapters", "adapters_workspace_bytes", "linear_adapters",
+    "PagePool", "pages_workspace_bytes", "kv_free", "kv_reserve", "kv_fork", "kv_compact",
     "device_status", "exported_symbols", "header_symbols",
 ]
 
@@ -67,7 +68,25 @@ class _KVCache(ctypes.Structure):
                 ("head_dim", ctypes.c_int), ("block", ctypes.c_int)]
 
 
-ABI_VERSION = 4   # DL_VERSION this binding marshals for
+
+class _Norm(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("offset", ctypes.c_float), ("kind", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
+class _Adapters(ctypes.Structure):
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("ranks", ctypes.c_void_p), ("num", ctypes.c_int), ("rank", ctypes.c_int), ("K", ctypes.c_int),
+                ("N", ctypes.c_int), ("parts", ctypes.c_int), ("part_end", ctypes.c_int * 8)]
+
+
+class _KVPages(ctypes.Structure):
+    _fields_ = [("caches", ctypes.POINTER(_KVCache)), ("refs", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("seq_lens", ctypes.c_void_p), ("num_caches", ctypes.c_int), ("num_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("rows", ctypes.c_int), ("table_cols", ctypes.c_int)]
+
+
+ABI_VERSION = 5   # DL_VERSION this binding marshals for
 
 
 def library_path() -> str:
@@ -111,6 +130,10 @@ def load():
         lib.dl_linear_swiglu.restype = i
         lib.dl_attention_workspace_bytes.argtypes = [i, i, i, i, i, i]
         lib.dl_attention_workspace_bytes.restype = sz
+        lib.dl_adapters_workspace_bytes.argtypes = [i, i, i, i]
+        lib.dl_adapters_workspace_bytes.restype = sz
+        lib.dl_kv_pages_workspace_bytes.argtypes = [i, i]
+        lib.dl_kv_pages_workspace_bytes.restype = sz
         lib.dl_set_override.argtypes = [i, i, i]
         lib.dl_set_override.restype = i
         lib.dl_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint)]
@@ -123,7 +146,10 @@ def load():
         _binding.bind(torch.Tensor, torch.bfloat16, torch.int32, torch.float32,
                       torch._C._cuda_getCurrentRawStream, address(lib.cudaGetDevice),
                       address(lib.dl_kv_append), address(lib.dl_attention_paged), address(lib.dl_verify_draft))
-        _native.update(append=_binding.append, attention=_binding.attention, verify=_binding.verify)
+        _binding.bind_more(address(lib.dl_block_norm), address(lib.dl_linear_adapters), address(lib.dl_kv_free),
+                           address(lib.dl_kv_reserve), address(lib.dl_kv_fork), address(lib.dl_kv_compact))
+        _native.update(append=_binding.append, attention=_binding.attention, verify=_binding.verify,
+                       norm=_binding.norm, adapters=_binding.adapters, pages=_binding.pages)
         _lib = lib
         return lib
 
@@ -758,6 +784,303 @@ def _explain_verify(draft_tokens, target_probs, u_accept, u_next, draft_probs, d
     if out_tokens.numel() != B * (S + 1) or out_count.numel() != B:
         raise ValueError("out_tokens must be [batch, drafts + 1] and out_count [batch]")
     raise ValueError("stream must be an integer or a stream, sizes below 2^31")
+
+
+_NORMS = {"rms": 1, "layer": 2}
+
+
+def _need_vector(t, name, device, shape, dtypes):
+    """A contiguous CUDA tensor of one of `dtypes` and of `shape`, on `device` (None: any)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    _need(t, name, t.dtype, device)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+class Norm:
+    """A norm of block_norm: c / sqrt(mean(c^2) + eps) * (offset + weight) + bias over a row, with
+    c = v (kind "rms") or v - mean(v) ("layer").  weight, bias: bf16 or fp32 [dim], both of one type, or
+    None; offset=1 where weights are stored as differences from 1.  Made once; it holds its tensors."""
+
+    def __init__(self, weight=None, bias=None, *, kind="rms", eps=1e-6, offset=0.0):
+        if kind not in _NORMS:
+            raise ValueError(f"kind must be 'rms' or 'layer', got {kind!r}")
+        first = weight if weight is not None else bias
+        for t, n in ((weight, "weight"), (bias, "bias")):
+            if t is not None:
+                _need_vector(t, n, None if t is first or not isinstance(first, torch.Tensor) else first.device,
+                             first.shape[:1] if isinstance(first, torch.Tensor) else (),
+                             (torch.bfloat16, torch.float32))
+                if t.dtype != first.dtype:
+                    raise ValueError("weight and bias must be of one type")
+        self.weight, self.bias, self.kind, self.eps, self.offset = weight, bias, kind, float(eps), float(offset)
+        self._struct = _Norm(None if weight is None else weight.data_ptr(), None if bias is None else bias.data_ptr(),
+                             self.eps, self.offset, _NORMS[kind],
+                             1 if first is not None and first.dtype == torch.float32 else 0)
+        self._args = (ctypes.addressof(self._struct), -1 if first is None else first.shape[0],
+                      -1 if first is None else first.device.index)
+
+
+_GATE_ACTS = {None: 0, "sigmoid": 1}
+
+
+def block_norm(y, h=None, *, post: Norm | None = None, pre: Norm | None = None, gate=None, gate_act=None,
+               scale=1.0, h_scale=1.0, out_h=None, out_x=None, stream=None):
+    """(r, x): r = h_scale * h + scale * act(gate) * post(y) and x = pre(r), the end of one block and the
+    start of the next.
+
+    y (a block's output) and h (the residual stream): bf16 or fp32 [rows, dim], any stride between
+    rows; one of them may be None.  gate: bf16 or fp32 [dim], [rows, 1] or [rows, dim]; gate_act None or
+    "sigmoid".  Results go to out_h and out_x, which may be h or y; those not given are made: r like h
+    (like y without h; without y the stream does not change and r is None), x in bf16 where there
+    is a `pre`.  See dl_block_norm.
+    """
+    like = h if h is not None else y
+    if not isinstance(like, torch.Tensor):
+        raise TypeError("y or h must be a torch.Tensor")
+    if out_h is None and y is not None:
+        out_h = torch.empty_like(like, memory_format=torch.contiguous_format) if stream is None else \
+            _empty(like.shape, like.dtype, like.device, stream)
+    if out_x is None and (pre is not None or y is None):
+        out_x = torch.empty_like(like, dtype=torch.bfloat16, memory_format=torch.contiguous_format) \
+            if stream is None else _empty(like.shape, torch.bfloat16, like.device, stream)
+    index = like.get_device()
+    if index < 0 or gate_act not in _GATE_ACTS or \
+            not _call("norm", like.device, index, y, None if post is None else post._args, gate, _GATE_ACTS[gate_act],
+                      scale, h, h_scale, None if pre is None else pre._args, out_h, out_x, stream):
+        _explain_norm(y, h, post, pre, gate, gate_act, out_h, out_x)
+    return out_h, out_x
+
+
+def _need_matrix(t, name, device, shape=None, dtypes=(torch.bfloat16, torch.float32)):
+    """Rows of bf16 or fp32, a row dense."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{name} must be a CUDA tensor{'' if device is None else f' on {device}'} (there is no CPU path)")
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} must be {'[rows, dim]' if shape is None else list(shape)}, got {list(t.shape)}")
+    if t.shape[0] and t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"a row of {name} must be dense")
+
+
+def _explain_norm(y, h, post, pre, gate, gate_act, out_h, out_x):
+    """Raise for the first argument of a block_norm call that is not in order."""
+    like = y if y is not None else h
+    _need_matrix(like, "y" if y is not None else "h", None)
+    dev, shape = like.device, like.shape
+    for t, n in ((h, "h"), (out_h, "out_h"), (out_x, "out_x")):
+        if t is not None:
+            _need_matrix(t, n, dev, shape)
+    for n, name in ((post, "post"), (pre, "pre")):
+        if n is not None and (n._args[1] not in (-1, shape[1]) or n._args[2] not in (-1, dev.index)):
+            raise ValueError(f"{name}'s weights must be [{shape[1]}] on {dev}")
+    if gate_act not in _GATE_ACTS:
+        raise ValueError(f"gate_act must be None or 'sigmoid', got {gate_act!r}")
+    if gate is not None:
+        if not isinstance(gate, torch.Tensor) or tuple(gate.shape) not in ((shape[1],), (shape[0], 1), tuple(shape)):
+            raise ValueError("gate must be a tensor [dim], [rows, 1] or [rows, dim]")
+        if gate.dim() == 1:
+            _need_vector(gate, "gate", dev, shape[1:], (torch.bfloat16, torch.float32))
+        else:
+            _need_matrix(gate, "gate", dev)
+    raise ValueError("scale and h_scale must be numbers, stream an integer or a stream, sizes below 2^31")
+
+
+class Adapters:
+    """Low-rank adapters of one projection K -> N (see dl_adapters in dl_linear.h).
+
+    a       bf16 [num, parts * rank, K], b  bf16 [num, N, rank]: the store
+    scale   fp32 [num] or None (1); ranks  int32 [num] or None: how many of the `rank` rows and columns of
+            each adapter are its own
+    parts   columns of each of several projections that lie side by side in N, each with its own rows of a
+            (None: one projection)
+
+    The object holds the tensors and is made once; what they hold may change between calls.
+    """
+
+    def __init__(self, a, b, *, scale=None, ranks=None, parts=None):
+        for t, n in ((a, "a"), (b, "b")):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{n} must be a torch.Tensor")
+            _need(t, n, torch.bfloat16, None if t is a else a.device)
+        if a.dim() != 3 or b.dim() != 3 or b.shape[0] != a.shape[0]:
+            raise ValueError("a must be [num, parts * rank, K] and b [num, N, rank]")
+        num, N, rank = b.shape
+        parts = [N] if parts is None else [int(c) for c in parts]
+        if sum(parts) != N or a.shape[1] != len(parts) * rank:
+            raise ValueError("the columns of parts must add up to N, and a must have rank rows for each part")
+        if not 1 <= len(parts) <= 8:
+            raise ValueError("there must be 1 to 8 parts")
+        if scale is not None:
+            _need_vector(scale, "scale", a.device, (num,), (torch.float32,))
+        if ranks is not None:
+            _need_vector(ranks, "ranks", a.device, (num,), (torch.int32,))
+        self.a, self.b, self.scale, self.ranks, self.parts, self.device = a, b, scale, ranks, parts, a.device
+        self.num, self.rank, self.K, self.N = num, rank, a.shape[2], N
+        ends = [sum(parts[:i + 1]) for i in range(len(parts))]
+        self._struct = _Adapters(a.data_ptr(), b.data_ptr(), None if scale is None else scale.data_ptr(),
+                                 None if ranks is None else ranks.data_ptr(), num, rank, self.K, N, len(parts),
+                                 (ctypes.c_int * 8)(*ends))
+        self._args = (ctypes.addressof(self._struct), a.device.index, self.K, N)
+
+
+def adapters_workspace_bytes(tokens: int, adapters: Adapters) -> int:
+    """Workspace linear_adapters needs for up to `tokens` tokens (0 = invalid sizes)."""
+    return int(load().dl_adapters_workspace_bytes(tokens, adapters.num, adapters.rank, len(adapters.parts)))
+
+
+def linear_adapters(x, adapters: Adapters, index, base=None, *, out=None, out_f32=None,
+                    workspace: Workspace | None = None, stream=None):
+    """out[t] = base[t] + scale_a * (x[t] a_a^T) b_a^T with a = index[t]: each token's own adapter
+    beside a projection that they share.
+
+    x bf16 [tokens, K]; index int32 [tokens], in any order (outside [0, num): no adapter); base
+    bf16 or fp32 [tokens, N], the projection's output, or None (0).  Returns out, bf16 [tokens, N];
+    out_f32 gets the values before rounding.  Each may be base itself.  See dl_linear_adapters.
+    """
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    if out is None:
+        _need_matrix(x, "x", adapters.device, dtypes=(torch.bfloat16,))
+        out = _empty((x.shape[0], adapters.N), torch.bfloat16, adapters.device, stream)
+    if workspace is None:
+        _explain_adapters(x, adapters, index, base, out, out_f32)
+        with torch.cuda.device(adapters.device):
+            workspace = _workspace(None, adapters_workspace_bytes(x.shape[0], adapters), adapters.device, stream)
+    elif workspace.tensor.device != adapters.device:
+        raise ValueError(f"workspace is on {workspace.tensor.device}, expected {adapters.device}")
+    if not _call("adapters", adapters.device, adapters._args, x, index, base, out, out_f32, workspace.addr,
+                 workspace.nbytes, stream):
+        _explain_adapters(x, adapters, index, base, out, out_f32)
+        raise ValueError("stream must be an integer or a stream, sizes below 2^31")
+    return out
+
+
+def _explain_adapters(x, adapters, index, base, out, out_f32):
+    """Raise for the first argument of a linear_adapters call that is not in order."""
+    dev = adapters.device
+    _need_matrix(x, "x", dev, dtypes=(torch.bfloat16,))
+    if x.shape[1] != adapters.K:
+        raise ValueError(f"x must be [tokens, {adapters.K}]")
+    shape = (x.shape[0], adapters.N)
+    _need(index, "index", torch.int32, dev)
+    if index.numel() != x.shape[0]:
+        raise ValueError("index must be [tokens]")
+    if base is not None:
+        _need_matrix(base, "base", dev, shape)
+    _need_matrix(out, "out", dev, shape, (torch.bfloat16,))
+    if out_f32 is not None:
+        _need_matrix(out_f32, "out_f32", dev, shape, (torch.float32,))
+
+
+class PagePool:
+    """Whose pages are: the state that goes with the paged caches of all layers (see dl_kv_pages).
+
+    caches       one PagedKVCache, or a list with one of each layer, all of one shape (or empty)
+    block_table  int32 [rows, columns], seq_lens int32 [rows]: as kv_append and attention_paged take them
+    refs         int32 [num_pages]: how many rows' tables name each page (0: free)
+
+    The object holds the tensors and is made once; kv_free, kv_reserve, kv_fork and kv_compact change
+    them in place.  ``PagePool.empty`` makes a pool whose rows have no pages.
+    """
+
+    def __init__(self, caches, block_table, seq_lens, refs, *, page_size=None):
+        caches = [caches] if isinstance(caches, PagedKVCache) else list(caches)
+        for c in caches:
+            if not isinstance(c, PagedKVCache):
+                raise TypeError("caches must be PagedKVCache objects")
+        _need(refs, "refs", torch.int32)
+        dev = refs.device
+        _need(block_table, "block_table", torch.int32, dev)
+        _need(seq_lens, "seq_lens", torch.int32, dev)
+        if block_table.dim() != 2 or seq_lens.dim() != 1 or refs.dim() != 1 or seq_lens.shape[0] != block_table.shape[0]:
+            raise ValueError("block_table must be [rows, columns], seq_lens [rows], refs [num_pages]")
+        if page_size is None:
+            if not caches:
+                raise ValueError("without caches, page_size must be given")
+            page_size = caches[0].page_size
+        shape = lambda c: (c.kv_heads, c.head_dim, c.block)   # noqa: E731
+        for c in caches:
+            if c.device != dev:
+                raise ValueError(f"a cache is on {c.device}, expected {dev}")
+            if c.num_pages != refs.shape[0] or c.page_size != page_size or shape(c) != shape(caches[0]):
+                raise ValueError("the caches must be of one shape, with refs' pages and page_size")
+        self.caches, self.block_table, self.seq_lens, self.refs = caches, block_table, seq_lens, refs
+        self.page_size, self.num_pages, self.rows, self.device = page_size, refs.shape[0], seq_lens.shape[0], dev
+        self._caches = (_KVCache * max(1, len(caches)))(*[c._struct for c in caches])
+        self._struct = _KVPages(self._caches, refs.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), len(caches),
+                                self.num_pages, page_size, self.rows, block_table.shape[1])
+        self._args = (ctypes.addressof(self._struct), dev.index)
+
+    @classmethod
+    def empty(cls, caches, rows, columns):
+        """A pool of the caches' pages, all free, and `rows` empty rows of up to `columns` pages."""
+        first = caches if isinstance(caches, PagedKVCache) else caches[0]
+        zeros = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=first.device)   # noqa: E731
+        return cls(caches, zeros(rows, columns) - 1, zeros(rows), zeros(first.num_pages))
+
+
+def pages_workspace_bytes(pool: PagePool) -> int:
+    """Workspace kv_reserve, kv_fork and kv_compact need for this pool (0 = invalid sizes)."""
+    return int(load().dl_kv_pages_workspace_bytes(pool.num_pages, pool.rows))
+
+
+def _pages(what, pool, first, second, out, workspace, stream):
+    if what == 0:
+        addr = nbytes = 0
+    else:
+        if out is None:
+            n = 1 if what == 3 else first.numel() if isinstance(first, torch.Tensor) else 0
+            out = _empty((n,), torch.int32, pool.device, stream)
+        if workspace is None:
+            with torch.cuda.device(pool.device):
+                workspace = _workspace(None, pages_workspace_bytes(pool), pool.device, stream)
+        elif workspace.tensor.device != pool.device:
+            raise ValueError(f"workspace is on {workspace.tensor.device}, expected {pool.device}")
+        addr, nbytes = workspace.addr, workspace.nbytes
+    if not _call("pages", pool.device, what, pool._args, first, second, out, addr, nbytes, stream):
+        lists = {0: ("rows",), 1: ("rows", "tokens"), 2: ("parents", "children"), 3: ()}[what]
+        for t, n in zip((first, second), lists):
+            _need(t, n, torch.int32, pool.device)
+            if t.dim() != 1 or t.shape != first.shape:
+                raise ValueError(f"{' and '.join(lists)} must be [n]")
+        if what:
+            _need(out, "out_live" if what == 3 else "out_done", torch.int32, pool.device)
+            if out.dim() != 1 or out.shape[0] != (1 if what == 3 else first.shape[0]):
+                raise ValueError("out_live must be [1]" if what == 3 else "out_done must be [n]")
+        raise ValueError("stream must be an integer or a stream, sizes below 2^31")
+    return out
+
+
+def kv_free(pool: PagePool, rows, *, stream=None):
+    """Give the pages of the listed rows (int32 [n], n <= pool.rows) back; the rows become empty.  See
+    dl_kv_free."""
+    _pages(0, pool, rows, None, None, None, stream)
+
+
+def kv_reserve(pool: PagePool, rows, tokens, *, out_done=None, workspace: Workspace | None = None, stream=None):
+    """Room for tokens[i] more tokens in row rows[i] (int32 [n] each): lengths grow, pages are taken.
+    Returns done, int32 [n]: 1 where it was served.  See dl_kv_reserve."""
+    return _pages(1, pool, rows, tokens, out_done, workspace, stream)
+
+
+def kv_fork(pool: PagePool, parents, children, *, out_done=None, workspace: Workspace | None = None, stream=None):
+    """The empty row children[i] becomes a copy of row parents[i] (int32 [n] each): full pages are
+    shared, a page that is begun is copied in every cache.  Returns done, int32 [n]: 1 where it was
+    served.  See dl_kv_fork."""
+    return _pages(2, pool, parents, children, out_done, workspace, stream)
+
+
+def kv_compact(pool: PagePool, *, out_live=None, workspace: Workspace | None = None, stream=None):
+    """Move the pages in use to the front of the pool, in every cache.  Returns live, int32 [1]: how
+    many there are.  See dl_kv_compact."""
+    return _pages(3, pool, None, None, out_live, workspace, stream)
 
 
 def graph_cache_clear():

@@ -1,5 +1,5 @@
 /*
- * Calls of the cached-attention entry points from Python: reads the tensors'
+ * Calls of the entry points around the linears from Python: reads the tensors'
  * types, devices, shapes and addresses through their Python attributes, checks
  * what the library cannot (that a pointer means what it should) and calls.
  *
@@ -28,11 +28,24 @@ typedef dl_status (*attention_fn)(const dl_kv_cache*, const void*, long long, vo
 typedef dl_status (*verify_fn)(const int*, const void*, const void*, int, const float*, const float*, const int*, int*,
                                int*, int, int, int, void*);
 
+typedef dl_status (*norm_fn)(const dl_rows*, const dl_norm*, const dl_rows*, int, int, float, const dl_rows*, float,
+                             const dl_norm*, const dl_rows*, const dl_rows*, int, int, void*);
+typedef dl_status (*adapters_fn)(const dl_adapters*, const dl_rows*, const int*, const dl_rows*, const dl_rows*,
+                                 const dl_rows*, int, void*, size_t, void*);
+typedef dl_status (*free_fn)(const dl_kv_pages*, const int*, int, void*);
+typedef dl_status (*list_fn)(const dl_kv_pages*, const int*, const int*, int*, int, void*, size_t, void*);
+typedef dl_status (*compact_fn)(const dl_kv_pages*, int*, void*, size_t, void*);
+
 static PyObject *g_tensor, *g_bf16, *g_i32, *g_f32, *g_raw_stream;
 static get_device_fn g_get_device;
 static append_fn g_append;
 static attention_fn g_attention;
 static verify_fn g_verify;
+static norm_fn g_norm;
+static adapters_fn g_adapters;
+static free_fn g_free;
+static list_fn g_reserve, g_fork;
+static compact_fn g_compact;
 static PyObject *s_dtype, *s_shape, *s_stride, *s_get_device, *s_is_contiguous, *s_data_ptr, *s_cuda_stream;
 
 /* Up to 4 integers of a tuple; -1 if it is none or has more. */
@@ -254,6 +267,144 @@ static PyObject* verify(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     return answer(status);
 }
 
+/* bf16 or fp32 rows [n, dim] of device `dev`, a row dense (None: none). */
+static int look_at_matrix(PyObject* t, long long dev, view* v, dl_rows* r) {
+    r->data = NULL;
+    if (t == Py_None) return 1;
+    if (!PyObject_TypeCheck(t, (PyTypeObject*)g_tensor)) return 0;
+    PyObject* a = PyObject_GetAttr(t, s_dtype);
+    if (!a) return 0;
+    const int f32 = a == g_f32;
+    Py_DECREF(a);
+    if (!look_at(t, f32 ? g_f32 : g_bf16, dev, 1, v) || v->dims != 2 || !fits(v->shape[0]) || !fits(v->shape[1]) ||
+        (v->shape[1] > 1 && v->shape[0] > 0 && v->stride[1] != 1))
+        return 0;
+    r->data = v->ptr;
+    r->stride = v->shape[0] > 1 ? v->stride[0] : v->shape[1];
+    r->dtype = f32 ? DL_ROWS_F32 : DL_ROWS_BF16;
+    return 1;
+}
+
+/* A norm's description (address, length of its weights or -1, their device or -1), or None. */
+static int look_at_norm(PyObject* t, long long dim, long long dev, const dl_norm** out) {
+    long long v[4];
+    *out = NULL;
+    if (t == Py_None) return 1;
+    if (integers(t, v) != 3 || (v[1] >= 0 && (v[1] != dim || v[2] != dev))) return 0;
+    *out = (const dl_norm*)(uintptr_t)v[0];
+    return 1;
+}
+
+/* norm(device, y, post, gate, act, scale, h, h_scale, pre, out_h, out_x, stream) */
+static PyObject* norm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    if (n != 12) return answer(LOOK);
+    const long long dev = PyLong_AsLongLong(a[0]), act = PyLong_AsLongLong(a[4]);
+    const double scale = PyFloat_AsDouble(a[5]), h_scale = PyFloat_AsDouble(a[7]);
+    view v[5];
+    dl_rows y, h, gate = {0}, r, x;
+    const dl_norm *post, *pre;
+    void* stream;
+    int kind = DL_GATE_NONE;
+    if (PyErr_Occurred() || !look_at_matrix(a[1], dev, &v[0], &y) || !look_at_matrix(a[6], dev, &v[1], &h) ||
+        (a[1] == Py_None && a[6] == Py_None))
+        return answer(LOOK);
+    const view* like = a[1] != Py_None ? &v[0] : &v[1];
+    const long long rows = like->shape[0], dim = like->shape[1];
+    if ((a[6] != Py_None && (v[1].shape[0] != rows || v[1].shape[1] != dim)) ||
+        !look_at_matrix(a[9], dev, &v[2], &r) || (a[9] != Py_None && (v[2].shape[0] != rows || v[2].shape[1] != dim)) ||
+        !look_at_matrix(a[10], dev, &v[3], &x) || (a[10] != Py_None && (v[3].shape[0] != rows || v[3].shape[1] != dim)) ||
+        !look_at_norm(a[2], dim, dev, &post) || !look_at_norm(a[8], dim, dev, &pre) || !stream_of(a[11], dev, &stream))
+        return answer(LOOK);
+    if (a[3] != Py_None) {
+        if (look_at_matrix(a[3], dev, &v[4], &gate)) {
+            if (v[4].shape[0] != rows || (v[4].shape[1] != 1 && v[4].shape[1] != dim)) return answer(LOOK);
+            kind = v[4].shape[1] == dim ? DL_GATE_FULL : DL_GATE_ROW;
+        } else {
+            PyErr_Clear();
+            gate.dtype = DL_ROWS_F32;
+            if (!look_at(a[3], g_f32, dev, 0, &v[4])) {
+                PyErr_Clear();
+                gate.dtype = DL_ROWS_BF16;
+                if (!look_at(a[3], g_bf16, dev, 0, &v[4])) return answer(LOOK);
+            }
+            if (v[4].dims != 1 || v[4].shape[0] != dim) return answer(LOOK);
+            gate.data = v[4].ptr;
+            gate.stride = dim;
+            kind = DL_GATE_CHANNEL;
+        }
+    }
+    if (!current(dev)) return answer(OTHER_DEVICE);
+    dl_status status;
+    CALL(status, g_norm(&y, post, &gate, kind, (int)act, (float)scale, &h, (float)h_scale, pre, &r, &x, (int)rows, (int)dim,
+                        stream));
+    return answer(status);
+}
+
+/* adapters((address, device, K, N), x, index, base, out, out_f32, workspace, bytes, stream) */
+static PyObject* adapters(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    long long d[4];
+    if (n != 9 || integers(a[0], d) != 4) return answer(LOOK);
+    const long long dev = d[1], K = d[2], N = d[3];
+    const uintptr_t ws = (uintptr_t)PyLong_AsUnsignedLongLong(a[6]);
+    const unsigned long long bytes = PyLong_AsUnsignedLongLong(a[7]);
+    view v, i;
+    dl_rows x, base, y, y32;
+    void* stream;
+    if (PyErr_Occurred() || a[1] == Py_None || !look_at_matrix(a[1], dev, &v, &x) || x.dtype != DL_ROWS_BF16 || v.shape[1] != K)
+        return answer(LOOK);
+    const long long T = v.shape[0];
+    if (!look_at(a[2], g_i32, dev, 0, &i) || numel(&i) != T || !look_at_matrix(a[3], dev, &v, &base) ||
+        (a[3] != Py_None && (v.shape[0] != T || v.shape[1] != N)) || a[4] == Py_None || !look_at_matrix(a[4], dev, &v, &y) ||
+        y.dtype != DL_ROWS_BF16 || v.shape[0] != T || v.shape[1] != N || !look_at_matrix(a[5], dev, &v, &y32) ||
+        (a[5] != Py_None && (y32.dtype != DL_ROWS_F32 || v.shape[0] != T || v.shape[1] != N)) ||
+        !stream_of(a[8], dev, &stream))
+        return answer(LOOK);
+    if (!current(dev)) return answer(OTHER_DEVICE);
+    dl_status status;
+    CALL(status, g_adapters((const dl_adapters*)(uintptr_t)d[0], &x, (const int*)i.ptr, &base, &y, &y32, (int)T, (void*)ws,
+                            (size_t)bytes, stream));
+    return answer(status);
+}
+
+/* pages(what, (address, device), list, list or None, done or live or None, workspace, bytes, stream); what: 0 free,
+ * 1 reserve, 2 fork, 3 compact (no lists) */
+static PyObject* pages(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    long long d[4];
+    if (n != 8 || integers(a[1], d) != 2) return answer(LOOK);
+    const long long what = PyLong_AsLongLong(a[0]), dev = d[1];
+    const dl_kv_pages* pool = (const dl_kv_pages*)(uintptr_t)d[0];
+    const uintptr_t ws = (uintptr_t)PyLong_AsUnsignedLongLong(a[5]);
+    const unsigned long long bytes = PyLong_AsUnsignedLongLong(a[6]);
+    view x = {0}, y = {0}, z = {0};
+    void* stream;
+    if (PyErr_Occurred() || what < 0 || what > 3 || !stream_of(a[7], dev, &stream)) return answer(LOOK);
+    if (what < 3 && (!look_at(a[2], g_i32, dev, 0, &x) || x.dims != 1 || !fits(x.shape[0]))) return answer(LOOK);
+    if ((what == 1 || what == 2) && (!look_at(a[3], g_i32, dev, 0, &y) || y.dims != 1 || y.shape[0] != x.shape[0]))
+        return answer(LOOK);
+    if (what > 0 && (!look_at(a[4], g_i32, dev, 0, &z) || z.dims != 1 || z.shape[0] != (what == 3 ? 1 : x.shape[0])))
+        return answer(LOOK);
+    if (!current(dev)) return answer(OTHER_DEVICE);
+    const int count = (int)x.shape[0];
+    dl_status status;
+    if (what == 0)
+        CALL(status, g_free(pool, (const int*)x.ptr, count, stream));
+    else if (what == 3)
+        CALL(status, g_compact(pool, (int*)z.ptr, (void*)ws, (size_t)bytes, stream));
+    else
+        CALL(status, (what == 1 ? g_reserve : g_fork)(pool, (const int*)x.ptr, (const int*)y.ptr, (int*)z.ptr, count,
+                                                      (void*)ws, (size_t)bytes, stream));
+    return answer(status);
+}
+
+/* `n` addresses from Python integers. */
+static int addresses(PyObject* const* a, uintptr_t* f, int n) {
+    for (int i = 0; i < n; ++i) f[i] = (uintptr_t)PyLong_AsUnsignedLongLong(a[i]);
+    return !PyErr_Occurred();
+}
+
 /* bind(Tensor, bfloat16, int32, float32, raw_stream, get_device, append, attention, verify): types, and addresses */
 static PyObject* bind(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     (void)self;
@@ -262,8 +413,7 @@ static PyObject* bind(PyObject* self, PyObject* const* a, Py_ssize_t n) {
         return NULL;
     }
     uintptr_t f[4];
-    for (int i = 0; i < 4; ++i) f[i] = (uintptr_t)PyLong_AsUnsignedLongLong(a[5 + i]);
-    if (PyErr_Occurred()) return NULL;
+    if (!addresses(a + 5, f, 4)) return NULL;
     PyObject** to[5] = {&g_tensor, &g_bf16, &g_i32, &g_f32, &g_raw_stream};
     for (int i = 0; i < 5; ++i) {
         Py_INCREF(a[i]);
@@ -276,10 +426,32 @@ static PyObject* bind(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     Py_RETURN_NONE;
 }
 
+/* bind_more(norm, adapters, free, reserve, fork, compact): addresses */
+static PyObject* bind_more(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    if (n != 6) {
+        PyErr_SetString(PyExc_TypeError, "bind_more takes six addresses");
+        return NULL;
+    }
+    uintptr_t f[6];
+    if (!addresses(a, f, 6)) return NULL;
+    g_norm = (norm_fn)f[0];
+    g_adapters = (adapters_fn)f[1];
+    g_free = (free_fn)f[2];
+    g_reserve = (list_fn)f[3];
+    g_fork = (list_fn)f[4];
+    g_compact = (compact_fn)f[5];
+    Py_RETURN_NONE;
+}
+
 static PyMethodDef methods[] = {{"bind", (PyCFunction)(void (*)(void))bind, METH_FASTCALL, NULL},
+                                {"bind_more", (PyCFunction)(void (*)(void))bind_more, METH_FASTCALL, NULL},
                                 {"append", (PyCFunction)(void (*)(void))append, METH_FASTCALL, NULL},
                                 {"attention", (PyCFunction)(void (*)(void))attention, METH_FASTCALL, NULL},
                                 {"verify", (PyCFunction)(void (*)(void))verify, METH_FASTCALL, NULL},
+                                {"norm", (PyCFunction)(void (*)(void))norm, METH_FASTCALL, NULL},
+                                {"adapters", (PyCFunction)(void (*)(void))adapters, METH_FASTCALL, NULL},
+                                {"pages", (PyCFunction)(void (*)(void))pages, METH_FASTCALL, NULL},
                                 {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", NULL, -1, methods, NULL, NULL, NULL, NULL};
