@@ -77,63 +77,94 @@ __device__ __forceinline__ int rank_of(const AdapterParams& p, int adapter) {
 }
 
 // The small tiles of at most kFewTokens tokens, made by every CTA for itself, all alike.  A token's place
-// among those of its adapter is the number of earlier ones; every kTile-th opens a tile.  Comparing
-// with all earlier tokens takes up to 64 broadcast reads a thread, less than a kernel that sorts.
+// among those of its adapter is the number of earlier ones; every kTile-th opens a tile, and tiles are numbered
+// by the tokens that open them.  Up to 32 tokens one warp sees all; beyond, a table of the adapters that
+// occur, by hash, holds how many tokens of it each warp has.  (Where in the table an adapter is does
+// not matter.)
+constexpr int kSlots = 512;
 struct FewTiles {
-    int adapter[kFewTokens];
-    int opened[kFewTokens / 32];
-    int tile_of[kFewTokens];
     Tile tile[kFewTokens];
+    int slot[kSlots];                            // adapter + 2 of each slot, 0: free
+    unsigned long long held[kSlots];             // its tokens in each warp, a byte each (32 at most)
+    unsigned char number[kSlots][kFewTokens / kTile];   // of its tiles
+    int opened[kFewTokens / 32];
+    int n;
 };
 
+__device__ __forceinline__ int nth_bit(unsigned m, int n) {
+    for (; n > 0; --n) m &= m - 1;
+    return __ffs(m) - 1;
+}
+
 __device__ __forceinline__ int make_tiles(const AdapterParams& p, FewTiles& s) {
+    static_assert(kFewTokens == 256, "a byte for each of 8 warps");
     const int T = p.tokens, t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    int mine = -2;
-    if (t < kFewTokens) {
-        if (t < T) mine = adapter_of(p, t);
-        s.adapter[t] = mine;
-    }
+    const unsigned below = (1u << lane) - 1;
+    const int mine = t < T ? adapter_of(p, t) : -2;
     for (int i = t; i < T * (int)(sizeof(Tile) / 4); i += blockDim.x) reinterpret_cast<int*>(s.tile)[i] = -1;
+    if (T <= 32) {
+        __syncthreads();
+        if (warp == 0) {
+            const unsigned same = __match_any_sync(~0u, mine);
+            const int place = __popc(same & below);
+            const unsigned m = __ballot_sync(~0u, t < T && place % kTile == 0);
+            if (t < T) {
+                const int opener = nth_bit(same, place / kTile * kTile);
+                Tile& tile = s.tile[__popc(m & ((1u << opener) - 1))];
+                if (opener == t) tile.adapter = mine;
+                tile.token[place % kTile] = t;
+            }
+            if (lane == 0) s.n = __popc(m);
+        }
+        __syncthreads();
+        return s.n;
+    }
+    for (int i = t; i < kSlots; i += blockDim.x) {
+        s.slot[i] = 0;
+        s.held[i] = 0;
+    }
     __syncthreads();
-    int place = 0, opener = -1;
+    unsigned same = 0;
+    int at = 0, place = 0;
     bool opens = false;
-    if (warp < kFewTokens / 32) {
-        const unsigned same = __match_any_sync(~0u, mine);
-        for (int i = 0; i < 32 * warp && 32 * warp < T; i += 4) {
-            const int4 v = *reinterpret_cast<const int4*>(s.adapter + i);
-            const int w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (w[k] == mine) {
-                    if (place % kTile == 0) opener = i + k;
-                    ++place;
-                }
+    if (t < kFewTokens) {
+        same = __match_any_sync(~0u, mine);
+        const int leader = __ffs(same) - 1;
+        if (t < T && lane == leader) {
+            at = (mine * 0x9E3779B1u) >> 23;     // 9 bits
+            while (true) {
+                const int found = atomicCAS(&s.slot[at], 0, mine + 2);
+                if (found == 0 || found == mine + 2) break;
+                at = (at + 1) % kSlots;
+            }
+            reinterpret_cast<unsigned char*>(&s.held[at])[warp] = (unsigned char)__popc(same);
         }
-        // and those of this warp
-        unsigned before = same & ((1u << lane) - 1);
-        while (before) {
-            if (place % kTile == 0) opener = 32 * warp + __ffs(before) - 1;
-            ++place;
-            before &= before - 1;
-        }
+        at = __shfl_sync(~0u, at, leader);
+    }
+    __syncthreads();
+    if (t < kFewTokens) {
+        // the bytes of the warps before this one
+        const unsigned long long before = s.held[at] & ((1ull << (8 * warp)) - 1);
+        place = __dp4a((unsigned)before, 0x01010101u, __dp4a((unsigned)(before >> 32), 0x01010101u, 0u)) + __popc(same & below);
         opens = t < T && place % kTile == 0;
-        if (opens) opener = t;
         const unsigned m = __ballot_sync(~0u, opens);
         if (lane == 0) s.opened[warp] = __popc(m);
-        if (opens) s.tile_of[t] = __popc(m & ((1u << lane) - 1));
+        same = m;                                // openers of this warp
     }
     __syncthreads();
     int n = 0, first = 0;
 #pragma unroll
     for (int w = 0; w < kFewTokens / 32; ++w) {
-        if (w < opener >> 5) first += s.opened[w];
+        if (w < warp) first += s.opened[w];
         n += s.opened[w];
     }
-    if (t < T) {
-        Tile& tile = s.tile[first + s.tile_of[opener]];
-        if (opens) tile.adapter = mine;
-        tile.token[place % kTile] = t;
+    if (opens) {
+        const int number = first + __popc(same & below);
+        s.number[at][place / kTile] = (unsigned char)number;
+        s.tile[number].adapter = mine;
     }
+    __syncthreads();
+    if (t < T) s.tile[s.number[at][place / kTile]].token[place % kTile] = t;
     __syncthreads();
     return n;
 }
@@ -261,41 +292,60 @@ __global__ void __launch_bounds__(kLowThreads) adapters_low_kernel(const __grid_
         n_tiles = l.counts[0];
         tiles = l.small;
     }
-    const int R = p.rank, groups = (R + 15) / 16, K = p.K;
+    const int R = p.rank, K = p.K;
+    const unsigned groups = (R + 15) / 16;
     // this warp's part of K: whole runs of 32
     const int runs = (K + 31) / 32, workers = size * kLowWarps, worker = rank * kLowWarps + warp;
     const int k0 = (int)((long long)runs * worker / workers) * 32;
     const int k1 = (int)((long long)runs * (worker + 1) / workers) * 32;
-    const long long items = (long long)n_tiles * p.parts * groups;
-    for (long long item = blockIdx.x / size; item < items; item += gridDim.x / size) {
-        const int j0 = (int)(item % groups) * 16, pt = (int)(item / groups) % p.parts;
-        const Tile& tile = tiles[item / groups / p.parts];
+    const unsigned per = p.parts * groups, items = n_tiles * per;      // fits: a launch of more is refused
+    for (unsigned item = blockIdx.x / size; item < items; item += gridDim.x / size) {
+        const unsigned i = item % per;
+        const int j0 = (int)(i % groups) * 16, pt = (int)(i / groups);
+        const Tile& tile = tiles[item / per];
         const int ad = tile.adapter;
         if (ad < 0) continue;
         const int r = rank_of(p, ad);
         if (j0 >= r) continue;
-        const uint16_t* a = p.a + ((size_t)ad * p.parts + pt) * R * K + (size_t)j0 * K;
         const int t0 = tile.token[g], t1 = tile.token[g + 8];
         const bool two = tile.token[8] >= 0, row0 = j0 + g < r, row1 = j0 + g + 8 < r;
-        const uint16_t* a0 = a + (size_t)g * K;
+        const uint16_t* a0 = p.a + (((size_t)ad * p.parts + pt) * R + j0 + g) * K + 8 * c;
         const uint16_t* a1 = a0 + (size_t)8 * K;
-        const char *x0 = row_ptr(p.x, max(t0, 0)), *x1 = row_ptr(p.x, max(t1, 0));
+        const char *x0 = row_ptr(p.x, max(t0, 0)) + 16 * c, *x1 = row_ptr(p.x, max(t1, 0)) + 16 * c;
         float d0[4] = {}, d1[4] = {};
         const uint4 none = {0, 0, 0, 0};
-#pragma unroll 4
-        for (int run = k0; run < k1; run += 32) {       // every lane takes part in every product
-            const int k = run + 8 * c;
-            const bool in = k < K;
-            const uint4 va = in && row0 ? ldg128(a0 + k) : none, vb = in && row1 ? ldg128(a1 + k) : none;
-            const uint4 xa = in && t0 >= 0 ? ldg128(x0 + 2 * (size_t)k) : none;
-            const uint4 xb = in && t1 >= 0 ? ldg128(x1 + 2 * (size_t)k) : none;
+        auto step = [&](int run, bool in) {              // every lane takes part in every product
+            const uint4 va = in && row0 ? ldg128(a0 + run) : none, vb = in && row1 ? ldg128(a1 + run) : none;
+            const uint4 xa = in && t0 >= 0 ? ldg128(x0 + 2 * run) : none;
             mma_bf16_16816(d0, va.x, vb.x, va.y, vb.y, xa.x, xa.y);
             mma_bf16_16816(d0, va.z, vb.z, va.w, vb.w, xa.z, xa.w);
             if (two) {
+                const uint4 xb = in && t1 >= 0 ? ldg128(x1 + 2 * run) : none;
                 mma_bf16_16816(d1, va.x, vb.x, va.y, vb.y, xb.x, xb.y);
                 mma_bf16_16816(d1, va.z, vb.z, va.w, vb.w, xb.z, xb.w);
             }
+        };
+        int run = k0;
+        for (; run + 128 <= k1 && run + 128 <= K; run += 128) {
+            uint4 va[4], vb[4], xa[4], xb[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                va[i] = row0 ? ldg128(a0 + run + 32 * i) : none;
+                vb[i] = row1 ? ldg128(a1 + run + 32 * i) : none;
+                xa[i] = t0 >= 0 ? ldg128(x0 + 2 * (run + 32 * i)) : none;
+                xb[i] = t1 >= 0 ? ldg128(x1 + 2 * (run + 32 * i)) : none;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                mma_bf16_16816(d0, va[i].x, vb[i].x, va[i].y, vb[i].y, xa[i].x, xa[i].y);
+                mma_bf16_16816(d0, va[i].z, vb[i].z, va[i].w, vb[i].w, xa[i].z, xa[i].w);
+                if (two) {
+                    mma_bf16_16816(d1, va[i].x, vb[i].x, va[i].y, vb[i].y, xb[i].x, xb[i].y);
+                    mma_bf16_16816(d1, va[i].z, vb[i].z, va[i].w, vb[i].w, xb[i].z, xb[i].w);
+                }
+            }
         }
+        for (; run < k1; run += 32) step(run, run + 8 * c < K);
         // sum[warp][token * 16 + row]
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -408,6 +458,24 @@ __device__ __forceinline__ uint2 rank_mask(int at, int r) {
                       (at + 2 < r ? 0xffffu : 0u) | (at + 3 < r ? 0xffff0000u : 0u));
 }
 
+// A token's results in one tensor: 16 columns of a warp's, four of them this lane's, from n on.
+__device__ __forceinline__ void put_wide(char* row, bool f32, int n, const float (&v)[4]) {
+    if (f32)
+        *reinterpret_cast<float4*>(row + 4 * (size_t)n) = make_float4(v[0], v[1], v[2], v[3]);
+    else
+        *reinterpret_cast<uint2*>(row + 2 * (size_t)n) = make_uint2(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]));
+}
+__device__ __forceinline__ void load_wide(const char* row, bool f32, int n, float (&v)[4]) {
+    if (f32) {
+        const uint4 u = ldg128(row + 4 * (size_t)n);
+        v[0] = __uint_as_float(u.x); v[1] = __uint_as_float(u.y); v[2] = __uint_as_float(u.z); v[3] = __uint_as_float(u.w);
+    } else {
+        const uint2 u = ldg64(row + 2 * (size_t)n);
+        bf16x2_to_f32(u.x, v[0], v[1]);
+        bf16x2_to_f32(u.y, v[2], v[3]);
+    }
+}
+
 // Small tiles: a warp takes U times 16 columns of a tile, B's values of 16 C at a time.  What does not depend
 // on the first products (the tiles, base, B) is fetched before they are waited for: the kernel that
 // makes them lets this one start only after it had waited for all earlier ones.
@@ -428,16 +496,16 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapters_up_kernel(const __grid
         n_tiles = l.counts[0];
         tiles = l.small;
     }
-    const int R = p.rank, N = p.N, units = (N + 16 * U - 1) / (16 * U);
-    const int items = n_tiles * units;   // fits: a launch of more is refused
-    const int parts = p.y32.ptr ? 3 : 2;
+    const int R = p.rank, N = p.N, parts = p.y32.ptr ? 3 : 2;
+    const unsigned units = (N + 16 * U - 1) / (16 * U), items = n_tiles * units;    // fits: a launch of more is refused
     const size_t step = (size_t)p.parts * R;
     bool waited = false;
-    for (int item = blockIdx.x * kUpWarps + warp; item < items; item += gridDim.x * kUpWarps) {
+    for (unsigned item = blockIdx.x * kUpWarps + warp; item < items; item += gridDim.x * kUpWarps) {
         const Tile& tile = tiles[item / units];
-        const int n0 = (item % units) * 16 * U;
+        const int n0 = (int)(item % units) * 16 * U;
         const int ad = tile.adapter, t0 = tile.token[g], t1 = tile.token[g + 8];
         const int r = rank_of(p, ad);
+        const bool whole = n0 + 16 * U <= N, fast = whole && p.wide;
         const uint16_t* b = p.b + (size_t)max(ad, 0) * N * R;
         float base[U][2][4];
 #pragma unroll
@@ -445,58 +513,75 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapters_up_kernel(const __grid
 #pragma unroll
             for (int k = 0; k < 4; ++k) base[u][0][k] = base[u][1][k] = 0.f;
         if (p.base.ptr) {
+            const char *from0 = row_ptr(p.base, max(t0, 0)), *from1 = row_ptr(p.base, max(t1, 0));
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (t0 >= 0) load4(p.base, t0, n0 + 16 * u + 4 * c, N, p.wide, base[u][0]);
-                if (t1 >= 0) load4(p.base, t1, n0 + 16 * u + 4 * c, N, p.wide, base[u][1]);
+                const int n = n0 + 16 * u + 4 * c;
+                if (fast) {
+                    if (t0 >= 0) load_wide(from0, p.base.f32, n, base[u][0]);
+                    if (t1 >= 0) load_wide(from1, p.base.f32, n, base[u][1]);
+                } else {
+                    if (t0 >= 0) load4(p.base, t0, n, N, p.wide, base[u][0]);
+                    if (t1 >= 0) load4(p.base, t1, n, N, p.wide, base[u][1]);
+                }
             }
         }
         float d[U][2][4] = {};               // [product][row g: 2 columns, row g + 8: 2 columns]
+        const int col0 = n0 + (g >> 1) * 4 + (g & 1);
         for (int r0 = 0; r0 < r; r0 += 16 * C) {
             uint2 w[C][U][2];
+            const uint16_t* bl = b + (size_t)col0 * R + r0 + 4 * c;
 #pragma unroll
-            for (int q = 0; q < C; ++q)
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int u = 0; u < U; ++u)
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int col = n0 + 16 * u + (g >> 1) * 4 + (g & 1) + 2 * i, at = r0 + 16 * q + 4 * c;
-                        w[q][u][i] = at < r && col < N ? ldg64(b + (size_t)col * R + at) : make_uint2(0, 0);
+                    for (int q = 0; q < C; ++q) {
+                        const bool in = r0 + 16 * q + 4 * c < r && (whole || col0 + 16 * u + 2 * i < N);
+                        w[q][u][i] = in ? ldg64(bl + (16 * u + 2 * i) * R + 16 * q) : make_uint2(0, 0);
                     }
             if (!waited) {
                 griddep_wait();
                 griddep_launch_dependents();
                 waited = true;
             }
-            int held = -1;                   // the part whose first products `s0`, `s1` are
-            float4 s0[C], s1[C];
+            int held = -1;                   // the part whose first products `a` has
+            Parts a[C][4];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int pt = part_of(p, n0 + 16 * u);
                 if (pt != held) {
-                    const float* low = p.low + pt * R + r0 + 4 * c;
+                    held = pt;
+                    const float *low0 = p.low + t0 * step + pt * R + r0 + 4 * c, *low1 = p.low + t1 * step + pt * R + r0 + 4 * c;
+                    float4 s0[C], s1[C];
 #pragma unroll
                     for (int q = 0; q < C; ++q) {
                         const bool in = r0 + 16 * q + 4 * c < r;
-                        s0[q] = in && t0 >= 0 ? ld_cg_f32x4(low + t0 * step + 16 * q) : make_float4(0.f, 0.f, 0.f, 0.f);
-                        s1[q] = in && t1 >= 0 ? ld_cg_f32x4(low + t1 * step + 16 * q) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        s0[q] = in && t0 >= 0 ? ld_cg_f32x4(low0 + 16 * q) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        s1[q] = in && t1 >= 0 ? ld_cg_f32x4(low1 + 16 * q) : make_float4(0.f, 0.f, 0.f, 0.f);
                     }
-                    held = pt;
+#pragma unroll
+                    for (int q = 0; q < C; ++q) {
+                        const int at = r0 + 16 * q + 4 * c;
+                        const bool in1 = at + 1 < r, in2 = at + 2 < r, in3 = at + 3 < r;
+                        a[q][0] = split(s0[q].x, in1 ? s0[q].y : 0.f, parts);
+                        a[q][1] = split(s1[q].x, in1 ? s1[q].y : 0.f, parts);
+                        a[q][2] = split(in2 ? s0[q].z : 0.f, in3 ? s0[q].w : 0.f, parts);
+                        a[q][3] = split(in2 ? s1[q].z : 0.f, in3 ? s1[q].w : 0.f, parts);
+                    }
                 }
 #pragma unroll
                 for (int q = 0; q < C; ++q) {
                     const int at = r0 + 16 * q + 4 * c;
                     if (r0 + 16 * q >= r) break;
                     const uint2 m = rank_mask(at, r);
-                    const bool in1 = at + 1 < r, in2 = at + 2 < r, in3 = at + 3 < r;
-                    const Parts a0 = split(s0[q].x, in1 ? s0[q].y : 0.f, parts), a1 = split(s1[q].x, in1 ? s1[q].y : 0.f, parts);
-                    const Parts a2 = split(in2 ? s0[q].z : 0.f, in3 ? s0[q].w : 0.f, parts);
-                    const Parts a3 = split(in2 ? s1[q].z : 0.f, in3 ? s1[q].w : 0.f, parts);
 #pragma unroll
                     for (int i = 0; i < 3; ++i) {
                         if (i < parts) {
-                            mma_bf16_16816(d[u][0], a0.v[i], a1.v[i], a2.v[i], a3.v[i], w[q][u][0].x & m.x, w[q][u][0].y & m.y);
-                            mma_bf16_16816(d[u][1], a0.v[i], a1.v[i], a2.v[i], a3.v[i], w[q][u][1].x & m.x, w[q][u][1].y & m.y);
+                            mma_bf16_16816(d[u][0], a[q][0].v[i], a[q][1].v[i], a[q][2].v[i], a[q][3].v[i], w[q][u][0].x & m.x,
+                                           w[q][u][0].y & m.y);
+                            mma_bf16_16816(d[u][1], a[q][0].v[i], a[q][1].v[i], a[q][2].v[i], a[q][3].v[i], w[q][u][1].x & m.x,
+                                           w[q][u][1].y & m.y);
                         }
                     }
                 }
@@ -514,19 +599,24 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapters_up_kernel(const __grid
             for (int k = 0; k < 4; ++k) odd = fmaf(d[u][0][k], 0.f, fmaf(d[u][1][k], 0.f, odd));
         const bool put = ad >= 0 || !p.in_place, put32 = p.y32.ptr && (ad >= 0 || !p.in_place32);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int n = n0 + 16 * u + 4 * c;
+        for (int h = 0; h < 2; ++h) {        // rows t0 and t1
+            const int t = h ? t1 : t0;
+            if (t < 0) continue;
+            char *to = row_ptr(p.y, t), *to32 = row_ptr(p.y32, t);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {    // rows t0 and t1
-                const int t = h ? t1 : t0;
-                if (t < 0) continue;
+            for (int u = 0; u < U; ++u) {
+                const int n = n0 + 16 * u + 4 * c;
                 float v[4] = {d[u][0][2 * h], d[u][0][2 * h + 1], d[u][1][2 * h], d[u][1][2 * h + 1]};
-                if (odd != odd)
-                    plain_up(p, p.low + t * step, 1.f, b, n, r, v);
+                if (odd != odd) plain_up(p, p.low + t * step, 1.f, b, n, r, v);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[k] += base[u][h][k];
-                if (put) put4(p.y, t, n, N, p.wide, v);
-                if (put32) put4(p.y32, t, n, N, p.wide, v);
+                if (fast) {
+                    if (put) put_wide(to, false, n, v);
+                    if (put32) put_wide(to32, true, n, v);
+                } else {
+                    if (put) put4(p.y, t, n, N, p.wide, v);
+                    if (put32) put4(p.y32, t, n, N, p.wide, v);
+                }
             }
         }
     }
@@ -622,25 +712,32 @@ __global__ void __launch_bounds__(kBigThreads) adapters_low_big_kernel(const __g
         const BigTile tile = l.big[ti];
         if (tile.adapter < 0) continue;
         const int r = rank_of(p, tile.adapter);
+        // what this thread copies: a 16-byte chunk of four rows of x and of every 32nd row of A; a row
+        // that is not there arrives as zeros
         const char* xr[kBigTile / 32];
+        int xb[kBigTile / 32];
 #pragma unroll
         for (int i = 0; i < kBigTile / 32; ++i) {
             const int row = row0 + 32 * i;
-            xr[i] = row < tile.count ? row_ptr(p.x, l.order[tile.first + row]) : nullptr;
+            xb[i] = row < tile.count ? 16 : 0;
+            xr[i] = (xb[i] ? row_ptr(p.x, l.order[tile.first + row]) : p.x.ptr) + 16 * chunk + s0 * 128;
         }
-        const uint16_t* a = p.a + ((size_t)tile.adapter * SR + j0) * K;
-        unsigned mine = 0;               // which of its rows of A, 32 apart, are within the rank
+        const char* ar = reinterpret_cast<const char*>(p.a + ((size_t)tile.adapter * SR + j0 + row0) * K) + 16 * chunk + s0 * 128;
+        const size_t a32 = (size_t)K * 64;
+        unsigned mine = 0;
         for (int i = 0; 32 * i + row0 < cols; ++i) mine |= ((j0 + 32 * i + row0) % p.rank < r ? 1u : 0u) << i;
         auto load = [&](int s) {         // step s of this tile
             const uint32_t to = base + (uint32_t)((used + s) % kBigStages) * shape.stage + put;
-            const int k = (s0 + s) * 64 + 8 * chunk;
-            const bool in = k < K;
+            const int off = s * 128;
+            const bool in = (s0 + s) * 64 + 8 * chunk < K;           // (the last step may end early)
+            const char* none = p.x.ptr;
 #pragma unroll
-            for (int i = 0; i < kBigTile / 32; ++i)
-                copy16_async(to + i * 4096, in && xr[i] ? xr[i] + 2 * (size_t)k : (const char*)p.x.ptr, in && xr[i] ? 16 : 0);
-            for (int i = 0; 32 * i + row0 < shape.cols; ++i) {
+            for (int i = 0; i < kBigTile / 32; ++i) copy16_async(to + i * 4096, in ? xr[i] + off : none, in ? xb[i] : 0);
+            const char* from = ar + off;
+#pragma unroll 2
+            for (int i = 0; 32 * i + row0 < shape.cols; ++i, from += a32) {
                 const bool take = in && (mine >> i & 1);
-                copy16_async(to + kBigTile * 128 + i * 4096, take ? a + (size_t)(32 * i + row0) * K + k : p.a, take ? 16 : 0);
+                copy16_async(to + kBigTile * 128 + i * 4096, take ? from : none, take ? 16 : 0);
             }
         };
         bool bad = dead;
@@ -768,6 +865,10 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapters_up_big_kernel(const __
     uint4* mine = reinterpret_cast<uint4*>(smem) + warp * C * P * 32 + lane;
     const uint32_t ring = smem_u32(smem) + kUpWarps * C * P * 512;
     constexpr int kStage = kUpBlock * C * 32, kGranules = kUpBlock * C * 2;         // 16 bytes each
+    auto swap = [](int row) { return C >= 4 ? row : C == 2 ? row >> 1 : 0; };
+    uint32_t piece_at[C];                // this lane's 8 bytes of a run of 16 r, in its row of eight
+#pragma unroll
+    for (int q = 0; q < C; ++q) piece_at[q] = g * 32 * C + 16 * ((2 * q + (c >> 1)) ^ swap(g)) + 8 * (c & 1);
     const size_t step = (size_t)p.parts * R;
     const int blocks = count_blocks(p);
     const long long all = (long long)n_tiles * blocks;
@@ -784,17 +885,22 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapters_up_big_kernel(const __
         const int t0 = i0 < tile.count ? l.order[tile.first + i0] : -1, t1 = i1 < tile.count ? l.order[tile.first + i1] : -1;
         const uint16_t* b = p.b + (size_t)max(ad, 0) * N * R;
         const char *from0 = row_ptr(p.base, max(t0, 0)), *from1 = row_ptr(p.base, max(t1, 0));
-        // a block of B into ring stage `i`; what lies past the rank or the part arrives as zeros
+        char *to0 = row_ptr(p.y, max(t0, 0)), *to1 = row_ptr(p.y, max(t1, 0));
+        char *to320 = row_ptr(p.y32, max(t0, 0)), *to321 = row_ptr(p.y32, max(t1, 0));
+        // A block of B into its ring stage: columns in the order of the products' operands, 16-byte pieces
+        // exchanged by row so that eight rows' reads meet no bank twice more than they must.  What lies past
+        // the rank or the part arrives as zeros.
         auto load = [&](int blk) {
             if (r == 0) return;
             const Blocks k = block_at(p, blk);
             const uint32_t to = ring + (uint32_t)((blk - b0) % kUpRing) * kStage;
 #pragma unroll
             for (int j = 0; j < (kGranules + kUpThreads - 1) / kUpThreads; ++j) {
-                const int i = tid + j * kUpThreads, col = i / (2 * C), r0 = i % (2 * C) * 8, n = k.n0 + col;
+                const int i = tid + j * kUpThreads, row = i / (2 * C), piece = i % (2 * C);
                 if (kGranules % kUpThreads && i >= kGranules) break;
-                const int bytes = n < k.end ? min(max(2 * (r - r0), 0), 16) : 0;
-                copy16_async(to + 16 * (i ^ ((i >> 3) & 7)), bytes ? b + (size_t)n * R + r0 : p.b, bytes);
+                const int rg = row & 7, n = k.n0 + (row >> 4) * 16 + (rg >> 1) * 4 + (rg & 1) + (row >> 3 & 1) * 2;
+                const int bytes = n < k.end ? min(max(2 * (r - 8 * piece), 0), 16) : 0;
+                copy16_async(to + row * 32 * C + 16 * (piece ^ swap(rg)), bytes ? b + (size_t)n * R + 8 * piece : p.b, bytes);
             }
         };
         uint4 next0[4], next1[4];
@@ -859,7 +965,7 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapters_up_big_kernel(const __
             }
             float d[4][2][4] = {};
             if (r > 0) {
-                const uint32_t bt = ring + (uint32_t)((blk - b0) % kUpRing) * kStage + 8 * (c & 1);
+                const uint32_t bt = ring + (uint32_t)((blk - b0) % kUpRing) * kStage;
 #pragma unroll
                 for (int q = 0; q < C; ++q) {
                     uint4 a[P];
@@ -869,10 +975,9 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapters_up_big_kernel(const __
                     for (int u = 0; u < 4; ++u)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const int col = 16 * u + (g >> 1) * 4 + (g & 1) + 2 * h, i = col * 2 * C + 2 * q + (c >> 1);
                             uint2 w;
                             asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                                         : "=r"(w.x), "=r"(w.y) : "r"(bt + 16 * (i ^ ((i >> 3) & 7))));
+                                         : "=r"(w.x), "=r"(w.y) : "r"(bt + piece_at[q] + (16 * u + 8 * h) * 32 * C));
 #pragma unroll
                             for (int j = 0; j < P; ++j) mma_bf16_16816(d[u][h], a[j].x, a[j].y, a[j].z, a[j].w, w.x, w.y);
                         }
@@ -883,42 +988,64 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapters_up_big_kernel(const __
             for (int u = 0; u < 4; ++u)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) odd = fmaf(d[u][0][j], 0.f, fmaf(d[u][1][j], 0.f, odd));
+            if (odd != odd) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int n = k.n0 + 16 * u + 4 * c;
+                for (int u = 0; u < 4; ++u)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int t = h ? t1 : t0;
-                    if (t < 0 || n >= k.end) continue;
-                    const uint4 raw = h ? next1[u] : next0[u];
-                    float from[4] = {};
-                    if (BASE == 0 || n + 4 > k.end) {
-                        if (p.base.ptr) load4(p.base, t, n, k.end, p.wide, from);
-                    } else if (BASE == 1) {
-                        bf16x2_to_f32(raw.x, from[0], from[1]);
-                        bf16x2_to_f32(raw.y, from[2], from[3]);
-                    } else {
-                        from[0] = __uint_as_float(raw.x); from[1] = __uint_as_float(raw.y);
-                        from[2] = __uint_as_float(raw.z); from[3] = __uint_as_float(raw.w);
+                    for (int h = 0; h < 2; ++h) {
+                        if ((h ? t1 : t0) < 0) continue;
+                        float v[4] = {d[u][0][2 * h], d[u][0][2 * h + 1], d[u][1][2 * h], d[u][1][2 * h + 1]};
+                        plain_up(p, low0 + (h ? 8 * step : 0), scale, b, k.n0 + 16 * u + 4 * c, r, v);
+                        d[u][0][2 * h] = v[0]; d[u][0][2 * h + 1] = v[1]; d[u][1][2 * h] = v[2]; d[u][1][2 * h + 1] = v[3];
                     }
-                    float v[4] = {d[u][0][2 * h], d[u][0][2 * h + 1], d[u][1][2 * h], d[u][1][2 * h + 1]};
-                    if (odd != odd) plain_up(p, low0 + (h ? 8 * step : 0), scale, b, n, r, v);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) d[u][j >> 1][2 * h + (j & 1)] = v[j] + from[j];
-                }
             }
-            fetch(blk + 1);              // base is in the sums: the next block's may come
+            if (k.n0 + kUpBlock <= k.end && p.wide) {
+                if (BASE != 0) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int n = k.n0 + 16 * u + 4 * c;
+                    for (int u = 0; u < 4; ++u)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint4 raw = h ? next1[u] : next0[u];
+                            float from[4];
+                            if (BASE == 1) {
+                                bf16x2_to_f32(raw.x, from[0], from[1]);
+                                bf16x2_to_f32(raw.y, from[2], from[3]);
+                            } else {
+                                from[0] = __uint_as_float(raw.x); from[1] = __uint_as_float(raw.y);
+                                from[2] = __uint_as_float(raw.z); from[3] = __uint_as_float(raw.w);
+                            }
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) d[u][j >> 1][2 * h + (j & 1)] += from[j];
+                        }
+                    fetch(blk + 1);      // base is in the sums: the next block's may come
+                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int t = h ? t1 : t0;
-                    if (t < 0 || n >= k.end) continue;
-                    const float v[4] = {d[u][0][2 * h], d[u][0][2 * h + 1], d[u][1][2 * h], d[u][1][2 * h + 1]};
-                    if (put) put4(p.y, t, n, k.end, p.wide, v);
-                    if (put32) put4(p.y32, t, n, k.end, p.wide, v);
+                    if ((h ? t1 : t0) < 0) continue;
+                    char *to = (h ? to1 : to0) + 2 * (size_t)(k.n0 + 4 * c), *to32 = (h ? to321 : to320) + 4 * (size_t)(k.n0 + 4 * c);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const float v[4] = {d[u][0][2 * h], d[u][0][2 * h + 1], d[u][1][2 * h], d[u][1][2 * h + 1]};
+                        if (put) put_wide(to, false, 16 * u, v);
+                        if (put32) put_wide(to32, true, 16 * u, v);
+                    }
                 }
+            } else {
+                // the part's last columns, or rows that do not allow wide accesses
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int t = h ? t1 : t0, n = k.n0 + 16 * u + 4 * c;
+                        if (t < 0 || n >= k.end) continue;
+                        float v[4] = {d[u][0][2 * h], d[u][0][2 * h + 1], d[u][1][2 * h], d[u][1][2 * h + 1]}, from[4] = {};
+                        if (p.base.ptr) load4(p.base, t, n, k.end, p.wide, from);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[j] += from[j];
+                        if (put) put4(p.y, t, n, k.end, p.wide, v);
+                        if (put32) put4(p.y32, t, n, k.end, p.wide, v);
+                    }
+                fetch(blk + 1);
             }
         }
         copies_wait<0>();
@@ -1115,7 +1242,7 @@ extern "C" dl_status dl_linear_adapters(const dl_adapters* adapters, const dl_ro
     for (const Rows* r : {&p.base, &p.y, &p.y32})
         if (r->ptr) p.wide = p.wide && !(((uintptr_t)r->ptr | (uintptr_t)r->stride) & (r->f32 ? 15 : 7));
     const long long small = tokens <= kFewTokens ? tokens : max_small(tokens, p.num);
-    if (small * ((N + 15) / 16) > 0x7fff0000LL)
+    if (small * ((N + 15) / 16) > 0x7fff0000LL || small * p.parts * ((p.rank + 15) / 16) > 0x7fff0000LL)
         return host_fail(DL_ERR_UNSUPPORTED_SHAPE, "tokens=%d with N=%d exceed one launch", tokens, N);
     HostDevice dev;
     if ((s = host_device(dev)) != DL_OK) return s;
