@@ -1,7 +1,7 @@
 // Low-rank adapters of many requests beside a shared projection (dl_linear_adapters).
 #include <cooperative_groups.h>
 
-#include <atomic>
+#include <type_traits>
 
 #include "dl_device.cuh"
 #include "dl_host.h"
@@ -30,7 +30,7 @@ struct AdapterParams {
     int* tiles;              // more than kFewTokens tokens: what sort_tokens_kernel writes
     int big_from;            // kBigFrom, or none if ranks are too large
     bool in_place, in_place32;   // base is y, y32: rows without an adapter stay as they are
-    bool wide;               // four consecutive columns of base, y and y32 are aligned to their size
+    bool wide;               // groups of eight columns of base, y and y32 are 16-byte aligned
     // big tiles
     float* low_big;          // [tokens][parts * rank], by place in `order`, without scale
     WaitCtl wait;
@@ -38,12 +38,12 @@ struct AdapterParams {
 
 // Tokens of one adapter, up to kTile of them; the others -1.
 struct Tile {
-    int adapter;             // -1: tokens without one
+    int adapter, rank;       // adapter -1, rank 0: tokens without one
     int token[kTile];
 };
 // Tokens order[first .. first + count) of one adapter.
 struct BigTile {
-    int adapter, first, count, unused;
+    int adapter, first, count, rank;
 };
 
 // The lists of more than kFewTokens tokens.
@@ -101,6 +101,7 @@ __device__ __forceinline__ int make_tiles(const AdapterParams& p, FewTiles& s) {
     const int T = p.tokens, t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const unsigned below = (1u << lane) - 1;
     const int mine = t < T ? adapter_of(p, t) : -2;
+    const int r = rank_of(p, mine);      // (its load overlaps what follows)
     for (int i = t; i < T * (int)(sizeof(Tile) / 4); i += blockDim.x) reinterpret_cast<int*>(s.tile)[i] = -1;
     if (T <= 32) {
         __syncthreads();
@@ -111,7 +112,10 @@ __device__ __forceinline__ int make_tiles(const AdapterParams& p, FewTiles& s) {
             if (t < T) {
                 const int opener = nth_bit(same, place / kTile * kTile);
                 Tile& tile = s.tile[__popc(m & ((1u << opener) - 1))];
-                if (opener == t) tile.adapter = mine;
+                if (opener == t) {
+                    tile.adapter = mine;
+                    tile.rank = r;
+                }
                 tile.token[place % kTile] = t;
             }
             if (lane == 0) s.n = __popc(m);
@@ -162,6 +166,7 @@ __device__ __forceinline__ int make_tiles(const AdapterParams& p, FewTiles& s) {
         const int number = first + __popc(same & below);
         s.number[at][place / kTile] = (unsigned char)number;
         s.tile[number].adapter = mine;
+        s.tile[number].rank = r;
     }
     __syncthreads();
     if (t < T) s.tile[s.number[at][place / kTile]].token[place % kTile] = t;
@@ -222,14 +227,15 @@ __global__ void __launch_bounds__(1024) sort_tokens_kernel(const __grid_constant
                 total[j] += warp_sum[j][w];
             }
         }
-        const int ad = i < p.num ? i : -1;
+        const int ad = i < p.num ? i : -1, r = n ? rank_of(p, ad) : 0;
         for (int j = 0; j < mine[0]; ++j) {
             Tile& tile = l.small[first[0] + j];
             tile.adapter = ad;
+            tile.rank = r;
             for (int k = min(n - j * kTile, kTile); k < kTile; ++k) tile.token[k] = -1;
         }
         for (int j = 0; j < mine[1]; ++j)
-            l.big[first[1] + j] = BigTile{ad, first[2] + j * kBigTile, min(n - j * kBigTile, kBigTile), 0};
+            l.big[first[1] + j] = BigTile{ad, first[2] + j * kBigTile, min(n - j * kBigTile, kBigTile), r};
         if (i <= p.num) count[i] = big ? kBig | (unsigned)first[2] : (unsigned)first[0] * kTile;
     }
     __syncthreads();
@@ -267,11 +273,12 @@ __global__ void __launch_bounds__(1024) sort_tokens_kernel(const __grid_constant
 // a tile's 16 tokens over its part of K.  A (and x) go from global memory straight into
 // the operands of mma.m16n8k16: the sum over k may take its terms in any order, so a lane's
 // 16-byte load of 8 consecutive k is the k-slots that it holds in two products.
+template <int N>
+using Int = std::integral_constant<int, N>;
 constexpr int kLowThreads = 256, kLowWarps = kLowThreads / 32;
 constexpr int kLowCluster = 8;
 
-template <bool FEW>
-__global__ void __launch_bounds__(kLowThreads) adapters_low_kernel(const __grid_constant__ AdapterParams p) {
+__global__ void __launch_bounds__(kLowThreads, 2) adapters_low_kernel(const __grid_constant__ AdapterParams p) {
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
     extern __shared__ __align__(16) unsigned char smem[];
@@ -283,7 +290,7 @@ __global__ void __launch_bounds__(kLowThreads) adapters_low_kernel(const __grid_
     griddep_launch_dependents();
     const Tile* tiles;
     int n_tiles;
-    if (FEW) {
+    if (p.tokens <= kFewTokens) {
         FewTiles& s = *reinterpret_cast<FewTiles*>(smem);
         n_tiles = make_tiles(p, s);
         tiles = s.tile;
@@ -303,9 +310,7 @@ __global__ void __launch_bounds__(kLowThreads) adapters_low_kernel(const __grid_
         const unsigned i = item % per;
         const int j0 = (int)(i % groups) * 16, pt = (int)(i / groups);
         const Tile& tile = tiles[item / per];
-        const int ad = tile.adapter;
-        if (ad < 0) continue;
-        const int r = rank_of(p, ad);
+        const int ad = tile.adapter, r = tile.rank;
         if (j0 >= r) continue;
         const int t0 = tile.token[g], t1 = tile.token[g + 8];
         const bool two = tile.token[8] >= 0, row0 = j0 + g < r, row1 = j0 + g + 8 < r;
@@ -314,38 +319,40 @@ __global__ void __launch_bounds__(kLowThreads) adapters_low_kernel(const __grid_
         const char *x0 = row_ptr(p.x, max(t0, 0)) + 16 * c, *x1 = row_ptr(p.x, max(t1, 0)) + 16 * c;
         float d0[4] = {}, d1[4] = {};
         const uint4 none = {0, 0, 0, 0};
-        auto step = [&](int run, bool in) {              // every lane takes part in every product
-            const uint4 va = in && row0 ? ldg128(a0 + run) : none, vb = in && row1 ? ldg128(a1 + run) : none;
-            const uint4 xa = in && t0 >= 0 ? ldg128(x0 + 2 * run) : none;
-            mma_bf16_16816(d0, va.x, vb.x, va.y, vb.y, xa.x, xa.y);
-            mma_bf16_16816(d0, va.z, vb.z, va.w, vb.w, xa.z, xa.w);
-            if (two) {
-                const uint4 xb = in && t1 >= 0 ? ldg128(x1 + 2 * run) : none;
-                mma_bf16_16816(d1, va.x, vb.x, va.y, vb.y, xb.x, xb.y);
-                mma_bf16_16816(d1, va.z, vb.z, va.w, vb.w, xb.z, xb.w);
-            }
-        };
-        int run = k0;
-        for (; run + 128 <= k1 && run + 128 <= K; run += 128) {
-            uint4 va[4], vb[4], xa[4], xb[4];
+        // `n` runs at a time, their loads all in flight; every lane takes part in every product
+        auto steps = [&](auto count, auto second, int run) {
+            constexpr int n = decltype(count)::value;
+            constexpr bool both = decltype(second)::value;
+            uint4 va[n], vb[n], xa[n], xb[both ? n : 1];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                va[i] = row0 ? ldg128(a0 + run + 32 * i) : none;
-                vb[i] = row1 ? ldg128(a1 + run + 32 * i) : none;
-                xa[i] = t0 >= 0 ? ldg128(x0 + 2 * (run + 32 * i)) : none;
-                xb[i] = t1 >= 0 ? ldg128(x1 + 2 * (run + 32 * i)) : none;
+            for (int i = 0; i < n; ++i) {
+                const int k = run + 32 * i;
+                const bool in = n > 1 || k + 8 * c < K;
+                va[i] = in && row0 ? ldg128(a0 + k) : none;
+                vb[i] = in && row1 ? ldg128(a1 + k) : none;
+                xa[i] = in && t0 >= 0 ? ldg128(x0 + 2 * k) : none;
+                if (both) xb[i] = in && t1 >= 0 ? ldg128(x1 + 2 * k) : none;
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < n; ++i) {
                 mma_bf16_16816(d0, va[i].x, vb[i].x, va[i].y, vb[i].y, xa[i].x, xa[i].y);
                 mma_bf16_16816(d0, va[i].z, vb[i].z, va[i].w, vb[i].w, xa[i].z, xa[i].w);
-                if (two) {
+                if (both) {
                     mma_bf16_16816(d1, va[i].x, vb[i].x, va[i].y, vb[i].y, xb[i].x, xb[i].y);
                     mma_bf16_16816(d1, va[i].z, vb[i].z, va[i].w, vb[i].w, xb[i].z, xb[i].w);
                 }
             }
+        };
+        const int whole = min(k1, K / 32 * 32);
+        int run = k0;
+        if (two) {
+            for (; run + 128 <= whole; run += 128) steps(Int<4>(), std::true_type(), run);
+            for (; run < k1; run += 32) steps(Int<1>(), std::true_type(), run);
+        } else {
+            for (; run + 256 <= whole; run += 256) steps(Int<8>(), std::false_type(), run);
+            for (; run + 128 <= whole; run += 128) steps(Int<4>(), std::false_type(), run);
+            for (; run < k1; run += 32) steps(Int<1>(), std::false_type(), run);
         }
-        for (; run < k1; run += 32) step(run, run + 8 * c < K);
         // sum[warp][token * 16 + row]
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -376,9 +383,10 @@ __global__ void __launch_bounds__(kLowThreads) adapters_low_kernel(const __grid_
 
 // ---------------------------------------------------------------- second product
 
-// out[t][n] = base[t][n] + sum_r low[t][r] B[n][r]: tokens are the rows of mma.m16n8k16, 16
-// columns of a warp two products.  Which n is which product's column is chosen so that a lane's
-// results are four consecutive columns; r is dealt to k-slots as k is above.
+// out[t][n] = base[t][n] + sum_r low[t][r] B[n][r]: tokens are the rows of the product, 16 for a warp,
+// B's rows its columns.  32 consecutive columns are four products of 8 whose results lie four lanes to a
+// row, two columns a lane; which column is which product's is chosen so that a lane's eight results are
+// consecutive: lane c of a row has columns 8 c .. 8 c + 7, product i has 2 i and 2 i + 1 of each lane's.
 //
 // The fp32 values of `low` go into the products as two bf16 parts (2^-18 of the value is lost), three
 // (24 bits: nothing) where an fp32 result is asked for.  The parts of a value and their products can
@@ -404,33 +412,22 @@ __device__ __forceinline__ Parts split(float a, float b, int parts) {
     return r;
 }
 
-__device__ __forceinline__ void load4(const Rows& m, int t, int n, int N, bool wide, float (&v)[4]) {
-    const char* row = row_ptr(m, t);
-    if (wide && n + 4 <= N) {
-        if (m.f32) {
-            const uint4 u = ldg128(row + 4 * (size_t)n);
-            v[0] = __uint_as_float(u.x); v[1] = __uint_as_float(u.y); v[2] = __uint_as_float(u.z); v[3] = __uint_as_float(u.w);
-        } else {
-            const uint2 u = ldg64(row + 2 * (size_t)n);
-            bf16x2_to_f32(u.x, v[0], v[1]);
-            bf16x2_to_f32(u.y, v[2], v[3]);
-        }
+// Eight columns of a row from n on, as far as `end`; `wide`: whole and aligned.
+__device__ __forceinline__ void load_cols(const char* row, bool f32, int n, int end, bool wide, float (&v)[8]) {
+    if (wide) {
+        row_load8(row, f32, n, v);
     } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = n + k < N ? row_load1(row, m.f32, n + k) : 0.f;
+        for (int k = 0; k < 8; ++k) v[k] = n + k < end ? row_load1(row, f32, n + k) : 0.f;
     }
 }
-__device__ __forceinline__ void put4(const Rows& m, int t, int n, int N, bool wide, const float (&v)[4]) {
-    char* row = row_ptr(m, t);
-    if (wide && n + 4 <= N) {
-        if (m.f32)
-            *reinterpret_cast<float4*>(row + 4 * (size_t)n) = make_float4(v[0], v[1], v[2], v[3]);
-        else
-            *reinterpret_cast<uint2*>(row + 2 * (size_t)n) = make_uint2(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]));
+__device__ __forceinline__ void put_cols(char* row, bool f32, int n, int end, bool wide, const float (&v)[8]) {
+    if (wide) {
+        row_store8(row, f32, n, v);
     } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (n + k < N) row_store1(row, m.f32, n + k, v[k]);
+        for (int k = 0; k < 8; ++k)
+            if (n + k < end) row_store1(row, f32, n + k, v[k]);
     }
 }
 
@@ -440,11 +437,11 @@ __device__ __forceinline__ int part_of(const AdapterParams& p, int n) {
     return pt;
 }
 
-// Sums of four columns from n on that came out NaN, as they stand; low: the token's first products, times
+// Sums of eight columns from n on that came out NaN, as they stand; low: the token's first products, times
 // scale.
 __device__ __noinline__ void plain_up(const AdapterParams& p, const float* low, float scale, const uint16_t* b, int n, int r,
-                                      float (&v)[4]) {
-    for (int k = 0; k < 4; ++k) {
+                                      float (&v)[8]) {
+    for (int k = 0; k < 8; ++k) {
         if (v[k] == v[k] || n + k >= p.N) continue;
         const float* s = low + part_of(p, n + k) * p.rank;
         v[k] = 0.f;
@@ -458,36 +455,18 @@ __device__ __forceinline__ uint2 rank_mask(int at, int r) {
                       (at + 2 < r ? 0xffffu : 0u) | (at + 3 < r ? 0xffff0000u : 0u));
 }
 
-// A token's results in one tensor: 16 columns of a warp's, four of them this lane's, from n on.
-__device__ __forceinline__ void put_wide(char* row, bool f32, int n, const float (&v)[4]) {
-    if (f32)
-        *reinterpret_cast<float4*>(row + 4 * (size_t)n) = make_float4(v[0], v[1], v[2], v[3]);
-    else
-        *reinterpret_cast<uint2*>(row + 2 * (size_t)n) = make_uint2(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]));
-}
-__device__ __forceinline__ void load_wide(const char* row, bool f32, int n, float (&v)[4]) {
-    if (f32) {
-        const uint4 u = ldg128(row + 4 * (size_t)n);
-        v[0] = __uint_as_float(u.x); v[1] = __uint_as_float(u.y); v[2] = __uint_as_float(u.z); v[3] = __uint_as_float(u.w);
-    } else {
-        const uint2 u = ldg64(row + 2 * (size_t)n);
-        bf16x2_to_f32(u.x, v[0], v[1]);
-        bf16x2_to_f32(u.y, v[2], v[3]);
-    }
-}
-
-// Small tiles: a warp takes U times 16 columns of a tile, B's values of 16 C at a time.  What does not depend
-// on the first products (the tiles, base, B) is fetched before they are waited for: the kernel that
-// makes them lets this one start only after it had waited for all earlier ones.
+// Small tiles: a warp takes 32 columns of a tile, B's values of 32 r at a time.  What does not depend on the
+// first products (the tiles, base, B) is fetched before they are waited for: the kernel that makes them lets
+// this one start only after it had waited for all earlier ones.  P: parts of a first product.
 constexpr int kUpThreads = 256, kUpWarps = kUpThreads / 32;
 
-template <bool FEW, int U, int C>
+template <int P>
 __global__ void __launch_bounds__(kUpThreads, 2) adapters_up_kernel(const __grid_constant__ AdapterParams p) {
     extern __shared__ __align__(16) unsigned char smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
     const Tile* tiles;
     int n_tiles;
-    if (FEW) {
+    if (p.tokens <= kFewTokens) {
         FewTiles& s = *reinterpret_cast<FewTiles*>(smem);
         n_tiles = make_tiles(p, s);
         tiles = s.tile;
@@ -496,94 +475,67 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapters_up_kernel(const __grid
         n_tiles = l.counts[0];
         tiles = l.small;
     }
-    const int R = p.rank, N = p.N, parts = p.y32.ptr ? 3 : 2;
-    const unsigned units = (N + 16 * U - 1) / (16 * U), items = n_tiles * units;    // fits: a launch of more is refused
+    const int R = p.rank, N = p.N;
+    const unsigned units = (N + 31) / 32, items = n_tiles * units;      // fits: a launch of more is refused
     const size_t step = (size_t)p.parts * R;
     bool waited = false;
     for (unsigned item = blockIdx.x * kUpWarps + warp; item < items; item += gridDim.x * kUpWarps) {
         const Tile& tile = tiles[item / units];
-        const int n0 = (int)(item % units) * 16 * U;
-        const int ad = tile.adapter, t0 = tile.token[g], t1 = tile.token[g + 8];
-        const int r = rank_of(p, ad);
-        const bool whole = n0 + 16 * U <= N, fast = whole && p.wide;
+        const int n0 = (int)(item % units) * 32, n = n0 + 8 * c;
+        const int ad = tile.adapter, r = tile.rank, t0 = tile.token[g], t1 = tile.token[g + 8];
+        const bool whole = n0 + 32 <= N, wide = whole && p.wide;
         const uint16_t* b = p.b + (size_t)max(ad, 0) * N * R;
-        float base[U][2][4];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) base[u][0][k] = base[u][1][k] = 0.f;
+        float base[2][8] = {};
         if (p.base.ptr) {
-            const char *from0 = row_ptr(p.base, max(t0, 0)), *from1 = row_ptr(p.base, max(t1, 0));
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int n = n0 + 16 * u + 4 * c;
-                if (fast) {
-                    if (t0 >= 0) load_wide(from0, p.base.f32, n, base[u][0]);
-                    if (t1 >= 0) load_wide(from1, p.base.f32, n, base[u][1]);
-                } else {
-                    if (t0 >= 0) load4(p.base, t0, n, N, p.wide, base[u][0]);
-                    if (t1 >= 0) load4(p.base, t1, n, N, p.wide, base[u][1]);
-                }
-            }
+            if (t0 >= 0) load_cols(row_ptr(p.base, t0), p.base.f32, n, N, wide, base[0]);
+            if (t1 >= 0) load_cols(row_ptr(p.base, t1), p.base.f32, n, N, wide, base[1]);
         }
-        float d[U][2][4] = {};               // [product][row g: 2 columns, row g + 8: 2 columns]
-        const int col0 = n0 + (g >> 1) * 4 + (g & 1);
-        for (int r0 = 0; r0 < r; r0 += 16 * C) {
-            uint2 w[C][U][2];
-            const uint16_t* bl = b + (size_t)col0 * R + r0 + 4 * c;
+        const int pt = part_of(p, n0), second = min(pt + 1, p.parts - 1);
+        const bool two = pt < second && n0 + 16 >= p.part_end[pt];      // the last 16 columns are the next part's
+        float d[4][4] = {};                  // [product][row g: 2 columns, row g + 8: 2 columns]
+        const int col = n0 + (g >> 1) * 8 + (g & 1);                    // of product 0; the others' are 2, 4, 6 further
+        for (int r0 = 0; r0 < r; r0 += 32) {
+            uint2 w[2][4];
+            const uint16_t* bl = b + (size_t)col * R + r0 + 4 * c;
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+            for (int q = 0; q < 2; ++q)
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int q = 0; q < C; ++q) {
-                        const bool in = r0 + 16 * q + 4 * c < r && (whole || col0 + 16 * u + 2 * i < N);
-                        w[q][u][i] = in ? ldg64(bl + (16 * u + 2 * i) * R + 16 * q) : make_uint2(0, 0);
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    const bool in = r0 + 16 * q + 4 * c < r && (whole || col + 2 * i < N);
+                    w[q][i] = in ? ldg64(bl + 2 * i * R + 16 * q) : make_uint2(0, 0);
+                }
             if (!waited) {
                 griddep_wait();
                 griddep_launch_dependents();
                 waited = true;
             }
-            int held = -1;                   // the part whose first products `a` has
-            Parts a[C][4];
+            for (int k = 0; k <= (two ? 1 : 0); ++k) {
+                const float *low0 = p.low + t0 * step + (k ? second : pt) * R + r0 + 4 * c;
+                const float* low1 = p.low + t1 * step + (k ? second : pt) * R + r0 + 4 * c;
+                float4 s0[2], s1[2];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int pt = part_of(p, n0 + 16 * u);
-                if (pt != held) {
-                    held = pt;
-                    const float *low0 = p.low + t0 * step + pt * R + r0 + 4 * c, *low1 = p.low + t1 * step + pt * R + r0 + 4 * c;
-                    float4 s0[C], s1[C];
-#pragma unroll
-                    for (int q = 0; q < C; ++q) {
-                        const bool in = r0 + 16 * q + 4 * c < r;
-                        s0[q] = in && t0 >= 0 ? ld_cg_f32x4(low0 + 16 * q) : make_float4(0.f, 0.f, 0.f, 0.f);
-                        s1[q] = in && t1 >= 0 ? ld_cg_f32x4(low1 + 16 * q) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    }
-#pragma unroll
-                    for (int q = 0; q < C; ++q) {
-                        const int at = r0 + 16 * q + 4 * c;
-                        const bool in1 = at + 1 < r, in2 = at + 2 < r, in3 = at + 3 < r;
-                        a[q][0] = split(s0[q].x, in1 ? s0[q].y : 0.f, parts);
-                        a[q][1] = split(s1[q].x, in1 ? s1[q].y : 0.f, parts);
-                        a[q][2] = split(in2 ? s0[q].z : 0.f, in3 ? s0[q].w : 0.f, parts);
-                        a[q][3] = split(in2 ? s1[q].z : 0.f, in3 ? s1[q].w : 0.f, parts);
-                    }
+                for (int q = 0; q < 2; ++q) {
+                    const bool in = r0 + 16 * q + 4 * c < r;
+                    s0[q] = in && t0 >= 0 ? ld_cg_f32x4(low0 + 16 * q) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    s1[q] = in && t1 >= 0 ? ld_cg_f32x4(low1 + 16 * q) : make_float4(0.f, 0.f, 0.f, 0.f);
                 }
+                // lanes g < 4 bring the first 16 columns of B, the others the last
+                const bool mine = !two || (g >= 4) == (k == 1);
 #pragma unroll
-                for (int q = 0; q < C; ++q) {
+                for (int q = 0; q < 2; ++q) {
                     const int at = r0 + 16 * q + 4 * c;
                     if (r0 + 16 * q >= r) break;
-                    const uint2 m = rank_mask(at, r);
+                    uint2 m = rank_mask(at, r);
+                    if (!mine) m = make_uint2(0, 0);
+                    const bool in1 = at + 1 < r, in2 = at + 2 < r, in3 = at + 3 < r;
+                    const Parts a0 = split(s0[q].x, in1 ? s0[q].y : 0.f, P), a1 = split(s1[q].x, in1 ? s1[q].y : 0.f, P);
+                    const Parts a2 = split(in2 ? s0[q].z : 0.f, in3 ? s0[q].w : 0.f, P);
+                    const Parts a3 = split(in2 ? s1[q].z : 0.f, in3 ? s1[q].w : 0.f, P);
 #pragma unroll
-                    for (int i = 0; i < 3; ++i) {
-                        if (i < parts) {
-                            mma_bf16_16816(d[u][0], a[q][0].v[i], a[q][1].v[i], a[q][2].v[i], a[q][3].v[i], w[q][u][0].x & m.x,
-                                           w[q][u][0].y & m.y);
-                            mma_bf16_16816(d[u][1], a[q][0].v[i], a[q][1].v[i], a[q][2].v[i], a[q][3].v[i], w[q][u][1].x & m.x,
-                                           w[q][u][1].y & m.y);
-                        }
-                    }
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int j = 0; j < P; ++j)
+                            mma_bf16_16816(d[i], a0.v[j], a1.v[j], a2.v[j], a3.v[j], w[q][i].x & m.x, w[q][i].y & m.y);
                 }
             }
         }
@@ -594,30 +546,22 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapters_up_kernel(const __grid
         }
         float odd = 0.f;                     // NaN if any sum is, or infinite
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) odd = fmaf(d[u][0][k], 0.f, fmaf(d[u][1][k], 0.f, odd));
-        const bool put = ad >= 0 || !p.in_place, put32 = p.y32.ptr && (ad >= 0 || !p.in_place32);
+            for (int k = 0; k < 4; ++k) odd = fmaf(d[i][k], 0.f, odd);
+        const bool put = ad >= 0 || !p.in_place, put32 = P == 3 && (ad >= 0 || !p.in_place32);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {        // rows t0 and t1
             const int t = h ? t1 : t0;
             if (t < 0) continue;
-            char *to = row_ptr(p.y, t), *to32 = row_ptr(p.y32, t);
+            float v[8];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int n = n0 + 16 * u + 4 * c;
-                float v[4] = {d[u][0][2 * h], d[u][0][2 * h + 1], d[u][1][2 * h], d[u][1][2 * h + 1]};
-                if (odd != odd) plain_up(p, p.low + t * step, 1.f, b, n, r, v);
+            for (int k = 0; k < 8; ++k) v[k] = d[k >> 1][2 * h + (k & 1)];
+            if (odd != odd) plain_up(p, p.low + t * step, 1.f, b, n, r, v);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] += base[u][h][k];
-                if (fast) {
-                    if (put) put_wide(to, false, n, v);
-                    if (put32) put_wide(to32, true, n, v);
-                } else {
-                    if (put) put4(p.y, t, n, N, p.wide, v);
-                    if (put32) put4(p.y32, t, n, N, p.wide, v);
-                }
-            }
+            for (int k = 0; k < 8; ++k) v[k] += base[h][k];
+            if (put) put_cols(row_ptr(p.y, t), false, n, N, wide, v);
+            if (put32) put_cols(row_ptr(p.y32, t), true, n, N, wide, v);
         }
     }
     if (!waited) griddep_wait();
@@ -651,17 +595,18 @@ __device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t a_desc, uint
 // thread issues the products.  A cluster shares K: each CTA leaves its sums in its shared memory,
 // where the cluster's CTAs add them up, a share of the tokens each, always in the same order.
 constexpr int kBigThreads = 256;
-constexpr int kBigStages = 4;
 constexpr int kBigCols = 256;            // rows of A of one CTA, at most
 
 struct BigSmem {
-    int cols, stage, total;              // columns of the accumulator, bytes of a stage, and of all
+    int cols, stage, stages, total;      // columns of the accumulator, bytes of a stage, stages, bytes of all
 };
 __host__ __device__ inline BigSmem big_smem(int columns) {
     BigSmem s;
     s.cols = (columns < kBigCols ? columns + 15 : kBigCols) / 16 * 16;
-    s.stage = (kBigTile + s.cols) * 128;     // four of them hold the sums, 128 x (cols + 4) x 4 bytes, too
-    s.total = 1024 + kBigStages * s.stage + 256;
+    s.stage = (kBigTile + s.cols) * 128;
+    s.stages = (224 * 1024) / s.stage;       // 4 to 12; four hold the sums, 128 x (cols + 4) x 4 bytes, too
+    if (s.stages > 6) s.stages = 6;
+    s.total = 1024 + s.stages * s.stage + 256;
     return s;
 }
 
@@ -674,8 +619,9 @@ __global__ void __launch_bounds__(kBigThreads) adapters_low_big_kernel(const __g
     const Lists l = lists_of(p.tiles, p.tokens, p.num);
     const int SR = p.parts * p.rank, K = p.K;
     const BigSmem shape = big_smem(SR);
-    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u, bars = base + kBigStages * shape.stage;
-    const uint32_t slot = bars + 8 * kBigStages;
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u, bars = base + shape.stages * shape.stage;
+    const uint32_t slot = bars + 8 * shape.stages;
+    const int stages = shape.stages;
     // The lists are complete and the buffers free: the kernel before this one let it start only after
     // it had waited for sort_tokens_kernel.  (Its own results are other ones; the wait is at the end.)
     const int n_tiles = l.counts[1];
@@ -688,7 +634,7 @@ __global__ void __launch_bounds__(kBigThreads) adapters_low_big_kernel(const __g
     while ((int)tmem_cols < shape.cols) tmem_cols *= 2;
     if (warp == 0) tmem_alloc(slot, tmem_cols);
     if (tid == 0) {
-        for (int i = 0; i < kBigStages; ++i) mbar_init(bars + 8 * i, 1);
+        for (int i = 0; i < stages; ++i) mbar_init(bars + 8 * i, 1);
         fence_mbarrier_init();
     }
     tc_fence_before_sync();
@@ -706,73 +652,93 @@ __global__ void __launch_bounds__(kBigThreads) adapters_low_big_kernel(const __g
     const uint32_t put = (uint32_t)(row0 * 128 + ((chunk ^ (row0 & 7)) << 4));      // rows 32 apart keep row & 7
     float* sums = reinterpret_cast<float*>(raw + (base - smem_u32(raw)));
     const int pitch = shape.cols + 4;
-    int used = 0;                        // steps of earlier tiles
+    // the stage that the next step's products read, how often it has been read, and its place
+    int stage = 0, parity = 0;
     bool dead = false;                   // a wait gave up: the CTA goes on with the cluster, without its copies and products
     for (int ti = blockIdx.y; ti < n_tiles; ti += gridDim.y) {
         const BigTile tile = l.big[ti];
         if (tile.adapter < 0) continue;
-        const int r = rank_of(p, tile.adapter);
-        // what this thread copies: a 16-byte chunk of four rows of x and of every 32nd row of A; a row
-        // that is not there arrives as zeros
+        const int r = tile.rank;
+        // What this thread copies: a 16-byte chunk of four rows of x and of every 32nd row of A.  Rows that are not
+        // there are zeros in every stage, written once: no copy touches them.
         const char* xr[kBigTile / 32];
-        int xb[kBigTile / 32];
 #pragma unroll
         for (int i = 0; i < kBigTile / 32; ++i) {
             const int row = row0 + 32 * i;
-            xb[i] = row < tile.count ? 16 : 0;
-            xr[i] = (xb[i] ? row_ptr(p.x, l.order[tile.first + row]) : p.x.ptr) + 16 * chunk + s0 * 128;
+            xr[i] = row < tile.count ? row_ptr(p.x, l.order[tile.first + row]) + 16 * chunk + s0 * 128 : nullptr;
         }
         const char* ar = reinterpret_cast<const char*>(p.a + ((size_t)tile.adapter * SR + j0 + row0) * K) + 16 * chunk + s0 * 128;
         const size_t a32 = (size_t)K * 64;
         unsigned mine = 0;
         for (int i = 0; 32 * i + row0 < cols; ++i) mine |= ((j0 + 32 * i + row0) % p.rank < r ? 1u : 0u) << i;
-        auto load = [&](int s) {         // step s of this tile
-            const uint32_t to = base + (uint32_t)((used + s) % kBigStages) * shape.stage + put;
-            const int off = s * 128;
-            const bool in = (s0 + s) * 64 + 8 * chunk < K;           // (the last step may end early)
-            const char* none = p.x.ptr;
+        for (int i = 0; i < stages; ++i) {
+            const uint32_t to = base + i * shape.stage + put;
 #pragma unroll
-            for (int i = 0; i < kBigTile / 32; ++i) copy16_async(to + i * 4096, in ? xr[i] + off : none, in ? xb[i] : 0);
+            for (int j = 0; j < kBigTile / 32; ++j)
+                if (!xr[j]) sts128(to + j * 4096, 0, 0, 0, 0);
+            for (int j = 0; 32 * j + row0 < shape.cols; ++j)
+                if (!(mine >> j & 1)) sts128(to + kBigTile * 128 + j * 4096, 0, 0, 0, 0);
+        }
+        // step s of this tile into the stage at `to`
+        auto load = [&](int s, uint32_t to) {
+            const int off = s * 128;
             const char* from = ar + off;
-#pragma unroll 2
-            for (int i = 0; 32 * i + row0 < shape.cols; ++i, from += a32) {
-                const bool take = in && (mine >> i & 1);
-                copy16_async(to + kBigTile * 128 + i * 4096, take ? from : none, take ? 16 : 0);
+            to += put;
+            if ((s0 + s + 1) * 64 <= K) {
+#pragma unroll
+                for (int i = 0; i < kBigTile / 32; ++i)
+                    if (xr[i]) copy16_async(to + i * 4096, xr[i] + off, 16);
+                to += kBigTile * 128;
+#pragma unroll
+                for (int i = 0; i < kBigCols / 32; ++i) {
+                    if (mine >> i & 1) copy16_async(to + i * 4096, from, 16);
+                    from += a32;
+                }
+            } else {                     // the last step of K ends early
+                const int bytes = (s0 + s) * 64 + 8 * chunk < K ? 16 : 0;
+#pragma unroll
+                for (int i = 0; i < kBigTile / 32; ++i)
+                    if (xr[i]) copy16_async(to + i * 4096, bytes ? xr[i] + off : p.x.ptr, bytes);
+                to += kBigTile * 128;
+                for (int i = 0; i < kBigCols / 32; ++i)
+                    if (mine >> i & 1) copy16_async(to + i * 4096, bytes ? from + i * a32 : p.x.ptr, bytes);
             }
         };
         bool bad = dead;
-        for (int s = 0; s < kBigStages - 1; ++s) {
-            if (s < n && !dead) load(s);
+        int fill = stage;                // the stage that the next copies go to
+        for (int s = 0; s < stages - 1; ++s) {
+            if (s < n && !dead) load(s, base + (uint32_t)fill * shape.stage);
+            if (++fill == stages) fill = 0;
             copies_commit();
         }
+        int before = 0, parity_before = 0;       // of step s - 1
         for (int s = 0; s < n; ++s) {
-            copies_wait<kBigStages - 2>();
+            if (stages == 4) copies_wait<2>();
+            else if (stages == 5) copies_wait<3>();
+            else copies_wait<4>();
             fence_async_smem();
             if (__syncthreads_or(bad)) break;
             if (tid == 0) {
                 tc_fence_after_sync();
-                const uint32_t at = base + (uint32_t)((used + s) % kBigStages) * shape.stage;
+                const uint32_t at = base + (uint32_t)stage * shape.stage;
                 const uint64_t xa = umma_desc_sw128(at), wa = umma_desc_sw128(at + kBigTile * 128);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) umma_bf16(tmem, xa + 2 * k, wa + 2 * k, idesc, s > 0 || k > 0);
-                umma_commit(bars + 8 * ((used + s) % kBigStages));
+                umma_commit(bars + 8 * stage);
             }
-            const int next = s + kBigStages - 1;
+            const int next = s + stages - 1;
             if (next < n) {
                 // the stage of step s - 1 is free once its products have read it
-                if (s > 0) {
-                    const int u = used + s - 1;
-                    bad = !mbar_wait_bounded(bars + 8 * (u % kBigStages), (u / kBigStages) & 1, p.wait, kErrConsumerWait);
-                }
-                if (!bad) load(next);
+                if (s > 0) bad = !mbar_wait_bounded(bars + 8 * before, parity_before, p.wait, kErrConsumerWait);
+                if (!bad) load(next, base + (uint32_t)fill * shape.stage);
+                if (++fill == stages) fill = 0;
             }
             copies_commit();
+            before = stage;
+            parity_before = parity;
+            if (++stage == stages) stage = 0, parity ^= 1;
         }
-        if (!bad) {
-            const int u = used + n - 1;
-            bad = !mbar_wait_bounded(bars + 8 * (u % kBigStages), (u / kBigStages) & 1, p.wait, kErrConsumerWait);
-        }
-        used += n;
+        if (!bad) bad = !mbar_wait_bounded(bars + 8 * before, parity_before, p.wait, kErrConsumerWait);
         copies_wait<0>();
         dead = __syncthreads_or(bad);
         tc_fence_after_sync();
@@ -799,9 +765,14 @@ __global__ void __launch_bounds__(kBigThreads) adapters_low_big_kernel(const __g
             for (int i = tid; i < (last - first) * (cols / 4); i += kBigThreads) {
                 const int t = first + i / (cols / 4), j = i % (cols / 4) * 4;
                 float4 v = {0.f, 0.f, 0.f, 0.f};
-                for (int q = 0; q < splits; ++q) {
-                    const float4 w = *reinterpret_cast<const float4*>(cluster.map_shared_rank(sums, q) + t * pitch + j);
-                    v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
+                float4 w[kMaxSplits];
+#pragma unroll
+                for (int q = 0; q < kMaxSplits; ++q)
+                    if (q < splits) w[q] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(sums, q) + t * pitch + j);
+#pragma unroll
+                for (int q = 0; q < kMaxSplits; ++q) {
+                    if (q >= splits) break;
+                    v.x += w[q].x; v.y += w[q].y; v.z += w[q].z; v.w += w[q].w;
                 }
                 *reinterpret_cast<float4*>(out + (size_t)t * SR + j) = v;
             }
@@ -818,239 +789,270 @@ __global__ void __launch_bounds__(kBigThreads) adapters_low_big_kernel(const __g
     griddep_wait();
 }
 
-// Second product of big tiles: a warp has 16 of the tile's tokens, whose first products it keeps in shared
-// memory as bf16 parts in the order of the operands; the CTA goes over blocks of 64 columns of a part, B's
-// rows a few blocks ahead in a ring, base one block ahead in registers.  All tiles' blocks are dealt
-// to the CTAs in equal runs.  Bound by base and out.
-constexpr int kUpBlock = 64, kUpRing = 3;
+// Second product of big tiles, out[t][n] = base[t][n] + sum_r low[t][r] B[n][r] for 128 tokens and blocks of 64
+// columns: bound by base and out.  A block is one product on the tensor cores, 128 x 64 over r and the parts of
+// the first products, which lie in shared memory as bf16 operands; B's rows come a few blocks ahead into a
+// ring, base a block ahead into registers, and while a block is multiplied the one before leaves tensor
+// memory.  The rows of B are put into the order that gives a lane eight consecutive columns (as above).
+// All tiles' blocks are dealt to the CTAs in equal runs.
+constexpr int kUpBlock = 64, kUpRing = 3, kUpCtas = 2, kUpTmem = 2 * kUpBlock;
+static_assert(kUpCtas * kUpTmem <= 512, "tensor memory of an SM");
 
-__host__ __device__ constexpr int up_big_smem(int chunks, int parts) {
-    return kUpWarps * chunks * parts * 512 + kUpRing * kUpBlock * chunks * 32;
+// A: parts of 128 rows, B: ring stages of 64, each in pieces of 64 r with rows of 128 bytes, swizzled.
+__host__ __device__ inline int up_big_smem(int rank, int parts) {
+    const int pieces = (rank + 63) / 64;
+    return 1024 + (parts * kBigTile + kUpRing * kUpBlock) * 128 * pieces + 64;
 }
 
-// Blocks of columns: each lies in one part.
-struct Blocks {
-    int part, n0, end;       // the part, the block's first column, the part's end
-};
-__device__ __forceinline__ int count_blocks(const AdapterParams& p) {
-    int n = 0;
-    for (int i = 0; i < p.parts; ++i) n += (p.part_end[i] - (i ? p.part_end[i - 1] : 0) + kUpBlock - 1) / kUpBlock;
-    return n;
-}
-__device__ __forceinline__ Blocks block_at(const AdapterParams& p, int b) {
-    Blocks k = {0, 0, p.part_end[0]};
-    while (k.part + 1 < p.parts) {
-        const int n = (k.end - k.n0 + kUpBlock - 1) / kUpBlock;
-        if (b < n) break;
-        b -= n;
-        ++k.part;
-        k.n0 = k.end;
-        k.end = p.part_end[k.part];
-    }
-    k.n0 += b * kUpBlock;
-    return k;
+// Blocks of columns, each in one part.
+__device__ __forceinline__ int part_blocks(const AdapterParams& p, int part) {
+    return (p.part_end[part] - (part ? p.part_end[part - 1] : 0) + kUpBlock - 1) / kUpBlock;
 }
 
-// C: runs of 16 r, at least rank / 16; BASE 0: none, or rows that do not allow wide accesses, 1: bf16,
-// 2: fp32; P: parts of a first product
-template <int C, int BASE, int P>
-__global__ void __launch_bounds__(kUpThreads, 2) adapters_up_big_kernel(const __grid_constant__ AdapterParams p) {
-    extern __shared__ __align__(16) unsigned char smem[];
+// 64 columns of 16 rows of tensor memory, as the products of mma.m16n8 lie: v[i] has columns 8 i + 2 c and + 1 of
+// rows g and g + 8.
+__device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, float (&v)[8][4]) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(&v[0][0]);
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+                   "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+                   "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(taddr));
+}
+
+// BASE 0: none, or rows that do not allow wide accesses, 1: bf16, 2: fp32; P: parts of a first product
+template <int BASE, int P>
+__global__ void __launch_bounds__(kUpThreads, kUpCtas) adapters_up_big_kernel(const __grid_constant__ AdapterParams p) {
+    extern __shared__ __align__(16) unsigned char raw[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
     const Lists l = lists_of(p.tiles, p.tokens, p.num);
+    const int R = p.rank, N = p.N, pieces = (R + 63) / 64;
+    const uint32_t a_at = (smem_u32(raw) + 1023u) & ~1023u, ring = a_at + P * kBigTile * 128 * pieces;
+    const uint32_t stage_bytes = kUpBlock * 128 * pieces, bars = ring + kUpRing * stage_bytes, slot = bars + 16;
     // the first products are there: the kernel before this one let it start after it had waited for them
     const int n_tiles = l.counts[1];
-    griddep_launch_dependents();
-    const int R = p.rank, N = p.N;
-    uint4* mine = reinterpret_cast<uint4*>(smem) + warp * C * P * 32 + lane;
-    const uint32_t ring = smem_u32(smem) + kUpWarps * C * P * 512;
-    constexpr int kStage = kUpBlock * C * 32, kGranules = kUpBlock * C * 2;         // 16 bytes each
-    auto swap = [](int row) { return C >= 4 ? row : C == 2 ? row >> 1 : 0; };
-    uint32_t piece_at[C];                // this lane's 8 bytes of a run of 16 r, in its row of eight
-#pragma unroll
-    for (int q = 0; q < C; ++q) piece_at[q] = g * 32 * C + 16 * ((2 * q + (c >> 1)) ^ swap(g)) + 8 * (c & 1);
-    const size_t step = (size_t)p.parts * R;
-    const int blocks = count_blocks(p);
+    int blocks = 0;
+    for (int i = 0; i < p.parts; ++i) blocks += part_blocks(p, i);
     const long long all = (long long)n_tiles * blocks;
     long long at = all * blockIdx.x / gridDim.x;
     const long long end = all * (blockIdx.x + 1) / gridDim.x;
-    while (at < end) {
+    if (at == end) {
+        griddep_launch_dependents();
+        griddep_wait();
+        return;
+    }
+    if (warp == 0) tmem_alloc(slot, kUpTmem);
+    if (tid == 0) {
+        mbar_init(bars, 1);
+        mbar_init(bars + 8, 1);
+        fence_mbarrier_init();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    // only now: a kernel after this one that allocates tensor memory before it waits must find this one's taken
+    griddep_launch_dependents();
+    uint32_t tmem;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(slot));
+    const uint32_t idesc = umma_idesc_bf16(kUpBlock);
+    const int row0 = 32 * (warp & 3) + 16 * (warp >> 2);        // this warp's rows of the tile
+    const size_t step = (size_t)p.parts * R;
+    unsigned made = 0;                   // products so far: the next one's accumulator and phase
+    bool bad = false;
+    while (at < end && !bad) {
+        // a run of blocks of one tile and part: columns n0 on, the part ends at n_end
         const BigTile tile = l.big[at / blocks];
-        const int b0 = (int)(at % blocks), b1 = (int)min((long long)blocks, b0 + end - at);
-        at += b1 - b0;
-        const int ad = tile.adapter, r = rank_of(p, ad);
+        int b0 = (int)(at % blocks), part = 0, n_end = p.part_end[0], n0 = 0;
+        for (int n; b0 >= (n = part_blocks(p, part)); n_end = p.part_end[++part]) {
+            b0 -= n;
+            n0 = n_end;
+        }
+        const int runs = (int)min((long long)(part_blocks(p, part) - b0), end - at);
+        n0 += b0 * kUpBlock;
+        at += runs;
+        const int ad = tile.adapter, r = tile.rank, steps = (r + 15) / 16;
         const float scale = ad >= 0 && p.scale ? p.scale[ad] : 1.f;
-        const bool active = 16 * warp < tile.count;
-        const int i0 = 16 * warp + g, i1 = i0 + 8;
+        const bool active = row0 < tile.count;
+        const int i0 = row0 + g, i1 = i0 + 8;
         const int t0 = i0 < tile.count ? l.order[tile.first + i0] : -1, t1 = i1 < tile.count ? l.order[tile.first + i1] : -1;
         const uint16_t* b = p.b + (size_t)max(ad, 0) * N * R;
-        const char *from0 = row_ptr(p.base, max(t0, 0)), *from1 = row_ptr(p.base, max(t1, 0));
-        char *to0 = row_ptr(p.y, max(t0, 0)), *to1 = row_ptr(p.y, max(t1, 0));
-        char *to320 = row_ptr(p.y32, max(t0, 0)), *to321 = row_ptr(p.y32, max(t1, 0));
-        // A block of B into its ring stage: columns in the order of the products' operands, 16-byte pieces
-        // exchanged by row so that eight rows' reads meet no bank twice more than they must.  What lies past
-        // the rank or the part arrives as zeros.
-        auto load = [&](int blk) {
-            if (r == 0) return;
-            const Blocks k = block_at(p, blk);
-            const uint32_t to = ring + (uint32_t)((blk - b0) % kUpRing) * kStage;
-#pragma unroll
-            for (int j = 0; j < (kGranules + kUpThreads - 1) / kUpThreads; ++j) {
-                const int i = tid + j * kUpThreads, row = i / (2 * C), piece = i % (2 * C);
-                if (kGranules % kUpThreads && i >= kGranules) break;
-                const int rg = row & 7, n = k.n0 + (row >> 4) * 16 + (rg >> 1) * 4 + (rg & 1) + (row >> 3 & 1) * 2;
-                const int bytes = n < k.end ? min(max(2 * (r - 8 * piece), 0), 16) : 0;
-                copy16_async(to + row * 32 * C + 16 * (piece ^ swap(rg)), bytes ? b + (size_t)n * R + 8 * piece : p.b, bytes);
-            }
-        };
-        uint4 next0[4], next1[4];
-        auto fetch = [&](int blk) {      // base of block `blk`
-            const Blocks k = block_at(p, min(blk, b1 - 1));
-#pragma unroll
-            for (int u = 0; BASE != 0 && u < 4; ++u) {
-                const int n = k.n0 + 16 * u + 4 * c;
-                const bool in = blk < b1 && n + 4 <= k.end;
-                if (BASE == 1) {
-                    const uint2 none = {0, 0};
-                    const uint2 x = in && t0 >= 0 ? ldg64(from0 + 2 * (size_t)n) : none;
-                    const uint2 y = in && t1 >= 0 ? ldg64(from1 + 2 * (size_t)n) : none;
-                    next0[u].x = x.x; next0[u].y = x.y;
-                    next1[u].x = y.x; next1[u].y = y.y;
-                } else {
-                    const uint4 none = {0, 0, 0, 0};
-                    next0[u] = in && t0 >= 0 ? ldg128(from0 + 4 * (size_t)n) : none;
-                    next1[u] = in && t1 >= 0 ? ldg128(from1 + 4 * (size_t)n) : none;
-                }
-            }
-        };
-#pragma unroll
-        for (int i = 0; i < kUpRing - 1; ++i) {
-            if (b0 + i < b1) load(b0 + i);
-            copies_commit();
-        }
-        fetch(b0);
-        int held = -1;                   // the part whose first products are in `mine`
-        const float* low0 = p.low_big + (size_t)(tile.first + i0) * step;
         const bool put = ad >= 0 || !p.in_place, put32 = P == 3 && (ad >= 0 || !p.in_place32);
-        for (int blk = b0; blk < b1; ++blk) {
-            copies_wait<kUpRing - 2>();
-            __syncthreads();
-            if (blk + kUpRing - 1 < b1) load(blk + kUpRing - 1);
-            copies_commit();
-            if (!active) continue;
-            const Blocks k = block_at(p, blk);
-            if (k.part != held && r > 0) {
-                held = k.part;
-                __syncwarp();
-                float4 s0[C], s1[C];
-#pragma unroll
-                for (int q = 0; q < C; ++q) {
-                    const float* low = low0 + held * R + 16 * q + 4 * c;
-                    const bool in = 16 * q + 4 * c < r;
-                    s0[q] = in && t0 >= 0 ? ld_cg_f32x4(low) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    s1[q] = in && t1 >= 0 ? ld_cg_f32x4(low + 8 * step) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const char *from0 = row_ptr(p.base, max(t0, 0)) + (size_t)(n0 + 8 * c) * (BASE == 2 ? 4 : 2);
+        const char *from1 = row_ptr(p.base, max(t1, 0)) + (size_t)(n0 + 8 * c) * (BASE == 2 ? 4 : 2);
+        char *to0 = row_ptr(p.y, max(t0, 0)) + (size_t)(n0 + 8 * c) * 2, *to1 = row_ptr(p.y, max(t1, 0)) + (size_t)(n0 + 8 * c) * 2;
+        // B's rows of a block, four threads a row, into its ring stage; what lies past the rank or the part
+        // arrives as zeros
+        const int b_row = tid >> 2, b_col = (b_row >> 5) * 32 + ((b_row & 7) >> 1) * 8 + (b_row >> 3 & 3) * 2 + (b_row & 1);
+        const uint16_t* b_from = b + (size_t)(n0 + b_col) * R + 8 * (tid & 3);
+        const size_t b_step = (size_t)kUpBlock * R;
+        const uint32_t b_to = ring + b_row * 128;
+        int b_left = n_end - n0 - b_col, b_stage = 0;    // the part's columns from this thread's of the next block on
+        auto load = [&]() {              // the next block
+            if (r > 0 && b_left > -kUpBlock) {
+                const uint32_t to = b_to + (uint32_t)b_stage * stage_bytes;
+#pragma unroll 2
+                for (int i = tid & 3, j = 0; i < 2 * steps; i += 4, j += 32) {
+                    const int bytes = b_left > 0 ? min(2 * (r - 8 * i), 16) : 0;
+                    copy16_async(to + (i >> 3) * (kUpBlock * 128) + 16 * ((i & 7) ^ (b_row & 7)), bytes > 0 ? b_from + j : p.b, max(bytes, 0));
                 }
-#pragma unroll
-                for (int q = 0; q < C; ++q) {
-                    const int rr = 16 * q + 4 * c;
-                    const bool in1 = rr + 1 < r, in2 = rr + 2 < r, in3 = rr + 3 < r;
-                    const Parts a0 = split(s0[q].x * scale, in1 ? s0[q].y * scale : 0.f, P);
-                    const Parts a1 = split(s1[q].x * scale, in1 ? s1[q].y * scale : 0.f, P);
-                    const Parts a2 = split(in2 ? s0[q].z * scale : 0.f, in3 ? s0[q].w * scale : 0.f, P);
-                    const Parts a3 = split(in2 ? s1[q].z * scale : 0.f, in3 ? s1[q].w * scale : 0.f, P);
-#pragma unroll
-                    for (int i = 0; i < P; ++i) mine[(q * P + i) * 32] = make_uint4(a0.v[i], a1.v[i], a2.v[i], a3.v[i]);
-                }
-                __syncwarp();
             }
-            float d[4][2][4] = {};
-            if (r > 0) {
-                const uint32_t bt = ring + (uint32_t)((blk - b0) % kUpRing) * kStage;
-#pragma unroll
-                for (int q = 0; q < C; ++q) {
-                    uint4 a[P];
-#pragma unroll
-                    for (int i = 0; i < P; ++i) a[i] = mine[(q * P + i) * 32];
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint2 w;
-                            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                                         : "=r"(w.x), "=r"(w.y) : "r"(bt + piece_at[q] + (16 * u + 8 * h) * 32 * C));
-#pragma unroll
-                            for (int j = 0; j < P; ++j) mma_bf16_16816(d[u][h], a[j].x, a[j].y, a[j].z, a[j].w, w.x, w.y);
-                        }
+            if (++b_stage == kUpRing) b_stage = 0;
+            b_left -= kUpBlock;
+            b_from += b_step;
+            copies_commit();
+        };
+        // The tile's first products of a part, two threads a row
+        auto take = [&]() {
+            const int row = tid >> 1;
+            const float* low = p.low_big + (size_t)(tile.first + min(row, tile.count - 1)) * step + part * R;
+            for (int i = tid & 1; i < 2 * steps; i += 2) {
+                float v[8] = {};
+                if (row < tile.count && 8 * i < r) {     // (8 i + 8 is within the row)
+                    const float4 x = ld_cg_f32x4(low + 8 * i), y = ld_cg_f32x4(low + 8 * i + 4);
+                    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+                    v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
                 }
+                uint32_t out[P][4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const bool in0 = 8 * i + 2 * k < r, in1 = 8 * i + 2 * k + 1 < r;
+                    const Parts s = split(in0 ? v[2 * k] * scale : 0.f, in1 ? v[2 * k + 1] * scale : 0.f, P);
+#pragma unroll
+                    for (int j = 0; j < P; ++j) out[j][k] = s.v[j];
+                }
+#pragma unroll
+                for (int j = 0; j < P; ++j)
+                    sts128(a_at + (j * pieces + (i >> 3)) * (kBigTile * 128) + row * 128 + 16 * ((i & 7) ^ (row & 7)), out[j][0],
+                           out[j][1], out[j][2], out[j][3]);
+            }
+        };
+        uint4 base[2][2][BASE == 2 ? 2 : 1];     // [row][32 columns]: eight columns of this lane
+        auto fetch = [&](int i) {        // of block i
+            if (BASE == 0 || !active || i >= runs || n0 + (i + 1) * kUpBlock > n_end) return;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if ((h ? t1 : t0) < 0) continue;
+                const char* from = (h ? from1 : from0) + (size_t)i * (kUpBlock * (BASE == 2 ? 4 : 2));
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    base[h][v][0] = ldg128(from + v * (BASE == 2 ? 128 : 64));
+                    if (BASE == 2) base[h][v][BASE == 2] = ldg128(from + v * 128 + 16);
+                }
+            }
+        };
+        // The results of block i, whose product (if there is one) has accumulator `acc`
+        auto finish = [&](int i, unsigned acc) {
+            if (!active) return;
+            float d[8][4] = {};
+            if (r > 0) {
+                tmem_ld_16x64(tmem + ((uint32_t)row0 << 16) + acc * kUpBlock, d);
+                tmem_wait_ld();
             }
             float odd = 0.f;             // NaN if any sum is, or infinite
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
+            for (int k = 0; k < 8; ++k)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) odd = fmaf(d[u][0][j], 0.f, fmaf(d[u][1][j], 0.f, odd));
-            if (odd != odd) {
+                for (int j = 0; j < 4; ++j) odd = fmaf(d[k][j], 0.f, odd);
+            const bool wide = n0 + (i + 1) * kUpBlock <= n_end && p.wide;
+            if (wide && odd == odd) {
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if ((h ? t1 : t0) < 0) continue;
-                        float v[4] = {d[u][0][2 * h], d[u][0][2 * h + 1], d[u][1][2 * h], d[u][1][2 * h + 1]};
-                        plain_up(p, low0 + (h ? 8 * step : 0), scale, b, k.n0 + 16 * u + 4 * c, r, v);
-                        d[u][0][2 * h] = v[0]; d[u][0][2 * h + 1] = v[1]; d[u][1][2 * h] = v[2]; d[u][1][2 * h + 1] = v[3];
-                    }
-            }
-            if (k.n0 + kUpBlock <= k.end && p.wide) {
-                if (BASE != 0) {
+                    for (int v = 0; v < 2; ++v) {
+                        if (BASE == 1) {
+                            const uint4 x = base[h][v][0];
+                            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint4 raw = h ? next1[u] : next0[u];
-                            float from[4];
-                            if (BASE == 1) {
-                                bf16x2_to_f32(raw.x, from[0], from[1]);
-                                bf16x2_to_f32(raw.y, from[2], from[3]);
-                            } else {
-                                from[0] = __uint_as_float(raw.x); from[1] = __uint_as_float(raw.y);
-                                from[2] = __uint_as_float(raw.z); from[3] = __uint_as_float(raw.w);
+                            for (int j = 0; j < 4; ++j) {
+                                float lo, hi;
+                                bf16x2_to_f32(w[j], lo, hi);
+                                d[4 * v + j][2 * h] += lo;
+                                d[4 * v + j][2 * h + 1] += hi;
                             }
+                        } else if (BASE == 2) {
+                            const uint4 x = base[h][v][0], y = base[h][v][BASE == 2];
+                            const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) d[u][j >> 1][2 * h + (j & 1)] += from[j];
+                            for (int j = 0; j < 8; ++j) d[4 * v + (j >> 1)][2 * h + (j & 1)] += __uint_as_float(w[j]);
                         }
-                    fetch(blk + 1);      // base is in the sums: the next block's may come
-                }
+                    }
+                fetch(i + 1);            // base is in the sums: the next block's may come
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     if ((h ? t1 : t0) < 0) continue;
-                    char *to = (h ? to1 : to0) + 2 * (size_t)(k.n0 + 4 * c), *to32 = (h ? to321 : to320) + 4 * (size_t)(k.n0 + 4 * c);
+                    char* to = (h ? to1 : to0) + (size_t)i * (kUpBlock * 2);
+                    char* to32 = P == 3 ? row_ptr(p.y32, h ? t1 : t0) + (size_t)(n0 + i * kUpBlock + 8 * c) * 4 : nullptr;
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const float v[4] = {d[u][0][2 * h], d[u][0][2 * h + 1], d[u][1][2 * h], d[u][1][2 * h + 1]};
-                        if (put) put_wide(to, false, 16 * u, v);
-                        if (put32) put_wide(to32, true, 16 * u, v);
+                    for (int v = 0; v < 2; ++v) {
+                        float x[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) x[j] = d[4 * v + (j >> 1)][2 * h + (j & 1)];
+                        if (put) row_store8(to, false, 32 * v, x);
+                        if (put32) row_store8(to32, true, 32 * v, x);
                     }
                 }
             } else {
-                // the part's last columns, or rows that do not allow wide accesses
+                // the part's last columns, rows that do not allow wide accesses, or NaN
+                const float* low = p.low_big + (size_t)(tile.first + i0) * step;
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int t = h ? t1 : t0, n = k.n0 + 16 * u + 4 * c;
-                        if (t < 0 || n >= k.end) continue;
-                        float v[4] = {d[u][0][2 * h], d[u][0][2 * h + 1], d[u][1][2 * h], d[u][1][2 * h + 1]}, from[4] = {};
-                        if (p.base.ptr) load4(p.base, t, n, k.end, p.wide, from);
+                    for (int v = 0; v < 2; ++v) {
+                        const int t = h ? t1 : t0, n = n0 + i * kUpBlock + 32 * v + 8 * c;
+                        if (t < 0 || n >= n_end) continue;
+                        float x[8], from[8] = {};
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) v[j] += from[j];
-                        if (put) put4(p.y, t, n, k.end, p.wide, v);
-                        if (put32) put4(p.y32, t, n, k.end, p.wide, v);
+                        for (int j = 0; j < 8; ++j) x[j] = d[4 * v + (j >> 1)][2 * h + (j & 1)];
+                        if (odd != odd) plain_up(p, low + (h ? 8 * step : 0), scale, b, n, r, x);
+                        if (p.base.ptr) load_cols(row_ptr(p.base, t), p.base.f32, n, n_end, wide, from);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) x[j] += from[j];
+                        if (put) put_cols(row_ptr(p.y, t), false, n, n_end, wide, x);
+                        if (put32) put_cols(row_ptr(p.y32, t), true, n, n_end, wide, x);
                     }
-                fetch(blk + 1);
+                fetch(i + 1);
             }
+        };
+        load();
+        load();
+        fetch(0);
+        if (r > 0) take();
+        for (int i = 0; i <= runs; ++i) {
+            if (r > 0) {
+                copies_wait<kUpRing - 2>();
+                // the product before has read its operands: they may be replaced
+                if (i > 0 && !bad)
+                    bad = !mbar_wait_bounded(bars + 8 * ((made - 1) & 1), ((made - 1) >> 1) & 1, p.wait, kErrConsumerWait);
+                fence_async_smem();
+                tc_fence_before_sync();
+                bad = __syncthreads_or(bad);
+                tc_fence_after_sync();
+                if (bad) break;
+                if (i < runs) {
+                    if (tid == 0) {
+                        const uint32_t bt = ring + (uint32_t)(i % kUpRing) * stage_bytes;
+                        for (int j = 0; j < P; ++j)
+                            for (int q = 0; q < steps; ++q)
+                                umma_bf16(tmem + (made & 1) * kUpBlock,
+                                          umma_desc_sw128(a_at + (j * pieces + (q >> 2)) * (kBigTile * 128)) + 2 * (q & 3),
+                                          umma_desc_sw128(bt + (q >> 2) * (kUpBlock * 128)) + 2 * (q & 3), idesc, j + q > 0);
+                        umma_commit(bars + 8 * (made & 1));
+                    }
+                    load();
+                    ++made;
+                }
+            }
+            if (i > 0) finish(i - 1, (made - (i < runs ? 2 : 1)) & 1);
         }
         copies_wait<0>();
-        __syncthreads();                 // the ring is free for the next tile
     }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    if (warp == 0) tmem_dealloc(tmem, kUpTmem);
     griddep_wait();
 }
 
@@ -1118,19 +1120,15 @@ static cudaError_t raise_smem(F kernel, size_t bytes) {
     return bytes > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) : cudaSuccess;
 }
 
-template <bool FEW>
 static cudaError_t launch_small(const AdapterParams& p, long long tiles, int sm_count, cudaStream_t stream, bool up) {
-    const size_t smem = FEW ? sizeof(FewTiles) : 0;
+    const size_t smem = p.tokens <= kFewTokens ? sizeof(FewTiles) : 0;
     if (up) {
-        // few columns a warp while that leaves warps for every SM
-        const long long fine = tiles * ((p.N + 15) / 16), coarse = tiles * ((p.N + 63) / 64);
-        const bool small = fine <= 8LL * sm_count;
-        const long long ctas = ((small ? fine : coarse) + kUpWarps - 1) / kUpWarps, most = 2LL * sm_count;
+        const long long ctas = (tiles * ((p.N + 31) / 32) + kUpWarps - 1) / kUpWarps, most = 2LL * sm_count;
         const dim3 grid((unsigned)(ctas < most ? ctas : most));
-        return small ? launch_dependent(adapters_up_kernel<FEW, 1, 4>, grid, dim3(kUpThreads), smem, stream, p)
-                     : launch_dependent(adapters_up_kernel<FEW, 4, 2>, grid, dim3(kUpThreads), smem, stream, p);
+        return p.y32.ptr ? launch_dependent(adapters_up_kernel<3>, grid, dim3(kUpThreads), smem, stream, p)
+                         : launch_dependent(adapters_up_kernel<2>, grid, dim3(kUpThreads), smem, stream, p);
     }
-    const long long items = tiles * p.parts * ((p.rank + 15) / 16), most = 4LL * sm_count / kLowCluster;
+    const long long items = tiles * p.parts * ((p.rank + 15) / 16), most = 2LL * sm_count / kLowCluster;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1145,7 +1143,7 @@ static cudaError_t launch_small(const AdapterParams& p, long long tiles, int sm_
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, adapters_low_kernel<FEW>, p);
+    return cudaLaunchKernelEx(&cfg, adapters_low_kernel, p);
 }
 
 static cudaError_t launch_low_big(const AdapterParams& p, long long tiles, int sm_count, cudaStream_t stream) {
@@ -1171,23 +1169,20 @@ static cudaError_t launch_low_big(const AdapterParams& p, long long tiles, int s
     return cudaLaunchKernelEx(&cfg, adapters_low_big_kernel, p);
 }
 
-template <int C, int BASE, int P>
+template <int BASE, int P>
 static cudaError_t launch_up_big(const AdapterParams& p, int sm_count, cudaStream_t stream) {
-    constexpr int smem = up_big_smem(C, P);
-    const cudaError_t e = raise_smem(adapters_up_big_kernel<C, BASE, P>, smem);
+    const int smem = up_big_smem(p.rank, P);
+    const cudaError_t e = raise_smem(adapters_up_big_kernel<BASE, P>, smem);
     if (e != cudaSuccess) return e;
-    const int ctas = 2 * (smem + 1024) <= 228 * 1024 ? 2 : 1;
-    return launch_dependent(adapters_up_big_kernel<C, BASE, P>, dim3(ctas * sm_count), dim3(kUpThreads), smem, stream, p);
+    int ctas = 228 * 1024 / (smem + 1024);
+    ctas = ctas > kUpCtas ? kUpCtas : ctas;
+    return launch_dependent(adapters_up_big_kernel<BASE, P>, dim3(ctas * sm_count), dim3(kUpThreads), smem, stream, p);
 }
 
-template <int C>
-static cudaError_t launch_up_big_rank(const AdapterParams& p, int sm_count, cudaStream_t stream) {
-    const int base = !p.base.ptr || !p.wide ? 0 : p.base.f32 ? 2 : 1;
-    if (p.y32.ptr)
-        return base == 0 ? launch_up_big<C, 0, 3>(p, sm_count, stream)
-               : base == 1 ? launch_up_big<C, 1, 3>(p, sm_count, stream) : launch_up_big<C, 2, 3>(p, sm_count, stream);
-    return base == 0 ? launch_up_big<C, 0, 2>(p, sm_count, stream)
-           : base == 1 ? launch_up_big<C, 1, 2>(p, sm_count, stream) : launch_up_big<C, 2, 2>(p, sm_count, stream);
+template <int P>
+static cudaError_t launch_up_big_base(const AdapterParams& p, int sm_count, cudaStream_t stream) {
+    if (!p.base.ptr || !p.wide) return launch_up_big<0, P>(p, sm_count, stream);
+    return p.base.f32 ? launch_up_big<2, P>(p, sm_count, stream) : launch_up_big<1, P>(p, sm_count, stream);
 }
 
 }  // namespace dl
@@ -1240,7 +1235,7 @@ extern "C" dl_status dl_linear_adapters(const dl_adapters* adapters, const dl_ro
     p.in_place32 = p.y32.ptr && same_rows(p.y32, p.base);
     p.wide = true;
     for (const Rows* r : {&p.base, &p.y, &p.y32})
-        if (r->ptr) p.wide = p.wide && !(((uintptr_t)r->ptr | (uintptr_t)r->stride) & (r->f32 ? 15 : 7));
+        if (r->ptr) p.wide = p.wide && rows_aligned16(*r, tokens);
     const long long small = tokens <= kFewTokens ? tokens : max_small(tokens, p.num);
     if (small * ((N + 15) / 16) > 0x7fff0000LL || small * p.parts * ((p.rank + 15) / 16) > 0x7fff0000LL)
         return host_fail(DL_ERR_UNSUPPORTED_SHAPE, "tokens=%d with N=%d exceed one launch", tokens, N);
@@ -1250,8 +1245,8 @@ extern "C" dl_status dl_linear_adapters(const dl_adapters* adapters, const dl_ro
     p.wait = WaitCtl{dev.err_word, dev.wait_limit_ns};
     cudaError_t e;
     if (tokens <= kFewTokens) {
-        if ((e = launch_small<true>(p, small, dev.sm_count, st, false)) == cudaSuccess)
-            e = launch_small<true>(p, small, dev.sm_count, st, true);
+        if ((e = launch_small(p, small, dev.sm_count, st, false)) == cudaSuccess)
+            e = launch_small(p, small, dev.sm_count, st, true);
     } else {
         // Each list's kernels find how much there is on the device.  Both first products may run at the
         // same time, then both second ones.
@@ -1259,14 +1254,11 @@ extern "C" dl_status dl_linear_adapters(const dl_adapters* adapters, const dl_ro
         const size_t counters = (size_t)(p.num + 1) * 4;
         if ((e = raise_smem(sort_tokens_kernel, counters)) == cudaSuccess)
             e = launch_dependent(sort_tokens_kernel, dim3(1), dim3(1024), counters, st, p);
-        if (e == cudaSuccess) e = launch_small<false>(p, small, dev.sm_count, st, false);
+        if (e == cudaSuccess) e = launch_small(p, small, dev.sm_count, st, false);
         if (e == cudaSuccess && p.rank <= kBigRank) e = launch_low_big(p, big, dev.sm_count, st);
-        if (e == cudaSuccess) e = launch_small<false>(p, small, dev.sm_count, st, true);
+        if (e == cudaSuccess) e = launch_small(p, small, dev.sm_count, st, true);
         if (e == cudaSuccess && p.rank <= kBigRank)
-            e = p.rank <= 16   ? launch_up_big_rank<1>(p, dev.sm_count, st)
-                : p.rank <= 32 ? launch_up_big_rank<2>(p, dev.sm_count, st)
-                : p.rank <= 64 ? launch_up_big_rank<4>(p, dev.sm_count, st)
-                               : launch_up_big_rank<8>(p, dev.sm_count, st);
+            e = p.y32.ptr ? launch_up_big_base<3>(p, dev.sm_count, st) : launch_up_big_base<2>(p, dev.sm_count, st);
     }
     if (e != cudaSuccess) return host_fail(DL_ERR_CUDA, "linear_adapters launch: %s", cudaGetErrorString(e));
     return host_ok();
