@@ -92,6 +92,22 @@ def test_row_counts(cuda_device, rows):
         check(c, call(c, cuda_device))
 
 
+@pytest.mark.parametrize("dim", [1032, 2048, 4096, 4104, 8192, 8200, 16384])
+@pytest.mark.parametrize("y,h", [("bf16", "bf16"), ("bf16", "fp32"), ("fp32", "bf16"), ("fp32", "fp32")])
+def test_many_long_rows(cuda_device, dim, y, h):
+    """Rows that go through shared memory, several a CTA; the same in place, and with x as wide as y."""
+    c = make(700, dim, y=y, h=h, post="rms" if dim % 16 else None, pre="layer" if dim == 4096 else "rms", bias=dim == 2048,
+             gate="channel" if dim == 8192 else None, scale=0.5)
+    want = [t.clone() for t in call(c, cuda_device)]
+    check(c, want)
+    ty, th = c["y"].to(cuda_device), c["h"].to(cuda_device)
+    kw = dict(post=norm_on(c["post"], cuda_device), pre=norm_on(c["pre"], cuda_device), scale=0.5,
+              gate=None if c["gate"] is None else c["gate"].to(cuda_device))
+    r, x = dl.block_norm(ty, th, out_h=th, out_x=ty, **kw)
+    assert r is th and x is ty and torch.equal(r, want[0])
+    check(c, (r, x))
+
+
 def test_no_rows(cuda_device):
     c = make(0, 64)
     r, x = call(c, cuda_device)

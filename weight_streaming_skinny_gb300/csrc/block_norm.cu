@@ -24,243 +24,506 @@ struct BlockNormParams {
 // What bounds it: the bytes of y, h and the two outputs; every element is read once, held in
 // registers over both norms' sums and written once.  A row belongs to one team of threads, a part of a
 // warp for short rows and a CTA for long ones, so that a sum is a few shuffles, with one barrier where
-// the team is a CTA.
+// the team is a CTA.  CTAs go over many rows, the next row's loads ahead of this one's sums.
 //
 // Sums of squares run over centred values in fp32: for the centred norm a first mean is taken
 // off, then what the centred values still sum to (its rounding error), so that a mean far
 // larger than the spread costs no digits.  Squares that leave fp32's range (beyond 1e37, or
 // below 1e-30 where eps does not cover them) are summed again with the values scaled by a power
 // of two.
-template <int E, bool VEC, bool CTA>
+template <bool CTA>
 struct Team {
     float2* red;         // CTA teams: two buffers of 32 pairs, used in turn
-    int lanes, turn = 0;
+    int lanes;           // of a team inside a warp
+    int threads = 0;     // of a CTA team (all of the CTA's, or its first ones)
+    int turn = 0;
 
     // The team's lanes: teams of one warp may go different ways.
     __device__ unsigned mask() const {
         return CTA || lanes == 32 ? ~0u : ((1u << lanes) - 1) << (threadIdx.x & 31 & ~(lanes - 1));
     }
-
-    __device__ float2 sum(float2 v) {
-        if (CTA) {
-#pragma unroll
-            for (int o = 16; o; o >>= 1) {
-                v.x += __shfl_xor_sync(~0u, v.x, o);
-                v.y += __shfl_xor_sync(~0u, v.y, o);
-            }
-            return across(v, [](float2 a, float2 b) { return make_float2(a.x + b.x, a.y + b.y); });
-        }
+    __device__ float sum(float v) {
         const unsigned m = mask();
-        for (int o = lanes >> 1; o; o >>= 1) {
+        for (int o = CTA ? 16 : lanes >> 1; o; o >>= 1) v += __shfl_xor_sync(m, v, o);
+        if (!CTA) return v;
+        v = across(make_float2(v, 0.f), 0.f).x;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+        return v;
+    }
+    __device__ float2 sum(float2 v) {
+        const unsigned m = mask();
+        for (int o = CTA ? 16 : lanes >> 1; o; o >>= 1) {
             v.x += __shfl_xor_sync(m, v.x, o);
             v.y += __shfl_xor_sync(m, v.y, o);
         }
+        if (!CTA) return v;
+        v = across(v, 0.f);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            v.x += __shfl_xor_sync(~0u, v.x, o);
+            v.y += __shfl_xor_sync(~0u, v.y, o);
+        }
         return v;
     }
-    __device__ float sum(float v) { return sum(make_float2(v, 0.f)).x; }
-    __device__ float max(float v) {
+    __device__ float max(float v) {      // of values >= 0
         const unsigned m = mask();
         for (int o = CTA ? 16 : lanes >> 1; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(m, v, o));
         if (!CTA) return v;
-        return across(make_float2(v, 0.f), [](float2 a, float2 b) { return make_float2(fmaxf(a.x, b.x), 0.f); }).x;
-    }
-    // Join the warps' values of a CTA, the same way in every warp.  The two buffers take turns:
-    // whoever writes one has passed the barrier after its last readers' reads.
-    template <class F>
-    __device__ float2 across(float2 v, F join) {
-        float2* buf = red + 32 * (turn ^= 1);
-        const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-        if (lane == 0) buf[threadIdx.x >> 5] = v;
-        __syncthreads();
-        v = lane < warps ? buf[lane] : make_float2(0.f, 0.f);
+        v = across(make_float2(v, 0.f), 0.f).x;
 #pragma unroll
-        for (int o = 16; o; o >>= 1)
-            v = join(v, make_float2(__shfl_xor_sync(~0u, v.x, o), __shfl_xor_sync(~0u, v.y, o)));
+        for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
         return v;
+    }
+    // The CTA's warps' values, a lane each, the same in every warp.  The two buffers take turns: whoever writes
+    // one has passed the barrier after its last readers' reads.
+    __device__ float2 across(float2 v, float none) {
+        float2* buf = red + 32 * (turn ^= 1);
+        const int lane = threadIdx.x & 31;
+        if (lane == 0) buf[threadIdx.x >> 5] = v;
+        asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+        return lane < threads >> 5 ? buf[lane] : make_float2(none, none);
     }
 };
 
-// Elements that a thread of a team of `size` holds: groups of 8 consecutive ones, or single ones
-// where rows or weights are not aligned for groups.
-template <int E, bool VEC, class F>
-__device__ __forceinline__ void each_group(int rank, int size, F f) {
-#pragma unroll
-    for (int i = 0; i < E / 8; ++i) {
-        if (VEC)
-            f(i, (rank + i * size) * 8, 1);
-        else
-            f(i, rank + i * 8 * size, size);
-    }
-}
+// The elements of a row that a thread of a team holds: groups of 8 consecutive ones, or (VEC false: rows
+// or weights that are not aligned for groups) every size-th one.
+template <int E, bool VEC>
+struct Slots {
+    int first, step, count;      // groups or elements: the thread's first, from one to the next, how many of E (/ 8)
 
-// Eight values, `step` apart from element e on; zeros from `dim` on.
-template <bool VEC>
-__device__ __forceinline__ void load8(const void* p, bool f32, int e, int step, int dim, float* v) {
-    if (VEC) {
-        if (e < dim) {
-            row_load8(p, f32, e, v);
+    __device__ Slots(int rank, int size, int dim) : first(rank), step(size) {
+        const int n = VEC ? (dim + 7) / 8 : dim;
+        count = rank < n ? (n - rank + size - 1) / size : 0;
+    }
+    __device__ __forceinline__ bool has(int i) const { return (VEC ? i / 8 : i) < count; }
+    __device__ __forceinline__ void load(const void* p, bool f32, float (&v)[E]) const {
+        if (VEC) {
+#pragma unroll
+            for (int i = 0; i < E / 8; ++i) {
+                if (i < count) {
+                    row_load8(p, f32, (first + i * step) * 8, v + 8 * i);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[8 * i + k] = 0.f;
+                }
+            }
+        } else if (f32) {
+            const float* q = static_cast<const float*>(p) + first;
+#pragma unroll
+            for (int i = 0; i < E; ++i) v[i] = i < count ? q[i * step] : 0.f;
         } else {
+            const uint16_t* q = static_cast<const uint16_t*>(p) + first;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = 0.f;
+            for (int i = 0; i < E; ++i) v[i] = i < count ? bf16_bits_to_f32(q[i * step]) : 0.f;
         }
-    } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = e + k * step < dim ? row_load1(p, f32, e + k * step) : 0.f;
     }
+    // The same from and to a row in shared memory (VEC).
+    __device__ __forceinline__ void load_shared(uint32_t p, bool f32, float (&v)[E]) const {
+#pragma unroll
+        for (int i = 0; i < E / 8; ++i) {
+            const int e = (first + i * step) * 8;
+            float* t = v + 8 * i;
+            if (i >= count) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) t[k] = 0.f;
+            } else if (f32) {
+                const uint4 a = lds128(p + 4 * e), b = lds128(p + 4 * e + 16);
+                t[0] = __uint_as_float(a.x); t[1] = __uint_as_float(a.y); t[2] = __uint_as_float(a.z); t[3] = __uint_as_float(a.w);
+                t[4] = __uint_as_float(b.x); t[5] = __uint_as_float(b.y); t[6] = __uint_as_float(b.z); t[7] = __uint_as_float(b.w);
+            } else {
+                const uint4 a = lds128(p + 2 * e);
+                bf16x2_to_f32(a.x, t[0], t[1]);
+                bf16x2_to_f32(a.y, t[2], t[3]);
+                bf16x2_to_f32(a.z, t[4], t[5]);
+                bf16x2_to_f32(a.w, t[6], t[7]);
+            }
+        }
+    }
+    __device__ __forceinline__ void store_shared(uint32_t p, bool f32, const float (&v)[E]) const {
+#pragma unroll
+        for (int i = 0; i < E / 8; ++i) {
+            if (i >= count) continue;
+            const int e = (first + i * step) * 8;
+            const float* t = v + 8 * i;
+            if (f32) {
+                sts128(p + 4 * e, __float_as_int(t[0]), __float_as_int(t[1]), __float_as_int(t[2]), __float_as_int(t[3]));
+                sts128(p + 4 * e + 16, __float_as_int(t[4]), __float_as_int(t[5]), __float_as_int(t[6]), __float_as_int(t[7]));
+            } else {
+                sts128(p + 2 * e, f32x2_to_bf16x2(t[0], t[1]), f32x2_to_bf16x2(t[2], t[3]), f32x2_to_bf16x2(t[4], t[5]),
+                       f32x2_to_bf16x2(t[6], t[7]));
+            }
+        }
+    }
+    __device__ __forceinline__ void store(void* p, bool f32, const float (&v)[E]) const {
+        if (VEC) {
+#pragma unroll
+            for (int i = 0; i < E / 8; ++i)
+                if (i < count) row_store8(p, f32, (first + i * step) * 8, v + 8 * i);
+        } else if (f32) {
+            float* q = static_cast<float*>(p) + first;
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                if (i < count) q[i * step] = v[i];
+        } else {
+            uint16_t* q = static_cast<uint16_t*>(p) + first;
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                if (i < count) q[i * step] = f32_to_bf16_rne(v[i]);
+        }
+    }
+};
+
+// Pairs of a thread's elements: v = v * s, v = v * w, sums of squares.
+template <int E>
+__device__ __forceinline__ void times(float (&v)[E], float s) {
+#pragma unroll
+    for (int i = 0; i < E; i += 2) unpack(mul2(f2(v[i], v[i + 1]), f2(s, s)), v[i], v[i + 1]);
 }
-template <bool VEC>
-__device__ __forceinline__ void store8(void* p, bool f32, int e, int step, int dim, const float* v) {
-    if (VEC) {
-        if (e < dim) row_store8(p, f32, e, v);
-    } else {
+template <int E>
+__device__ __forceinline__ void times(float (&v)[E], const float (&w)[E]) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (e + k * step < dim) row_store1(p, f32, e + k * step, v[k]);
+    for (int i = 0; i < E; i += 2) unpack(mul2(f2(v[i], v[i + 1]), f2(w[i], w[i + 1])), v[i], v[i + 1]);
+}
+template <int E>
+__device__ __forceinline__ float squares(const float (&v)[E]) {
+    F2 s = f2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < E; i += 2) {
+        const F2 x = f2(v[i], v[i + 1]);
+        s = fma2(x, x, s);
     }
+    float a, b;
+    unpack(s, a, b);
+    return a + b;
 }
 
 // v = N(v): the elements of one row, zeros past its end.
 template <int E, bool VEC, bool CTA>
-__device__ __forceinline__ void normalise(float (&v)[E], const NormSide& n, Team<E, VEC, CTA>& team, int rank, int size,
-                                          int dim) {
+__device__ __forceinline__ void normalise(float (&v)[E], const NormSide& n, Team<CTA>& team, const Slots<E, VEC>& slots, int dim) {
     const float inv_dim = 1.f / dim;
-    float ss = 0.f;
+    float ss;
     if (n.kind == DL_NORM_LAYER) {
         float s = 0.f;
 #pragma unroll
         for (int i = 0; i < E; ++i) s = fmaf(v[i], inv_dim, s);
         const float mean = team.sum(s);
         float2 t = {0.f, 0.f};
-        each_group<E, VEC>(rank, size, [&](int i, int e, int step) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                float& x = v[8 * i + k];
-                x = e + k * step < dim ? x - mean : 0.f;
-                t.x = fmaf(x, inv_dim, t.x);
-                t.y = fmaf(x, x, t.y);
-            }
-        });
+        for (int i = 0; i < E; ++i) {
+            v[i] = slots.has(i) ? v[i] - mean : 0.f;
+            t.x = fmaf(v[i], inv_dim, t.x);
+        }
+        t.y = squares(v);
         t = team.sum(t);
-        const float rest = t.x;
-        ss = t.y <= 1e37f ? fmaxf(fmaf(-dim * rest, rest, t.y), 0.f) : t.y;
-        each_group<E, VEC>(rank, size, [&](int i, int e, int step) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (e + k * step < dim) v[8 * i + k] -= rest;
-        });
+        for (int i = 0; i < E; ++i) v[i] = slots.has(i) ? v[i] - t.x : 0.f;
+        ss = t.y <= 1e37f ? fmaxf(fmaf(-dim * t.x, t.x, t.y), 0.f) : t.y;
     } else {
-#pragma unroll
-        for (int i = 0; i < E; ++i) ss = fmaf(v[i], v[i], ss);
-        ss = team.sum(ss);
+        ss = team.sum(squares(v));
     }
-    float up = 1.f, inv = 1.f / sqrtf(fmaf(ss, inv_dim, n.eps));
+    float inv = 1.f / sqrtf(fmaf(ss, inv_dim, n.eps));
     if (ss > 1e37f || (ss < 1e-30f && n.eps < 1e-30f)) {
         float m = 0.f;
 #pragma unroll
         for (int i = 0; i < E; ++i) m = fmaxf(m, fabsf(v[i]));
         m = team.max(m);
         if (m > 0.f && m <= 3.4028235e38f) {
-            up = ldexpf(1.f, -max(ilogbf(m), -100));
-            ss = 0.f;
-#pragma unroll
-            for (int i = 0; i < E; ++i) ss = fmaf(v[i] * up, v[i] * up, ss);
-            ss = team.sum(ss);
+            const float up = ldexpf(1.f, -max(ilogbf(m), -100));
+            times(v, up);
+            ss = team.sum(squares(v));
             inv = 1.f / sqrtf(fmaf(ss, inv_dim, n.eps * up * up));
         }
     }
-    each_group<E, VEC>(rank, size, [&](int i, int e, int step) {
-        float w[8], b[8];
-        if (n.weight) load8<VEC>(n.weight, n.f32, e, step, dim, w);
-        if (n.bias) load8<VEC>(n.bias, n.f32, e, step, dim, b);
+    times(v, inv);
+    float w[E];
+    if (n.weight) {
+        slots.load(n.weight, n.f32, w);
+        if (n.offset != 0.f) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            float x = v[8 * i + k] * up * inv;
-            if (n.weight) x *= w[k] + n.offset;
-            v[8 * i + k] = n.bias ? x + b[k] : x;
+            for (int i = 0; i < E; ++i) w[i] += n.offset;
         }
-    });
+        times(v, w);
+    }
+    if (n.bias) {
+        slots.load(n.bias, n.f32, w);
+#pragma unroll
+        for (int i = 0; i < E; ++i) v[i] += w[i];
+    }
 }
 
-template <int E, bool VEC, bool CTA>
-__global__ void __launch_bounds__(1024) block_norm_kernel(const __grid_constant__ BlockNormParams p) {
-    __shared__ float2 red[CTA ? 64 : 1];
-    Team<E, VEC, CTA> team{red, p.lanes};
-    const int size = CTA ? blockDim.x : p.lanes, rank = CTA ? threadIdx.x : threadIdx.x & (p.lanes - 1);
-    const long long row = CTA ? blockIdx.x : ((long long)blockIdx.x * blockDim.x + threadIdx.x) / p.lanes;
-    const bool mine = row < p.rows;         // a warp's teams stay together for their shuffles
-    const int dim = mine ? p.dim : 0;
-    griddep_wait();
-    griddep_launch_dependents();
-    const long long at = mine ? row : 0;
-    float v[E], h[E];
-    const char *py = row_ptr(p.y, at), *ph = row_ptr(p.h, at);
-    each_group<E, VEC>(rank, size, [&](int i, int e, int step) {
-        if (p.y.ptr) load8<VEC>(py, p.y.f32, e, step, dim, v + 8 * i);
-        if (p.h.ptr) load8<VEC>(ph, p.h.f32, e, step, dim, h + 8 * i);
-    });
-    if (p.y.ptr) {
-        if (p.post.kind != DL_NORM_NONE) normalise<E, VEC, CTA>(v, p.post, team, rank, size, dim);
-        const float row_gate = p.gate_kind == DL_GATE_ROW ? row_load1(row_ptr(p.gate, at), p.gate.f32, 0) : 1.f;
-        const char* pg = p.gate_kind == DL_GATE_FULL ? row_ptr(p.gate, at) : static_cast<const char*>(p.gate.ptr);
-        each_group<E, VEC>(rank, size, [&](int i, int e, int step) {
-            float g[8];
-            if (p.gate_kind >= DL_GATE_CHANNEL) load8<VEC>(pg, p.gate.f32, e, step, dim, g);
+// What is read of a row ahead of its turn: up to 16 elements of y and h a thread, of 16 bits, or of 32.
+template <int E, bool VEC, bool WIDE>
+struct Ahead {
+    static constexpr bool kOn = VEC && E <= 16;
+    uint4 v[kOn ? E / 8 : 1][WIDE ? 2 : 1];
+
+    __device__ __forceinline__ void load(const Slots<E, VEC>& s, const char* p, bool f32) {
+        if (!kOn) return;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                float& x = v[8 * i + k];
-                if (p.gate_kind != DL_GATE_NONE) {
-                    const float t = p.gate_kind == DL_GATE_ROW ? row_gate : g[k];
-                    x *= p.sigmoid ? 1.f / (1.f + expf(-t)) : t;
-                }
-                x *= p.scale;
-                if (p.h.ptr) x = fmaf(p.h_scale, h[8 * i + k], x);
-                if (e + k * step >= dim) x = 0.f;      // a gate of infinity times an absent element
+        for (int i = 0; i < (kOn ? E / 8 : 1); ++i) {
+            if (i >= s.count) continue;
+            const int e = (s.first + i * s.step) * 8;
+            if (WIDE && f32) {
+                v[i][0] = ldg128(p + 4 * e);
+                v[i][WIDE] = ldg128(p + 4 * e + 16);
+            } else {
+                v[i][0] = ldg128(p + 2 * e);
             }
-        });
+        }
+    }
+    __device__ __forceinline__ void get(const Slots<E, VEC>& s, const char* p, bool f32, float (&x)[E]) const {
+        if (!kOn) return s.load(p, f32, x);
+#pragma unroll
+        for (int i = 0; i < (kOn ? E / 8 : 1); ++i) {
+            float* t = x + 8 * i;
+            const uint4 a = v[i][0], b = v[i][WIDE];
+            if (i >= s.count) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) t[k] = 0.f;
+            } else if (WIDE && f32) {
+                t[0] = __uint_as_float(a.x); t[1] = __uint_as_float(a.y); t[2] = __uint_as_float(a.z); t[3] = __uint_as_float(a.w);
+                t[4] = __uint_as_float(b.x); t[5] = __uint_as_float(b.y); t[6] = __uint_as_float(b.z); t[7] = __uint_as_float(b.w);
+            } else {
+                bf16x2_to_f32(a.x, t[0], t[1]);
+                bf16x2_to_f32(a.y, t[2], t[3]);
+                bf16x2_to_f32(a.z, t[4], t[5]);
+                bf16x2_to_f32(a.w, t[6], t[7]);
+            }
+        }
+    }
+};
+
+// v = h_scale h + scale act(gate) post(v), of what there is.
+template <int E, bool VEC, bool CTA>
+__device__ __forceinline__ void join(float (&v)[E], const float (&h)[E], const BlockNormParams& p, long long row, Team<CTA>& team,
+                                     const Slots<E, VEC>& slots) {
+    if (p.y.ptr) {
+        if (p.post.kind != DL_NORM_NONE) normalise<E, VEC, CTA>(v, p.post, team, slots, p.dim);
+        if (p.gate_kind != DL_GATE_NONE) {
+            float g[E];
+            if (p.gate_kind == DL_GATE_ROW) {
+                const float one = row_load1(row_ptr(p.gate, row), p.gate.f32, 0);
+#pragma unroll
+                for (int i = 0; i < E; ++i) g[i] = one;
+            } else {
+                slots.load(p.gate_kind == DL_GATE_FULL ? row_ptr(p.gate, row) : p.gate.ptr, p.gate.f32, g);
+            }
+            if (p.sigmoid) {
+#pragma unroll
+                for (int i = 0; i < E; ++i) g[i] = 1.f / (1.f + expf(-g[i]));
+            }
+            times(v, g);
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                if (!slots.has(i)) v[i] = 0.f;       // (an infinite gate times an absent element)
+        }
+        if (p.scale != 1.f) times(v, p.scale);
+        if (p.h.ptr) {
+#pragma unroll
+            for (int i = 0; i < E; i += 2)
+                unpack(fma2(f2(h[i], h[i + 1]), f2(p.h_scale, p.h_scale), f2(v[i], v[i + 1])), v[i], v[i + 1]);
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < E; ++i) v[i] = p.h_scale * h[i];
     }
-    if (p.r.ptr) {
-        char* pr = row_ptr(p.r, at);
-        each_group<E, VEC>(rank, size, [&](int i, int e, int step) { store8<VEC>(pr, p.r.f32, e, step, dim, v + 8 * i); });
+}
+
+// WIDE: y or h is fp32; T: the most threads of a CTA
+template <int E, bool VEC, bool CTA, bool WIDE, int T>
+__global__ void __launch_bounds__(T, T == 128 ? 4 : 1024 / T) block_norm_kernel(const __grid_constant__ BlockNormParams p) {
+    __shared__ float2 red[CTA ? 64 : 1];
+    Team<CTA> team{red, p.lanes, (int)blockDim.x};
+    const int size = CTA ? blockDim.x : p.lanes, rank = CTA ? threadIdx.x : threadIdx.x & (p.lanes - 1);
+    long long row = CTA ? blockIdx.x : ((long long)blockIdx.x * blockDim.x + threadIdx.x) / p.lanes;
+    const long long step = CTA ? gridDim.x : (long long)gridDim.x * blockDim.x / p.lanes;
+    const Slots<E, VEC> slots(rank, size, p.dim);
+    griddep_wait();
+    griddep_launch_dependents();
+    Ahead<E, VEC, WIDE> next_y, next_h;
+    if (row < p.rows) {
+        if (p.y.ptr) next_y.load(slots, row_ptr(p.y, row), p.y.f32);
+        if (p.h.ptr) next_h.load(slots, row_ptr(p.h, row), p.h.f32);
     }
-    if (p.x.ptr) {
-        if (p.pre.kind != DL_NORM_NONE) normalise<E, VEC, CTA>(v, p.pre, team, rank, size, dim);
-        char* px = row_ptr(p.x, at);
-        each_group<E, VEC>(rank, size, [&](int i, int e, int step) { store8<VEC>(px, p.x.f32, e, step, dim, v + 8 * i); });
+    for (; row < p.rows; row += step) {  // (teams of a warp may leave at different times: their shuffles are their own)
+        float v[E], h[E];
+        if (p.y.ptr) next_y.get(slots, row_ptr(p.y, row), p.y.f32, v);
+        if (p.h.ptr) next_h.get(slots, row_ptr(p.h, row), p.h.f32, h);
+        if (row + step < p.rows) {
+            if (p.y.ptr) next_y.load(slots, row_ptr(p.y, row + step), p.y.f32);
+            if (p.h.ptr) next_h.load(slots, row_ptr(p.h, row + step), p.h.f32);
+        }
+        join(v, h, p, row, team, slots);
+        if (p.r.ptr) slots.store(row_ptr(p.r, row), p.r.f32, v);
+        if (p.x.ptr) {
+            if (p.pre.kind != DL_NORM_NONE) normalise<E, VEC, CTA>(v, p.pre, team, slots, p.dim);
+            slots.store(row_ptr(p.x, row), p.x.f32, v);
+        }
+    }
+}
+
+// Many long rows, all streams there and in 16-byte pieces: rows come into a ring of shared memory by bulk copies,
+// stages ahead, and what is made of them goes back from the same place: r over h, x over y.  One warp has the
+// copies made both ways; the others wait for a row, and, once, for its sum.
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+
+struct RingParams {
+    BlockNormParams n;
+    int stages, y_bytes, h_bytes;        // of a row
+    WaitCtl wait;
+};
+
+// T: the most threads that compute (a warp more copies)
+template <int E, int T>
+__global__ void __launch_bounds__(T + 32, T == 256 ? 2 : 1) block_norm_ring_kernel(const __grid_constant__ RingParams q) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ float2 red[64];
+    __shared__ __align__(8) unsigned long long bars[16];         // rows in place, rows made
+    __shared__ volatile int dead;        // a wait gave up: nobody waits any more, nothing is copied
+    const BlockNormParams& p = q.n;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = (blockDim.x >> 5) - 1, S = q.stages;
+    const uint32_t full = smem_u32(bars), made = full + 64, ring = smem_u32(smem);
+    const int stage_bytes = q.y_bytes + q.h_bytes;
+    if (tid == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(made + 8 * i, warps);
+        }
+        fence_mbarrier_init();
+        dead = 0;
+    }
+    __syncthreads();
+    griddep_wait();
+    griddep_launch_dependents();
+    const int n = (int)((p.rows - 1 - (int)blockIdx.x) / (int)gridDim.x) + 1;       // rows of this CTA
+    auto row_of = [&](int i) { return (long long)blockIdx.x + (long long)i * gridDim.x; };
+    if (warp == warps) {
+        if (lane == 0) {
+            auto load = [&](int i) {
+                const uint32_t to = ring + i % S * stage_bytes, bar = full + 8 * (i % S);
+                mbar_arrive_expect_tx(bar, stage_bytes);
+                bulk_load(to, row_ptr(p.y, row_of(i)), q.y_bytes, bar);
+                bulk_load(to + q.y_bytes, row_ptr(p.h, row_of(i)), q.h_bytes, bar);
+            };
+            int loaded = 0;
+            while (loaded < min(S, n)) load(loaded++);
+            for (int i = 0; i < n && !dead; ++i) {
+                if (!mbar_wait_bounded(made + 8 * (i % S), (i / S) & 1, q.wait, kErrProducerWait)) {
+                    dead = 1;
+                    break;
+                }
+                if (dead) break;
+                const uint32_t from = ring + i % S * stage_bytes;
+                bulk_store(row_ptr(p.x, row_of(i)), from, p.dim * (p.x.f32 ? 4 : 2));
+                bulk_store(row_ptr(p.r, row_of(i)), from + q.y_bytes, q.h_bytes);
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                if (loaded < n) {
+                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    load(loaded++);
+                }
+            }
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+            if (dead)                    // what is on its way arrives before the CTA leaves
+                for (int i = max(loaded - S, 0); i < loaded; ++i)
+                    mbar_wait_bounded(full + 8 * (i % S), (i / S) & 1, q.wait, kErrDrainWait);
+        }
+        return;
+    }
+    Team<true> team{red, 0, 32 * warps};
+    const Slots<E, true> slots(tid, 32 * warps, p.dim);
+    for (int i = 0; i < n; ++i) {
+        if (!dead && !mbar_wait_bounded(full + 8 * (i % S), (i / S) & 1, q.wait, kErrConsumerWait)) dead = 1;
+        __syncwarp();
+        const uint32_t at = ring + i % S * stage_bytes;
+        float v[E], h[E];
+        slots.load_shared(at, p.y.f32, v);
+        slots.load_shared(at + q.y_bytes, p.h.f32, h);
+        join(v, h, p, row_of(i), team, slots);
+        slots.store_shared(at + q.y_bytes, p.r.f32, v);
+        normalise<E, true, true>(v, p.pre, team, slots, p.dim);
+        slots.store_shared(at, p.x.f32, v);      // (all have read y: the norm's sum came after it)
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(made + 8 * (i % S));
     }
 }
 
 constexpr int kMaxDim = 32768;
 
-template <int E, bool VEC, bool CTA>
+template <int E, bool VEC, bool CTA, int T>
 cudaError_t launch_norm(const BlockNormParams& p, long long grid, int threads, cudaStream_t stream) {
-    return launch_dependent(block_norm_kernel<E, VEC, CTA>, dim3((unsigned)grid), dim3(threads), 0, stream, p);
+    constexpr bool kWide = VEC && E <= 16;
+    return kWide && (p.y.f32 || p.h.f32)
+               ? launch_dependent(block_norm_kernel<E, VEC, CTA, kWide, T>, dim3((unsigned)grid), dim3(threads), 0, stream, p)
+               : launch_dependent(block_norm_kernel<E, VEC, CTA, false, T>, dim3((unsigned)grid), dim3(threads), 0, stream, p);
+}
+
+template <int E, int T>
+cudaError_t launch_ring_kernel(const RingParams& q, int threads, int sm_count, cudaStream_t stream) {
+    const size_t smem = (size_t)q.stages * (q.y_bytes + q.h_bytes);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(block_norm_ring_kernel<E, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    const int by_smem = 226 * 1024 / (int)(smem + 2048), by_threads = T == 256 ? 2 * 256 / threads : 1;
+    const int ctas = by_smem < by_threads ? by_smem : by_threads;
+    const int most = ctas * sm_count;
+    return launch_dependent(block_norm_ring_kernel<E, T>, dim3(q.n.rows < most ? q.n.rows : most), dim3(threads + 32), smem, stream, q);
+}
+
+// Many rows of more than 1024 elements through the ring: where all streams are there, r has h's type, x is no
+// wider than y, and a few rows fit shared memory.  (Fewer rows are no faster: ...)
+static bool launch_ring(const BlockNormParams& p, int groups, int sm_count, const WaitCtl& wait, cudaStream_t stream, cudaError_t& e) {
+    if (!p.y.ptr || !p.h.ptr || !p.r.ptr || !p.x.ptr || p.pre.kind == DL_NORM_NONE || p.r.f32 != p.h.f32 ||
+        (p.x.f32 && !p.y.f32) || p.rows < 4 * sm_count || p.dim > 16384)
+        return false;
+    RingParams q = {p, 0, p.dim * (p.y.f32 ? 4 : 2), p.dim * (p.h.f32 ? 4 : 2), wait};
+    const int stage = q.y_bytes + q.h_bytes;
+    const bool small = p.dim <= 4096, large = p.dim > 8192;
+    const int threads = ((small ? (groups + 1) / 2 : (groups + 3) / 4) + 31) / 32 * 32;
+    const int ctas = large ? 1 : 2 * 256 / threads;
+    q.stages = 220 * 1024 / (ctas * stage);
+    if (q.stages < 2) q.stages = 220 * 1024 / stage;
+    if (q.stages < 2) return false;
+    if (q.stages > 4) q.stages = 4;
+    e = small ? launch_ring_kernel<16, 256>(q, threads, sm_count, stream)
+        : large ? launch_ring_kernel<32, 512>(q, threads, sm_count, stream) : launch_ring_kernel<32, 256>(q, threads, sm_count, stream);
+    return true;
 }
 
 template <bool VEC>
-cudaError_t launch_norm_rows(BlockNormParams& p, int sm_count, cudaStream_t stream) {
+cudaError_t launch_norm_rows(BlockNormParams& p, int sm_count, const WaitCtl& wait, cudaStream_t stream) {
     const int groups = (p.dim + 7) / 8;
     if (groups <= 128) {                    // teams inside a warp, at most 32 elements a thread
         int lanes = 8;
         while (lanes < 32 && lanes * 4 < groups) lanes *= 2;
         const int per = (groups + lanes - 1) / lanes, threads = 128;
-        const long long grid = ((long long)p.rows * lanes + threads - 1) / threads;
+        const long long all = ((long long)p.rows * lanes + threads - 1) / threads, most = 16LL * sm_count;
+        const long long grid = all < most ? all : most;
         p.lanes = lanes;
-        if (per <= 1) return launch_norm<8, VEC, false>(p, grid, threads, stream);
-        if (per <= 2) return launch_norm<16, VEC, false>(p, grid, threads, stream);
-        return launch_norm<32, VEC, false>(p, grid, threads, stream);
+        if (per <= 1) return launch_norm<8, VEC, false, 128>(p, grid, threads, stream);
+        if (per <= 2) return launch_norm<16, VEC, false, 128>(p, grid, threads, stream);
+        return launch_norm<32, VEC, false, 128>(p, grid, threads, stream);
     }
-    // A CTA each: one group a thread where there are few rows, so that a row is loaded at once, two
-    // where there are many
-    const int want = p.rows <= 2 * sm_count ? 1 : 2;
-    int per = want;
+    cudaError_t e;
+    if (VEC && launch_ring(p, groups, sm_count, wait, stream, e)) return e;
+    // A CTA each: one group a thread where there are few rows, so that a row is loaded at once, or short
+    // ones; two where there are many long ones
+    int per = p.rows <= 2 * sm_count || groups <= 256 ? 1 : 2;
     while ((groups + per - 1) / per > 1024) per *= 2;
     const int threads = ((groups + per - 1) / per + 31) / 32 * 32;
-    if (per == 1) return launch_norm<8, VEC, true>(p, p.rows, threads, stream);
-    if (per == 2) return launch_norm<16, VEC, true>(p, p.rows, threads, stream);
-    return launch_norm<32, VEC, true>(p, p.rows, threads, stream);
+    const long long fit = 1024 / threads, most = (fit > 8 ? 8 : fit) * sm_count;
+    const long long grid = p.rows < most ? p.rows : most;
+    if (per == 1)
+        return threads <= 256 ? launch_norm<8, VEC, true, 256>(p, grid, threads, stream)
+                              : launch_norm<8, VEC, true, 1024>(p, grid, threads, stream);
+    if (per == 2)
+        return threads <= 512 ? launch_norm<16, VEC, true, 512>(p, grid, threads, stream)
+                              : launch_norm<16, VEC, true, 1024>(p, grid, threads, stream);
+    return launch_norm<32, VEC, true, 1024>(p, grid, threads, stream);
 }
 
 static dl_status check_norm(const dl_norm* n, const char* name, NormSide& out) {
@@ -342,7 +605,8 @@ extern "C" dl_status dl_block_norm(const dl_rows* y, const dl_norm* post, const 
     HostDevice dev;
     if ((s = host_device(dev)) != DL_OK) return s;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = vec ? launch_norm_rows<true>(p, dev.sm_count, st) : launch_norm_rows<false>(p, dev.sm_count, st);
+    const WaitCtl wait = {dev.err_word, dev.wait_limit_ns};
+    const cudaError_t e = vec ? launch_norm_rows<true>(p, dev.sm_count, wait, st) : launch_norm_rows<false>(p, dev.sm_count, wait, st);
     if (e != cudaSuccess) return host_fail(DL_ERR_CUDA, "block_norm launch: %s", cudaGetErrorString(e));
     return host_ok();
 }
