@@ -92,7 +92,7 @@ def test_row_counts(cuda_device, rows):
         check(c, call(c, cuda_device))
 
 
-@pytest.mark.parametrize("dim", [1032, 2048, 4096, 4104, 8192, 8200, 16384])
+@pytest.mark.parametrize("dim", [1032, 1536, 2048, 4096, 4104, 4608, 5120, 8192, 8200, 16384])
 @pytest.mark.parametrize("y,h", [("bf16", "bf16"), ("bf16", "fp32"), ("fp32", "bf16"), ("fp32", "fp32")])
 def test_many_long_rows(cuda_device, dim, y, h):
     """Rows that go through shared memory, several a CTA; the same in place, and with x as wide as y."""

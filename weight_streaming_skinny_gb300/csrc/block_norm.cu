@@ -118,43 +118,6 @@ struct Slots {
             for (int i = 0; i < E; ++i) v[i] = i < count ? bf16_bits_to_f32(q[i * step]) : 0.f;
         }
     }
-    // The same from and to a row in shared memory (VEC).
-    __device__ __forceinline__ void load_shared(uint32_t p, bool f32, float (&v)[E]) const {
-#pragma unroll
-        for (int i = 0; i < E / 8; ++i) {
-            const int e = (first + i * step) * 8;
-            float* t = v + 8 * i;
-            if (i >= count) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) t[k] = 0.f;
-            } else if (f32) {
-                const uint4 a = lds128(p + 4 * e), b = lds128(p + 4 * e + 16);
-                t[0] = __uint_as_float(a.x); t[1] = __uint_as_float(a.y); t[2] = __uint_as_float(a.z); t[3] = __uint_as_float(a.w);
-                t[4] = __uint_as_float(b.x); t[5] = __uint_as_float(b.y); t[6] = __uint_as_float(b.z); t[7] = __uint_as_float(b.w);
-            } else {
-                const uint4 a = lds128(p + 2 * e);
-                bf16x2_to_f32(a.x, t[0], t[1]);
-                bf16x2_to_f32(a.y, t[2], t[3]);
-                bf16x2_to_f32(a.z, t[4], t[5]);
-                bf16x2_to_f32(a.w, t[6], t[7]);
-            }
-        }
-    }
-    __device__ __forceinline__ void store_shared(uint32_t p, bool f32, const float (&v)[E]) const {
-#pragma unroll
-        for (int i = 0; i < E / 8; ++i) {
-            if (i >= count) continue;
-            const int e = (first + i * step) * 8;
-            const float* t = v + 8 * i;
-            if (f32) {
-                sts128(p + 4 * e, __float_as_int(t[0]), __float_as_int(t[1]), __float_as_int(t[2]), __float_as_int(t[3]));
-                sts128(p + 4 * e + 16, __float_as_int(t[4]), __float_as_int(t[5]), __float_as_int(t[6]), __float_as_int(t[7]));
-            } else {
-                sts128(p + 2 * e, f32x2_to_bf16x2(t[0], t[1]), f32x2_to_bf16x2(t[2], t[3]), f32x2_to_bf16x2(t[4], t[5]),
-                       f32x2_to_bf16x2(t[6], t[7]));
-            }
-        }
-    }
     __device__ __forceinline__ void store(void* p, bool f32, const float (&v)[E]) const {
         if (VEC) {
 #pragma unroll
@@ -376,9 +339,129 @@ struct RingParams {
     WaitCtl wait;
 };
 
-// T: the most threads that compute (a warp more copies)
-template <int E, int T>
-__global__ void __launch_bounds__(T + 32, T == 256 ? 2 : 1) block_norm_ring_kernel(const __grid_constant__ RingParams q) {
+// Eight values as pairs, and back.
+__device__ __forceinline__ void pairs_bf16(uint4 a, F2 (&t)[4]) {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) t[k] = f2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
+}
+template <bool F32>
+__device__ __forceinline__ void pairs_shared(uint32_t p, F2 (&t)[4]) {
+    if (F32) {
+        const uint4 a = lds128(p), b = lds128(p + 16);
+        t[0] = f2(__uint_as_float(a.x), __uint_as_float(a.y));
+        t[1] = f2(__uint_as_float(a.z), __uint_as_float(a.w));
+        t[2] = f2(__uint_as_float(b.x), __uint_as_float(b.y));
+        t[3] = f2(__uint_as_float(b.z), __uint_as_float(b.w));
+    } else {
+        pairs_bf16(lds128(p), t);
+    }
+}
+template <bool F32>
+__device__ __forceinline__ void put_pairs_shared(uint32_t p, const F2* t) {
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) unpack(t[k], v[2 * k], v[2 * k + 1]);
+    if (F32) {
+        sts128(p, __float_as_int(v[0]), __float_as_int(v[1]), __float_as_int(v[2]), __float_as_int(v[3]));
+        sts128(p + 16, __float_as_int(v[4]), __float_as_int(v[5]), __float_as_int(v[6]), __float_as_int(v[7]));
+    } else {
+        sts128(p, f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]), f32x2_to_bf16x2(v[4], v[5]), f32x2_to_bf16x2(v[6], v[7]));
+    }
+}
+__device__ __forceinline__ void pairs_global(const void* p, bool f32, int e, F2 (&t)[4]) {
+    float v[8];
+    row_load8(p, f32, e, v);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) t[k] = f2(v[2 * k], v[2 * k + 1]);
+}
+
+template <int N>
+__device__ __forceinline__ float pair_squares(const F2 (&v)[N]) {
+    F2 s = f2(0.f, 0.f), t = s;
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        s = fma2(v[i], v[i], s);
+        t = fma2(v[i + 1], v[i + 1], t);
+    }
+    float a, b;
+    unpack(add2(s, t), a, b);
+    return a + b;
+}
+template <int N>
+__device__ __forceinline__ float pair_sum(const F2 (&v)[N], float scale) {
+    F2 s = f2(0.f, 0.f);
+    const F2 w = f2(scale, scale);
+#pragma unroll
+    for (int i = 0; i < N; ++i) s = fma2(v[i], w, s);
+    float a, b;
+    unpack(s, a, b);
+    return a + b;
+}
+
+// As normalise(), for a row that the team's threads hold to the last element: the centred (and, beyond
+// fp32's range, scaled) values stay in v, what they are to be multiplied with is returned.
+template <int N>
+__device__ __forceinline__ float centred(F2 (&v)[N], const NormSide& n, Team<true>& team, int dim) {
+    const float inv_dim = 1.f / dim;
+    float ss;
+    if (n.kind == DL_NORM_LAYER) {
+        const float mean = team.sum(pair_sum(v, inv_dim));
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = add2(v[i], f2(-mean, -mean));
+        const float2 t = team.sum(make_float2(pair_sum(v, inv_dim), pair_squares(v)));
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = add2(v[i], f2(-t.x, -t.x));
+        ss = t.y <= 1e37f ? fmaxf(fmaf(-dim * t.x, t.x, t.y), 0.f) : t.y;
+    } else {
+        ss = team.sum(pair_squares(v));
+    }
+    float inv = 1.f / sqrtf(fmaf(ss, inv_dim, n.eps));
+    if (ss > 1e37f || (ss < 1e-30f && n.eps < 1e-30f)) {
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float a, b;
+            unpack(v[i], a, b);
+            m = fmaxf(m, fmaxf(fabsf(a), fabsf(b)));
+        }
+        m = team.max(m);
+        if (m > 0.f && m <= 3.4028235e38f) {
+            const float up = ldexpf(1.f, -max(ilogbf(m), -100));
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = mul2(v[i], f2(up, up));
+            ss = team.sum(pair_squares(v));
+            inv = 1.f / sqrtf(fmaf(ss, inv_dim, n.eps * up * up));
+        }
+    }
+    return inv;
+}
+
+// Eight values of N(v): v inv w + b.
+__device__ __forceinline__ void finish8(F2* v, float inv, const NormSide& n, int e) {
+    F2 w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = mul2(v[k], f2(inv, inv));
+    if (n.weight) {
+        pairs_global(n.weight, n.f32, e, w);
+        if (n.offset != 0.f) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = add2(w[k], f2(n.offset, n.offset));
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = mul2(v[k], w[k]);
+    }
+    if (n.bias) {
+        pairs_global(n.bias, n.f32, e, w);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = add2(v[k], w[k]);
+    }
+}
+
+// The threads that compute hold E elements of a row each, all of it; a warp more copies.  YF, HF, XF: y, h and r, x
+// are fp32.
+template <int E, bool YF, bool HF, bool XF>
+__global__ void __launch_bounds__(256 + 32, 2) block_norm_ring_kernel(const __grid_constant__ RingParams q) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float2 red[64];
     __shared__ __align__(8) unsigned long long bars[16];         // rows in place, rows made
@@ -402,28 +485,29 @@ __global__ void __launch_bounds__(T + 32, T == 256 ? 2 : 1) block_norm_ring_kern
     auto row_of = [&](int i) { return (long long)blockIdx.x + (long long)i * gridDim.x; };
     if (warp == warps) {
         if (lane == 0) {
-            auto load = [&](int i) {
-                const uint32_t to = ring + i % S * stage_bytes, bar = full + 8 * (i % S);
+            auto load = [&](int i, int stage) {
+                const uint32_t to = ring + stage * stage_bytes, bar = full + 8 * stage;
                 mbar_arrive_expect_tx(bar, stage_bytes);
                 bulk_load(to, row_ptr(p.y, row_of(i)), q.y_bytes, bar);
                 bulk_load(to + q.y_bytes, row_ptr(p.h, row_of(i)), q.h_bytes, bar);
             };
-            int loaded = 0;
-            while (loaded < min(S, n)) load(loaded++);
+            int loaded = 0, stage = 0, turn = 0;
+            for (; loaded < min(S, n); ++loaded) load(loaded, loaded);
             for (int i = 0; i < n && !dead; ++i) {
-                if (!mbar_wait_bounded(made + 8 * (i % S), (i / S) & 1, q.wait, kErrProducerWait)) {
+                if (!mbar_wait_bounded(made + 8 * stage, turn & 1, q.wait, kErrProducerWait)) {
                     dead = 1;
                     break;
                 }
                 if (dead) break;
-                const uint32_t from = ring + i % S * stage_bytes;
-                bulk_store(row_ptr(p.x, row_of(i)), from, p.dim * (p.x.f32 ? 4 : 2));
+                const uint32_t from = ring + stage * stage_bytes;
+                bulk_store(row_ptr(p.x, row_of(i)), from, p.dim * (XF ? 4 : 2));
                 bulk_store(row_ptr(p.r, row_of(i)), from + q.y_bytes, q.h_bytes);
                 asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                 if (loaded < n) {
                     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                    load(loaded++);
+                    load(loaded++, stage);
                 }
+                if (++stage == S) stage = 0, ++turn;
             }
             asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
             if (dead)                    // what is on its way arrives before the CTA leaves
@@ -433,21 +517,69 @@ __global__ void __launch_bounds__(T + 32, T == 256 ? 2 : 1) block_norm_ring_kern
         return;
     }
     Team<true> team{red, 0, 32 * warps};
-    const Slots<E, true> slots(tid, 32 * warps, p.dim);
+    const int size = 256 * warps;        // elements from one of a thread's groups of 8 to the next
+    int stage = 0, turn = 0;
     for (int i = 0; i < n; ++i) {
-        if (!dead && !mbar_wait_bounded(full + 8 * (i % S), (i / S) & 1, q.wait, kErrConsumerWait)) dead = 1;
+        if (!dead && !mbar_wait_bounded(full + 8 * stage, turn & 1, q.wait, kErrConsumerWait)) dead = 1;
         __syncwarp();
-        const uint32_t at = ring + i % S * stage_bytes;
-        float v[E], h[E];
-        slots.load_shared(at, p.y.f32, v);
-        slots.load_shared(at + q.y_bytes, p.h.f32, h);
-        join(v, h, p, row_of(i), team, slots);
-        slots.store_shared(at + q.y_bytes, p.r.f32, v);
-        normalise<E, true, true>(v, p.pre, team, slots, p.dim);
-        slots.store_shared(at, p.x.f32, v);      // (all have read y: the norm's sum came after it)
+        const uint32_t at = ring + stage * stage_bytes, at_y = at + tid * (YF ? 32 : 16), at_h = at + q.y_bytes + tid * (HF ? 32 : 16);
+        F2 v[E / 2];
+#pragma unroll
+        for (int k = 0; k < E / 8; ++k) {
+            F2 t[4];
+            pairs_shared<YF>(at_y + k * size * (YF ? 4 : 2), t);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[4 * k + j] = t[j];
+        }
+        if (p.post.kind != DL_NORM_NONE) {
+            const float inv = centred(v, p.post, team, p.dim);
+#pragma unroll
+            for (int k = 0; k < E / 8; ++k) finish8(v + 4 * k, inv, p.post, tid * 8 + k * size);
+        }
+        if (p.gate_kind != DL_GATE_NONE) {
+            const char* gate = p.gate_kind == DL_GATE_CHANNEL ? p.gate.ptr : row_ptr(p.gate, row_of(i));
+            const float one = p.gate_kind == DL_GATE_ROW ? row_load1(gate, p.gate.f32, 0) : 0.f;
+#pragma unroll
+            for (int k = 0; k < E / 8; ++k) {
+                float g[8], a, b;
+                if (p.gate_kind == DL_GATE_ROW) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) g[j] = one;
+                } else {
+                    row_load8(gate, p.gate.f32, tid * 8 + k * size, g);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    a = g[2 * j];
+                    b = g[2 * j + 1];
+                    if (p.sigmoid) {
+                        a = 1.f / (1.f + expf(-a));
+                        b = 1.f / (1.f + expf(-b));
+                    }
+                    v[4 * k + j] = mul2(v[4 * k + j], f2(a, b));
+                }
+            }
+        }
+        const F2 scale = f2(p.scale, p.scale), h_scale = f2(p.h_scale, p.h_scale);
+#pragma unroll
+        for (int k = 0; k < E / 8; ++k) {
+            F2 t[4];
+            pairs_shared<HF>(at_h + k * size * (HF ? 4 : 2), t);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[4 * k + j] = fma2(t[j], h_scale, mul2(v[4 * k + j], scale));
+            put_pairs_shared<HF>(at_h + k * size * (HF ? 4 : 2), v + 4 * k);
+        }
+        const float inv = centred(v, p.pre, team, p.dim);
+#pragma unroll
+        for (int k = 0; k < E / 8; ++k) {
+            finish8(v + 4 * k, inv, p.pre, tid * 8 + k * size);
+            // (all have read y: the norm's sum came after it)
+            put_pairs_shared<XF>(at + (tid * 8 + k * size) * (XF ? 4 : 2), v + 4 * k);
+        }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(made + 8 * (i % S));
+        if (lane == 0) mbar_arrive(made + 8 * stage);
+        if (++stage == S) stage = 0, ++turn;
     }
 }
 
@@ -461,36 +593,42 @@ cudaError_t launch_norm(const BlockNormParams& p, long long grid, int threads, c
                : launch_dependent(block_norm_kernel<E, VEC, CTA, false, T>, dim3((unsigned)grid), dim3(threads), 0, stream, p);
 }
 
-template <int E, int T>
-cudaError_t launch_ring_kernel(const RingParams& q, int threads, int sm_count, cudaStream_t stream) {
-    const size_t smem = (size_t)q.stages * (q.y_bytes + q.h_bytes);
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(block_norm_ring_kernel<E, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+template <int E, bool YF, bool HF, bool XF>
+cudaError_t launch_ring_kernel(RingParams& q, int sm_count, cudaStream_t stream) {
+    const int threads = q.n.dim / E, stage = q.y_bytes + q.h_bytes;
+    // CTAs of an SM: 512 threads' worth, with two rows each at least
+    int ctas = 512 / threads;
+    while (ctas > 1 && 220 * 1024 / (ctas * stage) < 2) --ctas;
+    q.stages = 220 * 1024 / (ctas * stage);
+    if (q.stages > 4) q.stages = 4;
+    const size_t smem = (size_t)q.stages * stage;
+    if (smem > 47 * 1024) {                  // (and less than 1 KB that is not dynamic)
+        const cudaError_t e = cudaFuncSetAttribute(block_norm_ring_kernel<E, YF, HF, XF>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    const int by_smem = 226 * 1024 / (int)(smem + 2048), by_threads = T == 256 ? 2 * 256 / threads : 1;
-    const int ctas = by_smem < by_threads ? by_smem : by_threads;
     const int most = ctas * sm_count;
-    return launch_dependent(block_norm_ring_kernel<E, T>, dim3(q.n.rows < most ? q.n.rows : most), dim3(threads + 32), smem, stream, q);
+    return launch_dependent(block_norm_ring_kernel<E, YF, HF, XF>, dim3(q.n.rows < most ? q.n.rows : most), dim3(threads + 32),
+                            smem, stream, q);
+}
+
+template <int E>
+cudaError_t launch_ring_types(RingParams& q, int sm_count, cudaStream_t stream) {
+    const bool h = q.n.h.f32;
+    if (!q.n.y.f32)
+        return h ? launch_ring_kernel<E, false, true, false>(q, sm_count, stream) : launch_ring_kernel<E, false, false, false>(q, sm_count, stream);
+    if (!q.n.x.f32)
+        return h ? launch_ring_kernel<E, true, true, false>(q, sm_count, stream) : launch_ring_kernel<E, true, false, false>(q, sm_count, stream);
+    return h ? launch_ring_kernel<E, true, true, true>(q, sm_count, stream) : launch_ring_kernel<E, true, false, true>(q, sm_count, stream);
 }
 
 // Many rows of more than 1024 elements through the ring: where all streams are there, r has h's type, x is no
-// wider than y, and a few rows fit shared memory.  (Fewer rows are no faster: ...)
-static bool launch_ring(const BlockNormParams& p, int groups, int sm_count, const WaitCtl& wait, cudaStream_t stream, cudaError_t& e) {
+// wider than y, and whole warps of threads hold a row: 16 elements each up to 4096, 32 up to 8192.
+static bool launch_ring(const BlockNormParams& p, int sm_count, const WaitCtl& wait, cudaStream_t stream, cudaError_t& e) {
     if (!p.y.ptr || !p.h.ptr || !p.r.ptr || !p.x.ptr || p.pre.kind == DL_NORM_NONE || p.r.f32 != p.h.f32 ||
-        (p.x.f32 && !p.y.f32) || p.rows < 4 * sm_count || p.dim > 16384)
+        (p.x.f32 && !p.y.f32) || p.rows < 4 * sm_count || p.dim > 8192 || p.dim % (p.dim <= 4096 ? 512 : 1024))
         return false;
     RingParams q = {p, 0, p.dim * (p.y.f32 ? 4 : 2), p.dim * (p.h.f32 ? 4 : 2), wait};
-    const int stage = q.y_bytes + q.h_bytes;
-    const bool small = p.dim <= 4096, large = p.dim > 8192;
-    const int threads = ((small ? (groups + 1) / 2 : (groups + 3) / 4) + 31) / 32 * 32;
-    const int ctas = large ? 1 : 2 * 256 / threads;
-    q.stages = 220 * 1024 / (ctas * stage);
-    if (q.stages < 2) q.stages = 220 * 1024 / stage;
-    if (q.stages < 2) return false;
-    if (q.stages > 4) q.stages = 4;
-    e = small ? launch_ring_kernel<16, 256>(q, threads, sm_count, stream)
-        : large ? launch_ring_kernel<32, 512>(q, threads, sm_count, stream) : launch_ring_kernel<32, 256>(q, threads, sm_count, stream);
+    e = p.dim <= 4096 ? launch_ring_types<16>(q, sm_count, stream) : launch_ring_types<32>(q, sm_count, stream);
     return true;
 }
 
@@ -509,7 +647,7 @@ cudaError_t launch_norm_rows(BlockNormParams& p, int sm_count, const WaitCtl& wa
         return launch_norm<32, VEC, false, 128>(p, grid, threads, stream);
     }
     cudaError_t e;
-    if (VEC && launch_ring(p, groups, sm_count, wait, stream, e)) return e;
+    if (VEC && launch_ring(p, sm_count, wait, stream, e)) return e;
     // A CTA each: one group a thread where there are few rows, so that a row is loaded at once, or short
     // ones; two where there are many long ones
     int per = p.rows <= 2 * sm_count || groups <= 256 ? 1 : 2;
