@@ -274,7 +274,7 @@ __device__ __forceinline__ void join(float (&v)[E], const float (&h)[E], const B
             }
             if (p.sigmoid) {
 #pragma unroll
-                for (int i = 0; i < E; ++i) g[i] = 1.f / (1.f + expf(-g[i]));
+                for (int i = 0; i < E; ++i) g[i] = __fdividef(1.f, 1.f + expf(-g[i]));
             }
             times(v, g);
 #pragma unroll
@@ -553,8 +553,8 @@ __global__ void __launch_bounds__(256 + 32, 2) block_norm_ring_kernel(const __gr
                     a = g[2 * j];
                     b = g[2 * j + 1];
                     if (p.sigmoid) {
-                        a = 1.f / (1.f + expf(-a));
-                        b = 1.f / (1.f + expf(-b));
+                        a = __fdividef(1.f, 1.f + expf(-a));
+                        b = __fdividef(1.f, 1.f + expf(-b));
                     }
                     v[4 * k + j] = mul2(v[4 * k + j], f2(a, b));
                 }
@@ -648,12 +648,16 @@ cudaError_t launch_norm_rows(BlockNormParams& p, int sm_count, const WaitCtl& wa
     }
     cudaError_t e;
     if (VEC && launch_ring(p, sm_count, wait, stream, e)) return e;
-    // A CTA each: one group a thread where there are few rows, so that a row is loaded at once, or short
-    // ones; two where there are many long ones
-    int per = p.rows <= 2 * sm_count || groups <= 256 ? 1 : 2;
-    while ((groups + per - 1) / per > 1024) per *= 2;
-    const int threads = ((groups + per - 1) / per + 31) / 32 * 32;
-    const long long fit = 1024 / threads, most = (fit > 8 ? 8 : fit) * sm_count;
+    // A CTA each: as few groups a thread as leave all rows an SM at once, two if none does; single elements
+    // one group (999 rows of 1537: 14 us; two 30 us)
+    int per = 1, threads = 0;
+    long long most = 0;
+    for (;; per *= 2) {
+        threads = ((groups + per - 1) / per + 31) / 32 * 32;
+        const long long fit = 1024 / threads;
+        most = (fit > 8 ? 8 : fit) * sm_count;
+        if (threads <= 1024 && (p.rows <= most || per >= 2 || !VEC)) break;
+    }
     const long long grid = p.rows < most ? p.rows : most;
     if (per == 1)
         return threads <= 256 ? launch_norm<8, VEC, true, 256>(p, grid, threads, stream)
