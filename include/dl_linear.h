@@ -549,6 +549,7 @@ size_t dl_adapters_workspace_bytes(int tokens, int num, int rank, int parts);
 typedef struct dl_kv_pages {
     const dl_kv_cache* caches;   /* HOST array, one of each layer: num_pages and page_size as
                                     here, the other sizes alike; may be NULL (no caches) */
+    const dl_kv_cache* device_caches;    /* the same array on the device                  */
     int* refs;                   /* [num_pages]         */
     int* block_table;            /* [rows][table_cols]  */
     int* seq_lens;               /* [rows]              */

@@ -102,13 +102,13 @@ def test_adapters_workspace():
     assert linear(nbytes=fn(5, 4, 16, 2) - 1) == 4
 
 
-def pool(refs=REFS, table=TAB, lens=LENS, num_pages=10, page_size=64, rows=8, cols=4, caches=1, **kw):
+def pool(refs=REFS, table=TAB, lens=LENS, num_pages=10, page_size=64, rows=8, cols=4, caches=1, dev=W, **kw):
     d = dict(k=Y, v=H, k_scale=G, v_scale=R, page_stride=2 * 64 * 128, head_stride=64 * 128, scale_page_stride=8,
              scale_head_stride=4, num_pages=10, num_heads=2, page_size=64, head_dim=128, block=16)
     n = max(caches, 1)
     arr = (dl._KVCache * n)(*[dl._KVCache(*({**d, **(kw if j == n - 1 else {})}[k] for k, _ in dl._KVCache._fields_))
                               for j in range(n)])
-    p = dl._KVPages(arr if caches else None, refs, table, lens, max(caches, 0) or caches, num_pages, page_size, rows, cols)
+    p = dl._KVPages(arr if caches else None, dev, refs, table, lens, max(caches, 0) or caches, num_pages, page_size, rows, cols)
     p.keep = arr
     return p
 
@@ -143,7 +143,7 @@ def test_bad_pools(fault, status):
 @pytest.mark.parametrize("fault,status", [
     (dict(caches=2, num_heads=1), 1), (dict(caches=2, head_dim=64), 1), (dict(caches=2, block=8, scale_head_stride=8, scale_page_stride=16), 1),
     (dict(caches=3, k=Y + 8), 3), (dict(caches=1, num_pages=11), 1), (dict(num_pages=11, caches=2), 1),
-    (dict(caches=2, v=None), 1)])
+    (dict(caches=2, v=None), 1), (dict(dev=None), 1), (dict(dev=W + 4), 3)])
 def test_bad_caches_of_a_pool(fault, status):
     if fault.get("num_pages") == 11 and fault["caches"] == 1:
         p = pool()
@@ -178,7 +178,7 @@ def test_pages_workspace():
 def test_descriptor_layouts():
     assert ctypes.sizeof(dl._Norm) == 32 and dl._Norm.kind.offset == 24
     assert ctypes.sizeof(dl._Adapters) == 4 * 8 + 5 * 4 + 8 * 4 + 4 and dl._Adapters.part_end.offset == 52
-    assert ctypes.sizeof(dl._KVPages) == 4 * 8 + 5 * 4 + 4 and dl._KVPages.rows.offset == 44
+    assert ctypes.sizeof(dl._KVPages) == 5 * 8 + 5 * 4 + 4 and dl._KVPages.rows.offset == 52
 
 
 def test_cpu_tensors_are_refused():

@@ -81,7 +81,7 @@ class _Adapters(ctypes.Structure):
 
 
 class _KVPages(ctypes.Structure):
-    _fields_ = [("caches", ctypes.POINTER(_KVCache)), ("refs", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+    _fields_ = [("caches", ctypes.POINTER(_KVCache)), ("device_caches", ctypes.c_void_p), ("refs", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
                 ("seq_lens", ctypes.c_void_p), ("num_caches", ctypes.c_int), ("num_pages", ctypes.c_int),
                 ("page_size", ctypes.c_int), ("rows", ctypes.c_int), ("table_cols", ctypes.c_int)]
 
@@ -841,16 +841,19 @@ def block_norm(y, h=None, *, post: Norm | None = None, pre: Norm | None = None, 
     like = h if h is not None else y
     if not isinstance(like, torch.Tensor):
         raise TypeError("y or h must be a torch.Tensor")
+    made = 0
     if out_h is None and y is not None:
         out_h = torch.empty_like(like, memory_format=torch.contiguous_format) if stream is None else \
             _empty(like.shape, like.dtype, like.device, stream)
+        made = 1
     if out_x is None and (pre is not None or y is None):
         out_x = torch.empty_like(like, dtype=torch.bfloat16, memory_format=torch.contiguous_format) \
             if stream is None else _empty(like.shape, torch.bfloat16, like.device, stream)
+        made += 2
     index = like.get_device()
     if index < 0 or gate_act not in _GATE_ACTS or \
             not _call("norm", like.device, index, y, None if post is None else post._args, gate, _GATE_ACTS[gate_act],
-                      scale, h, h_scale, None if pre is None else pre._args, out_h, out_x, stream):
+                      scale, h, h_scale, None if pre is None else pre._args, out_h, out_x, stream, made):
         _explain_norm(y, h, post, pre, gate, gate_act, out_h, out_x)
     return out_h, out_x
 
@@ -946,9 +949,12 @@ def linear_adapters(x, adapters: Adapters, index, base=None, *, out=None, out_f3
     """
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
-    if out is None:
-        _need_matrix(x, "x", adapters.device, dtypes=(torch.bfloat16,))
-        out = _empty((x.shape[0], adapters.N), torch.bfloat16, adapters.device, stream)
+    made = out is None
+    if made:
+        if x.dim() != 2:
+            _need_matrix(x, "x", adapters.device, dtypes=(torch.bfloat16,))
+        out = torch.empty((x.shape[0], adapters.N), dtype=torch.bfloat16, device=adapters.device) if stream is None else \
+            _empty((x.shape[0], adapters.N), torch.bfloat16, adapters.device, stream)
     if workspace is None:
         _explain_adapters(x, adapters, index, base, out, out_f32)
         with torch.cuda.device(adapters.device):
@@ -956,7 +962,7 @@ def linear_adapters(x, adapters: Adapters, index, base=None, *, out=None, out_f3
     elif workspace.tensor.device != adapters.device:
         raise ValueError(f"workspace is on {workspace.tensor.device}, expected {adapters.device}")
     if not _call("adapters", adapters.device, adapters._args, x, index, base, out, out_f32, workspace.addr,
-                 workspace.nbytes, stream):
+                 workspace.nbytes, stream, made):
         _explain_adapters(x, adapters, index, base, out, out_f32)
         raise ValueError("stream must be an integer or a stream, sizes below 2^31")
     return out
@@ -1014,7 +1020,9 @@ class PagePool:
         self.caches, self.block_table, self.seq_lens, self.refs = caches, block_table, seq_lens, refs
         self.page_size, self.num_pages, self.rows, self.device = page_size, refs.shape[0], seq_lens.shape[0], dev
         self._caches = (_KVCache * max(1, len(caches)))(*[c._struct for c in caches])
-        self._struct = _KVPages(self._caches, refs.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), len(caches),
+        # the kernels read the caches' descriptions from the device
+        self._device_caches = torch.frombuffer(bytearray(self._caches), dtype=torch.uint8).to(dev)
+        self._struct = _KVPages(self._caches, self._device_caches.data_ptr(), refs.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), len(caches),
                                 self.num_pages, page_size, self.rows, block_table.shape[1])
         self._args = (ctypes.addressof(self._struct), dev.index)
 
@@ -1032,19 +1040,22 @@ def pages_workspace_bytes(pool: PagePool) -> int:
 
 
 def _pages(what, pool, first, second, out, workspace, stream):
+    made = what > 0 and out is None
     if what == 0:
         addr = nbytes = 0
     else:
-        if out is None:
-            n = 1 if what == 3 else first.numel() if isinstance(first, torch.Tensor) else 0
-            out = _empty((n,), torch.int32, pool.device, stream)
+        if made:
+            if what < 3:
+                _need(first, "rows" if what == 1 else "parents", torch.int32, pool.device)
+            out = torch.empty_like(first) if what < 3 and stream is None else \
+                _empty((1,) if what == 3 else first.shape, torch.int32, pool.device, stream)
         if workspace is None:
             with torch.cuda.device(pool.device):
                 workspace = _workspace(None, pages_workspace_bytes(pool), pool.device, stream)
         elif workspace.tensor.device != pool.device:
             raise ValueError(f"workspace is on {workspace.tensor.device}, expected {pool.device}")
         addr, nbytes = workspace.addr, workspace.nbytes
-    if not _call("pages", pool.device, what, pool._args, first, second, out, addr, nbytes, stream):
+    if not _call("pages", pool.device, what, pool._args, first, second, out, addr, nbytes, stream, made):
         lists = {0: ("rows",), 1: ("rows", "tokens"), 2: ("parents", "children"), 3: ()}[what]
         for t, n in zip((first, second), lists):
             _need(t, n, torch.int32, pool.device)

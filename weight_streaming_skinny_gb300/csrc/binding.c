@@ -285,6 +285,16 @@ static int look_at_matrix(PyObject* t, long long dev, view* v, dl_rows* r) {
     return 1;
 }
 
+/* The address of a dense tensor that the caller has just made. */
+static int look_at_made(PyObject* t, dl_rows* r, long long stride, int dtype) {
+    long long x;
+    if (!call_long(t, s_data_ptr, &x)) return 0;
+    r->data = (void*)(uintptr_t)x;
+    r->stride = stride;
+    r->dtype = dtype;
+    return 1;
+}
+
 /* A norm's description (address, length of its weights or -1, their device or -1), or None. */
 static int look_at_norm(PyObject* t, long long dim, long long dev, const dl_norm** out) {
     long long v[4];
@@ -295,11 +305,12 @@ static int look_at_norm(PyObject* t, long long dim, long long dev, const dl_norm
     return 1;
 }
 
-/* norm(device, y, post, gate, act, scale, h, h_scale, pre, out_h, out_x, stream) */
+/* norm(device, y, post, gate, act, scale, h, h_scale, pre, out_h, out_x, stream, made); made: 1 out_h, 2 out_x was made
+ * for this call, like h (or y), in bf16 */
 static PyObject* norm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     (void)self;
-    if (n != 12) return answer(LOOK);
-    const long long dev = PyLong_AsLongLong(a[0]), act = PyLong_AsLongLong(a[4]);
+    if (n != 13) return answer(LOOK);
+    const long long dev = PyLong_AsLongLong(a[0]), act = PyLong_AsLongLong(a[4]), made = PyLong_AsLongLong(a[12]);
     const double scale = PyFloat_AsDouble(a[5]), h_scale = PyFloat_AsDouble(a[7]);
     view v[5];
     dl_rows y, h, gate = {0}, r, x;
@@ -312,8 +323,10 @@ static PyObject* norm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     const view* like = a[1] != Py_None ? &v[0] : &v[1];
     const long long rows = like->shape[0], dim = like->shape[1];
     if ((a[6] != Py_None && (v[1].shape[0] != rows || v[1].shape[1] != dim)) ||
-        !look_at_matrix(a[9], dev, &v[2], &r) || (a[9] != Py_None && (v[2].shape[0] != rows || v[2].shape[1] != dim)) ||
-        !look_at_matrix(a[10], dev, &v[3], &x) || (a[10] != Py_None && (v[3].shape[0] != rows || v[3].shape[1] != dim)) ||
+        !(made & 1 ? look_at_made(a[9], &r, dim, a[6] != Py_None ? h.dtype : y.dtype)
+                   : look_at_matrix(a[9], dev, &v[2], &r) && (a[9] == Py_None || (v[2].shape[0] == rows && v[2].shape[1] == dim))) ||
+        !(made & 2 ? look_at_made(a[10], &x, dim, DL_ROWS_BF16)
+                   : look_at_matrix(a[10], dev, &v[3], &x) && (a[10] == Py_None || (v[3].shape[0] == rows && v[3].shape[1] == dim))) ||
         !look_at_norm(a[2], dim, dev, &post) || !look_at_norm(a[8], dim, dev, &pre) || !stream_of(a[11], dev, &stream))
         return answer(LOOK);
     if (a[3] != Py_None) {
@@ -341,12 +354,13 @@ static PyObject* norm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     return answer(status);
 }
 
-/* adapters((address, device, K, N), x, index, base, out, out_f32, workspace, bytes, stream) */
+/* adapters((address, device, K, N), x, index, base, out, out_f32, workspace, bytes, stream, made); made: 1 out was made
+ * for this call */
 static PyObject* adapters(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     (void)self;
     long long d[4];
-    if (n != 9 || integers(a[0], d) != 4) return answer(LOOK);
-    const long long dev = d[1], K = d[2], N = d[3];
+    if (n != 10 || integers(a[0], d) != 4) return answer(LOOK);
+    const long long dev = d[1], K = d[2], N = d[3], made = PyLong_AsLongLong(a[9]);
     const uintptr_t ws = (uintptr_t)PyLong_AsUnsignedLongLong(a[6]);
     const unsigned long long bytes = PyLong_AsUnsignedLongLong(a[7]);
     view v, i;
@@ -356,8 +370,10 @@ static PyObject* adapters(PyObject* self, PyObject* const* a, Py_ssize_t n) {
         return answer(LOOK);
     const long long T = v.shape[0];
     if (!look_at(a[2], g_i32, dev, 0, &i) || numel(&i) != T || !look_at_matrix(a[3], dev, &v, &base) ||
-        (a[3] != Py_None && (v.shape[0] != T || v.shape[1] != N)) || a[4] == Py_None || !look_at_matrix(a[4], dev, &v, &y) ||
-        y.dtype != DL_ROWS_BF16 || v.shape[0] != T || v.shape[1] != N || !look_at_matrix(a[5], dev, &v, &y32) ||
+        (a[3] != Py_None && (v.shape[0] != T || v.shape[1] != N)) ||
+        !(made ? look_at_made(a[4], &y, N, DL_ROWS_BF16)
+               : a[4] != Py_None && look_at_matrix(a[4], dev, &v, &y) && y.dtype == DL_ROWS_BF16 && v.shape[0] == T && v.shape[1] == N) ||
+        !look_at_matrix(a[5], dev, &v, &y32) ||
         (a[5] != Py_None && (y32.dtype != DL_ROWS_F32 || v.shape[0] != T || v.shape[1] != N)) ||
         !stream_of(a[8], dev, &stream))
         return answer(LOOK);
@@ -368,13 +384,14 @@ static PyObject* adapters(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     return answer(status);
 }
 
-/* pages(what, (address, device), list, list or None, done or live or None, workspace, bytes, stream); what: 0 free,
- * 1 reserve, 2 fork, 3 compact (no lists) */
+/* pages(what, (address, device), list, list or None, done or live or None, workspace, bytes, stream, made); what: 0 free,
+ * 1 reserve, 2 fork, 3 compact (no lists); made: 1 done or live was made for this call */
 static PyObject* pages(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     (void)self;
     long long d[4];
-    if (n != 8 || integers(a[1], d) != 2) return answer(LOOK);
-    const long long what = PyLong_AsLongLong(a[0]), dev = d[1];
+    if (n != 9 || integers(a[1], d) != 2) return answer(LOOK);
+    const long long what = PyLong_AsLongLong(a[0]), dev = d[1], made = PyLong_AsLongLong(a[8]);
+    dl_rows out;
     const dl_kv_pages* pool = (const dl_kv_pages*)(uintptr_t)d[0];
     const uintptr_t ws = (uintptr_t)PyLong_AsUnsignedLongLong(a[5]);
     const unsigned long long bytes = PyLong_AsUnsignedLongLong(a[6]);
@@ -384,7 +401,10 @@ static PyObject* pages(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     if (what < 3 && (!look_at(a[2], g_i32, dev, 0, &x) || x.dims != 1 || !fits(x.shape[0]))) return answer(LOOK);
     if ((what == 1 || what == 2) && (!look_at(a[3], g_i32, dev, 0, &y) || y.dims != 1 || y.shape[0] != x.shape[0]))
         return answer(LOOK);
-    if (what > 0 && (!look_at(a[4], g_i32, dev, 0, &z) || z.dims != 1 || z.shape[0] != (what == 3 ? 1 : x.shape[0])))
+    if (made) {
+        if (!look_at_made(a[4], &out, 0, 0)) return answer(LOOK);
+        z.ptr = out.data;
+    } else if (what > 0 && (!look_at(a[4], g_i32, dev, 0, &z) || z.dims != 1 || z.shape[0] != (what == 3 ? 1 : x.shape[0])))
         return answer(LOOK);
     if (!current(dev)) return answer(OTHER_DEVICE);
     const int count = (int)x.shape[0];

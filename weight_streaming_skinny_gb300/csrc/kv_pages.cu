@@ -58,25 +58,30 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sum, int& total) {
     return inc + (warp > 0 ? before : 0);
 }
 
+// Which of 16 pages from p on are free.
+__device__ __forceinline__ unsigned free_mask(const PageState& s, int p) {
+    unsigned m = 0;
+    if (!((uintptr_t)s.refs & 15) && p + 16 <= s.num_pages) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint4 v = ldg128(s.refs + p + 4 * k);
+            m |= ((int)v.x <= 0 ? 1u : 0u) << (4 * k) | ((int)v.y <= 0 ? 2u : 0u) << (4 * k) |
+                 ((int)v.z <= 0 ? 4u : 0u) << (4 * k) | ((int)v.w <= 0 ? 8u : 0u) << (4 * k);
+        }
+    } else {
+        for (int k = 0; k < 16; ++k)
+            if (p + k < s.num_pages && s.refs[p + k] <= 0) m |= 1u << k;
+    }
+    return m;
+}
+
 // The first `want` free pages, lowest first, into list; returns how many there are (at most want).
-// A thread looks at 16 pages a round.
-__device__ int free_pages(const PageState& s, int want, int* list, int* warp_sum) {
+// A thread looks at 16 pages a round; the first round's is done (`is_free`).
+__device__ int free_pages(const PageState& s, int want, unsigned is_free, int* list, int* warp_sum) {
     int found = 0;
-    const bool wide = !((uintptr_t)s.refs & 15);
     for (int p0 = 0; p0 < s.num_pages && found < want; p0 += 16 * kPlanThreads) {
         const int p = p0 + 16 * threadIdx.x;
-        unsigned is_free = 0;
-        if (wide && p + 16 <= s.num_pages) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint4 v = ldg128(s.refs + p + 4 * k);
-                is_free |= ((int)v.x <= 0 ? 1u : 0u) << (4 * k) | ((int)v.y <= 0 ? 2u : 0u) << (4 * k) |
-                           ((int)v.z <= 0 ? 4u : 0u) << (4 * k) | ((int)v.w <= 0 ? 8u : 0u) << (4 * k);
-            }
-        } else {
-            for (int k = 0; k < 16; ++k)
-                if (p + k < s.num_pages && s.refs[p + k] <= 0) is_free |= 1u << k;
-        }
+        if (p0) is_free = free_mask(s, p);
         int total;
         const int n = __popc(is_free);
         int at = found + block_scan(n, warp_sum, total) - n;
@@ -127,6 +132,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     const int tid = threadIdx.x;
     griddep_wait();
     griddep_launch_dependents();
+    const unsigned is_free = free_mask(s, 16 * tid);     // (its loads overlap what follows)
     for (int i = tid; i < s.rows; i += kPlanThreads) first[i] = 0x7fffffff;
     __syncthreads();
     for (int i = tid; i < p.n; i += kPlanThreads) {
@@ -162,7 +168,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         asked += total;
         if (i < p.n) p.plan[i] = q;
     }
-    const int got = free_pages(s, asked, p.list, warp_sum);
+    const int got = free_pages(s, asked, is_free, p.list, warp_sum);
     // all lengths have been read: they may change now
     for (int i = tid; i < p.n; i += kPlanThreads) {
         Plan q = p.plan[i];
@@ -205,25 +211,25 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
 
 // ---------------------------------------------------------------- copies
 
-constexpr int kCopyCaches = 64;          // caches of one launch
 constexpr int kCopyThreads = 256;
 
 struct CopyCaches {
-    char* codes[kCopyCaches][2];         // keys, values
-    float* scales[kCopyCaches][2];
-    long long page[kCopyCaches], head[kCopyCaches], scale_page[kCopyCaches], scale_head[kCopyCaches];
+    const dl_kv_cache* at;   // on the device
     int n, heads, dim, block;
 };
 
 // One head's `tokens` first tokens of a page, keys or values, by a warp.
 __device__ __forceinline__ void copy_head(const CopyCaches& c, int cache, int kv, int head, int src, int dst, int tokens) {
     const int lane = threadIdx.x & 31;
-    const char* from = c.codes[cache][kv] + src * c.page[cache] + head * c.head[cache];
-    char* to = c.codes[cache][kv] + dst * c.page[cache] + head * c.head[cache];
+    const dl_kv_cache& k = c.at[cache];
+    char* codes = static_cast<char*>(kv ? k.v : k.k) + head * k.head_stride;
+    float* scales = (kv ? k.v_scale : k.k_scale) + head * k.scale_head_stride;
+    const char* from = codes + src * k.page_stride;
+    char* to = codes + dst * k.page_stride;
     const int bytes = tokens * c.dim;    // a multiple of 64
     const int blocks = (tokens + c.block - 1) / c.block;
-    const float* sf = c.scales[cache][kv] + src * c.scale_page[cache] + head * c.scale_head[cache];
-    float* st = c.scales[cache][kv] + dst * c.scale_page[cache] + head * c.scale_head[cache];
+    const float* sf = scales + src * k.scale_page_stride;
+    float* st = scales + dst * k.scale_page_stride;
     for (int i = lane; i < blocks; i += 32) st[i] = sf[i];
     constexpr int kGroup = 8;            // 16-byte loads in flight
     for (int b0 = 16 * lane; b0 < bytes; b0 += 512 * kGroup) {
@@ -241,7 +247,6 @@ struct ForkParams {
     PageState s;
     const Plan* plan;
     int n;
-    bool tables;           // the first launch of a call: tables and counts too
 };
 
 // The forked rows' tables, the counts of the pages that they share, and their begun pages' contents.
@@ -252,16 +257,14 @@ __global__ void __launch_bounds__(kCopyThreads) fork_copy_kernel(const __grid_co
     const PageState& s = p.s;
     const int lane = threadIdx.x & 31;
     const long long warp = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5, warps = ((long long)gridDim.x * blockDim.x) >> 5;
-    if (p.tables) {
-        for (long long i = warp; i < p.n; i += warps) {
-            const Plan q = p.plan[i];
-            if (q.len < 0) continue;
-            const int full = q.len / s.page_size;
-            for (int k = lane; k < full; k += 32) {
-                const int page = s.table[(size_t)q.from * s.cols + k];
-                s.table[(size_t)q.row * s.cols + k] = page;
-                if (in_pool(s, page)) atomicAdd(&s.refs[page], 1);
-            }
+    for (long long i = warp; i < p.n; i += warps) {
+        const Plan q = p.plan[i];
+        if (q.len < 0) continue;
+        const int full = q.len / s.page_size;
+        for (int k = lane; k < full; k += 32) {
+            const int page = s.table[(size_t)q.from * s.cols + k];
+            s.table[(size_t)q.row * s.cols + k] = page;
+            if (in_pool(s, page)) atomicAdd(&s.refs[page], 1);
         }
     }
     const long long units = (long long)p.n * c.n * 2 * c.heads;
@@ -278,7 +281,6 @@ struct CompactParams {
     int *head;             // moves, pages in use
     int *src, *dst, *to;   // the moves; where a page at or past the used ones went
     int* live;
-    bool tables;
 };
 
 // Pages in use from the front on: those past the first `live` places move, in order, into the free
@@ -343,12 +345,10 @@ __global__ void __launch_bounds__(kCopyThreads) compact_copy_kernel(const __grid
     const long long thread = (long long)blockIdx.x * blockDim.x + threadIdx.x, threads = (long long)gridDim.x * blockDim.x;
     const int moves = p.head[0], live = p.head[1];
     if (moves == 0) return;
-    if (p.tables) {
-        for (long long i = thread; i < (long long)s.rows * s.cols; i += threads) {
-            if ((int)(i % s.cols) >= pages_for(s, row_len(s, (int)(i / s.cols)))) continue;
-            const int page = s.table[i];
-            if (page >= live && page < s.num_pages) s.table[i] = p.to[page];
-        }
+    for (long long i = thread; i < (long long)s.rows * s.cols; i += threads) {
+        if ((int)(i % s.cols) >= pages_for(s, row_len(s, (int)(i / s.cols)))) continue;
+        const int page = s.table[i];
+        if (page >= live && page < s.num_pages) s.table[i] = p.to[page];
     }
     const long long units = (long long)moves * c.n * 2 * c.heads;
     for (long long u = thread >> 5; u < units; u += threads >> 5) {
@@ -382,8 +382,9 @@ static dl_status check_pages(const dl_kv_pages* g, bool caches, PageState& s) {
         return host_fail(DL_ERR_INVALID_ARG, "refs, block_table or seq_lens is NULL");
     if (((uintptr_t)g->refs | (uintptr_t)g->block_table | (uintptr_t)g->seq_lens) & 3)
         return host_fail(DL_ERR_MISALIGNED, "refs, block_table and seq_lens must be 4-byte aligned");
-    if (g->num_caches < 0 || (g->num_caches && !g->caches))
-        return host_fail(DL_ERR_INVALID_ARG, "caches is NULL or num_caches=%d negative", g->num_caches);
+    if (g->num_caches < 0 || (g->num_caches && (!g->caches || (caches && !g->device_caches))))
+        return host_fail(DL_ERR_INVALID_ARG, "caches or device_caches is NULL or num_caches=%d negative", g->num_caches);
+    if (caches && ((uintptr_t)g->device_caches & 7)) return host_fail(DL_ERR_MISALIGNED, "device_caches must be 8-byte aligned");
     for (int i = 0; caches && i < g->num_caches; ++i) {
         const dl_kv_cache &c = g->caches[i], &c0 = g->caches[0];
         const dl_status st = check_cache(&c);
@@ -428,24 +429,10 @@ static dl_status pages_scratch(const dl_kv_pages* g, void* ws, size_t ws_bytes, 
     return DL_OK;
 }
 
-// Caches first .. first + 63 of the pool.
-static void some_caches(const dl_kv_pages* g, int first, CopyCaches& c) {
-    c.n = g->num_caches - first < kCopyCaches ? g->num_caches - first : kCopyCaches;
-    for (int i = 0; i < c.n; ++i) {
-        const dl_kv_cache& k = g->caches[first + i];
-        c.codes[i][0] = static_cast<char*>(k.k);
-        c.codes[i][1] = static_cast<char*>(k.v);
-        c.scales[i][0] = k.k_scale;
-        c.scales[i][1] = k.v_scale;
-        c.page[i] = k.page_stride;
-        c.head[i] = k.head_stride;
-        c.scale_page[i] = k.scale_page_stride;
-        c.scale_head[i] = k.scale_head_stride;
-        c.heads = k.num_heads;
-        c.dim = k.head_dim;
-        c.block = k.block;
-    }
-    if (c.n <= 0) c.n = 0, c.heads = 1, c.dim = 64, c.block = 1;
+static CopyCaches copy_caches(const dl_kv_pages* g) {
+    if (!g->num_caches) return CopyCaches{nullptr, 0, 1, 64, 1};
+    const dl_kv_cache& k = g->caches[0];
+    return CopyCaches{g->device_caches, g->num_caches, k.num_heads, k.head_dim, k.block};
 }
 
 template <bool FORK>
@@ -505,17 +492,12 @@ extern "C" dl_status dl_kv_fork(const dl_kv_pages* pages, const int* parents, co
     const cudaStream_t stm = static_cast<cudaStream_t>(stream);
     const ListParams p = {s, parents, children, done, n, w.plan, w.list[0]};
     cudaError_t e = launch_plan<true>(p, stm);
-    int first = 0;
-    do {
-        CopyCaches c;
-        some_caches(pages, first, c);
-        const ForkParams f = {s, w.plan, n, first == 0};
-        const long long warps = (long long)n * (c.n ? c.n * 2 * c.heads : 1);
-        const long long ctas = (warps + kCopyThreads / 32 - 1) / (kCopyThreads / 32), most = 8LL * dev.sm_count;
-        if (e == cudaSuccess)
-            e = launch_dependent(fork_copy_kernel, dim3((unsigned)(ctas < most ? ctas : most)), dim3(kCopyThreads), 0, stm, f, c);
-        first += kCopyCaches;
-    } while (first < pages->num_caches);
+    const CopyCaches c = copy_caches(pages);
+    const ForkParams f = {s, w.plan, n};
+    const long long warps = (long long)n * (c.n ? c.n * 2LL * c.heads : 1);
+    const long long ctas = (warps + kCopyThreads / 32 - 1) / (kCopyThreads / 32), most = 8LL * dev.sm_count;
+    if (e == cudaSuccess)
+        e = launch_dependent(fork_copy_kernel, dim3((unsigned)(ctas < most ? ctas : most)), dim3(kCopyThreads), 0, stm, f, c);
     if (e != cudaSuccess) return host_fail(DL_ERR_CUDA, "kv_fork launch: %s", cudaGetErrorString(e));
     return host_ok();
 }
@@ -532,17 +514,10 @@ extern "C" dl_status dl_kv_compact(const dl_kv_pages* pages, int* live, void* wo
     HostDevice dev;
     if ((st = host_device(dev)) != DL_OK) return st;
     const cudaStream_t stm = static_cast<cudaStream_t>(stream);
-    CompactParams p = {s, w.head, w.list[0], w.list[1], w.list[2], live, true};
+    const CompactParams p = {s, w.head, w.list[0], w.list[1], w.list[2], live};
     cudaError_t e = launch_dependent(compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stm, p);
-    int first = 0;
-    do {
-        CopyCaches c;
-        some_caches(pages, first, c);
-        p.tables = first == 0;
-        if (e == cudaSuccess)
-            e = launch_dependent(compact_copy_kernel, dim3((unsigned)(8 * dev.sm_count)), dim3(kCopyThreads), 0, stm, p, c);
-        first += kCopyCaches;
-    } while (first < pages->num_caches);
+    if (e == cudaSuccess)
+        e = launch_dependent(compact_copy_kernel, dim3((unsigned)(8 * dev.sm_count)), dim3(kCopyThreads), 0, stm, p, copy_caches(pages));
     if (e != cudaSuccess) return host_fail(DL_ERR_CUDA, "kv_compact launch: %s", cudaGetErrorString(e));
     return host_ok();
 }
