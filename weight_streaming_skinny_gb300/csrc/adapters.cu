@@ -26,7 +26,7 @@ struct AdapterParams {
     Rows x, base, y, y32;
     const int* index;
     int tokens;
-    float* low;              // [tokens][parts * rank] scaled first products (small tiles)
+    uint16_t* low;           // [tokens][2 or 3][parts * rank] scaled first products in bf16 parts (small tiles)
     int* tiles;              // more than kFewTokens tokens: what sort_tokens_kernel writes
     int big_from;            // kBigFrom, or none if ranks are too large
     bool in_place, in_place32;   // base is y, y32: rows without an adapter stay as they are
@@ -36,10 +36,12 @@ struct AdapterParams {
     WaitCtl wait;
 };
 
-// Tokens of one adapter, up to kTile of them; the others -1.
+// Up to kTile tokens of one adapter.
 struct Tile {
-    int adapter, rank;       // adapter -1, rank 0: tokens without one
+    int adapter, rank, count;    // adapter -1, rank 0: tokens without one
+    float scale;
     int token[kTile];
+    __device__ int at(int i) const { return i < count ? token[i] : -1; }
 };
 // Tokens order[first .. first + count) of one adapter.
 struct BigTile {
@@ -72,6 +74,9 @@ __device__ __forceinline__ int adapter_of(const AdapterParams& p, int t) {
     const int a = p.index[t];
     return a >= 0 && a < p.num ? a : -1;
 }
+__device__ __forceinline__ float scale_of(const AdapterParams& p, int adapter) {
+    return adapter >= 0 && p.scale ? p.scale[adapter] : 1.f;
+}
 __device__ __forceinline__ int rank_of(const AdapterParams& p, int adapter) {
     return adapter < 0 ? 0 : p.ranks ? min(max(p.ranks[adapter], 0), p.rank) : p.rank;
 }
@@ -95,66 +100,66 @@ __device__ __forceinline__ int nth_bit(unsigned m, int n) {
     for (; n > 0; --n) m &= m - 1;
     return __ffs(m) - 1;
 }
+// The sum of a number's bytes.
+__device__ __forceinline__ int byte_sum(unsigned long long v) {
+    return __dp4a((unsigned)v, 0x01010101u, __dp4a((unsigned)(v >> 32), 0x01010101u, 0u));
+}
 
 __device__ __forceinline__ int make_tiles(const AdapterParams& p, FewTiles& s) {
     static_assert(kFewTokens == 256, "a byte for each of 8 warps");
     const int T = p.tokens, t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const unsigned below = (1u << lane) - 1;
-    const int mine = t < T ? adapter_of(p, t) : -2;
-    const int r = rank_of(p, mine);      // (its load overlaps what follows)
-    for (int i = t; i < T * (int)(sizeof(Tile) / 4); i += blockDim.x) reinterpret_cast<int*>(s.tile)[i] = -1;
     if (T <= 32) {
-        __syncthreads();
         if (warp == 0) {
+            const int mine = lane < T ? adapter_of(p, lane) : -2, r = rank_of(p, mine);
+            const float scale = scale_of(p, mine);
             const unsigned same = __match_any_sync(~0u, mine);
             const int place = __popc(same & below);
-            const unsigned m = __ballot_sync(~0u, t < T && place % kTile == 0);
-            if (t < T) {
+            const unsigned m = __ballot_sync(~0u, lane < T && place % kTile == 0);
+            if (lane < T) {
                 const int opener = nth_bit(same, place / kTile * kTile);
                 Tile& tile = s.tile[__popc(m & ((1u << opener) - 1))];
-                if (opener == t) {
+                if (opener == lane) {
                     tile.adapter = mine;
                     tile.rank = r;
+                    tile.scale = scale;
+                    tile.count = min(__popc(same) - place, kTile);
                 }
-                tile.token[place % kTile] = t;
+                tile.token[place % kTile] = lane;
             }
             if (lane == 0) s.n = __popc(m);
         }
         __syncthreads();
         return s.n;
     }
+    const int mine = t < T ? adapter_of(p, t) : -2;
+    const int r = rank_of(p, mine);      // (these loads overlap what follows)
+    const float scale = scale_of(p, mine);
     for (int i = t; i < kSlots; i += blockDim.x) {
         s.slot[i] = 0;
         s.held[i] = 0;
     }
+    const unsigned same = __match_any_sync(~0u, mine);
+    const int leader = __ffs(same) - 1;
+    int at = 0;
     __syncthreads();
-    unsigned same = 0;
-    int at = 0, place = 0;
-    bool opens = false;
-    if (t < kFewTokens) {
-        same = __match_any_sync(~0u, mine);
-        const int leader = __ffs(same) - 1;
-        if (t < T && lane == leader) {
-            at = (mine * 0x9E3779B1u) >> 23;     // 9 bits
-            while (true) {
-                const int found = atomicCAS(&s.slot[at], 0, mine + 2);
-                if (found == 0 || found == mine + 2) break;
-                at = (at + 1) % kSlots;
-            }
-            reinterpret_cast<unsigned char*>(&s.held[at])[warp] = (unsigned char)__popc(same);
+    if (t < T && lane == leader) {
+        at = (mine * 0x9E3779B1u) >> 23;         // 9 bits
+        while (true) {
+            const int found = atomicCAS(&s.slot[at], 0, mine + 2);
+            if (found == 0 || found == mine + 2) break;
+            at = (at + 1) % kSlots;
         }
-        at = __shfl_sync(~0u, at, leader);
+        reinterpret_cast<unsigned char*>(&s.held[at])[warp] = (unsigned char)__popc(same);
     }
+    at = __shfl_sync(~0u, at, leader);
     __syncthreads();
-    if (t < kFewTokens) {
-        // the bytes of the warps before this one
-        const unsigned long long before = s.held[at] & ((1ull << (8 * warp)) - 1);
-        place = __dp4a((unsigned)before, 0x01010101u, __dp4a((unsigned)(before >> 32), 0x01010101u, 0u)) + __popc(same & below);
-        opens = t < T && place % kTile == 0;
-        const unsigned m = __ballot_sync(~0u, opens);
-        if (lane == 0) s.opened[warp] = __popc(m);
-        same = m;                                // openers of this warp
-    }
+    // the bytes of the warps before this one, and of all
+    const unsigned long long held = s.held[at];
+    const int place = byte_sum(held & ((1ull << (8 * warp)) - 1)) + __popc(same & below);
+    const bool opens = t < T && place % kTile == 0;
+    const unsigned m = __ballot_sync(~0u, opens);
+    if (lane == 0) s.opened[warp] = __popc(m);
     __syncthreads();
     int n = 0, first = 0;
 #pragma unroll
@@ -163,10 +168,13 @@ __device__ __forceinline__ int make_tiles(const AdapterParams& p, FewTiles& s) {
         n += s.opened[w];
     }
     if (opens) {
-        const int number = first + __popc(same & below);
+        const int number = first + __popc(m & below);
         s.number[at][place / kTile] = (unsigned char)number;
-        s.tile[number].adapter = mine;
-        s.tile[number].rank = r;
+        Tile& tile = s.tile[number];
+        tile.adapter = mine;
+        tile.rank = r;
+        tile.scale = scale;
+        tile.count = min(byte_sum(held) - place, kTile);
     }
     __syncthreads();
     if (t < T) s.tile[s.number[at][place / kTile]].token[place % kTile] = t;
@@ -232,7 +240,8 @@ __global__ void __launch_bounds__(1024) sort_tokens_kernel(const __grid_constant
             Tile& tile = l.small[first[0] + j];
             tile.adapter = ad;
             tile.rank = r;
-            for (int k = min(n - j * kTile, kTile); k < kTile; ++k) tile.token[k] = -1;
+            tile.scale = scale_of(p, ad);
+            tile.count = min(n - j * kTile, kTile);
         }
         for (int j = 0; j < mine[1]; ++j)
             l.big[first[1] + j] = BigTile{ad, first[2] + j * kBigTile, min(n - j * kBigTile, kBigTile), r};
@@ -267,16 +276,37 @@ __global__ void __launch_bounds__(1024) sort_tokens_kernel(const __grid_constant
     }
 }
 
+// ---------------------------------------------------------------- parts
+
+// The fp32 first products go into the second ones as two bf16 parts (2^-18 of the value is lost), three
+// (24 bits: nothing) where an fp32 result is asked for.  The parts of a value and their products can
+// leave NaN where the value's own product is an infinity; what comes out NaN is summed again as it stands.
+// Two values as packed bf16 parts, each the next 8 bits of the value, rounded.  (An infinity's later parts are
+// NaN, and so is then what they are multiplied to.)
+template <int P>
+__device__ __forceinline__ void split(float a, float b, uint32_t (&v)[P]) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        v[i] = f32x2_to_bf16x2(a, b);
+        if (i + 1 < P) {
+            float ha, hb;
+            bf16x2_to_f32(v[i], ha, hb);
+            a -= ha;
+            b -= hb;
+        }
+    }
+}
+
 // ---------------------------------------------------------------- small tiles: first product
 
-// low[t][j] = scale * sum_k A[j][k] x[t][k]: a cluster of CTAs shares K, a warp takes 16 rows of A and
+// low[t][j] = scale * sum_k A[j][k] x[t][k], as the bf16 parts that the second product takes: a cluster of CTAs shares K, a warp takes 16 rows of A and
 // a tile's 16 tokens over its part of K.  A (and x) go from global memory straight into
 // the operands of mma.m16n8k16: the sum over k may take its terms in any order, so a lane's
 // 16-byte load of 8 consecutive k is the k-slots that it holds in two products.
 template <int N>
 using Int = std::integral_constant<int, N>;
 constexpr int kLowThreads = 256, kLowWarps = kLowThreads / 32;
-constexpr int kLowCluster = 8;
+constexpr int kLowCluster = 8;           // at most
 
 __global__ void __launch_bounds__(kLowThreads, 2) adapters_low_kernel(const __grid_constant__ AdapterParams p) {
     namespace cg = cooperative_groups;
@@ -303,23 +333,26 @@ __global__ void __launch_bounds__(kLowThreads, 2) adapters_low_kernel(const __gr
     const unsigned groups = (R + 15) / 16;
     // this warp's part of K: whole runs of 32
     const int runs = (K + 31) / 32, workers = size * kLowWarps, worker = rank * kLowWarps + warp;
-    const int k0 = (int)((long long)runs * worker / workers) * 32;
-    const int k1 = (int)((long long)runs * (worker + 1) / workers) * 32;
+    static_assert((kLowWarps & (kLowWarps - 1)) == 0, "a shift divides");
+    const int shift = 31 - __clz(workers);
+    const int k0 = (int)((long long)runs * worker >> shift) * 32, k1 = (int)((long long)runs * (worker + 1) >> shift) * 32;
     const unsigned per = p.parts * groups, items = n_tiles * per;      // fits: a launch of more is refused
+    bool waiting = false;
     for (unsigned item = blockIdx.x / size; item < items; item += gridDim.x / size) {
         const unsigned i = item % per;
         const int j0 = (int)(i % groups) * 16, pt = (int)(i / groups);
         const Tile& tile = tiles[item / per];
         const int ad = tile.adapter, r = tile.rank;
         if (j0 >= r) continue;
-        const int t0 = tile.token[g], t1 = tile.token[g + 8];
-        const bool two = tile.token[8] >= 0, row0 = j0 + g < r, row1 = j0 + g + 8 < r;
+        const int t0 = tile.at(g), t1 = tile.at(g + 8);
+        const bool two = tile.count > 8, row0 = j0 + g < r, row1 = j0 + g + 8 < r;
         const uint16_t* a0 = p.a + (((size_t)ad * p.parts + pt) * R + j0 + g) * K + 8 * c;
         const uint16_t* a1 = a0 + (size_t)8 * K;
         const char *x0 = row_ptr(p.x, max(t0, 0)) + 16 * c, *x1 = row_ptr(p.x, max(t1, 0)) + 16 * c;
         float d0[4] = {}, d1[4] = {};
         const uint4 none = {0, 0, 0, 0};
-        // `n` runs at a time, their loads all in flight; every lane takes part in every product
+        // `n` runs at a time, their loads all in flight (as far as this warp's part and K go); every lane takes
+        // part in every product
         auto steps = [&](auto count, auto second, int run) {
             constexpr int n = decltype(count)::value;
             constexpr bool both = decltype(second)::value;
@@ -327,7 +360,7 @@ __global__ void __launch_bounds__(kLowThreads, 2) adapters_low_kernel(const __gr
 #pragma unroll
             for (int i = 0; i < n; ++i) {
                 const int k = run + 32 * i;
-                const bool in = n > 1 || k + 8 * c < K;
+                const bool in = k < k1 && k + 8 * c < K;
                 va[i] = in && row0 ? ldg128(a0 + k) : none;
                 vb[i] = in && row1 ? ldg128(a1 + k) : none;
                 xa[i] = in && t0 >= 0 ? ldg128(x0 + 2 * k) : none;
@@ -343,15 +376,10 @@ __global__ void __launch_bounds__(kLowThreads, 2) adapters_low_kernel(const __gr
                 }
             }
         };
-        const int whole = min(k1, K / 32 * 32);
-        int run = k0;
         if (two) {
-            for (; run + 128 <= whole; run += 128) steps(Int<4>(), std::true_type(), run);
-            for (; run < k1; run += 32) steps(Int<1>(), std::true_type(), run);
+            for (int run = k0; run < k1; run += 128) steps(Int<4>(), std::true_type(), run);
         } else {
-            for (; run + 256 <= whole; run += 256) steps(Int<8>(), std::false_type(), run);
-            for (; run + 128 <= whole; run += 128) steps(Int<4>(), std::false_type(), run);
-            for (; run < k1; run += 32) steps(Int<1>(), std::false_type(), run);
+            for (int run = k0; run < k1; run += 256) steps(Int<8>(), std::false_type(), run);
         }
         // sum[warp][token * 16 + row]
 #pragma unroll
@@ -364,21 +392,31 @@ __global__ void __launch_bounds__(kLowThreads, 2) adapters_low_kernel(const __gr
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < kLowWarps; ++w) v += sum[w][tid];
+        if (waiting) cluster.barrier_wait();     // the others have read the last item's sums
         part[tid] = v;
         cluster.sync();
         // rank i finishes a share of the 256 sums
         const int each = 256 / size;
         if (tid < each) {
-            const int at = rank * each + tid, t = tile.token[at / 16], j = j0 + at % 16;
+            const int at = rank * each + tid, t = tile.at(at / 16), j = j0 + at % 16;
             float all = 0.f;
 #pragma unroll
             for (int q = 0; q < kLowCluster; ++q)
                 if (q < size) all += cluster.map_shared_rank(part, q)[at];
-            if (t >= 0 && j < r)
-                p.low[(size_t)t * p.parts * R + pt * R + j] = all * (p.scale ? p.scale[ad] : 1.f);
+            if (t >= 0 && j < R) {       // (zeros past the rank: it may end inside four that are read at once)
+                const size_t step = (size_t)p.parts * R;
+                uint16_t* to = p.low + (size_t)t * (p.y32.ptr ? 3 : 2) * step + pt * R + j;
+                uint32_t v[3];
+                split(j < r ? all * tile.scale : 0.f, 0.f, v);
+                to[0] = (uint16_t)v[0];
+                to[step] = (uint16_t)v[1];
+                if (p.y32.ptr) to[2 * step] = (uint16_t)v[2];
+            }
         }
-        cluster.sync();
+        cluster.barrier_arrive();
+        waiting = true;
     }
+    if (waiting) cluster.barrier_wait();
 }
 
 // ---------------------------------------------------------------- second product
@@ -387,30 +425,6 @@ __global__ void __launch_bounds__(kLowThreads, 2) adapters_low_kernel(const __gr
 // B's rows its columns.  32 consecutive columns are four products of 8 whose results lie four lanes to a
 // row, two columns a lane; which column is which product's is chosen so that a lane's eight results are
 // consecutive: lane c of a row has columns 8 c .. 8 c + 7, product i has 2 i and 2 i + 1 of each lane's.
-//
-// The fp32 values of `low` go into the products as two bf16 parts (2^-18 of the value is lost), three
-// (24 bits: nothing) where an fp32 result is asked for.  The parts of a value and their products can
-// leave NaN where the value's own product is an infinity; what comes out NaN is summed again as it stands.
-struct Parts {
-    uint32_t v[3];
-};
-// Two values as packed bf16 parts, each the next 8 bits of the value, rounded.
-__device__ __forceinline__ Parts split(float a, float b, int parts) {
-    Parts r = {};
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        if (i < parts) {
-            r.v[i] = f32x2_to_bf16x2(a, b);
-            float ha, hb;
-            bf16x2_to_f32(r.v[i], ha, hb);
-            a -= ha;
-            b -= hb;
-            if (a != a) a = 0.f;        // an infinity or NaN is whole in its first part
-            if (b != b) b = 0.f;
-        }
-    }
-    return r;
-}
 
 // Eight columns of a row from n on, as far as `end`; `wide`: whole and aligned.
 __device__ __forceinline__ void load_cols(const char* row, bool f32, int n, int end, bool wide, float (&v)[8]) {
@@ -437,15 +451,28 @@ __device__ __forceinline__ int part_of(const AdapterParams& p, int n) {
     return pt;
 }
 
-// Sums of eight columns from n on that came out NaN, as they stand; low: the token's first products, times
-// scale.
-__device__ __noinline__ void plain_up(const AdapterParams& p, const float* low, float scale, const uint16_t* b, int n, int r,
+// Sums of eight columns from n on that came out NaN, as they stand; `low`: a token's first products, times scale,
+// in fp32 (PACKED 0) or in that many bf16 parts.
+template <int PACKED>
+__device__ __noinline__ void plain_up(const AdapterParams& p, const void* low, float scale, const uint16_t* b, int n, int r,
                                       float (&v)[8]) {
+    const size_t step = (size_t)p.parts * p.rank;
     for (int k = 0; k < 8; ++k) {
         if (v[k] == v[k] || n + k >= p.N) continue;
-        const float* s = low + part_of(p, n + k) * p.rank;
+        const int at = part_of(p, n + k) * p.rank;
         v[k] = 0.f;
-        for (int i = 0; i < r; ++i) v[k] = fmaf(s[i] * scale, bf16_bits_to_f32(b[(size_t)(n + k) * p.rank + i]), v[k]);
+        for (int i = 0; i < r; ++i) {
+            float s = 0.f;
+            if (PACKED == 0) {
+                s = static_cast<const float*>(low)[at + i];
+            } else {
+                const uint16_t* q = static_cast<const uint16_t*>(low) + at + i;
+                s = bf16_bits_to_f32(q[0]);
+                if (fabsf(s) <= 3.4028235e38f)       // (an infinity's later parts are NaN)
+                    for (int j = 1; j < PACKED; ++j) s += bf16_bits_to_f32(q[j * step]);
+            }
+            v[k] = fmaf(s * scale, bf16_bits_to_f32(b[(size_t)(n + k) * p.rank + i]), v[k]);
+        }
     }
 }
 
@@ -455,15 +482,17 @@ __device__ __forceinline__ uint2 rank_mask(int at, int r) {
                       (at + 2 < r ? 0xffffu : 0u) | (at + 3 < r ? 0xffff0000u : 0u));
 }
 
-// Small tiles: a warp takes 32 columns of a tile, B's values of 32 r at a time.  What does not depend on the
-// first products (the tiles, base, B) is fetched before they are waited for: the kernel that makes them lets
-// this one start only after it had waited for all earlier ones.  P: parts of a first product.
-constexpr int kUpThreads = 256, kUpWarps = kUpThreads / 32;
+// Small tiles: a warp takes 64 columns of a tile, 16 r at a time.  What does not depend on the first products
+// (the tiles, base, B) is fetched before they are waited for: the kernel that makes them lets this one start only
+// after it had waited for all earlier ones.  Bound by instructions and latencies: a tile of few tokens costs as
+// much as one of 16, so each lane has all its loads of 16 r in flight at once.
+// BASE 0: none, 1: bf16, 2: fp32; P: parts of a first product (3: there is an fp32 result)
+constexpr int kUpThreads = 256, kUpWarps = kUpThreads / 32, kUpUnit = 64;
 
-template <int P>
+template <int BASE, int P>
 __global__ void __launch_bounds__(kUpThreads, 2) adapters_up_kernel(const __grid_constant__ AdapterParams p) {
     extern __shared__ __align__(16) unsigned char smem[];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     const Tile* tiles;
     int n_tiles;
     if (p.tokens <= kFewTokens) {
@@ -476,66 +505,71 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapters_up_kernel(const __grid
         tiles = l.small;
     }
     const int R = p.rank, N = p.N;
-    const unsigned units = (N + 31) / 32, items = n_tiles * units;      // fits: a launch of more is refused
+    const unsigned units = (N + kUpUnit - 1) / kUpUnit, items = n_tiles * units;    // fits: a launch of more is refused
     const size_t step = (size_t)p.parts * R;
     bool waited = false;
     for (unsigned item = blockIdx.x * kUpWarps + warp; item < items; item += gridDim.x * kUpWarps) {
         const Tile& tile = tiles[item / units];
-        const int n0 = (int)(item % units) * 32, n = n0 + 8 * c;
-        const int ad = tile.adapter, r = tile.rank, t0 = tile.token[g], t1 = tile.token[g + 8];
-        const bool whole = n0 + 32 <= N, wide = whole && p.wide;
-        const uint16_t* b = p.b + (size_t)max(ad, 0) * N * R;
-        float base[2][8] = {};
-        if (p.base.ptr) {
-            if (t0 >= 0) load_cols(row_ptr(p.base, t0), p.base.f32, n, N, wide, base[0]);
-            if (t1 >= 0) load_cols(row_ptr(p.base, t1), p.base.f32, n, N, wide, base[1]);
-        }
-        const int pt = part_of(p, n0), second = min(pt + 1, p.parts - 1);
-        const bool two = pt < second && n0 + 16 >= p.part_end[pt];      // the last 16 columns are the next part's
-        float d[4][4] = {};                  // [product][row g: 2 columns, row g + 8: 2 columns]
-        const int col = n0 + (g >> 1) * 8 + (g & 1);                    // of product 0; the others' are 2, 4, 6 further
-        for (int r0 = 0; r0 < r; r0 += 32) {
-            uint2 w[2][4];
-            const uint16_t* bl = b + (size_t)col * R + r0 + 4 * c;
+        const int n0 = (int)(item % units) * kUpUnit, n = n0 + 8 * c;
+        const int ad = tile.adapter, r = tile.rank, t0 = tile.at(g), t1 = tile.at(g + 8);
+        const bool whole = n0 + kUpUnit <= N, wide = whole && p.wide;
+        uint4 base[2][2][BASE == 2 ? 2 : 1];             // [row][32 columns]: eight of this lane
+        if (BASE != 0 && wide) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
+            for (int h = 0; h < 2; ++h) {
+                if ((h ? t1 : t0) < 0) continue;
+                const char* from = row_ptr(p.base, h ? t1 : t0) + (size_t)n * (BASE == 2 ? 4 : 2);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool in = r0 + 16 * q + 4 * c < r && (whole || col + 2 * i < N);
-                    w[q][i] = in ? ldg64(bl + 2 * i * R + 16 * q) : make_uint2(0, 0);
+                for (int u = 0; u < 2; ++u) {
+                    base[h][u][0] = ldg128(from + u * (BASE == 2 ? 128 : 64));
+                    if (BASE == 2) base[h][u][BASE == 2] = ldg128(from + u * 128 + 16);
                 }
+            }
+        }
+        // the parts of these columns: more than one only at a part's end
+        const int first = part_of(p, n0), last = part_of(p, min(n0 + kUpUnit, N) - 1);
+        float d[8][4] = {};                  // [product][row g: 2 columns, row g + 8: 2 columns]
+        const int col = n0 + (g >> 1) * 8 + (g & 1);     // of product 0; the others' are 2, 4, 6, 32, .. further
+        const uint16_t* b = p.b + ((size_t)max(ad, 0) * N + col) * R + 4 * c;
+        const uint16_t *low0 = p.low + (size_t)max(t0, 0) * P * step + 4 * c, *low1 = p.low + (size_t)max(t1, 0) * P * step + 4 * c;
+        for (int r0 = 0; r0 < r; r0 += 16) {
+            const bool in = r0 + 4 * c < r;
+            uint2 w[8];
+            if (whole) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = in ? ldg64(b + (2 * (i & 3) + 32 * (i >> 2)) * R + r0) : make_uint2(0, 0);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int at = 2 * (i & 3) + 32 * (i >> 2);
+                    w[i] = in && col + at < N ? ldg64(b + at * R + r0) : make_uint2(0, 0);
+                }
+            }
             if (!waited) {
                 griddep_wait();
                 griddep_launch_dependents();
                 waited = true;
             }
-            for (int k = 0; k <= (two ? 1 : 0); ++k) {
-                const float *low0 = p.low + t0 * step + (k ? second : pt) * R + r0 + 4 * c;
-                const float* low1 = p.low + t1 * step + (k ? second : pt) * R + r0 + 4 * c;
-                float4 s0[2], s1[2];
+            if (r0 + 16 > r) {               // what lies past the rank is nobody's
+                const uint2 m = rank_mask(r0 + 4 * c, r);
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const bool in = r0 + 16 * q + 4 * c < r;
-                    s0[q] = in && t0 >= 0 ? ld_cg_f32x4(low0 + 16 * q) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    s1[q] = in && t1 >= 0 ? ld_cg_f32x4(low1 + 16 * q) : make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int i = 0; i < 8; ++i) w[i] = make_uint2(w[i].x & m.x, w[i].y & m.y);
+            }
+            for (int pt = first; pt <= last; ++pt) {
+                uint2 a0[P], a1[P];
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    a0[j] = in && t0 >= 0 ? ldg64(low0 + j * step + pt * R + r0) : make_uint2(0, 0);
+                    a1[j] = in && t1 >= 0 ? ldg64(low1 + j * step + pt * R + r0) : make_uint2(0, 0);
                 }
-                // lanes g < 4 bring the first 16 columns of B, the others the last
-                const bool mine = !two || (g >= 4) == (k == 1);
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int at = r0 + 16 * q + 4 * c;
-                    if (r0 + 16 * q >= r) break;
-                    uint2 m = rank_mask(at, r);
-                    if (!mine) m = make_uint2(0, 0);
-                    const bool in1 = at + 1 < r, in2 = at + 2 < r, in3 = at + 3 < r;
-                    const Parts a0 = split(s0[q].x, in1 ? s0[q].y : 0.f, P), a1 = split(s1[q].x, in1 ? s1[q].y : 0.f, P);
-                    const Parts a2 = split(in2 ? s0[q].z : 0.f, in3 ? s0[q].w : 0.f, P);
-                    const Parts a3 = split(in2 ? s1[q].z : 0.f, in3 ? s1[q].w : 0.f, P);
+                for (int i = 0; i < 8; ++i) {
+                    // the columns of this part: 16 are brought by the lanes of four g
+                    const int at = n0 + 32 * (i >> 2) + (g >= 4 ? 16 : 0);
+                    const bool mine = first == last || (at < p.part_end[pt] && (pt == 0 || at >= p.part_end[pt - 1]));
+                    const uint2 v = mine ? w[i] : make_uint2(0, 0);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int j = 0; j < P; ++j)
-                            mma_bf16_16816(d[i], a0.v[j], a1.v[j], a2.v[j], a3.v[j], w[q][i].x & m.x, w[q][i].y & m.y);
+                    for (int j = 0; j < P; ++j) mma_bf16_16816(d[i], a0[j].x, a1[j].x, a0[j].y, a1[j].y, v.x, v.y);
                 }
             }
         }
@@ -546,7 +580,7 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapters_up_kernel(const __grid
         }
         float odd = 0.f;                     // NaN if any sum is, or infinite
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
             for (int k = 0; k < 4; ++k) odd = fmaf(d[i][k], 0.f, odd);
         const bool put = ad >= 0 || !p.in_place, put32 = P == 3 && (ad >= 0 || !p.in_place32);
@@ -554,14 +588,35 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapters_up_kernel(const __grid
         for (int h = 0; h < 2; ++h) {        // rows t0 and t1
             const int t = h ? t1 : t0;
             if (t < 0) continue;
-            float v[8];
+            char *to = row_ptr(p.y, t), *to32 = row_ptr(p.y32, t);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = d[k >> 1][2 * h + (k & 1)];
-            if (odd != odd) plain_up(p, p.low + t * step, 1.f, b, n, r, v);
+            for (int u = 0; u < 2; ++u) {
+                const int at = n + 32 * u;
+                float v[8], from[8] = {};
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] += base[h][k];
-            if (put) put_cols(row_ptr(p.y, t), false, n, N, wide, v);
-            if (put32) put_cols(row_ptr(p.y32, t), true, n, N, wide, v);
+                for (int k = 0; k < 8; ++k) v[k] = d[4 * u + (k >> 1)][2 * h + (k & 1)];
+                if (odd != odd) plain_up<P>(p, p.low + (size_t)t * P * step, 1.f, p.b + (size_t)max(ad, 0) * N * R, at, r, v);
+                if (BASE != 0) {
+                    if (!wide) {
+                        load_cols(row_ptr(p.base, t), BASE == 2, at, N, false, from);
+                    } else if (BASE == 1) {
+                        const uint4 x = base[h][u][0];
+                        bf16x2_to_f32(x.x, from[0], from[1]);
+                        bf16x2_to_f32(x.y, from[2], from[3]);
+                        bf16x2_to_f32(x.z, from[4], from[5]);
+                        bf16x2_to_f32(x.w, from[6], from[7]);
+                    } else {
+                        const uint4 x = base[h][u][0], y = base[h][u][BASE == 2];
+                        const uint32_t q[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) from[k] = __uint_as_float(q[k]);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] += from[k];
+                if (put) put_cols(to, false, at, N, wide, v);
+                if (put32) put_cols(to32, true, at, N, wide, v);
+            }
         }
     }
     if (!waited) griddep_wait();
@@ -919,9 +974,10 @@ __global__ void __launch_bounds__(kUpThreads, kUpCtas) adapters_up_big_kernel(co
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const bool in0 = 8 * i + 2 * k < r, in1 = 8 * i + 2 * k + 1 < r;
-                    const Parts s = split(in0 ? v[2 * k] * scale : 0.f, in1 ? v[2 * k + 1] * scale : 0.f, P);
+                    uint32_t s[P];
+                    split(in0 ? v[2 * k] * scale : 0.f, in1 ? v[2 * k + 1] * scale : 0.f, s);
 #pragma unroll
-                    for (int j = 0; j < P; ++j) out[j][k] = s.v[j];
+                    for (int j = 0; j < P; ++j) out[j][k] = s[j];
                 }
 #pragma unroll
                 for (int j = 0; j < P; ++j)
@@ -1006,7 +1062,7 @@ __global__ void __launch_bounds__(kUpThreads, kUpCtas) adapters_up_big_kernel(co
                         float x[8], from[8] = {};
 #pragma unroll
                         for (int j = 0; j < 8; ++j) x[j] = d[4 * v + (j >> 1)][2 * h + (j & 1)];
-                        if (odd != odd) plain_up(p, low + (h ? 8 * step : 0), scale, b, n, r, x);
+                        if (odd != odd) plain_up<0>(p, low + (h ? 8 * step : 0), scale, b, n, r, x);
                         if (p.base.ptr) load_cols(row_ptr(p.base, t), p.base.f32, n, n_end, wide, from);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) x[j] += from[j];
@@ -1069,9 +1125,9 @@ static int big_splits(long long tokens, int K) {
 }
 
 static size_t up256(size_t n) { return (n + 255) / 256 * 256; }
-static size_t low_bytes(long long tokens, int rank, int parts) { return up256((size_t)tokens * rank * parts * 4); }
+static size_t low_bytes(long long tokens, int rank, int parts) { return up256((size_t)tokens * rank * parts * 6); }
 static size_t low_big_bytes(long long tokens, int rank, int parts) {
-    return tokens > kFewTokens && rank <= kBigRank ? low_bytes(tokens, rank, parts) : 0;
+    return tokens > kFewTokens && rank <= kBigRank ? up256((size_t)tokens * rank * parts * 4) : 0;
 }
 static size_t lists_bytes(long long tokens, int num) {
     return tokens > kFewTokens ? up256(16 + (size_t)max_big(tokens, num) * sizeof(BigTile) + (size_t)tokens * 4 +
@@ -1123,21 +1179,32 @@ static cudaError_t raise_smem(F kernel, size_t bytes) {
 static cudaError_t launch_small(const AdapterParams& p, long long tiles, int sm_count, cudaStream_t stream, bool up) {
     const size_t smem = p.tokens <= kFewTokens ? sizeof(FewTiles) : 0;
     if (up) {
-        const long long ctas = (tiles * ((p.N + 31) / 32) + kUpWarps - 1) / kUpWarps, most = 2LL * sm_count;
-        const dim3 grid((unsigned)(ctas < most ? ctas : most));
-        return p.y32.ptr ? launch_dependent(adapters_up_kernel<3>, grid, dim3(kUpThreads), smem, stream, p)
-                         : launch_dependent(adapters_up_kernel<2>, grid, dim3(kUpThreads), smem, stream, p);
+        const long long ctas = (tiles * ((p.N + kUpUnit - 1) / kUpUnit) + kUpWarps - 1) / kUpWarps, most = 2LL * sm_count;
+        const dim3 grid((unsigned)(ctas < most ? ctas : most)), block(kUpThreads);
+        const int base = !p.base.ptr ? 0 : p.base.f32 ? 2 : 1;
+        if (p.y32.ptr)
+            return base == 0 ? launch_dependent(adapters_up_kernel<0, 3>, grid, block, smem, stream, p)
+                   : base == 1 ? launch_dependent(adapters_up_kernel<1, 3>, grid, block, smem, stream, p)
+                               : launch_dependent(adapters_up_kernel<2, 3>, grid, block, smem, stream, p);
+        return base == 0 ? launch_dependent(adapters_up_kernel<0, 2>, grid, block, smem, stream, p)
+               : base == 1 ? launch_dependent(adapters_up_kernel<1, 2>, grid, block, smem, stream, p)
+                           : launch_dependent(adapters_up_kernel<2, 2>, grid, block, smem, stream, p);
     }
-    const long long items = tiles * p.parts * ((p.rank + 15) / 16), most = 2LL * sm_count / kLowCluster;
+    // Eight CTAs share K while all of them find places, two to an SM in whole clusters (128 SMs of which do),
+    // four beyond
+    // (of one part, so that sums do not depend on how many parts there are)
+    const long long groups = (p.rank + 15) / 16, items = tiles * p.parts * groups;
+    const int size = tiles * groups * kLowCluster <= 2 * 128 ? kLowCluster : kLowCluster / 2;
+    const long long most = 2LL * sm_count / size;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = kLowCluster;
+    attr[1].val.clusterDim.x = size;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((items < most ? items : most) * kLowCluster));
+    cfg.gridDim = dim3((unsigned)((items < most ? items : most) * size));
     cfg.blockDim = dim3(kLowThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -1225,7 +1292,7 @@ extern "C" dl_status dl_linear_adapters(const dl_adapters* adapters, const dl_ro
     const size_t need = adapters_bytes(tokens, p.num, p.rank, p.parts);
     if (ws_bytes < need) return host_fail(DL_ERR_WORKSPACE, "workspace has %zu bytes, %zu are needed", ws_bytes, need);
     char* scratch = static_cast<char*>(workspace) + DL_WORKSPACE_ZERO_BYTES;
-    p.low = reinterpret_cast<float*>(scratch);
+    p.low = reinterpret_cast<uint16_t*>(scratch);
     p.low_big = reinterpret_cast<float*>(scratch + low_bytes(tokens, p.rank, p.parts));
     p.tiles = reinterpret_cast<int*>(scratch + low_bytes(tokens, p.rank, p.parts) + low_big_bytes(tokens, p.rank, p.parts));
     p.big_from = p.rank <= kBigRank ? kBigFrom : 0x7fffffff;
