@@ -13,7 +13,7 @@ constexpr int kMaxParts = 8, kMaxRank = 256, kMaxAdapters = 16384;
 constexpr int kTile = 16;                // tokens of a small tile: all of one adapter
 constexpr int kFewTokens = 256;          // up to here every CTA makes the list of tiles for itself
 constexpr int kBigTile = 128;            // tokens of a big tile
-constexpr int kBigFrom = 64;             // tokens of an adapter from which on they go in big tiles
+constexpr int kBigFrom = 64;             // tokens in a row of one adapter from which on they go in big tiles
 constexpr int kBigRank = 128;            // the largest rank whose second factor fits beside the big tiles' first one
 constexpr int kMaxSplits = 8;            // CTAs that share K of a big tile
 
@@ -32,7 +32,8 @@ struct AdapterParams {
     bool in_place, in_place32;   // base is y, y32: rows without an adapter stay as they are
     bool wide;               // groups of eight columns of base, y and y32 are 16-byte aligned
     // big tiles
-    float* low_big;          // [tokens][parts * rank], by place in `order`, without scale
+    float* low_big;          // [tokens][parts * rank] first products without scale
+    int up_stages;           // of adapters_up_big_kernel's ring
     WaitCtl wait;
 };
 
@@ -43,7 +44,7 @@ struct Tile {
     int token[kTile];
     __device__ int at(int i) const { return i < count ? token[i] : -1; }
 };
-// Tokens order[first .. first + count) of one adapter.
+// Tokens first .. first + count - 1, all of one adapter.
 struct BigTile {
     int adapter, first, count, rank;
 };
@@ -51,22 +52,22 @@ struct BigTile {
 // The lists of more than kFewTokens tokens.
 struct Lists {
     int *counts;             // small tiles, big tiles
-    int* order;              // [tokens] the big tiles' tokens
+    int* start;              // [tokens + 1] where the adapter changes
     BigTile* big;
     Tile* small;
 };
-__host__ __device__ inline long long max_big(long long tokens, int num) {
-    return tokens / kBigTile + (tokens / kBigFrom < num + 1 ? tokens / kBigFrom : num + 1) + 1;
+__host__ __device__ inline long long max_big(long long tokens) {
+    return tokens / kBigTile + tokens / kBigFrom + 1;
 }
 __host__ __device__ inline long long max_small(long long tokens, int num) {
     return tokens / kTile + (tokens < num + 1 ? tokens : num + 1) + 1;
 }
-__host__ __device__ inline Lists lists_of(int* at, long long tokens, int num) {
+__host__ __device__ inline Lists lists_of(int* at, long long tokens) {
     Lists l;
     l.counts = at;
     l.big = reinterpret_cast<BigTile*>(at + 4);
-    l.order = reinterpret_cast<int*>(l.big + max_big(tokens, num));
-    l.small = reinterpret_cast<Tile*>(l.order + tokens);
+    l.start = reinterpret_cast<int*>(l.big + max_big(tokens));
+    l.small = reinterpret_cast<Tile*>(l.start + tokens + 1);
     return l;
 }
 
@@ -182,97 +183,117 @@ __device__ __forceinline__ int make_tiles(const AdapterParams& p, FewTiles& s) {
     return n;
 }
 
-// The lists of many tokens, by one CTA: a counting sort by adapter.  Which tokens of an adapter share a
-// tile, and their order in it, do not change any result.
+// An inclusive sum over 1024 threads of three counts; `total`: over all.
+__device__ __forceinline__ void scan3(int (&v)[3], int (*warp_sum)[32], int (&total)[3]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+            const int u = __shfl_up_sync(~0u, v[j], o);
+            if (lane >= o) v[j] += u;
+        }
+    __syncthreads();                     // the last scan's sums have been read
+    if (lane == 31)
+        for (int j = 0; j < 3; ++j) warp_sum[j][warp] = v[j];
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+        int w = warp_sum[j][lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(~0u, w, o);
+            if (lane >= o) w += u;
+        }
+        total[j] = __shfl_sync(~0u, w, 31);
+        const int before = __shfl_sync(~0u, w, max(warp - 1, 0));
+        if (warp > 0) v[j] += before;
+    }
+}
+
+// The lists of many tokens, by one CTA.  Tokens of one adapter in a row, enough of them, make big tiles; the
+// others are sorted by adapter (counted, then placed) into small ones.  Which tokens of an adapter share a
+// small tile, and their order in it, do not change any result.
 __global__ void __launch_bounds__(1024) sort_tokens_kernel(const __grid_constant__ AdapterParams p) {
-    extern __shared__ unsigned count[];  // of each adapter, then its next place; the last: without one
+    extern __shared__ int count[];       // of each adapter, then its next place; the last: without one
     __shared__ int warp_sum[3][32];
-    constexpr unsigned kBig = 1u << 31;  // a place in `order`, not in the small tiles
-    constexpr int kEach = 4;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const Lists l = lists_of(p.tiles, p.tokens, p.num);
+    const int tid = threadIdx.x, T = p.tokens;
+    const Lists l = lists_of(p.tiles, T);
     griddep_wait();
     griddep_launch_dependents();
     for (int i = tid; i <= p.num; i += 1024) count[i] = 0;
+    // where the adapter changes, four tokens in a row a thread
+    int runs = 0;
+    for (long long t0 = 4LL * tid; t0 - 4 * tid < T; t0 += 4096) {
+        int a[5];
+#pragma unroll
+        for (int k = 0; k < 5; ++k) {
+            const long long t = t0 + k - 1;
+            a[k] = t >= 0 && t < T ? adapter_of(p, (int)t) : -2;
+        }
+        int v[3] = {0, 0, 0}, total[3];
+        bool starts[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            starts[k] = t0 + k < T && a[k + 1] != a[k];
+            v[0] += starts[k];
+        }
+        const int mine = v[0];
+        scan3(v, warp_sum, total);
+        int at = runs + v[0] - mine;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (starts[k]) l.start[at++] = (int)(t0 + k);
+        runs += total[0];
+    }
+    if (tid == 0) l.start[runs] = T;
     __syncthreads();
-    for (long long t0 = 0; t0 < p.tokens; t0 += 1024 * kEach) {
-        int a[kEach];
-#pragma unroll
-        for (int k = 0; k < kEach; ++k) {
-            const long long t = t0 + 1024 * k + tid;
-            a[k] = t < p.tokens ? adapter_of(p, (int)t) : -2;
+    int big = 0;
+    for (int i0 = 0; i0 < runs; i0 += 1024) {
+        const int i = i0 + tid;
+        int v[3] = {0, 0, 0}, total[3], first = 0, n = 0, ad = -1;
+        if (i < runs) {
+            first = l.start[i];
+            n = l.start[i + 1] - first;
+            ad = adapter_of(p, first);
+            if (n >= p.big_from) v[0] = (n + kBigTile - 1) / kBigTile;
+            else atomicAdd(&count[ad < 0 ? p.num : ad], n);
         }
-#pragma unroll
-        for (int k = 0; k < kEach; ++k) {
-            const unsigned same = __match_any_sync(~0u, a[k]);
-            if (a[k] != -2 && lane == __ffs(same) - 1) atomicAdd(&count[a[k] < 0 ? p.num : a[k]], __popc(same));
-        }
+        const int mine = v[0];
+        scan3(v, warp_sum, total);
+        const int r = mine ? rank_of(p, ad) : 0;
+        for (int j = 0; j < mine; ++j)
+            l.big[big + v[0] - mine + j] = BigTile{ad, first + j * kBigTile, min(n - j * kBigTile, kBigTile), r};
+        big += total[0];
     }
     __syncthreads();
-    int total[3] = {0, 0, 0};            // small tiles, big tiles, tokens of big tiles
+    int small = 0;
     for (int i0 = 0; i0 <= p.num; i0 += 1024) {
-        const int i = i0 + tid, n = i <= p.num ? (int)count[i] : 0;
-        const bool big = n >= p.big_from;
-        const int mine[3] = {big ? 0 : (n + kTile - 1) / kTile, big ? (n + kBigTile - 1) / kBigTile : 0, big ? n : 0};
-        int inc[3] = {mine[0], mine[1], mine[2]};
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1)
-#pragma unroll
-            for (int j = 0; j < 3; ++j) {
-                const int v = __shfl_up_sync(~0u, inc[j], o);
-                if (lane >= o) inc[j] += v;
-            }
-        __syncthreads();
-        if (lane == 31)
-            for (int j = 0; j < 3; ++j) warp_sum[j][warp] = inc[j];
-        __syncthreads();
-        int first[3];
-#pragma unroll
-        for (int j = 0; j < 3; ++j) {
-            first[j] = total[j] + inc[j] - mine[j];
-            for (int w = 0; w < 32; ++w) {
-                if (w < warp) first[j] += warp_sum[j][w];
-                total[j] += warp_sum[j][w];
-            }
-        }
-        const int ad = i < p.num ? i : -1, r = n ? rank_of(p, ad) : 0;
-        for (int j = 0; j < mine[0]; ++j) {
-            Tile& tile = l.small[first[0] + j];
+        const int i = i0 + tid, n = i <= p.num ? count[i] : 0, mine = (n + kTile - 1) / kTile;
+        int v[3] = {mine, 0, 0}, total[3];
+        scan3(v, warp_sum, total);
+        const int first = small + v[0] - mine, ad = i < p.num ? i : -1, r = mine ? rank_of(p, ad) : 0;
+        const float scale = mine ? scale_of(p, ad) : 1.f;
+        for (int j = 0; j < mine; ++j) {
+            Tile& tile = l.small[first + j];
             tile.adapter = ad;
             tile.rank = r;
-            tile.scale = scale_of(p, ad);
+            tile.scale = scale;
             tile.count = min(n - j * kTile, kTile);
         }
-        for (int j = 0; j < mine[1]; ++j)
-            l.big[first[1] + j] = BigTile{ad, first[2] + j * kBigTile, min(n - j * kBigTile, kBigTile), r};
-        if (i <= p.num) count[i] = big ? kBig | (unsigned)first[2] : (unsigned)first[0] * kTile;
+        if (i <= p.num) count[i] = first * kTile;
+        small += total[0];
     }
     __syncthreads();
-    for (long long t0 = 0; t0 < p.tokens; t0 += 1024 * kEach) {
-        int a[kEach];
-#pragma unroll
-        for (int k = 0; k < kEach; ++k) {
-            const long long t = t0 + 1024 * k + tid;
-            a[k] = t < p.tokens ? adapter_of(p, (int)t) : -2;
-        }
-#pragma unroll
-        for (int k = 0; k < kEach; ++k) {
-            const unsigned same = __match_any_sync(~0u, a[k]);
-            const int leader = __ffs(same) - 1;
-            unsigned at = 0;
-            if (a[k] != -2 && lane == leader) at = atomicAdd(&count[a[k] < 0 ? p.num : a[k]], __popc(same));
-            at = __shfl_sync(~0u, at, leader) + __popc(same & ((1u << lane) - 1));
-            const int t = (int)(t0 + 1024 * k + tid);
-            if (a[k] == -2) continue;
-            if (at & kBig)
-                l.order[at & ~kBig] = t;
-            else
-                l.small[at / kTile].token[at % kTile] = t;
-        }
+    for (int i = tid; i < runs; i += 1024) {
+        const int first = l.start[i], n = l.start[i + 1] - first;
+        if (n >= p.big_from) continue;
+        const int ad = adapter_of(p, first), at = atomicAdd(&count[ad < 0 ? p.num : ad], n);
+        for (int k = 0; k < n; ++k) l.small[(at + k) / kTile].token[(at + k) % kTile] = first + k;
     }
     if (tid == 0) {
-        l.counts[0] = total[0];
-        l.counts[1] = total[1];
+        l.counts[0] = small;
+        l.counts[1] = big;
     }
 }
 
@@ -325,7 +346,7 @@ __global__ void __launch_bounds__(kLowThreads, 2) adapters_low_kernel(const __gr
         n_tiles = make_tiles(p, s);
         tiles = s.tile;
     } else {
-        const Lists l = lists_of(p.tiles, p.tokens, p.num);
+        const Lists l = lists_of(p.tiles, p.tokens);
         n_tiles = l.counts[0];
         tiles = l.small;
     }
@@ -500,7 +521,7 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapters_up_kernel(const __grid
         n_tiles = make_tiles(p, s);
         tiles = s.tile;
     } else {
-        const Lists l = lists_of(p.tiles, p.tokens, p.num);
+        const Lists l = lists_of(p.tiles, p.tokens);
         n_tiles = l.counts[0];
         tiles = l.small;
     }
@@ -624,14 +645,6 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapters_up_kernel(const __grid
 
 // ---------------------------------------------------------------- big tiles
 
-__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // One K step of 16 of two bf16 operands: kind::f16, fp32 accumulator, 128 rows, n columns.
@@ -644,12 +657,13 @@ __device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t a_desc, uint
                  ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
 
-// First product of big tiles: low_big[place][j] = sum_k A[j][k] x[token][k], a product of 128 tokens
-// and up to 256 rows of A on the tensor cores, the sums in tensor memory.  It is bound by the read of x;
-// all threads gather its rows (and A's) into 128-byte swizzled stages of 64 k, several ahead, and one
-// thread issues the products.  A cluster shares K: each CTA leaves its sums in its shared memory,
-// where the cluster's CTAs add them up, a share of the tokens each, always in the same order.
-constexpr int kBigThreads = 256;
+// First product of big tiles: low_big[token][j] = sum_k A[j][k] x[token][k], a product of 128 tokens
+// and up to 256 rows of A on the tensor cores, the sums in tensor memory.  It is bound by what an SM reads
+// from L2: a tile's x once, A once a tile.  One thread has x and A copied into 128-byte swizzled stages of 64 k,
+// another one issues the products.  A cluster shares K: each CTA leaves its sums in its shared memory, where
+// the cluster's CTAs add them up, a share of the tokens each, always in the same order.  Rows of A past the
+// rank, and of x past the tile, are read like the others: what they make are values that nobody takes.
+constexpr int kBigWarps = 8, kBigThreads = 32 * (kBigWarps + 2);
 constexpr int kBigCols = 256;            // rows of A of one CTA, at most
 
 struct BigSmem {
@@ -659,29 +673,31 @@ __host__ __device__ inline BigSmem big_smem(int columns) {
     BigSmem s;
     s.cols = (columns < kBigCols ? columns + 15 : kBigCols) / 16 * 16;
     s.stage = (kBigTile + s.cols) * 128;
-    s.stages = (224 * 1024) / s.stage;       // 4 to 12; four hold the sums, 128 x (cols + 4) x 4 bytes, too
-    if (s.stages > 6) s.stages = 6;
+    s.stages = (224 * 1024) / s.stage;       // 4 to 8; four hold the sums, 128 x (cols + 4) x 4 bytes, too
+    if (s.stages > 8) s.stages = 8;
     s.total = 1024 + s.stages * s.stage + 256;
     return s;
 }
 
-__global__ void __launch_bounds__(kBigThreads) adapters_low_big_kernel(const __grid_constant__ AdapterParams p) {
+__global__ void __launch_bounds__(kBigThreads) adapters_low_big_kernel(const __grid_constant__ CUtensorMap map_x,
+                                                                       const __grid_constant__ CUtensorMap map_a,
+                                                                       const __grid_constant__ AdapterParams p) {
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
     extern __shared__ __align__(16) unsigned char raw[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int splits = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-    const Lists l = lists_of(p.tiles, p.tokens, p.num);
+    const Lists l = lists_of(p.tiles, p.tokens);
     const int SR = p.parts * p.rank, K = p.K;
     const BigSmem shape = big_smem(SR);
-    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u, bars = base + shape.stages * shape.stage;
-    const uint32_t slot = bars + 8 * shape.stages;
     const int stages = shape.stages;
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u, bars = base + stages * shape.stage;
+    const uint32_t full = bars, empty = bars + 8 * stages, done = bars + 16 * stages, slot = done + 8;
     // The lists are complete and the buffers free: the kernel before this one let it start only after
     // it had waited for sort_tokens_kernel.  (Its own results are other ones; the wait is at the end.)
     const int n_tiles = l.counts[1];
-    griddep_launch_dependents();
     if ((int)blockIdx.y >= n_tiles) {
+        griddep_launch_dependents();
         griddep_wait();
         return;
     }
@@ -689,12 +705,17 @@ __global__ void __launch_bounds__(kBigThreads) adapters_low_big_kernel(const __g
     while ((int)tmem_cols < shape.cols) tmem_cols *= 2;
     if (warp == 0) tmem_alloc(slot, tmem_cols);
     if (tid == 0) {
-        for (int i = 0; i < stages; ++i) mbar_init(bars + 8 * i, 1);
+        for (int i = 0; i < stages; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, 1);
+        }
+        mbar_init(done, 1);
         fence_mbarrier_init();
     }
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
+    griddep_launch_dependents();
     uint32_t tmem;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(slot));
     // this CTA's columns and part of K
@@ -703,133 +724,98 @@ __global__ void __launch_bounds__(kBigThreads) adapters_low_big_kernel(const __g
     const int s0 = (int)((long long)steps_all * rank / splits), s1 = (int)((long long)steps_all * (rank + 1) / splits);
     const int n = s1 - s0;
     const uint32_t idesc = umma_idesc_bf16(shape.cols);
-    const int chunk = tid & 7, row0 = tid >> 3;
-    const uint32_t put = (uint32_t)(row0 * 128 + ((chunk ^ (row0 & 7)) << 4));      // rows 32 apart keep row & 7
     float* sums = reinterpret_cast<float*>(raw + (base - smem_u32(raw)));
     const int pitch = shape.cols + 4;
-    // the stage that the next step's products read, how often it has been read, and its place
-    int stage = 0, parity = 0;
+    int stage = 0, turn = 0;             // of the next step: its stage, and how often all stages have been used before
+    int tiles_done = 0;
     bool dead = false;                   // a wait gave up: the CTA goes on with the cluster, without its copies and products
     for (int ti = blockIdx.y; ti < n_tiles; ti += gridDim.y) {
         const BigTile tile = l.big[ti];
         if (tile.adapter < 0) continue;
-        const int r = tile.rank;
-        // What this thread copies: a 16-byte chunk of four rows of x and of every 32nd row of A.  Rows that are not
-        // there are zeros in every stage, written once: no copy touches them.
-        const char* xr[kBigTile / 32];
-#pragma unroll
-        for (int i = 0; i < kBigTile / 32; ++i) {
-            const int row = row0 + 32 * i;
-            xr[i] = row < tile.count ? row_ptr(p.x, l.order[tile.first + row]) + 16 * chunk + s0 * 128 : nullptr;
-        }
-        const char* ar = reinterpret_cast<const char*>(p.a + ((size_t)tile.adapter * SR + j0 + row0) * K) + 16 * chunk + s0 * 128;
-        const size_t a32 = (size_t)K * 64;
-        unsigned mine = 0;
-        for (int i = 0; 32 * i + row0 < cols; ++i) mine |= ((j0 + 32 * i + row0) % p.rank < r ? 1u : 0u) << i;
-        for (int i = 0; i < stages; ++i) {
-            const uint32_t to = base + i * shape.stage + put;
-#pragma unroll
-            for (int j = 0; j < kBigTile / 32; ++j)
-                if (!xr[j]) sts128(to + j * 4096, 0, 0, 0, 0);
-            for (int j = 0; 32 * j + row0 < shape.cols; ++j)
-                if (!(mine >> j & 1)) sts128(to + kBigTile * 128 + j * 4096, 0, 0, 0, 0);
-        }
-        // step s of this tile into the stage at `to`
-        auto load = [&](int s, uint32_t to) {
-            const int off = s * 128;
-            const char* from = ar + off;
-            to += put;
-            if ((s0 + s + 1) * 64 <= K) {
-#pragma unroll
-                for (int i = 0; i < kBigTile / 32; ++i)
-                    if (xr[i]) copy16_async(to + i * 4096, xr[i] + off, 16);
-                to += kBigTile * 128;
-#pragma unroll
-                for (int i = 0; i < kBigCols / 32; ++i) {
-                    if (mine >> i & 1) copy16_async(to + i * 4096, from, 16);
-                    from += a32;
-                }
-            } else {                     // the last step of K ends early
-                const int bytes = (s0 + s) * 64 + 8 * chunk < K ? 16 : 0;
-#pragma unroll
-                for (int i = 0; i < kBigTile / 32; ++i)
-                    if (xr[i]) copy16_async(to + i * 4096, bytes ? xr[i] + off : p.x.ptr, bytes);
-                to += kBigTile * 128;
-                for (int i = 0; i < kBigCols / 32; ++i)
-                    if (mine >> i & 1) copy16_async(to + i * 4096, bytes ? from + i * a32 : p.x.ptr, bytes);
-            }
-        };
         bool bad = dead;
-        int fill = stage;                // the stage that the next copies go to
-        for (int s = 0; s < stages - 1; ++s) {
-            if (s < n && !dead) load(s, base + (uint32_t)fill * shape.stage);
-            if (++fill == stages) fill = 0;
-            copies_commit();
-        }
-        int before = 0, parity_before = 0;       // of step s - 1
-        for (int s = 0; s < n; ++s) {
-            if (stages == 4) copies_wait<2>();
-            else if (stages == 5) copies_wait<3>();
-            else copies_wait<4>();
-            fence_async_smem();
-            if (__syncthreads_or(bad)) break;
-            if (tid == 0) {
+        if (dead) {
+        } else if (warp == kBigWarps) {
+            if (lane == 0) {
+                for (int s = 0; s < n && !bad; ++s) {
+                    if (turn > 0) bad = !mbar_wait_bounded(empty + 8 * stage, (turn - 1) & 1, p.wait, kErrProducerWait);
+                    if (bad) break;
+                    const uint32_t to = base + (uint32_t)stage * shape.stage, bar = full + 8 * stage;
+                    mbar_arrive_expect_tx(bar, shape.stage);
+                    tma_load_2d(to, &map_x, bar, (s0 + s) * 64, tile.first, policy_evict_first());
+                    tma_load_2d(to + kBigTile * 128, &map_a, bar, (s0 + s) * 64, tile.adapter * SR + j0, policy_evict_last());
+                    if (++stage == stages) stage = 0, ++turn;
+                }
+            }
+            __syncwarp();
+        } else if (warp == kBigWarps + 1 && lane == 0) {
+            for (int s = 0; s < n && !bad; ++s) {
+                bad = !mbar_wait_bounded(full + 8 * stage, turn & 1, p.wait, kErrConsumerWait);
+                if (bad) break;
                 tc_fence_after_sync();
                 const uint32_t at = base + (uint32_t)stage * shape.stage;
                 const uint64_t xa = umma_desc_sw128(at), wa = umma_desc_sw128(at + kBigTile * 128);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) umma_bf16(tmem, xa + 2 * k, wa + 2 * k, idesc, s > 0 || k > 0);
-                umma_commit(bars + 8 * stage);
+                umma_commit(empty + 8 * stage);
+                if (++stage == stages) stage = 0, ++turn;
             }
-            const int next = s + stages - 1;
-            if (next < n) {
-                // the stage of step s - 1 is free once its products have read it
-                if (s > 0) bad = !mbar_wait_bounded(bars + 8 * before, parity_before, p.wait, kErrConsumerWait);
-                if (!bad) load(next, base + (uint32_t)fill * shape.stage);
-                if (++fill == stages) fill = 0;
-            }
-            copies_commit();
-            before = stage;
-            parity_before = parity;
-            if (++stage == stages) stage = 0, parity ^= 1;
+            if (!bad) umma_commit(done);
         }
-        if (!bad) bad = !mbar_wait_bounded(bars + 8 * before, parity_before, p.wait, kErrConsumerWait);
-        copies_wait<0>();
-        dead = __syncthreads_or(bad);
+        // (one thread waits for the products; the others sleep at the barrier)
+        if (warp == kBigWarps + 1 && lane == 0 && !bad) bad = !mbar_wait_bounded(done, tiles_done & 1, p.wait, kErrConsumerWait);
+        ++tiles_done;
+        tc_fence_before_sync();
+        if (__syncthreads_or(bad)) {
+            // Nothing more is copied or multiplied; what is on its way arrives before the CTA leaves.
+            if (!dead && warp == kBigWarps && lane == 0)
+                for (int i = 0; i < stages; ++i) mbar_wait_bounded(full + 8 * i, (turn - (i >= stage ? 1 : 0)) & 1, p.wait, kErrDrainWait);
+            dead = true;
+            __syncthreads();
+        }
         tc_fence_after_sync();
         // a thread has a token's row; two warps share 32 tokens' columns
-        const int row = 32 * (warp & 3) + lane;
         const bool alone = splits == 1;
         float* out = p.low_big + (size_t)tile.first * SR + j0;
-        float* to = alone ? out + (size_t)row * SR : sums + row * pitch;
-        for (int j = 16 * (warp >> 2); j < shape.cols; j += 32) {
-            float v[16];
-            tmem_ld16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + j, v);
-            tmem_wait_ld();
-            if (row < tile.count) {
+        if (warp < kBigWarps) {
+            const int row = 32 * (warp & 3) + lane;
+            float* to = alone ? out + (size_t)row * SR : sums + row * pitch;
+            for (int j = 16 * (warp >> 2); j < shape.cols; j += 32) {
+                float v[16];
+                tmem_ld16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + j, v);
+                tmem_wait_ld();
+                if (row < tile.count) {
 #pragma unroll
-                for (int k = 0; k < 16; k += 4)
-                    if (j + k < cols) *reinterpret_cast<float4*>(to + j + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                    for (int k = 0; k < 16; k += 4)
+                        if (j + k < cols) *reinterpret_cast<float4*>(to + j + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                }
             }
         }
         tc_fence_before_sync();
         if (!alone) {
             cluster.sync();
-            // this CTA's share of the tokens
-            const int first = tile.count * rank / splits, last = tile.count * (rank + 1) / splits;
-            for (int i = tid; i < (last - first) * (cols / 4); i += kBigThreads) {
-                const int t = first + i / (cols / 4), j = i % (cols / 4) * 4;
-                float4 v = {0.f, 0.f, 0.f, 0.f};
-                float4 w[kMaxSplits];
+            // this CTA's share of the tokens, four columns a thread, two of them at a time
+            const int first = tile.count * rank / splits, quads = cols / 4;
+            const int all = (tile.count * (rank + 1) / splits - first) * quads;
+            for (int i0 = tid; i0 < all; i0 += 2 * kBigThreads) {
+                float4 w[2][kMaxSplits];
 #pragma unroll
-                for (int q = 0; q < kMaxSplits; ++q)
-                    if (q < splits) w[q] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(sums, q) + t * pitch + j);
+                for (int h = 0; h < 2; ++h) {
+                    const int i = min(i0 + h * kBigThreads, all - 1), t = first + i / quads, j = i % quads * 4;
 #pragma unroll
-                for (int q = 0; q < kMaxSplits; ++q) {
-                    if (q >= splits) break;
-                    v.x += w[q].x; v.y += w[q].y; v.z += w[q].z; v.w += w[q].w;
+                    for (int q = 0; q < kMaxSplits; ++q)
+                        if (q < splits) w[h][q] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(sums, q) + t * pitch + j);
                 }
-                *reinterpret_cast<float4*>(out + (size_t)t * SR + j) = v;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int i = i0 + h * kBigThreads, t = first + i / quads, j = i % quads * 4;
+                    float4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int q = 0; q < kMaxSplits; ++q) {
+                        if (q >= splits) break;
+                        v.x += w[h][q].x; v.y += w[h][q].y; v.z += w[h][q].z; v.w += w[h][q].w;
+                    }
+                    if (i < all) *reinterpret_cast<float4*>(out + (size_t)t * SR + j) = v;
+                }
             }
             cluster.sync();              // the others have read this CTA's sums: its stages are free
         } else {
@@ -846,17 +832,28 @@ __global__ void __launch_bounds__(kBigThreads) adapters_low_big_kernel(const __g
 
 // Second product of big tiles, out[t][n] = base[t][n] + sum_r low[t][r] B[n][r] for 128 tokens and blocks of 64
 // columns: bound by base and out.  A block is one product on the tensor cores, 128 x 64 over r and the parts of
-// the first products, which lie in shared memory as bf16 operands; B's rows come a few blocks ahead into a
-// ring, base a block ahead into registers, and while a block is multiplied the one before leaves tensor
-// memory.  The rows of B are put into the order that gives a lane eight consecutive columns (as above).
-// All tiles' blocks are dealt to the CTAs in equal runs.
-constexpr int kUpBlock = 64, kUpRing = 3, kUpCtas = 2, kUpTmem = 2 * kUpBlock;
+// the first products, which lie in shared memory as bf16 operands.  One thread has B's rows and base copied
+// into a ring of stages and, from there again, the finished blocks to y; another one issues the products, two
+// accumulators in turn; eight warps add base, half a row of 64 a thread.  All tiles' blocks are dealt to the
+// CTAs in equal runs.  Blocks that a whole copy does not fit (the tile's or the part's end, rows that do not
+// allow it) read base and write y by themselves.
+constexpr int kUpBlock = 64, kUpCtas = 2, kUpTmem = 2 * kUpBlock, kUpBigThreads = kUpThreads + 64;
 static_assert(kUpCtas * kUpTmem <= 512, "tensor memory of an SM");
 
-// A: parts of 128 rows, B: ring stages of 64, each in pieces of 64 r with rows of 128 bytes, swizzled.
-__host__ __device__ inline int up_big_smem(int rank, int parts) {
+// Shared memory: the first products' parts (128 rows each), then stages: B (64 rows), y (and, of bf16, base
+// before it), base of fp32 (and y_f32 after it) or y_f32.  Rows of 128 bytes, swizzled; B and the parts in pieces of
+// 64 r, fp32 in halves of 32 columns.
+struct UpSmem {
+    int a, stage, wide_at, total;        // bytes of the parts, of a stage; of it before the fp32 halves; of all
+};
+__host__ __device__ inline UpSmem up_smem(int rank, int parts, bool f32, int stages) {
     const int pieces = (rank + 63) / 64;
-    return 1024 + (parts * kBigTile + kUpRing * kUpBlock) * 128 * pieces + 64;
+    UpSmem s;
+    s.a = parts * kBigTile * 128 * pieces;
+    s.wide_at = kUpBlock * 128 * pieces + kBigTile * 128;
+    s.stage = s.wide_at + (f32 ? 2 * kBigTile * 128 : 0);
+    s.total = 1024 + s.a + stages * s.stage + 256;
+    return s;
 }
 
 // Blocks of columns, each in one part.
@@ -864,11 +861,15 @@ __device__ __forceinline__ int part_blocks(const AdapterParams& p, int part) {
     return (p.part_end[part] - (part ? p.part_end[part - 1] : 0) + kUpBlock - 1) / kUpBlock;
 }
 
-// 64 columns of 16 rows of tensor memory, as the products of mma.m16n8 lie: v[i] has columns 8 i + 2 c and + 1 of
-// rows g and g + 8.
-__device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, float (&v)[8][4]) {
-    uint32_t* r = reinterpret_cast<uint32_t*>(&v[0][0]);
-    asm volatile("tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, uint32_t src, int c0, int c1) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];"
+                 ::"l"(reinterpret_cast<uint64_t>(m)), "r"(src), "r"(c0), "r"(c1) : "memory");
+}
+
+// 32 consecutive columns of this thread's row of tensor memory.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
                  "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
                  "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
@@ -878,15 +879,23 @@ __device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, float (&v)[8][4]) 
                  : "r"(taddr));
 }
 
-// BASE 0: none, or rows that do not allow wide accesses, 1: bf16, 2: fp32; P: parts of a first product
+struct UpMaps {
+    CUtensorMap b, base, y, y32;
+};
+
+// BASE 0: none, 1: bf16, 2: fp32; P: parts of a first product (3: there is an fp32 result)
 template <int BASE, int P>
-__global__ void __launch_bounds__(kUpThreads, kUpCtas) adapters_up_big_kernel(const __grid_constant__ AdapterParams p) {
+__global__ void __launch_bounds__(kUpBigThreads, kUpCtas) adapters_up_big_kernel(const __grid_constant__ UpMaps maps,
+                                                                                  const __grid_constant__ AdapterParams p) {
     extern __shared__ __align__(16) unsigned char raw[];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
-    const Lists l = lists_of(p.tiles, p.tokens, p.num);
-    const int R = p.rank, N = p.N, pieces = (R + 63) / 64;
-    const uint32_t a_at = (smem_u32(raw) + 1023u) & ~1023u, ring = a_at + P * kBigTile * 128 * pieces;
-    const uint32_t stage_bytes = kUpBlock * 128 * pieces, bars = ring + kUpRing * stage_bytes, slot = bars + 16;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const Lists l = lists_of(p.tiles, p.tokens);
+    const int R = p.rank, N = p.N, pieces = (R + 63) / 64, S = p.up_stages;
+    const UpSmem shape = up_smem(R, P, BASE == 2 || P == 3, S);
+    const uint32_t a_at = (smem_u32(raw) + 1023u) & ~1023u, ring = a_at + shape.a, bars = ring + S * shape.stage;
+    // stages filled (4 at most) and finished, sums made (two accumulators) and read, the first products of a run in place
+    const uint32_t full = bars, written = bars + 32, made = bars + 64, taken = bars + 80, ready = bars + 96, slot = bars + 104;
+    const int y_at = kUpBlock * 128 * pieces;
     // the first products are there: the kernel before this one let it start after it had waited for them
     const int n_tiles = l.counts[1];
     int blocks = 0;
@@ -901,8 +910,15 @@ __global__ void __launch_bounds__(kUpThreads, kUpCtas) adapters_up_big_kernel(co
     }
     if (warp == 0) tmem_alloc(slot, kUpTmem);
     if (tid == 0) {
-        mbar_init(bars, 1);
-        mbar_init(bars + 8, 1);
+        for (int i = 0; i < S; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(written + 8 * i, kUpWarps);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(made + 8 * i, 1);
+            mbar_init(taken + 8 * i, kUpWarps);
+        }
+        mbar_init(ready, kUpWarps);
         fence_mbarrier_init();
     }
     tc_fence_before_sync();
@@ -912,11 +928,14 @@ __global__ void __launch_bounds__(kUpThreads, kUpCtas) adapters_up_big_kernel(co
     griddep_launch_dependents();
     uint32_t tmem;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(slot));
-    const uint32_t idesc = umma_idesc_bf16(kUpBlock);
-    const int row0 = 32 * (warp & 3) + 16 * (warp >> 2);        // this warp's rows of the tile
     const size_t step = (size_t)p.parts * R;
-    unsigned made = 0;                   // products so far: the next one's accumulator and phase
+    // Blocks so far give a stage and its phase, products an accumulator and its, runs with products `ready`'s.
+    int stage = 0, turn = 0;             // of the next block
+    unsigned products = 0, runs_made = 0;
     bool bad = false;
+    auto advance = [&]() {
+        if (++stage == S) stage = 0, ++turn;
+    };
     while (at < end && !bad) {
         // a run of blocks of one tile and part: columns n0 on, the part ends at n_end
         const BigTile tile = l.big[at / blocks];
@@ -928,39 +947,114 @@ __global__ void __launch_bounds__(kUpThreads, kUpCtas) adapters_up_big_kernel(co
         const int runs = (int)min((long long)(part_blocks(p, part) - b0), end - at);
         n0 += b0 * kUpBlock;
         at += runs;
-        const int ad = tile.adapter, r = tile.rank, steps = (r + 15) / 16;
-        const float scale = ad >= 0 && p.scale ? p.scale[ad] : 1.f;
-        const bool active = row0 < tile.count;
-        const int i0 = row0 + g, i1 = i0 + 8;
-        const int t0 = i0 < tile.count ? l.order[tile.first + i0] : -1, t1 = i1 < tile.count ? l.order[tile.first + i1] : -1;
-        const uint16_t* b = p.b + (size_t)max(ad, 0) * N * R;
+        const int ad = tile.adapter, r = tile.rank, steps = (r + 15) / 16, used = (steps + 3) / 4;
         const bool put = ad >= 0 || !p.in_place, put32 = P == 3 && (ad >= 0 || !p.in_place32);
-        const char *from0 = row_ptr(p.base, max(t0, 0)) + (size_t)(n0 + 8 * c) * (BASE == 2 ? 4 : 2);
-        const char *from1 = row_ptr(p.base, max(t1, 0)) + (size_t)(n0 + 8 * c) * (BASE == 2 ? 4 : 2);
-        char *to0 = row_ptr(p.y, max(t0, 0)) + (size_t)(n0 + 8 * c) * 2, *to1 = row_ptr(p.y, max(t1, 0)) + (size_t)(n0 + 8 * c) * 2;
-        // B's rows of a block, four threads a row, into its ring stage; what lies past the rank or the part
-        // arrives as zeros
-        const int b_row = tid >> 2, b_col = (b_row >> 5) * 32 + ((b_row & 7) >> 1) * 8 + (b_row >> 3 & 3) * 2 + (b_row & 1);
-        const uint16_t* b_from = b + (size_t)(n0 + b_col) * R + 8 * (tid & 3);
-        const size_t b_step = (size_t)kUpBlock * R;
-        const uint32_t b_to = ring + b_row * 128;
-        int b_left = n_end - n0 - b_col, b_stage = 0;    // the part's columns from this thread's of the next block on
-        auto load = [&]() {              // the next block
-            if (r > 0 && b_left > -kUpBlock) {
-                const uint32_t to = b_to + (uint32_t)b_stage * stage_bytes;
-#pragma unroll 2
-                for (int i = tid & 3, j = 0; i < 2 * steps; i += 4, j += 32) {
-                    const int bytes = b_left > 0 ? min(2 * (r - 8 * i), 16) : 0;
-                    copy16_async(to + (i >> 3) * (kUpBlock * 128) + 16 * ((i & 7) ^ (b_row & 7)), bytes > 0 ? b_from + j : p.b, max(bytes, 0));
+        if (!put && !put32) continue;
+        auto whole = [&](int i) { return tile.count == kBigTile && p.wide && n0 + (i + 1) * kUpBlock <= n_end; };
+        if (warp == kUpWarps) {          // copies
+            if (lane == 0) {
+                const int first = stage, first_turn = turn;
+                auto load = [&](int i) {
+                    const uint32_t to = ring + stage * shape.stage, bar = full + 8 * stage;
+                    const int n = n0 + i * kUpBlock;
+                    const bool with = BASE != 0 && whole(i);
+                    mbar_arrive_expect_tx(bar, used * (kUpBlock * 128) + (with ? (BASE == 2 ? 2 : 1) * kBigTile * 128 : 0));
+                    for (int k = 0; k < used; ++k)
+                        tma_load_2d(to + k * (kUpBlock * 128), &maps.b, bar, 64 * k, ad * N + n, policy_evict_last());
+                    if (with) {
+                        if (BASE == 2) {
+                            tma_load_2d(to + shape.wide_at, &maps.base, bar, n, tile.first, policy_evict_first());
+                            tma_load_2d(to + shape.wide_at + kBigTile * 128, &maps.base, bar, n + 32, tile.first, policy_evict_first());
+                        } else {
+                            tma_load_2d(to + y_at, &maps.base, bar, n, tile.first, policy_evict_first());
+                        }
+                    }
+                    advance();
+                };
+                int loaded = 0;
+                while (loaded < min(S, runs)) load(loaded++);
+                int st = first, tn = first_turn;
+                for (int i = 0; i < runs; ++i) {
+                    bad = !mbar_wait_bounded(written + 8 * st, tn & 1, p.wait, kErrProducerWait);
+                    if (bad) break;
+                    if (whole(i)) {
+                        const uint32_t from = ring + st * shape.stage;
+                        const int n = n0 + i * kUpBlock;
+                        if (put) tma_store_2d(&maps.y, from + y_at, n, tile.first);
+                        if (put32) {
+                            tma_store_2d(&maps.y32, from + shape.wide_at, n, tile.first);
+                            tma_store_2d(&maps.y32, from + shape.wide_at + kBigTile * 128, n + 32, tile.first);
+                        }
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    }
+                    if (loaded < runs) {
+                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                        load(loaded++);
+                    }
+                    if (++st == S) st = 0, ++tn;
                 }
+                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                if (bad)                 // what is on its way arrives before the CTA leaves
+                    for (int i = 0; i < min(S, loaded); ++i) {
+                        if (--stage < 0) stage = S - 1, --turn;
+                        mbar_wait_bounded(full + 8 * stage, turn & 1, p.wait, kErrDrainWait);
+                    }
             }
-            if (++b_stage == kUpRing) b_stage = 0;
-            b_left -= kUpBlock;
-            b_from += b_step;
-            copies_commit();
-        };
-        // The tile's first products of a part, two threads a row
-        auto take = [&]() {
+            bad = __any_sync(~0u, bad);
+            continue;
+        }
+        if (warp == kUpWarps + 1) {      // products
+            if (r > 0) {
+                const uint32_t idesc = umma_idesc_bf16(kUpBlock);
+                const uint64_t a_desc = umma_desc_sw128(a_at), ring_desc = umma_desc_sw128(ring);
+                bad = !mbar_wait_bounded(ready, runs_made & 1, p.wait, kErrConsumerWait);
+                ++runs_made;
+                for (int i = 0; i < runs; ++i) {
+                    const unsigned acc = products & 1, before = products >> 1;
+                    if (!bad && before > 0) bad = !mbar_wait_bounded(taken + 8 * acc, (before - 1) & 1, p.wait, kErrConsumerWait);
+                    if (!bad) bad = !mbar_wait_bounded(full + 8 * stage, turn & 1, p.wait, kErrConsumerWait);
+                    if (__any_sync(~0u, bad)) break;
+                    const uint32_t b_at = ring + stage * shape.stage;
+                    if (r & 15) {        // what lies past the rank in the last 16 r, NaN perhaps, becomes zeros
+#pragma unroll 1
+                        for (int k = r >> 3; k < 2 * steps; ++k)
+                            for (int row = lane; row < kUpBlock; row += 32) {
+                                const uint32_t at16 = b_at + (k >> 3) * (kUpBlock * 128) + row * 128 + 16 * ((k & 7) ^ (row & 7));
+                                const uint4 v = lds128(at16);
+                                uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    w[j] &= (8 * k + 2 * j < r ? 0xffffu : 0u) | (8 * k + 2 * j + 1 < r ? 0xffff0000u : 0u);
+                                sts128(at16, w[0], w[1], w[2], w[3]);
+                            }
+                        fence_async_smem();
+                        __syncwarp();
+                    }
+                    tc_fence_after_sync();
+                    if (lane == 0) {
+                        const uint64_t bt = ring_desc + (uint64_t)(stage * shape.stage >> 4);
+                        for (int j = 0; j < P; ++j)
+                            for (int q = 0; q < steps; ++q)
+                                umma_bf16(tmem + acc * kUpBlock,
+                                          a_desc + (uint64_t)((j * pieces + (q >> 2)) * (kBigTile * 128 >> 4) + 2 * (q & 3)),
+                                          bt + (uint64_t)((q >> 2) * (kUpBlock * 128 >> 4) + 2 * (q & 3)), idesc, j + q > 0);
+                        umma_commit(made + 8 * acc);
+                    }
+                    __syncwarp();
+                    ++products;
+                    advance();
+                }
+                bad = __any_sync(~0u, bad);
+            } else {
+                for (int i = 0; i < runs; ++i) advance();
+            }
+            continue;
+        }
+        // Eight warps: a thread has a token's row and 32 of a block's 64 columns.
+        const float scale = scale_of(p, ad);
+        if (r > 0) {
+            // The run's first products, two threads a row.  (All products of the run before are done: this
+            // thread has waited for the last.)
             const int row = tid >> 1;
             const float* low = p.low_big + (size_t)(tile.first + min(row, tile.count - 1)) * step + part * R;
             for (int i = tid & 1; i < 2 * steps; i += 2) {
@@ -984,127 +1078,102 @@ __global__ void __launch_bounds__(kUpThreads, kUpCtas) adapters_up_big_kernel(co
                     sts128(a_at + (j * pieces + (i >> 3)) * (kBigTile * 128) + row * 128 + 16 * ((i & 7) ^ (row & 7)), out[j][0],
                            out[j][1], out[j][2], out[j][3]);
             }
-        };
-        uint4 base[2][2][BASE == 2 ? 2 : 1];     // [row][32 columns]: eight columns of this lane
-        auto fetch = [&](int i) {        // of block i
-            if (BASE == 0 || !active || i >= runs || n0 + (i + 1) * kUpBlock > n_end) return;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if ((h ? t1 : t0) < 0) continue;
-                const char* from = (h ? from1 : from0) + (size_t)i * (kUpBlock * (BASE == 2 ? 4 : 2));
-#pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    base[h][v][0] = ldg128(from + v * (BASE == 2 ? 128 : 64));
-                    if (BASE == 2) base[h][v][BASE == 2] = ldg128(from + v * 128 + 16);
-                }
-            }
-        };
-        // The results of block i, whose product (if there is one) has accumulator `acc`
-        auto finish = [&](int i, unsigned acc) {
-            if (!active) return;
-            float d[8][4] = {};
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ready);
+        }
+        const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
+        const bool mine = row < tile.count;
+        const int t = tile.first + (mine ? row : 0);
+        for (int i = 0; i < runs; ++i) {
+            bad = !mbar_wait_bounded(full + 8 * stage, turn & 1, p.wait, kErrConsumerWait);
+            float d[32];
             if (r > 0) {
-                tmem_ld_16x64(tmem + ((uint32_t)row0 << 16) + acc * kUpBlock, d);
+                const unsigned acc = products & 1;
+                if (!bad) bad = !mbar_wait_bounded(made + 8 * acc, (products >> 1) & 1, p.wait, kErrConsumerWait);
+                bad = __any_sync(~0u, bad);
+                if (bad) break;
+                ++products;
+                tc_fence_after_sync();
+                tmem_ld32(tmem + ((uint32_t)(32 * quarter) << 16) + acc * kUpBlock + 32 * half, d);
                 tmem_wait_ld();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(taken + 8 * acc);
+            } else {
+                bad = __any_sync(~0u, bad);
+                if (bad) break;
+#pragma unroll
+                for (int k = 0; k < 32; ++k) d[k] = 0.f;
             }
             float odd = 0.f;             // NaN if any sum is, or infinite
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
+            for (int k = 0; k < 32; ++k) odd = fmaf(d[k], 0.f, odd);
+            const int n = n0 + i * kUpBlock + 32 * half;
+            if (odd != odd && mine) {
+                const float* low = p.low_big + (size_t)t * step;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) odd = fmaf(d[k][j], 0.f, odd);
-            const bool wide = n0 + (i + 1) * kUpBlock <= n_end && p.wide;
-            if (wide && odd == odd) {
+                for (int k = 0; k < 4; ++k) {
+                    float x[8];
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                    for (int j = 0; j < 8; ++j) x[j] = d[8 * k + j];
+                    plain_up<0>(p, low, scale, p.b + (size_t)max(ad, 0) * N * R, n + 8 * k, r, x);
 #pragma unroll
-                    for (int v = 0; v < 2; ++v) {
-                        if (BASE == 1) {
-                            const uint4 x = base[h][v][0];
-                            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                    for (int j = 0; j < 8; ++j) d[8 * k + j] = x[j];
+                }
+            }
+            if (whole(i)) {
+                const uint32_t to = ring + stage * shape.stage, y_row = to + y_at + row * 128, swap = row & 7;
+                const uint32_t f_row = to + shape.wide_at + half * (kBigTile * 128) + row * 128;
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                float lo, hi;
-                                bf16x2_to_f32(w[j], lo, hi);
-                                d[4 * v + j][2 * h] += lo;
-                                d[4 * v + j][2 * h + 1] += hi;
-                            }
-                        } else if (BASE == 2) {
-                            const uint4 x = base[h][v][0], y = base[h][v][BASE == 2];
-                            const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t y16 = y_row + 16 * ((4 * half + k) ^ swap);
+                    const uint32_t f0 = f_row + 16 * ((2 * k) ^ swap), f1 = f_row + 16 * ((2 * k + 1) ^ swap);
+                    float* v = d + 8 * k;
+                    if (BASE == 1) {
+                        const uint4 x = lds128(y16);
+                        float from[8];
+                        bf16x2_to_f32(x.x, from[0], from[1]);
+                        bf16x2_to_f32(x.y, from[2], from[3]);
+                        bf16x2_to_f32(x.z, from[4], from[5]);
+                        bf16x2_to_f32(x.w, from[6], from[7]);
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) d[4 * v + (j >> 1)][2 * h + (j & 1)] += __uint_as_float(w[j]);
-                        }
+                        for (int j = 0; j < 8; ++j) v[j] += from[j];
+                    } else if (BASE == 2) {
+                        const uint4 x = lds128(f0), y = lds128(f1);
+                        const uint32_t q[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[j] += __uint_as_float(q[j]);
                     }
-                fetch(i + 1);            // base is in the sums: the next block's may come
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if ((h ? t1 : t0) < 0) continue;
-                    char* to = (h ? to1 : to0) + (size_t)i * (kUpBlock * 2);
-                    char* to32 = P == 3 ? row_ptr(p.y32, h ? t1 : t0) + (size_t)(n0 + i * kUpBlock + 8 * c) * 4 : nullptr;
-#pragma unroll
-                    for (int v = 0; v < 2; ++v) {
-                        float x[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) x[j] = d[4 * v + (j >> 1)][2 * h + (j & 1)];
-                        if (put) row_store8(to, false, 32 * v, x);
-                        if (put32) row_store8(to32, true, 32 * v, x);
+                    sts128(y16, f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]), f32x2_to_bf16x2(v[4], v[5]), f32x2_to_bf16x2(v[6], v[7]));
+                    if (P == 3) {
+                        sts128(f0, __float_as_int(v[0]), __float_as_int(v[1]), __float_as_int(v[2]), __float_as_int(v[3]));
+                        sts128(f1, __float_as_int(v[4]), __float_as_int(v[5]), __float_as_int(v[6]), __float_as_int(v[7]));
                     }
                 }
-            } else {
-                // the part's last columns, rows that do not allow wide accesses, or NaN
-                const float* low = p.low_big + (size_t)(tile.first + i0) * step;
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int v = 0; v < 2; ++v) {
-                        const int t = h ? t1 : t0, n = n0 + i * kUpBlock + 32 * v + 8 * c;
-                        if (t < 0 || n >= n_end) continue;
-                        float x[8], from[8] = {};
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) x[j] = d[4 * v + (j >> 1)][2 * h + (j & 1)];
-                        if (odd != odd) plain_up<0>(p, low + (h ? 8 * step : 0), scale, b, n, r, x);
-                        if (p.base.ptr) load_cols(row_ptr(p.base, t), p.base.f32, n, n_end, wide, from);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) x[j] += from[j];
-                        if (put) put_cols(row_ptr(p.y, t), false, n, n_end, wide, x);
-                        if (put32) put_cols(row_ptr(p.y32, t), true, n, n_end, wide, x);
-                    }
-                fetch(i + 1);
-            }
-        };
-        load();
-        load();
-        fetch(0);
-        if (r > 0) take();
-        for (int i = 0; i <= runs; ++i) {
-            if (r > 0) {
-                copies_wait<kUpRing - 2>();
-                // the product before has read its operands: they may be replaced
-                if (i > 0 && !bad)
-                    bad = !mbar_wait_bounded(bars + 8 * ((made - 1) & 1), ((made - 1) >> 1) & 1, p.wait, kErrConsumerWait);
                 fence_async_smem();
-                tc_fence_before_sync();
-                bad = __syncthreads_or(bad);
-                tc_fence_after_sync();
-                if (bad) break;
-                if (i < runs) {
-                    if (tid == 0) {
-                        const uint32_t bt = ring + (uint32_t)(i % kUpRing) * stage_bytes;
-                        for (int j = 0; j < P; ++j)
-                            for (int q = 0; q < steps; ++q)
-                                umma_bf16(tmem + (made & 1) * kUpBlock,
-                                          umma_desc_sw128(a_at + (j * pieces + (q >> 2)) * (kBigTile * 128)) + 2 * (q & 3),
-                                          umma_desc_sw128(bt + (q >> 2) * (kUpBlock * 128)) + 2 * (q & 3), idesc, j + q > 0);
-                        umma_commit(bars + 8 * (made & 1));
-                    }
-                    load();
-                    ++made;
+            } else if (mine) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int c = n + 8 * k;
+                    if (c >= n_end) continue;
+                    const bool wide = p.wide && c + 8 <= n_end;
+                    float v[8], from[8] = {};
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = d[8 * k + j];
+                    if (BASE != 0) load_cols(row_ptr(p.base, t), BASE == 2, c, n_end, wide, from);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] += from[j];
+                    if (put) put_cols(row_ptr(p.y, t), false, c, n_end, wide, v);
+                    if (put32) put_cols(row_ptr(p.y32, t), true, c, n_end, wide, v);
                 }
             }
-            if (i > 0) finish(i - 1, (made - (i < runs ? 2 : 1)) & 1);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(written + 8 * stage);
+            advance();
         }
-        copies_wait<0>();
     }
+    if (warp == kUpWarps && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
@@ -1130,7 +1199,7 @@ static size_t low_big_bytes(long long tokens, int rank, int parts) {
     return tokens > kFewTokens && rank <= kBigRank ? up256((size_t)tokens * rank * parts * 4) : 0;
 }
 static size_t lists_bytes(long long tokens, int num) {
-    return tokens > kFewTokens ? up256(16 + (size_t)max_big(tokens, num) * sizeof(BigTile) + (size_t)tokens * 4 +
+    return tokens > kFewTokens ? up256(16 + (size_t)max_big(tokens) * sizeof(BigTile) + ((size_t)tokens + 1) * 4 +
                                        (size_t)max_small(tokens, num) * sizeof(Tile)) : 0;
 }
 
@@ -1148,6 +1217,8 @@ static dl_status check_adapters(const dl_adapters* a, AdapterParams& p) {
         return host_fail(DL_ERR_UNSUPPORTED_SHAPE, "K=%d must be a multiple of 8 and N=%d positive", a->K, a->N);
     if (a->parts < 1 || a->parts > kMaxParts)
         return host_fail(DL_ERR_UNSUPPORTED_SHAPE, "parts=%d is outside [1, %d]", a->parts, kMaxParts);
+    if ((long long)a->num * a->N > 0x7fffff00LL)
+        return host_fail(DL_ERR_UNSUPPORTED_SHAPE, "num=%d adapters of N=%d rows exceed 2^31 - 256", a->num, a->N);
     int before = 0;
     for (int i = 0; i < a->parts; ++i) {
         const int end = a->part_end[i];
@@ -1213,7 +1284,37 @@ static cudaError_t launch_small(const AdapterParams& p, long long tiles, int sm_
     return cudaLaunchKernelEx(&cfg, adapters_low_kernel, p);
 }
 
-static cudaError_t launch_low_big(const AdapterParams& p, long long tiles, int sm_count, cudaStream_t stream) {
+// A tensor map of rows: boxes of 128 bytes of columns and `high` rows, 128-byte swizzled.
+static dl_status rows_map(CUtensorMap& map, const void* data, bool f32, long long rows, long long columns, long long stride, int high) {
+    EncodeTiled encode;
+    const dl_status s = host_encode(encode);
+    if (s != DL_OK) return s;
+    const cuuint64_t dims[2] = {(cuuint64_t)columns, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride};
+    const cuuint32_t box[2] = {f32 ? 32u : 64u, (cuuint32_t)high}, ones[2] = {1, 1};
+    const CUresult r = encode(&map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                              const_cast<void*>(data), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? DL_OK : host_fail(DL_ERR_CUDA, "a tensor map of %lld rows: CUresult %d", rows, (int)r);
+}
+
+struct BigMaps {
+    CUtensorMap x, a;
+    UpMaps up;
+};
+static dl_status big_maps(const AdapterParams& p, BigMaps& m) {
+    const int SR = p.parts * p.rank;
+    dl_status s = rows_map(m.x, p.x.ptr, false, p.tokens, p.K, p.x.stride, kBigTile);
+    if (s == DL_OK) s = rows_map(m.a, p.a, false, (long long)p.num * SR, p.K, 2LL * p.K, big_smem(SR).cols);
+    if (s == DL_OK) s = rows_map(m.up.b, p.b, false, (long long)p.num * p.N, p.rank, 2LL * p.rank, kUpBlock);
+    m.up.base = m.up.y = m.up.y32 = m.up.b;
+    if (!p.wide) return s;               // (no copies then)
+    if (s == DL_OK && p.base.ptr) s = rows_map(m.up.base, p.base.ptr, p.base.f32, p.tokens, p.N, p.base.stride, kBigTile);
+    if (s == DL_OK) s = rows_map(m.up.y, p.y.ptr, false, p.tokens, p.N, p.y.stride, kBigTile);
+    if (s == DL_OK && p.y32.ptr) s = rows_map(m.up.y32, p.y32.ptr, true, p.tokens, p.N, p.y32.stride, kBigTile);
+    return s;
+}
+
+static cudaError_t launch_low_big(const AdapterParams& p, const BigMaps& m, long long tiles, int sm_count, cudaStream_t stream) {
     const int columns = p.parts * p.rank, groups = (columns + kBigCols - 1) / kBigCols, splits = big_splits(p.tokens, p.K);
     const long long most = 4LL * sm_count / (splits * groups) + 1;
     const size_t smem = big_smem(columns).total;
@@ -1233,23 +1334,29 @@ static cudaError_t launch_low_big(const AdapterParams& p, long long tiles, int s
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, adapters_low_big_kernel, p);
+    return cudaLaunchKernelEx(&cfg, adapters_low_big_kernel, m.x, m.a, p);
 }
 
 template <int BASE, int P>
-static cudaError_t launch_up_big(const AdapterParams& p, int sm_count, cudaStream_t stream) {
-    const int smem = up_big_smem(p.rank, P);
+static cudaError_t launch_up_big(AdapterParams& p, const BigMaps& m, int sm_count, cudaStream_t stream) {
+    constexpr bool f32 = BASE == 2 || P == 3;
+    const UpSmem one = up_smem(p.rank, P, f32, 1);
+    // three stages, two CTAs to an SM, as far as they fit
+    constexpr int kSm = 227 * 1024;
+    int ctas = kUpCtas, stages = 3;
+    if (2 * (one.total + 2 * one.stage) + 2048 > kSm) ctas = 1;
+    while (stages > 1 && one.total + (stages - 1) * one.stage > kSm) --stages;
+    p.up_stages = stages;
+    const int smem = up_smem(p.rank, P, f32, stages).total;
     const cudaError_t e = raise_smem(adapters_up_big_kernel<BASE, P>, smem);
     if (e != cudaSuccess) return e;
-    int ctas = 228 * 1024 / (smem + 1024);
-    ctas = ctas > kUpCtas ? kUpCtas : ctas;
-    return launch_dependent(adapters_up_big_kernel<BASE, P>, dim3(ctas * sm_count), dim3(kUpThreads), smem, stream, p);
+    return launch_dependent(adapters_up_big_kernel<BASE, P>, dim3(ctas * sm_count), dim3(kUpBigThreads), smem, stream, m.up, p);
 }
 
 template <int P>
-static cudaError_t launch_up_big_base(const AdapterParams& p, int sm_count, cudaStream_t stream) {
-    if (!p.base.ptr || !p.wide) return launch_up_big<0, P>(p, sm_count, stream);
-    return p.base.f32 ? launch_up_big<2, P>(p, sm_count, stream) : launch_up_big<1, P>(p, sm_count, stream);
+static cudaError_t launch_up_big_base(AdapterParams& p, const BigMaps& m, int sm_count, cudaStream_t stream) {
+    if (!p.base.ptr) return launch_up_big<0, P>(p, m, sm_count, stream);
+    return p.base.f32 ? launch_up_big<2, P>(p, m, sm_count, stream) : launch_up_big<1, P>(p, m, sm_count, stream);
 }
 
 }  // namespace dl
@@ -1317,15 +1424,17 @@ extern "C" dl_status dl_linear_adapters(const dl_adapters* adapters, const dl_ro
     } else {
         // Each list's kernels find how much there is on the device.  Both first products may run at the
         // same time, then both second ones.
-        const long long big = max_big(tokens, p.num);
+        const long long big = max_big(tokens);
+        BigMaps maps;
+        if (p.rank <= kBigRank && (s = big_maps(p, maps)) != DL_OK) return s;
         const size_t counters = (size_t)(p.num + 1) * 4;
         if ((e = raise_smem(sort_tokens_kernel, counters)) == cudaSuccess)
             e = launch_dependent(sort_tokens_kernel, dim3(1), dim3(1024), counters, st, p);
         if (e == cudaSuccess) e = launch_small(p, small, dev.sm_count, st, false);
-        if (e == cudaSuccess && p.rank <= kBigRank) e = launch_low_big(p, big, dev.sm_count, st);
+        if (e == cudaSuccess && p.rank <= kBigRank) e = launch_low_big(p, maps, big, dev.sm_count, st);
         if (e == cudaSuccess) e = launch_small(p, small, dev.sm_count, st, true);
         if (e == cudaSuccess && p.rank <= kBigRank)
-            e = p.y32.ptr ? launch_up_big_base<3>(p, dev.sm_count, st) : launch_up_big_base<2>(p, dev.sm_count, st);
+            e = p.y32.ptr ? launch_up_big_base<3>(p, maps, dev.sm_count, st) : launch_up_big_base<2>(p, maps, dev.sm_count, st);
     }
     if (e != cudaSuccess) return host_fail(DL_ERR_CUDA, "linear_adapters launch: %s", cudaGetErrorString(e));
     return host_ok();
