@@ -299,3 +299,42 @@ def test_refusals(cuda_device):
         dl.Adapters(ad.a, ad.b, scale=torch.ones(2, device=cuda_device))
     with pytest.raises(ValueError, match="b"):
         dl.Adapters(ad.a, ad.b.float())
+
+
+@pytest.mark.parametrize("R", [8, 24, 64, 104, 128])
+@pytest.mark.parametrize("base,f32", [("bf16", False), ("bf16", True), ("fp32", False), ("fp32", True), (None, False), (None, True)])
+def test_long_runs(cuda_device, R, base, f32):
+    """Runs of tokens of one adapter: whole tiles of 128, their ends, runs that are just too short; columns in
+    whole blocks of 64, at a part's end and rows that allow no wide access; ranks that end inside 16."""
+    g = torch.Generator().manual_seed(R)
+    for N, cols, K in ((192, [128, 64], 72), (200, None, 1000), (100, None, 520), (65, None, 64)):
+        c = Case(900, K, N, R, 5, cols=cols, base=base, f32=f32, seed=R + N)
+        runs, index = [1, 300, 63, 64, 128, 2, 200, 65, 77], []
+        for n in runs:
+            index += [int(torch.randint(-1, 5, (1,), generator=g))] * n
+        c.index = torch.tensor(index, dtype=torch.int32)
+        out, out32 = c.run(cuda_device)
+        c.check(out, out32)
+        if base == "bf16":                   # in place: rows without an adapter stay as they are, bit for bit
+            y = c.base.to(cuda_device)
+            none = (c.index < 0).nonzero()[:, 0].to(cuda_device)
+            y.view(torch.int16)[none] = 0x7fab
+            c.run(cuda_device)
+            dl.linear_adapters(c.x.to(cuda_device), c.adapters(cuda_device), c.index.to(cuda_device), y, out=y,
+                               out_f32=torch.empty(900, N, device=cuda_device) if f32 else None)
+            some = (c.index >= 0).nonzero()[:, 0].to(cuda_device)
+            assert torch.equal(y[some], out[some]) and bool((y.view(torch.int16)[none] == 0x7fab).all())
+
+
+def test_long_runs_repeat(cuda_device):
+    """Bitwise repeatable among other calls, on one workspace of the largest of several token counts."""
+    cases = [Case(T, 512, 192, 32, 4, cols=[128, 64], order="runs", none=0.0, seed=T) for T in (300, 5000, 1100)]
+    ws = dl.Workspace(dl.adapters_workspace_bytes(5000, cases[0].adapters(cuda_device)))
+    args = [(c.x.to(cuda_device), c.adapters(cuda_device), c.index.to(cuda_device), c.base.to(cuda_device)) for c in cases]
+    want = [dl.linear_adapters(*a).clone() for a in args]
+    for c, w in zip(cases[:1] + cases[2:], want[:1] + want[2:]):
+        c.check(w)
+    for _ in range(3):
+        got = [dl.linear_adapters(*a, workspace=ws) for a in args]
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    assert dl.device_status() == 0

@@ -1033,11 +1033,15 @@ __global__ void __launch_bounds__(kUpBigThreads, kUpCtas) adapters_up_big_kernel
                     tc_fence_after_sync();
                     if (lane == 0) {
                         const uint64_t bt = ring_desc + (uint64_t)(stage * shape.stage >> 4);
-                        for (int j = 0; j < P; ++j)
-                            for (int q = 0; q < steps; ++q)
-                                umma_bf16(tmem + acc * kUpBlock,
-                                          a_desc + (uint64_t)((j * pieces + (q >> 2)) * (kBigTile * 128 >> 4) + 2 * (q & 3)),
-                                          bt + (uint64_t)((q >> 2) * (kUpBlock * 128 >> 4) + 2 * (q & 3)), idesc, j + q > 0);
+                        for (int k = 0; k < used; ++k)
+#pragma unroll
+                            for (int j = 0; j < P; ++j) {
+                                const uint64_t x = a_desc + (uint64_t)((j * pieces + k) * (kBigTile * 128 >> 4));
+                                const uint64_t y = bt + (uint64_t)(k * (kUpBlock * 128 >> 4));
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    if (4 * k + q < steps) umma_bf16(tmem + acc * kUpBlock, x + 2 * q, y + 2 * q, idesc, k + j + q > 0);
+                            }
                         umma_commit(made + 8 * acc);
                     }
                     __syncwarp();
