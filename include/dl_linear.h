@@ -511,7 +511,7 @@ typedef struct dl_adapters {
 } dl_adapters;
 
 /*
- * y[t][n] = base[t][n] + scale_a * sum_{r < ranks_a} b_a[n][r] * (a_a[p * rank + r] . x[t]),
+ * y[t][n] = base[t][n] + sum_{r < ranks_a} b_a[n][r] * (scale_a * (a_a[p * rank + r] . x[t])),
  * a = index[t], p the part that holds n.  A token whose index is outside [0, num) has no
  * adapter: its row of y is base (left as it is where base is y).
  *   x      bf16 [tokens][K], rows 16-byte aligned
@@ -519,11 +519,15 @@ typedef struct dl_adapters {
  *   base   [tokens][N], bf16 or fp32 (a linear's y or y_f32), or missing: 0
  *   y      bf16 [tokens][N], rounded once; y_f32 fp32 [tokens][N] or missing: the value
  *          before that.  Each may be base itself; they overlap nothing else.
- * Sums are fp32, over tokens one by one: what a token gets does not depend on the
- * others.  First products go into the second ones as fp32 rounded to 2^-18 of their value,
- * whole where y_f32 is asked for.
- *   tokens any number; workspace: dl_adapters_workspace_bytes(...), zero prefix as
- *   for the linear layers (not used); one workspace serves all.
+ * Sums are fp32.  First products go into the second ones as fp32 rounded to 2^-18 of their
+ * value, whole where y_f32 is asked for.  What a token gets is repeatable bit for bit; its last bits
+ * depend on how many tokens the call has and, beyond 256, on whether it lies in a run of 64 or more
+ * tokens in a row of one adapter (ranks up to 128): such runs go in tiles of 128.  Nothing else of
+ * the other tokens reaches it.
+ *   tokens any number, num * N up to 2^31 - 256; columns go fastest where N's rows of
+ *   base, y and y_f32 are 16-byte aligned (stride and data).
+ *   workspace: dl_adapters_workspace_bytes(...); its zero prefix is left alone, so one
+ *   workspace serves these and the linear layers, one call after the other.
  */
 dl_status dl_linear_adapters(const dl_adapters* adapters, const dl_rows* x, const int* index,
                              const dl_rows* base, const dl_rows* y, const dl_rows* y_f32,

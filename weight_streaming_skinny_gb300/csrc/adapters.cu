@@ -183,32 +183,21 @@ __device__ __forceinline__ int make_tiles(const AdapterParams& p, FewTiles& s) {
     return n;
 }
 
-// An inclusive sum over 1024 threads of three counts; `total`: over all.
-__device__ __forceinline__ void scan3(int (&v)[3], int (*warp_sum)[32], int (&total)[3]) {
+// The sum of `v` over the threads up to this one of 1024; `total`: over all.  Calls take turns with the two
+// halves of `warp_sum`, so one barrier is enough: who writes a half has passed the barrier after its last reads.
+__device__ __forceinline__ int scan(int v, int (*warp_sum)[32], int& half, int& total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1)
-#pragma unroll
-        for (int j = 0; j < 3; ++j) {
-            const int u = __shfl_up_sync(~0u, v[j], o);
-            if (lane >= o) v[j] += u;
-        }
-    __syncthreads();                     // the last scan's sums have been read
-    if (lane == 31)
-        for (int j = 0; j < 3; ++j) warp_sum[j][warp] = v[j];
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < 3; ++j) {
-        int w = warp_sum[j][lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(~0u, w, o);
-            if (lane >= o) w += u;
-        }
-        total[j] = __shfl_sync(~0u, w, 31);
-        const int before = __shfl_sync(~0u, w, max(warp - 1, 0));
-        if (warp > 0) v[j] += before;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(~0u, v, o);
+        if (lane >= o) v += u;
     }
+    if (lane == 31) warp_sum[half][warp] = v;
+    __syncthreads();
+    const int mine = warp_sum[half][lane];
+    half ^= 1;
+    total = (int)__reduce_add_sync(~0u, (unsigned)mine);
+    return v + (int)__reduce_add_sync(~0u, lane < warp ? (unsigned)mine : 0u);
 }
 
 // The lists of many tokens, by one CTA.  Tokens of one adapter in a row, enough of them, make big tiles; the
@@ -216,8 +205,9 @@ __device__ __forceinline__ void scan3(int (&v)[3], int (*warp_sum)[32], int (&to
 // small tile, and their order in it, do not change any result.
 __global__ void __launch_bounds__(1024) sort_tokens_kernel(const __grid_constant__ AdapterParams p) {
     extern __shared__ int count[];       // of each adapter, then its next place; the last: without one
-    __shared__ int warp_sum[3][32];
+    __shared__ int warp_sum[2][32];
     const int tid = threadIdx.x, T = p.tokens;
+    int half = 0, total;
     const Lists l = lists_of(p.tiles, T);
     griddep_wait();
     griddep_launch_dependents();
@@ -231,48 +221,42 @@ __global__ void __launch_bounds__(1024) sort_tokens_kernel(const __grid_constant
             const long long t = t0 + k - 1;
             a[k] = t >= 0 && t < T ? adapter_of(p, (int)t) : -2;
         }
-        int v[3] = {0, 0, 0}, total[3];
+        int mine = 0;
         bool starts[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             starts[k] = t0 + k < T && a[k + 1] != a[k];
-            v[0] += starts[k];
+            mine += starts[k];
         }
-        const int mine = v[0];
-        scan3(v, warp_sum, total);
-        int at = runs + v[0] - mine;
+        int at = runs + scan(mine, warp_sum, half, total) - mine;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             if (starts[k]) l.start[at++] = (int)(t0 + k);
-        runs += total[0];
+        runs += total;
     }
     if (tid == 0) l.start[runs] = T;
     __syncthreads();
     int big = 0;
     for (int i0 = 0; i0 < runs; i0 += 1024) {
         const int i = i0 + tid;
-        int v[3] = {0, 0, 0}, total[3], first = 0, n = 0, ad = -1;
+        int mine = 0, first = 0, n = 0, ad = -1;
         if (i < runs) {
             first = l.start[i];
             n = l.start[i + 1] - first;
             ad = adapter_of(p, first);
-            if (n >= p.big_from) v[0] = (n + kBigTile - 1) / kBigTile;
+            if (n >= p.big_from) mine = (n + kBigTile - 1) / kBigTile;
             else atomicAdd(&count[ad < 0 ? p.num : ad], n);
         }
-        const int mine = v[0];
-        scan3(v, warp_sum, total);
         const int r = mine ? rank_of(p, ad) : 0;
-        for (int j = 0; j < mine; ++j)
-            l.big[big + v[0] - mine + j] = BigTile{ad, first + j * kBigTile, min(n - j * kBigTile, kBigTile), r};
-        big += total[0];
+        BigTile* to = l.big + big + scan(mine, warp_sum, half, total) - mine;
+        for (int j = 0; j < mine; ++j) to[j] = BigTile{ad, first + j * kBigTile, min(n - j * kBigTile, kBigTile), r};
+        big += total;
     }
     __syncthreads();
     int small = 0;
     for (int i0 = 0; i0 <= p.num; i0 += 1024) {
         const int i = i0 + tid, n = i <= p.num ? count[i] : 0, mine = (n + kTile - 1) / kTile;
-        int v[3] = {mine, 0, 0}, total[3];
-        scan3(v, warp_sum, total);
-        const int first = small + v[0] - mine, ad = i < p.num ? i : -1, r = mine ? rank_of(p, ad) : 0;
+        const int first = small + scan(mine, warp_sum, half, total) - mine, ad = i < p.num ? i : -1, r = mine ? rank_of(p, ad) : 0;
         const float scale = mine ? scale_of(p, ad) : 1.f;
         for (int j = 0; j < mine; ++j) {
             Tile& tile = l.small[first + j];
@@ -282,7 +266,7 @@ __global__ void __launch_bounds__(1024) sort_tokens_kernel(const __grid_constant
             tile.count = min(n - j * kTile, kTile);
         }
         if (i <= p.num) count[i] = first * kTile;
-        small += total[0];
+        small += total;
     }
     __syncthreads();
     for (int i = tid; i < runs; i += 1024) {
@@ -320,10 +304,10 @@ __device__ __forceinline__ void split(float a, float b, uint32_t (&v)[P]) {
 
 // ---------------------------------------------------------------- small tiles: first product
 
-// low[t][j] = scale * sum_k A[j][k] x[t][k], as the bf16 parts that the second product takes: a cluster of CTAs shares K, a warp takes 16 rows of A and
-// a tile's 16 tokens over its part of K.  A (and x) go from global memory straight into
-// the operands of mma.m16n8k16: the sum over k may take its terms in any order, so a lane's
-// 16-byte load of 8 consecutive k is the k-slots that it holds in two products.
+// low[t][j] = scale * sum_k A[j][k] x[t][k], as the bf16 parts that the second product takes: a cluster of CTAs
+// shares K, a warp takes 16 rows of A and a tile's 16 tokens over its part of K.  A (and x) go from global
+// memory straight into the operands of mma.m16n8k16: the sum over k may take its terms in any order, so
+// a lane's 16-byte load of 8 consecutive k is the k-slots that it holds in two products.
 template <int N>
 using Int = std::integral_constant<int, N>;
 constexpr int kLowThreads = 256, kLowWarps = kLowThreads / 32;
@@ -1415,7 +1399,7 @@ extern "C" dl_status dl_linear_adapters(const dl_adapters* adapters, const dl_ro
     for (const Rows* r : {&p.base, &p.y, &p.y32})
         if (r->ptr) p.wide = p.wide && rows_aligned16(*r, tokens);
     const long long small = tokens <= kFewTokens ? tokens : max_small(tokens, p.num);
-    if (small * ((N + 15) / 16) > 0x7fff0000LL || small * p.parts * ((p.rank + 15) / 16) > 0x7fff0000LL)
+    if (tokens > 0x7fff0000 || small * ((N + 15) / 16) > 0x7fff0000LL || small * p.parts * ((p.rank + 15) / 16) > 0x7fff0000LL)
         return host_fail(DL_ERR_UNSUPPORTED_SHAPE, "tokens=%d with N=%d exceed one launch", tokens, N);
     HostDevice dev;
     if ((s = host_device(dev)) != DL_OK) return s;
