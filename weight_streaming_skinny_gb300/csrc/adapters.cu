@@ -33,7 +33,6 @@ struct AdapterParams {
     bool wide;               // groups of eight columns of base, y and y32 are 16-byte aligned
     // big tiles
     float* low_big;          // [tokens][parts * rank] first products without scale
-    int up_stages;           // of adapters_up_big_kernel's ring
     WaitCtl wait;
 };
 
@@ -816,28 +815,30 @@ __global__ void __launch_bounds__(kBigThreads) adapters_low_big_kernel(const __g
 
 // Second product of big tiles, out[t][n] = base[t][n] + sum_r low[t][r] B[n][r] for 128 tokens and blocks of 64
 // columns: bound by base and out.  A block is one product on the tensor cores, 128 x 64 over r and the parts of
-// the first products, which lie in shared memory as bf16 operands.  One thread has B's rows and base copied
+// the first products, which lie in tensor memory as bf16 operands (35 us at 4096 tokens, N 10240, rank 64; with
+// them in shared memory, read again for every block, 38).  One thread has B's rows and base copied
 // into a ring of stages and, from there again, the finished blocks to y; another one issues the products, two
 // accumulators in turn; eight warps add base, half a row of 64 a thread.  All tiles' blocks are dealt to the
 // CTAs in equal runs.  Blocks that a whole copy does not fit (the tile's or the part's end, rows that do not
 // allow it) read base and write y by themselves.
-constexpr int kUpBlock = 64, kUpCtas = 2, kUpTmem = 2 * kUpBlock, kUpBigThreads = kUpThreads + 64;
-static_assert(kUpCtas * kUpTmem <= 512, "tensor memory of an SM");
+// Stages: three (35 us as above; two 40, four 41).
+constexpr int kUpBlock = 64, kUpCtas = 2, kUpStages = 3, kUpBigThreads = kUpThreads + 64;
 
-// Shared memory: the first products' parts (128 rows each), then stages: B (64 rows), y (and, of bf16, base
-// before it), base of fp32 (and y_f32 after it) or y_f32.  Rows of 128 bytes, swizzled; B and the parts in pieces of
-// 64 r, fp32 in halves of 32 columns.
+// Shared memory, stages of: B (64 rows), y (and, of bf16, base before it), base of fp32 (and y_f32 after it) or
+// y_f32.  Rows of 128 bytes, swizzled; B in pieces of 64 r, fp32 in halves of 32 columns.
 struct UpSmem {
-    int a, stage, wide_at, total;        // bytes of the parts, of a stage; of it before the fp32 halves; of all
+    int stage, wide_at, total;           // bytes of a stage; of it before the fp32 halves; of all
 };
-__host__ __device__ inline UpSmem up_smem(int rank, int parts, bool f32, int stages) {
-    const int pieces = (rank + 63) / 64;
+__host__ __device__ inline UpSmem up_smem(int rank, bool f32) {
     UpSmem s;
-    s.a = parts * kBigTile * 128 * pieces;
-    s.wide_at = kUpBlock * 128 * pieces + kBigTile * 128;
+    s.wide_at = kUpBlock * 128 * ((rank + 63) / 64) + kBigTile * 128;
     s.stage = s.wide_at + (f32 ? 2 * kBigTile * 128 : 0);
-    s.total = 1024 + s.a + stages * s.stage + 256;
+    s.total = 1024 + kUpStages * s.stage + 256;      // (195 KB at most)
     return s;
+}
+// Tensor memory: two accumulators, then the parts, a row a lane, two r a column.
+__host__ __device__ inline int up_tmem(int rank, int parts) {
+    return 2 * kUpBlock + parts * ((rank + 15) / 16 * 8) <= 256 ? 256 : 512;     // (at most 128 + 3 x 64)
 }
 
 // Blocks of columns, each in one part.
@@ -863,6 +864,23 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
                  : "r"(taddr));
 }
 
+// Four columns of this thread's row.
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&v)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};"
+                 ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// D += A B^T of 128 x n over 16 k, A in tensor memory (eight columns), B in shared memory.
+__device__ __forceinline__ void umma_bf16_from_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+
 struct UpMaps {
     CUtensorMap b, base, y, y32;
 };
@@ -874,10 +892,10 @@ __global__ void __launch_bounds__(kUpBigThreads, kUpCtas) adapters_up_big_kernel
     extern __shared__ __align__(16) unsigned char raw[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Lists l = lists_of(p.tiles, p.tokens);
-    const int R = p.rank, N = p.N, pieces = (R + 63) / 64, S = p.up_stages;
-    const UpSmem shape = up_smem(R, P, BASE == 2 || P == 3, S);
-    const uint32_t a_at = (smem_u32(raw) + 1023u) & ~1023u, ring = a_at + shape.a, bars = ring + S * shape.stage;
-    // stages filled (4 at most) and finished, sums made (two accumulators) and read, the first products of a run in place
+    const int R = p.rank, N = p.N, pieces = (R + 63) / 64, S = kUpStages, part_columns = (R + 15) / 16 * 8;
+    const UpSmem shape = up_smem(R, BASE == 2 || P == 3);
+    const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u, bars = ring + S * shape.stage;
+    // stages filled and finished, sums made (two accumulators) and read, the first products of a run in place
     const uint32_t full = bars, written = bars + 32, made = bars + 64, taken = bars + 80, ready = bars + 96, slot = bars + 104;
     const int y_at = kUpBlock * 128 * pieces;
     // the first products are there: the kernel before this one let it start after it had waited for them
@@ -892,7 +910,7 @@ __global__ void __launch_bounds__(kUpBigThreads, kUpCtas) adapters_up_big_kernel
         griddep_wait();
         return;
     }
-    if (warp == 0) tmem_alloc(slot, kUpTmem);
+    if (warp == 0) tmem_alloc(slot, up_tmem(R, P));
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
             mbar_init(full + 8 * i, 1);
@@ -912,6 +930,7 @@ __global__ void __launch_bounds__(kUpBigThreads, kUpCtas) adapters_up_big_kernel
     griddep_launch_dependents();
     uint32_t tmem;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(slot));
+    const uint32_t parts_at = tmem + 2 * kUpBlock;
     const size_t step = (size_t)p.parts * R;
     // Blocks so far give a stage and its phase, products an accumulator and its, runs with products `ready`'s.
     int stage = 0, turn = 0;             // of the next block
@@ -990,7 +1009,7 @@ __global__ void __launch_bounds__(kUpBigThreads, kUpCtas) adapters_up_big_kernel
         if (warp == kUpWarps + 1) {      // products
             if (r > 0) {
                 const uint32_t idesc = umma_idesc_bf16(kUpBlock);
-                const uint64_t a_desc = umma_desc_sw128(a_at), ring_desc = umma_desc_sw128(ring);
+                const uint64_t ring_desc = umma_desc_sw128(ring);
                 bad = !mbar_wait_bounded(ready, runs_made & 1, p.wait, kErrConsumerWait);
                 ++runs_made;
                 for (int i = 0; i < runs; ++i) {
@@ -1019,13 +1038,12 @@ __global__ void __launch_bounds__(kUpBigThreads, kUpCtas) adapters_up_big_kernel
                         const uint64_t bt = ring_desc + (uint64_t)(stage * shape.stage >> 4);
                         for (int k = 0; k < used; ++k)
 #pragma unroll
-                            for (int j = 0; j < P; ++j) {
-                                const uint64_t x = a_desc + (uint64_t)((j * pieces + k) * (kBigTile * 128 >> 4));
-                                const uint64_t y = bt + (uint64_t)(k * (kUpBlock * 128 >> 4));
+                            for (int j = 0; j < P; ++j)
 #pragma unroll
                                 for (int q = 0; q < 4; ++q)
-                                    if (4 * k + q < steps) umma_bf16(tmem + acc * kUpBlock, x + 2 * q, y + 2 * q, idesc, k + j + q > 0);
-                            }
+                                    if (4 * k + q < steps)
+                                        umma_bf16_from_tmem(tmem + acc * kUpBlock, parts_at + j * part_columns + 8 * (4 * k + q),
+                                                            bt + (uint64_t)(k * (kUpBlock * 128 >> 4) + 2 * q), idesc, k + j + q > 0);
                         umma_commit(made + 8 * acc);
                     }
                     __syncwarp();
@@ -1040,39 +1058,46 @@ __global__ void __launch_bounds__(kUpBigThreads, kUpCtas) adapters_up_big_kernel
         }
         // Eight warps: a thread has a token's row and 32 of a block's 64 columns.
         const float scale = scale_of(p, ad);
-        if (r > 0) {
-            // The run's first products, two threads a row.  (All products of the run before are done: this
-            // thread has waited for the last.)
-            const int row = tid >> 1;
-            const float* low = p.low_big + (size_t)(tile.first + min(row, tile.count - 1)) * step + part * R;
-            for (int i = tid & 1; i < 2 * steps; i += 2) {
-                float v[8] = {};
-                if (row < tile.count && 8 * i < r) {     // (8 i + 8 is within the row)
-                    const float4 x = ld_cg_f32x4(low + 8 * i), y = ld_cg_f32x4(low + 8 * i + 4);
-                    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-                    v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
-                }
-                uint32_t out[P][4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const bool in0 = 8 * i + 2 * k < r, in1 = 8 * i + 2 * k + 1 < r;
-                    uint32_t s[P];
-                    split(in0 ? v[2 * k] * scale : 0.f, in1 ? v[2 * k + 1] * scale : 0.f, s);
-#pragma unroll
-                    for (int j = 0; j < P; ++j) out[j][k] = s[j];
-                }
-#pragma unroll
-                for (int j = 0; j < P; ++j)
-                    sts128(a_at + (j * pieces + (i >> 3)) * (kBigTile * 128) + row * 128 + 16 * ((i & 7) ^ (row & 7)), out[j][0],
-                           out[j][1], out[j][2], out[j][3]);
-            }
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(ready);
-        }
         const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
         const bool mine = row < tile.count;
         const int t = tile.first + (mine ? row : 0);
+        if (r > 0) {
+            // The run's first products, two threads a row, 8 r at a time each.  (All products of the run before are
+            // done: this thread has waited for the last.)
+            const float* low = p.low_big + (size_t)t * step + part * R;
+            const uint32_t to = parts_at + ((uint32_t)(32 * quarter) << 16);
+#pragma unroll 1
+            for (int i0 = half; i0 < 2 * steps; i0 += 4) {
+                float4 x[2][2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {            // (8 r from one below R on are within the row)
+                    const int at = min(8 * (i0 + 2 * k), R - 8);
+                    x[k][0] = ld_cg_f32x4(low + at);
+                    x[k][1] = ld_cg_f32x4(low + at + 4);
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int i = i0 + 2 * k;
+                    if (i >= 2 * steps) break;
+                    const float v[8] = {x[k][0].x, x[k][0].y, x[k][0].z, x[k][0].w, x[k][1].x, x[k][1].y, x[k][1].z, x[k][1].w};
+                    uint32_t out[P][4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const bool in0 = mine && 8 * i + 2 * j < r, in1 = mine && 8 * i + 2 * j + 1 < r;
+                        uint32_t s[P];
+                        split(in0 ? v[2 * j] * scale : 0.f, in1 ? v[2 * j + 1] * scale : 0.f, s);
+#pragma unroll
+                        for (int n = 0; n < P; ++n) out[n][j] = s[n];
+                    }
+#pragma unroll
+                    for (int j = 0; j < P; ++j) tmem_st4(to + j * part_columns + 4 * i, out[j]);
+                }
+            }
+            tmem_wait_st();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ready);
+        }
         for (int i = 0; i < runs; ++i) {
             bad = !mbar_wait_bounded(full + 8 * stage, turn & 1, p.wait, kErrConsumerWait);
             float d[32];
@@ -1165,7 +1190,7 @@ __global__ void __launch_bounds__(kUpBigThreads, kUpCtas) adapters_up_big_kernel
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    if (warp == 0) tmem_dealloc(tmem, kUpTmem);
+    if (warp == 0) tmem_dealloc(tmem, up_tmem(R, P));
     griddep_wait();
 }
 
@@ -1328,14 +1353,10 @@ static cudaError_t launch_low_big(const AdapterParams& p, const BigMaps& m, long
 template <int BASE, int P>
 static cudaError_t launch_up_big(AdapterParams& p, const BigMaps& m, int sm_count, cudaStream_t stream) {
     constexpr bool f32 = BASE == 2 || P == 3;
-    const UpSmem one = up_smem(p.rank, P, f32, 1);
-    // three stages, two CTAs to an SM, as far as they fit
+    // two CTAs to an SM where their stages and their 256 of tensor memory's 512 columns fit twice
     constexpr int kSm = 227 * 1024;
-    int ctas = kUpCtas, stages = 3;
-    if (2 * (one.total + 2 * one.stage) + 2048 > kSm) ctas = 1;
-    while (stages > 1 && one.total + (stages - 1) * one.stage > kSm) --stages;
-    p.up_stages = stages;
-    const int smem = up_smem(p.rank, P, f32, stages).total;
+    const int smem = up_smem(p.rank, f32).total;
+    const int ctas = up_tmem(p.rank, P) == 256 && 2 * (smem + 1024) <= kSm ? kUpCtas : 1;
     const cudaError_t e = raise_smem(adapters_up_big_kernel<BASE, P>, smem);
     if (e != cudaSuccess) return e;
     return launch_dependent(adapters_up_big_kernel<BASE, P>, dim3(ctas * sm_count), dim3(kUpBigThreads), smem, stream, m.up, p);
