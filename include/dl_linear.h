@@ -476,8 +476,8 @@ typedef struct dl_norm {
  *          gate_act DL_GATE_SIGMOID: 1 / (1 + exp(-gate))
  *   h_out, x_out  [rows][dim]; one of them may be missing.  Each may be y or h
  *          itself (the same rows, stride and type); they overlap nothing else.
- * A square that leaves fp32's range does not: such rows are summed scaled.  NaN and
- * infinities give what the formulas give, in their row only.
+ * A square that leaves fp32's range does not: such rows are summed scaled (a difference
+ * from the mean does).  NaN and infinities give what the formulas give, in their row only.
  */
 #define DL_GATE_NONE 0
 #define DL_GATE_ROW 1
@@ -513,7 +513,7 @@ typedef struct dl_adapters {
 /*
  * y[t][n] = base[t][n] + sum_{r < ranks_a} b_a[n][r] * (scale_a * (a_a[p * rank + r] . x[t])),
  * a = index[t], p the part that holds n.  A token whose index is outside [0, num) has no
- * adapter: its row of y is base (left as it is where base is y).
+ * adapter: its row of y is base (left as it is where base is y); one of rank 0 adds nothing.
  *   x      bf16 [tokens][K], rows 16-byte aligned
  *   index  int32 [tokens], in any order
  *   base   [tokens][N], bf16 or fp32 (a linear's y or y_f32), or missing: 0
@@ -548,7 +548,8 @@ size_t dl_adapters_workspace_bytes(int tokens, int num, int rank, int parts);
  * items of a list in their order: from the first that finds too few left on, those that
  * need any are refused.  done[i] is 1 if item i was served, 0 if it was refused (its row
  * is as it was).  A row that a list names twice is served at the first place, refused at
- * the others.
+ * the others.  Every item of a list sees the rows as they were before the call.  Calls on one
+ * pool, and what reads its tables, follow each other on one stream (or are ordered by events).
  */
 typedef struct dl_kv_pages {
     const dl_kv_cache* caches;   /* HOST array, one of each layer: num_pages and page_size as
@@ -558,7 +559,7 @@ typedef struct dl_kv_pages {
     int* block_table;            /* [rows][table_cols]  */
     int* seq_lens;               /* [rows]              */
     int num_caches, num_pages, page_size;
-    int rows, table_cols;        /* rows <= 16384       */
+    int rows, table_cols;        /* rows <= 16384; rows * table_cols and a row's tokens < 2^31 */
 } dl_kv_pages;
 
 /* Give the pages of `n` <= rows listed rows back: their counts fall by one (not below

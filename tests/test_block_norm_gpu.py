@@ -163,6 +163,22 @@ def test_range(cuda_device, kind, spread):
         check(c, call(c, cuda_device))
 
 
+@pytest.mark.parametrize("rows,dim", [(3, 264), (3, 1537), (3, 2048), (700, 2048)])
+def test_far_gates(cuda_device, rows, dim):
+    """Sigmoids next to 0, down to fp32's smallest numbers, times values that bring them back; and next to 1.
+
+    The exponential is off by 2 units of 2^-23 or, below 2^-126, of 2^-149; a sum, a quotient and two products
+    add 4 roundings: 2^-20 of the gate and 2^-147."""
+    gate = torch.tensor([-86.0, -87.5, -88.5, -90.0, -100.0, -103.0, -110.0, -1e30, float("-inf"), 20.0, 90.0, 3e38, float("inf")])
+    gate = gate.repeat(dim // 13 + 1)[:dim]
+    y = torch.full((rows, dim), 1e30)
+    h = torch.zeros(rows, dim)
+    r, _ = dl.block_norm(y.to(cuda_device), h.to(cuda_device), gate=gate.to(cuda_device), gate_act="sigmoid", pre=dl.Norm())
+    want = torch.sigmoid(gate.double())
+    bound = 1e30 * (2.0 ** -20 * want + 2.0 ** -147)
+    assert_near(r, (1e30 * want).expand(rows, dim), bound.expand(rows, dim))
+
+
 def test_far_mean(cuda_device):
     """A mean of 1000 spreads: its rounding errors do not reach the result beyond the inputs' own."""
     for dim in (200, 4096, 30001):

@@ -169,6 +169,15 @@ def test_empty_lists_are_no_call():
     assert call("free", n=0) == call("reserve", n=0) == call("fork", n=0) == 0
 
 
+def test_a_table_too_large():
+    """What all rows can ask for together is below 2^31."""
+    lib = dl.load()
+    for rows, cols, status in ((16384, 1 << 17, 2), (16384, (1 << 17) - 1, 4), (9, 1 << 20, 4)):
+        for what in ("reserve", "fork"):
+            assert call(what, pool(rows=rows, cols=cols), nbytes=0) == status
+    assert b"bytes" in lib.dl_last_error()
+
+
 def test_pages_workspace():
     fn = dl.load().dl_kv_pages_workspace_bytes
     assert fn(0, 1) == fn(1, 0) == fn(1, 16385) == fn((1 << 28) + 1, 1) == 0

@@ -222,40 +222,50 @@ struct Ahead {
     uint4 v[kOn ? E / 8 : 1][WIDE ? 2 : 1];
 
     __device__ __forceinline__ void load(const Slots<E, VEC>& s, const char* p, bool f32) {
-        if (!kOn) return;
+        if constexpr (kOn) {
 #pragma unroll
-        for (int i = 0; i < (kOn ? E / 8 : 1); ++i) {
-            if (i >= s.count) continue;
-            const int e = (s.first + i * s.step) * 8;
-            if (WIDE && f32) {
-                v[i][0] = ldg128(p + 4 * e);
-                v[i][WIDE] = ldg128(p + 4 * e + 16);
-            } else {
-                v[i][0] = ldg128(p + 2 * e);
+            for (int i = 0; i < E / 8; ++i) {
+                if (i >= s.count) continue;
+                const int e = (s.first + i * s.step) * 8;
+                if (WIDE && f32) {
+                    v[i][0] = ldg128(p + 4 * e);
+                    v[i][WIDE] = ldg128(p + 4 * e + 16);
+                } else {
+                    v[i][0] = ldg128(p + 2 * e);
+                }
             }
         }
     }
     __device__ __forceinline__ void get(const Slots<E, VEC>& s, const char* p, bool f32, float (&x)[E]) const {
-        if (!kOn) return s.load(p, f32, x);
+        if constexpr (kOn) {
 #pragma unroll
-        for (int i = 0; i < (kOn ? E / 8 : 1); ++i) {
-            float* t = x + 8 * i;
-            const uint4 a = v[i][0], b = v[i][WIDE];
-            if (i >= s.count) {
+            for (int i = 0; i < E / 8; ++i) {
+                float* t = x + 8 * i;
+                const uint4 a = v[i][0], b = v[i][WIDE];
+                if (i >= s.count) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) t[k] = 0.f;
-            } else if (WIDE && f32) {
-                t[0] = __uint_as_float(a.x); t[1] = __uint_as_float(a.y); t[2] = __uint_as_float(a.z); t[3] = __uint_as_float(a.w);
-                t[4] = __uint_as_float(b.x); t[5] = __uint_as_float(b.y); t[6] = __uint_as_float(b.z); t[7] = __uint_as_float(b.w);
-            } else {
-                bf16x2_to_f32(a.x, t[0], t[1]);
-                bf16x2_to_f32(a.y, t[2], t[3]);
-                bf16x2_to_f32(a.z, t[4], t[5]);
-                bf16x2_to_f32(a.w, t[6], t[7]);
+                    for (int k = 0; k < 8; ++k) t[k] = 0.f;
+                } else if (WIDE && f32) {
+                    t[0] = __uint_as_float(a.x); t[1] = __uint_as_float(a.y); t[2] = __uint_as_float(a.z); t[3] = __uint_as_float(a.w);
+                    t[4] = __uint_as_float(b.x); t[5] = __uint_as_float(b.y); t[6] = __uint_as_float(b.z); t[7] = __uint_as_float(b.w);
+                } else {
+                    bf16x2_to_f32(a.x, t[0], t[1]);
+                    bf16x2_to_f32(a.y, t[2], t[3]);
+                    bf16x2_to_f32(a.z, t[4], t[5]);
+                    bf16x2_to_f32(a.w, t[6], t[7]);
+                }
             }
+        } else {
+            s.load(p, f32, x);
         }
     }
 };
+
+// 1 / (1 + exp(-x)), by an exponential that is at most 1: the quick quotient takes divisors below 2^126 only.
+__device__ __forceinline__ float sigmoid(float x) {
+    const float e = expf(-fabsf(x)), q = __fdividef(1.f, 1.f + e);
+    return x < 0.f ? e * q : q;
+}
 
 // v = h_scale h + scale act(gate) post(v), of what there is.
 template <int E, bool VEC, bool CTA>
@@ -274,7 +284,7 @@ __device__ __forceinline__ void join(float (&v)[E], const float (&h)[E], const B
             }
             if (p.sigmoid) {
 #pragma unroll
-                for (int i = 0; i < E; ++i) g[i] = __fdividef(1.f, 1.f + expf(-g[i]));
+                for (int i = 0; i < E; ++i) g[i] = sigmoid(g[i]);
             }
             times(v, g);
 #pragma unroll
@@ -553,8 +563,8 @@ __global__ void __launch_bounds__(256 + 32, 2) block_norm_ring_kernel(const __gr
                     a = g[2 * j];
                     b = g[2 * j + 1];
                     if (p.sigmoid) {
-                        a = __fdividef(1.f, 1.f + expf(-a));
-                        b = __fdividef(1.f, 1.f + expf(-b));
+                        a = sigmoid(a);
+                        b = sigmoid(b);
                     }
                     v[4 * k + j] = mul2(v[4 * k + j], f2(a, b));
                 }

@@ -378,6 +378,9 @@ static dl_status check_pages(const dl_kv_pages* g, bool caches, PageState& s) {
     if (g->table_cols < 1) return host_fail(DL_ERR_INVALID_ARG, "table_cols=%d must be >= 1", g->table_cols);
     if ((long long)g->table_cols * g->page_size > 0x7fffffffLL)
         return host_fail(DL_ERR_UNSUPPORTED_SHAPE, "a row of %d pages of %d tokens exceeds 2^31 - 1", g->table_cols, g->page_size);
+    // (what a list asks for is counted in 31 bits)
+    if ((long long)g->rows * g->table_cols > 0x7fffffffLL)
+        return host_fail(DL_ERR_UNSUPPORTED_SHAPE, "a table of %d x %d pages exceeds 2^31 - 1", g->rows, g->table_cols);
     if (!g->refs || !g->block_table || !g->seq_lens)
         return host_fail(DL_ERR_INVALID_ARG, "refs, block_table or seq_lens is NULL");
     if (((uintptr_t)g->refs | (uintptr_t)g->block_table | (uintptr_t)g->seq_lens) & 3)
