@@ -521,9 +521,8 @@ typedef struct dl_adapters {
  *          before that.  Each may be base itself; they overlap nothing else.
  * Sums are fp32.  First products go into the second ones as fp32 rounded to 2^-18 of their
  * value, whole where y_f32 is asked for.  What a token gets is repeatable bit for bit; its last bits
- * depend on how many tokens the call has and, beyond 256, on whether it lies in a run of 64 or more
- * tokens in a row of one adapter (ranks up to 128): such runs go in tiles of 128.  Nothing else of
- * the other tokens reaches it.
+ * depend on how many tokens the call has and, beyond 256, on how many of them (and how many in a row)
+ * have its adapter: many go in tiles of 128.  Nothing else of the other tokens reaches it.
  *   tokens any number, num * N up to 2^31 - 256; columns go fastest where N's rows of
  *   base, y and y_f32 are 16-byte aligned (stride and data).
  *   workspace: dl_adapters_workspace_bytes(...); its zero prefix is left alone, so one

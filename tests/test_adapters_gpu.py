@@ -338,3 +338,23 @@ def test_long_runs_repeat(cuda_device):
         got = [dl.linear_adapters(*a, workspace=ws) for a in args]
         assert all(torch.equal(x, y) for x, y in zip(got, want))
     assert dl.device_status() == 0
+
+
+@pytest.mark.parametrize("R", [8, 40, 64, 128, 136])
+@pytest.mark.parametrize("base,f32", [("bf16", False), ("fp32", True), (None, False), ("bf16", True)])
+def test_mixed_tokens_of_few_adapters(cuda_device, R, base, f32):
+    """Many tokens of each adapter, in no order: tiles by lists of tokens, beside long runs and adapters with few."""
+    for T, K, N, cols, num in ((700, 520, 192, [128, 64], 3), (1500, 64, 100, None, 9), (400, 1032, 65, None, 1)):
+        c = Case(T, K, N, R, num, cols=cols, base=base, f32=f32, seed=R + T)
+        g = torch.Generator().manual_seed(R)
+        c.index[:] = torch.randint(-1, num, (T,), generator=g).int()
+        c.index[100:300] = 0                 # a run, with others of the same adapter left over
+        if num > 2:
+            c.index[c.index == 2] = 1        # (fewer than enough of one adapter)
+            c.index[[5, 50, 350]] = 2
+        out, out32 = c.run(cuda_device)
+        c.check(out, out32)
+        perm = torch.randperm(T, generator=g)       # another order, without the run: to the tolerance alike
+        c.x, c.index = c.x[perm], c.index[perm]
+        c.base = None if c.base is None else c.base[perm]
+        c.check(*c.run(cuda_device))

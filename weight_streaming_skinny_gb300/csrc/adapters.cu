@@ -14,6 +14,10 @@ constexpr int kTile = 16;                // tokens of a small tile: all of one a
 constexpr int kFewTokens = 256;          // up to here every CTA makes the list of tiles for itself
 constexpr int kBigTile = 128;            // tokens of a big tile
 constexpr int kBigFrom = 64;             // tokens in a row of one adapter from which on they go in big tiles
+// Tokens of one adapter in no order: as many, and as many as make 2048 times the rank (4096 tokens, 8192 -> 8192, in
+// small tiles and in big ones: 64 of each adapter and rank 16, 32, 64: 115 and 121, 159 and 145, 250 and 214 us;
+// 128 or more of each: 111 and 74, 152 and 79, 231 and 79).
+constexpr int kListFrom = 2048;
 constexpr int kBigRank = 128;            // the largest rank whose second factor fits beside the big tiles' first one
 constexpr int kMaxSplits = 8;            // CTAs that share K of a big tile
 
@@ -28,7 +32,7 @@ struct AdapterParams {
     int tokens;
     uint16_t* low;           // [tokens][2 or 3][parts * rank] scaled first products in bf16 parts (small tiles)
     int* tiles;              // more than kFewTokens tokens: what sort_tokens_kernel writes
-    int big_from;            // kBigFrom, or none if ranks are too large
+    int big_from, list_from; // tokens from which on there are big tiles: in a row, in no order (ranks too large: none)
     bool in_place, in_place32;   // base is y, y32: rows without an adapter stay as they are
     bool wide;               // groups of eight columns of base, y and y32 are 16-byte aligned
     // big tiles
@@ -43,7 +47,8 @@ struct Tile {
     int token[kTile];
     __device__ int at(int i) const { return i < count ? token[i] : -1; }
 };
-// Tokens first .. first + count - 1, all of one adapter.
+// Up to kBigTile tokens of one adapter: first .. first + count - 1, or, first < 0, those that the list `order` names
+// from ~first on.
 struct BigTile {
     int adapter, first, count, rank;
 };
@@ -52,6 +57,7 @@ struct BigTile {
 struct Lists {
     int *counts;             // small tiles, big tiles
     int* start;              // [tokens + 1] where the adapter changes
+    int* order;              // [tokens] of big tiles whose tokens are not in a row
     BigTile* big;
     Tile* small;
 };
@@ -66,8 +72,13 @@ __host__ __device__ inline Lists lists_of(int* at, long long tokens) {
     l.counts = at;
     l.big = reinterpret_cast<BigTile*>(at + 4);
     l.start = reinterpret_cast<int*>(l.big + max_big(tokens));
-    l.small = reinterpret_cast<Tile*>(l.start + tokens + 1);
+    l.order = l.start + tokens + 1;
+    l.small = reinterpret_cast<Tile*>(l.order + tokens);
     return l;
+}
+// Token `row` of a big tile.
+__device__ __forceinline__ int token_of(const Lists& l, const BigTile& t, int row) {
+    return t.first >= 0 ? t.first + row : l.order[~t.first + row];
 }
 
 __device__ __forceinline__ int adapter_of(const AdapterParams& p, int t) {
@@ -200,8 +211,9 @@ __device__ __forceinline__ int scan(int v, int (*warp_sum)[32], int& half, int& 
 }
 
 // The lists of many tokens, by one CTA.  Tokens of one adapter in a row, enough of them, make big tiles; the
-// others are sorted by adapter (counted, then placed) into small ones.  Which tokens of an adapter share a
-// small tile, and their order in it, do not change any result.
+// others are sorted by adapter (counted, then placed): an adapter that has enough of them left gets big tiles
+// with a list of its tokens, one that has fewer small tiles.  Which tokens of an adapter share a tile, and their
+// order in it, do not change any result.
 __global__ void __launch_bounds__(1024) sort_tokens_kernel(const __grid_constant__ AdapterParams p) {
     extern __shared__ int count[];       // of each adapter, then its next place; the last: without one
     __shared__ int warp_sum[2][32];
@@ -252,10 +264,16 @@ __global__ void __launch_bounds__(1024) sort_tokens_kernel(const __grid_constant
         big += total;
     }
     __syncthreads();
-    int small = 0;
+    // an adapter's places: in small tiles, or (~place) in the list that big ones name
+    int small = 0, listed = 0;
     for (int i0 = 0; i0 <= p.num; i0 += 1024) {
-        const int i = i0 + tid, n = i <= p.num ? count[i] : 0, mine = (n + kTile - 1) / kTile;
-        const int first = small + scan(mine, warp_sum, half, total) - mine, ad = i < p.num ? i : -1, r = mine ? rank_of(p, ad) : 0;
+        const int i = i0 + tid, n = i <= p.num ? count[i] : 0, ad = i < p.num ? i : -1;
+        const bool gathered = ad >= 0 && n >= p.list_from;
+        const int mine = gathered ? 0 : (n + kTile - 1) / kTile, mine_big = gathered ? (n + kBigTile - 1) / kBigTile : 0;
+        const int first = small + scan(mine, warp_sum, half, total) - mine, r = n ? rank_of(p, ad) : 0;
+        small += total;
+        const int place = listed + scan(gathered ? n : 0, warp_sum, half, total) - (gathered ? n : 0);
+        listed += total;
         const float scale = mine ? scale_of(p, ad) : 1.f;
         for (int j = 0; j < mine; ++j) {
             Tile& tile = l.small[first + j];
@@ -264,15 +282,24 @@ __global__ void __launch_bounds__(1024) sort_tokens_kernel(const __grid_constant
             tile.scale = scale;
             tile.count = min(n - j * kTile, kTile);
         }
-        if (i <= p.num) count[i] = first * kTile;
-        small += total;
+        BigTile* to = l.big + big + scan(mine_big, warp_sum, half, total) - mine_big;
+        big += total;
+        for (int j = 0; j < mine_big; ++j) to[j] = BigTile{ad, ~(place + j * kBigTile), min(n - j * kBigTile, kBigTile), r};
+        if (i <= p.num) count[i] = gathered ? ~place : first * kTile;
     }
     __syncthreads();
     for (int i = tid; i < runs; i += 1024) {
         const int first = l.start[i], n = l.start[i + 1] - first;
         if (n >= p.big_from) continue;
-        const int ad = adapter_of(p, first), at = atomicAdd(&count[ad < 0 ? p.num : ad], n);
-        for (int k = 0; k < n; ++k) l.small[(at + k) / kTile].token[(at + k) % kTile] = first + k;
+        const int ad = adapter_of(p, first);
+        int& next = count[ad < 0 ? p.num : ad];
+        if (*(volatile int*)&next < 0) {                 // (which of the two it is never changes)
+            const int at = ~atomicSub(&next, n);
+            for (int k = 0; k < n; ++k) l.order[at + k] = first + k;
+        } else {
+            const int at = atomicAdd(&next, n);
+            for (int k = 0; k < n; ++k) l.small[(at + k) / kTile].token[(at + k) % kTile] = first + k;
+        }
     }
     if (tid == 0) {
         l.counts[0] = small;
@@ -643,11 +670,22 @@ __device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t a_desc, uint
 // First product of big tiles: low_big[token][j] = sum_k A[j][k] x[token][k], a product of 128 tokens
 // and up to 256 rows of A on the tensor cores, the sums in tensor memory.  It is bound by what an SM reads
 // from L2: a tile's x once, A once a tile.  One thread has x and A copied into 128-byte swizzled stages of 64 k,
-// another one issues the products.  A cluster shares K: each CTA leaves its sums in its shared memory, where
+// another one issues the products.  Where the tokens are not in a row, eight warps copy x in pieces of 16 bytes (30 us
+// for 4096 tokens, K 8192, rank 64; by tile::gather4, four rows an instruction, 53; in a row 25).  A cluster shares K: each CTA leaves its sums in its shared memory, where
 // the cluster's CTAs add them up, a share of the tokens each, always in the same order.  Rows of A past the
 // rank, and of x past the tile, are read like the others: what they make are values that nobody takes.
 constexpr int kBigWarps = 8, kBigThreads = 32 * (kBigWarps + 2);
 constexpr int kBigCols = 256;            // rows of A of one CTA, at most
+
+// 16 bytes into shared memory, zeros if not `in`; and waits for all but the last N groups of such.
+__device__ __forceinline__ void copy16(uint32_t dst, const char* src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy16_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy16_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 struct BigSmem {
     int cols, stage, stages, total;      // columns of the accumulator, bytes of a stage, stages, bytes of all
@@ -675,7 +713,7 @@ __global__ void __launch_bounds__(kBigThreads) adapters_low_big_kernel(const __g
     const BigSmem shape = big_smem(SR);
     const int stages = shape.stages;
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u, bars = base + stages * shape.stage;
-    const uint32_t full = bars, empty = bars + 8 * stages, done = bars + 16 * stages, slot = done + 8;
+    const uint32_t full = bars, empty = bars + 8 * stages, copied = bars + 16 * stages, done = bars + 24 * stages, slot = done + 8;
     // The lists are complete and the buffers free: the kernel before this one let it start only after
     // it had waited for sort_tokens_kernel.  (Its own results are other ones; the wait is at the end.)
     const int n_tiles = l.counts[1];
@@ -691,6 +729,7 @@ __global__ void __launch_bounds__(kBigThreads) adapters_low_big_kernel(const __g
         for (int i = 0; i < stages; ++i) {
             mbar_init(full + 8 * i, 1);
             mbar_init(empty + 8 * i, 1);
+            mbar_init(copied + 8 * i, kBigWarps);
         }
         mbar_init(done, 1);
         fence_mbarrier_init();
@@ -711,10 +750,12 @@ __global__ void __launch_bounds__(kBigThreads) adapters_low_big_kernel(const __g
     const int pitch = shape.cols + 4;
     int stage = 0, turn = 0;             // of the next step: its stage, and how often all stages have been used before
     int tiles_done = 0;
+    unsigned copies = 0;                 // parities of `copied`, which gathered tiles alone use
     bool dead = false;                   // a wait gave up: the CTA goes on with the cluster, without its copies and products
     for (int ti = blockIdx.y; ti < n_tiles; ti += gridDim.y) {
         const BigTile tile = l.big[ti];
         if (tile.adapter < 0) continue;
+        const bool gathered = tile.first < 0;
         bool bad = dead;
         if (dead) {
         } else if (warp == kBigWarps) {
@@ -723,16 +764,57 @@ __global__ void __launch_bounds__(kBigThreads) adapters_low_big_kernel(const __g
                     if (turn > 0) bad = !mbar_wait_bounded(empty + 8 * stage, (turn - 1) & 1, p.wait, kErrProducerWait);
                     if (bad) break;
                     const uint32_t to = base + (uint32_t)stage * shape.stage, bar = full + 8 * stage;
-                    mbar_arrive_expect_tx(bar, shape.stage);
-                    tma_load_2d(to, &map_x, bar, (s0 + s) * 64, tile.first, policy_evict_first());
+                    mbar_arrive_expect_tx(bar, shape.stage - (gathered ? kBigTile * 128 : 0));
+                    if (!gathered) tma_load_2d(to, &map_x, bar, (s0 + s) * 64, tile.first, policy_evict_first());
                     tma_load_2d(to + kBigTile * 128, &map_a, bar, (s0 + s) * 64, tile.adapter * SR + j0, policy_evict_last());
                     if (++stage == stages) stage = 0, ++turn;
                 }
             }
             __syncwarp();
+        } else if (warp < kBigWarps && gathered) {
+            // eight threads a row of 128 bytes, four rows a thread; a step's copies are given away when those of
+            // kAhead steps more are on their way
+            constexpr int kAhead = 3;
+            const char* from[4];
+            uint32_t at[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = (tid >> 3) + 32 * i;
+                from[i] = row_ptr(p.x, token_of(l, tile, min(row, tile.count - 1))) + 16 * (tid & 7);
+                at[i] = base + row * 128 + 16 * ((tid & 7) ^ (row & 7));
+            }
+            int given = stage;
+            for (int s = 0; s < n + kAhead; ++s) {
+                if (s < n) {
+                    if (turn > 0) bad = !mbar_wait_bounded(empty + 8 * stage, (turn - 1) & 1, p.wait, kErrProducerWait);
+                    if (__any_sync(~0u, bad)) break;
+                    const int k = (s0 + s) * 64;
+                    const bool in = k + 8 * (tid & 7) < K;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) copy16(at[i] + (uint32_t)stage * shape.stage, in ? from[i] + 2 * k : from[i], in);
+                    if (++stage == stages) stage = 0, ++turn;
+                }
+                copy16_commit();
+                if (s >= kAhead) {
+                    copy16_wait<kAhead>();
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(copied + 8 * given);
+                    if (++given == stages) given = 0;
+                }
+            }
+            copy16_wait<0>();
+            bad = __any_sync(~0u, bad);
+        } else if (warp < kBigWarps) {
+            turn += (stage + n) / stages;
+            stage = (stage + n) % stages;
         } else if (warp == kBigWarps + 1 && lane == 0) {
             for (int s = 0; s < n && !bad; ++s) {
                 bad = !mbar_wait_bounded(full + 8 * stage, turn & 1, p.wait, kErrConsumerWait);
+                if (gathered && !bad) {
+                    bad = !mbar_wait_bounded(copied + 8 * stage, copies >> stage & 1, p.wait, kErrConsumerWait);
+                    copies ^= 1u << stage;
+                }
                 if (bad) break;
                 tc_fence_after_sync();
                 const uint32_t at = base + (uint32_t)stage * shape.stage;
@@ -758,10 +840,10 @@ __global__ void __launch_bounds__(kBigThreads) adapters_low_big_kernel(const __g
         tc_fence_after_sync();
         // a thread has a token's row; two warps share 32 tokens' columns
         const bool alone = splits == 1;
-        float* out = p.low_big + (size_t)tile.first * SR + j0;
+        float* out = p.low_big + j0;
         if (warp < kBigWarps) {
             const int row = 32 * (warp & 3) + lane;
-            float* to = alone ? out + (size_t)row * SR : sums + row * pitch;
+            float* to = alone ? out + (size_t)token_of(l, tile, min(row, tile.count - 1)) * SR : sums + row * pitch;
             for (int j = 16 * (warp >> 2); j < shape.cols; j += 32) {
                 float v[16];
                 tmem_ld16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + j, v);
@@ -797,7 +879,7 @@ __global__ void __launch_bounds__(kBigThreads) adapters_low_big_kernel(const __g
                         if (q >= splits) break;
                         v.x += w[h][q].x; v.y += w[h][q].y; v.z += w[h][q].z; v.w += w[h][q].w;
                     }
-                    if (i < all) *reinterpret_cast<float4*>(out + (size_t)t * SR + j) = v;
+                    if (i < all) *reinterpret_cast<float4*>(out + (size_t)token_of(l, tile, t) * SR + j) = v;
                 }
             }
             cluster.sync();              // the others have read this CTA's sums: its stages are free
@@ -819,8 +901,10 @@ __global__ void __launch_bounds__(kBigThreads) adapters_low_big_kernel(const __g
 // them in shared memory, read again for every block, 38).  One thread has B's rows and base copied
 // into a ring of stages and, from there again, the finished blocks to y; another one issues the products, two
 // accumulators in turn; eight warps add base, half a row of 64 a thread.  All tiles' blocks are dealt to the
-// CTAs in equal runs.  Blocks that a whole copy does not fit (the tile's or the part's end, rows that do not
-// allow it) read base and write y by themselves.
+// CTAs in equal runs.  Tiles that whole copies do not fit (fewer than 128 tokens, or not in a row) are copied by the
+// eight warps in pieces of 16 bytes, a warp its own rows, through the same stages (37 us for 4096 tokens in no
+// order, N 8192; a thread straight from and to its own row, 59).  Rows that are not aligned, and a part's end inside
+// a piece, go element by element.
 // Stages: three (35 us as above; two 40, four 41).
 constexpr int kUpBlock = 64, kUpCtas = 2, kUpStages = 3, kUpBigThreads = kUpThreads + 64;
 
@@ -953,7 +1037,7 @@ __global__ void __launch_bounds__(kUpBigThreads, kUpCtas) adapters_up_big_kernel
         const int ad = tile.adapter, r = tile.rank, steps = (r + 15) / 16, used = (steps + 3) / 4;
         const bool put = ad >= 0 || !p.in_place, put32 = P == 3 && (ad >= 0 || !p.in_place32);
         if (!put && !put32) continue;
-        auto whole = [&](int i) { return tile.count == kBigTile && p.wide && n0 + (i + 1) * kUpBlock <= n_end; };
+        auto whole = [&](int i) { return tile.count == kBigTile && tile.first >= 0 && p.wide && n0 + (i + 1) * kUpBlock <= n_end; };
         if (warp == kUpWarps) {          // copies
             if (lane == 0) {
                 const int first = stage, first_turn = turn;
@@ -1060,7 +1144,7 @@ __global__ void __launch_bounds__(kUpBigThreads, kUpCtas) adapters_up_big_kernel
         const float scale = scale_of(p, ad);
         const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
         const bool mine = row < tile.count;
-        const int t = tile.first + (mine ? row : 0);
+        const int t = token_of(l, tile, mine ? row : 0);
         if (r > 0) {
             // The run's first products, two threads a row, 8 r at a time each.  (All products of the run before are
             // done: this thread has waited for the last.)
@@ -1098,8 +1182,35 @@ __global__ void __launch_bounds__(kUpBigThreads, kUpCtas) adapters_up_big_kernel
             __syncwarp();
             if (lane == 0) mbar_arrive(ready);
         }
+        // Of tiles that are not copied, blocks of whole pieces of 16 bytes: a warp brings and takes its own 32 rows'
+        // halves of the stage, whole rows by neighbouring lanes, base a block ahead.
+        const bool listed = p.wide && (tile.first < 0 || tile.count < kBigTile);
+        auto in_pieces = [&](int i) { return listed && (n0 + (i + 1) * kUpBlock <= n_end || n_end % 8 == 0); };
+        // this lane's k-th piece: where in the stage, of which token, from which column on
+        auto piece = [&](int i, int k, bool f32, int at, uint32_t& to, int& token, int& c) {
+            const int r32 = k * (f32 ? 4 : 8) + (lane >> (f32 ? 3 : 2)), q = lane & (f32 ? 7 : 3), rw = 32 * quarter + r32;
+            token = __shfl_sync(~0u, t, r32);
+            c = n0 + i * kUpBlock + 32 * half + q * (f32 ? 4 : 8);
+            const uint32_t base_at = ring + at * shape.stage;
+            to = f32 ? base_at + shape.wide_at + half * (kBigTile * 128) + rw * 128 + 16 * (q ^ (rw & 7))
+                     : base_at + y_at + rw * 128 + 16 * ((4 * half + q) ^ (rw & 7));
+            return rw < tile.count && c < n_end;
+        };
+        auto fetch = [&](int i, int at) {
+            if (BASE != 0 && in_pieces(i)) {
+#pragma unroll
+                for (int k = 0; k < (BASE == 2 ? 8 : 4); ++k) {
+                    uint32_t to;
+                    int token, c;
+                    if (piece(i, k, BASE == 2, at, to, token, c))
+                        copy16(to, row_ptr(p.base, token) + (size_t)c * (BASE == 2 ? 4 : 2), true);
+                }
+            }
+            copy16_commit();
+        };
         for (int i = 0; i < runs; ++i) {
             bad = !mbar_wait_bounded(full + 8 * stage, turn & 1, p.wait, kErrConsumerWait);
+            if (listed && i == 0) fetch(0, stage);
             float d[32];
             if (r > 0) {
                 const unsigned acc = products & 1;
@@ -1135,7 +1246,22 @@ __global__ void __launch_bounds__(kUpBigThreads, kUpCtas) adapters_up_big_kernel
                     for (int j = 0; j < 8; ++j) d[8 * k + j] = x[j];
                 }
             }
-            if (whole(i)) {
+            if (!listed) {
+            } else if (i + 1 < runs) {
+                const int next = stage + 1 == S ? 0 : stage + 1;
+                if (in_pieces(i + 1)) bad = !mbar_wait_bounded(full + 8 * next, (turn + (next == 0)) & 1, p.wait, kErrConsumerWait);
+                bad = __any_sync(~0u, bad);
+                if (bad) break;
+                fetch(i + 1, next);
+            } else {
+                copy16_commit();
+            }
+            const bool pieces_here = in_pieces(i);
+            if (pieces_here || whole(i)) {
+                if (pieces_here) {
+                    copy16_wait<1>();
+                    __syncwarp();
+                }
                 const uint32_t to = ring + stage * shape.stage, y_row = to + y_at + row * 128, swap = row & 7;
                 const uint32_t f_row = to + shape.wide_at + half * (kBigTile * 128) + row * 128;
 #pragma unroll
@@ -1162,6 +1288,25 @@ __global__ void __launch_bounds__(kUpBigThreads, kUpCtas) adapters_up_big_kernel
                     if (P == 3) {
                         sts128(f0, __float_as_int(v[0]), __float_as_int(v[1]), __float_as_int(v[2]), __float_as_int(v[3]));
                         sts128(f1, __float_as_int(v[4]), __float_as_int(v[5]), __float_as_int(v[6]), __float_as_int(v[7]));
+                    }
+                }
+                if (pieces_here) {
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t from;
+                        int token, c;
+                        if (piece(i, k, false, stage, from, token, c) && put)
+                            *reinterpret_cast<uint4*>(row_ptr(p.y, token) + (size_t)c * 2) = lds128(from);
+                    }
+                    if (P == 3) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            uint32_t from;
+                            int token, c;
+                            if (piece(i, k, true, stage, from, token, c) && put32)
+                                *reinterpret_cast<uint4*>(row_ptr(p.y32, token) + (size_t)c * 4) = lds128(from);
+                        }
                     }
                 }
                 fence_async_smem();
@@ -1212,7 +1357,7 @@ static size_t low_big_bytes(long long tokens, int rank, int parts) {
     return tokens > kFewTokens && rank <= kBigRank ? up256((size_t)tokens * rank * parts * 4) : 0;
 }
 static size_t lists_bytes(long long tokens, int num) {
-    return tokens > kFewTokens ? up256(16 + (size_t)max_big(tokens) * sizeof(BigTile) + ((size_t)tokens + 1) * 4 +
+    return tokens > kFewTokens ? up256(16 + (size_t)max_big(tokens) * sizeof(BigTile) + (2 * (size_t)tokens + 1) * 4 +
                                        (size_t)max_small(tokens, num) * sizeof(Tile)) : 0;
 }
 
@@ -1411,7 +1556,11 @@ extern "C" dl_status dl_linear_adapters(const dl_adapters* adapters, const dl_ro
     p.low = reinterpret_cast<uint16_t*>(scratch);
     p.low_big = reinterpret_cast<float*>(scratch + low_bytes(tokens, p.rank, p.parts));
     p.tiles = reinterpret_cast<int*>(scratch + low_bytes(tokens, p.rank, p.parts) + low_big_bytes(tokens, p.rank, p.parts));
-    p.big_from = p.rank <= kBigRank ? kBigFrom : 0x7fffffff;
+    p.big_from = p.list_from = 0x7fffffff;
+    if (p.rank <= kBigRank) {
+        p.big_from = kBigFrom;
+        p.list_from = kBigFrom * p.rank < kListFrom ? kListFrom / p.rank : kBigFrom;
+    }
     p.index = index;
     p.tokens = tokens;
     p.in_place = same_rows(p.y, p.base);
