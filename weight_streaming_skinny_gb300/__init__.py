@@ -1,7 +1,9 @@
 """GB300 (sm_103a) decode-linear weight streaming: Python binding.
 
 y[M, N] = x[M, K] . W[N, K]^T (+ bias) for M = 1..16 decode tokens, with bf16
-weights or weight-only FP8 (e4m3, one fp32 scale per 128x128 block).  Every
+weights or weight-only FP8 (e4m3, one fp32 scale per 128x128 block); what a
+step does around them: norms with the residual stream, low-rank adapters, a
+paged 8-bit cache with its attention and its pages, draft verification.  Every
 step runs in the CUDA kernels of ``libdecode_linear.so`` behind the C ABI in
 ``include/dl_linear.h``; this module only checks torch tensors and passes raw
 device pointers, sizes and the current stream through ctypes.  There is no CPU
