@@ -615,7 +615,8 @@ dl_status dl_set_override(int kernel, int ctas_per_sm, int max_ctas);
  *                   bytes) but never issues the copies that would fill it, so
  *                   every wait on that stage runs out; no copy is in flight
  *                   for it when the CTA leaves.  In an attention launch CTA 0
- *                   does the same with the keys of its k-th tile of 128 tokens.  Needs 0 < wait_limit_ns <=
+ *                   does the same with the keys of its k-th tile of 128 tokens, in a norm of many long rows with
+ *                   its k-th row, in the products of an adapter's many tokens with their k-th stage.  Needs 0 < wait_limit_ns <=
  *                   100 ms (else DL_ERR_INVALID_ARG).
  * A launch that ran with a withheld stage leaves wrong outputs and may leave
  * arrival counters set in its workspace: zero the workspace's first

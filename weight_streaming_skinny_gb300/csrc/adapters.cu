@@ -37,6 +37,7 @@ struct AdapterParams {
     bool wide;               // groups of eight columns of base, y and y32 are 16-byte aligned
     // big tiles
     float* low_big;          // [tokens][parts * rank] first products without scale
+    int withhold;            // test hook: CTA 0 of each product never copies its k-th stage (0: none)
     WaitCtl wait;
 };
 
@@ -766,8 +767,10 @@ __global__ void __launch_bounds__(kBigThreads) adapters_low_big_kernel(const __g
                     if (bad) break;
                     const uint32_t to = base + (uint32_t)stage * shape.stage, bar = full + 8 * stage;
                     mbar_arrive_expect_tx(bar, shape.stage - (gathered ? kBigTile * 128 : 0));
-                    if (!gathered) tma_load_2d(to, &map_x, bar, (s0 + s) * 64, tile.first, policy_evict_first());
-                    tma_load_2d(to + kBigTile * 128, &map_a, bar, (s0 + s) * 64, tile.adapter * SR + j0, policy_evict_last());
+                    if (blockIdx.x + blockIdx.y + blockIdx.z > 0 || turn * stages + stage + 1 != p.withhold) {
+                        if (!gathered) tma_load_2d(to, &map_x, bar, (s0 + s) * 64, tile.first, policy_evict_first());
+                        tma_load_2d(to + kBigTile * 128, &map_a, bar, (s0 + s) * 64, tile.adapter * SR + j0, policy_evict_last());
+                    }
                     if (++stage == stages) stage = 0, ++turn;
                 }
             }
@@ -1047,6 +1050,7 @@ __global__ void __launch_bounds__(kUpBigThreads, kUpCtas) adapters_up_big_kernel
                     const int n = n0 + i * kUpBlock;
                     const bool with = BASE != 0 && whole(i);
                     mbar_arrive_expect_tx(bar, used * (kUpBlock * 128) + (with ? (BASE == 2 ? 2 : 1) * kBigTile * 128 : 0));
+                    if (blockIdx.x == 0 && turn * S + stage + 1 == p.withhold) return advance();
                     for (int k = 0; k < used; ++k)
                         tma_load_2d(to + k * (kUpBlock * 128), &maps.b, bar, 64 * k, ad * N + n, policy_evict_last());
                     if (with) {
@@ -1333,6 +1337,7 @@ __global__ void __launch_bounds__(kUpBigThreads, kUpCtas) adapters_up_big_kernel
         }
     }
     if (warp == kUpWarps && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    copy16_wait<0>();
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
@@ -1576,6 +1581,7 @@ extern "C" dl_status dl_linear_adapters(const dl_adapters* adapters, const dl_ro
     if ((s = host_device(dev)) != DL_OK) return s;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     p.wait = WaitCtl{dev.err_word, dev.wait_limit_ns};
+    p.withhold = dev.withhold_stage;
     cudaError_t e;
     if (tokens <= kFewTokens) {
         if ((e = launch_small(p, small, dev.sm_count, st, false)) == cudaSuccess)

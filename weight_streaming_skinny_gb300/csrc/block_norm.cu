@@ -349,6 +349,7 @@ struct RingParams {
     BlockNormParams n;
     int stages, y_bytes, h_bytes;        // of a row
     WaitCtl wait;
+    int withhold;                        // test hook: CTA 0 never copies its k-th row (0: none)
 };
 
 // Eight values as pairs, and back.
@@ -500,6 +501,7 @@ __global__ void __launch_bounds__(256 + 32, 2) block_norm_ring_kernel(const __gr
             auto load = [&](int i, int stage) {
                 const uint32_t to = ring + stage * stage_bytes, bar = full + 8 * stage;
                 mbar_arrive_expect_tx(bar, stage_bytes);
+                if (blockIdx.x == 0 && i + 1 == q.withhold) return;
                 bulk_load(to, row_ptr(p.y, row_of(i)), q.y_bytes, bar);
                 bulk_load(to + q.y_bytes, row_ptr(p.h, row_of(i)), q.h_bytes, bar);
             };
@@ -635,17 +637,17 @@ cudaError_t launch_ring_types(RingParams& q, int sm_count, cudaStream_t stream) 
 
 // Many rows of more than 1024 elements through the ring: where all streams are there, r has h's type, x is no
 // wider than y, and whole warps of threads hold a row: 16 elements each up to 4096, 32 up to 8192.
-static bool launch_ring(const BlockNormParams& p, int sm_count, const WaitCtl& wait, cudaStream_t stream, cudaError_t& e) {
+static bool launch_ring(const BlockNormParams& p, int sm_count, const WaitCtl& wait, int withhold, cudaStream_t stream, cudaError_t& e) {
     if (!p.y.ptr || !p.h.ptr || !p.r.ptr || !p.x.ptr || p.pre.kind == DL_NORM_NONE || p.r.f32 != p.h.f32 ||
         (p.x.f32 && !p.y.f32) || p.rows < 4 * sm_count || p.dim > 8192 || p.dim % (p.dim <= 4096 ? 512 : 1024))
         return false;
-    RingParams q = {p, 0, p.dim * (p.y.f32 ? 4 : 2), p.dim * (p.h.f32 ? 4 : 2), wait};
+    RingParams q = {p, 0, p.dim * (p.y.f32 ? 4 : 2), p.dim * (p.h.f32 ? 4 : 2), wait, withhold};
     e = p.dim <= 4096 ? launch_ring_types<16>(q, sm_count, stream) : launch_ring_types<32>(q, sm_count, stream);
     return true;
 }
 
 template <bool VEC>
-cudaError_t launch_norm_rows(BlockNormParams& p, int sm_count, const WaitCtl& wait, cudaStream_t stream) {
+cudaError_t launch_norm_rows(BlockNormParams& p, int sm_count, const WaitCtl& wait, int withhold, cudaStream_t stream) {
     const int groups = (p.dim + 7) / 8;
     if (groups <= 128) {                    // teams inside a warp, at most 32 elements a thread
         int lanes = 8;
@@ -659,7 +661,7 @@ cudaError_t launch_norm_rows(BlockNormParams& p, int sm_count, const WaitCtl& wa
         return launch_norm<32, VEC, false, 128>(p, grid, threads, stream);
     }
     cudaError_t e;
-    if (VEC && launch_ring(p, sm_count, wait, stream, e)) return e;
+    if (VEC && launch_ring(p, sm_count, wait, withhold, stream, e)) return e;
     // A CTA each: as few groups a thread as leave all rows an SM at once, two if none does; single elements
     // one group (999 rows of 1537: 14 us; two 30 us)
     int per = 1, threads = 0;
@@ -760,7 +762,8 @@ extern "C" dl_status dl_block_norm(const dl_rows* y, const dl_norm* post, const 
     if ((s = host_device(dev)) != DL_OK) return s;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const WaitCtl wait = {dev.err_word, dev.wait_limit_ns};
-    const cudaError_t e = vec ? launch_norm_rows<true>(p, dev.sm_count, wait, st) : launch_norm_rows<false>(p, dev.sm_count, wait, st);
+    const cudaError_t e = vec ? launch_norm_rows<true>(p, dev.sm_count, wait, dev.withhold_stage, st)
+                              : launch_norm_rows<false>(p, dev.sm_count, wait, dev.withhold_stage, st);
     if (e != cudaSuccess) return host_fail(DL_ERR_CUDA, "block_norm launch: %s", cudaGetErrorString(e));
     return host_ok();
 }
