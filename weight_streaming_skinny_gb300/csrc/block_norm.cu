@@ -649,37 +649,27 @@ static bool launch_ring(const BlockNormParams& p, int sm_count, const WaitCtl& w
 template <bool VEC>
 cudaError_t launch_norm_rows(BlockNormParams& p, int sm_count, const WaitCtl& wait, int withhold, cudaStream_t stream) {
     const int groups = (p.dim + 7) / 8;
-    if (groups <= 128) {                    // teams inside a warp, at most 32 elements a thread
+    if (groups <= 64) {                     // teams inside a warp, two groups a thread at most
         int lanes = 8;
-        while (lanes < 32 && lanes * 4 < groups) lanes *= 2;
-        const int per = (groups + lanes - 1) / lanes, threads = 128;
+        while (lanes < 32 && lanes < groups) lanes *= 2;
+        const int threads = 128;
         const long long all = ((long long)p.rows * lanes + threads - 1) / threads, most = 16LL * sm_count;
         const long long grid = all < most ? all : most;
         p.lanes = lanes;
-        if (per <= 1) return launch_norm<8, VEC, false, 128>(p, grid, threads, stream);
-        if (per <= 2) return launch_norm<16, VEC, false, 128>(p, grid, threads, stream);
-        return launch_norm<32, VEC, false, 128>(p, grid, threads, stream);
+        return groups <= lanes ? launch_norm<8, VEC, false, 128>(p, grid, threads, stream)
+                               : launch_norm<16, VEC, false, 128>(p, grid, threads, stream);
     }
     cudaError_t e;
     if (VEC && launch_ring(p, sm_count, wait, withhold, stream, e)) return e;
-    // A CTA each: as few groups a thread as leave all rows an SM at once, two if none does; single elements
-    // one group (999 rows of 1537: 14 us; two 30 us)
-    int per = 1, threads = 0;
-    long long most = 0;
-    for (;; per *= 2) {
-        threads = ((groups + per - 1) / per + 31) / 32 * 32;
-        const long long fit = 1024 / threads;
-        most = (fit > 8 ? 8 : fit) * sm_count;
-        if (threads <= 1024 && (p.rows <= most || per >= 2 || !VEC)) break;
-    }
-    const long long grid = p.rows < most ? p.rows : most;
+    // A CTA each, as few groups a thread as 1024 threads allow: one up to 8192 (8000 rows of 1000, 2000, 3000, 8000: 11, 23, 38,
+    // 92 us; two 20, 29, 44, 118 us; rows of 1000 by a warp 26), single elements too (999 rows of 1537: 13 us; two 30)
+    const int per = groups <= 1024 ? 1 : groups <= 2048 ? 2 : 4, threads = ((groups + per - 1) / per + 31) / 32 * 32;
+    const long long fit = 1024 / threads, most = fit * sm_count, grid = p.rows < most ? p.rows : most;
     if (per == 1)
         return threads <= 256 ? launch_norm<8, VEC, true, 256>(p, grid, threads, stream)
                               : launch_norm<8, VEC, true, 1024>(p, grid, threads, stream);
-    if (per == 2)
-        return threads <= 512 ? launch_norm<16, VEC, true, 512>(p, grid, threads, stream)
-                              : launch_norm<16, VEC, true, 1024>(p, grid, threads, stream);
-    return launch_norm<32, VEC, true, 1024>(p, grid, threads, stream);
+    return per == 2 ? launch_norm<16, VEC, true, 1024>(p, grid, threads, stream)
+                    : launch_norm<32, VEC, true, 1024>(p, grid, threads, stream);
 }
 
 static dl_status check_norm(const dl_norm* n, const char* name, NormSide& out) {
