@@ -46,7 +46,8 @@ def withheld(dev, call, withhold):
 def test_norm(cuda_device, dim, withhold):
     """3000 rows, at least 4 to a CTA."""
     g = torch.Generator(device=cuda_device).manual_seed(dim)
-    y, h = (torch.randn(3000, dim, device=cuda_device, generator=g).bfloat16() for _ in range(2))
+    y, h = (torch.randn(3000, dim, device=cuda_device, generator=g) for _ in range(2))
+    y = y.bfloat16()
     withheld(cuda_device, lambda: dl.block_norm(y, h, pre=dl.Norm()), withhold)
 
 

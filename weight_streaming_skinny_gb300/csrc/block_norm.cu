@@ -551,8 +551,7 @@ __global__ void __launch_bounds__(256 + 32, 2) block_norm_ring_kernel(const __gr
             for (int k = 0; k < E / 8; ++k) finish8(v + 4 * k, inv, p.post, tid * 8 + k * size);
         }
         if (p.gate_kind != DL_GATE_NONE) {
-            const char* gate = p.gate_kind == DL_GATE_CHANNEL ? p.gate.ptr : row_ptr(p.gate, row_of(i));
-            const float one = p.gate_kind == DL_GATE_ROW ? row_load1(gate, p.gate.f32, 0) : 0.f;
+            const float one = p.gate_kind == DL_GATE_ROW ? row_load1(row_ptr(p.gate, row_of(i)), p.gate.f32, 0) : 0.f;
 #pragma unroll
             for (int k = 0; k < E / 8; ++k) {
                 float g[8], a, b;
@@ -560,7 +559,7 @@ __global__ void __launch_bounds__(256 + 32, 2) block_norm_ring_kernel(const __gr
 #pragma unroll
                     for (int j = 0; j < 8; ++j) g[j] = one;
                 } else {
-                    row_load8(gate, p.gate.f32, tid * 8 + k * size, g);
+                    row_load8(p.gate.ptr, p.gate.f32, tid * 8 + k * size, g);
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -625,24 +624,27 @@ cudaError_t launch_ring_kernel(RingParams& q, int sm_count, cudaStream_t stream)
                             smem, stream, q);
 }
 
-template <int E>
+template <int E, bool HF>
 cudaError_t launch_ring_types(RingParams& q, int sm_count, cudaStream_t stream) {
-    const bool h = q.n.h.f32;
-    if (!q.n.y.f32)
-        return h ? launch_ring_kernel<E, false, true, false>(q, sm_count, stream) : launch_ring_kernel<E, false, false, false>(q, sm_count, stream);
-    if (!q.n.x.f32)
-        return h ? launch_ring_kernel<E, true, true, false>(q, sm_count, stream) : launch_ring_kernel<E, true, false, false>(q, sm_count, stream);
-    return h ? launch_ring_kernel<E, true, true, true>(q, sm_count, stream) : launch_ring_kernel<E, true, false, true>(q, sm_count, stream);
+    if (!q.n.y.f32) return launch_ring_kernel<E, false, HF, false>(q, sm_count, stream);
+    return q.n.x.f32 ? launch_ring_kernel<E, true, HF, true>(q, sm_count, stream)
+                     : launch_ring_kernel<E, true, HF, false>(q, sm_count, stream);
 }
 
-// Many rows of more than 1024 elements through the ring: where all streams are there, r has h's type, x is no
-// wider than y, and whole warps of threads hold a row: 16 elements each up to 4096, 32 up to 8192.
+// Many long rows through the ring: where all streams are there, r has h's type, x is no wider than y, and
+// whole warps of threads hold a row: 16 elements each up to 4096, 32 up to 8192.  Rows of up to 4096 with h in bf16
+// have enough of them in registers (4000 x 4096: 24 us both, with a norm of y 35 and 33; with h in fp32 37 and 47), and
+// a gate for each element would not come through it (4000 x 8192: 81 and 74 us; without 47 and 46, with a norm of y 49
+// and 69).
 static bool launch_ring(const BlockNormParams& p, int sm_count, const WaitCtl& wait, int withhold, cudaStream_t stream, cudaError_t& e) {
     if (!p.y.ptr || !p.h.ptr || !p.r.ptr || !p.x.ptr || p.pre.kind == DL_NORM_NONE || p.r.f32 != p.h.f32 ||
-        (p.x.f32 && !p.y.f32) || p.rows < 4 * sm_count || p.dim > 8192 || p.dim % (p.dim <= 4096 ? 512 : 1024))
+        (p.x.f32 && !p.y.f32) || p.gate_kind == DL_GATE_FULL || (p.dim <= 4096 && !p.h.f32) || p.rows < 4 * sm_count ||
+        p.dim > 8192 || p.dim % (p.dim <= 4096 ? 512 : 1024))
         return false;
     RingParams q = {p, 0, p.dim * (p.y.f32 ? 4 : 2), p.dim * (p.h.f32 ? 4 : 2), wait, withhold};
-    e = p.dim <= 4096 ? launch_ring_types<16>(q, sm_count, stream) : launch_ring_types<32>(q, sm_count, stream);
+    e = p.dim <= 4096  ? launch_ring_types<16, true>(q, sm_count, stream)
+        : p.h.f32 ? launch_ring_types<32, true>(q, sm_count, stream)
+                  : launch_ring_types<32, false>(q, sm_count, stream);
     return true;
 }
 
