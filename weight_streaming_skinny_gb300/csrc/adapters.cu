@@ -215,12 +215,14 @@ __device__ __forceinline__ int scan(int v, int (*warp_sum)[32], int& half, int& 
 // others are sorted by adapter (counted, then placed): an adapter that has enough of them left gets big tiles
 // with a list of its tokens, one that has fewer small tiles.  Which tokens of an adapter share a tile, and their
 // order in it, do not change any result.
+constexpr int kStartsHere = 8192;        // tokens whose runs' starts fit shared memory beside the counts
 __global__ void __launch_bounds__(1024) sort_tokens_kernel(const __grid_constant__ AdapterParams p) {
     extern __shared__ int count[];       // of each adapter, then its next place; the last: without one
     __shared__ int warp_sum[2][32];
     const int tid = threadIdx.x, T = p.tokens;
     int half = 0, total;
     const Lists l = lists_of(p.tiles, T);
+    int* start = T <= kStartsHere ? count + p.num + 1 : l.start;
     griddep_wait();
     griddep_launch_dependents();
     for (int i = tid; i <= p.num; i += 1024) count[i] = 0;
@@ -243,18 +245,18 @@ __global__ void __launch_bounds__(1024) sort_tokens_kernel(const __grid_constant
         int at = runs + scan(mine, warp_sum, half, total) - mine;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            if (starts[k]) l.start[at++] = (int)(t0 + k);
+            if (starts[k]) start[at++] = (int)(t0 + k);
         runs += total;
     }
-    if (tid == 0) l.start[runs] = T;
+    if (tid == 0) start[runs] = T;
     __syncthreads();
     int big = 0;
     for (int i0 = 0; i0 < runs; i0 += 1024) {
         const int i = i0 + tid;
         int mine = 0, first = 0, n = 0, ad = -1;
         if (i < runs) {
-            first = l.start[i];
-            n = l.start[i + 1] - first;
+            first = start[i];
+            n = start[i + 1] - first;
             ad = adapter_of(p, first);
             if (n >= p.big_from) mine = (n + kBigTile - 1) / kBigTile;
             else atomicAdd(&count[ad < 0 ? p.num : ad], n);
@@ -290,7 +292,7 @@ __global__ void __launch_bounds__(1024) sort_tokens_kernel(const __grid_constant
     }
     __syncthreads();
     for (int i = tid; i < runs; i += 1024) {
-        const int first = l.start[i], n = l.start[i + 1] - first;
+        const int first = start[i], n = start[i + 1] - first;
         if (n >= p.big_from) continue;
         const int ad = adapter_of(p, first);
         int& next = count[ad < 0 ? p.num : ad];
@@ -1592,7 +1594,7 @@ extern "C" dl_status dl_linear_adapters(const dl_adapters* adapters, const dl_ro
         const long long big = max_big(tokens);
         BigMaps maps;
         if (p.rank <= kBigRank && (s = big_maps(p, maps)) != DL_OK) return s;
-        const size_t counters = (size_t)(p.num + 1) * 4;
+        const size_t counters = ((size_t)p.num + 1 + (tokens <= kStartsHere ? tokens + 1 : 0)) * 4;
         if ((e = raise_smem(sort_tokens_kernel, counters)) == cudaSuccess)
             e = launch_dependent(sort_tokens_kernel, dim3(1), dim3(1024), counters, st, p);
         if (e == cudaSuccess) e = launch_small(p, small, dev.sm_count, st, false);
