@@ -194,23 +194,6 @@ __device__ __forceinline__ int make_tiles(const AdapterParams& p, FewTiles& s) {
     return n;
 }
 
-// The sum of `v` over the threads up to this one of 1024; `total`: over all.  Calls take turns with the two
-// halves of `warp_sum`, so one barrier is enough: who writes a half has passed the barrier after its last reads.
-__device__ __forceinline__ int scan(int v, int (*warp_sum)[32], int& half, int& total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(~0u, v, o);
-        if (lane >= o) v += u;
-    }
-    if (lane == 31) warp_sum[half][warp] = v;
-    __syncthreads();
-    const int mine = warp_sum[half][lane];
-    half ^= 1;
-    total = (int)__reduce_add_sync(~0u, (unsigned)mine);
-    return v + (int)__reduce_add_sync(~0u, lane < warp ? (unsigned)mine : 0u);
-}
-
 // The lists of many tokens, by one CTA.  Tokens of one adapter in a row, enough of them, make big tiles; the
 // others are sorted by adapter (counted, then placed): an adapter that has enough of them left gets big tiles
 // with a list of its tokens, one that has fewer small tiles.  Which tokens of an adapter share a tile, and their
@@ -219,8 +202,9 @@ constexpr int kStartsHere = 8192;        // tokens whose runs' starts fit shared
 __global__ void __launch_bounds__(1024) sort_tokens_kernel(const __grid_constant__ AdapterParams p) {
     extern __shared__ int count[];       // of each adapter, then its next place; the last: without one
     __shared__ int warp_sum[2][32];
+    Scan scan{warp_sum};
     const int tid = threadIdx.x, T = p.tokens;
-    int half = 0, total;
+    int total;
     const Lists l = lists_of(p.tiles, T);
     int* start = T <= kStartsHere ? count + p.num + 1 : l.start;
     griddep_wait();
@@ -242,7 +226,7 @@ __global__ void __launch_bounds__(1024) sort_tokens_kernel(const __grid_constant
             starts[k] = t0 + k < T && a[k + 1] != a[k];
             mine += starts[k];
         }
-        int at = runs + scan(mine, warp_sum, half, total) - mine;
+        int at = runs + scan(mine, total) - mine;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             if (starts[k]) start[at++] = (int)(t0 + k);
@@ -262,7 +246,7 @@ __global__ void __launch_bounds__(1024) sort_tokens_kernel(const __grid_constant
             else atomicAdd(&count[ad < 0 ? p.num : ad], n);
         }
         const int r = mine ? rank_of(p, ad) : 0;
-        BigTile* to = l.big + big + scan(mine, warp_sum, half, total) - mine;
+        BigTile* to = l.big + big + scan(mine, total) - mine;
         for (int j = 0; j < mine; ++j) to[j] = BigTile{ad, first + j * kBigTile, min(n - j * kBigTile, kBigTile), r};
         big += total;
     }
@@ -273,9 +257,9 @@ __global__ void __launch_bounds__(1024) sort_tokens_kernel(const __grid_constant
         const int i = i0 + tid, n = i <= p.num ? count[i] : 0, ad = i < p.num ? i : -1;
         const bool gathered = ad >= 0 && n >= p.list_from;
         const int mine = gathered ? 0 : (n + kTile - 1) / kTile, mine_big = gathered ? (n + kBigTile - 1) / kBigTile : 0;
-        const int first = small + scan(mine, warp_sum, half, total) - mine, r = n ? rank_of(p, ad) : 0;
+        const int first = small + scan(mine, total) - mine, r = n ? rank_of(p, ad) : 0;
         small += total;
-        const int place = listed + scan(gathered ? n : 0, warp_sum, half, total) - (gathered ? n : 0);
+        const int place = listed + scan(gathered ? n : 0, total) - (gathered ? n : 0);
         listed += total;
         const float scale = mine ? scale_of(p, ad) : 1.f;
         for (int j = 0; j < mine; ++j) {
@@ -285,7 +269,7 @@ __global__ void __launch_bounds__(1024) sort_tokens_kernel(const __grid_constant
             tile.scale = scale;
             tile.count = min(n - j * kTile, kTile);
         }
-        BigTile* to = l.big + big + scan(mine_big, warp_sum, half, total) - mine_big;
+        BigTile* to = l.big + big + scan(mine_big, total) - mine_big;
         big += total;
         for (int j = 0; j < mine_big; ++j) to[j] = BigTile{ad, ~(place + j * kBigTile), min(n - j * kBigTile, kBigTile), r};
         if (i <= p.num) count[i] = gathered ? ~place : first * kTile;

@@ -35,29 +35,6 @@ struct Plan {
 constexpr int kPlanThreads = 1024;
 constexpr int kMaxRows = 16384;          // `first` of the planning kernels fits shared memory
 
-// An inclusive sum over the CTA's threads; `total` is the sum over all.
-__device__ __forceinline__ int block_scan(int v, int* warp_sum, int& total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int inc = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(~0u, inc, o);
-        if (lane >= o) inc += u;
-    }
-    __syncthreads();                     // the last scan's sums have been read
-    if (lane == 31) warp_sum[warp] = inc;
-    __syncthreads();
-    int w = warp_sum[lane];              // 32 warps
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(~0u, w, o);
-        if (lane >= o) w += u;
-    }
-    total = __shfl_sync(~0u, w, 31);
-    const int before = __shfl_sync(~0u, w, warp > 0 ? warp - 1 : 0);
-    return inc + (warp > 0 ? before : 0);
-}
-
 // Which of 16 pages from p on are free.
 __device__ __forceinline__ unsigned free_mask(const PageState& s, int p) {
     unsigned m = 0;
@@ -77,14 +54,14 @@ __device__ __forceinline__ unsigned free_mask(const PageState& s, int p) {
 
 // The first `want` free pages, lowest first, into list; returns how many there are (at most want).
 // A thread looks at 16 pages a round; the first round's is done (`is_free`).
-__device__ int free_pages(const PageState& s, int want, unsigned is_free, int* list, int* warp_sum) {
+__device__ int free_pages(const PageState& s, int want, unsigned is_free, int* list, Scan& scan) {
     int found = 0;
     for (int p0 = 0; p0 < s.num_pages && found < want; p0 += 16 * kPlanThreads) {
         const int p = p0 + 16 * threadIdx.x;
         if (p0) is_free = free_mask(s, p);
         int total;
         const int n = __popc(is_free);
-        int at = found + block_scan(n, warp_sum, total) - n;
+        int at = found + scan(n, total) - n;
         for (; is_free && at < want; ++at) {
             list[at] = p + __ffs(is_free) - 1;
             is_free &= is_free - 1;
@@ -128,7 +105,8 @@ struct ListParams {
 template <bool FORK>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ ListParams p) {
     extern __shared__ int first[];       // of each row, the first item that changes it
-    __shared__ int warp_sum[32];
+    __shared__ int warp_sum[2][32];
+    Scan scan{warp_sum};
     const PageState& s = p.s;
     const int tid = threadIdx.x;
     griddep_wait();
@@ -165,11 +143,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
             }
         }
         int total;
-        q.first = asked + block_scan(q.need, warp_sum, total) - q.need;
+        q.first = asked + scan(q.need, total) - q.need;
         asked += total;
         if (i < p.n) p.plan[i] = q;
     }
-    const int got = free_pages(s, asked, is_free, p.list, warp_sum);
+    const int got = free_pages(s, asked, is_free, p.list, scan);
     // all lengths have been read: they may change now
     for (int i = tid; i < p.n; i += kPlanThreads) {
         Plan q = p.plan[i];
@@ -289,7 +267,8 @@ struct CompactParams {
 // Pages in use from the front on: those past the first `live` places move, in order, into the free
 // places before it.  One CTA.
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const __grid_constant__ CompactParams p) {
-    __shared__ int warp_sum[32];
+    __shared__ int warp_sum[2][32];
+    Scan scan{warp_sum};
     const PageState& s = p.s;
     const int tid = threadIdx.x;
     griddep_wait();
@@ -302,7 +281,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const __grid
             const int page = p0 + k * kPlanThreads + tid;
             n += page < s.num_pages && s.refs[page] > 0;
         }
-        block_scan(n, warp_sum, total);
+        scan(n, total);
         live += total;
     }
     int holes = 0, moves = 0;
@@ -319,10 +298,10 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const __grid
         }
         int total;
         const int nh = __popc(hole), nm = __popc(move);
-        int at = holes + block_scan(nh, warp_sum, total) - nh;
+        int at = holes + scan(nh, total) - nh;
         holes += total;
         for (; hole; hole &= hole - 1) p.dst[at++] = page0 + __ffs(hole) - 1;
-        at = moves + block_scan(nm, warp_sum, total) - nm;
+        at = moves + scan(nm, total) - nm;
         moves += total;
         for (; move; move &= move - 1) p.src[at++] = page0 + __ffs(move) - 1;
     }

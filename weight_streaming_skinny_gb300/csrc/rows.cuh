@@ -63,6 +63,28 @@ __device__ __forceinline__ void row_store8(void* p, bool f32, int e, const float
     }
 }
 
+// Sums of counts over the threads up to each one of a CTA of 1024; `total`: over all.  Calls take turns with the two halves
+// of `warp_sum`, so one barrier is enough: who writes a half has passed the barrier after its last reads.
+struct Scan {
+    int (*warp_sum)[32];     // [2][32] shared
+    int half = 0;
+
+    __device__ __forceinline__ int operator()(int v, int& total) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(~0u, v, o);
+            if (lane >= o) v += u;
+        }
+        if (lane == 31) warp_sum[half][warp] = v;
+        __syncthreads();
+        const int mine = warp_sum[half][lane];
+        half ^= 1;
+        total = (int)__reduce_add_sync(~0u, (unsigned)mine);
+        return v + (int)__reduce_add_sync(~0u, lane < warp ? (unsigned)mine : 0u);
+    }
+};
+
 // ---------------------------------------------------------------- host
 
 // The checked form of an argument (NULL, or without data: none).
