@@ -501,14 +501,23 @@ __device__ __forceinline__ uint2 rank_mask(int at, int r) {
                       (at + 2 < r ? 0xffffu : 0u) | (at + 3 < r ? 0xffff0000u : 0u));
 }
 
-// Small tiles: a warp takes 64 columns of a tile, 16 r at a time.  What does not depend on the first products
+// Four or eight consecutive r of a row, zeros if not `in`: the k-slots that a lane holds in one product or in two.
+__device__ __forceinline__ void load_r(const uint16_t* p, bool in, uint2 (&v)[1]) { v[0] = in ? ldg64(p) : make_uint2(0, 0); }
+__device__ __forceinline__ void load_r(const uint16_t* p, bool in, uint2 (&v)[2]) {
+    const uint4 x = in ? ldg128(p) : make_uint4(0, 0, 0, 0);
+    v[0] = make_uint2(x.x, x.y);
+    v[1] = make_uint2(x.z, x.w);
+}
+
+// Small tiles: a warp takes 64 columns of a tile, 16 or 32 r at a time.  What does not depend on the first products
 // (the tiles, base, B) is fetched before they are waited for: the kernel that makes them lets this one start only
 // after it had waited for all earlier ones.  Bound by instructions and latencies: a tile of few tokens costs as
-// much as one of 16, so each lane has all its loads of 16 r in flight at once.
-// BASE 0: none, 1: bf16, 2: fp32; P: parts of a first product (3: there is an fp32 result)
+// much as one of 16, so each lane has all its loads of these r in flight at once.  Ranks up to 32 by 16, beyond by 32
+// (250 tokens of 64 adapters, 8192 -> 8192: rank 16, 64, 128 21, 45, 78 us and 23, 39.5, 67).
+// BASE 0: none, 1: bf16, 2: fp32; P: parts of a first product (3: there is an fp32 result); 16 Q r at a time
 constexpr int kUpThreads = 256, kUpWarps = kUpThreads / 32, kUpUnit = 64;
 
-template <int BASE, int P>
+template <int BASE, int P, int Q>
 __global__ void __launch_bounds__(kUpThreads, 2) adapters_up_kernel(const __grid_constant__ AdapterParams p) {
     extern __shared__ __align__(16) unsigned char smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
@@ -549,19 +558,21 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapters_up_kernel(const __grid
         const int first = part_of(p, n0), last = part_of(p, min(n0 + kUpUnit, N) - 1);
         float d[8][4] = {};                  // [product][row g: 2 columns, row g + 8: 2 columns]
         const int col = n0 + (g >> 1) * 8 + (g & 1);     // of product 0; the others' are 2, 4, 6, 32, .. further
-        const uint16_t* b = p.b + ((size_t)max(ad, 0) * N + col) * R + 4 * c;
-        const uint16_t *low0 = p.low + (size_t)max(t0, 0) * P * step + 4 * c, *low1 = p.low + (size_t)max(t1, 0) * P * step + 4 * c;
-        for (int r0 = 0; r0 < r; r0 += 16) {
-            const bool in = r0 + 4 * c < r;
-            uint2 w[8];
+        const uint16_t* b = p.b + ((size_t)max(ad, 0) * N + col) * R + 4 * Q * c;
+        const uint16_t* low0 = p.low + (size_t)max(t0, 0) * P * step + 4 * Q * c;
+        const uint16_t* low1 = p.low + (size_t)max(t1, 0) * P * step + 4 * Q * c;
+        for (int r0 = 0; r0 < r; r0 += 16 * Q) {
+            const int mine_from = r0 + 4 * Q * c;
+            const bool in = mine_from < r;
+            uint2 w[8][Q];
             if (whole) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = in ? ldg64(b + (2 * (i & 3) + 32 * (i >> 2)) * R + r0) : make_uint2(0, 0);
+                for (int i = 0; i < 8; ++i) load_r(b + (2 * (i & 3) + 32 * (i >> 2)) * R + r0, in, w[i]);
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int at = 2 * (i & 3) + 32 * (i >> 2);
-                    w[i] = in && col + at < N ? ldg64(b + at * R + r0) : make_uint2(0, 0);
+                    load_r(b + at * R + r0, in && col + at < N, w[i]);
                 }
             }
             if (!waited) {
@@ -569,26 +580,32 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapters_up_kernel(const __grid
                 griddep_launch_dependents();
                 waited = true;
             }
-            if (r0 + 16 > r) {               // what lies past the rank is nobody's
-                const uint2 m = rank_mask(r0 + 4 * c, r);
+            if (r0 + 16 * Q > r) {           // what lies past the rank is nobody's
 #pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = make_uint2(w[i].x & m.x, w[i].y & m.y);
+                for (int q = 0; q < Q; ++q) {
+                    const uint2 m = rank_mask(mine_from + 4 * q, r);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) w[i][q] = make_uint2(w[i][q].x & m.x, w[i][q].y & m.y);
+                }
             }
             for (int pt = first; pt <= last; ++pt) {
-                uint2 a0[P], a1[P];
+                uint2 a0[P][Q], a1[P][Q];
 #pragma unroll
                 for (int j = 0; j < P; ++j) {
-                    a0[j] = in && t0 >= 0 ? ldg64(low0 + j * step + pt * R + r0) : make_uint2(0, 0);
-                    a1[j] = in && t1 >= 0 ? ldg64(low1 + j * step + pt * R + r0) : make_uint2(0, 0);
+                    load_r(low0 + j * step + pt * R + r0, in && t0 >= 0, a0[j]);
+                    load_r(low1 + j * step + pt * R + r0, in && t1 >= 0, a1[j]);
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     // the columns of this part: 16 are brought by the lanes of four g
                     const int at = n0 + 32 * (i >> 2) + (g >= 4 ? 16 : 0);
                     const bool mine = first == last || (at < p.part_end[pt] && (pt == 0 || at >= p.part_end[pt - 1]));
-                    const uint2 v = mine ? w[i] : make_uint2(0, 0);
 #pragma unroll
-                    for (int j = 0; j < P; ++j) mma_bf16_16816(d[i], a0[j].x, a1[j].x, a0[j].y, a1[j].y, v.x, v.y);
+                    for (int q = 0; q < Q; ++q) {
+                        const uint2 v = mine ? w[i][q] : make_uint2(0, 0);
+#pragma unroll
+                        for (int j = 0; j < P; ++j) mma_bf16_16816(d[i], a0[j][q].x, a1[j][q].x, a0[j][q].y, a1[j][q].y, v.x, v.y);
+                    }
                 }
             }
         }
@@ -1397,25 +1414,32 @@ static cudaError_t raise_smem(F kernel, size_t bytes) {
     return bytes > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) : cudaSuccess;
 }
 
+template <int Q>
+static cudaError_t launch_up(const AdapterParams& p, dim3 grid, dim3 block, size_t smem, cudaStream_t stream) {
+    const int base = !p.base.ptr ? 0 : p.base.f32 ? 2 : 1;
+    if (p.y32.ptr)
+        return base == 0   ? launch_dependent(adapters_up_kernel<0, 3, Q>, grid, block, smem, stream, p)
+               : base == 1 ? launch_dependent(adapters_up_kernel<1, 3, Q>, grid, block, smem, stream, p)
+                           : launch_dependent(adapters_up_kernel<2, 3, Q>, grid, block, smem, stream, p);
+    return base == 0   ? launch_dependent(adapters_up_kernel<0, 2, Q>, grid, block, smem, stream, p)
+           : base == 1 ? launch_dependent(adapters_up_kernel<1, 2, Q>, grid, block, smem, stream, p)
+                       : launch_dependent(adapters_up_kernel<2, 2, Q>, grid, block, smem, stream, p);
+}
+
 static cudaError_t launch_small(const AdapterParams& p, long long tiles, int sm_count, cudaStream_t stream, bool up) {
     const size_t smem = p.tokens <= kFewTokens ? sizeof(FewTiles) : 0;
     if (up) {
         const long long ctas = (tiles * ((p.N + kUpUnit - 1) / kUpUnit) + kUpWarps - 1) / kUpWarps, most = 2LL * sm_count;
         const dim3 grid((unsigned)(ctas < most ? ctas : most)), block(kUpThreads);
-        const int base = !p.base.ptr ? 0 : p.base.f32 ? 2 : 1;
-        if (p.y32.ptr)
-            return base == 0 ? launch_dependent(adapters_up_kernel<0, 3>, grid, block, smem, stream, p)
-                   : base == 1 ? launch_dependent(adapters_up_kernel<1, 3>, grid, block, smem, stream, p)
-                               : launch_dependent(adapters_up_kernel<2, 3>, grid, block, smem, stream, p);
-        return base == 0 ? launch_dependent(adapters_up_kernel<0, 2>, grid, block, smem, stream, p)
-               : base == 1 ? launch_dependent(adapters_up_kernel<1, 2>, grid, block, smem, stream, p)
-                           : launch_dependent(adapters_up_kernel<2, 2>, grid, block, smem, stream, p);
+        return p.rank <= 32 ? launch_up<1>(p, grid, block, smem, stream) : launch_up<2>(p, grid, block, smem, stream);
     }
-    // Eight CTAs share K while all of them find places, two to an SM in whole clusters (128 SMs of which do),
-    // four beyond
-    // (of one part, so that sums do not depend on how many parts there are)
-    const long long groups = (p.rank + 15) / 16, items = tiles * p.parts * groups;
-    const int size = tiles * groups * kLowCluster <= 2 * 128 ? kLowCluster : kLowCluster / 2;
+    // CTAs that share K, by the pieces of work that there can be (of one part, so that sums do not depend on how many
+    // parts there are): eight while all of them find places, two to an SM in whole clusters (128 SMs of which do),
+    // then as few as fill the GPU (8192 -> 8192, 64 adapters; of 4, 2 and 1 CTAs, 80 pieces: 19.2, 19.8, 23 us; 158: 30, 28, 30;
+    // 256: 36, 34, 32; 632: 107, 83, 78).
+    const long long any = p.tokens / kTile + p.num + 1, groups = (p.rank + 15) / 16;
+    const long long pieces = (p.tokens < any ? p.tokens : any) * groups, items = tiles * p.parts * groups;
+    const int size = pieces <= 32 ? kLowCluster : pieces <= 100 ? 4 : pieces <= 200 ? 2 : 1;
     const long long most = 2LL * sm_count / size;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
