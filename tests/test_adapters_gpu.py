@@ -344,7 +344,8 @@ def test_long_runs_repeat(cuda_device):
 @pytest.mark.parametrize("base,f32", [("bf16", False), ("fp32", True), (None, False), ("bf16", True)])
 def test_mixed_tokens_of_few_adapters(cuda_device, R, base, f32):
     """Many tokens of each adapter, in no order: tiles by lists of tokens, beside long runs and adapters with few."""
-    for T, K, N, cols, num in ((700, 520, 192, [128, 64], 3), (1500, 64, 100, None, 9), (400, 1032, 65, None, 1)):
+    for T, K, N, cols, num in ((700, 520, 192, [128, 64], 3), (1500, 64, 100, None, 9), (400, 1032, 65, None, 1),
+                               (1500, 136, 72, None, 1)):
         c = Case(T, K, N, R, num, cols=cols, base=base, f32=f32, seed=R + T)
         g = torch.Generator().manual_seed(R)
         c.index[:] = torch.randint(-1, num, (T,), generator=g).int()
@@ -358,3 +359,11 @@ def test_mixed_tokens_of_few_adapters(cuda_device, R, base, f32):
         c.x, c.index = c.x[perm], c.index[perm]
         c.base = None if c.base is None else c.base[perm]
         c.check(*c.run(cuda_device))
+
+
+def test_most_tiles(cuda_device):
+    """As many adapters as have just enough tokens for tiles by lists."""
+    c = Case(4080, 64, 64, 64, 102, none=0.0, ranks=False)
+    c.index = (torch.arange(4080) % 102).int()
+    ws = dl.Workspace(dl.adapters_workspace_bytes(4080, c.adapters(cuda_device)))
+    c.check(*c.run(cuda_device, workspace=ws))

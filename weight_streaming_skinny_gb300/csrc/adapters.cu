@@ -14,10 +14,12 @@ constexpr int kTile = 16;                // tokens of a small tile: all of one a
 constexpr int kFewTokens = 256;          // up to here every CTA makes the list of tiles for itself
 constexpr int kBigTile = 128;            // tokens of a big tile
 constexpr int kBigFrom = 64;             // tokens in a row of one adapter from which on they go in big tiles
-// Tokens of one adapter in no order: as many, and as many as make 2048 times the rank (4096 tokens, 8192 -> 8192, in
-// small tiles and in big ones: 64 of each adapter and rank 16, 32, 64: 115 and 121, 159 and 145, 250 and 214 us;
-// 128 or more of each: 111 and 74, 152 and 79, 231 and 79).
-constexpr int kListFrom = 2048;
+// Tokens of one adapter in no order: 40, and as many as make this times all tokens and the rank (8192 -> 8192, in small
+// tiles and in big ones: 4096 tokens, 64 of each adapter, rank 16, 32, 64: 99 and 115, 122 and 116, 157 and 119 us; 128 of
+// each: 95 and 76, 116 and 78, 150 and 82; rank 64, 1000 tokens, 125 of each: 48 and 39, 300, 150 of each: 22 and 32).
+constexpr int kListFrom = 40;
+constexpr long long kListWork = 6LL << 20;
+static_assert(kListFrom <= kBigFrom && 2 * kListFrom <= kBigTile, "max_big");
 constexpr int kBigRank = 128;            // the largest rank whose second factor fits beside the big tiles' first one
 constexpr int kMaxSplits = 8;            // CTAs that share K of a big tile
 
@@ -62,9 +64,8 @@ struct Lists {
     BigTile* big;
     Tile* small;
 };
-__host__ __device__ inline long long max_big(long long tokens) {
-    return tokens / kBigTile + tokens / kBigFrom + 1;
-}
+// (each adapter's, or each run's, n tokens make ceil(n / kBigTile) <= n / kListFrom of them)
+__host__ __device__ inline long long max_big(long long tokens) { return tokens / kListFrom + 1; }
 __host__ __device__ inline long long max_small(long long tokens, int num) {
     return tokens / kTile + (tokens < num + 1 ? tokens : num + 1) + 1;
 }
@@ -1575,7 +1576,8 @@ extern "C" dl_status dl_linear_adapters(const dl_adapters* adapters, const dl_ro
     p.big_from = p.list_from = 0x7fffffff;
     if (p.rank <= kBigRank) {
         p.big_from = kBigFrom;
-        p.list_from = kBigFrom * p.rank < kListFrom ? kListFrom / p.rank : kBigFrom;
+        const long long need = kListWork / ((long long)tokens * p.rank) + 1;
+        p.list_from = need > kListFrom ? (int)need : kListFrom;
     }
     p.index = index;
     p.tokens = tokens;
