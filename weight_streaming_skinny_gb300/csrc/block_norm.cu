@@ -87,53 +87,175 @@ struct Team {
     }
 };
 
-// The elements of a row that a thread of a team holds: groups of 8 consecutive ones, or (VEC false: rows
-// or weights that are not aligned for groups) every size-th one.
-template <int E, bool VEC>
-struct Slots {
-    int first, step, count;      // groups or elements: the thread's first, from one to the next, how many of E (/ 8)
-
-    __device__ Slots(int rank, int size, int dim) : first(rank), step(size) {
-        const int n = VEC ? (dim + 7) / 8 : dim;
-        count = rank < n ? (n - rank + size - 1) / size : 0;
+// Eight consecutive elements of a row anywhere (aligned to their type), the first n of them its own: read as the
+// aligned pieces of 16 bytes that hold them, as far as these lie in the whole array [lo, hi), and moved by what the address
+// is off when they are used; at the array's ends element by element.
+struct Piece {
+    uint4 a, b, c;
+    bool moved;              // a, b (and c) hold the group, to be moved; or a (and b) the group itself
+};
+struct Bounds {
+    const char *lo, *hi;
+};
+template <bool WIDE>
+__device__ __forceinline__ void any_load(Piece& p, const char* row, bool f32, int e, int n, const Bounds& in) {
+    const bool wide = WIDE && f32;
+    const char* at = row + (wide ? 4LL : 2LL) * e;
+    const int off = (int)((uintptr_t)at & 15);
+    const char* from = at - off;
+    p.moved = from >= in.lo && from + (wide ? 48 : 32) <= in.hi;
+    if (p.moved) {
+        p.a = ldg128(from);
+        p.b = ldg128(from + 16);
+        if (wide) p.c = ldg128(from + 32);
+    } else if (wide) {
+        const uint32_t* q = reinterpret_cast<const uint32_t*>(at);
+        uint32_t w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] = k < n ? q[k] : 0;
+        p.a = make_uint4(w[0], w[1], w[2], w[3]);
+        p.b = make_uint4(w[4], w[5], w[6], w[7]);
+    } else {
+        const uint16_t* q = reinterpret_cast<const uint16_t*>(at);
+        uint32_t w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] = k < n ? q[k] : 0;
+        p.a = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
     }
-    __device__ __forceinline__ bool has(int i) const { return (VEC ? i / 8 : i) < count; }
-    __device__ __forceinline__ void load(const void* p, bool f32, float (&v)[E]) const {
-        if (VEC) {
+}
+template <bool WIDE>
+__device__ __forceinline__ void any_get(const Piece& p, const char* row, bool f32, int e, int n, float* v) {
+    const int off = p.moved ? (int)((uintptr_t)(row + (WIDE && f32 ? 4LL : 2LL) * e) & 15) : 0;
+    uint32_t t[12] = {p.a.x, p.a.y, p.a.z, p.a.w, p.b.x, p.b.y, p.b.z, p.b.w, p.c.x, p.c.y, p.c.z, p.c.w};
+    if (WIDE && f32) {
+#pragma unroll
+        for (int k = 0; k < 10; ++k) t[k] = off & 8 ? t[k + 2] : t[k];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(off & 4 ? t[k + 1] : t[k]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 6; ++k) t[k] = off & 8 ? t[k + 2] : t[k];
+#pragma unroll
+        for (int k = 0; k < 5; ++k) t[k] = off & 4 ? t[k + 1] : t[k];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) bf16x2_to_f32(__funnelshift_r(t[k], t[k + 1], (off & 2) * 8), v[2 * k], v[2 * k + 1]);
+    }
+    if (n < 8) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k >= n) v[k] = 0.f;
+    }
+}
+// Eight values to a row anywhere, the first n of them.
+__device__ __forceinline__ void any_store(char* row, bool f32, int e, int n, const float* v) {
+    if (f32) {
+        float* q = reinterpret_cast<float*>(row) + e;
+        if (n < 8) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k < n) q[k] = v[k];
+        } else if ((uintptr_t)q & 4) {
+            q[0] = v[0];
+#pragma unroll
+            for (int k = 1; k < 7; k += 2) *reinterpret_cast<float2*>(q + k) = make_float2(v[k], v[k + 1]);
+            q[7] = v[7];
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; k += 2) *reinterpret_cast<float2*>(q + k) = make_float2(v[k], v[k + 1]);
+        }
+        return;
+    }
+    uint16_t* q = reinterpret_cast<uint16_t*>(row) + e;
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = f32x2_to_bf16x2(v[2 * k], v[2 * k + 1]);
+    if (n < 8) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < n) q[k] = (uint16_t)(w[k >> 1] >> 16 * (k & 1));
+    } else if ((uintptr_t)q & 2) {
+        q[0] = (uint16_t)w[0];
+        uint32_t* two = reinterpret_cast<uint32_t*>(q + 1);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) two[k] = __funnelshift_r(w[k], w[k + 1], 16);
+        q[7] = (uint16_t)(w[3] >> 16);
+    } else {
+        uint32_t* two = reinterpret_cast<uint32_t*>(q);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) two[k] = w[k];
+    }
+}
+
+// How a thread of a team holds its elements of a row: every size-th one; groups of 8 consecutive ones, whole and
+// aligned; the same of rows that are not.
+constexpr int kSingle = 0, kGroups = 1, kMoved = 2;
+template <int E, int M>
+struct Slots {
+    int first, step, count, n, dim;      // elements or groups: the thread's first, from one to the next, how many; its elements
+
+    __device__ Slots(int rank, int size, int dim_) : first(rank), step(size), dim(dim_) {
+        const int all = M == kSingle ? dim : (dim + 7) / 8;
+        count = rank < all ? (all - rank + size - 1) / size : 0;
+        n = M == kSingle ? count : M == kGroups ? 8 * count : count ? 8 * (count - 1) + min(8, dim - 8 * (rank + (count - 1) * size)) : 0;
+    }
+    __device__ __forceinline__ bool has(int i) const { return i < n; }
+    // of a row of an array
+    __device__ __forceinline__ void load(const void* p, bool f32, float (&v)[E], const Bounds& in) const {
+        if constexpr (M == kSingle) {
+            if (f32) {
+                const float* q = static_cast<const float*>(p) + first;
+#pragma unroll
+                for (int i = 0; i < E; ++i) v[i] = i < count ? q[i * step] : 0.f;
+            } else {
+                const uint16_t* q = static_cast<const uint16_t*>(p) + first;
+#pragma unroll
+                for (int i = 0; i < E; ++i) v[i] = i < count ? bf16_bits_to_f32(q[i * step]) : 0.f;
+            }
+        } else {
 #pragma unroll
             for (int i = 0; i < E / 8; ++i) {
-                if (i < count) {
-                    row_load8(p, f32, (first + i * step) * 8, v + 8 * i);
-                } else {
+                const int e = (first + i * step) * 8;
+                if (i >= count) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k) v[8 * i + k] = 0.f;
+                } else if (M == kGroups) {
+                    row_load8(p, f32, e, v + 8 * i);
+                } else {
+                    Piece t = {};
+                    any_load<true>(t, static_cast<const char*>(p), f32, e, min(n - 8 * i, 8), in);
+                    any_get<true>(t, static_cast<const char*>(p), f32, e, min(n - 8 * i, 8), v + 8 * i);
                 }
             }
-        } else if (f32) {
-            const float* q = static_cast<const float*>(p) + first;
-#pragma unroll
-            for (int i = 0; i < E; ++i) v[i] = i < count ? q[i * step] : 0.f;
-        } else {
-            const uint16_t* q = static_cast<const uint16_t*>(p) + first;
-#pragma unroll
-            for (int i = 0; i < E; ++i) v[i] = i < count ? bf16_bits_to_f32(q[i * step]) : 0.f;
         }
     }
+    // of a row by itself
+    __device__ __forceinline__ void load(const void* p, bool f32, float (&v)[E]) const {
+        const char* at = static_cast<const char*>(p);
+        load(p, f32, v, Bounds{at, at + (size_t)dim * (f32 ? 4 : 2)});
+    }
     __device__ __forceinline__ void store(void* p, bool f32, const float (&v)[E]) const {
-        if (VEC) {
+        if constexpr (M == kSingle) {
+            if (f32) {
+                float* q = static_cast<float*>(p) + first;
 #pragma unroll
-            for (int i = 0; i < E / 8; ++i)
-                if (i < count) row_store8(p, f32, (first + i * step) * 8, v + 8 * i);
-        } else if (f32) {
-            float* q = static_cast<float*>(p) + first;
+                for (int i = 0; i < E; ++i)
+                    if (i < count) q[i * step] = v[i];
+            } else {
+                uint16_t* q = static_cast<uint16_t*>(p) + first;
 #pragma unroll
-            for (int i = 0; i < E; ++i)
-                if (i < count) q[i * step] = v[i];
+                for (int i = 0; i < E; ++i)
+                    if (i < count) q[i * step] = f32_to_bf16_rne(v[i]);
+            }
         } else {
-            uint16_t* q = static_cast<uint16_t*>(p) + first;
 #pragma unroll
-            for (int i = 0; i < E; ++i)
-                if (i < count) q[i * step] = f32_to_bf16_rne(v[i]);
+            for (int i = 0; i < E / 8; ++i) {
+                if (i >= count) continue;
+                const int e = (first + i * step) * 8;
+                if (M == kGroups)
+                    row_store8(p, f32, e, v + 8 * i);
+                else
+                    any_store(static_cast<char*>(p), f32, e, min(n - 8 * i, 8), v + 8 * i);
+            }
         }
     }
 };
@@ -163,8 +285,8 @@ __device__ __forceinline__ float squares(const float (&v)[E]) {
 }
 
 // v = N(v): the elements of one row, zeros past its end.
-template <int E, bool VEC, bool CTA>
-__device__ __forceinline__ void normalise(float (&v)[E], const NormSide& n, Team<CTA>& team, const Slots<E, VEC>& slots, int dim) {
+template <int E, int M, bool CTA>
+__device__ __forceinline__ void normalise(float (&v)[E], const NormSide& n, Team<CTA>& team, const Slots<E, M>& slots, int dim) {
     const float inv_dim = 1.f / dim;
     float ss;
     if (n.kind == DL_NORM_LAYER) {
@@ -216,13 +338,15 @@ __device__ __forceinline__ void normalise(float (&v)[E], const NormSide& n, Team
     }
 }
 
-// What is read of a row ahead of its turn: up to 16 elements of y and h a thread, of 16 bits, or of 32.
-template <int E, bool VEC, bool WIDE>
+// What is read of a row ahead of its turn: up to 16 elements of y and h a thread (up to 8 where they are not
+// aligned), of 16 bits, or of 32.
+template <int E, int M, bool WIDE>
 struct Ahead {
-    static constexpr bool kOn = VEC && E <= 16;
+    static constexpr bool kOn = M == kGroups && E <= 16, kPieces = M == kMoved && E == 8;
     uint4 v[kOn ? E / 8 : 1][WIDE ? 2 : 1];
+    Piece piece;
 
-    __device__ __forceinline__ void load(const Slots<E, VEC>& s, const char* p, bool f32) {
+    __device__ __forceinline__ void load(const Slots<E, M>& s, const char* p, bool f32, const Bounds& in) {
         if constexpr (kOn) {
 #pragma unroll
             for (int i = 0; i < E / 8; ++i) {
@@ -235,9 +359,11 @@ struct Ahead {
                     v[i][0] = ldg128(p + 2 * e);
                 }
             }
+        } else if constexpr (kPieces) {
+            if (s.count) any_load<WIDE>(piece, p, f32, 8 * s.first, s.n, in);
         }
     }
-    __device__ __forceinline__ void get(const Slots<E, VEC>& s, const char* p, bool f32, float (&x)[E]) const {
+    __device__ __forceinline__ void get(const Slots<E, M>& s, const char* p, bool f32, float (&x)[E], const Bounds& in) const {
         if constexpr (kOn) {
 #pragma unroll
             for (int i = 0; i < E / 8; ++i) {
@@ -256,8 +382,15 @@ struct Ahead {
                     bf16x2_to_f32(a.w, t[6], t[7]);
                 }
             }
+        } else if constexpr (kPieces) {
+            if (s.count) {
+                any_get<WIDE>(piece, p, f32, 8 * s.first, s.n, x);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = 0.f;
+            }
         } else {
-            s.load(p, f32, x);
+            s.load(p, f32, x, in);
         }
     }
 };
@@ -268,12 +401,16 @@ __device__ __forceinline__ float sigmoid(float x) {
     return x < 0.f ? e * q : q;
 }
 
+__device__ __forceinline__ Bounds bounds_of(const Rows& r, int rows, int dim) {
+    return Bounds{r.ptr, row_ptr(r, rows - 1) + (size_t)dim * (r.f32 ? 4 : 2)};
+}
+
 // v = h_scale h + scale act(gate) post(v), of what there is.
-template <int E, bool VEC, bool CTA>
+template <int E, int M, bool CTA>
 __device__ __forceinline__ void join(float (&v)[E], const float (&h)[E], const BlockNormParams& p, long long row, Team<CTA>& team,
-                                     const Slots<E, VEC>& slots) {
+                                     const Slots<E, M>& slots) {
     if (p.y.ptr) {
-        if (p.post.kind != DL_NORM_NONE) normalise<E, VEC, CTA>(v, p.post, team, slots, p.dim);
+        if (p.post.kind != DL_NORM_NONE) normalise<E, M, CTA>(v, p.post, team, slots, p.dim);
         if (p.gate_kind != DL_GATE_NONE) {
             float g[E];
             if (p.gate_kind == DL_GATE_ROW) {
@@ -281,7 +418,10 @@ __device__ __forceinline__ void join(float (&v)[E], const float (&h)[E], const B
 #pragma unroll
                 for (int i = 0; i < E; ++i) g[i] = one;
             } else {
-                slots.load(p.gate_kind == DL_GATE_FULL ? row_ptr(p.gate, row) : p.gate.ptr, p.gate.f32, g);
+                if (p.gate_kind == DL_GATE_FULL)
+                    slots.load(row_ptr(p.gate, row), p.gate.f32, g, bounds_of(p.gate, p.rows, p.dim));
+                else
+                    slots.load(p.gate.ptr, p.gate.f32, g);
             }
             if (p.sigmoid) {
 #pragma unroll
@@ -305,33 +445,34 @@ __device__ __forceinline__ void join(float (&v)[E], const float (&h)[E], const B
 }
 
 // WIDE: y or h is fp32; T: the most threads of a CTA
-template <int E, bool VEC, bool CTA, bool WIDE, int T>
+template <int E, int M, bool CTA, bool WIDE, int T>
 __global__ void __launch_bounds__(T, T == 128 ? 4 : 1024 / T) block_norm_kernel(const __grid_constant__ BlockNormParams p) {
     __shared__ float2 red[CTA ? 64 : 1];
     Team<CTA> team{red, p.lanes, (int)blockDim.x};
     const int size = CTA ? blockDim.x : p.lanes, rank = CTA ? threadIdx.x : threadIdx.x & (p.lanes - 1);
     long long row = CTA ? blockIdx.x : ((long long)blockIdx.x * blockDim.x + threadIdx.x) / p.lanes;
     const long long step = CTA ? gridDim.x : (long long)gridDim.x * blockDim.x / p.lanes;
-    const Slots<E, VEC> slots(rank, size, p.dim);
+    const Slots<E, M> slots(rank, size, p.dim);
     griddep_wait();
     griddep_launch_dependents();
-    Ahead<E, VEC, WIDE> next_y, next_h;
+    Ahead<E, M, WIDE> next_y = {}, next_h = {};
+    const Bounds in_y = bounds_of(p.y, p.rows, p.dim), in_h = bounds_of(p.h, p.rows, p.dim);
     if (row < p.rows) {
-        if (p.y.ptr) next_y.load(slots, row_ptr(p.y, row), p.y.f32);
-        if (p.h.ptr) next_h.load(slots, row_ptr(p.h, row), p.h.f32);
+        if (p.y.ptr) next_y.load(slots, row_ptr(p.y, row), p.y.f32, in_y);
+        if (p.h.ptr) next_h.load(slots, row_ptr(p.h, row), p.h.f32, in_h);
     }
     for (; row < p.rows; row += step) {  // (teams of a warp may leave at different times: their shuffles are their own)
         float v[E], h[E];
-        if (p.y.ptr) next_y.get(slots, row_ptr(p.y, row), p.y.f32, v);
-        if (p.h.ptr) next_h.get(slots, row_ptr(p.h, row), p.h.f32, h);
+        if (p.y.ptr) next_y.get(slots, row_ptr(p.y, row), p.y.f32, v, in_y);
+        if (p.h.ptr) next_h.get(slots, row_ptr(p.h, row), p.h.f32, h, in_h);
         if (row + step < p.rows) {
-            if (p.y.ptr) next_y.load(slots, row_ptr(p.y, row + step), p.y.f32);
-            if (p.h.ptr) next_h.load(slots, row_ptr(p.h, row + step), p.h.f32);
+            if (p.y.ptr) next_y.load(slots, row_ptr(p.y, row + step), p.y.f32, in_y);
+            if (p.h.ptr) next_h.load(slots, row_ptr(p.h, row + step), p.h.f32, in_h);
         }
         join(v, h, p, row, team, slots);
         if (p.r.ptr) slots.store(row_ptr(p.r, row), p.r.f32, v);
         if (p.x.ptr) {
-            if (p.pre.kind != DL_NORM_NONE) normalise<E, VEC, CTA>(v, p.pre, team, slots, p.dim);
+            if (p.pre.kind != DL_NORM_NONE) normalise<E, M, CTA>(v, p.pre, team, slots, p.dim);
             slots.store(row_ptr(p.x, row), p.x.f32, v);
         }
     }
@@ -598,12 +739,12 @@ __global__ void __launch_bounds__(256 + 32, 2) block_norm_ring_kernel(const __gr
 
 constexpr int kMaxDim = 32768;
 
-template <int E, bool VEC, bool CTA, int T>
+template <int E, int M, bool CTA, int T>
 cudaError_t launch_norm(const BlockNormParams& p, long long grid, int threads, cudaStream_t stream) {
-    constexpr bool kWide = VEC && E <= 16;
+    constexpr bool kWide = M == kGroups && E <= 16;
     return kWide && (p.y.f32 || p.h.f32)
-               ? launch_dependent(block_norm_kernel<E, VEC, CTA, kWide, T>, dim3((unsigned)grid), dim3(threads), 0, stream, p)
-               : launch_dependent(block_norm_kernel<E, VEC, CTA, false, T>, dim3((unsigned)grid), dim3(threads), 0, stream, p);
+               ? launch_dependent(block_norm_kernel<E, M, CTA, kWide, T>, dim3((unsigned)grid), dim3(threads), 0, stream, p)
+               : launch_dependent(block_norm_kernel<E, M, CTA, false, T>, dim3((unsigned)grid), dim3(threads), 0, stream, p);
 }
 
 template <int E, bool YF, bool HF, bool XF>
@@ -648,7 +789,7 @@ static bool launch_ring(const BlockNormParams& p, int sm_count, const WaitCtl& w
     return true;
 }
 
-template <bool VEC>
+template <int M>
 cudaError_t launch_norm_rows(BlockNormParams& p, int sm_count, const WaitCtl& wait, int withhold, cudaStream_t stream) {
     const int groups = (p.dim + 7) / 8;
     if (groups <= 64) {                     // teams inside a warp, two groups a thread at most
@@ -658,20 +799,20 @@ cudaError_t launch_norm_rows(BlockNormParams& p, int sm_count, const WaitCtl& wa
         const long long all = ((long long)p.rows * lanes + threads - 1) / threads, most = 16LL * sm_count;
         const long long grid = all < most ? all : most;
         p.lanes = lanes;
-        return groups <= lanes ? launch_norm<8, VEC, false, 128>(p, grid, threads, stream)
-                               : launch_norm<16, VEC, false, 128>(p, grid, threads, stream);
+        return groups <= lanes ? launch_norm<8, M, false, 128>(p, grid, threads, stream)
+                               : launch_norm<16, M, false, 128>(p, grid, threads, stream);
     }
     cudaError_t e;
-    if (VEC && launch_ring(p, sm_count, wait, withhold, stream, e)) return e;
+    if (M == kGroups && launch_ring(p, sm_count, wait, withhold, stream, e)) return e;
     // A CTA each, as few groups a thread as 1024 threads allow: one up to 8192 (8000 rows of 1000, 2000, 3000, 8000: 11, 23, 38,
     // 92 us; two 20, 29, 44, 118 us; rows of 1000 by a warp 26), single elements too (999 rows of 1537: 13 us; two 30)
     const int per = groups <= 1024 ? 1 : groups <= 2048 ? 2 : 4, threads = ((groups + per - 1) / per + 31) / 32 * 32;
     const long long fit = 1024 / threads, most = fit * sm_count, grid = p.rows < most ? p.rows : most;
     if (per == 1)
-        return threads <= 256 ? launch_norm<8, VEC, true, 256>(p, grid, threads, stream)
-                              : launch_norm<8, VEC, true, 1024>(p, grid, threads, stream);
-    return per == 2 ? launch_norm<16, VEC, true, 1024>(p, grid, threads, stream)
-                    : launch_norm<32, VEC, true, 1024>(p, grid, threads, stream);
+        return threads <= 256 ? launch_norm<8, M, true, 256>(p, grid, threads, stream)
+                              : launch_norm<8, M, true, 1024>(p, grid, threads, stream);
+    return per == 2 ? launch_norm<16, M, true, 1024>(p, grid, threads, stream)
+                    : launch_norm<32, M, true, 1024>(p, grid, threads, stream);
 }
 
 static dl_status check_norm(const dl_norm* n, const char* name, NormSide& out) {
@@ -754,8 +895,12 @@ extern "C" dl_status dl_block_norm(const dl_rows* y, const dl_norm* post, const 
     if ((s = host_device(dev)) != DL_OK) return s;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const WaitCtl wait = {dev.err_word, dev.wait_limit_ns};
-    const cudaError_t e = vec ? launch_norm_rows<true>(p, dev.sm_count, wait, dev.withhold_stage, st)
-                              : launch_norm_rows<false>(p, dev.sm_count, wait, dev.withhold_stage, st);
+    // Rows that are not aligned: of bf16 and more than 64 elements in groups (8000 x 1001, 2999, 4000 x 16383: 23, 84, 247 us;
+    // singly 25, 101, 406), others singly (16384 x 41: 4.3 us, in groups 6.0; 8000 x 2999 of fp32, gated, 130 and 152)
+    const int hold = vec ? kGroups : dim > 64 && !p.y.f32 && !p.h.f32 ? kMoved : kSingle;
+    const cudaError_t e = hold == kGroups  ? launch_norm_rows<kGroups>(p, dev.sm_count, wait, dev.withhold_stage, st)
+                          : hold == kMoved ? launch_norm_rows<kMoved>(p, dev.sm_count, wait, dev.withhold_stage, st)
+                                           : launch_norm_rows<kSingle>(p, dev.sm_count, wait, dev.withhold_stage, st);
     if (e != cudaSuccess) return host_fail(DL_ERR_CUDA, "block_norm launch: %s", cudaGetErrorString(e));
     return host_ok();
 }
