@@ -252,3 +252,32 @@ def test_refusals(cuda_device):
         dl.block_norm(y, h, pre=pre, gate=y[:1].expand(4, 64))       # rows that share their memory
     with pytest.raises(dl.DLError, match="needs y"):
         dl.block_norm(None, h, post=pre)
+
+
+@pytest.mark.parametrize("dim", [65, 72, 200, 517, 1001, 8195])
+@pytest.mark.parametrize("x32", [False, True])
+def test_views_at_any_offset(cuda_device, dim, x32):
+    """Rows of bf16 that begin anywhere in wider ones, weights and gates too: what lies around them stays."""
+    g = torch.Generator().manual_seed(dim)
+    for offset, extra in ((0, 1), (1, 3), (3, 8), (5, 2), (7, 9)):
+        c = make(5, dim, h="bf16", post="rms", pre="layer", gate="full", act="sigmoid", bias=True, seed=dim + offset)
+
+        def place(t, dtype=None, fill=float("nan")):
+            wide = torch.full((t.shape[0], t.shape[1] + offset + extra), fill, dtype=dtype or t.dtype, device=cuda_device)
+            wide[:, offset:offset + t.shape[1]] = t.to(wide)
+            return wide, wide[:, offset:offset + t.shape[1]]
+
+        def vector(t):
+            wide = torch.full((t.numel() + offset,), float("nan"), dtype=t.dtype, device=cuda_device)
+            wide[offset:] = t.to(cuda_device)
+            return wide[offset:]
+
+        norms = {n: dl.Norm(vector(c[n][1]), vector(c[n][2]), kind=c[n][0], eps=c[n][3], offset=c[n][4]) for n in ("post", "pre")}
+        zero = torch.zeros(5, dim)
+        r_wide, r = place(zero, torch.bfloat16, 7.0)
+        x_wide, x = place(zero, F32 if x32 else torch.bfloat16, 7.0)
+        dl.block_norm(place(c["y"])[1], place(c["h"])[1], **norms, gate=place(c["gate"])[1], gate_act="sigmoid", scale=c["scale"],
+                      h_scale=c["h_scale"], out_h=r, out_x=x)
+        check(c, (r, x))
+        for wide in (r_wide, x_wide):
+            assert bool((wide[:, :offset] == 7).all()) and bool((wide[:, offset + dim:] == 7).all())
