@@ -1024,8 +1024,9 @@ class PagePool:
         self._caches = (_KVCache * max(1, len(caches)))(*[c._struct for c in caches])
         # the kernels read the caches' descriptions from the device
         self._device_caches = torch.frombuffer(bytearray(self._caches), dtype=torch.uint8).to(dev)
-        self._struct = _KVPages(self._caches, self._device_caches.data_ptr(), refs.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), len(caches),
-                                self.num_pages, page_size, self.rows, block_table.shape[1])
+        self._struct = _KVPages(self._caches, self._device_caches.data_ptr(), refs.data_ptr(), block_table.data_ptr(),
+                                seq_lens.data_ptr(), len(caches), self.num_pages, page_size, self.rows,
+                                block_table.shape[1])
         self._args = (ctypes.addressof(self._struct), dev.index)
 
     @classmethod
