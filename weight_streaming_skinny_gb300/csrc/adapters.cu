@@ -677,8 +677,9 @@ __device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t a_desc, uint
 // and up to 256 rows of A on the tensor cores, the sums in tensor memory.  It is bound by what an SM reads
 // from L2: a tile's x once, A once a tile.  One thread has x and A copied into 128-byte swizzled stages of 64 k,
 // another one issues the products.  Where the tokens are not in a row, eight warps copy x in pieces of 16 bytes (30 us
-// for 4096 tokens, K 8192, rank 64; by tile::gather4, four rows an instruction, 53; in a row 25).  A cluster shares K: each CTA leaves its sums in its shared memory, where
-// the cluster's CTAs add them up, a share of the tokens each, always in the same order.  Rows of A past the
+// for 4096 tokens, K 8192, rank 64; by tile::gather4, four rows an instruction, 53; in a row 25).  A cluster shares
+// K: each CTA leaves its sums in its shared memory, where the cluster's CTAs add them up, a share of the tokens
+// each, always in the same order (left to the second product to add, they cost it 48 us more).  Rows of A past the
 // rank, and of x past the tile, are read like the others: what they make are values that nobody takes.
 constexpr int kBigWarps = 8, kBigThreads = 32 * (kBigWarps + 2);
 constexpr int kBigCols = 256;            // rows of A of one CTA, at most
