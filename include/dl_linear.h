@@ -47,7 +47,10 @@
  *    device-side error.  The rest is scratch (split-K partial sums and, for
  *    FP8, an f16 copy of x) that every call writes before it reads.  One
  *    workspace serves calls of any shape in turn; two calls that may run at
- *    the same time (different streams) must not share a workspace.
+ *    the same time (different streams) must not share a workspace, nor may two
+ *    threads be inside calls on one workspace at the same time, on one stream
+ *    either: a call may enqueue several kernels that hand each other results
+ *    there, and another call's must not come between them.
  *  - Results are deterministic: the same inputs, shape, device (SM count) and
  *    overrides give bitwise identical outputs on every call.
  */

@@ -239,6 +239,10 @@ class Workspace:
     (split-K partial sums, the FP8 activation copy).  Do not share one
     Workspace between streams that may run at the same time; a call without
     one takes the default of the stream that it runs on.
+
+    Threads may share one on one stream: the kernels of a call hand each other
+    results through it, so a call holds ``calls`` until all of its kernels are
+    enqueued, and no other thread's call puts its own between them.
     """
 
     def __init__(self, nbytes: int, device="cuda"):
@@ -247,6 +251,7 @@ class Workspace:
         # the zeros must be in place before a kernel on any stream reads them
         torch.cuda.synchronize(self.tensor.device)
         self.addr = self.tensor.data_ptr()
+        self.calls = threading.RLock()
 
     @classmethod
     def for_shapes(cls, shapes, device="cuda"):
@@ -272,6 +277,7 @@ class Workspace:
 
 
 _default_ws: dict = {}
+_default_lock = threading.RLock()
 _outgrown: list = []     # default workspaces that larger ones replaced: calls under way and graphs name them
 
 
@@ -280,13 +286,14 @@ def _workspace(ws, need: int, device, stream):
     if ws is not None:
         return ws
     key = (device.index, _handle(stream, device))
-    cur = _default_ws.get(key)
-    if cur is None or cur.nbytes < need:
-        if cur is not None:
-            _outgrown.append(cur)
-        cur = Workspace(need, device)
-        _default_ws[key] = cur
-    return cur
+    with _default_lock:
+        cur = _default_ws.get(key)
+        if cur is None or cur.nbytes < need:
+            if cur is not None:
+                _outgrown.append(cur)
+            cur = Workspace(need, device)
+            _default_ws[key] = cur
+        return cur
 
 
 def _out(out, out_f32, M, N, device, stream):
@@ -320,8 +327,9 @@ def linear_bf16(x, w, bias=None, *, out=None, out_f32=None, workspace: Workspace
     with torch.cuda.device(dev):
         need = workspace_bytes(M, N, K, BF16)
         ws = _workspace(workspace, need, dev, stream)
-        _check(load().dl_linear_bf16(_ptr(x), _ptr(w), _ptr(bias), _ptr(out), _ptr(out_f32),
-                                     M, N, K, ws.ptr, ws.nbytes, _stream(stream, dev)))
+        with ws.calls:
+            _check(load().dl_linear_bf16(_ptr(x), _ptr(w), _ptr(bias), _ptr(out), _ptr(out_f32),
+                                         M, N, K, ws.ptr, ws.nbytes, _stream(stream, dev)))
     return out
 
 
@@ -353,8 +361,9 @@ def linear_swiglu(x, w, scales=None, bias=None, *, out=None, out_f32=None,
     dt = FP8_B128 if fp8 else BF16
     with torch.cuda.device(dev):
         ws = _workspace(workspace, workspace_bytes(M, N, K, dt), dev, stream)
-        _check(load().dl_linear_swiglu(dt, _ptr(x), _ptr(w), _ptr(scales), _ptr(bias), _ptr(out),
-                                       _ptr(out_f32), M, N, K, ws.ptr, ws.nbytes, _stream(stream, dev)))
+        with ws.calls:
+            _check(load().dl_linear_swiglu(dt, _ptr(x), _ptr(w), _ptr(scales), _ptr(bias), _ptr(out),
+                                           _ptr(out_f32), M, N, K, ws.ptr, ws.nbytes, _stream(stream, dev)))
     return out
 
 
@@ -389,9 +398,10 @@ def linear_argmax(x, w, scales=None, bias=None, *, out_idx=None, out_max=None, o
     dt = FP8_B128 if fp8 else BF16
     with torch.cuda.device(dev):
         ws = _workspace(workspace, workspace_bytes(M, N, K, dt), dev, stream)
-        _check(load().dl_linear_argmax(dt, _ptr(x), _ptr(w), _ptr(scales), _ptr(bias), _ptr(out_idx),
-                                       _ptr(out_max), _ptr(out), _ptr(out_f32), M, N, K, ws.ptr,
-                                       ws.nbytes, _stream(stream, dev)))
+        with ws.calls:
+            _check(load().dl_linear_argmax(dt, _ptr(x), _ptr(w), _ptr(scales), _ptr(bias), _ptr(out_idx),
+                                           _ptr(out_max), _ptr(out), _ptr(out_f32), M, N, K, ws.ptr,
+                                           ws.nbytes, _stream(stream, dev)))
     return out_idx
 
 
@@ -468,9 +478,10 @@ def linear_fp8_block128(x, wq, scales, bias=None, *, out=None, out_f32=None,
     with torch.cuda.device(dev):
         need = workspace_bytes(M, N, K, FP8_B128)
         ws = _workspace(workspace, need, dev, stream)
-        _check(load().dl_linear_fp8_block128(_ptr(x), _ptr(wq), _ptr(scales), _ptr(bias),
-                                             _ptr(out), _ptr(out_f32), M, N, K, ws.ptr,
-                                             ws.nbytes, _stream(stream, dev)))
+        with ws.calls:
+            _check(load().dl_linear_fp8_block128(_ptr(x), _ptr(wq), _ptr(scales), _ptr(bias),
+                                                 _ptr(out), _ptr(out_f32), M, N, K, ws.ptr,
+                                                 ws.nbytes, _stream(stream, dev)))
     return out
 
 
@@ -506,7 +517,7 @@ def decode_stream(layers, workspace: Workspace, *, use_graph: bool = False, stre
     """Run the layers back to back on one stream (optionally as a cached CUDA graph)."""
     arr = (_Layer * max(1, len(layers)))(*[_layer_struct(L) for L in layers])
     dev = layers[0].x.device if layers else torch.device("cuda", torch.cuda.current_device())
-    with torch.cuda.device(dev):
+    with torch.cuda.device(dev), workspace.calls:
         _check(load().dl_decode_stream(arr, len(layers), workspace.ptr, workspace.nbytes,
                                        _stream(stream, dev), 1 if use_graph else 0))
 
@@ -709,9 +720,11 @@ def attention_paged(q, cache: PagedKVCache, block_table, seq_lens, q_start, *, m
                 stream)
     elif workspace.tensor.device != cache.device:
         raise ValueError(f"workspace is on {workspace.tensor.device}, expected {cache.device}")
-    if not _call("attention", cache.device, *cache._args, q, block_table, seq_lens, q_start, max_q,
-                 cache.head_dim ** -0.5 if scale is None else scale, out, out_lse, workspace.addr,
-                 workspace.nbytes, stream):
+    with workspace.calls:
+        enqueued = _call("attention", cache.device, *cache._args, q, block_table, seq_lens, q_start, max_q,
+                         cache.head_dim ** -0.5 if scale is None else scale, out, out_lse, workspace.addr,
+                         workspace.nbytes, stream)
+    if not enqueued:
         _explain_attention(q, cache, block_table, seq_lens, q_start, out, out_lse)
         raise ValueError("max_q and stream must be integers, scale a number, sizes below 2^31")
     return out
@@ -963,8 +976,10 @@ def linear_adapters(x, adapters: Adapters, index, base=None, *, out=None, out_f3
             workspace = _workspace(None, adapters_workspace_bytes(x.shape[0], adapters), adapters.device, stream)
     elif workspace.tensor.device != adapters.device:
         raise ValueError(f"workspace is on {workspace.tensor.device}, expected {adapters.device}")
-    if not _call("adapters", adapters.device, adapters._args, x, index, base, out, out_f32, workspace.addr,
-                 workspace.nbytes, stream, made):
+    with workspace.calls:
+        enqueued = _call("adapters", adapters.device, adapters._args, x, index, base, out, out_f32, workspace.addr,
+                         workspace.nbytes, stream, made)
+    if not enqueued:
         _explain_adapters(x, adapters, index, base, out, out_f32)
         raise ValueError("stream must be an integer or a stream, sizes below 2^31")
     return out
@@ -1045,7 +1060,7 @@ def pages_workspace_bytes(pool: PagePool) -> int:
 def _pages(what, pool, first, second, out, workspace, stream):
     made = what > 0 and out is None
     if what == 0:
-        addr = nbytes = 0
+        enqueued = _call("pages", pool.device, what, pool._args, first, second, out, 0, 0, stream, made)
     else:
         if made:
             if what < 3:
@@ -1057,8 +1072,10 @@ def _pages(what, pool, first, second, out, workspace, stream):
                 workspace = _workspace(None, pages_workspace_bytes(pool), pool.device, stream)
         elif workspace.tensor.device != pool.device:
             raise ValueError(f"workspace is on {workspace.tensor.device}, expected {pool.device}")
-        addr, nbytes = workspace.addr, workspace.nbytes
-    if not _call("pages", pool.device, what, pool._args, first, second, out, addr, nbytes, stream, made):
+        with workspace.calls:
+            enqueued = _call("pages", pool.device, what, pool._args, first, second, out, workspace.addr,
+                             workspace.nbytes, stream, made)
+    if not enqueued:
         lists = {0: ("rows",), 1: ("rows", "tokens"), 2: ("parents", "children"), 3: ()}[what]
         for t, n in zip((first, second), lists):
             _need(t, n, torch.int32, pool.device)
