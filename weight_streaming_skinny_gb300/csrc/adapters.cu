@@ -662,6 +662,7 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapters_up_kernel(const __grid
 // ---------------------------------------------------------------- big tiles
 
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_cluster() { asm volatile("fence.proxy.async.shared::cluster;" ::: "memory"); }
 
 // One K step of 16 of two bf16 operands: kind::f16, fp32 accumulator, 128 rows, n columns.
 __host__ __device__ constexpr uint32_t umma_idesc_bf16(int n) {
@@ -891,7 +892,10 @@ __global__ void __launch_bounds__(kBigThreads) adapters_low_big_kernel(const __g
                     if (i < all) *reinterpret_cast<float4*>(out + (size_t)token_of(l, tile, t) * SR + j) = v;
                 }
             }
-            cluster.sync();              // the others have read this CTA's sums: its stages are free
+            // The others have read this CTA's sums: its stages are free, for copies that another proxy writes than the
+            // one that wrote and read the sums.
+            fence_async_cluster();
+            cluster.sync();
         } else {
             __syncthreads();
         }
