@@ -1,4 +1,6 @@
-"""linear_adapters with more tiles of 128 tokens than CTAs that take them: every token, in 64 bits."""
+"""linear_adapters with more tiles of 128 tokens than CTAs that take them, more rows of the first factor than one CTA
+has columns for, and more tokens than the lists have shared memory for: every token, in 64 bits.
+"""
 import pytest
 import torch
 
@@ -97,5 +99,35 @@ def test_runs_then_lists(cuda_device, parts, K):
     """Tiles of tokens in a row, then tiles by lists, of the same CTAs."""
     runs, rest = in_runs(60 * 64, 60, 64), 60 + dealt(100 * 42, 100)
     c = Many(cuda_device, 60 * 64 + 100 * 42, K, 128, 160, parts, torch.cat([rest[:2000], runs, rest[2000:]]))
+    c.check(c.run())
+    assert dl.device_status() == 0
+
+
+@pytest.mark.parametrize("parts", [3, 8])
+@pytest.mark.parametrize("mixed", [False, True])
+@pytest.mark.parametrize("base,f32", [(BF16, False), (F32, True), (None, True)])
+def test_many_rows_of_the_first_factor(cuda_device, parts, mixed, base, f32):
+    """384 and 1024 rows: two and four groups of up to 256 columns, K shared by a cluster."""
+    for T, K, R in ((600, 1024, 128), (300, 520, 128), (900, 2048, 104)):
+        c = Many(cuda_device, T, K, R, 3, parts, dealt(T, 3) if mixed else in_runs(T, 3, 100), base=base, seed=T)
+        out32 = torch.empty(T, 32 * parts, device=cuda_device) if f32 else None
+        out = c.run(out_f32=out32)
+        c.check(out, f32)
+        if f32:
+            c.check(out32, True)
+            assert torch.equal(out, out32.to(BF16))
+    assert dl.device_status() == 0
+
+
+@pytest.mark.parametrize("T", [8191, 8192, 8193, 20011])
+@pytest.mark.parametrize("order", ["mixed", "runs", "singles"])
+def test_many_tokens(cuda_device, T, order):
+    """The runs' starts in shared memory, and in the workspace; every token a run of its own, tokens without an
+    adapter among them; many adapters with few tokens each."""
+    num = 3000 if order == "singles" else 60
+    index = in_runs(T, num, 97) if order == "runs" else dealt(T, num, T)
+    index[5000:5400] = -1
+    index[::1009] = -1
+    c = Many(cuda_device, T, 128, 16, num, 2, index, seed=T)
     c.check(c.run())
     assert dl.device_status() == 0
