@@ -339,6 +339,21 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
 std::once_flag g_encode_once;
 EncodeTiledFn g_encode = nullptr;
 
+// The driver's call wants a context on the calling thread.  A thread whose first CUDA call this is has none
+// yet (the runtime binds the device's at a launch, not at cudaGetDevice): it is bound here.
+CUresult encode_bound(CUtensorMap* map, CUtensorMapDataType type, cuuint32_t rank, void* data, const cuuint64_t* dims,
+                      const cuuint64_t* strides, const cuuint32_t* box, const cuuint32_t* steps,
+                      CUtensorMapInterleave interleave, CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promotion,
+                      CUtensorMapFloatOOBfill fill) {
+    auto encode = [&] {
+        return g_encode(map, type, rank, data, dims, strides, box, steps, interleave, swizzle, promotion, fill);
+    };
+    const CUresult r = encode();
+    int dev = 0;
+    if (r != CUDA_ERROR_INVALID_CONTEXT || cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return r;
+    return encode();
+}
+
 dl_status get_encode(EncodeTiledFn& fn) {
     std::call_once(g_encode_once, [] {
         void* p = nullptr;
@@ -349,7 +364,7 @@ dl_status get_encode(EncodeTiledFn& fn) {
             g_encode = reinterpret_cast<EncodeTiledFn>(p);
     });
     if (!g_encode) return fail(DL_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-    fn = g_encode;
+    fn = encode_bound;
     return DL_OK;
 }
 
