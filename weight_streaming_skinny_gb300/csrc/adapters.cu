@@ -1415,11 +1415,6 @@ static dl_status check_adapters(const dl_adapters* a, AdapterParams& p) {
     return DL_OK;
 }
 
-template <class F>
-static cudaError_t raise_smem(F kernel, size_t bytes) {
-    return bytes > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) : cudaSuccess;
-}
-
 template <int Q>
 static cudaError_t launch_up(const AdapterParams& p, dim3 grid, dim3 block, size_t smem, cudaStream_t stream) {
     const int base = !p.base.ptr ? 0 : p.base.f32 ? 2 : 1;

@@ -756,10 +756,8 @@ cudaError_t launch_ring_kernel(RingParams& q, int sm_count, cudaStream_t stream)
     q.stages = 220 * 1024 / (ctas * stage);
     if (q.stages > 4) q.stages = 4;
     const size_t smem = (size_t)q.stages * stage;
-    if (smem > 47 * 1024) {                  // (and less than 1 KB that is not dynamic)
-        const cudaError_t e = cudaFuncSetAttribute(block_norm_ring_kernel<E, YF, HF, XF>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    const cudaError_t e = raise_smem(block_norm_ring_kernel<E, YF, HF, XF>, smem);
+    if (e != cudaSuccess) return e;
     const int most = ctas * sm_count;
     return launch_dependent(block_norm_ring_kernel<E, YF, HF, XF>, dim3(q.n.rows < most ? q.n.rows : most), dim3(threads + 32),
                             smem, stream, q);

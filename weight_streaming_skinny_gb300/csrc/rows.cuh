@@ -121,6 +121,13 @@ inline bool rows_meet(const Rows& a, long long na, long long da, const Rows& b, 
     return !(off >= wa && stride - off >= wb);
 }
 
+// What a kernel may have of dynamic shared memory, where `bytes` and its static part (below 1 KB) need more than the
+// 48 KB that any kernel has.
+template <class... P>
+cudaError_t raise_smem(void (*kernel)(P...), size_t bytes) {
+    return bytes > 47 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) : cudaSuccess;
+}
+
 // Launch that may start while the kernel before it on the stream still runs (it waits in
 // griddep_wait before it touches anything that kernel may write).
 template <class... P>
