@@ -695,6 +695,7 @@ __device__ __forceinline__ void copy16_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+constexpr int kBigStages = 224 * 1024;   // bytes of all stages, at most
 struct BigSmem {
     int cols, stage, stages, total;      // columns of the accumulator, bytes of a stage, stages, bytes of all
 };
@@ -702,7 +703,7 @@ __host__ __device__ inline BigSmem big_smem(int columns) {
     BigSmem s;
     s.cols = (columns < kBigCols ? columns + 15 : kBigCols) / 16 * 16;
     s.stage = (kBigTile + s.cols) * 128;
-    s.stages = (224 * 1024) / s.stage;       // 4 to 8; four hold the sums, 128 x (cols + 4) x 4 bytes, too
+    s.stages = kBigStages / s.stage;         // 4 to 8; four hold the sums, 128 x (cols + 4) x 4 bytes, too
     if (s.stages > 8) s.stages = 8;
     s.total = 1024 + s.stages * s.stage + 256;
     return s;
@@ -1493,7 +1494,7 @@ static cudaError_t launch_low_big(const AdapterParams& p, const BigMaps& m, long
     const int columns = p.parts * p.rank, groups = (columns + kBigCols - 1) / kBigCols, splits = big_splits(p.tokens, p.K);
     const long long most = 4LL * sm_count / (splits * groups) + 1;
     const size_t smem = big_smem(columns).total;
-    const cudaError_t e = raise_smem(adapters_low_big_kernel, smem);
+    const cudaError_t e = raise_smem<adapters_low_big_kernel>(1024 + kBigStages + 256);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1519,7 +1520,7 @@ static cudaError_t launch_up_big(AdapterParams& p, const BigMaps& m, int sm_coun
     constexpr int kSm = 227 * 1024;
     const int smem = up_smem(p.rank, f32).total;
     const int ctas = up_tmem(p.rank, P) == 256 && 2 * (smem + 1024) <= kSm ? kUpCtas : 1;
-    const cudaError_t e = raise_smem(adapters_up_big_kernel<BASE, P>, smem);
+    const cudaError_t e = raise_smem<adapters_up_big_kernel<BASE, P>>(up_smem(kBigRank, f32).total);
     if (e != cudaSuccess) return e;
     return launch_dependent(adapters_up_big_kernel<BASE, P>, dim3(ctas * sm_count), dim3(kUpBigThreads), smem, stream, m.up, p);
 }
@@ -1605,7 +1606,7 @@ extern "C" dl_status dl_linear_adapters(const dl_adapters* adapters, const dl_ro
         BigMaps maps;
         if (p.rank <= kBigRank && (s = big_maps(p, maps)) != DL_OK) return s;
         const size_t counters = ((size_t)p.num + 1 + (tokens <= kStartsHere ? tokens + 1 : 0)) * 4;
-        if ((e = raise_smem(sort_tokens_kernel, counters)) == cudaSuccess)
+        if ((e = raise_smem<sort_tokens_kernel>((kMaxAdapters + 1 + kStartsHere + 1) * 4)) == cudaSuccess)
             e = launch_dependent(sort_tokens_kernel, dim3(1), dim3(1024), counters, st, p);
         if (e == cudaSuccess) e = launch_small(p, small, dev.sm_count, st, false);
         if (e == cudaSuccess && p.rank <= kBigRank) e = launch_low_big(p, maps, big, dev.sm_count, st);

@@ -751,12 +751,13 @@ template <int E, bool YF, bool HF, bool XF>
 cudaError_t launch_ring_kernel(RingParams& q, int sm_count, cudaStream_t stream) {
     const int threads = q.n.dim / E, stage = q.y_bytes + q.h_bytes;
     // CTAs of an SM: 512 threads' worth, with two rows each at least
+    constexpr int kSm = 220 * 1024;
     int ctas = 512 / threads;
-    while (ctas > 1 && 220 * 1024 / (ctas * stage) < 2) --ctas;
-    q.stages = 220 * 1024 / (ctas * stage);
+    while (ctas > 1 && kSm / (ctas * stage) < 2) --ctas;
+    q.stages = kSm / (ctas * stage);
     if (q.stages > 4) q.stages = 4;
     const size_t smem = (size_t)q.stages * stage;
-    const cudaError_t e = raise_smem(block_norm_ring_kernel<E, YF, HF, XF>, smem);
+    const cudaError_t e = raise_smem<block_norm_ring_kernel<E, YF, HF, XF>>(kSm);
     if (e != cudaSuccess) return e;
     const int most = ctas * sm_count;
     return launch_dependent(block_norm_ring_kernel<E, YF, HF, XF>, dim3(q.n.rows < most ? q.n.rows : most), dim3(threads + 32),

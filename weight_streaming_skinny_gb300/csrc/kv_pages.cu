@@ -424,7 +424,7 @@ static CopyCaches copy_caches(const dl_kv_pages* g) {
 template <bool FORK>
 static cudaError_t launch_plan(const ListParams& p, cudaStream_t stream) {
     const size_t smem = (size_t)p.s.rows * 4;
-    const cudaError_t e = raise_smem(plan_kernel<FORK>, smem);
+    const cudaError_t e = raise_smem<plan_kernel<FORK>>((size_t)kMaxRows * 4);
     if (e != cudaSuccess) return e;
     return launch_dependent(plan_kernel<FORK>, dim3(1), dim3(kPlanThreads), smem, stream, p);
 }

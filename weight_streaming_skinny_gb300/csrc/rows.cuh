@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "dl_device.cuh"
 #include "dl_host.h"
 
@@ -121,11 +123,20 @@ inline bool rows_meet(const Rows& a, long long na, long long da, const Rows& b, 
     return !(off >= wa && stride - off >= wb);
 }
 
-// What a kernel may have of dynamic shared memory, where `bytes` and its static part (below 1 KB) need more than the
-// 48 KB that any kernel has.
-template <class... P>
-cudaError_t raise_smem(void (*kernel)(P...), size_t bytes) {
-    return bytes > 47 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) : cudaSuccess;
+// Lets a kernel have up to `most` bytes of dynamic shared memory, the most that any of its launches asks for.  Once a
+// device and never changed again: the limit is the process's, and a thread that set it to what its own call
+// needs would take it from under another thread's launch.
+template <auto Kernel>
+cudaError_t raise_smem(size_t most) {
+    static std::atomic<bool> raised[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (raised[dev].load()) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    if (e == cudaSuccess) raised[dev].store(true);
+    return e;
 }
 
 // Launch that may start while the kernel before it on the stream still runs (it waits in
