@@ -549,8 +549,8 @@ size_t dl_adapters_workspace_bytes(int tokens, int num, int rank, int parts);
  * [0, table_cols * page_size].  Pages are taken from the lowest free number on, for the
  * items of a list in their order: from the first that finds too few left on, those that
  * need any are refused.  done[i] is 1 if item i was served, 0 if it was refused (its row
- * is as it was).  A row that a list names twice is served at the first place, refused at
- * the others.  Every item of a list sees the rows as they were before the call.  Calls on one
+ * is as it was); it may lie where a list does.  A row that a list names twice is served at
+ * the first place, refused at the others.  Every item of a list sees the rows as they were before the call.  Calls on one
  * pool, and what reads its tables, follow each other on one stream (or are ordered by events).
  */
 typedef struct dl_kv_pages {

@@ -29,7 +29,8 @@ __device__ __forceinline__ bool in_pool(const PageState& s, int page) { return p
 struct Plan {
     int row, from;         // the row that changes; fork: the row that it is a copy of
     int len, need, first;  // its length before (-1: refused), pages asked for, those asked for before it
-    int src, dst, tail;    // fork: the begun page, its copy, tokens in it (dst -1: nothing to copy)
+    int src, dst;          // fork: the begun page and its copy (-1: nothing to copy)
+    int tail;              // fork: tokens in the begun page; reserve: tokens asked for
 };
 
 constexpr int kPlanThreads = 1024;
@@ -138,6 +139,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
                     if (more >= 0 && (long long)len + more <= (long long)s.cols * s.page_size) {
                         q.len = len;
                         q.need = pages_for(s, len + more) - pages_for(s, len);
+                        q.tail = more;
                     }
                 }
             }
@@ -148,7 +150,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         if (i < p.n) p.plan[i] = q;
     }
     const int got = free_pages(s, asked, is_free, p.list, scan);
-    // all lengths have been read: they may change now
+    // all lengths and lists have been read: lengths may change now, and `done` may lie where a list does
     for (int i = tid; i < p.n; i += kPlanThreads) {
         Plan q = p.plan[i];
         const bool ok = q.len >= 0 && (q.need == 0 || q.first + q.need <= got);
@@ -170,7 +172,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
             }
             p.plan[i] = q;
         } else if (ok) {
-            s.lens[q.row] = q.len + p.b[i];
+            s.lens[q.row] = q.len + q.tail;
         }
     }
     if (!FORK) {
