@@ -596,6 +596,7 @@ class PagedKVCache:
                                 k_scale.stride(0) if pages > 1 else heads * blocks,
                                 k_scale.stride(1) if heads > 1 else blocks,
                                 pages, heads, page, dim, self.block)
+        self._lists: dict = {}       # lists of caches that begin with this one, as pools have them on the device
         # what a call passes of it: its description's address, its device, heads and dims
         self._args = (ctypes.addressof(self._struct), self.device.index, heads, dim)
 
@@ -1010,7 +1011,10 @@ class PagePool:
     refs         int32 [num_pages]: how many rows' tables name each page (0: free)
 
     The object holds the tensors and is made once; kv_free, kv_reserve, kv_fork and kv_compact change
-    them in place.  ``PagePool.empty`` makes a pool whose rows have no pages.
+    them in place.  kv_fork and kv_compact also read the caches' descriptions on the device, which belong
+    to the first cache: who replays a graph of them, or has calls under way on other streams, keeps the
+    cache objects as well as the tensors (the pool itself may go).  ``PagePool.empty`` makes a pool whose
+    rows have no pages.
     """
 
     def __init__(self, caches, block_table, seq_lens, refs, *, page_size=None):
@@ -1038,7 +1042,10 @@ class PagePool:
         self.page_size, self.num_pages, self.rows, self.device = page_size, refs.shape[0], seq_lens.shape[0], dev
         self._caches = (_KVCache * max(1, len(caches)))(*[c._struct for c in caches])
         # the kernels read the caches' descriptions from the device
-        self._device_caches = torch.frombuffer(bytearray(self._caches), dtype=torch.uint8).to(dev)
+        lists, described = caches[0]._lists if caches else {}, bytes(self._caches)
+        if described not in lists:
+            lists[described] = torch.frombuffer(bytearray(described), dtype=torch.uint8).to(dev)
+        self._device_caches = lists[described]
         self._struct = _KVPages(self._caches, self._device_caches.data_ptr(), refs.data_ptr(), block_table.data_ptr(),
                                 seq_lens.data_ptr(), len(caches), self.num_pages, page_size, self.rows,
                                 block_table.shape[1])
