@@ -316,21 +316,17 @@ __device__ __forceinline__ void split(float a, float b, uint32_t (&v)[P]) {
     }
 }
 
-// A finite value beyond bf16's largest number and half a step, where split() rounds the first part to an infinity: that
-// number, then the rest.  Three parts are cut, not rounded: 8 bits each hold all 24.  Of two the second is rounded,
-// but not up to where both add up to 2^128: 2^-17 of the value is lost as elsewhere, or there, within 2^-17 of fp32's
-// largest number, 2^-16.
-__device__ __forceinline__ bool rounds_to_infinity(float a) { return fabsf(a) <= 3.4028235e38f && fabsf(a) >= 0x1.ffp127f; }
-__device__ __noinline__ void split_large(float a, int parts, uint32_t (&v)[3]) {
-    v[0] = __float_as_uint(a) >> 16;
-    a -= __uint_as_float(v[0] << 16);        // exact
-    v[1] = __float_as_uint(a) >> 16;
-    if (parts == 3) {
-        v[2] = __float_as_uint(a - __uint_as_float(v[1] << 16)) >> 16;
-    } else {
-        const uint32_t near = f32_to_bf16_rne(a);
-        if (fabsf(__uint_as_float(near << 16)) < 0x1p120f) v[1] = near;
-    }
+// One value's three parts.  A finite one beyond bf16's largest number and half a step, where split() rounds the first part
+// to an infinity, begins with that number.  Where three are taken, its second one is cut, not rounded: 8 bits each
+// hold all 24.  Of two the second is cut only where both would add up to 2^128, within 2^-17 of fp32's largest
+// number, and 2^-16 of the value is lost.
+__device__ __forceinline__ void split_one(float a, bool three, uint32_t (&v)[3]) {
+    const bool large = fabsf(a) <= 3.4028235e38f && fabsf(a) >= 0x1.ffp127f;
+    v[0] = large ? __float_as_uint(a) >> 16 : f32x2_to_bf16x2(a, 0.f);
+    a -= __uint_as_float(v[0] << 16);
+    v[1] = f32x2_to_bf16x2(a, 0.f);
+    if (large && (three || fabsf(__uint_as_float(v[1] << 16)) >= 0x1p120f)) v[1] = __float_as_uint(a) >> 16;
+    v[2] = f32x2_to_bf16x2(a - __uint_as_float(v[1] << 16), 0.f);
 }
 
 // ---------------------------------------------------------------- small tiles: first product
@@ -443,10 +439,8 @@ __global__ void __launch_bounds__(kLowThreads, 2) adapters_low_kernel(const __gr
             if (t >= 0 && j < R) {       // (zeros past the rank: it may end inside four that are read at once)
                 const size_t step = (size_t)p.parts * R;
                 uint16_t* to = p.low + (size_t)t * (p.y32.ptr ? 3 : 2) * step + pt * R + j;
-                const float low = j < r ? all * tile.scale : 0.f;
                 uint32_t v[3];
-                split(low, 0.f, v);
-                if (rounds_to_infinity(low)) split_large(low, p.y32.ptr ? 3 : 2, v);
+                split_one(j < r ? all * tile.scale : 0.f, p.y32.ptr != nullptr, v);
                 to[0] = (uint16_t)v[0];
                 to[step] = (uint16_t)v[1];
                 if (p.y32.ptr) to[2 * step] = (uint16_t)v[2];
