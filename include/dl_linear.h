@@ -480,7 +480,7 @@ typedef struct dl_norm {
  *   h_out, x_out  [rows][dim]; one of them may be missing.  Each may be y or h
  *          itself (the same rows, stride and type); they overlap nothing else.
  * A square that leaves fp32's range does not: such rows are summed scaled (a difference
- * from the mean does).  NaN and infinities give what the formulas give, in their row only.
+ * from the mean does, and a mean is held to dim * 2^-150 at best).  NaN and infinities give what the formulas give, in their row only.
  */
 #define DL_GATE_NONE 0
 #define DL_GATE_ROW 1
@@ -522,10 +522,11 @@ typedef struct dl_adapters {
  *   base   [tokens][N], bf16 or fp32 (a linear's y or y_f32), or missing: 0
  *   y      bf16 [tokens][N], rounded once; y_f32 fp32 [tokens][N] or missing: the value
  *          before that.  Each may be base itself; they overlap nothing else.
- * Sums are fp32.  First products go into the second ones as fp32 rounded to 2^-18 of their
- * value, whole where y_f32 is asked for.  What a token gets is repeatable bit for bit; its last bits
- * depend on how many tokens the call has and, beyond 256, on how many of them (and how many in a row)
- * have its adapter: many go in tiles of 128.  Nothing else of the other tokens reaches it.
+ * Sums are fp32.  First products go into the second ones as fp32 rounded to 2^-17 of their
+ * value (2^-16 next to fp32's largest number), whole where y_f32 is asked for.  What a token
+ * gets is repeatable bit for bit; its last bits depend on how many tokens the call has and,
+ * beyond 256, on how many of them (and how many in a row) have its adapter: many go in tiles
+ * of 128.  Nothing else of the other tokens reaches it.
  *   tokens any number, num * N up to 2^31 - 256; columns go fastest where N's rows of
  *   base, y and y_f32 are 16-byte aligned (stride and data).
  *   workspace: dl_adapters_workspace_bytes(...); its zero prefix is left alone, so one

@@ -35,7 +35,8 @@ class Many:
 
     def want(self, whole):
         """(out, bound of its error before rounding) in 64 bits; the bound is adapters64's, for all tokens of
-        an adapter at once."""
+        an adapter at once, with 2^-17 for two parts: a first part leaves at most half its step, 2^-8 of the value,
+        exactly a part itself; anything less has steps half as large, and is off by 2^-9 of 2^-8."""
         T, K = self.x.shape
         num, N, R = self.b.shape
         out = torch.zeros(T, N, dtype=F64, device=self.x.device) if self.base is None else self.base.double()
@@ -50,7 +51,7 @@ class Many:
             for p, c in enumerate(self.cols):
                 A, B = self.a[i, p * R:p * R + r].double(), self.b[i, n0:n0 + c, :r].double()
                 low, spread = s * (x @ A.T), abs(s) * (x.abs() @ A.abs().T)
-                dlow = (K / 16 + 32) * 2.0 ** -23 * spread + (2.0 ** -23 + (2.0 ** -26 if whole else 2.0 ** -18)) * low.abs()
+                dlow = (K / 16 + 32) * 2.0 ** -23 * spread + (2.0 ** -23 + (2.0 ** -26 if whole else 2.0 ** -17)) * low.abs()
                 out[at, n0:n0 + c] += low @ B.T
                 err[at, n0:n0 + c] += dlow @ B.abs().T + (3 * r / 16 + 8) * 2.0 ** -23 * (low.abs() @ B.abs().T)
                 n0 += c

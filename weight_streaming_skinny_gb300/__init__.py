@@ -238,7 +238,10 @@ class Workspace:
     zero-filled here once; every call leaves them zero) and the calls' scratch
     (split-K partial sums, the FP8 activation copy).  Do not share one
     Workspace between streams that may run at the same time; a call without
-    one takes the default of the stream that it runs on.
+    one takes the default of the stream that it runs on.  Graphs that may be
+    replayed at the same time need workspaces of their own, and a call that is
+    captured should be given one: a default that has to be made first waits
+    for the device, which a capture refuses.
 
     Threads may share one on one stream: the kernels of a call hand each other
     results through it, so a call holds ``calls`` until all of its kernels are
@@ -851,7 +854,7 @@ def block_norm(y, h=None, *, post: Norm | None = None, pre: Norm | None = None, 
     y (a block's output) and h (the residual stream): bf16 or fp32 [rows, dim], any stride between
     rows; one of them may be None.  gate: bf16 or fp32 [dim], [rows, 1] or [rows, dim]; gate_act None or
     "sigmoid".  Results go to out_h and out_x, which may be h or y; those not given are made: r like h
-    (like y without h; without y the stream does not change and r is None), x in bf16 where there
+    (like y without h; without y it is not made, and r is None), x in bf16 where there
     is a `pre`.  See dl_block_norm.
     """
     like = h if h is not None else y

@@ -297,8 +297,9 @@ __global__ void __launch_bounds__(1024) sort_tokens_kernel(const __grid_constant
 
 // ---------------------------------------------------------------- parts
 
-// The fp32 first products go into the second ones as two bf16 parts (2^-18 of the value is lost), three
-// (24 bits: nothing) where an fp32 result is asked for.  The parts of a value and their products can
+// The fp32 first products go into the second ones as two bf16 parts (2^-17 of the value is lost: the first
+// leaves half its step at most, 2^-8 of the value, which the second holds; of anything less it loses 2^-9), three (24
+// bits: nothing) where an fp32 result is asked for.  The parts of a value and their products can
 // leave NaN where the value's own product is an infinity; what comes out NaN is summed again as it stands.
 // Two values as packed bf16 parts, each the next 8 bits of the value, rounded.  (An infinity's later parts are
 // NaN, and so is then what they are multiplied to.)

@@ -804,7 +804,7 @@ cudaError_t launch_norm_rows(BlockNormParams& p, int sm_count, const WaitCtl& wa
     cudaError_t e;
     if (M == kGroups && launch_ring(p, sm_count, wait, withhold, stream, e)) return e;
     // A CTA each, as few groups a thread as 1024 threads allow: one up to 8192 (8000 rows of 1000, 2000, 3000, 8000: 11, 23, 38,
-    // 92 us; two 20, 29, 44, 118 us; rows of 1000 by a warp 26), single elements too (999 rows of 1537: 13 us; two 30)
+    // 88 us; two 20, 29, 44, 118 us; rows of 1000 by a warp 26), single elements too (999 rows of 1537: 13 us; two 30)
     const int per = groups <= 1024 ? 1 : groups <= 2048 ? 2 : 4, threads = ((groups + per - 1) / per + 31) / 32 * 32;
     const long long fit = 1024 / threads, most = fit * sm_count, grid = p.rows < most ? p.rows : most;
     if (per == 1)
@@ -894,8 +894,11 @@ extern "C" dl_status dl_block_norm(const dl_rows* y, const dl_norm* post, const 
     if ((s = host_device(dev)) != DL_OK) return s;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const WaitCtl wait = {dev.err_word, dev.wait_limit_ns};
-    // Rows that are not aligned: of bf16 and more than 64 elements in groups (8000 x 1001, 2999, 4000 x 16383: 23, 84, 247 us;
-    // singly 25, 101, 406), others singly (16384 x 41: 4.3 us, in groups 6.0; 8000 x 2999 of fp32, gated, 130 and 152)
+    // Rows that are not aligned: of bf16 and more than 64 elements in groups, moved, others singly.  Many rows gain by it
+    // (moved and singly: 8000 x 1001 22.7 and 26.1 us, 2999 83.5 and 102; 4000 x 16383 246 and 451; 30000 x 100 13.6 and 14.5),
+    // and so do few beyond 8192 (16 x 9001 6.8 and 13.0); few shorter ones, and those next to the limit, lose (400 x 2999 7.3
+    // and 6.4, 5001 9.6 and 8.9; 16384 x 65 9.3 and 8.9), as they would up to it (16384 x 41 6.2 and 5.8) and in fp32
+    // (8000 x 2999, gated, 152 and 131).
     const int hold = vec ? kGroups : dim > 64 && !p.y.f32 && !p.h.f32 ? kMoved : kSingle;
     const cudaError_t e = hold == kGroups  ? launch_norm_rows<kGroups>(p, dev.sm_count, wait, dev.withhold_stage, st)
                           : hold == kMoved ? launch_norm_rows<kMoved>(p, dev.sm_count, wait, dev.withhold_stage, st)

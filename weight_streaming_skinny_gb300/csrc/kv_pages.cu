@@ -231,8 +231,8 @@ struct ForkParams {
 };
 
 // The forked rows' tables, the counts of the pages that they share, and their begun pages' contents, in all caches
-// at once: a warp copies a head's keys or values, eight loads in flight a lane.  Bound by these copies (52 MB both
-// ways in 17 us).
+// at once: a warp copies a head's keys or values, eight loads in flight a lane.  Bound by these copies (101 MB both
+// ways in 18 us, half of it DRAM's: what is written stays in L2).
 __global__ void __launch_bounds__(kCopyThreads) fork_copy_kernel(const __grid_constant__ ForkParams p,
                                                                  const __grid_constant__ CopyCaches c) {
     griddep_wait();
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const __grid
     }
 }
 
-// The moves' contents in all caches, and the tables: memory bounds it (1.08 GB both ways in 155 us, 6.9 TB/s).
+// The moves' contents in all caches, and the tables: memory bounds it (1.08 GB both ways in 158 us).
 __global__ void __launch_bounds__(kCopyThreads) compact_copy_kernel(const __grid_constant__ CompactParams p,
                                                                     const __grid_constant__ CopyCaches c) {
     griddep_wait();
