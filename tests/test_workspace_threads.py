@@ -125,6 +125,15 @@ def test_calls_on_one_workspace_of_the_caller(lib, name):
     assert lib.most == 1
 
 
+def test_a_workspace_over_other_memory(lib):
+    """One that is made without its constructor, from a part of a larger buffer."""
+    ws = dl.Workspace.__new__(dl.Workspace)
+    ws.nbytes, ws.tensor = 4096, torch.zeros(4096, dtype=torch.uint8)
+    call = calls()["linear_bf16"]
+    threads(*[lambda: call(workspace=ws, stream=7)] * 3)
+    assert lib.most == 1
+
+
 def test_streams_of_layers_on_one_workspace(lib):
     ws = dl.Workspace(4096, DEV)
     layers = [SimpleNamespace(x=torch.zeros(1, 8))] * 2

@@ -248,13 +248,17 @@ class Workspace:
     enqueued, and no other thread's call puts its own between them.
     """
 
+    def __new__(cls, *args, **kw):
+        ws = super().__new__(cls)        # (one made over other memory, without __init__, has it too)
+        ws.calls = threading.RLock()
+        return ws
+
     def __init__(self, nbytes: int, device="cuda"):
         self.nbytes = max(int(nbytes), 256)
         self.tensor = torch.zeros(self.nbytes, dtype=torch.uint8, device=device)
         # the zeros must be in place before a kernel on any stream reads them
         torch.cuda.synchronize(self.tensor.device)
         self.addr = self.tensor.data_ptr()
-        self.calls = threading.RLock()
 
     @classmethod
     def for_shapes(cls, shapes, device="cuda"):
